@@ -83,6 +83,93 @@ int awq_int8_linear(const void* x, int64_t ldx, const float* s, int64_t n_tokens
                     int64_t in_features, const void* bias, int32_t dtype, void* y, int64_t ldy,
                     void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------------------
+ * Key/value cache in 4 bits
+ *   Keys and values of a token and head are quantised along head_dim in groups of group_size
+ *   channels by the quantiser of awq_quantize_pack with w_bit 4 and no channel scales (fp32,
+ *   one rounding an operation; symmetric or zero-point); a value reads as
+ *   (code - zero) * fp16(step) [AWQ-blog §1.2, §2.1; AutoAWQ-70B §四 (metadata per group)].
+ *   A group that holds a NaN or an infinity is stored with step NaN, codes and zero 0.
+ *
+ *   cache        uint8 [n_pages][kv_heads][record], 16-byte aligned; record =
+ *                awq_kv4_record_bytes(cfg).  With D = head_dim, P = page_size, g = group_size,
+ *                G = D / g a record is
+ *                  K codes   P rows of D / 2 bytes: [q 0..3][j < G][u < g / 32] 32-bit words;
+ *                            nibble n (bits 4 n) is channel j g + q g / 4 + 8 u + n
+ *                  V codes   P / 8 blocks of 8 tokens: [h < D / 64][r < 16][i < 4] 32-bit words;
+ *                            the low half is token 2 i of the block, the high half 2 i + 1,
+ *                            nibble c of a half is channel 16 (4 h + c) + r
+ *                  K params  [G][P] pairs of fp16 step, fp16 zero
+ *                  V params  the same
+ *   block_table  int32 [n_seqs][max_blocks] (row-major): token t of sequence b is token
+ *                t mod P of page block_table[b][t / P].  Entries past a sequence's length are
+ *                not read.  Entries outside [0, n_pages) and positions past max_blocks are
+ *                no memory: a write there is dropped, and keys there are masked
+ *   seq_lens     int32 [n_seqs]: tokens of each sequence, the new ones included
+ *   q_start      int32 [n_seqs + 1], ascending from 0: rows q_start[b] .. q_start[b + 1] - 1 of
+ *                k, v and q are the last tokens of sequence b (positions seq_lens[b] - count
+ *                .. seq_lens[b] - 1).  Rows at negative positions do not exist: they are not
+ *                written, read as zeros and attend to nothing
+ *   k, v, q      fp16 or bf16 [token][head][head_dim], unit stride in head_dim, token and head
+ *                strides in elements (multiples of 8, 16-byte aligned base)
+ * All sizes are device data except the bounds named below; a call may be captured and replayed
+ * while lengths and tables change within those bounds.
+ * ---------------------------------------------------------------------------------- */
+typedef struct awq_kv4_config {
+  int32_t head_dim;   /* 64 or 128                             */
+  int32_t kv_heads;   /* 1 .. 65535                            */
+  int32_t page_size;  /* tokens a page: 16, 32, 64, 128 or 256 */
+  int32_t group_size; /* 32, 64 or 128, at most head_dim       */
+  int32_t zero_point; /* 0 = symmetric, 1 = zero-point         */
+} awq_kv4_config;
+
+/* Bytes of one page of one head, or 0 for an invalid configuration. */
+size_t awq_kv4_record_bytes(const awq_kv4_config* cfg);
+
+/* Quantise the new tokens' keys and values (n_tokens rows of k and v, rows past
+ * q_start[n_seqs] ignored) into the cache. */
+int awq_kv4_append(const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                   int64_t v_token_stride, int64_t v_head_stride, int64_t n_tokens, int32_t dtype,
+                   void* cache, int64_t n_pages, const int32_t* block_table, int64_t n_seqs,
+                   int64_t max_blocks, const int32_t* seq_lens, const int32_t* q_start,
+                   const awq_kv4_config* cfg, void* stream);
+
+/* The stored values of the same rows: k_out and v_out [n_tokens][kv_heads][head_dim], contiguous,
+ * 16-byte aligned, (code - zero) * step in fp32 rounded once to dtype; rows that do not exist
+ * are zeros. */
+int awq_kv4_read(const void* cache, int64_t n_pages, const int32_t* block_table, int64_t n_seqs,
+                 int64_t max_blocks, const int32_t* seq_lens, const int32_t* q_start,
+                 int64_t n_tokens, const awq_kv4_config* cfg, int32_t dtype, void* k_out,
+                 void* v_out, void* stream);
+
+/* Attention of the rows of q over the cached keys and values:
+ *   out[r][h] = sum_t p_t v_t,  p = softmax over t of scale q[r][h] . k_t,
+ *   t <= position of r (and t > position - window if window > 0), with key/value head
+ *   h / (heads / kv_heads); lse[r][h] = log sum_t exp(scale q . k_t).
+ * A row without keys gives out 0 and lse -infinity.  Scores, softmax statistics and sums are
+ * fp32; q enters the products exactly in fp16 (each row scaled by a power of two), the
+ * probabilities times the value's step rounded to fp16 with 2^-11 relative error.  The order
+ * of every sum is fixed: results repeat bit for bit for the same bounds.
+ *   q        as above, n_tokens rows, heads a multiple of kv_heads
+ *   max_q    bound on the rows of one sequence, max_len bound on seq_lens (both host values:
+ *            they size the launch; rows and keys beyond them are not computed)
+ *   scale    finite, > 0; window 0 or more
+ *   out      [n_tokens][heads][head_dim] contiguous, q's type, 16-byte aligned; rows past
+ *            q_start[n_seqs] are not written
+ *   lse_out  fp32 [n_tokens][heads] or NULL
+ *   workspace  device, 256-byte aligned, awq_kv4_attention_workspace_bytes(...) bytes (0: may
+ *            be NULL), contents unspecified before and after */
+size_t awq_kv4_attention_workspace_bytes(int64_t n_tokens, int64_t n_seqs, int64_t heads,
+                                         const awq_kv4_config* cfg, int64_t max_q,
+                                         int64_t max_len);
+int awq_kv4_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                      int64_t n_tokens, int64_t heads, int32_t dtype, const void* cache,
+                      int64_t n_pages, const int32_t* block_table, int64_t n_seqs,
+                      int64_t max_blocks, const int32_t* seq_lens, const int32_t* q_start,
+                      const awq_kv4_config* cfg, int64_t max_q, int64_t max_len, float scale,
+                      int64_t window, void* out, float* lse_out, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

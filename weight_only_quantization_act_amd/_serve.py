@@ -18,6 +18,20 @@ from ._lib import lib as _base_lib
 AWQ_FP16, AWQ_BF16 = 0, 1
 AWQ_FOLD_DIVIDE, AWQ_FOLD_MULTIPLY = 0, 1
 
+class awq_kv4_config(ctypes.Structure):
+    """Layout of a 4-bit key/value cache: head_dim (64 or 128), kv_heads, page_size (tokens a
+    page: 16 .. 256, a power of two), group_size (32, 64, 128) and zero_point (0 or 1)."""
+    _fields_ = [("head_dim", _i32), ("kv_heads", _i32), ("page_size", _i32), ("group_size", _i32),
+                ("zero_point", _i32)]
+
+    def __init__(self, head_dim: int = 128, kv_heads: int = 8, page_size: int = 64,
+                 group_size: int = 64, zero_point: int = 1):
+        super().__init__(int(head_dim), int(kv_heads), int(page_size), int(group_size),
+                         int(zero_point))
+
+
+_kvp = ctypes.POINTER(awq_kv4_config)
+
 _SIGNATURES = {
     "awq_int8_quantize": (ctypes.c_int, [_vp, _i64, _i64, _i64, _i32, _vp, _i32, _vp, _i64, _vp,
                                          _vp]),
@@ -27,6 +41,15 @@ _SIGNATURES = {
     "awq_int8_linear_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "awq_int8_linear": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i32,
                                        _vp, _i64, _vp, _sz, _vp]),
+    "awq_kv4_record_bytes": (_sz, [_kvp]),
+    "awq_kv4_append": (ctypes.c_int, [_vp, _i64, _i64, _vp, _i64, _i64, _i64, _i32, _vp, _i64, _vp,
+                                      _i64, _i64, _vp, _vp, _kvp, _vp]),
+    "awq_kv4_read": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _kvp, _i32, _vp, _vp,
+                                    _vp]),
+    "awq_kv4_attention_workspace_bytes": (_sz, [_i64, _i64, _i64, _kvp, _i64, _i64]),
+    "awq_kv4_attention": (ctypes.c_int, [_vp, _i64, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _i64,
+                                         _i64, _vp, _vp, _kvp, _i64, _i64, ctypes.c_float, _i64, _vp,
+                                         _vp, _vp, _sz, _vp]),
 }
 
 _BOUND: Optional[ctypes.CDLL] = None
@@ -189,3 +212,132 @@ def awq_int8_linear(x: torch.Tensor, wq: torch.Tensor, wstep: torch.Tensor,
                                _stream_ptr(stream))
     _check(st, "awq_int8_linear")
     return y
+
+
+# -------------------------------------------------------------- key/value cache in 4 bits
+def awq_kv4_record_bytes(cfg: awq_kv4_config) -> int:
+    """Bytes of one page of one head (0 for an invalid configuration)."""
+    return int(lib().awq_kv4_record_bytes(ctypes.byref(cfg)))
+
+
+def awq_kv4_cache(n_pages: int, cfg: awq_kv4_config, device="cuda") -> torch.Tensor:
+    """An empty cache: uint8 [n_pages, kv_heads, record], zeroed."""
+    rec = awq_kv4_record_bytes(cfg)
+    if rec == 0:
+        raise ValueError("invalid awq_kv4_config")
+    return torch.zeros((n_pages, cfg.kv_heads, rec), dtype=torch.uint8, device=device)
+
+
+def _kv4_args(cache, table, lens, starts, cfg):
+    rec = awq_kv4_record_bytes(cfg)
+    if rec == 0:
+        raise ValueError("invalid awq_kv4_config")
+    _dev(cache, torch.uint8, "cache")
+    if cache.dim() != 3 or cache.shape[1] != cfg.kv_heads or cache.shape[2] != rec:
+        raise ValueError(f"cache has shape {tuple(cache.shape)}, expected "
+                         f"[n_pages, {cfg.kv_heads}, {rec}]")
+    _dev(table, torch.int32, "block_table")
+    if table.dim() != 2:
+        raise ValueError("block_table must be [n_seqs, max_blocks]")
+    n = table.shape[0]
+    _dev(lens, torch.int32, "seq_lens", (n,))
+    _dev(starts, torch.int32, "q_start", (n + 1,))
+    return n
+
+
+def _heads(t, name, heads, dim, dtype=None):
+    """Check [tokens, heads, dim] with unit stride in dim; returns token and head strides."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a device (HIP) tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [tokens, "
+                         f"{'heads' if heads is None else heads}, {dim}]")
+    if t.stride(2) != 1:
+        raise ValueError(f"{name} must be contiguous along head_dim")
+    return (t.stride(0) if t.shape[0] > 1 else 0), (t.stride(1) if t.shape[1] > 1 else 0)
+
+
+@_on_stream
+def awq_kv4_append(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
+                   seq_lens: torch.Tensor, q_start: torch.Tensor, cfg: awq_kv4_config,
+                   stream=None) -> None:
+    """Quantise the rows k, v (fp16 or bf16 [T, kv_heads, head_dim], any token and head strides
+    that are multiples of 8) into the pages of their sequences.  Rows q_start[b] ..
+    q_start[b + 1] - 1 are the last tokens of sequence b, whose length with them is seq_lens[b]."""
+    n = _kv4_args(cache, block_table, seq_lens, q_start, cfg)
+    dt = _dtype(k.dtype, "k")
+    kt, kh = _heads(k, "k", cfg.kv_heads, cfg.head_dim)
+    vt, vh = _heads(v, "v", cfg.kv_heads, cfg.head_dim, k.dtype)
+    if v.shape[0] != k.shape[0]:
+        raise ValueError("k and v differ in tokens")
+    if k.shape[0] == 0 or n == 0:
+        return
+    st = lib().awq_kv4_append(_ptr(k), kt, kh, _ptr(v), vt, vh, k.shape[0], dt, _ptr(cache),
+                              cache.shape[0], _ptr(block_table), n, block_table.shape[1],
+                              _ptr(seq_lens), _ptr(q_start), ctypes.byref(cfg), _stream_ptr(stream))
+    _check(st, "awq_kv4_append")
+
+
+@_on_stream
+def awq_kv4_read(cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                 q_start: torch.Tensor, cfg: awq_kv4_config, n_tokens: int,
+                 dtype: torch.dtype = torch.float16, stream=None):
+    """The stored keys and values of the same rows as awq_kv4_append: two tensors
+    [n_tokens, kv_heads, head_dim] of dtype (zeros where no such token exists)."""
+    n = _kv4_args(cache, block_table, seq_lens, q_start, cfg)
+    dt = _dtype(dtype, "dtype")
+    shape = (n_tokens, cfg.kv_heads, cfg.head_dim)
+    k = torch.empty(shape, dtype=dtype, device=cache.device)
+    v = torch.empty(shape, dtype=dtype, device=cache.device)
+    if n_tokens == 0:
+        return k, v
+    if n == 0:
+        return k.zero_(), v.zero_()
+    st = lib().awq_kv4_read(_ptr(cache), cache.shape[0], _ptr(block_table), n, block_table.shape[1],
+                            _ptr(seq_lens), _ptr(q_start), n_tokens, ctypes.byref(cfg), dt, _ptr(k),
+                            _ptr(v), _stream_ptr(stream))
+    _check(st, "awq_kv4_read")
+    return k, v
+
+
+def awq_kv4_attention_workspace_bytes(n_tokens: int, n_seqs: int, heads: int, cfg: awq_kv4_config,
+                                      max_q: int, max_len: int) -> int:
+    return int(lib().awq_kv4_attention_workspace_bytes(n_tokens, n_seqs, heads, ctypes.byref(cfg),
+                                                       max_q, max_len))
+
+
+@_on_stream
+def awq_kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
+                      seq_lens: torch.Tensor, q_start: torch.Tensor, cfg: awq_kv4_config, *,
+                      max_q: int, max_len: int, scale: Optional[float] = None, window: int = 0,
+                      out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                      stream=None):
+    """Causal attention of q (fp16 or bf16 [T, heads, head_dim]) over the cache: returns out
+    [T, heads, head_dim] in q's type and lse fp32 [T, heads].  max_q and max_len are host
+    bounds on the rows of a sequence and on seq_lens; scale defaults to 1 / sqrt(head_dim);
+    window > 0 keeps the last `window` keys of each row.  Rows without keys give 0 and -inf.
+    A workspace (see awq_kv4_attention_workspace_bytes) is allocated unless one is passed."""
+    n = _kv4_args(cache, block_table, seq_lens, q_start, cfg)
+    dt = _dtype(q.dtype, "q")
+    qt, qh = _heads(q, "q", None, cfg.head_dim)
+    T, H = q.shape[0], q.shape[1]
+    if out is None:
+        out = torch.empty((T, H, cfg.head_dim), dtype=q.dtype, device=q.device)
+    else:
+        _dev(out, q.dtype, "out", (T, H, cfg.head_dim))
+    lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+    if T == 0 or n == 0:
+        return out, lse
+    ws, nw = _workspace(workspace,
+                        awq_kv4_attention_workspace_bytes(T, n, H, cfg, max_q, max_len), q.device)
+    st = lib().awq_kv4_attention(_ptr(q), qt, qh, T, H, dt, _ptr(cache), cache.shape[0],
+                                 _ptr(block_table), n, block_table.shape[1], _ptr(seq_lens),
+                                 _ptr(q_start), ctypes.byref(cfg), max_q, max_len,
+                                 float(cfg.head_dim ** -0.5 if scale is None else scale), int(window),
+                                 _ptr(out), _ptr(lse), _addr(ws, out), nw, _stream_ptr(stream))
+    _check(st, "awq_kv4_attention")
+    return out, lse

@@ -1,0 +1,638 @@
+// Attention over the 4-bit key/value cache.
+//
+//   s_t = scale q . k_t,  k_t = step_t (c_t - z_t)  =>  s_t = scale step_t (q . c_t - z_t sum q)
+//   out = sum_t e^{s_t} v_t / sum_t e^{s_t},  v_t = step'_t (c'_t - z'_t)
+//       = (sum_t w_t c'_t - sum_t w_t z'_t) / sum_t e^{s_t},  w_t = e^{s_t} step'_t
+// (per group of channels for the steps and zeros).  So the matrix cores multiply the raw codes,
+// and step and zero enter once per score instead of once per channel.
+//
+// Pages: kwkr.cn AWQ 技术解析 §1.2, §4.2 (dequantisation fused into the product), lnrq.cn §四
+// (decoding is bound by reading what was quantised).
+//
+// Codes as operands: a nibble in the top four mantissa bits of a fp16 pattern whose other bits
+// are those of 16.0 is the number 16 + c, exactly: a shift and a v_and_or per pair of codes.
+// The 16 goes into the zeros' sums.  (Lower bits would save shifts and cost accuracy: 64 + c or
+// 1024 + c cancel more of the fp32 sums, and the subnormals c 2^-24 lose their leading zeros in
+// the matrix cores, which align the terms of a sum by their exponent fields: 2^-17 of the sum,
+// measured.)  The cache's word order (awq_serve.h) is the operand order of these instructions.
+//
+// One wave, one tile of 32 keys, 16 columns (query rows x heads of the key head):
+//   S = K Q^T   two 16 x 16 results; result row 4 q + e of result j is key 8 q + 4 j + e, so that
+//               lane (column h, q) ends with the scores of keys 8 q .. 8 q + 7 of its column,
+//               which is the layout of an operand of the next product: no data moves between
+//               lanes.
+//   O = V^T W   D / 16 results, row 4 q + e of result n is channel 16 n + 4 q + e.
+// The running maximum is per column; weights are scaled by 2^f with f so chosen from the
+// largest value step seen that w 2^f stays below 2^15: fp16 holds them with full precision
+// down to 2^-29 of the largest.  A rise of the maximum or of that step multiplies what was
+// summed so far by exp2 of the difference.
+//
+// Few columns (decode): the four waves of a block take the tiles in turn and add their results
+// through LDS; long sequences are split over blocks and joined by a second launch.  Many
+// columns (prompts): each wave keeps NC column tiles and walks all keys itself.
+#include <hip/hip_runtime.h>
+
+#include "int8_quant.h"
+#include "kv4_cache.h"
+
+namespace awq {
+
+namespace {
+
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef _Float16 half8v __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kNegInf = -__builtin_inff();
+constexpr int kWaves = 4;
+
+__device__ __forceinline__ float max_q(float v) {  // over the four lanes of a column
+  v = fmaxf(v, __shfl_xor(v, 16));
+  return fmaxf(v, __shfl_xor(v, 32));
+}
+__device__ __forceinline__ float sum_q(float v) {
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
+// The operand pairs of one word: nibbles (n, n + 4) for n = 0..3, each as 16 + c.
+constexpr uint32_t kNibble = 0x03C003C0u, kOffset = 0x4C004C00u;
+constexpr float kOffsetF = 16.0f;
+template <int N>
+__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
+  constexpr int S = 6 - 4 * N;
+  return ((S > 0 ? w << (S > 0 ? S : 0) : w >> (S > 0 ? 0 : -S)) & kNibble) | kOffset;
+}
+__device__ __forceinline__ half8v word_operand(uint32_t w) {
+  const u32x4 v = {code_pair<0>(w), code_pair<1>(w), code_pair<2>(w), code_pair<3>(w)};
+  return __builtin_bit_cast(half8v, v);
+}
+
+// exponent e with 2^e <= v < 2^(e+1), for a positive normal v
+__device__ __forceinline__ int exponent_of(float v) {
+  return (int)(__builtin_bit_cast(uint32_t, v) >> 23 & 255u) - 127;
+}
+
+template <int D, int GS>
+struct Geo {
+  static constexpr int G = D / GS;          // groups
+  static constexpr int KW = D / 32;         // code words of a key and lane
+  static constexpr int WPG = GS / 32;       // of them, words a group
+  static constexpr int H = D / 64;          // 16-byte pieces of a lane's values of 8 tokens
+  static constexpr int N = D / 16;          // value results
+};
+
+// Codes and parameters of one tile, one lane's part.
+template <int D, int GS>
+struct TileRegs {
+  using X = Geo<D, GS>;
+  uint32_t k[2][X::KW];
+  u32x4 v[X::H];
+  u32x4 kp[X::G][2], vp[X::G][2];
+};
+
+template <int D, int GS>
+__device__ __forceinline__ void load_tile(TileRegs<D, GS>& r, const uint8_t* ra, const uint8_t* rb,
+                                          int oa, int ob, int P, int lane) {
+  using X = Geo<D, GS>;
+  const int lr = lane & 15, q = lane >> 4;
+  {
+    const uint8_t* rec = (lr >> 3) ? rb : ra;
+    const int off = ((lr >> 3) ? ob : oa) + 8 * ((lr >> 2) & 1) + (lr & 3);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint8_t* p = rec + (off + 4 * j) * (D / 2) + q * (D / 8);
+      if constexpr (X::KW == 2) {
+        const uint2 w = *(const uint2*)p;
+        r.k[j][0] = w.x;
+        r.k[j][1] = w.y;
+      } else {
+#pragma unroll
+        for (int i = 0; i < X::KW / 4; ++i) {
+          const u32x4 w = *(const u32x4*)(p + 16 * i);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) r.k[j][4 * i + e] = w[e];
+        }
+      }
+    }
+  }
+  const uint8_t* rec = (q >> 1) ? rb : ra;
+  const int off = ((q >> 1) ? ob : oa) + 8 * (q & 1);
+  const uint8_t* vb = rec + P * (D / 2) + (off >> 3) * (4 * D) + lr * 16;
+#pragma unroll
+  for (int h = 0; h < X::H; ++h) r.v[h] = *(const u32x4*)(vb + 256 * h);
+  const uint8_t* par = rec + P * D + 4 * off;
+#pragma unroll
+  for (int g = 0; g < X::G; ++g)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      r.kp[g][i] = *(const u32x4*)(par + 4 * P * g + 16 * i);
+      r.vp[g][i] = *(const u32x4*)(par + 4 * P * (X::G + g) + 16 * i);
+    }
+}
+
+// A column tile's state in one wave.
+template <int D, int GS>
+struct Column {
+  using X = Geo<D, GS>;
+  half8v q[X::KW];     // operands of S, in word order
+  float qsum[X::G];    // sum of a group's q
+  float sigma;         // from the raw score to log2 units
+  int pos;             // the row's position; -1: no row
+  float m;             // running maximum of the scores, log2 units
+  float M;             // m - f: what the exponents are taken against
+  float l;             // this lane's sum of exp2(s - M)
+  f32x4 z[X::G];       // sum of weight x (zero + 16): every row the same
+  f32x4 o[X::N];
+};
+
+// One row of q as operands: scaled by a power of two so that its largest magnitude lies in
+// [2^8, 2^9), then rounded to fp16 (exact but for what lies 2^-24 and more below the largest).
+template <int D, int GS>
+__device__ __forceinline__ void load_query(Column<D, GS>& c, const uint16_t* row, bool bf16,
+                                           int q, float scale) {
+  using X = Geo<D, GS>;
+  float v[X::KW][8];
+  float top = 0.0f;
+#pragma unroll
+  for (int w = 0; w < X::KW; ++w) {
+    const int c0 = (w / X::WPG) * GS + q * (GS / 4) + (w % X::WPG) * 8;
+    if (row) {
+      if (bf16) load_row8<true, true>(row, nullptr, kFoldNone, c0, D, v[w]);
+      else load_row8<false, true>(row, nullptr, kFoldNone, c0, D, v[w]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[w][i] = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[w][i]));
+  }
+  top = max_q(top);
+  // a row of zeros or one with infinities is left as it is
+  int e = top >= 0x1p-126f && top < __builtin_inff() ? 8 - exponent_of(top) : 0;
+  e = min(max(e, -100), 100);
+  c.sigma = ldexpf(scale * 1.44269504088896340736f, -e);
+#pragma unroll
+  for (int g = 0; g < X::G; ++g) c.qsum[g] = 0.0f;
+#pragma unroll
+  for (int w = 0; w < X::KW; ++w) {
+    half8v h;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const _Float16 lo = (_Float16)ldexpf(v[w][n], e), hi = (_Float16)ldexpf(v[w][n + 4], e);
+      h[2 * n] = lo;
+      h[2 * n + 1] = hi;
+      c.qsum[w / X::WPG] += (float)lo + (float)hi;
+    }
+    c.q[w] = h;
+  }
+#pragma unroll
+  for (int g = 0; g < X::G; ++g) {
+    c.qsum[g] = sum_q(c.qsum[g]);
+    c.z[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  c.m = kNegInf;
+  c.M = kNegInf;
+  c.l = 0.0f;
+#pragma unroll
+  for (int n = 0; n < X::N; ++n) c.o[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+}
+
+// Two floats as a pair of fp16, nearest even.
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pair16(float x, float y) {
+  const f32x2 v = {x, y};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, half2v));
+}
+
+__device__ __forceinline__ float lo16(uint32_t w) { return h2f((uint16_t)w); }
+__device__ __forceinline__ float hi16(uint32_t w) { return h2f((uint16_t)(w >> 16)); }
+
+// One tile of 32 keys for NC column tiles.  MASKED: some (key, column) pairs do not exist;
+// key0 is the tile's first key, lo_off = window - 1 (or a huge number) so that column pos sees
+// keys [pos - lo_off, pos]; dead: bit x set if the keys of half x lie on no page.
+template <int D, int GS, int NC, bool MASKED>
+__device__ __forceinline__ void do_tile(TileRegs<D, GS>& r, Column<D, GS> (&col)[NC], int key0,
+                                        int n_keys, int lo_off, int dead, float& f, int lane) {
+  using X = Geo<D, GS>;
+  const int q = lane >> 4;
+  const int kq = key0 + 8 * q;
+  if constexpr (MASKED) {
+    // parameters of keys that do not exist may hold anything
+#pragma unroll
+    for (int g = 0; g < X::G; ++g)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const bool ok = kq + e < n_keys && !((dead >> (q >> 1)) & 1);
+        r.kp[g][e >> 2][e & 3] = ok ? r.kp[g][e >> 2][e & 3] : 0u;
+        r.vp[g][e >> 2][e & 3] = ok ? r.vp[g][e >> 2][e & 3] : 0u;
+      }
+  }
+  // largest value step of the tile (non-finite ones count as the largest finite)
+  uint32_t top = 0;
+#pragma unroll
+  for (int g = 0; g < X::G; ++g)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, r.vp[g][e >> 2][e & 3] & 0x7fffu);
+  top = max(top, (uint32_t)__shfl_xor((int)top, 16));
+  top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+  // 2^f: 2^14 over the step's power of two (a zero or subnormal step counts as the smallest
+  // normal one)
+  const int ex = (int)(min(max(top, 0x0400u), 0x7bffu) >> 10) - 15;
+  const float ft = (float)(14 - ex);
+  const bool fnew = ft < f;
+  f = fminf(f, ft);
+
+#pragma unroll
+  for (int t = 0; t < NC; ++t) {
+    Column<D, GS>& c = col[t];
+    float s[8];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+      for (int g = 0; g < X::G; ++g) {
+        f32x4 a = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int u = 0; u < X::WPG; ++u)
+          a = __builtin_amdgcn_mfma_f32_16x16x32_f16(word_operand(r.k[j][g * X::WPG + u]),
+                                                     c.q[g * X::WPG + u], a, 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t w = r.kp[g][j][e];
+          const float x = fmaf(-(hi16(w) + kOffsetF), c.qsum[g], a[e]);
+          s[4 * j + e] = g == 0 ? lo16(w) * x : fmaf(lo16(w), x, s[4 * j + e]);
+        }
+      }
+    }
+    bool ok[8];
+    if constexpr (MASKED) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int key = kq + e;
+        ok[e] = key <= c.pos && key >= c.pos - lo_off && key < n_keys && !((dead >> (q >> 1)) & 1);
+        s[e] = ok[e] ? s[e] : kNegInf;
+      }
+    }
+    float mx = s[0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) mx = fmaxf(mx, s[e]);
+    mx = max_q(mx) * c.sigma;
+    const bool up = mx > c.m;
+    if (__any(up || fnew)) {
+      const float m = fmaxf(c.m, mx);
+      // no key yet: nothing is summed, any finite reference will do
+      const float M = m == kNegInf ? kNegInf : m - f;
+      const float a = c.M == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(c.M - M);
+      c.m = m;
+      c.M = M;
+      c.l *= a;
+#pragma unroll
+      for (int g = 0; g < X::G; ++g)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c.z[g][e] *= a;
+#pragma unroll
+      for (int n = 0; n < X::N; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c.o[n][e] *= a;
+    }
+    const float M = c.M == kNegInf ? 0.0f : c.M;
+    float p[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      p[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c.sigma, -M));
+      c.l += p[e];
+    }
+#pragma unroll
+    for (int g = 0; g < X::G; ++g) {
+      u32x4 w, zo;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t pa = r.vp[g][i >> 1][2 * (i & 1)], pb = r.vp[g][i >> 1][2 * (i & 1) + 1];
+        float x = p[2 * i] * lo16(pa), y = p[2 * i + 1] * lo16(pb);
+        if constexpr (MASKED) {  // a masked key's step may be NaN
+          x = ok[2 * i] ? x : 0.0f;
+          y = ok[2 * i + 1] ? y : 0.0f;
+        }
+        w[i] = pair16(x, y);
+        // zeros + 16, exact in fp16
+        zo[i] = __builtin_bit_cast(uint32_t,
+                                   __builtin_bit_cast(half2v, (pa >> 16) | (pb & 0xffff0000u)) +
+                                       __builtin_bit_cast(half2v, kOffset));
+      }
+      // the zeros' sum by the same instruction as the codes' (an operand whose 16 rows are
+      // equal), so that what the two sums share cancels as it was rounded
+      c.z[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8v, zo),
+                                                      __builtin_bit_cast(half8v, w), c.z[g], 0, 0, 0);
+#pragma unroll
+      for (int n = g * (GS / 16); n < (g + 1) * (GS / 16); ++n) {
+        const u32x4 vw = r.v[n >> 2];
+        u32x4 a;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          a[i] = (n & 3) == 0   ? code_pair<0>(vw[i])
+                 : (n & 3) == 1 ? code_pair<1>(vw[i])
+                 : (n & 3) == 2 ? code_pair<2>(vw[i])
+                                : code_pair<3>(vw[i]);
+        c.o[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8v, a),
+                                                       __builtin_bit_cast(half8v, w), c.o[n], 0, 0, 0);
+      }
+    }
+  }
+}
+
+// Results of a column tile: sums over the column's lanes, the zeros subtracted.  o is then sum_t w_t (c - z), l the weights' sum, both over exp2(M).
+template <int D, int GS>
+__device__ __forceinline__ void finish(Column<D, GS>& c) {
+  using X = Geo<D, GS>;
+  c.l = sum_q(c.l);
+#pragma unroll
+  for (int g = 0; g < X::G; ++g) {
+#pragma unroll
+    for (int n = g * (GS / 16); n < (g + 1) * (GS / 16); ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c.o[n][e] -= c.z[g][e];
+  }
+}
+
+__device__ __forceinline__ void store4(void* out, int64_t at, bool bf16, const float (&v)[4]) {
+  uint2 w;
+  if (bf16) {
+    w.x = to16<true>(v[0]) | ((uint32_t)to16<true>(v[1]) << 16);
+    w.y = to16<true>(v[2]) | ((uint32_t)to16<true>(v[3]) << 16);
+  } else {
+    w.x = to16<false>(v[0]) | ((uint32_t)to16<false>(v[1]) << 16);
+    w.y = to16<false>(v[2]) | ((uint32_t)to16<false>(v[3]) << 16);
+  }
+  *(uint2*)((uint16_t*)out + at) = w;
+}
+
+__device__ __forceinline__ float lse_of(float M, float l) {
+  return l == 0.0f ? kNegInf : (M + __builtin_amdgcn_logf(l)) * 0.69314718055994530942f;
+}
+
+// Workspace of a split call: o fp32 [rows][splits][D], then (M, l) [rows][splits] with rows =
+// (token, head).
+struct Partials {
+  float* o;
+  float* ml;
+  int splits;
+};
+
+// column tiles a wave of the WIDE form keeps (two do not fit the registers with four groups of
+// 32 channels)
+constexpr int wide_tiles(int dim, int group) { return dim / group > 2 ? 1 : 2; }
+
+// NC column tiles a wave; WIDE: the waves of a block hold different columns and walk all keys,
+// otherwise they share the columns and take the tiles in turn.
+template <int D, int GS, int NC, bool WIDE>
+__global__ __launch_bounds__(64 * kWaves) void k_kv4_attention(Kv4Cache c, Kv4Query a,
+                                                               Partials part) {
+  using X = Geo<D, GS>;
+  constexpr int kCols = 16 * NC * (WIDE ? kWaves : 1);  // columns a block
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int b = blockIdx.z, kvh = blockIdx.y % c.kv_heads;
+  const int split = blockIdx.y / c.kv_heads;
+  // later column tiles see more keys: they go first
+  const int tile = gridDim.x - 1 - blockIdx.x;
+  const int group = a.heads / c.kv_heads;
+  const int row0 = c.starts[b];
+  const int rows = min(c.starts[b + 1] - row0, a.max_q);
+  const int len0 = c.lens[b];
+  const int n_cols = rows * group;
+  if (tile * kCols >= n_cols) return;  // the whole block
+  const int P = 1 << c.log2p;
+  // keys that are there: bounded by the table and by the caller's bound
+  const int cap = (int)min((int64_t)c.max_blocks << c.log2p, (int64_t)a.max_len);
+  const int len = min(len0, cap);
+
+  Column<D, GS> col[NC];
+  const int col0 = tile * kCols + (WIDE ? wave * 16 * NC : 0);
+#pragma unroll
+  for (int t = 0; t < NC; ++t) {
+    const int x = col0 + 16 * t + (lane & 15);
+    const int i = x / group, h = x - i * group;
+    const bool has = x < n_cols;
+    const uint16_t* row =
+        has ? (const uint16_t*)a.q + (int64_t)(row0 + i) * a.qt + (int64_t)(kvh * group + h) * a.qh
+            : nullptr;
+    load_query<D, GS>(col[t], row, a.bf16, lane >> 4, a.scale);
+    col[t].pos = has ? len0 - (c.starts[b + 1] - row0) + i : -1;
+  }
+  // keys that some column of the block (WIDE: of the wave) sees
+  const int lo_off = a.window > 0 ? a.window - 1 : 0x3fffffff;
+  const int first_i = col0 / group;
+  const int last_i = min(col0 + 16 * NC - 1, n_cols - 1) / group;
+  const int pos0 = len0 - (c.starts[b + 1] - row0);
+  const int end = min(len, pos0 + last_i + 1);  // may be <= 0
+  const int begin = max(0, pos0 + first_i - lo_off);
+  int t_lo = begin >> 5, t_hi = max(0, end + 31) >> 5;
+  if (col0 >= n_cols) t_hi = t_lo;  // WIDE: a wave past the last column
+  {
+    // this split's share of the tiles
+    const int n = max(0, t_hi - t_lo), s = part.splits;
+    const int lo = t_lo + (int)((int64_t)n * split / s), hi = t_lo + (int)((int64_t)n * (split + 1) / s);
+    t_lo = lo;
+    t_hi = hi;
+  }
+  const int32_t* table = c.table + (int64_t)b * c.max_blocks;
+  const int last_blk = max(0, (len - 1) >> c.log2p);
+  auto page_of = [&](int key, int& bad) -> const uint8_t* {
+    const int pg = table[min(key >> c.log2p, last_blk)];
+    bad = pg < 0 || pg >= c.n_pages;
+    return c.pages + ((int64_t)(bad ? 0 : pg) * c.kv_heads + kvh) * (int64_t)c.record;
+  };
+  float f = 64.0f;
+  const int step = WIDE ? 1 : kWaves;
+  const int first = t_lo + (WIDE ? 0 : wave);
+  for (int t = first; t < t_hi; t += step) {
+    const int key0 = 32 * t;
+    int bad_a, bad_b;
+    const uint8_t* ra = page_of(key0, bad_a);
+    const uint8_t* rb = page_of(key0 + 16, bad_b);
+    TileRegs<D, GS> r;
+    load_tile<D, GS>(r, ra, rb, key0 & (P - 1), (key0 + 16) & (P - 1), P, lane);
+    const int dead = bad_a | (bad_b << 1);
+    // every key of the tile exists and every column sees all of it
+    const bool whole = !dead && key0 + 32 <= len && key0 + 31 <= pos0 + first_i &&
+                       key0 >= pos0 + last_i - lo_off;
+    if (whole) do_tile<D, GS, NC, false>(r, col, key0, len, lo_off, dead, f, lane);
+    else do_tile<D, GS, NC, true>(r, col, key0, len, lo_off, dead, f, lane);
+  }
+
+#pragma unroll
+  for (int t = 0; t < NC; ++t) finish<D, GS>(col[t]);
+
+  if constexpr (WIDE) {
+#pragma unroll
+    for (int t = 0; t < NC; ++t) {
+      const int x = col0 + 16 * t + (lane & 15);
+      if (x < n_cols) {
+        const int i = x / group, h = x - i * group;
+        const int64_t r = (int64_t)(row0 + i) * a.heads + kvh * group + h;
+        const Column<D, GS>& cc = col[t];
+        const bool join = part.splits > 1;
+        const float inv = join ? 1.0f : cc.l == 0.0f ? 0.0f : 1.0f / cc.l;
+#pragma unroll
+        for (int n = 0; n < X::N; ++n) {
+          const int ch = 16 * n + 4 * (lane >> 4);
+          if (join) {
+            *(f32x4*)(part.o + (r * part.splits + split) * D + ch) = cc.o[n];
+          } else {
+            const float v[4] = {cc.o[n][0] * inv, cc.o[n][1] * inv, cc.o[n][2] * inv, cc.o[n][3] * inv};
+            store4(a.out, r * D + ch, a.bf16, v);
+          }
+        }
+        if ((lane >> 4) == 0) {
+          if (join) {
+            part.ml[(r * part.splits + split) * 2] = cc.M;
+            part.ml[(r * part.splits + split) * 2 + 1] = cc.l;
+          } else if (a.lse) {
+            a.lse[r] = lse_of(cc.M, cc.l);
+          }
+        }
+      }
+    }
+  } else {
+    // the waves' results joined in wave order: each scaled to the block's largest M
+    __shared__ float so[kWaves][16][D + 4];
+    __shared__ float sm[kWaves][16], sl[kWaves][16];
+#pragma unroll
+    for (int t = 0; t < NC; ++t) {
+      const int x = lane & 15;
+      if (t > 0) __syncthreads();
+#pragma unroll
+      for (int n = 0; n < X::N; ++n) *(f32x4*)&so[wave][x][16 * n + 4 * (lane >> 4)] = col[t].o[n];
+      if ((lane >> 4) == 0) {
+        sm[wave][x] = col[t].M;
+        sl[wave][x] = col[t].l;
+      }
+      __syncthreads();
+      // thread -> column, 4 channels at a time
+      for (int w = threadIdx.x; w < 16 * (D / 4); w += 64 * kWaves) {
+        const int cx = w / (D / 4), ch = (w % (D / 4)) * 4;
+        const int xx = col0 + 16 * t + cx;
+        if (xx >= n_cols) continue;
+        float M = sm[0][cx];
+#pragma unroll
+        for (int i = 1; i < kWaves; ++i) M = fmaxf(M, sm[i][cx]);
+        float l = 0.0f;
+        f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) {
+          if (sm[i][cx] == kNegInf) continue;
+          const float k = __builtin_amdgcn_exp2f(sm[i][cx] - M);
+          l = fmaf(sl[i][cx], k, l);
+          const f32x4 v = *(const f32x4*)&so[i][cx][ch];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = fmaf(v[e], k, o[e]);
+        }
+        const int i = xx / group, h = xx - i * group;
+        const int64_t r = (int64_t)(row0 + i) * a.heads + kvh * group + h;
+        if (part.splits > 1) {
+          *(f32x4*)(part.o + (r * part.splits + split) * D + ch) = o;
+          if (ch == 0) {
+            part.ml[(r * part.splits + split) * 2] = M;
+            part.ml[(r * part.splits + split) * 2 + 1] = l;
+          }
+        } else {
+          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+          const float v[4] = {o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
+          store4(a.out, r * D + ch, a.bf16, v);
+          if (ch == 0 && a.lse) a.lse[r] = lse_of(M, l);
+        }
+      }
+    }
+  }
+}
+
+// Joins the splits of one (token, head) a wave, in split order.
+__global__ __launch_bounds__(256) void k_kv4_join(Kv4Cache c, Kv4Query a, Partials part, int D,
+                                                  int64_t n_rows) {
+  const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (r >= n_rows) return;
+  const int64_t t = r / a.heads;
+  const int b = kv4_sequence(c, t);
+  if (b < 0 || t - c.starts[b] >= a.max_q) return;  // no such row: its partials were not written
+  const float* ml = part.ml + r * part.splits * 2;
+  float M = kNegInf;
+  for (int s = lane; s < part.splits; s += 64) M = fmaxf(M, ml[2 * s]);
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off));
+  const int per = D / 64;  // channels a lane: 1, 2 or 4
+  float l = 0.0f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  const float* po = part.o + r * part.splits * D + lane * per;
+  for (int s = 0; s < part.splits; ++s) {
+    const float ms = ml[2 * s];
+    if (ms == kNegInf) continue;
+    const float k = __builtin_amdgcn_exp2f(ms - M);
+    l = fmaf(ml[2 * s + 1], k, l);
+    for (int e = 0; e < per; ++e) o[e] = fmaf(po[(int64_t)s * D + e], k, o[e]);
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  uint16_t* out = (uint16_t*)a.out + r * D + lane * per;
+  for (int e = 0; e < per; ++e) out[e] = a.bf16 ? to16<true>(o[e] * inv) : to16<false>(o[e] * inv);
+  if (lane == 0 && a.lse) a.lse[r] = lse_of(M, l);
+}
+
+template <int D, int GS>
+hipError_t launch_dg(const Kv4Cache& c, const Kv4Query& q, const Kv4Plan& p, const Partials& part,
+                     hipStream_t stream) {
+  const dim3 grid((unsigned)p.tiles, (unsigned)(c.kv_heads * p.splits), (unsigned)c.n_seqs);
+  if (p.wide)
+    hipLaunchKernelGGL((k_kv4_attention<D, GS, wide_tiles(D, GS), true>), grid, dim3(64 * kWaves), 0, stream, c, q, part);
+  else
+    hipLaunchKernelGGL((k_kv4_attention<D, GS, 1, false>), grid, dim3(64 * kWaves), 0, stream, c, q, part);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+Kv4Plan kv4_plan(int64_t n_seqs, int heads, int kv_heads, int dim, int group, int64_t max_q,
+                 int64_t max_len) {
+  Kv4Plan p;
+  const int64_t cols = max_q * (heads / kv_heads);
+  p.wide = cols > 16;
+  const int64_t per = p.wide ? 16 * wide_tiles(dim, group) * kWaves : 16;
+  p.tiles = (int)((cols + per - 1) / per);
+  const int64_t blocks = n_seqs * kv_heads * p.tiles;
+  // four blocks a compute unit, at least 256 keys a split
+  int64_t s = (1024 + blocks - 1) / blocks;
+  const int64_t most = (max_len + 255) / 256;
+  if (s > most) s = most;
+  if (kv_heads * s > 65535) s = 65535 / kv_heads;
+  p.splits = (int)(s < 1 ? 1 : s);
+  return p;
+}
+
+size_t kv4_workspace(const Kv4Plan& p, int64_t n_tokens, int heads, int dim) {
+  if (p.splits <= 1) return 0;
+  return (size_t)n_tokens * heads * p.splits * (dim + 2) * sizeof(float);
+}
+
+hipError_t launch_kv4_attention(const Kv4Cache& c, const Kv4Query& q, const Kv4Plan& p,
+                                void* workspace, hipStream_t stream) {
+  const int64_t rows = q.n_tokens * q.heads;
+  if (rows <= 0 || c.n_seqs <= 0) return hipSuccess;
+  Partials part;
+  part.splits = p.splits;
+  part.o = (float*)workspace;
+  part.ml = part.o + rows * p.splits * c.dim;
+  hipError_t e;
+  switch (c.dim * 1000 + c.group) {
+    case 64032: e = launch_dg<64, 32>(c, q, p, part, stream); break;
+    case 64064: e = launch_dg<64, 64>(c, q, p, part, stream); break;
+    case 128032: e = launch_dg<128, 32>(c, q, p, part, stream); break;
+    case 128064: e = launch_dg<128, 64>(c, q, p, part, stream); break;
+    case 128128: e = launch_dg<128, 128>(c, q, p, part, stream); break;
+    default: return hipErrorInvalidValue;
+  }
+  if (e != hipSuccess || p.splits <= 1) return e;
+  hipLaunchKernelGGL(k_kv4_join, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, c, q, part,
+                     c.dim, rows);
+  return hipGetLastError();
+}
+
+}  // namespace awq

@@ -5,6 +5,8 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <initializer_list>
+
 #include "awq_serve.h"
 #include "serve_internal.h"
 
@@ -134,6 +136,157 @@ int awq_int8_linear(const void* x, int64_t ldx, const float* s, int64_t n_tokens
   const awq::Int8Args a{xq, round16(K), xstep, wq, ldw, wstep, bias, y, ldy,
                         (int)T, (int)M, (int)round16(K), dtype == AWQ_BF16};
   return hip_status(awq::launch_int8_matmul(a, ws, (hipStream_t)stream));
+}
+
+namespace {
+
+bool kv4_valid(const awq_kv4_config* c) {
+  if (!c) return false;
+  if (c->head_dim != 64 && c->head_dim != 128) return false;
+  if (c->kv_heads < 1 || c->kv_heads > 65535) return false;
+  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return false;
+  if (c->group_size != 32 && c->group_size != 64 && c->group_size != 128) return false;
+  if (c->group_size > c->head_dim) return false;
+  return c->zero_point == 0 || c->zero_point == 1;
+}
+
+// Sizes common to the cache's calls; fills the launch description.
+int kv4_cache(const void* cache, int64_t n_pages, const int32_t* table, int64_t n_seqs,
+              int64_t max_blocks, const int32_t* lens, const int32_t* starts, int64_t n_tokens,
+              const awq_kv4_config* cfg, awq::Kv4Cache* out) {
+  if (!cache || !table || !lens || !starts || !cfg) return AWQ_E_NULL;
+  if (!kv4_valid(cfg)) return AWQ_E_CONFIG;
+  // n_seqs is a grid dimension; positions are 32-bit
+  if (n_pages < 1 || n_pages > 0x7fffffff || n_seqs < 0 || n_seqs > 65535 || max_blocks < 1 ||
+      max_blocks > 0x7fffffff / cfg->page_size || n_tokens < 0 || n_tokens > kMaxRows)
+    return AWQ_E_SHAPE;
+  if (!aligned(cache, 16) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(starts, 4))
+    return AWQ_E_ALIGN;
+  int log2p = 0;
+  while ((1 << log2p) < cfg->page_size) ++log2p;
+  *out = awq::Kv4Cache{(uint8_t*)cache, n_pages, table, lens, starts, (int)n_seqs, (int)max_blocks,
+                       cfg->kv_heads, cfg->head_dim, cfg->group_size, log2p, cfg->zero_point,
+                       awq::kv4_record(cfg->head_dim, cfg->group_size, cfg->page_size)};
+  return AWQ_OK;
+}
+
+// Rows of heads: 16-byte pieces from any (token, head); spans stay far from 64-bit overflow.
+int kv4_rows(const void* p, int64_t token_stride, int64_t head_stride) {
+  if (token_stride < 0 || head_stride < 0 || token_stride % 8 || head_stride % 8 ||
+      token_stride > ((int64_t)1 << 31) || head_stride > ((int64_t)1 << 31))
+    return AWQ_E_SHAPE;
+  return aligned(p, 16) ? AWQ_OK : AWQ_E_ALIGN;
+}
+
+}  // namespace
+
+size_t awq_kv4_record_bytes(const awq_kv4_config* cfg) {
+  return kv4_valid(cfg) ? awq::kv4_record(cfg->head_dim, cfg->group_size, cfg->page_size) : 0;
+}
+
+int awq_kv4_append(const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                   int64_t v_token_stride, int64_t v_head_stride, int64_t n_tokens, int32_t dtype,
+                   void* cache, int64_t n_pages, const int32_t* block_table, int64_t n_seqs,
+                   int64_t max_blocks, const int32_t* seq_lens, const int32_t* q_start,
+                   const awq_kv4_config* cfg, void* stream) {
+  if (!k || !v) return AWQ_E_NULL;
+  awq::Kv4Cache c;
+  int st = kv4_cache(cache, n_pages, block_table, n_seqs, max_blocks, seq_lens, q_start, n_tokens,
+                     cfg, &c);
+  if (st) return st;
+  if (!dtype_valid(dtype)) return AWQ_E_CONFIG;
+  if ((st = kv4_rows(k, k_token_stride, k_head_stride)) ||
+      (st = kv4_rows(v, v_token_stride, v_head_stride)))
+    return st;
+  if (n_tokens == 0 || n_seqs == 0) return AWQ_OK;
+  if (n_tokens > ((int64_t)1 << 38) / ((int64_t)cfg->kv_heads * cfg->head_dim)) return AWQ_E_SHAPE;
+  if ((st = device_ptrs({k, v, cache, block_table, seq_lens, q_start}))) return st;
+  clear_pending_error();
+  return hip_status(awq::launch_kv4_append(c, k, k_token_stride, k_head_stride, v, v_token_stride,
+                                           v_head_stride, n_tokens, dtype == AWQ_BF16,
+                                           (hipStream_t)stream));
+}
+
+int awq_kv4_read(const void* cache, int64_t n_pages, const int32_t* block_table, int64_t n_seqs,
+                 int64_t max_blocks, const int32_t* seq_lens, const int32_t* q_start,
+                 int64_t n_tokens, const awq_kv4_config* cfg, int32_t dtype, void* k_out,
+                 void* v_out, void* stream) {
+  if (!k_out || !v_out) return AWQ_E_NULL;
+  awq::Kv4Cache c;
+  int st = kv4_cache(cache, n_pages, block_table, n_seqs, max_blocks, seq_lens, q_start, n_tokens,
+                     cfg, &c);
+  if (st) return st;
+  if (!dtype_valid(dtype)) return AWQ_E_CONFIG;
+  if (!aligned(k_out, 16) || !aligned(v_out, 16)) return AWQ_E_ALIGN;
+  if (n_tokens == 0) return AWQ_OK;
+  if (n_tokens > ((int64_t)1 << 38) / ((int64_t)cfg->kv_heads * cfg->head_dim)) return AWQ_E_SHAPE;
+  if ((st = device_ptrs({cache, block_table, seq_lens, q_start, k_out, v_out}))) return st;
+  clear_pending_error();
+  return hip_status(awq::launch_kv4_read(c, n_tokens, dtype == AWQ_BF16, k_out, v_out,
+                                         (hipStream_t)stream));
+}
+
+namespace {
+
+int attention_shape(int64_t n_tokens, int64_t n_seqs, int64_t heads, const awq_kv4_config* cfg,
+                    int64_t max_q, int64_t max_len) {
+  if (n_tokens < 0 || n_tokens > kMaxRows || n_seqs < 0 || n_seqs > 65535 || max_q < 0 ||
+      max_len < 0 || max_len > ((int64_t)1 << 30) || max_q > ((int64_t)1 << 30))
+    return AWQ_E_SHAPE;
+  if (heads < 1 || heads > 65535 || heads % cfg->kv_heads) return AWQ_E_SHAPE;
+  // columns of a key head and (token, head) rows are counted in 32 bits
+  if (max_q * (heads / cfg->kv_heads) > ((int64_t)1 << 30)) return AWQ_E_SHAPE;
+  if (n_tokens > (((int64_t)1 << 31) - 1024) / heads) return AWQ_E_SHAPE;
+  return AWQ_OK;
+}
+
+}  // namespace
+
+size_t awq_kv4_attention_workspace_bytes(int64_t n_tokens, int64_t n_seqs, int64_t heads,
+                                         const awq_kv4_config* cfg, int64_t max_q,
+                                         int64_t max_len) {
+  if (!kv4_valid(cfg) || attention_shape(n_tokens, n_seqs, heads, cfg, max_q, max_len)) return 0;
+  if (n_tokens == 0 || n_seqs == 0 || max_q == 0) return 0;
+  const awq::Kv4Plan p =
+      awq::kv4_plan(n_seqs, (int)heads, cfg->kv_heads, cfg->head_dim,
+                                        cfg->group_size, max_q, max_len);
+  return round_up(awq::kv4_workspace(p, n_tokens, (int)heads, cfg->head_dim), kAlign);
+}
+
+int awq_kv4_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                      int64_t n_tokens, int64_t heads, int32_t dtype, const void* cache,
+                      int64_t n_pages, const int32_t* block_table, int64_t n_seqs,
+                      int64_t max_blocks, const int32_t* seq_lens, const int32_t* q_start,
+                      const awq_kv4_config* cfg, int64_t max_q, int64_t max_len, float scale,
+                      int64_t window, void* out, float* lse_out, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  if (!q || !out) return AWQ_E_NULL;
+  awq::Kv4Cache c;
+  int st = kv4_cache(cache, n_pages, block_table, n_seqs, max_blocks, seq_lens, q_start, n_tokens,
+                     cfg, &c);
+  if (st) return st;
+  if (!dtype_valid(dtype)) return AWQ_E_CONFIG;
+  if (!(scale > 0.0f) || !(scale < __builtin_inff())) return AWQ_E_CONFIG;
+  if (window < 0 || (st = attention_shape(n_tokens, n_seqs, heads, cfg, max_q, max_len)))
+    return AWQ_E_SHAPE;
+  if ((st = kv4_rows(q, q_token_stride, q_head_stride))) return st;
+  if (!aligned(out, 16) || !aligned(lse_out, 4)) return AWQ_E_ALIGN;
+  if (n_tokens == 0 || n_seqs == 0 || max_q == 0) return AWQ_OK;
+  const awq::Kv4Plan p =
+      awq::kv4_plan(n_seqs, (int)heads, cfg->kv_heads, cfg->head_dim,
+                                        cfg->group_size, max_q, max_len);
+  const size_t need =
+      round_up(awq::kv4_workspace(p, n_tokens, (int)heads, cfg->head_dim), kAlign);
+  if (need && (!workspace || workspace_bytes < need)) return AWQ_E_WORKSPACE;
+  if (need && !aligned(workspace, kAlign)) return AWQ_E_ALIGN;
+  if ((st = device_ptrs({q, cache, block_table, seq_lens, q_start, out, lse_out,
+                         need ? workspace : nullptr})))
+    return st;
+  clear_pending_error();
+  const awq::Kv4Query a{q, q_token_stride, q_head_stride, n_tokens, (int)heads, (int)max_q,
+                        (int)max_len, (int)(window < (1 << 30) ? window : 0), scale,
+                        dtype == AWQ_BF16, out, lse_out};
+  return hip_status(awq::launch_kv4_attention(c, a, p, workspace, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -32,4 +32,48 @@ struct Int8Args {
 size_t int8_matmul_workspace(int64_t T, int64_t M, int64_t K);
 hipError_t launch_int8_matmul(const Int8Args& a, void* workspace, hipStream_t stream);
 
+// ---- key/value cache in 4 bits ---------------------------------------------------------
+struct Kv4Cache {
+  uint8_t* pages;
+  int64_t n_pages;
+  const int32_t* table;   // [n_seqs][max_blocks]
+  const int32_t* lens;    // [n_seqs]
+  const int32_t* starts;  // [n_seqs + 1]
+  int n_seqs, max_blocks;
+  int kv_heads, dim, group, log2p;
+  int zero_point;
+  unsigned record;  // bytes of one page of one head
+};
+inline unsigned kv4_record(int dim, int group, int page) {
+  return (unsigned)page * dim + 8u * page * (dim / group);
+}
+hipError_t launch_kv4_append(const Kv4Cache& c, const void* k, int64_t kt, int64_t kh,
+                             const void* v, int64_t vt, int64_t vh, int64_t n_tokens, bool bf16,
+                             hipStream_t stream);
+hipError_t launch_kv4_read(const Kv4Cache& c, int64_t n_tokens, bool bf16, void* k, void* v,
+                           hipStream_t stream);
+
+struct Kv4Query {
+  const void* q;
+  int64_t qt, qh;  // token and head strides
+  int64_t n_tokens;
+  int heads, max_q, max_len, window;
+  float scale;
+  bool bf16;
+  void* out;
+  float* lse;
+};
+// How one attention call is laid out (by sizes only): columns (query rows x heads of a key
+// head) a block, and the splits of the keys.
+struct Kv4Plan {
+  int wide;    // 0: one 16-column tile a block, its waves share the keys; 1: a tile set a wave
+  int tiles;   // blocks of columns a (sequence, key head)
+  int splits;  // parts of the keys, joined by a second launch if more than one
+};
+Kv4Plan kv4_plan(int64_t n_seqs, int heads, int kv_heads, int dim, int group, int64_t max_q,
+                 int64_t max_len);
+size_t kv4_workspace(const Kv4Plan& p, int64_t n_tokens, int heads, int dim);
+hipError_t launch_kv4_attention(const Kv4Cache& c, const Kv4Query& q, const Kv4Plan& p,
+                                void* workspace, hipStream_t stream);
+
 }  // namespace awq
