@@ -8,11 +8,12 @@ views into a fused projection's output need no copy.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 import torch
 
-from ._lib import _buf, _check, _dev, _i32, _i64, _on_stream, _ptr, _stream_ptr, _sz, _vp
+from ._lib import _buf, _check, _dev, _i32, _i64, _sz, _vp
 from ._lib import lib as _base_lib
 
 AWQ_FP16, AWQ_BF16 = 0, 1
@@ -68,39 +69,63 @@ def lib() -> ctypes.CDLL:
     return _BOUND
 
 
-_DTYPES = {torch.float16: AWQ_FP16, torch.bfloat16: AWQ_BF16}
+# A decode step's calls last a few microseconds on the device, so the path to the C ABI is kept
+# short: one combined test per tensor (the detailed checks run only to say what is wrong), the
+# current stream's handle without a Stream object, workspace sizes remembered by their sizes.
+_FP16, _BF16, _FP32, _I8, _U8, _INT32 = (torch.float16, torch.bfloat16, torch.float32, torch.int8,
+                                         torch.uint8, torch.int32)
+_DTYPES = {_FP16: AWQ_FP16, _BF16: AWQ_BF16}
 
 
 def _dtype(dtype: torch.dtype, name: str) -> int:
-    if dtype not in _DTYPES:
+    dt = _DTYPES.get(dtype)
+    if dt is None:
         raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {dtype}")
-    return _DTYPES[dtype]
+    return dt
+
+
+def _current_stream() -> int:
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _on_stream(fn):
+    """Run the wrapper with `stream` (when given) as torch's current stream, so that what it
+    allocates belongs to the stream that the kernels are enqueued on."""
+    @functools.wraps(fn)
+    def wrapper(*args, stream=None, **kwargs):
+        if stream is None:
+            return fn(*args, **kwargs)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kwargs)
+    return wrapper
 
 
 def _rows(t: torch.Tensor, name: str, dtype: Optional[torch.dtype] = None) -> int:
     """Check a 2-D device tensor with unit stride along its rows; returns the row stride."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a device (HIP) tensor")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    sr, sc = t.stride()
+    if cols > 1 and sc != 1:
         raise ValueError(f"{name} must be contiguous along its rows")
-    ld = t.stride(0) if rows > 1 and cols > 0 else cols
+    ld = sr if rows > 1 and cols > 0 else cols
     if ld < cols:
         raise ValueError(f"{name} has overlapping rows (stride {ld} for {cols} columns)")
     return ld
 
 
-def _addr(t: Optional[torch.Tensor], other: torch.Tensor) -> Optional[int]:
-    # an empty tensor has no address; the call does not read it, any device pointer serves
-    if t is None:
-        return None
-    return t.data_ptr() or other.data_ptr()
+def _vec(t: torch.Tensor, dtype: torch.dtype, name: str, n: int) -> int:
+    """Check a contiguous device vector of n elements; returns its address."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.dim() == 1
+            and t.shape[0] == n and t.is_contiguous()):
+        _dev(t, dtype, name, (n,))
+    return t.data_ptr()
 
 
 def _round16(k: int) -> int:
@@ -109,8 +134,7 @@ def _round16(k: int) -> int:
 
 # ------------------------------------------------------------------- rows of 8-bit integers
 @_on_stream
-def awq_int8_quantize(A: torch.Tensor, s: Optional[torch.Tensor] = None, fold: str = "divide",
-                      stream=None):
+def awq_int8_quantize(A: torch.Tensor, s: Optional[torch.Tensor] = None, fold: str = "divide"):
     """Rows of A (fp16 or bf16 [R, K]) as int8 codes [R, K rounded up to 16] (zeros past K) and
     fp32 steps [R].  With s (fp32 [K]) the values are A / s (fold="divide", activations) or
     A * s (fold="multiply", weights)."""
@@ -119,34 +143,34 @@ def awq_int8_quantize(A: torch.Tensor, s: Optional[torch.Tensor] = None, fold: s
     if fold not in ("divide", "multiply"):
         raise ValueError('fold must be "divide" or "multiply"')
     R, K = A.shape
-    if s is not None:
-        _dev(s, torch.float32, "s", (K,))
-    codes = torch.empty((R, _round16(K)), dtype=torch.int8, device=A.device)
-    steps = torch.empty(R, dtype=torch.float32, device=A.device)
+    ps = None if s is None else _vec(s, _FP32, "s", K)
+    codes = torch.empty((R, _round16(K)), dtype=_I8, device=A.device)
+    steps = torch.empty(R, dtype=_FP32, device=A.device)
     if R == 0:
         return codes, steps
-    st = lib().awq_int8_quantize(_addr(A, steps), R, K, lda, dt, _addr(s, steps),
+    # an empty tensor has no address; the call does not read it, any device pointer serves
+    some = steps.data_ptr()
+    st = lib().awq_int8_quantize(A.data_ptr() or some, R, K, lda, dt, ps,
                                  AWQ_FOLD_MULTIPLY if fold == "multiply" else AWQ_FOLD_DIVIDE,
-                                 codes.data_ptr() or _ptr(_buf(256, A.device)), _round16(K),
-                                 _ptr(steps), _stream_ptr(stream))
+                                 codes.data_ptr() or _buf(256, A.device).data_ptr(), _round16(K),
+                                 some, _current_stream())
     _check(st, "awq_int8_quantize")
     return codes, steps
 
 
+@functools.lru_cache(maxsize=4096)
 def awq_int8_matmul_workspace_bytes(n_tokens: int, out_features: int, in_features: int) -> int:
     return int(lib().awq_int8_matmul_workspace_bytes(n_tokens, out_features, in_features))
 
 
+@functools.lru_cache(maxsize=4096)
 def awq_int8_linear_workspace_bytes(n_tokens: int, out_features: int, in_features: int) -> int:
     return int(lib().awq_int8_linear_workspace_bytes(n_tokens, out_features, in_features))
 
 
-def _out_and_bias(T, M, dtype, bias, out, device):
-    if bias is not None:
-        _dev(bias, dtype, "bias", (M,))
+def _out_rows(T, M, dtype, out, device):
     if out is None:
-        out = torch.empty((T, M), dtype=dtype, device=device)
-        return out, M
+        return torch.empty((T, M), dtype=dtype, device=device), M
     ldy = _rows(out, "out", dtype)
     if tuple(out.shape) != (T, M):
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {(T, M)}")
@@ -154,34 +178,38 @@ def _out_and_bias(T, M, dtype, bias, out, device):
 
 
 def _workspace(workspace, need, device):
+    """(tensor that must live until the call, address or None, bytes)."""
     if workspace is None:
-        return (torch.empty(need, dtype=torch.uint8, device=device), need) if need else (None, 0)
-    _dev(workspace, torch.uint8, "workspace")
-    return workspace, workspace.numel()
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=_U8, device=device)
+    else:
+        _dev(workspace, _U8, "workspace")
+    return workspace, workspace.data_ptr() or None, workspace.numel()
 
 
 @_on_stream
 def awq_int8_matmul(xq: torch.Tensor, xstep: torch.Tensor, wq: torch.Tensor, wstep: torch.Tensor,
                     dtype: torch.dtype = torch.float16, bias: Optional[torch.Tensor] = None,
-                    out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-                    stream=None) -> torch.Tensor:
+                    out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y [T, M] = (xq wq^T) xstep wstep (+ bias) for int8 codes xq [T, K], wq [M, K] (K a
     multiple of 16, rows 16-byte aligned) and fp32 steps xstep [T], wstep [M]; y in `dtype`."""
-    ldx, ldw = _rows(xq, "xq", torch.int8), _rows(wq, "wq", torch.int8)
+    ldx, ldw = _rows(xq, "xq", _I8), _rows(wq, "wq", _I8)
     T, K = xq.shape
     M = wq.shape[0]
     if wq.shape[1] != K or K % 16:
         raise ValueError("xq and wq must have the same number of columns, a multiple of 16")
     dt = _dtype(dtype, "dtype")
-    _dev(xstep, torch.float32, "xstep", (T,))
-    _dev(wstep, torch.float32, "wstep", (M,))
-    y, ldy = _out_and_bias(T, M, dtype, bias, out, xq.device)
+    px, pw = _vec(xstep, _FP32, "xstep", T), _vec(wstep, _FP32, "wstep", M)
+    pb = None if bias is None else _vec(bias, dtype, "bias", M)
+    y, ldy = _out_rows(T, M, dtype, out, xq.device)
     if T == 0 or M == 0:
         return y
-    ws, nw = _workspace(workspace, awq_int8_matmul_workspace_bytes(T, M, K), xq.device)
-    st = lib().awq_int8_matmul(_addr(xq, y), ldx, _ptr(xstep), T, _addr(wq, y), ldw, _ptr(wstep), M,
-                               K, _addr(bias, y), dt, _ptr(y), ldy, _addr(ws, y), nw,
-                               _stream_ptr(stream))
+    py = y.data_ptr()
+    ws, pws, nws = _workspace(workspace, awq_int8_matmul_workspace_bytes(T, M, K), xq.device)
+    st = lib().awq_int8_matmul(xq.data_ptr() or py, ldx, px, T, wq.data_ptr() or py, ldw, pw, M, K,
+                               pb, dt, py, ldy, pws, nws, _current_stream())
     _check(st, "awq_int8_matmul")
     return y
 
@@ -189,27 +217,29 @@ def awq_int8_matmul(xq: torch.Tensor, xstep: torch.Tensor, wq: torch.Tensor, wst
 @_on_stream
 def awq_int8_linear(x: torch.Tensor, wq: torch.Tensor, wstep: torch.Tensor,
                     s: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
-                    out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-                    stream=None) -> torch.Tensor:
+                    out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y [T, M] in x's type: each token of x (fp16 or bf16 [T, K]) divided by s (fp32 [K], if
     given), quantised to int8 with its own step and multiplied with the int8 weight wq
     [M, K rounded up to 16], wstep [M] (as awq_int8_quantize(W, s, "multiply") makes them)."""
-    ldx, ldw = _rows(x, "x"), _rows(wq, "wq", torch.int8)
-    dt = _dtype(x.dtype, "x")
+    ldx, ldw = _rows(x, "x"), _rows(wq, "wq", _I8)
+    dtype = x.dtype
+    dt = _dtype(dtype, "x")
     T, K = x.shape
     M = wq.shape[0]
     if wq.shape[1] != _round16(K):
         raise ValueError(f"wq has {wq.shape[1]} columns, expected {_round16(K)}")
-    _dev(wstep, torch.float32, "wstep", (M,))
-    if s is not None:
-        _dev(s, torch.float32, "s", (K,))
-    y, ldy = _out_and_bias(T, M, x.dtype, bias, out, x.device)
+    pw = _vec(wstep, _FP32, "wstep", M)
+    ps = None if s is None else _vec(s, _FP32, "s", K)
+    pb = None if bias is None else _vec(bias, dtype, "bias", M)
+    y, ldy = _out_rows(T, M, dtype, out, x.device)
     if T == 0 or M == 0:
         return y
-    ws, nw = _workspace(workspace, awq_int8_linear_workspace_bytes(T, M, K), x.device)
-    st = lib().awq_int8_linear(_addr(x, y), ldx, _addr(s, y), T, _addr(wq, y), ldw, _ptr(wstep), M,
-                               K, _addr(bias, y), dt, _ptr(y), ldy, _addr(ws, y), nw,
-                               _stream_ptr(stream))
+    py = y.data_ptr()
+    ws, pws, nws = _workspace(workspace, awq_int8_linear_workspace_bytes(T, M, K), x.device)
+    st = lib().awq_int8_linear(x.data_ptr() or py, ldx, (ps or py) if s is not None else None, T,
+                               wq.data_ptr() or py, ldw, pw, M, K, pb, dt, py, ldy, pws, nws,
+                               _current_stream())
     _check(st, "awq_int8_linear")
     return y
 
@@ -217,7 +247,7 @@ def awq_int8_linear(x: torch.Tensor, wq: torch.Tensor, wstep: torch.Tensor,
 # -------------------------------------------------------------- key/value cache in 4 bits
 def awq_kv4_record_bytes(cfg: awq_kv4_config) -> int:
     """Bytes of one page of one head (0 for an invalid configuration)."""
-    return int(lib().awq_kv4_record_bytes(ctypes.byref(cfg)))
+    return int(lib().awq_kv4_record_bytes(cfg))
 
 
 def awq_kv4_cache(n_pages: int, cfg: awq_kv4_config, device="cuda") -> torch.Tensor:
@@ -229,19 +259,23 @@ def awq_kv4_cache(n_pages: int, cfg: awq_kv4_config, device="cuda") -> torch.Ten
 
 
 def _kv4_args(cache, table, lens, starts, cfg):
-    rec = awq_kv4_record_bytes(cfg)
-    if rec == 0:
-        raise ValueError("invalid awq_kv4_config")
-    _dev(cache, torch.uint8, "cache")
-    if cache.dim() != 3 or cache.shape[1] != cfg.kv_heads or cache.shape[2] != rec:
-        raise ValueError(f"cache has shape {tuple(cache.shape)}, expected "
-                         f"[n_pages, {cfg.kv_heads}, {rec}]")
-    _dev(table, torch.int32, "block_table")
-    if table.dim() != 2:
+    """Check the cache and its index tensors; returns the number of sequences."""
+    d, p, hk, g = cfg.head_dim, cfg.page_size, cfg.kv_heads, cfg.group_size
+    rec = p * (d + 8 * (d // g)) if g > 0 else 0  # the C side refuses what is no configuration
+    if not (isinstance(cache, torch.Tensor) and cache.is_cuda and cache.dtype == _U8
+            and cache.dim() == 3 and cache.shape[1] == hk and cache.shape[2] == rec
+            and cache.is_contiguous()):
+        if awq_kv4_record_bytes(cfg) == 0:
+            raise ValueError("invalid awq_kv4_config")
+        _dev(cache, _U8, "cache")
+        raise ValueError(f"cache has shape {tuple(cache.shape)}, expected [n_pages, {hk}, {rec}]")
+    if not (isinstance(table, torch.Tensor) and table.is_cuda and table.dtype == _INT32
+            and table.dim() == 2 and table.is_contiguous()):
+        _dev(table, _INT32, "block_table")
         raise ValueError("block_table must be [n_seqs, max_blocks]")
     n = table.shape[0]
-    _dev(lens, torch.int32, "seq_lens", (n,))
-    _dev(starts, torch.int32, "q_start", (n + 1,))
+    _vec(lens, _INT32, "seq_lens", n)
+    _vec(starts, _INT32, "q_start", n + 1)
     return n
 
 
@@ -249,43 +283,46 @@ def _heads(t, name, heads, dim, dtype=None):
     """Check [tokens, heads, dim] with unit stride in dim; returns token and head strides."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a device (HIP) tensor")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [tokens, "
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [tokens, "
                          f"{'heads' if heads is None else heads}, {dim}]")
-    if t.stride(2) != 1:
+    st, sh, sd = t.stride()
+    if sd != 1:
         raise ValueError(f"{name} must be contiguous along head_dim")
-    return (t.stride(0) if t.shape[0] > 1 else 0), (t.stride(1) if t.shape[1] > 1 else 0)
+    return (st if shape[0] > 1 else 0), (sh if shape[1] > 1 else 0)
 
 
 @_on_stream
 def awq_kv4_append(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
-                   seq_lens: torch.Tensor, q_start: torch.Tensor, cfg: awq_kv4_config,
-                   stream=None) -> None:
+                   seq_lens: torch.Tensor, q_start: torch.Tensor, cfg: awq_kv4_config) -> None:
     """Quantise the rows k, v (fp16 or bf16 [T, kv_heads, head_dim], any token and head strides
     that are multiples of 8) into the pages of their sequences.  Rows q_start[b] ..
     q_start[b + 1] - 1 are the last tokens of sequence b, whose length with them is seq_lens[b]."""
     n = _kv4_args(cache, block_table, seq_lens, q_start, cfg)
     dt = _dtype(k.dtype, "k")
-    kt, kh = _heads(k, "k", cfg.kv_heads, cfg.head_dim)
-    vt, vh = _heads(v, "v", cfg.kv_heads, cfg.head_dim, k.dtype)
-    if v.shape[0] != k.shape[0]:
+    hk, d = cfg.kv_heads, cfg.head_dim
+    kt, kh = _heads(k, "k", hk, d)
+    vt, vh = _heads(v, "v", hk, d, k.dtype)
+    T = k.shape[0]
+    if v.shape[0] != T:
         raise ValueError("k and v differ in tokens")
-    if k.shape[0] == 0 or n == 0:
+    if T == 0 or n == 0:
         return
-    st = lib().awq_kv4_append(_ptr(k), kt, kh, _ptr(v), vt, vh, k.shape[0], dt, _ptr(cache),
-                              cache.shape[0], _ptr(block_table), n, block_table.shape[1],
-                              _ptr(seq_lens), _ptr(q_start), ctypes.byref(cfg), _stream_ptr(stream))
+    st = lib().awq_kv4_append(k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, T, dt, cache.data_ptr(),
+                              cache.shape[0], block_table.data_ptr(), n, block_table.shape[1],
+                              seq_lens.data_ptr(), q_start.data_ptr(), cfg, _current_stream())
     _check(st, "awq_kv4_append")
 
 
 @_on_stream
 def awq_kv4_read(cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
                  q_start: torch.Tensor, cfg: awq_kv4_config, n_tokens: int,
-                 dtype: torch.dtype = torch.float16, stream=None):
+                 dtype: torch.dtype = torch.float16):
     """The stored keys and values of the same rows as awq_kv4_append: two tensors
     [n_tokens, kv_heads, head_dim] of dtype (zeros where no such token exists)."""
     n = _kv4_args(cache, block_table, seq_lens, q_start, cfg)
@@ -297,47 +334,54 @@ def awq_kv4_read(cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch
         return k, v
     if n == 0:
         return k.zero_(), v.zero_()
-    st = lib().awq_kv4_read(_ptr(cache), cache.shape[0], _ptr(block_table), n, block_table.shape[1],
-                            _ptr(seq_lens), _ptr(q_start), n_tokens, ctypes.byref(cfg), dt, _ptr(k),
-                            _ptr(v), _stream_ptr(stream))
+    st = lib().awq_kv4_read(cache.data_ptr(), cache.shape[0], block_table.data_ptr(), n,
+                            block_table.shape[1], seq_lens.data_ptr(), q_start.data_ptr(), n_tokens,
+                            cfg, dt, k.data_ptr(), v.data_ptr(), _current_stream())
     _check(st, "awq_kv4_read")
     return k, v
 
 
+@functools.lru_cache(maxsize=4096)
+def _attention_workspace(T, n, H, d, hk, p, g, max_q, max_len):
+    cfg = awq_kv4_config(d, hk, p, g, 0)
+    return int(lib().awq_kv4_attention_workspace_bytes(T, n, H, cfg, max_q, max_len))
+
+
 def awq_kv4_attention_workspace_bytes(n_tokens: int, n_seqs: int, heads: int, cfg: awq_kv4_config,
                                       max_q: int, max_len: int) -> int:
-    return int(lib().awq_kv4_attention_workspace_bytes(n_tokens, n_seqs, heads, ctypes.byref(cfg),
-                                                       max_q, max_len))
+    return int(lib().awq_kv4_attention_workspace_bytes(n_tokens, n_seqs, heads, cfg, max_q, max_len))
 
 
 @_on_stream
 def awq_kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
                       seq_lens: torch.Tensor, q_start: torch.Tensor, cfg: awq_kv4_config, *,
                       max_q: int, max_len: int, scale: Optional[float] = None, window: int = 0,
-                      out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-                      stream=None):
+                      out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
     """Causal attention of q (fp16 or bf16 [T, heads, head_dim]) over the cache: returns out
     [T, heads, head_dim] in q's type and lse fp32 [T, heads].  max_q and max_len are host
     bounds on the rows of a sequence and on seq_lens; scale defaults to 1 / sqrt(head_dim);
     window > 0 keeps the last `window` keys of each row.  Rows without keys give 0 and -inf.
     A workspace (see awq_kv4_attention_workspace_bytes) is allocated unless one is passed."""
     n = _kv4_args(cache, block_table, seq_lens, q_start, cfg)
-    dt = _dtype(q.dtype, "q")
-    qt, qh = _heads(q, "q", None, cfg.head_dim)
-    T, H = q.shape[0], q.shape[1]
+    dtype = q.dtype
+    dt = _dtype(dtype, "q")
+    d = cfg.head_dim
+    qt, qh = _heads(q, "q", None, d)
+    T, H, _ = q.shape
     if out is None:
-        out = torch.empty((T, H, cfg.head_dim), dtype=q.dtype, device=q.device)
+        out = torch.empty((T, H, d), dtype=dtype, device=q.device)
     else:
-        _dev(out, q.dtype, "out", (T, H, cfg.head_dim))
-    lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+        _dev(out, dtype, "out", (T, H, d))
+    lse = torch.empty((T, H), dtype=_FP32, device=q.device)
     if T == 0 or n == 0:
         return out, lse
-    ws, nw = _workspace(workspace,
-                        awq_kv4_attention_workspace_bytes(T, n, H, cfg, max_q, max_len), q.device)
-    st = lib().awq_kv4_attention(_ptr(q), qt, qh, T, H, dt, _ptr(cache), cache.shape[0],
-                                 _ptr(block_table), n, block_table.shape[1], _ptr(seq_lens),
-                                 _ptr(q_start), ctypes.byref(cfg), max_q, max_len,
-                                 float(cfg.head_dim ** -0.5 if scale is None else scale), int(window),
-                                 _ptr(out), _ptr(lse), _addr(ws, out), nw, _stream_ptr(stream))
+    ws, pws, nws = _workspace(
+        workspace, _attention_workspace(T, n, H, d, cfg.kv_heads, cfg.page_size, cfg.group_size, max_q,
+                                        max_len) if workspace is None else 0, q.device)
+    st = lib().awq_kv4_attention(q.data_ptr(), qt, qh, T, H, dt, cache.data_ptr(), cache.shape[0],
+                                 block_table.data_ptr(), n, block_table.shape[1],
+                                 seq_lens.data_ptr(), q_start.data_ptr(), cfg, max_q, max_len,
+                                 d ** -0.5 if scale is None else scale, window, out.data_ptr(),
+                                 lse.data_ptr(), pws, nws, _current_stream())
     _check(st, "awq_kv4_attention")
     return out, lse
