@@ -32,8 +32,10 @@ HIP_FLAGS = [
     "-Wall", "-Wno-unused-function",
 ]
 # Per-source additions.  The clip-search kernels keep their small MFMA accumulators in
-# VGPRs (no accumulator-register moves in the epilogue); the large-tile GEMMs need AGPRs.
+# VGPRs (no accumulator-register moves in the epilogue), and so does the cache attention
+# (its running rescale); the large-tile GEMMs need AGPRs.
 HIP_FILE_FLAGS = {
+    "kv4_attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "clip_search.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__",

@@ -43,6 +43,7 @@ typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef _Float16 half8v __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kNegInf = -__builtin_inff();
 constexpr int kWaves = 4;
@@ -59,13 +60,25 @@ __device__ __forceinline__ float sum_q(float v) {
 // The operand pairs of one word: nibbles (n, n + 4) for n = 0..3, each as 16 + c.
 constexpr uint32_t kNibble = 0x03C003C0u, kOffset = 0x4C004C00u;
 constexpr float kOffsetF = 16.0f;
-template <int N>
-__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
-  constexpr int S = 6 - 4 * N;
-  return ((S > 0 ? w << (S > 0 ? S : 0) : w >> (S > 0 ? 0 : -S)) & kNibble) | kOffset;
+// The two constants in registers, the mask in a scalar and the offset in a vector one: a
+// three-operand instruction takes one scalar and no literal, and with a literal each the
+// compiler splits v_and_or_b32 in two.
+struct CodeConsts {
+  uint32_t mask, offset;
+};
+__device__ __forceinline__ CodeConsts code_consts() {
+  CodeConsts c;
+  asm volatile("s_mov_b32 %0, %1" : "=s"(c.mask) : "i"(kNibble));
+  asm volatile("v_mov_b32 %0, %1" : "=v"(c.offset) : "i"(kOffset));
+  return c;
 }
-__device__ __forceinline__ half8v word_operand(uint32_t w) {
-  const u32x4 v = {code_pair<0>(w), code_pair<1>(w), code_pair<2>(w), code_pair<3>(w)};
+template <int N>
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, const CodeConsts& cc) {
+  constexpr int S = 6 - 4 * N;
+  return ((S > 0 ? w << (S > 0 ? S : 0) : w >> (S > 0 ? 0 : -S)) & cc.mask) | cc.offset;
+}
+__device__ __forceinline__ half8v word_operand(uint32_t w, const CodeConsts& cc) {
+  const u32x4 v = {code_pair<0>(w, cc), code_pair<1>(w, cc), code_pair<2>(w, cc), code_pair<3>(w, cc)};
   return __builtin_bit_cast(half8v, v);
 }
 
@@ -137,14 +150,16 @@ template <int D, int GS>
 struct Column {
   using X = Geo<D, GS>;
   half8v q[X::KW];     // operands of S, in word order
+  f32x4 c16[X::G];     // -16 times the sum of a group's q: what S starts from
   float qsum[X::G];    // sum of a group's q
   float sigma;         // from the raw score to log2 units
   int pos;             // the row's position; -1: no row
   float m;             // running maximum of the scores, log2 units
-  float M;             // m - f: what the exponents are taken against
-  float l;             // this lane's sum of exp2(s - M)
+  float nM;            // f - m: weights are exp2(s + nM); 0 before the first key
+  float l;             // this lane's sum of exp2(s + nM)
   f32x4 z[X::G];       // sum of weight x (zero + 16): every row the same
   f32x4 o[X::N];
+  __device__ float M() const { return m == kNegInf ? kNegInf : -nM; }
 };
 
 // One row of q as operands: scaled by a power of two so that its largest magnitude lies in
@@ -190,10 +205,12 @@ __device__ __forceinline__ void load_query(Column<D, GS>& c, const uint16_t* row
 #pragma unroll
   for (int g = 0; g < X::G; ++g) {
     c.qsum[g] = sum_q(c.qsum[g]);
+    const float x = -kOffsetF * c.qsum[g];
+    c.c16[g] = f32x4{x, x, x, x};
     c.z[g] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
   c.m = kNegInf;
-  c.M = kNegInf;
+  c.nM = 0.0f;
   c.l = 0.0f;
 #pragma unroll
   for (int n = 0; n < X::N; ++n) c.o[n] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -209,16 +226,24 @@ __device__ __forceinline__ uint32_t pair16(float x, float y) {
 __device__ __forceinline__ float lo16(uint32_t w) { return h2f((uint16_t)w); }
 __device__ __forceinline__ float hi16(uint32_t w) { return h2f((uint16_t)(w >> 16)); }
 
-// One tile of 32 keys for NC column tiles.  MASKED: some (key, column) pairs do not exist;
-// key0 is the tile's first key, lo_off = window - 1 (or a huge number) so that column pos sees
+// The power of two of the weights of a wave: w = exp2(s - m + f) step stays below 2^15 for steps
+// below the fp16 pattern `limit`.
+struct WeightScale {
+  float f = 64.0f;
+  uint32_t limit = 0;
+};
+
+// One tile of 32 keys for NC column tiles.  !whole (the same in every lane): some (key, column)
+// pairs do not exist; key0 is the tile's first key, lo_off = window - 1 (or a huge number) so that column pos sees
 // keys [pos - lo_off, pos]; dead: bit x set if the keys of half x lie on no page.
-template <int D, int GS, int NC, bool MASKED>
-__device__ __forceinline__ void do_tile(TileRegs<D, GS>& r, Column<D, GS> (&col)[NC], int key0,
-                                        int n_keys, int lo_off, int dead, float& f, int lane) {
+template <int D, int GS, int NC>
+__device__ __forceinline__ void do_tile(TileRegs<D, GS>& r, Column<D, GS> (&col)[NC], bool whole,
+                                        int key0, int n_keys, int lo_off, int dead, WeightScale& ws,
+                                        const CodeConsts& cc, int lane) {
   using X = Geo<D, GS>;
   const int q = lane >> 4;
   const int kq = key0 + 8 * q;
-  if constexpr (MASKED) {
+  if (!whole) {
     // parameters of keys that do not exist may hold anything
 #pragma unroll
     for (int g = 0; g < X::G; ++g)
@@ -229,20 +254,15 @@ __device__ __forceinline__ void do_tile(TileRegs<D, GS>& r, Column<D, GS> (&col)
         r.vp[g][e >> 2][e & 3] = ok ? r.vp[g][e >> 2][e & 3] : 0u;
       }
   }
-  // largest value step of the tile (non-finite ones count as the largest finite)
-  uint32_t top = 0;
+  // largest value step of the lane's keys (as fp16 patterns; the packed maximum also forms that
+  // of the zeros, unused)
+  u16x2 tp = __builtin_bit_cast(u16x2, r.vp[0][0][0]);
 #pragma unroll
   for (int g = 0; g < X::G; ++g)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, r.vp[g][e >> 2][e & 3] & 0x7fffu);
-  top = max(top, (uint32_t)__shfl_xor((int)top, 16));
-  top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-  // 2^f: 2^14 over the step's power of two (a zero or subnormal step counts as the smallest
-  // normal one)
-  const int ex = (int)(min(max(top, 0x0400u), 0x7bffu) >> 10) - 15;
-  const float ft = (float)(14 - ex);
-  const bool fnew = ft < f;
-  f = fminf(f, ft);
+    for (int e = 0; e < 8; ++e)
+      tp = __builtin_elementwise_max(tp, __builtin_bit_cast(u16x2, r.vp[g][e >> 2][e & 3]));
+  const uint32_t top = tp[0];
 
 #pragma unroll
   for (int t = 0; t < NC; ++t) {
@@ -252,40 +272,51 @@ __device__ __forceinline__ void do_tile(TileRegs<D, GS>& r, Column<D, GS> (&col)
     for (int j = 0; j < 2; ++j) {
 #pragma unroll
       for (int g = 0; g < X::G; ++g) {
-        f32x4 a = {0.f, 0.f, 0.f, 0.f};
+        f32x4 a = c.c16[g];
 #pragma unroll
         for (int u = 0; u < X::WPG; ++u)
-          a = __builtin_amdgcn_mfma_f32_16x16x32_f16(word_operand(r.k[j][g * X::WPG + u]),
+          a = __builtin_amdgcn_mfma_f32_16x16x32_f16(word_operand(r.k[j][g * X::WPG + u], cc),
                                                      c.q[g * X::WPG + u], a, 0, 0, 0);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t w = r.kp[g][j][e];
-          const float x = fmaf(-(hi16(w) + kOffsetF), c.qsum[g], a[e]);
-          s[4 * j + e] = g == 0 ? lo16(w) * x : fmaf(lo16(w), x, s[4 * j + e]);
+          const float x = fmaf(-hi16(w), c.qsum[g], a[e]);
+          s[4 * j + e] = fmaf(lo16(w), x, g == 0 ? 0.0f : s[4 * j + e]);
         }
       }
     }
-    bool ok[8];
-    if constexpr (MASKED) {
+    uint32_t seen = 0xff;  // bit e: key 8 q + e exists for the column
+    if (!whole) {
+      seen = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int key = kq + e;
-        ok[e] = key <= c.pos && key >= c.pos - lo_off && key < n_keys && !((dead >> (q >> 1)) & 1);
-        s[e] = ok[e] ? s[e] : kNegInf;
+        const bool ok = key <= c.pos && key >= c.pos - lo_off && key < n_keys && !((dead >> (q >> 1)) & 1);
+        s[e] = ok ? s[e] : kNegInf;
+        seen |= ok ? 1u << e : 0u;
       }
     }
     float mx = s[0];
 #pragma unroll
     for (int e = 1; e < 8; ++e) mx = fmaxf(mx, s[e]);
-    mx = max_q(mx) * c.sigma;
-    const bool up = mx > c.m;
-    if (__any(up || fnew)) {
-      const float m = fmaxf(c.m, mx);
-      // no key yet: nothing is summed, any finite reference will do
-      const float M = m == kNegInf ? kNegInf : m - f;
-      const float a = c.M == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(c.M - M);
+    mx *= c.sigma;
+    // seldom: a score above the column's maximum, or a value step above what the weights' scale
+    // was made for
+    if (__any(mx > c.m || top >= ws.limit)) {
+      if (t == 0) {
+        uint32_t all = top;
+        all = max(all, (uint32_t)__shfl_xor((int)all, 16));
+        all = max(all, (uint32_t)__shfl_xor((int)all, 32));
+        // zero and subnormal steps count as the smallest normal one, others as finite
+        const uint32_t ex = min(max(all, 0x0400u), 0x7bffu) >> 10;
+        ws.limit = max(ws.limit, (ex + 1) << 10);
+        ws.f = fminf(ws.f, (float)(14 + 15 - (int)ex));
+      }
+      const float m = fmaxf(c.m, max_q(mx));
+      const float nM = m == kNegInf ? 0.0f : ws.f - m;
+      const float a = c.m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(nM - c.nM);
       c.m = m;
-      c.M = M;
+      c.nM = nM;
       c.l *= a;
 #pragma unroll
       for (int g = 0; g < X::G; ++g)
@@ -296,11 +327,10 @@ __device__ __forceinline__ void do_tile(TileRegs<D, GS>& r, Column<D, GS> (&col)
 #pragma unroll
         for (int e = 0; e < 4; ++e) c.o[n][e] *= a;
     }
-    const float M = c.M == kNegInf ? 0.0f : c.M;
     float p[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      p[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c.sigma, -M));
+      p[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c.sigma, c.nM));
       c.l += p[e];
     }
 #pragma unroll
@@ -309,16 +339,16 @@ __device__ __forceinline__ void do_tile(TileRegs<D, GS>& r, Column<D, GS> (&col)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t pa = r.vp[g][i >> 1][2 * (i & 1)], pb = r.vp[g][i >> 1][2 * (i & 1) + 1];
-        float x = p[2 * i] * lo16(pa), y = p[2 * i + 1] * lo16(pb);
-        if constexpr (MASKED) {  // a masked key's step may be NaN
-          x = ok[2 * i] ? x : 0.0f;
-          y = ok[2 * i + 1] ? y : 0.0f;
-        }
-        w[i] = pair16(x, y);
+        w[i] = pair16(fmaf(p[2 * i], lo16(pa), 0.0f), fmaf(p[2 * i + 1], lo16(pb), 0.0f));
         // zeros + 16, exact in fp16
-        zo[i] = __builtin_bit_cast(uint32_t,
-                                   __builtin_bit_cast(half2v, (pa >> 16) | (pb & 0xffff0000u)) +
-                                       __builtin_bit_cast(half2v, kOffset));
+        zo[i] = __builtin_bit_cast(
+            uint32_t, __builtin_bit_cast(half2v, __builtin_amdgcn_perm(pb, pa, 0x07060302u)) +
+                          __builtin_bit_cast(half2v, kOffset));
+      }
+      if (!whole) {  // a masked key's step may be NaN
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] &= (seen >> (2 * i) & 1 ? 0xffffu : 0u) | (seen >> (2 * i + 1) & 1 ? 0xffff0000u : 0u);
       }
       // the zeros' sum by the same instruction as the codes' (an operand whose 16 rows are
       // equal), so that what the two sums share cancels as it was rounded
@@ -330,10 +360,10 @@ __device__ __forceinline__ void do_tile(TileRegs<D, GS>& r, Column<D, GS> (&col)
         u32x4 a;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          a[i] = (n & 3) == 0   ? code_pair<0>(vw[i])
-                 : (n & 3) == 1 ? code_pair<1>(vw[i])
-                 : (n & 3) == 2 ? code_pair<2>(vw[i])
-                                : code_pair<3>(vw[i]);
+          a[i] = (n & 3) == 0   ? code_pair<0>(vw[i], cc)
+                 : (n & 3) == 1 ? code_pair<1>(vw[i], cc)
+                 : (n & 3) == 2 ? code_pair<2>(vw[i], cc)
+                                : code_pair<3>(vw[i], cc);
         c.o[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8v, a),
                                                        __builtin_bit_cast(half8v, w), c.o[n], 0, 0, 0);
       }
@@ -341,7 +371,7 @@ __device__ __forceinline__ void do_tile(TileRegs<D, GS>& r, Column<D, GS> (&col)
   }
 }
 
-// Results of a column tile: sums over the column's lanes, the zeros subtracted.  o is then sum_t w_t (c - z), l the weights' sum, both over exp2(M).
+// Results of a column tile: sums over the column's lanes, the zeros subtracted.  o is then sum_t w_t (c - z), l the weights' sum, both over exp2(M()).
 template <int D, int GS>
 __device__ __forceinline__ void finish(Column<D, GS>& c) {
   using X = Geo<D, GS>;
@@ -385,11 +415,21 @@ constexpr int wide_tiles(int dim, int group) { return dim / group > 2 ? 1 : 2; }
 
 // NC column tiles a wave; WIDE: the waves of a block hold different columns and walk all keys,
 // otherwise they share the columns and take the tiles in turn.
-template <int D, int GS, int NC, bool WIDE>
-__global__ __launch_bounds__(64 * kWaves) void k_kv4_attention(Kv4Cache c, Kv4Query a,
+#ifndef KV4_EU1
+#define KV4_EU1 3
+#endif
+#ifndef KV4_EU2
+#define KV4_EU2 3
+#endif
+constexpr int waves_per_simd(int dim, int group, bool wide) {
+  return wide ? 1 : dim / group > 2 ? 2 : dim == 64 && group == 64 ? 4 : dim == 128 && group==64 ? KV4_EU2 : KV4_EU1;
+}
+
+template <int D, int GS, int NC, bool WIDE, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(waves_per_simd(D, GS, WIDE)))) void k_kv4_attention(Kv4Cache c, Kv4Query a,
                                                                Partials part) {
   using X = Geo<D, GS>;
-  constexpr int kCols = 16 * NC * (WIDE ? kWaves : 1);  // columns a block
+  constexpr int kCols = 16 * NC * (WIDE ? WAVES : 1);  // columns a block
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int b = blockIdx.z, kvh = blockIdx.y % c.kv_heads;
@@ -443,22 +483,39 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv4_attention(Kv4Cache c, Kv4Qu
     bad = pg < 0 || pg >= c.n_pages;
     return c.pages + ((int64_t)(bad ? 0 : pg) * c.kv_heads + kvh) * (int64_t)c.record;
   };
-  float f = 64.0f;
-  const int step = WIDE ? 1 : kWaves;
-  const int first = t_lo + (WIDE ? 0 : wave);
-  for (int t = first; t < t_hi; t += step) {
-    const int key0 = 32 * t;
+  WeightScale ws;
+  const CodeConsts cc = code_consts();
+  const int step = WIDE ? 1 : WAVES;
+  struct Where {
+    const uint8_t *ra, *rb;
+    int dead;
+  };
+  auto where = [&](int t) {
+    Where w;
     int bad_a, bad_b;
-    const uint8_t* ra = page_of(key0, bad_a);
-    const uint8_t* rb = page_of(key0 + 16, bad_b);
-    TileRegs<D, GS> r;
-    load_tile<D, GS>(r, ra, rb, key0 & (P - 1), (key0 + 16) & (P - 1), P, lane);
-    const int dead = bad_a | (bad_b << 1);
+    w.ra = page_of(32 * t, bad_a);
+    w.rb = page_of(32 * t + 16, bad_b);
+    w.dead = bad_a | (bad_b << 1);
+    return w;
+  };
+  auto load = [&](TileRegs<D, GS>& r, const Where& w, int t) {
+    load_tile<D, GS>(r, w.ra, w.rb, (32 * t) & (P - 1), (32 * t + 16) & (P - 1), P, lane);
+  };
+  auto compute = [&](TileRegs<D, GS>& r, int dead, int t) {
+    const int key0 = 32 * t;
     // every key of the tile exists and every column sees all of it
     const bool whole = !dead && key0 + 32 <= len && key0 + 31 <= pos0 + first_i &&
                        key0 >= pos0 + last_i - lo_off;
-    if (whole) do_tile<D, GS, NC, false>(r, col, key0, len, lo_off, dead, f, lane);
-    else do_tile<D, GS, NC, true>(r, col, key0, len, lo_off, dead, f, lane);
+    do_tile<D, GS, NC>(r, col, whole, key0, len, lo_off, dead, ws, cc, lane);
+  };
+  int t = t_lo + (WIDE ? 0 : wave);
+  // three waves a SIMD hide each other's loads; a second tile's registers for loads ahead would
+  // cost one of them
+  for (; t < t_hi; t += step) {
+    const Where w = where(t);
+    TileRegs<D, GS> r;
+    load(r, w, t);
+    compute(r, w.dead, t);
   }
 
 #pragma unroll
@@ -471,33 +528,33 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv4_attention(Kv4Cache c, Kv4Qu
       if (x < n_cols) {
         const int i = x / group, h = x - i * group;
         const int64_t r = (int64_t)(row0 + i) * a.heads + kvh * group + h;
-        const Column<D, GS>& cc = col[t];
+        const Column<D, GS>& cx = col[t];
         const bool join = part.splits > 1;
-        const float inv = join ? 1.0f : cc.l == 0.0f ? 0.0f : 1.0f / cc.l;
+        const float inv = join ? 1.0f : cx.l == 0.0f ? 0.0f : 1.0f / cx.l;
 #pragma unroll
         for (int n = 0; n < X::N; ++n) {
           const int ch = 16 * n + 4 * (lane >> 4);
           if (join) {
-            *(f32x4*)(part.o + (r * part.splits + split) * D + ch) = cc.o[n];
+            *(f32x4*)(part.o + (r * part.splits + split) * D + ch) = cx.o[n];
           } else {
-            const float v[4] = {cc.o[n][0] * inv, cc.o[n][1] * inv, cc.o[n][2] * inv, cc.o[n][3] * inv};
+            const float v[4] = {cx.o[n][0] * inv, cx.o[n][1] * inv, cx.o[n][2] * inv, cx.o[n][3] * inv};
             store4(a.out, r * D + ch, a.bf16, v);
           }
         }
         if ((lane >> 4) == 0) {
           if (join) {
-            part.ml[(r * part.splits + split) * 2] = cc.M;
-            part.ml[(r * part.splits + split) * 2 + 1] = cc.l;
+            part.ml[(r * part.splits + split) * 2] = cx.M();
+            part.ml[(r * part.splits + split) * 2 + 1] = cx.l;
           } else if (a.lse) {
-            a.lse[r] = lse_of(cc.M, cc.l);
+            a.lse[r] = lse_of(cx.M(), cx.l);
           }
         }
       }
     }
   } else {
     // the waves' results joined in wave order: each scaled to the block's largest M
-    __shared__ float so[kWaves][16][D + 4];
-    __shared__ float sm[kWaves][16], sl[kWaves][16];
+    __shared__ float so[WAVES][16][D + 4];
+    __shared__ float sm[WAVES][16], sl[WAVES][16];
 #pragma unroll
     for (int t = 0; t < NC; ++t) {
       const int x = lane & 15;
@@ -505,22 +562,22 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv4_attention(Kv4Cache c, Kv4Qu
 #pragma unroll
       for (int n = 0; n < X::N; ++n) *(f32x4*)&so[wave][x][16 * n + 4 * (lane >> 4)] = col[t].o[n];
       if ((lane >> 4) == 0) {
-        sm[wave][x] = col[t].M;
+        sm[wave][x] = col[t].M();
         sl[wave][x] = col[t].l;
       }
       __syncthreads();
       // thread -> column, 4 channels at a time
-      for (int w = threadIdx.x; w < 16 * (D / 4); w += 64 * kWaves) {
+      for (int w = threadIdx.x; w < 16 * (D / 4); w += 64 * WAVES) {
         const int cx = w / (D / 4), ch = (w % (D / 4)) * 4;
         const int xx = col0 + 16 * t + cx;
         if (xx >= n_cols) continue;
         float M = sm[0][cx];
 #pragma unroll
-        for (int i = 1; i < kWaves; ++i) M = fmaxf(M, sm[i][cx]);
+        for (int i = 1; i < WAVES; ++i) M = fmaxf(M, sm[i][cx]);
         float l = 0.0f;
         f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < kWaves; ++i) {
+        for (int i = 0; i < WAVES; ++i) {
           if (sm[i][cx] == kNegInf) continue;
           const float k = __builtin_amdgcn_exp2f(sm[i][cx] - M);
           l = fmaf(sl[i][cx], k, l);
@@ -547,34 +604,75 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv4_attention(Kv4Cache c, Kv4Qu
   }
 }
 
-// Joins the splits of one (token, head) a wave, in split order.
-__global__ __launch_bounds__(256) void k_kv4_join(Kv4Cache c, Kv4Query a, Partials part, int D,
+// Joins the splits of one (token, head): RW waves a row, wave w adds splits w, w + RW, ... in
+// order, the waves in order.
+template <int D, int RW>
+__global__ __launch_bounds__(256) void k_kv4_join(Kv4Cache c, Kv4Query a, Partials part,
                                                   int64_t n_rows) {
-  const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (r >= n_rows) return;
-  const int64_t t = r / a.heads;
-  const int b = kv4_sequence(c, t);
-  if (b < 0 || t - c.starts[b] >= a.max_q) return;  // no such row: its partials were not written
-  const float* ml = part.ml + r * part.splits * 2;
-  float M = kNegInf;
-  for (int s = lane; s < part.splits; s += 64) M = fmaxf(M, ml[2 * s]);
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off));
-  const int per = D / 64;  // channels a lane: 1, 2 or 4
-  float l = 0.0f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  const float* po = part.o + r * part.splits * D + lane * per;
-  for (int s = 0; s < part.splits; ++s) {
-    const float ms = ml[2 * s];
-    if (ms == kNegInf) continue;
-    const float k = __builtin_amdgcn_exp2f(ms - M);
-    l = fmaf(ml[2 * s + 1], k, l);
-    for (int e = 0; e < per; ++e) o[e] = fmaf(po[(int64_t)s * D + e], k, o[e]);
+  constexpr int PER = D / 64;  // channels a lane
+  typedef float fvec __attribute__((ext_vector_type(PER)));
+  __shared__ float so[4][D], sl[4];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t r = (int64_t)blockIdx.x * (4 / RW) + wave / RW;
+  const int w = wave % RW, S = part.splits;
+  bool there = r < n_rows;
+  if (there) {  // a row past a sequence's bound has no partials
+    const int64_t t = r / a.heads;
+    const int b = kv4_sequence(c, t);
+    there = b >= 0 && t - c.starts[b] < a.max_q;
   }
+  float M = kNegInf, l = 0.0f;
+  fvec o;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) o[e] = 0.0f;
+  if (there) {
+    const float* ml = part.ml + r * S * 2;
+    for (int s = lane; s < S; s += 64) M = fmaxf(M, ml[2 * s]);
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off));
+    const float* po = part.o + r * S * D + lane * PER;
+#pragma unroll 8
+    for (int s = w; s < S; s += RW) {
+      const float2 x = *(const float2*)(ml + 2 * s);
+      const fvec v = *(const fvec*)(po + (int64_t)s * D);
+      const float k = x.x == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(x.x - M);
+      l = fmaf(x.y, k, l);
+#pragma unroll
+      for (int e = 0; e < PER; ++e) o[e] = fmaf(v[e], k, o[e]);
+    }
+  }
+  if constexpr (RW > 1) {
+    if (w > 0) {
+      *(fvec*)&so[wave][lane * PER] = o;
+      if (lane == 0) sl[wave] = l;
+    }
+    __syncthreads();
+    if (w > 0) return;
+#pragma unroll
+    for (int i = 1; i < RW; ++i) {
+      l += sl[wave + i];
+      const fvec v = *(const fvec*)&so[wave + i][lane * PER];
+#pragma unroll
+      for (int e = 0; e < PER; ++e) o[e] += v[e];
+    }
+  }
+  if (!there) return;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  uint16_t* out = (uint16_t*)a.out + r * D + lane * per;
-  for (int e = 0; e < per; ++e) out[e] = a.bf16 ? to16<true>(o[e] * inv) : to16<false>(o[e] * inv);
+  uint16_t* out = (uint16_t*)a.out + r * D + lane * PER;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) out[e] = a.bf16 ? to16<true>(o[e] * inv) : to16<false>(o[e] * inv);
   if (lane == 0 && a.lse) a.lse[r] = lse_of(M, l);
+}
+
+template <int D>
+hipError_t launch_join(const Kv4Cache& c, const Kv4Query& q, const Partials& part, int64_t rows,
+                       hipStream_t stream) {
+  if (part.splits >= 16)
+    hipLaunchKernelGGL((k_kv4_join<D, 4>), dim3((unsigned)rows), dim3(256), 0, stream, c, q, part, rows);
+  else
+    hipLaunchKernelGGL((k_kv4_join<D, 1>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, c, q,
+                       part, rows);
+  return hipGetLastError();
 }
 
 template <int D, int GS>
@@ -582,9 +680,13 @@ hipError_t launch_dg(const Kv4Cache& c, const Kv4Query& q, const Kv4Plan& p, con
                      hipStream_t stream) {
   const dim3 grid((unsigned)p.tiles, (unsigned)(c.kv_heads * p.splits), (unsigned)c.n_seqs);
   if (p.wide)
-    hipLaunchKernelGGL((k_kv4_attention<D, GS, wide_tiles(D, GS), true>), grid, dim3(64 * kWaves), 0, stream, c, q, part);
+    hipLaunchKernelGGL((k_kv4_attention<D, GS, wide_tiles(D, GS), true, kWaves>), grid, dim3(64 * kWaves),
+                       0, stream, c, q, part);
+  else if (p.waves == 8)
+    hipLaunchKernelGGL((k_kv4_attention<D, GS, 1, false, 8>), grid, dim3(512), 0, stream, c, q, part);
   else
-    hipLaunchKernelGGL((k_kv4_attention<D, GS, 1, false>), grid, dim3(64 * kWaves), 0, stream, c, q, part);
+    hipLaunchKernelGGL((k_kv4_attention<D, GS, 1, false, kWaves>), grid, dim3(64 * kWaves), 0, stream, c,
+                       q, part);
   return hipGetLastError();
 }
 
@@ -599,11 +701,20 @@ Kv4Plan kv4_plan(int64_t n_seqs, int heads, int kv_heads, int dim, int group, in
   p.tiles = (int)((cols + per - 1) / per);
   const int64_t blocks = n_seqs * kv_heads * p.tiles;
   // four blocks a compute unit, at least 256 keys a split
-  int64_t s = (1024 + blocks - 1) / blocks;
+#ifndef KV4_T
+#define KV4_T 1024
+#endif
+  int64_t s = (KV4_T + blocks - 1) / blocks;
   const int64_t most = (max_len + 255) / 256;
   if (s > most) s = most;
   if (kv_heads * s > 65535) s = 65535 / kv_heads;
   p.splits = (int)(s < 1 ? 1 : s);
+  p.waves = kWaves;
+  // short sequences in few blocks: eight waves a block and no second launch
+  if (!p.wide && blocks <= 256 && max_len <= 2048) {
+    p.waves = 8;
+    p.splits = 1;
+  }
   return p;
 }
 
@@ -630,9 +741,8 @@ hipError_t launch_kv4_attention(const Kv4Cache& c, const Kv4Query& q, const Kv4P
     default: return hipErrorInvalidValue;
   }
   if (e != hipSuccess || p.splits <= 1) return e;
-  hipLaunchKernelGGL(k_kv4_join, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, c, q, part,
-                     c.dim, rows);
-  return hipGetLastError();
+  return c.dim == 64 ? launch_join<64>(c, q, part, rows, stream)
+                     : launch_join<128>(c, q, part, rows, stream);
 }
 
 }  // namespace awq

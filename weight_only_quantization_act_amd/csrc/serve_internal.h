@@ -69,6 +69,7 @@ struct Kv4Plan {
   int wide;    // 0: one 16-column tile a block, its waves share the keys; 1: a tile set a wave
   int tiles;   // blocks of columns a (sequence, key head)
   int splits;  // parts of the keys, joined by a second launch if more than one
+  int waves;   // waves a block
 };
 Kv4Plan kv4_plan(int64_t n_seqs, int heads, int kv_heads, int dim, int group, int64_t max_q,
                  int64_t max_len);
