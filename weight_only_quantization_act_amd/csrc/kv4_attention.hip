@@ -34,6 +34,7 @@
 
 #include "int8_quant.h"
 #include "kv4_cache.h"
+#include "mfma_dma.h"
 
 namespace awq {
 
@@ -47,6 +48,10 @@ typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kNegInf = -__builtin_inff();
 constexpr int kWaves = 4;
+#ifndef KV4_NS
+#define KV4_NS 3
+#endif
+constexpr int kStages = KV4_NS;  // tiles a wave has in flight
 
 __device__ __forceinline__ float max_q(float v) {  // over the four lanes of a column
   v = fmaxf(v, __shfl_xor(v, 16));
@@ -105,43 +110,106 @@ struct TileRegs {
   u32x4 kp[X::G][2], vp[X::G][2];
 };
 
+// A stage of a wave's ring in LDS: one tile, [K pieces][V pieces][G][K params | V params].  It is
+// filled by DMA (no registers wait for data in flight) in the order in which the lanes read it
+// back: the 16-byte pieces of K and V by lane, a group's parameters by key.
 template <int D, int GS>
-__device__ __forceinline__ void load_tile(TileRegs<D, GS>& r, const uint8_t* ra, const uint8_t* rb,
-                                          int oa, int ob, int P, int lane) {
+struct Ring {
   using X = Geo<D, GS>;
+  static constexpr int KB = 16 * D, VB = 16 * D, BYTES = KB + VB + 256 * X::G;
+  static constexpr int DMAS = KB / 1024 + VB / 1024 + X::G;  // a stage, a wave
+};
+
+// lane l's 16 (4) bytes at its address land at LDS byte lds + 16 l (4 l); see mfma_dma.h.
+__device__ __forceinline__ void dma_piece(unsigned lds, const uint8_t* p) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               : : "s"(lds), "v"(p) : "memory", "m0");
+}
+__device__ __forceinline__ void dma_word(unsigned lds, const uint8_t* p) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+               : : "s"(lds), "v"(p) : "memory", "m0");
+}
+template <int N>
+__device__ __forceinline__ void wait_dma() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "i"(N) : "memory");
+}
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); }
+
+// Byte offsets of a lane's pieces from a tile's first key (K, V) and of its parameter words.
+template <int D, int GS>
+struct LaneOffsets {
+  int k[Ring<D, GS>::KB / 1024], v, par;  // V pieces are 256 bytes apart, groups 4 P
+  int k_half, v_half, par_half;           // which 16 keys of the tile they belong to
+};
+template <int D, int GS>
+__device__ __forceinline__ LaneOffsets<D, GS> lane_offsets(int lane, int P) {
+  using X = Geo<D, GS>;
+  LaneOffsets<D, GS> o;
   const int lr = lane & 15, q = lane >> 4;
-  {
-    const uint8_t* rec = (lr >> 3) ? rb : ra;
-    const int off = ((lr >> 3) ? ob : oa) + 8 * ((lr >> 2) & 1) + (lr & 3);
+  const int key = 8 * (lr >> 2) + (lr & 3);  // + 4 j: the key of result row lr of result j
+  if constexpr (D == 128) {
+    o.k[0] = key * 64 + q * 16;
+    o.k[1] = o.k[0] + 4 * 64;
+  } else {  // a piece holds the words of two lanes: [j][piece of the row][row]
+    o.k[0] = (key + 4 * (lane >> 5)) * 32 + (q & 1) * 16;
+  }
+  o.k_half = lr >> 3;
+  o.v = q * 4 * D + lr * 16;
+  o.v_half = q >> 1;
+  o.par = (lane & 31) * 4 + (lane >> 5) * 4 * P * X::G;
+  o.par_half = (lane >> 4) & 1;
+  return o;
+}
+
+// Start the DMAs of one tile: keys [off, off + 32) of the page at ra if it holds them all, else
+// (pages of 16) the pages at ra and rb.
+template <int D, int GS>
+__device__ __forceinline__ void dma_tile(unsigned lds, const uint8_t* ra, const uint8_t* rb, int off,
+                                         int P, const LaneOffsets<D, GS>& o) {
+  using X = Geo<D, GS>;
+  using R = Ring<D, GS>;
+  const uint8_t* k = ra + off * (D / 2);
+  const uint8_t* v = ra + P * (D / 2) + off * (D / 2);
+  const uint8_t* p = ra + P * D + 4 * off;
+  if (P == 16) {  // the second half's addresses count from the tile's first key too
+    k = o.k_half ? rb - 16 * (D / 2) : k;
+    v = o.v_half ? rb + P * (D / 2) - 16 * (D / 2) : v;
+    p = o.par_half ? rb + P * D - 64 : p;
+  }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint8_t* p = rec + (off + 4 * j) * (D / 2) + q * (D / 8);
-      if constexpr (X::KW == 2) {
-        const uint2 w = *(const uint2*)p;
-        r.k[j][0] = w.x;
-        r.k[j][1] = w.y;
-      } else {
+  for (int i = 0; i < R::KB / 1024; ++i) dma_piece(lds + 1024 * i, k + o.k[i]);
 #pragma unroll
-        for (int i = 0; i < X::KW / 4; ++i) {
-          const u32x4 w = *(const u32x4*)(p + 16 * i);
+  for (int h = 0; h < X::H; ++h) dma_piece(lds + R::KB + 1024 * h, v + o.v + 256 * h);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) r.k[j][4 * i + e] = w[e];
-        }
-      }
+  for (int g = 0; g < X::G; ++g) dma_word(lds + R::KB + R::VB + 256 * g, p + o.par + 4 * P * g);
+}
+
+template <int D, int GS>
+__device__ __forceinline__ void read_tile(TileRegs<D, GS>& r, const uint8_t* st, int lane) {
+  using X = Geo<D, GS>;
+  using R = Ring<D, GS>;
+  const int q = lane >> 4;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    if constexpr (D == 128) {
+      const u32x4 w = *(const u32x4*)(st + 1024 * j + 16 * lane);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r.k[j][e] = w[e];
+    } else {
+      const uint2 w = *(const uint2*)(st + 512 * j + (q >> 1) * 256 + (lane & 15) * 16 + (q & 1) * 8);
+      r.k[j][0] = w.x;
+      r.k[j][1] = w.y;
     }
   }
-  const uint8_t* rec = (q >> 1) ? rb : ra;
-  const int off = ((q >> 1) ? ob : oa) + 8 * (q & 1);
-  const uint8_t* vb = rec + P * (D / 2) + (off >> 3) * (4 * D) + lr * 16;
 #pragma unroll
-  for (int h = 0; h < X::H; ++h) r.v[h] = *(const u32x4*)(vb + 256 * h);
-  const uint8_t* par = rec + P * D + 4 * off;
+  for (int h = 0; h < X::H; ++h) r.v[h] = *(const u32x4*)(st + R::KB + 1024 * h + 16 * lane);
+  const uint8_t* par = st + R::KB + R::VB + 32 * q;
 #pragma unroll
   for (int g = 0; g < X::G; ++g)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      r.kp[g][i] = *(const u32x4*)(par + 4 * P * g + 16 * i);
-      r.vp[g][i] = *(const u32x4*)(par + 4 * P * (X::G + g) + 16 * i);
+      r.kp[g][i] = *(const u32x4*)(par + 256 * g + 16 * i);
+      r.vp[g][i] = *(const u32x4*)(par + 256 * g + 128 + 16 * i);
     }
 }
 
@@ -243,25 +311,29 @@ __device__ __forceinline__ void do_tile(TileRegs<D, GS>& r, Column<D, GS> (&col)
   using X = Geo<D, GS>;
   const int q = lane >> 4;
   const int kq = key0 + 8 * q;
+  int there = 8;  // keys kq .. kq + there - 1 exist
   if (!whole) {
+    there = (dead >> (q >> 1)) & 1 ? 0 : n_keys - kq;
+    asm volatile("" : "+v"(there));  // (keeps the comparisons inside these branches)
     // parameters of keys that do not exist may hold anything
 #pragma unroll
     for (int g = 0; g < X::G; ++g)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const bool ok = kq + e < n_keys && !((dead >> (q >> 1)) & 1);
-        r.kp[g][e >> 2][e & 3] = ok ? r.kp[g][e >> 2][e & 3] : 0u;
-        r.vp[g][e >> 2][e & 3] = ok ? r.vp[g][e >> 2][e & 3] : 0u;
+        r.kp[g][e >> 2][e & 3] = e < there ? r.kp[g][e >> 2][e & 3] : 0u;
+        r.vp[g][e >> 2][e & 3] = e < there ? r.vp[g][e >> 2][e & 3] : 0u;
       }
   }
   // largest value step of the lane's keys (as fp16 patterns; the packed maximum also forms that
   // of the zeros, unused)
-  u16x2 tp = __builtin_bit_cast(u16x2, r.vp[0][0][0]);
+  u16x2 tp = {0, 0};
 #pragma unroll
   for (int g = 0; g < X::G; ++g)
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      tp = __builtin_elementwise_max(tp, __builtin_bit_cast(u16x2, r.vp[g][e >> 2][e & 3]));
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t w = r.vp[g][e >> 2][e & 3];
+      tp = __builtin_elementwise_max(tp, __builtin_bit_cast(u16x2, w));
+    }
   const uint32_t top = tp[0];
 
 #pragma unroll
@@ -288,10 +360,11 @@ __device__ __forceinline__ void do_tile(TileRegs<D, GS>& r, Column<D, GS> (&col)
     uint32_t seen = 0xff;  // bit e: key 8 q + e exists for the column
     if (!whole) {
       seen = 0;
+      int last = min(there - 1, c.pos - kq), fst = c.pos - lo_off - kq;
+      asm volatile("" : "+v"(last), "+v"(fst));
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int key = kq + e;
-        const bool ok = key <= c.pos && key >= c.pos - lo_off && key < n_keys && !((dead >> (q >> 1)) & 1);
+        const bool ok = e <= last && e >= fst;
         s[e] = ok ? s[e] : kNegInf;
         seen |= ok ? 1u << e : 0u;
       }
@@ -476,46 +549,62 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(wave
     t_lo = lo;
     t_hi = hi;
   }
-  const int32_t* table = c.table + (int64_t)b * c.max_blocks;
+  // (the table is not written here: scalar loads)
+  const auto* table = (const __attribute__((address_space(4))) int32_t*)(uintptr_t)(
+      c.table + (int64_t)b * c.max_blocks);
   const int last_blk = max(0, (len - 1) >> c.log2p);
+  const int n_pages = (int)c.n_pages;
   auto page_of = [&](int key, int& bad) -> const uint8_t* {
     const int pg = table[min(key >> c.log2p, last_blk)];
-    bad = pg < 0 || pg >= c.n_pages;
+    bad = (unsigned)pg >= (unsigned)n_pages;
     return c.pages + ((int64_t)(bad ? 0 : pg) * c.kv_heads + kvh) * (int64_t)c.record;
   };
   WeightScale ws;
   const CodeConsts cc = code_consts();
+  using R = Ring<D, GS>;
+  constexpr int NS = kStages;
+  constexpr int kRing = NS * R::BYTES * WAVES;
+  constexpr int kJoin = WIDE ? 0 : WAVES * 16 * (D + 6) * (int)sizeof(float);
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing > kJoin ? kRing : kJoin];
+  uint8_t* ring = lds + wave * (NS * R::BYTES);
+  const unsigned ring_at = lds_address(ring);
+  const LaneOffsets<D, GS> lo = lane_offsets<D, GS>(lane, P);
   const int step = WIDE ? 1 : WAVES;
-  struct Where {
-    const uint8_t *ra, *rb;
-    int dead;
-  };
-  auto where = [&](int t) {
-    Where w;
+  const int t0 = t_lo + (WIDE ? 0 : wave);
+  // tiles t0, t0 + step, ...: tile i of the wave in stage i mod NS
+  const int n_tiles = t_hi > t0 ? (t_hi - t0 + step - 1) / step : 0;
+  int dead_of[NS];
+  auto start = [&](int i, int s) {
+    const int key = 32 * (t0 + i * step);
     int bad_a, bad_b;
-    w.ra = page_of(32 * t, bad_a);
-    w.rb = page_of(32 * t + 16, bad_b);
-    w.dead = bad_a | (bad_b << 1);
-    return w;
+    const uint8_t* ra = page_of(key, bad_a);
+    const uint8_t* rb = page_of(key + 16, bad_b);
+    dead_of[s] = bad_a | (bad_b << 1);
+    dma_tile<D, GS>(ring_at + s * R::BYTES, ra, rb, key & (P - 1), P, lo);
   };
-  auto load = [&](TileRegs<D, GS>& r, const Where& w, int t) {
-    load_tile<D, GS>(r, w.ra, w.rb, (32 * t) & (P - 1), (32 * t + 16) & (P - 1), P, lane);
-  };
-  auto compute = [&](TileRegs<D, GS>& r, int dead, int t) {
-    const int key0 = 32 * t;
-    // every key of the tile exists and every column sees all of it
-    const bool whole = !dead && key0 + 32 <= len && key0 + 31 <= pos0 + first_i &&
-                       key0 >= pos0 + last_i - lo_off;
-    do_tile<D, GS, NC>(r, col, whole, key0, len, lo_off, dead, ws, cc, lane);
-  };
-  int t = t_lo + (WIDE ? 0 : wave);
-  // three waves a SIMD hide each other's loads; a second tile's registers for loads ahead would
-  // cost one of them
-  for (; t < t_hi; t += step) {
-    const Where w = where(t);
-    TileRegs<D, GS> r;
-    load(r, w, t);
-    compute(r, w.dead, t);
+#pragma unroll
+  for (int s = 0; s < NS; ++s)
+    if (s < n_tiles) start(s, s);
+  for (int i0 = 0; i0 < n_tiles; i0 += NS) {
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const int i = i0 + s;
+      if (i < n_tiles) {
+        // this stage's DMAs have landed: NS - 1 later tiles may be in flight
+        if (i + NS <= n_tiles) wait_dma<(NS - 1) * R::DMAS>();
+        else wait_dma<0>();
+        TileRegs<D, GS> r;
+        read_tile<D, GS>(r, ring + s * R::BYTES, lane);
+        wait_lds();  // the stage is in registers: refill it
+        const int dead = dead_of[s];
+        if (i + NS < n_tiles) start(i + NS, s);
+        const int key0 = 32 * (t0 + i * step);
+        // every key of the tile exists and every column sees all of it
+        const bool whole = !dead && key0 + 32 <= len && key0 + 31 <= pos0 + first_i &&
+                           key0 >= pos0 + last_i - lo_off;
+        do_tile<D, GS, NC>(r, col, whole, key0, len, lo_off, dead, ws, cc, lane);
+      }
+    }
   }
 
 #pragma unroll
@@ -553,8 +642,10 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(wave
     }
   } else {
     // the waves' results joined in wave order: each scaled to the block's largest M
-    __shared__ float so[WAVES][16][D + 4];
-    __shared__ float sm[WAVES][16], sl[WAVES][16];
+    float (*so)[16][D + 4] = (float (*)[16][D + 4])lds;
+    float (*sm)[16] = (float (*)[16])(so + WAVES);
+    float (*sl)[16] = sm + WAVES;
+    __syncthreads();  // the rings are done with
 #pragma unroll
     for (int t = 0; t < NC; ++t) {
       const int x = lane & 15;
