@@ -482,27 +482,17 @@ struct Partials {
   int splits;
 };
 
-// column tiles a wave of the WIDE form keeps (two do not fit the registers with four groups of
-// 32 channels)
-constexpr int wide_tiles(int dim, int group) { return dim / group > 2 ? 1 : 2; }
-
-// NC column tiles a wave; WIDE: the waves of a block hold different columns and walk all keys,
-// otherwise they share the columns and take the tiles in turn.
-#ifndef KV4_EU1
-#define KV4_EU1 3
-#endif
-#ifndef KV4_EU2
-#define KV4_EU2 3
-#endif
-constexpr int waves_per_simd(int dim, int group, bool wide) {
-  return wide ? 1 : dim / group > 2 ? 2 : dim == 64 && group == 64 ? 4 : dim == 128 && group==64 ? KV4_EU2 : KV4_EU1;
+// waves a SIMD that the registers are kept to
+constexpr int waves_per_simd(int dim, int group) {
+  return dim / group > 2 ? 2 : dim == 64 && group == 64 ? 4 : 3;
 }
 
-template <int D, int GS, int NC, bool WIDE, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(waves_per_simd(D, GS, WIDE)))) void k_kv4_attention(Kv4Cache c, Kv4Query a,
+// Up to 16 columns (decode): the waves of a block share the columns and take the tiles in turn.
+template <int D, int GS, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(waves_per_simd(D, GS)))) void k_kv4_attention(Kv4Cache c, Kv4Query a,
                                                                Partials part) {
   using X = Geo<D, GS>;
-  constexpr int kCols = 16 * NC * (WIDE ? WAVES : 1);  // columns a block
+  constexpr int NC = 1, kCols = 16;  // columns a block
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int b = blockIdx.z, kvh = blockIdx.y % c.kv_heads;
@@ -521,7 +511,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(wave
   const int len = min(len0, cap);
 
   Column<D, GS> col[NC];
-  const int col0 = tile * kCols + (WIDE ? wave * 16 * NC : 0);
+  const int col0 = tile * kCols;
 #pragma unroll
   for (int t = 0; t < NC; ++t) {
     const int x = col0 + 16 * t + (lane & 15);
@@ -533,7 +523,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(wave
     load_query<D, GS>(col[t], row, a.bf16, lane >> 4, a.scale);
     col[t].pos = has ? len0 - (c.starts[b + 1] - row0) + i : -1;
   }
-  // keys that some column of the block (WIDE: of the wave) sees
+  // keys that some column sees
   const int lo_off = a.window > 0 ? a.window - 1 : 0x3fffffff;
   const int first_i = col0 / group;
   const int last_i = min(col0 + 16 * NC - 1, n_cols - 1) / group;
@@ -541,7 +531,6 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(wave
   const int end = min(len, pos0 + last_i + 1);  // may be <= 0
   const int begin = max(0, pos0 + first_i - lo_off);
   int t_lo = begin >> 5, t_hi = max(0, end + 31) >> 5;
-  if (col0 >= n_cols) t_hi = t_lo;  // WIDE: a wave past the last column
   {
     // this split's share of the tiles
     const int n = max(0, t_hi - t_lo), s = part.splits;
@@ -564,13 +553,13 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(wave
   using R = Ring<D, GS>;
   constexpr int NS = kStages;
   constexpr int kRing = NS * R::BYTES * WAVES;
-  constexpr int kJoin = WIDE ? 0 : WAVES * 16 * (D + 6) * (int)sizeof(float);
+  constexpr int kJoin = WAVES * 16 * (D + 6) * (int)sizeof(float);
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing > kJoin ? kRing : kJoin];
   uint8_t* ring = lds + wave * (NS * R::BYTES);
   const unsigned ring_at = lds_address(ring);
   const LaneOffsets<D, GS> lo = lane_offsets<D, GS>(lane, P);
-  const int step = WIDE ? 1 : WAVES;
-  const int t0 = t_lo + (WIDE ? 0 : wave);
+  const int step = WAVES;
+  const int t0 = t_lo + wave;
   // tiles t0, t0 + step, ...: tile i of the wave in stage i mod NS
   const int n_tiles = t_hi > t0 ? (t_hi - t0 + step - 1) / step : 0;
   int dead_of[NS];
@@ -610,37 +599,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(wave
 #pragma unroll
   for (int t = 0; t < NC; ++t) finish<D, GS>(col[t]);
 
-  if constexpr (WIDE) {
-#pragma unroll
-    for (int t = 0; t < NC; ++t) {
-      const int x = col0 + 16 * t + (lane & 15);
-      if (x < n_cols) {
-        const int i = x / group, h = x - i * group;
-        const int64_t r = (int64_t)(row0 + i) * a.heads + kvh * group + h;
-        const Column<D, GS>& cx = col[t];
-        const bool join = part.splits > 1;
-        const float inv = join ? 1.0f : cx.l == 0.0f ? 0.0f : 1.0f / cx.l;
-#pragma unroll
-        for (int n = 0; n < X::N; ++n) {
-          const int ch = 16 * n + 4 * (lane >> 4);
-          if (join) {
-            *(f32x4*)(part.o + (r * part.splits + split) * D + ch) = cx.o[n];
-          } else {
-            const float v[4] = {cx.o[n][0] * inv, cx.o[n][1] * inv, cx.o[n][2] * inv, cx.o[n][3] * inv};
-            store4(a.out, r * D + ch, a.bf16, v);
-          }
-        }
-        if ((lane >> 4) == 0) {
-          if (join) {
-            part.ml[(r * part.splits + split) * 2] = cx.M();
-            part.ml[(r * part.splits + split) * 2 + 1] = cx.l;
-          } else if (a.lse) {
-            a.lse[r] = lse_of(cx.M(), cx.l);
-          }
-        }
-      }
-    }
-  } else {
+  {
     // the waves' results joined in wave order: each scaled to the block's largest M
     float (*so)[16][D + 4] = (float (*)[16][D + 4])lds;
     float (*sm)[16] = (float (*)[16])(so + WAVES);
@@ -689,6 +648,369 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(wave
           const float v[4] = {o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
           store4(a.out, r * D + ch, a.bf16, v);
           if (ch == 0 && a.lse) a.lse[r] = lse_of(M, l);
+        }
+      }
+    }
+  }
+}
+
+// ---- many columns (prompts) ---------------------------------------------------------------
+//
+// A block of four waves takes 16 NC columns a wave and walks the keys 64 at a time.  The codes
+// are made operands once a block: each wave decodes a part of the next 64 keys, as the exact
+// integers c - z in fp16, into LDS (two buffers, one barrier a step) while the codes after that
+// are in flight to registers.  The steps stay fp32 factors of the scores and of the weights, as
+// above, so a value is never rounded.
+template <int D, int GS>
+struct Wide {
+  using X = Geo<D, GS>;
+  static constexpr int NC = 2;                       // column tiles a wave
+  static constexpr int COLS = 16 * NC * kWaves;      // columns a block
+  static constexpr int K_BYTES = 2 * 2 * X::KW * 1024;  // [32 keys][result j][word][lane] pieces
+  static constexpr int V_BYTES = 2 * X::N * 1024;       // [32 keys][value result][lane] pieces
+  static constexpr int P_BYTES = 2 * X::G * 256;        // [K, V][group][64 keys] parameter words
+  static constexpr int BYTES = K_BYTES + V_BYTES + P_BYTES;
+};
+
+// What a wave decodes of one step, in registers: the codes of a K pass (32 keys, result j) and
+// of a V pass (32 keys, 16-byte piece h), the zeros they need, and its part of the parameters.
+template <int D, int GS>
+struct Raw {
+  using X = Geo<D, GS>;
+  static constexpr int GH = GS == 32 ? 2 : 1;        // groups of one V piece
+  static constexpr int PW = (2 * X::G + kWaves - 1) / kWaves;  // parameter words a thread
+  uint32_t k[X::KW], kz[X::G];
+  u32x4 v, vz[GH][2];
+  uint32_t par[PW];
+};
+
+template <int D, int GS>
+__global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2)))
+void k_kv4_attention_wide(Kv4Cache c, Kv4Query a, Partials part) {
+  using X = Geo<D, GS>;
+  using W = Wide<D, GS>;
+  using R = Raw<D, GS>;
+  constexpr int NC = W::NC;
+  __shared__ __attribute__((aligned(1024))) uint8_t buf0[W::BYTES];
+  __shared__ __attribute__((aligned(1024))) uint8_t buf1[W::BYTES];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lr = lane & 15, q = lane >> 4;
+  const int b = blockIdx.z, kvh = blockIdx.y % c.kv_heads;
+  const int split = blockIdx.y / c.kv_heads;
+  const int tile = gridDim.x - 1 - blockIdx.x;  // later column tiles see more keys: they go first
+  const int group = a.heads / c.kv_heads;
+  const int row0 = c.starts[b];
+  const int rows = min(c.starts[b + 1] - row0, a.max_q);
+  const int len0 = c.lens[b];
+  const int n_cols = rows * group;
+  if (tile * W::COLS >= n_cols) return;  // the whole block
+  const int P = 1 << c.log2p;
+  const int cap = (int)min((int64_t)c.max_blocks << c.log2p, (int64_t)a.max_len);
+  const int len = min(len0, cap);
+  const int pos0 = len0 - (c.starts[b + 1] - row0);
+  const int lo_off = a.window > 0 ? a.window - 1 : 0x3fffffff;
+
+  Column<D, GS> col[NC];
+  const int col0 = tile * W::COLS + wave * 16 * NC;
+#pragma unroll
+  for (int t = 0; t < NC; ++t) {
+    const int x = col0 + 16 * t + lr;
+    const int i = x / group, h = x - i * group;
+    const bool has = x < n_cols;
+    const uint16_t* row =
+        has ? (const uint16_t*)a.q + (int64_t)(row0 + i) * a.qt + (int64_t)(kvh * group + h) * a.qh
+            : nullptr;
+    load_query<D, GS>(col[t], row, a.bf16, q, a.scale);
+    col[t].pos = has ? pos0 + i : -1;
+  }
+  // positions of the block's and of the wave's rows
+  const int blk_first = pos0 + tile * W::COLS / group;
+  const int blk_last = pos0 + min(tile * W::COLS + W::COLS - 1, n_cols - 1) / group;
+  const int first = pos0 + col0 / group;
+  const int last = col0 < n_cols ? pos0 + min(col0 + 16 * NC - 1, n_cols - 1) / group : -1;
+  int t_lo = max(0, blk_first - lo_off) >> 6, t_hi = max(0, min(len, blk_last + 1) + 63) >> 6;
+  {
+    const int n = max(0, t_hi - t_lo), s = part.splits;
+    const int lo = t_lo + (int)((int64_t)n * split / s), hi = t_lo + (int)((int64_t)n * (split + 1) / s);
+    t_lo = lo;
+    t_hi = hi;
+  }
+  const auto* table = (const __attribute__((address_space(4))) int32_t*)(uintptr_t)(
+      c.table + (int64_t)b * c.max_blocks);
+  const int last_blk = max(0, (len - 1) >> c.log2p);
+  const int n_pages = (int)c.n_pages;
+  auto page_of = [&](int key, int& bad) -> const uint8_t* {
+    const int pg = table[min(key >> c.log2p, last_blk)];
+    bad = (unsigned)pg >= (unsigned)n_pages;
+    return c.pages + ((int64_t)(bad ? 0 : pg) * c.kv_heads + kvh) * (int64_t)c.record;
+  };
+  const CodeConsts cc = code_consts();
+  const int tt = wave >> 1, sub = wave & 1;  // the wave's decode passes: 32 keys, K result / V piece
+
+  // the codes of step t into registers; parameters of keys that do not exist become zero
+  // (bit i of what it returns: the 16 keys i of the step lie on no page)
+  auto fetch = [&](R& r, int t) -> int {
+    const uint8_t* rec[4];
+    int bad[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) rec[i] = page_of(64 * t + 16 * i, bad[i]);
+    const int key32 = 64 * t + 32 * tt;
+    {
+      const int half = lr >> 3, in = 8 * (lr >> 2) + 4 * sub + (lr & 3);  // key of the tile of 32
+      const uint8_t* p = half ? (tt ? rec[3] : rec[1]) : (tt ? rec[2] : rec[0]);
+      const int off = (key32 + in) & (P - 1);
+      const uint8_t* kp = p + off * (D / 2) + q * (D / 8);
+      if constexpr (X::KW == 2) {
+        const uint2 w = *(const uint2*)kp;
+        r.k[0] = w.x;
+        r.k[1] = w.y;
+      } else {
+        const u32x4 w = *(const u32x4*)kp;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r.k[e] = w[e];
+      }
+      const bool ok = key32 + in < len && !(half ? (tt ? bad[3] : bad[1]) : (tt ? bad[2] : bad[0]));
+#pragma unroll
+      for (int g = 0; g < X::G; ++g) {
+        const uint32_t w = *(const uint32_t*)(p + P * D + 4 * (P * g + off));
+        r.kz[g] = ok ? w : 0u;
+      }
+    }
+    if (sub < X::H) {
+      const int half = q >> 1;
+      const uint8_t* p = half ? (tt ? rec[3] : rec[1]) : (tt ? rec[2] : rec[0]);
+      const int off = (key32 + 8 * q) & (P - 1);
+      r.v = *(const u32x4*)(p + P * (D / 2) + off * (D / 2) + 256 * sub + 16 * lr);
+      const int there = (half ? (tt ? bad[3] : bad[1]) : (tt ? bad[2] : bad[0])) ? 0 : len - key32 - 8 * q;
+#pragma unroll
+      for (int g = 0; g < R::GH; ++g) {
+        // the groups of channels 64 sub .. 64 sub + 63
+        const int gg = (64 * sub + 32 * g) / GS;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          u32x4 w = *(const u32x4*)(p + P * D + 4 * (P * (X::G + gg) + off) + 16 * i);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = 4 * i + e < there ? w[e] : 0u;
+          r.vz[g][i] = w;
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < R::PW; ++k) {
+      const int pg = wave + kWaves * k;  // side and group
+      if (pg < 2 * X::G) {
+        const int i = lane >> 4;
+        const uint8_t* p = i & 2 ? (i & 1 ? rec[3] : rec[2]) : (i & 1 ? rec[1] : rec[0]);
+        const int dead = i & 2 ? (i & 1 ? bad[3] : bad[2]) : (i & 1 ? bad[1] : bad[0]);
+        const uint32_t w = *(const uint32_t*)(p + P * D + 4 * (P * pg + ((64 * t + lane) & (P - 1))));
+        r.par[k] = 64 * t + lane < len && !dead ? w : 0u;
+      }
+    }
+    return bad[0] | bad[1] << 1 | bad[2] << 2 | bad[3] << 3;
+  };
+  // 16 + c minus 16 + z, exact in fp16
+  auto sub2 = [&](uint32_t code, uint32_t zero) -> uint32_t {
+    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, code) - __builtin_bit_cast(half2v, zero));
+  };
+  auto plus16 = [&](uint32_t zz) -> uint32_t {
+    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, zz) + __builtin_bit_cast(half2v, kOffset));
+  };
+  auto decode = [&](const R& r, uint8_t* buf) {
+#pragma unroll
+    for (int w = 0; w < X::KW; ++w) {
+      const uint32_t par = r.kz[w / X::WPG];
+      const uint32_t z = plus16(__builtin_amdgcn_perm(par, par, 0x03020302u));
+      const u32x4 o = {sub2(code_pair<0>(r.k[w], cc), z), sub2(code_pair<1>(r.k[w], cc), z),
+                       sub2(code_pair<2>(r.k[w], cc), z), sub2(code_pair<3>(r.k[w], cc), z)};
+      *(u32x4*)(buf + ((tt * 2 + sub) * X::KW + w) * 1024 + 16 * lane) = o;
+    }
+    if (sub < X::H) {
+      uint32_t z[R::GH][4];
+#pragma unroll
+      for (int g = 0; g < R::GH; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t pa = r.vz[g][i >> 1][2 * (i & 1)], pb = r.vz[g][i >> 1][2 * (i & 1) + 1];
+          z[g][i] = plus16(__builtin_amdgcn_perm(pb, pa, 0x07060302u));
+        }
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        u32x4 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w = r.v[i];
+          const uint32_t cp = n == 0 ? code_pair<0>(w, cc) : n == 1 ? code_pair<1>(w, cc)
+                              : n == 2 ? code_pair<2>(w, cc) : code_pair<3>(w, cc);
+          o[i] = sub2(cp, z[R::GH == 2 ? n >> 1 : 0][i]);
+        }
+        *(u32x4*)(buf + W::K_BYTES + (tt * X::N + 4 * sub + n) * 1024 + 16 * lane) = o;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < R::PW; ++k) {
+      const int pg = wave + kWaves * k;
+      if (pg < 2 * X::G) *(uint32_t*)(buf + W::K_BYTES + W::V_BYTES + 256 * pg + 4 * lane) = r.par[k];
+    }
+  };
+
+  WeightScale ws;
+  auto compute = [&](const uint8_t* buf, int t, int dead) {
+    const int key0 = 64 * t;
+    if (key0 > last || key0 + 63 < first - lo_off || last < 0) return;  // nothing for this wave
+    const bool whole = !dead && key0 + 64 <= len && key0 + 63 <= first && key0 >= last - lo_off;
+    const uint8_t* par = buf + W::K_BYTES + W::V_BYTES + 32 * q;
+    u32x4 vp[2][X::G][2];
+    u16x2 tp = {0, 0};
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int g = 0; g < X::G; ++g)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          vp[h][g][i] = *(const u32x4*)(par + 256 * (X::G + g) + 128 * h + 16 * i);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t w = vp[h][g][i][e];
+            tp = __builtin_elementwise_max(tp, __builtin_bit_cast(u16x2, w));
+          }
+        }
+    const uint32_t top = tp[0];
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+      Column<D, GS>& cl = col[n];
+      float s[16];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int g = 0; g < X::G; ++g) {
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int u = 0; u < X::WPG; ++u) {
+              const half8v kk = *(const half8v*)(buf + ((h * 2 + j) * X::KW + g * X::WPG + u) * 1024 + 16 * lane);
+              acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(kk, cl.q[g * X::WPG + u], acc, 0, 0, 0);
+            }
+            const u32x4 kp = *(const u32x4*)(par + 256 * g + 128 * h + 16 * j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int x = 8 * h + 4 * j + e;
+              s[x] = fmaf(lo16(kp[e]), acc[e], g == 0 ? 0.0f : s[x]);
+            }
+          }
+      uint32_t seen = 0xffff;
+      if (!whole) {
+        seen = 0;
+        int hi = min(len - 1, cl.pos) - key0 - 8 * q, lo = cl.pos - lo_off - key0 - 8 * q;
+        asm volatile("" : "+v"(hi), "+v"(lo));  // (keeps the comparisons inside this branch)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int at = e < 8 ? e : e + 24;  // key at + 8 q of the step
+          const bool ok = at <= hi && at >= lo && !((dead >> (2 * (e >> 3) + (q >> 1))) & 1);
+          s[e] = ok ? s[e] : kNegInf;
+          seen |= ok ? 1u << e : 0u;
+        }
+      }
+      float mx = s[0];
+#pragma unroll
+      for (int e = 1; e < 16; ++e) mx = fmaxf(mx, s[e]);
+      mx *= cl.sigma;
+      if (__any(mx > cl.m || top >= ws.limit)) {
+        if (n == 0) {
+          uint32_t all = top;
+          all = max(all, (uint32_t)__shfl_xor((int)all, 16));
+          all = max(all, (uint32_t)__shfl_xor((int)all, 32));
+          const uint32_t ex = min(max(all, 0x0400u), 0x7bffu) >> 10;
+          ws.limit = max(ws.limit, (ex + 1) << 10);
+          ws.f = fminf(ws.f, (float)(14 + 15 - (int)ex));
+        }
+        const float m = fmaxf(cl.m, max_q(mx));
+        const float nM = m == kNegInf ? 0.0f : ws.f - m;
+        const float x = cl.m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(nM - cl.nM);
+        cl.m = m;
+        cl.nM = nM;
+        cl.l *= x;
+#pragma unroll
+        for (int i = 0; i < X::N; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) cl.o[i][e] *= x;
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], cl.sigma, cl.nM));
+        cl.l += s[e];
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int g = 0; g < X::G; ++g) {
+          u32x4 w;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t pa = vp[h][g][i >> 1][2 * (i & 1)], pb = vp[h][g][i >> 1][2 * (i & 1) + 1];
+            w[i] = pair16(fmaf(s[8 * h + 2 * i], lo16(pa), 0.0f), fmaf(s[8 * h + 2 * i + 1], lo16(pb), 0.0f));
+          }
+          if (!whole) {  // a masked key's step may be NaN
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[i] &= (seen >> (8 * h + 2 * i) & 1 ? 0xffffu : 0u) |
+                      (seen >> (8 * h + 2 * i + 1) & 1 ? 0xffff0000u : 0u);
+          }
+#pragma unroll
+          for (int i = g * (GS / 16); i < (g + 1) * (GS / 16); ++i) {
+            const half8v vv = *(const half8v*)(buf + W::K_BYTES + (h * X::N + i) * 1024 + 16 * lane);
+            cl.o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, __builtin_bit_cast(half8v, w), cl.o[i], 0, 0, 0);
+          }
+        }
+    }
+  };
+
+  if (t_lo < t_hi) {
+    R r;
+    int dead0 = fetch(r, t_lo), dead1 = 0;
+    decode(r, buf0);
+    __syncthreads();
+    for (int t = t_lo; t < t_hi; t += 2) {
+      if (t + 1 < t_hi) dead1 = fetch(r, t + 1);
+      compute(buf0, t, dead0);
+      if (t + 1 >= t_hi) break;
+      decode(r, buf1);
+      __syncthreads();
+      if (t + 2 < t_hi) dead0 = fetch(r, t + 2);
+      compute(buf1, t + 1, dead1);
+      if (t + 2 >= t_hi) break;
+      decode(r, buf0);
+      __syncthreads();
+    }
+  }
+
+#pragma unroll
+  for (int t = 0; t < NC; ++t) {
+    const int x = col0 + 16 * t + lr;
+    Column<D, GS>& cl = col[t];
+    cl.l = sum_q(cl.l);
+    if (x < n_cols) {
+      const int i = x / group, h = x - i * group;
+      const int64_t r = (int64_t)(row0 + i) * a.heads + kvh * group + h;
+      const bool join = part.splits > 1;
+      const float inv = join ? 1.0f : cl.l == 0.0f ? 0.0f : 1.0f / cl.l;
+#pragma unroll
+      for (int n = 0; n < X::N; ++n) {
+        const int ch = 16 * n + 4 * q;
+        if (join) {
+          *(f32x4*)(part.o + (r * part.splits + split) * D + ch) = cl.o[n];
+        } else {
+          const float v[4] = {cl.o[n][0] * inv, cl.o[n][1] * inv, cl.o[n][2] * inv, cl.o[n][3] * inv};
+          store4(a.out, r * D + ch, a.bf16, v);
+        }
+      }
+      if (q == 0) {
+        if (join) {
+          part.ml[(r * part.splits + split) * 2] = cl.M();
+          part.ml[(r * part.splits + split) * 2 + 1] = cl.l;
+        } else if (a.lse) {
+          a.lse[r] = lse_of(cl.M(), cl.l);
         }
       }
     }
@@ -771,13 +1093,11 @@ hipError_t launch_dg(const Kv4Cache& c, const Kv4Query& q, const Kv4Plan& p, con
                      hipStream_t stream) {
   const dim3 grid((unsigned)p.tiles, (unsigned)(c.kv_heads * p.splits), (unsigned)c.n_seqs);
   if (p.wide)
-    hipLaunchKernelGGL((k_kv4_attention<D, GS, wide_tiles(D, GS), true, kWaves>), grid, dim3(64 * kWaves),
-                       0, stream, c, q, part);
+    hipLaunchKernelGGL((k_kv4_attention_wide<D, GS>), grid, dim3(64 * kWaves), 0, stream, c, q, part);
   else if (p.waves == 8)
-    hipLaunchKernelGGL((k_kv4_attention<D, GS, 1, false, 8>), grid, dim3(512), 0, stream, c, q, part);
+    hipLaunchKernelGGL((k_kv4_attention<D, GS, 8>), grid, dim3(512), 0, stream, c, q, part);
   else
-    hipLaunchKernelGGL((k_kv4_attention<D, GS, 1, false, kWaves>), grid, dim3(64 * kWaves), 0, stream, c,
-                       q, part);
+    hipLaunchKernelGGL((k_kv4_attention<D, GS, kWaves>), grid, dim3(64 * kWaves), 0, stream, c, q, part);
   return hipGetLastError();
 }
 
@@ -788,7 +1108,7 @@ Kv4Plan kv4_plan(int64_t n_seqs, int heads, int kv_heads, int dim, int group, in
   Kv4Plan p;
   const int64_t cols = max_q * (heads / kv_heads);
   p.wide = cols > 16;
-  const int64_t per = p.wide ? 16 * wide_tiles(dim, group) * kWaves : 16;
+  const int64_t per = p.wide ? Wide<128, 128>::COLS : 16;
   p.tiles = (int)((cols + per - 1) / per);
   const int64_t blocks = n_seqs * kv_heads * p.tiles;
   // four blocks a compute unit, at least 256 keys a split
