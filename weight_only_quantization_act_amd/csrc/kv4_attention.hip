@@ -22,8 +22,11 @@
 //               which is the layout of an operand of the next product: no data moves between
 //               lanes.
 //   O = V^T W   D / 16 results, row 4 q + e of result n is channel 16 n + 4 q + e.
-// The running maximum is per column; weights are scaled by 2^f with f so chosen from the
-// largest value step seen that w 2^f stays below 2^15: fp16 holds them with full precision
+// The reference of the exponents is per column and follows the running maximum with a slack of
+// 2^kSlack, so that after the first tiles hardly any tile has to rescale what was summed
+// (without it a column of random scores does so in one of t tiles after t, the wave's 16 or 32
+// columns in nearly all of the first few dozen).  The weights are scaled by 2^f, f so chosen
+// from the largest value step seen that w 2^f stays below 2^15: fp16 holds them with full precision
 // down to 2^-29 of the largest.  A rise of the maximum or of that step multiplies what was
 // summed so far by exp2 of the difference.
 //
@@ -46,6 +49,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
+constexpr float kSlack = 4.0f;
 constexpr float kNegInf = -__builtin_inff();
 constexpr int kWaves = 4;
 #ifndef KV4_NS
@@ -222,7 +226,7 @@ struct Column {
   float qsum[X::G];    // sum of a group's q
   float sigma;         // from the raw score to log2 units
   int pos;             // the row's position; -1: no row
-  float m;             // running maximum of the scores, log2 units
+  float m;             // reference of the scores, log2 units: their maximum to within kSlack
   float nM;            // f - m: weights are exp2(s + nM); 0 before the first key
   float l;             // this lane's sum of exp2(s + nM)
   f32x4 z[X::G];       // sum of weight x (zero + 16): every row the same
@@ -375,7 +379,7 @@ __device__ __forceinline__ void do_tile(TileRegs<D, GS>& r, Column<D, GS> (&col)
     mx *= c.sigma;
     // seldom: a score above the column's maximum, or a value step above what the weights' scale
     // was made for
-    if (__any(mx > c.m || top >= ws.limit)) {
+    if (__any(mx > c.m + kSlack || top >= ws.limit)) {
       if (t == 0) {
         uint32_t all = top;
         all = max(all, (uint32_t)__shfl_xor((int)all, 16));
@@ -383,7 +387,7 @@ __device__ __forceinline__ void do_tile(TileRegs<D, GS>& r, Column<D, GS> (&col)
         // zero and subnormal steps count as the smallest normal one, others as finite
         const uint32_t ex = min(max(all, 0x0400u), 0x7bffu) >> 10;
         ws.limit = max(ws.limit, (ex + 1) << 10);
-        ws.f = fminf(ws.f, (float)(14 + 15 - (int)ex));
+        ws.f = fminf(ws.f, 14.0f - kSlack + 15.0f - (float)ex);
       }
       const float m = fmaxf(c.m, max_q(mx));
       const float nM = m == kNegInf ? 0.0f : ws.f - m;
@@ -664,7 +668,10 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(wave
 template <int D, int GS>
 struct Wide {
   using X = Geo<D, GS>;
-  static constexpr int NC = 2;                       // column tiles a wave
+  #ifndef KV4_WNC
+#define KV4_WNC 2
+#endif
+  static constexpr int NC = KV4_WNC;                       // column tiles a wave
   static constexpr int COLS = 16 * NC * kWaves;      // columns a block
   static constexpr int K_BYTES = 2 * 2 * X::KW * 1024;  // [32 keys][result j][word][lane] pieces
   static constexpr int V_BYTES = 2 * X::N * 1024;       // [32 keys][value result][lane] pieces
@@ -876,56 +883,70 @@ void k_kv4_attention_wide(Kv4Cache c, Kv4Query a, Partials part) {
           }
         }
     const uint32_t top = tp[0];
+    // scores of all column tiles: an operand read once feeds NC products
+    float s[NC][16];
 #pragma unroll
-    for (int n = 0; n < NC; ++n) {
-      Column<D, GS>& cl = col[n];
-      float s[16];
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int g = 0; g < X::G; ++g) {
+          f32x4 acc[NC];
 #pragma unroll
-          for (int g = 0; g < X::G; ++g) {
-            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+          for (int n = 0; n < NC; ++n) acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int u = 0; u < X::WPG; ++u) {
-              const half8v kk = *(const half8v*)(buf + ((h * 2 + j) * X::KW + g * X::WPG + u) * 1024 + 16 * lane);
-              acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(kk, cl.q[g * X::WPG + u], acc, 0, 0, 0);
-            }
-            const u32x4 kp = *(const u32x4*)(par + 256 * g + 128 * h + 16 * j);
+          for (int u = 0; u < X::WPG; ++u) {
+            const half8v kk = *(const half8v*)(buf + ((h * 2 + j) * X::KW + g * X::WPG + u) * 1024 + 16 * lane);
+#pragma unroll
+            for (int n = 0; n < NC; ++n)
+              acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kk, col[n].q[g * X::WPG + u], acc[n], 0, 0, 0);
+          }
+          const u32x4 kp = *(const u32x4*)(par + 256 * g + 128 * h + 16 * j);
+#pragma unroll
+          for (int n = 0; n < NC; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int x = 8 * h + 4 * j + e;
-              s[x] = fmaf(lo16(kp[e]), acc[e], g == 0 ? 0.0f : s[x]);
+              s[n][x] = fmaf(lo16(kp[e]), acc[n][e], g == 0 ? 0.0f : s[n][x]);
             }
-          }
-      uint32_t seen = 0xffff;
-      if (!whole) {
-        seen = 0;
-        int hi = min(len - 1, cl.pos) - key0 - 8 * q, lo = cl.pos - lo_off - key0 - 8 * q;
+        }
+    uint32_t seen[NC];
+    if (!whole) {
+#pragma unroll
+      for (int n = 0; n < NC; ++n) {
+        seen[n] = 0;
+        int hi = min(len - 1, col[n].pos) - key0 - 8 * q, lo = col[n].pos - lo_off - key0 - 8 * q;
         asm volatile("" : "+v"(hi), "+v"(lo));  // (keeps the comparisons inside this branch)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const int at = e < 8 ? e : e + 24;  // key at + 8 q of the step
           const bool ok = at <= hi && at >= lo && !((dead >> (2 * (e >> 3) + (q >> 1))) & 1);
-          s[e] = ok ? s[e] : kNegInf;
-          seen |= ok ? 1u << e : 0u;
+          s[n][e] = ok ? s[n][e] : kNegInf;
+          seen[n] |= ok ? 1u << e : 0u;
         }
       }
-      float mx = s[0];
+    }
+    float mx[NC];
+    bool up = top >= ws.limit;
 #pragma unroll
-      for (int e = 1; e < 16; ++e) mx = fmaxf(mx, s[e]);
-      mx *= cl.sigma;
-      if (__any(mx > cl.m || top >= ws.limit)) {
-        if (n == 0) {
-          uint32_t all = top;
-          all = max(all, (uint32_t)__shfl_xor((int)all, 16));
-          all = max(all, (uint32_t)__shfl_xor((int)all, 32));
-          const uint32_t ex = min(max(all, 0x0400u), 0x7bffu) >> 10;
-          ws.limit = max(ws.limit, (ex + 1) << 10);
-          ws.f = fminf(ws.f, (float)(14 + 15 - (int)ex));
-        }
-        const float m = fmaxf(cl.m, max_q(mx));
+    for (int n = 0; n < NC; ++n) {
+      mx[n] = s[n][0];
+#pragma unroll
+      for (int e = 1; e < 16; ++e) mx[n] = fmaxf(mx[n], s[n][e]);
+      mx[n] *= col[n].sigma;
+      up |= mx[n] > col[n].m + kSlack;
+    }
+    if (__any(up)) {
+      uint32_t all = top;
+      all = max(all, (uint32_t)__shfl_xor((int)all, 16));
+      all = max(all, (uint32_t)__shfl_xor((int)all, 32));
+      const uint32_t ex = min(max(all, 0x0400u), 0x7bffu) >> 10;
+      ws.limit = max(ws.limit, (ex + 1) << 10);
+      ws.f = fminf(ws.f, 14.0f - kSlack + 15.0f - (float)ex);
+#pragma unroll
+      for (int n = 0; n < NC; ++n) {
+        Column<D, GS>& cl = col[n];
+        const float m = fmaxf(cl.m, max_q(mx[n]));
         const float nM = m == kNegInf ? 0.0f : ws.f - m;
         const float x = cl.m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(nM - cl.nM);
         cl.m = m;
@@ -936,34 +957,49 @@ void k_kv4_attention_wide(Kv4Cache c, Kv4Query a, Partials part) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) cl.o[i][e] *= x;
       }
+    }
+    u32x4 w[NC][2][X::G];
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], cl.sigma, cl.nM));
-        cl.l += s[e];
+        s[n][e] = __builtin_amdgcn_exp2f(fmaf(s[n][e], col[n].sigma, col[n].nM));
+        col[n].l += s[n][e];
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int g = 0; g < X::G; ++g) {
-          u32x4 w;
+        for (int g = 0; g < X::G; ++g)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint32_t pa = vp[h][g][i >> 1][2 * (i & 1)], pb = vp[h][g][i >> 1][2 * (i & 1) + 1];
-            w[i] = pair16(fmaf(s[8 * h + 2 * i], lo16(pa), 0.0f), fmaf(s[8 * h + 2 * i + 1], lo16(pb), 0.0f));
+            w[n][h][g][i] = pair16(fmaf(s[n][8 * h + 2 * i], lo16(pa), 0.0f),
+                                   fmaf(s[n][8 * h + 2 * i + 1], lo16(pb), 0.0f));
           }
-          if (!whole) {  // a masked key's step may be NaN
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[i] &= (seen >> (8 * h + 2 * i) & 1 ? 0xffffu : 0u) |
-                      (seen >> (8 * h + 2 * i + 1) & 1 ? 0xffff0000u : 0u);
-          }
-#pragma unroll
-          for (int i = g * (GS / 16); i < (g + 1) * (GS / 16); ++i) {
-            const half8v vv = *(const half8v*)(buf + W::K_BYTES + (h * X::N + i) * 1024 + 16 * lane);
-            cl.o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, __builtin_bit_cast(half8v, w), cl.o[i], 0, 0, 0);
-          }
-        }
     }
+    if (!whole) {  // a masked key's step may be NaN
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t bits = (seen[n] >> (8 * h + 2 * i) & 1 ? 0xffffu : 0u) |
+                                  (seen[n] >> (8 * h + 2 * i + 1) & 1 ? 0xffff0000u : 0u);
+#pragma unroll
+            for (int g = 0; g < X::G; ++g) w[n][h][g][i] &= bits;
+          }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < X::N; ++i) {
+        const half8v vv = *(const half8v*)(buf + W::K_BYTES + (h * X::N + i) * 1024 + 16 * lane);
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+          col[n].o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+              vv, __builtin_bit_cast(half8v, w[n][h][i / (GS / 16)]), col[n].o[i], 0, 0, 0);
+      }
   };
 
   if (t_lo < t_hi) {
