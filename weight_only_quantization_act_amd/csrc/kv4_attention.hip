@@ -665,13 +665,13 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(wave
 // integers c - z in fp16, into LDS (two buffers, one barrier a step) while the codes after that
 // are in flight to registers.  The steps stay fp32 factors of the scores and of the weights, as
 // above, so a value is never rounded.
+// (two do not fit the registers with four groups of 32 channels)
+constexpr int wide_tiles(int dim, int group) { return dim / group > 2 ? 1 : 2; }
+
 template <int D, int GS>
 struct Wide {
   using X = Geo<D, GS>;
-  #ifndef KV4_WNC
-#define KV4_WNC 2
-#endif
-  static constexpr int NC = KV4_WNC;                       // column tiles a wave
+    static constexpr int NC = wide_tiles(D, GS);           // column tiles a wave
   static constexpr int COLS = 16 * NC * kWaves;      // columns a block
   static constexpr int K_BYTES = 2 * 2 * X::KW * 1024;  // [32 keys][result j][word][lane] pieces
   static constexpr int V_BYTES = 2 * X::N * 1024;       // [32 keys][value result][lane] pieces
@@ -689,6 +689,9 @@ struct Raw {
   uint32_t k[X::KW], kz[X::G];
   u32x4 v, vz[GH][2];
   uint32_t par[PW];
+  // which of them exist (applied when they are decoded, so that nothing waits for a load here)
+  bool k_ok, par_ok;
+  int v_there;
 };
 
 template <int D, int GS>
@@ -747,21 +750,26 @@ void k_kv4_attention_wide(Kv4Cache c, Kv4Query a, Partials part) {
       c.table + (int64_t)b * c.max_blocks);
   const int last_blk = max(0, (len - 1) >> c.log2p);
   const int n_pages = (int)c.n_pages;
-  auto page_of = [&](int key, int& bad) -> const uint8_t* {
-    const int pg = table[min(key >> c.log2p, last_blk)];
-    bad = (unsigned)pg >= (unsigned)n_pages;
-    return c.pages + ((int64_t)(bad ? 0 : pg) * c.kv_heads + kvh) * (int64_t)c.record;
+  // the table entries of a step's four times 16 keys, read one step ahead
+  int pages[4];
+  auto look_up = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pages[i] = table[min((64 * t + 16 * i) >> c.log2p, last_blk)];
   };
   const CodeConsts cc = code_consts();
   const int tt = wave >> 1, sub = wave & 1;  // the wave's decode passes: 32 keys, K result / V piece
 
-  // the codes of step t into registers; parameters of keys that do not exist become zero
+  // the codes of step t into registers
   // (bit i of what it returns: the 16 keys i of the step lie on no page)
   auto fetch = [&](R& r, int t) -> int {
     const uint8_t* rec[4];
     int bad[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) rec[i] = page_of(64 * t + 16 * i, bad[i]);
+    for (int i = 0; i < 4; ++i) {
+      bad[i] = (unsigned)pages[i] >= (unsigned)n_pages;
+      rec[i] = c.pages + ((int64_t)(bad[i] ? 0 : pages[i]) * c.kv_heads + kvh) * (int64_t)c.record;
+    }
+    look_up(t + 1);
     const int key32 = 64 * t + 32 * tt;
     {
       const int half = lr >> 3, in = 8 * (lr >> 2) + 4 * sub + (lr & 3);  // key of the tile of 32
@@ -777,30 +785,23 @@ void k_kv4_attention_wide(Kv4Cache c, Kv4Query a, Partials part) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) r.k[e] = w[e];
       }
-      const bool ok = key32 + in < len && !(half ? (tt ? bad[3] : bad[1]) : (tt ? bad[2] : bad[0]));
+      r.k_ok = key32 + in < len && !(half ? (tt ? bad[3] : bad[1]) : (tt ? bad[2] : bad[0]));
 #pragma unroll
-      for (int g = 0; g < X::G; ++g) {
-        const uint32_t w = *(const uint32_t*)(p + P * D + 4 * (P * g + off));
-        r.kz[g] = ok ? w : 0u;
-      }
+      for (int g = 0; g < X::G; ++g) r.kz[g] = *(const uint32_t*)(p + P * D + 4 * (P * g + off));
     }
     if (sub < X::H) {
       const int half = q >> 1;
       const uint8_t* p = half ? (tt ? rec[3] : rec[1]) : (tt ? rec[2] : rec[0]);
       const int off = (key32 + 8 * q) & (P - 1);
       r.v = *(const u32x4*)(p + P * (D / 2) + off * (D / 2) + 256 * sub + 16 * lr);
-      const int there = (half ? (tt ? bad[3] : bad[1]) : (tt ? bad[2] : bad[0])) ? 0 : len - key32 - 8 * q;
+      r.v_there = (half ? (tt ? bad[3] : bad[1]) : (tt ? bad[2] : bad[0])) ? 0 : len - key32 - 8 * q;
 #pragma unroll
       for (int g = 0; g < R::GH; ++g) {
         // the groups of channels 64 sub .. 64 sub + 63
         const int gg = (64 * sub + 32 * g) / GS;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          u32x4 w = *(const u32x4*)(p + P * D + 4 * (P * (X::G + gg) + off) + 16 * i);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = 4 * i + e < there ? w[e] : 0u;
-          r.vz[g][i] = w;
-        }
+        for (int i = 0; i < 2; ++i)
+          r.vz[g][i] = *(const u32x4*)(p + P * D + 4 * (P * (X::G + gg) + off) + 16 * i);
       }
     }
 #pragma unroll
@@ -810,8 +811,8 @@ void k_kv4_attention_wide(Kv4Cache c, Kv4Query a, Partials part) {
         const int i = lane >> 4;
         const uint8_t* p = i & 2 ? (i & 1 ? rec[3] : rec[2]) : (i & 1 ? rec[1] : rec[0]);
         const int dead = i & 2 ? (i & 1 ? bad[3] : bad[2]) : (i & 1 ? bad[1] : bad[0]);
-        const uint32_t w = *(const uint32_t*)(p + P * D + 4 * (P * pg + ((64 * t + lane) & (P - 1))));
-        r.par[k] = 64 * t + lane < len && !dead ? w : 0u;
+        r.par[k] = *(const uint32_t*)(p + P * D + 4 * (P * pg + ((64 * t + lane) & (P - 1))));
+        r.par_ok = 64 * t + lane < len && !dead;
       }
     }
     return bad[0] | bad[1] << 1 | bad[2] << 2 | bad[3] << 3;
@@ -823,10 +824,11 @@ void k_kv4_attention_wide(Kv4Cache c, Kv4Query a, Partials part) {
   auto plus16 = [&](uint32_t zz) -> uint32_t {
     return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, zz) + __builtin_bit_cast(half2v, kOffset));
   };
+  // parameters of keys that do not exist may hold anything: they become zero
   auto decode = [&](const R& r, uint8_t* buf) {
 #pragma unroll
     for (int w = 0; w < X::KW; ++w) {
-      const uint32_t par = r.kz[w / X::WPG];
+      const uint32_t par = r.k_ok ? r.kz[w / X::WPG] : 0u;
       const uint32_t z = plus16(__builtin_amdgcn_perm(par, par, 0x03020302u));
       const u32x4 o = {sub2(code_pair<0>(r.k[w], cc), z), sub2(code_pair<1>(r.k[w], cc), z),
                        sub2(code_pair<2>(r.k[w], cc), z), sub2(code_pair<3>(r.k[w], cc), z)};
@@ -838,7 +840,8 @@ void k_kv4_attention_wide(Kv4Cache c, Kv4Query a, Partials part) {
       for (int g = 0; g < R::GH; ++g)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t pa = r.vz[g][i >> 1][2 * (i & 1)], pb = r.vz[g][i >> 1][2 * (i & 1) + 1];
+          const uint32_t pa = 2 * i < r.v_there ? r.vz[g][i >> 1][2 * (i & 1)] : 0u;
+          const uint32_t pb = 2 * i + 1 < r.v_there ? r.vz[g][i >> 1][2 * (i & 1) + 1] : 0u;
           z[g][i] = plus16(__builtin_amdgcn_perm(pb, pa, 0x07060302u));
         }
 #pragma unroll
@@ -857,7 +860,7 @@ void k_kv4_attention_wide(Kv4Cache c, Kv4Query a, Partials part) {
 #pragma unroll
     for (int k = 0; k < R::PW; ++k) {
       const int pg = wave + kWaves * k;
-      if (pg < 2 * X::G) *(uint32_t*)(buf + W::K_BYTES + W::V_BYTES + 256 * pg + 4 * lane) = r.par[k];
+      if (pg < 2 * X::G) *(uint32_t*)(buf + W::K_BYTES + W::V_BYTES + 256 * pg + 4 * lane) = r.par_ok ? r.par[k] : 0u;
     }
   };
 
@@ -867,49 +870,46 @@ void k_kv4_attention_wide(Kv4Cache c, Kv4Query a, Partials part) {
     if (key0 > last || key0 + 63 < first - lo_off || last < 0) return;  // nothing for this wave
     const bool whole = !dead && key0 + 64 <= len && key0 + 63 <= first && key0 >= last - lo_off;
     const uint8_t* par = buf + W::K_BYTES + W::V_BYTES + 32 * q;
-    u32x4 vp[2][X::G][2];
-    u16x2 tp = {0, 0};
+    // scores of all column tiles: an operand read once feeds NC products, and the reads of a
+    // result's operands go out before the products of the one before it
+    float s[NC][16];
+    half8v kk[2][X::KW];
+    auto read_k = [&](int hj, half8v (&o)[X::KW]) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+      for (int u = 0; u < X::KW; ++u) o[u] = *(const half8v*)(buf + (hj * X::KW + u) * 1024 + 16 * lane);
+    };
+    read_k(0, kk[0]);
+#pragma unroll
+    for (int hj = 0; hj < 4; ++hj) {
+      const int h = hj >> 1, j = hj & 1;
+      if (hj < 3) read_k(hj + 1, kk[(hj + 1) & 1]);
+      u32x4 kp[X::G];
+#pragma unroll
+      for (int g = 0; g < X::G; ++g) kp[g] = *(const u32x4*)(par + 256 * g + 128 * h + 16 * j);
+      __builtin_amdgcn_sched_barrier(0);
+      f32x4 acc[NC][X::G];
 #pragma unroll
       for (int g = 0; g < X::G; ++g)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          vp[h][g][i] = *(const u32x4*)(par + 256 * (X::G + g) + 128 * h + 16 * i);
+        for (int n = 0; n < NC; ++n) acc[n][g] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t w = vp[h][g][i][e];
-            tp = __builtin_elementwise_max(tp, __builtin_bit_cast(u16x2, w));
-          }
-        }
-    const uint32_t top = tp[0];
-    // scores of all column tiles: an operand read once feeds NC products
-    float s[NC][16];
+      for (int u = 0; u < X::WPG; ++u)
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int g = 0; g < X::G; ++g) {
-          f32x4 acc[NC];
-#pragma unroll
-          for (int n = 0; n < NC; ++n) acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int u = 0; u < X::WPG; ++u) {
-            const half8v kk = *(const half8v*)(buf + ((h * 2 + j) * X::KW + g * X::WPG + u) * 1024 + 16 * lane);
-#pragma unroll
-            for (int n = 0; n < NC; ++n)
-              acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kk, col[n].q[g * X::WPG + u], acc[n], 0, 0, 0);
-          }
-          const u32x4 kp = *(const u32x4*)(par + 256 * g + 128 * h + 16 * j);
+        for (int g = 0; g < X::G; ++g)
 #pragma unroll
           for (int n = 0; n < NC; ++n)
+            acc[n][g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kk[hj & 1][g * X::WPG + u],
+                                                               col[n].q[g * X::WPG + u], acc[n][g], 0, 0, 0);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int x = 8 * h + 4 * j + e;
-              s[n][x] = fmaf(lo16(kp[e]), acc[n][e], g == 0 ? 0.0f : s[n][x]);
-            }
-        }
+      for (int g = 0; g < X::G; ++g)
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int x = 8 * h + 4 * j + e;
+            s[n][x] = fmaf(lo16(kp[g][e]), acc[n][g][e], g == 0 ? 0.0f : s[n][x]);
+          }
+    }
     uint32_t seen[NC];
     if (!whole) {
 #pragma unroll
@@ -926,6 +926,22 @@ void k_kv4_attention_wide(Kv4Cache c, Kv4Query a, Partials part) {
         }
       }
     }
+    u32x4 vp[2][X::G][2];
+    u16x2 tp = {0, 0};
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int g = 0; g < X::G; ++g)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          vp[h][g][i] = *(const u32x4*)(par + 256 * (X::G + g) + 128 * h + 16 * i);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t w = vp[h][g][i][e];
+            tp = __builtin_elementwise_max(tp, __builtin_bit_cast(u16x2, w));
+          }
+        }
+    const uint32_t top = tp[0];
     float mx[NC];
     bool up = top >= ws.limit;
 #pragma unroll
@@ -990,20 +1006,31 @@ void k_kv4_attention_wide(Kv4Cache c, Kv4Query a, Partials part) {
             for (int g = 0; g < X::G; ++g) w[n][h][g][i] &= bits;
           }
     }
+    constexpr int PV = 2 * X::N / 4;  // groups of four value operands, each read a group ahead
+    half8v vv[2][4];
+    auto read_v = [&](int g, half8v (&o)[4]) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+      for (int i = 0; i < 4; ++i) o[i] = *(const half8v*)(buf + W::K_BYTES + (4 * g + i) * 1024 + 16 * lane);
+    };
+    read_v(0, vv[0]);
 #pragma unroll
-      for (int i = 0; i < X::N; ++i) {
-        const half8v vv = *(const half8v*)(buf + W::K_BYTES + (h * X::N + i) * 1024 + 16 * lane);
+    for (int g = 0; g < PV; ++g) {
+      if (g + 1 < PV) read_v(g + 1, vv[(g + 1) & 1]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int h = (4 * g + i) / X::N, o = (4 * g + i) % X::N;
 #pragma unroll
         for (int n = 0; n < NC; ++n)
-          col[n].o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-              vv, __builtin_bit_cast(half8v, w[n][h][i / (GS / 16)]), col[n].o[i], 0, 0, 0);
+          col[n].o[o] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+              vv[g & 1][i], __builtin_bit_cast(half8v, w[n][h][o / (GS / 16)]), col[n].o[o], 0, 0, 0);
       }
+    }
   };
 
   if (t_lo < t_hi) {
     R r;
+    look_up(t_lo);
     int dead0 = fetch(r, t_lo), dead1 = 0;
     decode(r, buf0);
     __syncthreads();
@@ -1144,7 +1171,7 @@ Kv4Plan kv4_plan(int64_t n_seqs, int heads, int kv_heads, int dim, int group, in
   Kv4Plan p;
   const int64_t cols = max_q * (heads / kv_heads);
   p.wide = cols > 16;
-  const int64_t per = p.wide ? Wide<128, 128>::COLS : 16;
+  const int64_t per = p.wide ? 16 * wide_tiles(dim, group) * kWaves : 16;
   p.tiles = (int)((cols + per - 1) / per);
   const int64_t blocks = n_seqs * kv_heads * p.tiles;
   // four blocks a compute unit, at least 256 keys a split
