@@ -43,8 +43,10 @@ struct Tile {
   __device__ static int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 };
 
+// splits > 1: block z sums its share of K and stores the int32 tile to part [splits][T][M].
 template <class S, bool BF16>
-__global__ __launch_bounds__(S::THREADS) void k_int8_tiles(Int8Args a, int tiles_t, int tiles_m) {
+__global__ __launch_bounds__(S::THREADS) void k_int8_tiles(Int8Args a, int tiles_t, int tiles_m,
+                                                           int splits, int* __restrict__ part) {
   __shared__ __attribute__((aligned(1024))) uint8_t sm0[S::BYTES];
   __shared__ __attribute__((aligned(1024))) uint8_t sm1[S::BYTES];
   const int tid = threadIdx.x;
@@ -79,11 +81,15 @@ __global__ __launch_bounds__(S::THREADS) void k_int8_tiles(Int8Args a, int tiles
   const int ce = (lane & 7) ^ S::swz(dr), co = (lane & 7) ^ S::swz(dr + 8);
   const unsigned row_x = wave * S::DMA_X * 8 + dr, row_w = wave * S::DMA_W * 8 + dr;
   const unsigned ldsb[2] = {lds_address(sm0), lds_address(sm1)};
-  const int nk = (a.K + 2 * S::BK - 1) / (2 * S::BK) * 2;  // whole pairs of stages
+  // whole pairs of stages of this split: stages kt0 .. kt0 + nk - 1
+  const int pairs = (a.K + 2 * S::BK - 1) / (2 * S::BK), z = blockIdx.y;
+  const int kt0 = (int)((int64_t)pairs * z / splits) * 2;
+  const int nk = (int)((int64_t)pairs * (z + 1) / splits) * 2 - kt0;
 
   auto dma = [&](int st, int kt) {
-    const int k0 = kt * S::BK;
-    const bool oke = k0 + ce * 16 < a.K, oko = k0 + co * 16 < a.K;
+    const int k0 = (kt0 + kt) * S::BK;
+    const bool in = kt < nk;
+    const bool oke = in && k0 + ce * 16 < a.K, oko = in && k0 + co * 16 < a.K;
 #pragma unroll
     for (int j = 0; j < S::DMA_X; ++j) {
       const bool odd = (wave * S::DMA_X + j) & 1;
@@ -163,6 +169,20 @@ __global__ __launch_bounds__(S::THREADS) void k_int8_tiles(Int8Args a, int tiles
     __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<0>::value);  // no LDS write may outlive the block
   }
 
+  if (splits > 1) {
+    int* dst = part + (int64_t)z * a.T * a.M;
+#pragma unroll
+    for (int j = 0; j < S::MI; ++j)
+#pragma unroll
+      for (int i = 0; i < S::TI; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int m = m0 + (wm * S::MI + j) * 32 + (lane & 31);
+          const int t = t0 + (wt * S::TI + i) * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
+          if (t < a.T && m < a.M) dst[(int64_t)t * a.M + m] = acc[i][j][e];
+        }
+    return;
+  }
   const uint16_t* bias = (const uint16_t*)a.bias;
   uint16_t* y = (uint16_t*)a.y;
 #pragma unroll
@@ -186,23 +206,299 @@ __global__ __launch_bounds__(S::THREADS) void k_int8_tiles(Int8Args a, int tiles
   }
 }
 
+// The sum of the splits' int32 tiles (exact, so their order does not matter), scaled.  Four
+// outputs a thread where M allows it.
+template <bool BF16, int V>
+__global__ __launch_bounds__(256) void k_int8_finish(Int8Args a, int splits,
+                                                     const int* __restrict__ part) {
+  typedef int ivec __attribute__((ext_vector_type(V)));
+  const int64_t n = (int64_t)a.T * a.M;
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;
+  if (i >= n) return;
+  const int t = (int)(i / a.M), m = (int)(i - (int64_t)t * a.M);
+  ivec s = *(const ivec*)(part + i);
+  for (int z = 1; z < splits; ++z) s += *(const ivec*)(part + z * n + i);
+  const float xs = a.xstep[t];
+  const uint16_t* bias = (const uint16_t*)a.bias;
+  uint16_t* y = (uint16_t*)a.y + (int64_t)t * a.ldy + m;
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    float v = scaled(s[e], xs, a.wstep[m + e]);
+    if (bias) v = v + from16<BF16>(bias[m + e]);
+    y[e] = to16<BF16>(v);
+  }
+}
+
+// ---- few tokens --------------------------------------------------------------------------
+//
+// Up to 16 NT tokens the product is bound by reading the weights once.  A block takes 16 RT
+// outputs and all tokens; its eight waves take 256-byte pieces of K in turn.  The weights go
+// from memory to the operand registers of v_mfma_i32_16x16x64_i8 directly (lane l: 16 bytes of
+// row l mod 16 at 16 (l div 16); four instructions cover 256 contiguous bytes of a row), the
+// next piece's ahead of the products of this one; the tokens' operands come from L2.  The
+// waves' int32 sums are added through LDS.  Result element e of lane l is output
+// 4 (l div 16) + e, token l mod 16.
+//
+// FUSED (one to four tokens, NT = 1): the block first quantises the tokens into LDS, with the
+// first weights already on their way; every block repeats that (a few thousand values from L2)
+// in place of a launch before this one.
+constexpr int kFewWaves = 8;
+constexpr int kFusedTokens = 4;
+constexpr int kFusedLds = 65536;  // bytes of codes
+
+struct FewArgs {
+  Int8Args g;
+  const void* x16;  // FUSED: activations, their stride, scales and columns
+  int64_t ldx16;
+  const float* s;
+  int cols;
+};
+
+inline __host__ __device__ int fused_stride(int K) { return K + 64; }  // tokens on different banks
+
+template <int RT, int NT, bool FUSED, bool BF16, bool VEC>
+__global__ __launch_bounds__(64 * kFewWaves) void k_int8_few(FewArgs f) {
+  const Int8Args& a = f.g;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 15, q = lane >> 4;
+  const int m0 = blockIdx.x * 16 * RT;
+  const int nch = (a.K + 255) >> 8;
+
+  // rows past the last repeat it and are dropped; pieces past K read the row's start and count 0
+  const int8_t* wrow[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) wrow[r] = a.w + (int64_t)min(m0 + 16 * r + lr, a.M - 1) * a.ldw;
+  auto load_w = [&](int32x4 (&o)[RT][4], int ch) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int k = ch * 256 + u * 64 + 16 * q;
+      const bool in = k < a.K;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) o[r][u] = *(const int32x4*)(wrow[r] + (in ? k : 0));
+    }
+  };
+  int32x4 w0[RT][4], w1[RT][4];
+  if (wave < nch) load_w(w0, wave);
+
+  __shared__ float steps[kFusedTokens];
+  if constexpr (FUSED) {
+    __shared__ uint32_t red[kFusedTokens][kFewWaves];
+    const int n8 = a.K >> 3;  // 8-column chunks (K whole 16-byte pieces)
+    const int stride = fused_stride(a.K);
+    for (int t = 0; t < a.T; ++t) {
+      const uint16_t* row = (const uint16_t*)f.x16 + t * f.ldx16;
+      uint32_t top = 0;
+      float v[8];
+      for (int ch = tid; ch < n8; ch += 64 * kFewWaves) {
+        load_row8<BF16, VEC>(row, f.s, f.s ? kFoldDivide : kFoldNone, 8 * ch, f.cols, v);
+        top = max_abs8(v, top);
+      }
+#pragma unroll
+      for (int off = 32; off > 0; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off));
+      if (lane == 0) red[t][wave] = top;
+    }
+    __syncthreads();
+    for (int t = 0; t < a.T; ++t) {
+      const uint16_t* row = (const uint16_t*)f.x16 + t * f.ldx16;
+      uint32_t top = red[t][0];
+#pragma unroll
+      for (int w = 1; w < kFewWaves; ++w) top = max(top, red[t][w]);
+      const RowStep st = row_step(top);
+      if (tid == 0) steps[t] = st.step;
+      float v[8];
+      for (int ch = tid; ch < n8; ch += 64 * kFewWaves) {
+        load_row8<BF16, VEC>(row, f.s, f.s ? kFoldDivide : kFoldNone, 8 * ch, f.cols, v);
+        *(uint2*)(lds + t * stride + 8 * ch) = row_codes8(v, st);
+      }
+    }
+    __syncthreads();
+  }
+
+  const int8_t* xrow[NT];
+  int toks[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    toks[n] = min(16 * n + lr, a.T - 1);
+    xrow[n] = FUSED ? nullptr : a.x + (int64_t)toks[n] * a.ldx;
+  }
+  int32x4 acc[RT][NT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[r][n] = int32x4{0, 0, 0, 0};
+  auto piece = [&](int32x4 (&w)[RT][4], int ch) {
+    int32x4 x[NT][4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int k = ch * 256 + u * 64 + 16 * q;
+      const bool in = k < a.K;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if constexpr (FUSED) x[n][u] = *(const int32x4*)(lds + toks[n] * fused_stride(a.K) + (in ? k : 0));
+        else x[n][u] = *(const int32x4*)(xrow[n] + (in ? k : 0));
+        if (!in) x[n][u] = int32x4{0, 0, 0, 0};
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          acc[r][n] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[r][u], x[n][u], acc[r][n], 0, 0, 0);
+  };
+  for (int ch = wave; ch < nch; ch += 2 * kFewWaves) {
+    if (ch + kFewWaves < nch) load_w(w1, ch + kFewWaves);
+    piece(w0, ch);
+    if (ch + kFewWaves >= nch) break;
+    if (ch + 2 * kFewWaves < nch) load_w(w0, ch + 2 * kFewWaves);
+    piece(w1, ch + kFewWaves);
+  }
+
+  // the waves' sums, then one (tile, lane) a thread
+  constexpr int kTiles = RT * NT;
+  __shared__ int32x4 sum[kFewWaves][kTiles][64];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) sum[wave][r * NT + n][lane] = acc[r][n];
+  __syncthreads();
+  const uint16_t* bias = (const uint16_t*)a.bias;
+  for (int i = tid; i < kTiles * 64; i += 64 * kFewWaves) {
+    const int tile = i >> 6, l = i & 63;
+    int32x4 v = sum[0][tile][l];
+#pragma unroll
+    for (int w = 1; w < kFewWaves; ++w) v += sum[w][tile][l];
+    const int t = 16 * (tile % NT) + (l & 15), m = m0 + 16 * (tile / NT) + 4 * (l >> 4);
+    if (t >= a.T) continue;
+    const float xs = FUSED ? steps[t] : a.xstep[t];
+    uint16_t o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (m + e < a.M) {
+        float y = scaled(v[e], xs, a.wstep[m + e]);
+        if (bias) y = y + from16<BF16>(bias[m + e]);
+        o[e] = to16<BF16>(y);
+      }
+    }
+    uint16_t* y = (uint16_t*)a.y + (int64_t)t * a.ldy + m;
+    if (m + 4 <= a.M && a.ldy % 4 == 0 && ((uintptr_t)a.y & 7) == 0) {
+      uint2 p;
+      p.x = o[0] | ((uint32_t)o[1] << 16);
+      p.y = o[2] | ((uint32_t)o[3] << 16);
+      *(uint2*)y = p;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (m + e < a.M) y[e] = o[e];
+    }
+  }
+}
+
 template <class S, bool BF16>
-hipError_t launch_tiles(const Int8Args& a, hipStream_t stream) {
+hipError_t launch_tiles(const Int8Args& a, int splits, int* part, hipStream_t stream) {
   const int tt = (a.T + S::BT - 1) / S::BT, tm = (a.M + S::BM - 1) / S::BM;
   if ((long long)tt * tm > 0x7fffffffLL) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((k_int8_tiles<S, BF16>), dim3((unsigned)(tt * tm)), dim3(S::THREADS), 0,
-                     stream, a, tt, tm);
+  hipLaunchKernelGGL((k_int8_tiles<S, BF16>), dim3((unsigned)(tt * tm), (unsigned)splits),
+                     dim3(S::THREADS), 0, stream, a, tt, tm, splits, part);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || splits <= 1) return e;
+  const int64_t n = (int64_t)a.T * a.M;
+  if (a.M % 4 == 0)
+    hipLaunchKernelGGL((k_int8_finish<BF16, 4>), dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0,
+                       stream, a, splits, part);
+  else
+    hipLaunchKernelGGL((k_int8_finish<BF16, 1>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0,
+                       stream, a, splits, part);
   return hipGetLastError();
+}
+
+template <int RT, int NT, bool FUSED, bool VEC>
+hipError_t launch_few(const FewArgs& f, hipStream_t stream) {
+  const dim3 grid((unsigned)((f.g.M + 16 * RT - 1) / (16 * RT))), block(64 * kFewWaves);
+  const size_t lds = FUSED ? (size_t)f.g.T * fused_stride(f.g.K) : 0;
+  if (f.g.bf16)
+    hipLaunchKernelGGL((k_int8_few<RT, NT, FUSED, true, VEC>), grid, block, lds, stream, f);
+  else
+    hipLaunchKernelGGL((k_int8_few<RT, NT, FUSED, false, VEC>), grid, block, lds, stream, f);
+  return hipGetLastError();
+}
+
+// How one product runs, by its sizes.
+struct Plan {
+  int few;     // 16-token tiles of the few-token form, or 0
+  int splits;  // of K, tiled form
+  bool large;  // 256 x 256 tiles
+};
+
+#ifndef I8FEW
+#define I8FEW 64
+#endif
+Plan plan_of(int64_t T, int64_t M, int64_t K) {
+  Plan p{0, 1, false};
+  if (T <= I8FEW) {
+    p.few = T <= 16 ? 1 : T <= 32 ? 2 : 4;
+    return p;
+  }
+  const int64_t large = ((T + 255) / 256) * ((M + 255) / 256);
+  if (large >= 256) {
+    p.large = true;
+    return p;
+  }
+  const int64_t small = ((T + 127) / 128) * ((M + 127) / 128);
+  int64_t s = 512 / small;              // two blocks a compute unit
+  const int64_t most = K / 1024;        // at least eight stages a split
+  if (s > most) s = most;
+  if (s > 8) s = 8;
+  p.splits = (int)(s < 1 ? 1 : s);
+  return p;
 }
 
 }  // namespace
 
-size_t int8_matmul_workspace(int64_t, int64_t, int64_t) { return 0; }
+size_t int8_matmul_workspace(int64_t T, int64_t M, int64_t K) {
+  const Plan p = plan_of(T, M, K);
+  return p.splits > 1 ? (size_t)p.splits * T * M * sizeof(int) : 0;
+}
 
-hipError_t launch_int8_matmul(const Int8Args& a, void*, hipStream_t stream) {
+hipError_t launch_int8_matmul(const Int8Args& a, void* workspace, hipStream_t stream) {
   if (a.T <= 0 || a.M <= 0) return hipSuccess;
-  using S = Tile<128, 128, 2, 2>;
-  return a.bf16 ? launch_tiles<S, true>(a, stream) : launch_tiles<S, false>(a, stream);
+  const Plan p = plan_of(a.T, a.M, a.K);
+  if (p.few) {
+    const FewArgs f{a, nullptr, 0, nullptr, 0};
+    // 32 outputs a block where that leaves a block a compute unit
+    const bool two = a.M >= 32 * 256;
+    switch (p.few * 2 + two) {
+      case 2: return launch_few<1, 1, false, false>(f, stream);
+      case 3: return launch_few<2, 1, false, false>(f, stream);
+      case 4: return launch_few<1, 2, false, false>(f, stream);
+      case 5: return launch_few<2, 2, false, false>(f, stream);
+      case 8: return launch_few<1, 4, false, false>(f, stream);
+      default: return launch_few<2, 4, false, false>(f, stream);
+    }
+  }
+  int* part = (int*)workspace;
+  if (p.large)
+    return a.bf16 ? launch_tiles<Tile<256, 256, 2, 8>, true>(a, 1, nullptr, stream)
+                  : launch_tiles<Tile<256, 256, 2, 8>, false>(a, 1, nullptr, stream);
+  return a.bf16 ? launch_tiles<Tile<128, 128, 2, 2>, true>(a, p.splits, part, stream)
+                : launch_tiles<Tile<128, 128, 2, 2>, false>(a, p.splits, part, stream);
+}
+
+bool int8_linear_fused(int64_t T, int64_t K) {
+  return T <= kFusedTokens && T * (K + 64) <= kFusedLds;
+}
+
+hipError_t launch_int8_linear_fused(const Int8Args& a, const void* x, int64_t ldx, const float* s,
+                                    int cols, hipStream_t stream) {
+  if (a.T <= 0 || a.M <= 0) return hipSuccess;
+  const FewArgs f{a, x, ldx, s, cols};
+  const bool vec = row_vector_loads(x, ldx, s);
+  const bool two = a.M >= 32 * 256;
+  if (vec) return two ? launch_few<2, 1, true, true>(f, stream) : launch_few<1, 1, true, true>(f, stream);
+  return two ? launch_few<2, 1, true, false>(f, stream) : launch_few<1, 1, true, false>(f, stream);
 }
 
 }  // namespace awq

@@ -102,6 +102,7 @@ int awq_int8_matmul(const int8_t* xq, int64_t ldx, const float* xstep, int64_t n
 
 size_t awq_int8_linear_workspace_bytes(int64_t T, int64_t M, int64_t K) {
   if (T <= 0 || M <= 0 || K < 0 || T > kMaxRows || M > kMaxRows || K > awq::kInt8MaxK) return 0;
+  if (awq::int8_linear_fused(T, round16(K))) return 0;
   return round_up((size_t)T * (size_t)round16(K), kAlign) + round_up((size_t)T * 4, kAlign) +
          awq_int8_matmul_workspace_bytes(T, M, K);
 }
@@ -124,6 +125,11 @@ int awq_int8_linear(const void* x, int64_t ldx, const float* s, int64_t n_tokens
   if (T == 0 || M == 0) return AWQ_OK;
   if ((st = device_ptrs({x, s, wq, wstep, bias, y, need ? workspace : nullptr}))) return st;
   clear_pending_error();
+  if (awq::int8_linear_fused(T, round16(K))) {
+    const awq::Int8Args a{nullptr, 0, nullptr, wq, ldw, wstep, bias, y, ldy,
+                          (int)T, (int)M, (int)round16(K), dtype == AWQ_BF16};
+    return hip_status(awq::launch_int8_linear_fused(a, x, ldx, s, (int)K, (hipStream_t)stream));
+  }
   char* ws = (char*)workspace;
   int8_t* xq = (int8_t*)ws;
   ws += round_up((size_t)T * (size_t)round16(K), kAlign);
