@@ -29,9 +29,9 @@ __device__ __forceinline__ float scaled(int acc, float xs, float ws) {
   return (float)acc * xs * ws;
 }
 
-template <int BT_, int BM_, int WT_, int WM_>
+template <int BT_, int BM_, int WT_, int WM_, int NS_>
 struct Tile {
-  static constexpr int BT = BT_, BM = BM_, WT = WT_, WM = WM_;
+  static constexpr int BT = BT_, BM = BM_, WT = WT_, WM = WM_, NS = NS_;
   static constexpr int BK = 128;  // bytes of K a stage
   static constexpr int WAVES = WT * WM, THREADS = 64 * WAVES;
   static constexpr int TI = BT / WT / 32, MI = BM / WM / 32;
@@ -47,8 +47,8 @@ struct Tile {
 template <class S, bool BF16>
 __global__ __launch_bounds__(S::THREADS) void k_int8_tiles(Int8Args a, int tiles_t, int tiles_m,
                                                            int splits, int* __restrict__ part) {
-  __shared__ __attribute__((aligned(1024))) uint8_t sm0[S::BYTES];
-  __shared__ __attribute__((aligned(1024))) uint8_t sm1[S::BYTES];
+  constexpr int NS = S::NS;
+  __shared__ __attribute__((aligned(1024))) uint8_t sm[NS * S::BYTES];
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lane = tid & 63;
@@ -80,15 +80,16 @@ __global__ __launch_bounds__(S::THREADS) void k_int8_tiles(Int8Args a, int tiles
   const int dr = lane >> 3;
   const int ce = (lane & 7) ^ S::swz(dr), co = (lane & 7) ^ S::swz(dr + 8);
   const unsigned row_x = wave * S::DMA_X * 8 + dr, row_w = wave * S::DMA_W * 8 + dr;
-  const unsigned ldsb[2] = {lds_address(sm0), lds_address(sm1)};
-  // whole pairs of stages of this split: stages kt0 .. kt0 + nk - 1
-  const int pairs = (a.K + 2 * S::BK - 1) / (2 * S::BK), z = blockIdx.y;
-  const int kt0 = (int)((int64_t)pairs * z / splits) * 2;
-  const int nk = (int)((int64_t)pairs * (z + 1) / splits) * 2 - kt0;
+  const unsigned ldsb = lds_address(sm);
+  // 128-byte steps of this split: kt0 .. kt1 - 1, walked in whole turns of the ring
+  const int steps = (a.K + S::BK - 1) / S::BK, z = blockIdx.y;
+  const int kt0 = (int)((int64_t)steps * z / splits);
+  const int n_steps = (int)((int64_t)steps * (z + 1) / splits) - kt0;
+  const int nk = (n_steps + NS - 1) / NS * NS;
 
   auto dma = [&](int st, int kt) {
     const int k0 = (kt0 + kt) * S::BK;
-    const bool in = kt < nk;
+    const bool in = kt < n_steps;
     const bool oke = in && k0 + ce * 16 < a.K, oko = in && k0 + co * 16 < a.K;
 #pragma unroll
     for (int j = 0; j < S::DMA_X; ++j) {
@@ -96,7 +97,7 @@ __global__ __launch_bounds__(S::THREADS) void k_int8_tiles(Int8Args a, int tiles
       const unsigned r = row_x + 8 * j;
       const unsigned v = (odd ? oko : oke) && r < (unsigned)rows_x
                              ? r * ldx + (odd ? co : ce) * 16 : kOut;
-      lds_dma16(rx, ldsb[st] + (wave * S::DMA_X + j) * 1024u, v, k0);
+      lds_dma16(rx, ldsb + st * S::BYTES + (wave * S::DMA_X + j) * 1024u, v, k0);
     }
 #pragma unroll
     for (int j = 0; j < S::DMA_W; ++j) {
@@ -104,7 +105,7 @@ __global__ __launch_bounds__(S::THREADS) void k_int8_tiles(Int8Args a, int tiles
       const unsigned r = row_w + 8 * j;
       const unsigned v = (odd ? oko : oke) && r < (unsigned)rows_w
                              ? r * ldw + (odd ? co : ce) * 16 : kOut;
-      lds_dma16(rw, ldsb[st] + S::X_BYTES + (wave * S::DMA_W + j) * 1024u, v, k0);
+      lds_dma16(rw, ldsb + st * S::BYTES + S::X_BYTES + (wave * S::DMA_W + j) * 1024u, v, k0);
     }
   };
 
@@ -136,11 +137,14 @@ __global__ __launch_bounds__(S::THREADS) void k_int8_tiles(Int8Args a, int tiles
         acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.x[i], f.w[j], acc[i][j], 0, 0, 0);
   };
 
-  // Two stages in flight; a stage is refilled after the barrier that follows its last
-  // fragment read, and the DMAs past the end of K read zeros into a slot nobody uses, so the
-  // number in flight, hence the vmcnt to wait for, is constant.
+  // NS stages in flight; a stage is refilled after the barrier that follows its last fragment
+  // read, and the DMAs past the end of K read zeros into a slot nobody uses, so the number in
+  // flight, hence the vmcnt to wait for, is constant.
+  constexpr int PER = S::DMA_X + S::DMA_W;
   Frag f0, f1;
-  auto step = [&](const uint8_t* cur, const uint8_t* next, int st, int kt) {
+  auto step = [&](int st, int kt) {
+    const uint8_t* cur = sm + st * S::BYTES;
+    const uint8_t* next = sm + (st + 1) % NS * S::BYTES;
 #pragma unroll
     for (int ks = 0; ks + 2 < S::KSTEPS; ks += 2) {
       load(cur, ks + 1, f1);
@@ -150,21 +154,21 @@ __global__ __launch_bounds__(S::THREADS) void k_int8_tiles(Int8Args a, int tiles
     }
     load(cur, S::KSTEPS - 1, f1);
     mma(f0);
-    __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<0>::value);  // stage kt + 1 has landed
+    __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<(NS - 2) * PER>::value);  // stage kt + 1 has landed
     __builtin_amdgcn_s_barrier();
-    dma(st, kt + 2);
+    dma(st, kt + NS);
     load(next, 0, f0);
     mma(f1);
   };
   if (nk > 0) {
-    dma(0, 0);
-    dma(1, 1);
-    __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<S::DMA_X + S::DMA_W>::value);
+#pragma unroll
+    for (int st = 0; st < NS; ++st) dma(st, st);
+    __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<(NS - 1) * PER>::value);
     __builtin_amdgcn_s_barrier();
-    load(sm0, 0, f0);
-    for (int kt = 0; kt < nk; kt += 2) {
-      step(sm0, sm1, 0, kt);
-      step(sm1, sm0, 1, kt + 1);
+    load(sm, 0, f0);
+    for (int kt = 0; kt < nk; kt += NS) {
+#pragma unroll
+      for (int st = 0; st < NS; ++st) step(st, kt + st);
     }
     __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<0>::value);  // no LDS write may outlive the block
   }
@@ -231,32 +235,29 @@ __global__ __launch_bounds__(256) void k_int8_finish(Int8Args a, int splits,
 
 // ---- few tokens --------------------------------------------------------------------------
 //
-// Up to 16 NT tokens the product is bound by reading the weights once.  A block takes 16 RT
-// outputs and all tokens; its eight waves take 256-byte pieces of K in turn.  The weights go
+// Up to 16 tokens the product is bound by reading the weights once.  A block takes 16 RT outputs
+// and all tokens; its eight waves take 256-byte pieces of K in turn.  The weights go
 // from memory to the operand registers of v_mfma_i32_16x16x64_i8 directly (lane l: 16 bytes of
 // row l mod 16 at 16 (l div 16); four instructions cover 256 contiguous bytes of a row), the
 // next piece's ahead of the products of this one; the tokens' operands come from L2.  The
 // waves' int32 sums are added through LDS.  Result element e of lane l is output
 // 4 (l div 16) + e, token l mod 16.
 //
-// FUSED (one to four tokens, NT = 1): the block first quantises the tokens into LDS, with the
-// first weights already on their way; every block repeats that (a few thousand values from L2)
-// in place of a launch before this one.
+// FUSED (one token): the block first quantises the token into LDS, with the first weights
+// already on their way; every block repeats that (a few thousand values from L2) in place of a
+// launch before this one.
 constexpr int kFewWaves = 8;
-constexpr int kFusedTokens = 4;
-constexpr int kFusedLds = 65536;  // bytes of codes
+constexpr int kFusedChunks = 4;  // 8-column chunks of the token a thread keeps
+constexpr int kFusedMaxK = 8 * 64 * kFewWaves * kFusedChunks;
 
 struct FewArgs {
   Int8Args g;
-  const void* x16;  // FUSED: activations, their stride, scales and columns
-  int64_t ldx16;
+  const void* x16;  // FUSED: the token, its scales and columns
   const float* s;
   int cols;
 };
 
-inline __host__ __device__ int fused_stride(int K) { return K + 64; }  // tokens on different banks
-
-template <int RT, int NT, bool FUSED, bool BF16, bool VEC>
+template <int RT, bool FUSED, bool BF16, bool VEC>
 __global__ __launch_bounds__(64 * kFewWaves) void k_int8_few(FewArgs f) {
   const Int8Args& a = f.g;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -282,98 +283,87 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_int8_few(FewArgs f) {
   int32x4 w0[RT][4], w1[RT][4];
   if (wave < nch) load_w(w0, wave);
 
-  __shared__ float steps[kFusedTokens];
+  float fused_step = 0.0f;
   if constexpr (FUSED) {
-    __shared__ uint32_t red[kFusedTokens][kFewWaves];
+    __shared__ uint32_t red[kFewWaves];
     const int n8 = a.K >> 3;  // 8-column chunks (K whole 16-byte pieces)
-    const int stride = fused_stride(a.K);
-    for (int t = 0; t < a.T; ++t) {
-      const uint16_t* row = (const uint16_t*)f.x16 + t * f.ldx16;
-      uint32_t top = 0;
-      float v[8];
-      for (int ch = tid; ch < n8; ch += 64 * kFewWaves) {
-        load_row8<BF16, VEC>(row, f.s, f.s ? kFoldDivide : kFoldNone, 8 * ch, f.cols, v);
-        top = max_abs8(v, top);
-      }
+    float v[kFusedChunks][8];
+    uint32_t top = 0;
 #pragma unroll
-      for (int off = 32; off > 0; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off));
-      if (lane == 0) red[t][wave] = top;
+    for (int c = 0; c < kFusedChunks; ++c) {
+      const int ch = tid + c * 64 * kFewWaves;
+      if (ch < n8) {
+        load_row8<BF16, VEC>((const uint16_t*)f.x16, f.s, f.s ? kFoldDivide : kFoldNone, 8 * ch, f.cols, v[c]);
+        top = max_abs8(v[c], top);
+      }
     }
-    __syncthreads();
-    for (int t = 0; t < a.T; ++t) {
-      const uint16_t* row = (const uint16_t*)f.x16 + t * f.ldx16;
-      uint32_t top = red[t][0];
+    const RowStep st = row_step(block_max<kFewWaves>(top, red));
+    fused_step = st.step;
 #pragma unroll
-      for (int w = 1; w < kFewWaves; ++w) top = max(top, red[t][w]);
-      const RowStep st = row_step(top);
-      if (tid == 0) steps[t] = st.step;
-      float v[8];
-      for (int ch = tid; ch < n8; ch += 64 * kFewWaves) {
-        load_row8<BF16, VEC>(row, f.s, f.s ? kFoldDivide : kFoldNone, 8 * ch, f.cols, v);
-        *(uint2*)(lds + t * stride + 8 * ch) = row_codes8(v, st);
-      }
+    for (int c = 0; c < kFusedChunks; ++c) {
+      const int ch = tid + c * 64 * kFewWaves;
+      if (ch < n8) *(uint2*)(lds + 8 * ch) = row_codes8(v[c], st);
     }
     __syncthreads();
   }
 
-  const int8_t* xrow[NT];
-  int toks[NT];
+  // columns past the last token repeat it and are dropped
+  const int8_t* xrow = FUSED ? nullptr : a.x + (int64_t)min(lr, a.T - 1) * a.ldx;
+  int32x4 acc[RT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    toks[n] = min(16 * n + lr, a.T - 1);
-    xrow[n] = FUSED ? nullptr : a.x + (int64_t)toks[n] * a.ldx;
-  }
-  int32x4 acc[RT][NT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[r][n] = int32x4{0, 0, 0, 0};
-  auto piece = [&](int32x4 (&w)[RT][4], int ch) {
-    int32x4 x[NT][4];
+  for (int r = 0; r < RT; ++r) acc[r] = int32x4{0, 0, 0, 0};
+  auto load_x = [&](int32x4 (&x)[4], int ch) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int k = ch * 256 + u * 64 + 16 * q;
-      const bool in = k < a.K;
+      const int at = k < a.K ? k : 0;
+      if constexpr (FUSED) x[u] = *(const int32x4*)(lds + at);
+      else x[u] = *(const int32x4*)(xrow + at);
+    }
+  };
+  auto piece = [&](int32x4 (&w)[RT][4], int32x4 (&x)[4], int ch) {
+    if (ch == nch - 1) {  // pieces past K count nothing
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if constexpr (FUSED) x[n][u] = *(const int32x4*)(lds + toks[n] * fused_stride(a.K) + (in ? k : 0));
-        else x[n][u] = *(const int32x4*)(xrow[n] + (in ? k : 0));
-        if (!in) x[n][u] = int32x4{0, 0, 0, 0};
-      }
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+          if (ch * 256 + u * 64 + 16 * q >= a.K) w[r][u] = int32x4{0, 0, 0, 0};
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u)
 #pragma unroll
       for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-          acc[r][n] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[r][u], x[n][u], acc[r][n], 0, 0, 0);
+        acc[r] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[r][u], x[u], acc[r], 0, 0, 0);
   };
+  // a piece's tokens are asked for before the next piece's weights: loads return in order, so
+  // waiting for the tokens does not wait for those weights
   for (int ch = wave; ch < nch; ch += 2 * kFewWaves) {
+    int32x4 x[4];
+    load_x(x, ch);
     if (ch + kFewWaves < nch) load_w(w1, ch + kFewWaves);
-    piece(w0, ch);
+    __builtin_amdgcn_sched_barrier(0);
+    piece(w0, x, ch);
     if (ch + kFewWaves >= nch) break;
+    load_x(x, ch + kFewWaves);
     if (ch + 2 * kFewWaves < nch) load_w(w0, ch + 2 * kFewWaves);
-    piece(w1, ch + kFewWaves);
+    __builtin_amdgcn_sched_barrier(0);
+    piece(w1, x, ch + kFewWaves);
   }
 
   // the waves' sums, then one (tile, lane) a thread
-  constexpr int kTiles = RT * NT;
-  __shared__ int32x4 sum[kFewWaves][kTiles][64];
+  __shared__ int32x4 sum[kFewWaves][RT][64];
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) sum[wave][r * NT + n][lane] = acc[r][n];
+  for (int r = 0; r < RT; ++r) sum[wave][r][lane] = acc[r];
   __syncthreads();
   const uint16_t* bias = (const uint16_t*)a.bias;
-  for (int i = tid; i < kTiles * 64; i += 64 * kFewWaves) {
+  for (int i = tid; i < RT * 64; i += 64 * kFewWaves) {
     const int tile = i >> 6, l = i & 63;
     int32x4 v = sum[0][tile][l];
 #pragma unroll
     for (int w = 1; w < kFewWaves; ++w) v += sum[w][tile][l];
-    const int t = 16 * (tile % NT) + (l & 15), m = m0 + 16 * (tile / NT) + 4 * (l >> 4);
+    const int t = l & 15, m = m0 + 16 * tile + 4 * (l >> 4);
     if (t >= a.T) continue;
-    const float xs = FUSED ? steps[t] : a.xstep[t];
+    const float xs = FUSED ? fused_step : a.xstep[t];
     uint16_t o[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -415,45 +405,49 @@ hipError_t launch_tiles(const Int8Args& a, int splits, int* part, hipStream_t st
   return hipGetLastError();
 }
 
-template <int RT, int NT, bool FUSED, bool VEC>
+// 32 outputs a block where that still leaves two blocks a compute unit
+constexpr int kTwoRows = 32 * 512;
+
+template <int RT, bool FUSED, bool VEC>
 hipError_t launch_few(const FewArgs& f, hipStream_t stream) {
   const dim3 grid((unsigned)((f.g.M + 16 * RT - 1) / (16 * RT))), block(64 * kFewWaves);
-  const size_t lds = FUSED ? (size_t)f.g.T * fused_stride(f.g.K) : 0;
+  const size_t lds = FUSED ? (size_t)f.g.K : 0;
   if (f.g.bf16)
-    hipLaunchKernelGGL((k_int8_few<RT, NT, FUSED, true, VEC>), grid, block, lds, stream, f);
+    hipLaunchKernelGGL((k_int8_few<RT, FUSED, true, VEC>), grid, block, lds, stream, f);
   else
-    hipLaunchKernelGGL((k_int8_few<RT, NT, FUSED, false, VEC>), grid, block, lds, stream, f);
+    hipLaunchKernelGGL((k_int8_few<RT, FUSED, false, VEC>), grid, block, lds, stream, f);
   return hipGetLastError();
 }
 
 // How one product runs, by its sizes.
+enum { kFew, kTile32, kTile64, kTile128, kTile256 };
 struct Plan {
-  int few;     // 16-token tiles of the few-token form, or 0
-  int splits;  // of K, tiled form
-  bool large;  // 256 x 256 tiles
+  int form, splits;
 };
 
-#ifndef I8FEW
-#define I8FEW 64
-#endif
 Plan plan_of(int64_t T, int64_t M, int64_t K) {
-  Plan p{0, 1, false};
-  if (T <= I8FEW) {
-    p.few = T <= 16 ? 1 : T <= 32 ? 2 : 4;
-    return p;
-  }
-  const int64_t large = ((T + 255) / 256) * ((M + 255) / 256);
-  if (large >= 256) {
-    p.large = true;
-    return p;
-  }
-  const int64_t small = ((T + 127) / 128) * ((M + 127) / 128);
-  int64_t s = 512 / small;              // two blocks a compute unit
-  const int64_t most = K / 1024;        // at least eight stages a split
+  Plan p{kTile256, 1};
+  p.form = T <= 16 && M * K < (int64_t)1 << 27 ? kFew : T <= 32 ? kTile32 : T <= 128 ? kTile64 : kTile128;
+  if (T > 128 && ((T + 255) / 256) * ((M + 255) / 256) >= 256) p.form = kTile256;
+  if (p.form < kTile32 || p.form == kTile256) return p;
+  const int bt = p.form == kTile32 ? 32 : p.form == kTile64 ? 64 : 128;
+  const int64_t tiles = ((T + bt - 1) / bt) * ((M + 127) / 128);
+  int64_t s = 512 / tiles;          // two blocks a compute unit
+  const int64_t most = K / 1024;        // at least eight steps a split
   if (s > most) s = most;
   if (s > 8) s = 8;
   p.splits = (int)(s < 1 ? 1 : s);
   return p;
+}
+
+template <bool BF16>
+hipError_t launch_plan(const Int8Args& a, const Plan& p, int* part, hipStream_t stream) {
+  switch (p.form) {
+    case kTile32: return launch_tiles<Tile<32, 128, 1, 4, 4>, BF16>(a, p.splits, part, stream);
+    case kTile64: return launch_tiles<Tile<64, 128, 2, 2, 3>, BF16>(a, p.splits, part, stream);
+    case kTile128: return launch_tiles<Tile<128, 128, 2, 2, 2>, BF16>(a, p.splits, part, stream);
+    default: return launch_tiles<Tile<256, 256, 2, 8, 2>, BF16>(a, 1, nullptr, stream);
+  }
 }
 
 }  // namespace
@@ -466,39 +460,24 @@ size_t int8_matmul_workspace(int64_t T, int64_t M, int64_t K) {
 hipError_t launch_int8_matmul(const Int8Args& a, void* workspace, hipStream_t stream) {
   if (a.T <= 0 || a.M <= 0) return hipSuccess;
   const Plan p = plan_of(a.T, a.M, a.K);
-  if (p.few) {
-    const FewArgs f{a, nullptr, 0, nullptr, 0};
-    // 32 outputs a block where that leaves a block a compute unit
-    const bool two = a.M >= 32 * 256;
-    switch (p.few * 2 + two) {
-      case 2: return launch_few<1, 1, false, false>(f, stream);
-      case 3: return launch_few<2, 1, false, false>(f, stream);
-      case 4: return launch_few<1, 2, false, false>(f, stream);
-      case 5: return launch_few<2, 2, false, false>(f, stream);
-      case 8: return launch_few<1, 4, false, false>(f, stream);
-      default: return launch_few<2, 4, false, false>(f, stream);
-    }
+  if (p.form < kTile32) {
+    const FewArgs f{a, nullptr, nullptr, 0};
+    return a.M >= kTwoRows ? launch_few<2, false, false>(f, stream) : launch_few<1, false, false>(f, stream);
   }
-  int* part = (int*)workspace;
-  if (p.large)
-    return a.bf16 ? launch_tiles<Tile<256, 256, 2, 8>, true>(a, 1, nullptr, stream)
-                  : launch_tiles<Tile<256, 256, 2, 8>, false>(a, 1, nullptr, stream);
-  return a.bf16 ? launch_tiles<Tile<128, 128, 2, 2>, true>(a, p.splits, part, stream)
-                : launch_tiles<Tile<128, 128, 2, 2>, false>(a, p.splits, part, stream);
+  return a.bf16 ? launch_plan<true>(a, p, (int*)workspace, stream)
+                : launch_plan<false>(a, p, (int*)workspace, stream);
 }
 
-bool int8_linear_fused(int64_t T, int64_t K) {
-  return T <= kFusedTokens && T * (K + 64) <= kFusedLds;
-}
+bool int8_linear_fused(int64_t T, int64_t K) { return T == 1 && K <= kFusedMaxK; }
 
-hipError_t launch_int8_linear_fused(const Int8Args& a, const void* x, int64_t ldx, const float* s,
-                                    int cols, hipStream_t stream) {
+hipError_t launch_int8_linear_fused(const Int8Args& a, const void* x, const float* s, int cols,
+                                    hipStream_t stream) {
   if (a.T <= 0 || a.M <= 0) return hipSuccess;
-  const FewArgs f{a, x, ldx, s, cols};
-  const bool vec = row_vector_loads(x, ldx, s);
-  const bool two = a.M >= 32 * 256;
-  if (vec) return two ? launch_few<2, 1, true, true>(f, stream) : launch_few<1, 1, true, true>(f, stream);
-  return two ? launch_few<2, 1, true, false>(f, stream) : launch_few<1, 1, true, false>(f, stream);
+  const FewArgs f{a, x, s, cols};
+  const bool vec = row_vector_loads(x, 0, s);
+  const bool two = a.M >= kTwoRows;
+  if (vec) return two ? launch_few<2, true, true>(f, stream) : launch_few<1, true, true>(f, stream);
+  return two ? launch_few<2, true, false>(f, stream) : launch_few<1, true, false>(f, stream);
 }
 
 }  // namespace awq

@@ -4,8 +4,9 @@
 // with an fp16 step a group).
 //
 // A row (token, head) is D / 8 lanes of 8 consecutive channels, for keys and values alike; a
-// group's range is reduced across its g / 8 lanes.  Bound by reading the fp16 rows from HBM
-// (4 bytes in for 1 byte of codes out).
+// group's range is reduced across its g / 8 lanes.  Value codes change their order through LDS
+// (a word of the record holds four channels, 16 apart, of two tokens).  Bound by the 16-bit
+// rows on the HBM side (4 bytes for 1 byte of codes).
 #include <hip/hip_runtime.h>
 
 #include "int8_quant.h"
@@ -35,77 +36,144 @@ __device__ __forceinline__ uint32_t quantise_group(const float (&v)[8], bool zp,
   return w;
 }
 
+// Which rows a block works on: R = 2048 / D consecutive positions of one sequence, the first a
+// multiple of R, so that a block's value codes are whole 8-token blocks of the record.
+// Sequence s owns the R-row groups from starts[s] / R + 2 s on: that leaves it enough of them
+// wherever its first position lies, without a sum over the sequences before it.  The groups
+// after the last sequence's hold the rows that belong to none.
+template <int D>
+struct Rows {
+  static constexpr int R = 2048 / D;
+  int seq, pos0, t0;  // sequence (-1: none), position and row index of the block's first row
+  int first, end;     // rows of the sequence: first <= t < end
+};
+template <int D>
+__device__ __forceinline__ Rows<D> rows_of(const Kv4Cache& c, int blk, int n_tokens) {
+  constexpr int R = Rows<D>::R;
+  const auto* starts = (const __attribute__((address_space(4))) int32_t*)(uintptr_t)c.starts;
+  Rows<D> r;
+  const int n = c.n_seqs;
+  auto own = [&](int s) { return starts[s] / R + 2 * s; };
+  if (blk >= own(n)) {
+    r.seq = -1;
+    r.pos0 = 0;
+    r.t0 = starts[n] + (blk - own(n)) * R;
+    r.first = starts[n];
+    r.end = n_tokens;
+    return r;
+  }
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (own(mid) <= blk) lo = mid; else hi = mid - 1;
+  }
+  r.seq = lo;
+  r.first = starts[lo];
+  r.end = min(starts[lo + 1], n_tokens);
+  const int p = c.lens[lo] - (starts[lo + 1] - r.first);  // position of the first row
+  r.pos0 = (p & ~(R - 1)) + (blk - own(lo)) * R;
+  r.t0 = r.first + (r.pos0 - p);
+  return r;
+}
+
+// Where the 32-bit word of value codes w of a block's R positions lies in the record (the block
+// is whole 8-token blocks: words in the record's order), and its two tokens' rows.
+template <int D>
+__device__ __forceinline__ int value_word_row(int w) { return (w / D) * 8 + 2 * (w & 3); }
+
 template <bool BF16, int D, int GS>
 __global__ __launch_bounds__(256) void k_kv4_append(Kv4Cache c, const uint16_t* __restrict__ k,
                                                     int64_t kt, int64_t kh,
                                                     const uint16_t* __restrict__ v, int64_t vt,
-                                                    int64_t vh, int64_t n_rows) {
-  constexpr int LPR = D / 8, G = D / GS;
-  const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPR;
-  const int l = threadIdx.x % LPR;
-  if (row >= n_rows) return;  // whole rows: the lanes of a group leave together
-  const int64_t t = row / c.kv_heads;
-  const int head = (int)(row - t * c.kv_heads);
-  float x[2][8];
-  load_row8<BF16, true>(k + t * kt + head * kh, nullptr, kFoldNone, 8 * l, D, x[0]);
-  load_row8<BF16, true>(v + t * vt + head * vh, nullptr, kFoldNone, 8 * l, D, x[1]);
-  const int b = kv4_sequence(c, t);
-  if (b < 0) return;
-  const int pos = c.lens[b] - (c.starts[b + 1] - (int)t);
-  const int64_t at = kv4_record_at(c, b, pos, head);
-  if (at < 0) return;
-  uint8_t* rec = c.pages + at;
-  const int P = 1 << c.log2p, p = pos & (P - 1);
-  uint32_t kp, vp;
-  const uint32_t kw = quantise_group<GS / 8>(x[0], c.zero_point, kp);
-  const uint32_t vw = quantise_group<GS / 8>(x[1], c.zero_point, vp);
-  // K: the lane's 8 channels are one word
-  const int j = 8 * l / GS, ing = 8 * l % GS;
-  const int q = ing / (GS / 4), u = ing % (GS / 4) / 8;
-  *(uint32_t*)(rec + p * (D / 2) + q * (D / 8) + j * (GS / 8) + u * 4) = kw;
-  // V: channel 16 n + r of a token is nibble n mod 4 of its half-word (n / 4, r).  The lane
-  // holds n = l / 2 for the 8 r of its parity; with the words of the other three n of the same
-  // n / 4 (lanes 2, 4 and 6 away) it assembles two of those 8 halves.
-  uint32_t w4[4];
-  const int c4 = (l >> 1) & 3;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w4[i] = (uint32_t)__shfl_xor((int)vw, 2 * (i ^ c4));
-  uint8_t* vb = rec + P * (D / 2) + (p >> 3) * (D * 4) + (l >> 3) * 256 + ((p & 7) >> 1) * 4 + (p & 1) * 2;
-#pragma unroll
-  for (int e = 2 * c4; e < 2 * c4 + 2; ++e) {
-    uint32_t h = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h |= ((w4[i] >> (4 * e)) & 15u) << (4 * i);
-    *(uint16_t*)(vb + (8 * (l & 1) + e) * 16) = (uint16_t)h;
+                                                    int64_t vh, int n_tokens) {
+  constexpr int LPR = D / 8, G = D / GS, R = Rows<D>::R;
+  __shared__ uint32_t vwords[R][LPR + 1];
+  const int head = blockIdx.y;
+  const Rows<D> rows = rows_of<D>(c, blockIdx.x, n_tokens);
+  if (rows.seq < 0 || rows.t0 >= rows.end || rows.t0 + R <= rows.first) return;  // the whole block
+  const int row = threadIdx.x / LPR, l = threadIdx.x % LPR;
+  const int P = 1 << c.log2p;
+  {
+    const int t = rows.t0 + row, pos = rows.pos0 + row;
+    const bool in = t >= rows.first && t < rows.end;
+    float x[2][8];
+    if (in) {  // asked for before the table's answer is waited for
+      load_row8<BF16, true>(k + t * kt + head * kh, nullptr, kFoldNone, 8 * l, D, x[0]);
+      load_row8<BF16, true>(v + t * vt + head * vh, nullptr, kFoldNone, 8 * l, D, x[1]);
+    }
+    const int64_t at = in ? kv4_record_at(c, rows.seq, pos, head) : -1;
+    if (at >= 0) {  // the lanes of a row alike
+      uint8_t* rec = c.pages + at;
+      const int p = pos & (P - 1);
+      uint32_t kp, vp;
+      const uint32_t kw = quantise_group<GS / 8>(x[0], c.zero_point, kp);
+      vwords[row][l] = quantise_group<GS / 8>(x[1], c.zero_point, vp);
+      // keys: the lane's 8 channels are one word
+      const int j = 8 * l / GS, ing = 8 * l % GS;
+      const int q = ing / (GS / 4), u = ing % (GS / 4) / 8;
+      *(uint32_t*)(rec + p * (D / 2) + q * (D / 8) + j * (GS / 8) + u * 4) = kw;
+      if (ing == 0) {
+        uint32_t* par = (uint32_t*)(rec + P * D);
+        par[j * P + p] = kp;
+        par[(G + j) * P + p] = vp;
+      }
+    }
   }
-  if (ing == 0) {
-    uint32_t* par = (uint32_t*)(rec + P * D);
-    par[j * P + p] = kp;
-    par[(G + j) * P + p] = vp;
+  __syncthreads();
+  // values: a thread assembles words of the record, two tokens of four channels 16 apart each
+#pragma unroll
+  for (int w = threadIdx.x; w < R * D / 8; w += 256) {
+    const int r0 = value_word_row<D>(w), h = w % D / 64, r = w % 64 / 4;
+    const int t = rows.t0 + r0, pos = rows.pos0 + r0;
+    const int64_t at = pos >= 0 || pos + 1 >= 0 ? kv4_record_at(c, rows.seq, max(pos, 0), head) : -1;
+    if (at < 0) continue;
+    const bool ok0 = t >= rows.first && t < rows.end && pos >= 0;
+    const bool ok1 = t + 1 >= rows.first && t + 1 < rows.end && pos + 1 >= 0;
+    uint32_t word = 0;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        word |= ((vwords[r0 + e][2 * (4 * h + n) + (r >> 3)] >> (4 * (r & 7))) & 15u) << (16 * e + 4 * n);
+    uint8_t* dst = c.pages + at + P * (D / 2) + ((pos & (P - 1)) >> 3) * (D * 4) + (w % D) * 4;
+    if (ok0 && ok1) *(uint32_t*)dst = word;
+    else if (ok0) *(uint16_t*)dst = (uint16_t)word;
+    else if (ok1) *(uint16_t*)(dst + 2) = (uint16_t)(word >> 16);
   }
 }
 
 template <bool BF16, int D, int GS>
 __global__ __launch_bounds__(256) void k_kv4_read(Kv4Cache c, uint16_t* __restrict__ k,
-                                                  uint16_t* __restrict__ v, int64_t n_rows) {
-  constexpr int LPR = D / 8, G = D / GS;
-  const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPR;
-  const int l = threadIdx.x % LPR;
-  if (row >= n_rows) return;
-  const int64_t t = row / c.kv_heads;
-  const int head = (int)(row - t * c.kv_heads);
+                                                  uint16_t* __restrict__ v, int n_tokens) {
+  constexpr int LPR = D / 8, G = D / GS, R = Rows<D>::R;
+  __shared__ uint32_t words[R * D / 8];
+  const int head = blockIdx.y;
+  const Rows<D> rows = rows_of<D>(c, blockIdx.x, n_tokens);
+  if (rows.t0 >= rows.end || rows.t0 + R <= rows.first) return;  // the whole block
+  const int P = 1 << c.log2p;
+  if (rows.seq >= 0) {
+    // the value codes of the block's positions, coalesced (those of other tokens unused)
+#pragma unroll
+    for (int w = threadIdx.x; w < R * D / 8; w += 256) {
+      const int pos = rows.pos0 + value_word_row<D>(w);
+      const int64_t at = kv4_record_at(c, rows.seq, pos, head);
+      words[w] = at < 0 ? 0u
+                        : *(const uint32_t*)(c.pages + at + P * (D / 2) +
+                                             ((pos & (P - 1)) >> 3) * (D * 4) + (w % D) * 4);
+    }
+  }
+  __syncthreads();
+  const int row = threadIdx.x / LPR, l = threadIdx.x % LPR;
+  const int t = rows.t0 + row, pos = rows.pos0 + row;
+  if (t < rows.first || t >= rows.end) return;
   uint4 ko = {0u, 0u, 0u, 0u}, vo = {0u, 0u, 0u, 0u};
-  const int b = kv4_sequence(c, t);
-  const int pos = b < 0 ? -1 : c.lens[b] - (c.starts[b + 1] - (int)t);
-  const int64_t at = b < 0 ? -1 : kv4_record_at(c, b, pos, head);
+  const int64_t at = rows.seq < 0 ? -1 : kv4_record_at(c, rows.seq, pos, head);
   if (at >= 0) {
     const uint8_t* rec = c.pages + at;
-    const int P = 1 << c.log2p, p = pos & (P - 1);
+    const int p = pos & (P - 1);
     const int j = 8 * l / GS, ing = 8 * l % GS;
     const int q = ing / (GS / 4), u = ing % (GS / 4) / 8;
     const uint32_t kw = *(const uint32_t*)(rec + p * (D / 2) + q * (D / 8) + j * (GS / 8) + u * 4);
-    const uint8_t* vb =
-        rec + P * (D / 2) + (p >> 3) * (D * 4) + (l >> 3) * 256 + ((p & 7) >> 1) * 4 + (p & 1) * 2;
     const uint32_t* par = (const uint32_t*)(rec + P * D);
     const uint32_t kp = par[j * P + p], vp = par[(G + j) * P + p];
     const float ks = h2f((uint16_t)kp), kz = h2f((uint16_t)(kp >> 16));
@@ -113,16 +181,17 @@ __global__ __launch_bounds__(256) void k_kv4_read(Kv4Cache c, uint16_t* __restri
     uint16_t kr[8], vr[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const uint32_t h = *(const uint16_t*)(vb + (8 * (l & 1) + e) * 16);
-      const int kc = (kw >> (4 * e)) & 15, vc = (h >> (4 * ((l >> 1) & 3))) & 15;
+      const uint32_t word = words[(row >> 3) * D + (l >> 3) * 64 + (8 * (l & 1) + e) * 4 + ((row & 7) >> 1)];
+      const int kc = (kw >> (4 * e)) & 15, vc = (word >> (16 * (row & 1) + 4 * ((l >> 1) & 3))) & 15;
       kr[e] = to16<BF16>(((float)kc - kz) * ks);
       vr[e] = to16<BF16>(((float)vc - vz) * vs);
     }
     __builtin_memcpy(&ko, kr, 16);
     __builtin_memcpy(&vo, vr, 16);
   }
-  *(uint4*)(k + row * D + 8 * l) = ko;
-  *(uint4*)(v + row * D + 8 * l) = vo;
+  const int64_t o = ((int64_t)t * c.kv_heads + head) * D + 8 * l;
+  *(uint4*)(k + o) = ko;
+  *(uint4*)(v + o) = vo;
 }
 
 }  // namespace
@@ -140,12 +209,11 @@ __global__ __launch_bounds__(256) void k_kv4_read(Kv4Cache c, uint16_t* __restri
 hipError_t launch_kv4_append(const Kv4Cache& c, const void* k, int64_t kt, int64_t kh,
                              const void* v, int64_t vt, int64_t vh, int64_t n_tokens, bool bf16,
                              hipStream_t stream) {
-  const int64_t rows = n_tokens * c.kv_heads, blocks = (rows * (c.dim / 8) + 255) / 256;
-  if (rows <= 0) return hipSuccess;
-  if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
-#define AWQ_APPEND(B, D, GS)                                                                   \
-  hipLaunchKernelGGL((k_kv4_append<B, D, GS>), dim3((unsigned)blocks), dim3(256), 0, stream, c, \
-                     (const uint16_t*)k, kt, kh, (const uint16_t*)v, vt, vh, rows)
+  if (n_tokens <= 0) return hipSuccess;
+  const dim3 grid((unsigned)(n_tokens / (2048 / c.dim) + 2 * c.n_seqs + 1), (unsigned)c.kv_heads);
+#define AWQ_APPEND(B, D, GS)                                                           \
+  hipLaunchKernelGGL((k_kv4_append<B, D, GS>), grid, dim3(256), 0, stream, c,           \
+                     (const uint16_t*)k, kt, kh, (const uint16_t*)v, vt, vh, (int)n_tokens)
   if (bf16) { AWQ_KV4_DG(AWQ_APPEND, true) } else { AWQ_KV4_DG(AWQ_APPEND, false) }
 #undef AWQ_APPEND
   return hipGetLastError();
@@ -153,12 +221,11 @@ hipError_t launch_kv4_append(const Kv4Cache& c, const void* k, int64_t kt, int64
 
 hipError_t launch_kv4_read(const Kv4Cache& c, int64_t n_tokens, bool bf16, void* k, void* v,
                            hipStream_t stream) {
-  const int64_t rows = n_tokens * c.kv_heads, blocks = (rows * (c.dim / 8) + 255) / 256;
-  if (rows <= 0) return hipSuccess;
-  if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
-#define AWQ_READ(B, D, GS)                                                                    \
-  hipLaunchKernelGGL((k_kv4_read<B, D, GS>), dim3((unsigned)blocks), dim3(256), 0, stream, c, \
-                     (uint16_t*)k, (uint16_t*)v, rows)
+  if (n_tokens <= 0) return hipSuccess;
+  const dim3 grid((unsigned)(n_tokens / (2048 / c.dim) + 2 * c.n_seqs + 1), (unsigned)c.kv_heads);
+#define AWQ_READ(B, D, GS)                                                     \
+  hipLaunchKernelGGL((k_kv4_read<B, D, GS>), grid, dim3(256), 0, stream, c, (uint16_t*)k, \
+                     (uint16_t*)v, (int)n_tokens)
   if (bf16) { AWQ_KV4_DG(AWQ_READ, true) } else { AWQ_KV4_DG(AWQ_READ, false) }
 #undef AWQ_READ
   return hipGetLastError();

@@ -128,7 +128,7 @@ int awq_int8_linear(const void* x, int64_t ldx, const float* s, int64_t n_tokens
   if (awq::int8_linear_fused(T, round16(K))) {
     const awq::Int8Args a{nullptr, 0, nullptr, wq, ldw, wstep, bias, y, ldy,
                           (int)T, (int)M, (int)round16(K), dtype == AWQ_BF16};
-    return hip_status(awq::launch_int8_linear_fused(a, x, ldx, s, (int)K, (hipStream_t)stream));
+    return hip_status(awq::launch_int8_linear_fused(a, x, s, (int)K, (hipStream_t)stream));
   }
   char* ws = (char*)workspace;
   int8_t* xq = (int8_t*)ws;

@@ -31,11 +31,11 @@ struct Int8Args {
 };
 size_t int8_matmul_workspace(int64_t T, int64_t M, int64_t K);
 hipError_t launch_int8_matmul(const Int8Args& a, void* workspace, hipStream_t stream);
-// The linear layer in one launch: a.x, a.ldx and a.xstep unused, x 16-bit [T][ldx] with `cols`
-// columns.  Taken where int8_linear_fused says so.
+// The linear layer of one token in one launch: a.x, a.ldx and a.xstep unused, x 16-bit with
+// `cols` columns.  Taken where int8_linear_fused says so.
 bool int8_linear_fused(int64_t T, int64_t K);
-hipError_t launch_int8_linear_fused(const Int8Args& a, const void* x, int64_t ldx, const float* s,
-                                    int cols, hipStream_t stream);
+hipError_t launch_int8_linear_fused(const Int8Args& a, const void* x, const float* s, int cols,
+                                    hipStream_t stream);
 
 // ---- key/value cache in 4 bits ---------------------------------------------------------
 struct Kv4Cache {
