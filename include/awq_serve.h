@@ -89,7 +89,8 @@ int awq_int8_linear(const void* x, int64_t ldx, const float* s, int64_t n_tokens
  *   channels by the quantiser of awq_quantize_pack with w_bit 4 and no channel scales (fp32,
  *   one rounding an operation; symmetric or zero-point); a value reads as
  *   (code - zero) * fp16(step) [AWQ-blog §1.2, §2.1; AutoAWQ-70B §四 (metadata per group)].
- *   A group that holds a NaN or an infinity is stored with step NaN, codes and zero 0.
+ *   A group whose range is not finite (it holds a NaN or an infinity, or the range overflows) is
+ *   stored with step NaN, codes and zero 0.
  *
  *   cache        uint8 [n_pages][kv_heads][record], 16-byte aligned; record =
  *                awq_kv4_record_bytes(cfg).  With D = head_dim, P = page_size, g = group_size,

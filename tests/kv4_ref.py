@@ -57,7 +57,10 @@ class Layout:
         v = np.where(bad[..., None], F32(0), v)
         if self.zp:
             hi, lo = np.maximum(v.max(-1), F32(0)), np.minimum(v.min(-1), F32(0))
-            st = ((hi - lo).astype(F32) / F32(15)).astype(F32)
+            with np.errstate(over="ignore"):
+                st = ((hi - lo).astype(F32) / F32(15)).astype(F32)
+            bad |= ~np.isfinite(st)                             # the range overflows
+            v, lo, st = np.where(bad[..., None], F32(0), v), np.where(bad, F32(0), lo), np.where(bad, F32(1), st)
             st = np.where(st == 0, F32(1), st)
             z = np.clip(np.rint((-lo / st).astype(F32)), 0, 15) + F32(0)  # an integer: no -0
             c = np.clip(np.rint((v / st[..., None]).astype(F32)) + z[..., None], 0, 15)

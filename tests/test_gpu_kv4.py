@@ -121,6 +121,48 @@ def test_append_bytes_and_read(D, g, zp, dtype):
                 assert np.array_equal(o[t, h], w, equal_nan=True), (t, h, side)
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("zp", [0, 1])
+def test_append_steps_at_the_ends(dtype, zp):
+    """Ranges from the type's subnormals to its largest values, each with every magnitude of its
+    16-bit values, exact halves of the step, steps of all mantissa bits, and ranges that overflow:
+    the bytes are the model's."""
+    lay = Layout(64, 1, 16, 32, zp)
+    info = torch.finfo(DT[dtype])
+    rng = np.random.default_rng(5)
+    n = 256
+    c = Case(64, 1, 16, 32, zp, (n,), (n,), dtype, seed=1)
+    x = rng.standard_normal((n, 1, 64))
+    exps = np.linspace(np.log2(float(info.tiny)) - 9, np.log2(float(info.max)) - 1, n)
+    x = np.clip(x, -2, 2) / 2 * (2.0 ** exps)[:, None, None]
+    x[10] = np.arange(64)[None] - 20                       # ties: range 31 or 43 over 15 steps
+    x[11] = (np.arange(64)[None] % 16) * 0.5               # step 1/2: quotients are integers
+    x[12] = (np.arange(64)[None] % 31 - 15) * 0.25
+    x[13, 0, :32], x[13, 0, 32:] = float(info.max), float(info.min)
+    x[14, 0, 0], x[14, 0, 1] = float(info.max), float(info.min)
+    k = torch.from_numpy(x).to(c.dt).cuda()
+    # steps whose mantissa is all ones or next to it, where a range of the type's values gives one
+    vals = torch.arange(0, 32768, device="cuda", dtype=torch.int32).to(torch.int16).view(c.dt)
+    vals = vals[torch.isfinite(vals)].float().cpu().numpy()
+    st = (vals / np.float32(15 if zp else 7)).astype(np.float32)
+    pick = vals[np.argsort(-(st.view(np.uint32) & 0x7fffff).astype(np.int64))[:n]]
+    v = rng.uniform(-1, 1, (n, 1, 64)) * pick[:, None, None] * (0 if zp else 1)
+    if zp:
+        v = rng.uniform(0, 1, (n, 1, 64)) * pick[:, None, None]
+    v[:, 0, 5] = pick
+    v[:, 0, 40] = pick
+    v = torch.from_numpy(v).to(c.dt).cuda()
+    want = c.cache.cpu().numpy().copy()
+    kn, vn = k.float().cpu().numpy(), v.float().cpu().numpy()
+    for t in range(n):
+        rec = want[c.table[0, t // 16], 0]
+        lay.write(rec, t % 16, 0, kn[t, 0])
+        lay.write(rec, t % 16, 1, vn[t, 0])
+    awq.awq_kv4_append(k, v, c.cache, c.dtable, c.dlens, c.dstarts, c.cfg)
+    got = c.cache.cpu().numpy()
+    assert np.array_equal(got, want), np.argwhere(got != want)[:5]
+
+
 def test_append_strided_and_lost_pages():
     """Views into a fused projection; table entries that name no page drop their tokens."""
     c = Case(128, 2, 32, 64, 1, (100, 40), (100, 40), seed=3)

@@ -16,24 +16,80 @@ namespace awq {
 
 namespace {
 
-// Codes (nibble e = channel e) and the parameter pair of the lane's group.
-template <int LANES>
-__device__ __forceinline__ uint32_t quantise_group(const float (&v)[8], bool zp, uint32_t& par) {
-  float code[8], step, zero;
-  quantize8<LANES>(v, 4, zp, code, step, zero);
-  float odd = 0.0f;
+// a / b, correctly rounded, from y = RN(1 / b): the residual a - b q of a quotient q within an ulp
+// is exact in one fused multiply-add, and q plus residual times y rounds to RN(a / b)
+// (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990)
+// while nothing underflows.
+__device__ __forceinline__ float quotient(float a, float b, float y) {
+  const float q = a * y;
+  return fmaf(fmaf(-q, b, a), y, q);
+}
+
+// Codes (nibble e = channel e) and the parameter pair of the lane's group, from eight 16-bit
+// values: the quantiser of quantizer.h (4 bits, no channel scales) with the same results.  Values
+// of 16 bits tie often (a wave of them nearly always somewhere), so the quotients are all
+// corrected, without its test for half-integers and division behind a branch.
+template <bool BF16, int LANES, bool ZP>
+__device__ __forceinline__ uint32_t quantise_group(const uint4 raw, uint32_t& par) {
+  const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w};
+  float v[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) odd = fabsf(v[i]) < __builtin_inff() ? odd : 1.0f;
-  odd = group_max<LANES>(odd);
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w |= (uint32_t)(int)code[i] << (4 * i);
-  par = (uint32_t)f2h(step) | ((uint32_t)f2h(zero) << 16);
-  if (odd != 0.0f) {
-    w = 0;
-    par = 0x7e00u;  // step NaN, zero 0
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = from16<BF16>(r[i] & 0xffffu);
+    v[2 * i + 1] = BF16 ? __builtin_bit_cast(float, r[i] & 0xffff0000u) : from16<BF16>(r[i] >> 16);
   }
-  return w;
+  // NaN or infinity in the lane: the largest pattern without the sign
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  u16x2 big = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    big = __builtin_elementwise_max(big, __builtin_bit_cast(u16x2, r[i] & 0x7fff7fffu));
+  const bool odd = max(big[0], big[1]) >= (BF16 ? 0x7f80 : 0x7c00);
+  float hi = 0.0f, lo = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    hi = fmaxf(hi, ZP ? v[i] : fabsf(v[i]));
+    lo = fminf(lo, v[i]);
+  }
+  hi = group_max<LANES>(odd ? __builtin_inff() : hi);
+  lo = ZP ? group_min<LANES>(lo) : 0.0f;
+  const float range = hi - lo, top = ZP ? 15.0f : 7.0f;
+  float st = quotient(range, top, ZP ? 1.0f / 15.0f : 1.0f / 7.0f);
+  // what the corrected quotients do not cover: steps whose residuals may underflow, and those of
+  // all mantissa bits, whose reciprocal one step of Newton's need not round correctly
+  const uint32_t bits = __builtin_bit_cast(uint32_t, st);
+  const bool rare = st < 0x1p-90f || (bits & 0x7fffffu) == 0x7fffffu;
+  float q[8], z;
+  if (rare) {
+    st = range / top;
+    if (st == 0.0f) st = 1.0f;
+    z = rintf(-lo / st);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = rintf(v[i] / st);
+  } else {
+    const float y0 = __builtin_amdgcn_rcpf(st);
+    const float y = fmaf(fmaf(-st, y0, 1.0f), y0, y0);
+    z = rintf(quotient(-lo, st, y));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = rintf(quotient(v[i], st, y));
+  }
+  z = ZP ? fminf(fmaxf(z, 0.0f), 15.0f) : 8.0f;
+  float code[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    code[i] = ZP ? fminf(fmaxf(q[i] + z, 0.0f), 15.0f) : fminf(fmaxf(q[i], -7.0f), 7.0f) + 8.0f;
+  // four codes at a time as one exact number below 2^16
+  uint32_t half[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    half[h] = (uint32_t)fmaf(fmaf(fmaf(code[4 * h + 3], 16.0f, code[4 * h + 2]), 16.0f, code[4 * h + 1]), 16.0f,
+                             code[4 * h]);
+  par = (uint32_t)f2h(st) | ((uint32_t)f2h(z) << 16);
+  if (!(range < __builtin_inff())) {
+    par = 0x7e00u;  // step NaN, zero 0
+    return 0;
+  }
+  return half[0] | (half[1] << 16);
 }
 
 // Which rows a block works on: R = 2048 / D consecutive positions of one sequence, the first a
@@ -81,36 +137,48 @@ __device__ __forceinline__ Rows<D> rows_of(const Kv4Cache& c, int blk, int n_tok
 template <int D>
 __device__ __forceinline__ int value_word_row(int w) { return (w / D) * 8 + 2 * (w & 3); }
 
-template <bool BF16, int D, int GS>
+// HPB heads a block: finding the sequence, the rows and the page takes a few dependent loads,
+// which one head's work does not hide (prompts of 8191 tokens, 8 heads: HEADS_1 us with one head a
+// block, HEADS_4 with four).
+template <bool BF16, int D, int GS, int HPB, bool ZP>
 __global__ __launch_bounds__(256) void k_kv4_append(Kv4Cache c, const uint16_t* __restrict__ k,
                                                     int64_t kt, int64_t kh,
                                                     const uint16_t* __restrict__ v, int64_t vt,
                                                     int64_t vh, int n_tokens) {
   constexpr int LPR = D / 8, G = D / GS, R = Rows<D>::R;
-  __shared__ uint32_t vwords[R][LPR + 1];
-  const int head = blockIdx.y;
-  const Rows<D> rows = rows_of<D>(c, blockIdx.x, n_tokens);
+  __shared__ uint32_t vwords[HPB][R][LPR + 1];
+  __shared__ int64_t page_at[R];  // each row's page, as its offset for head 0, or -1
+  const int per = (c.kv_heads + HPB - 1) / HPB;
+  const int group = blockIdx.x / per, head0 = (blockIdx.x - group * per) * HPB;
+  const Rows<D> rows = rows_of<D>(c, group, n_tokens);
   if (rows.seq < 0 || rows.t0 >= rows.end || rows.t0 + R <= rows.first) return;  // the whole block
   const int row = threadIdx.x / LPR, l = threadIdx.x % LPR;
   const int P = 1 << c.log2p;
   {
     const int t = rows.t0 + row, pos = rows.pos0 + row;
     const bool in = t >= rows.first && t < rows.end;
-    float x[2][8];
-    if (in) {  // asked for before the table's answer is waited for
-      load_row8<BF16, true>(k + t * kt + head * kh, nullptr, kFoldNone, 8 * l, D, x[0]);
-      load_row8<BF16, true>(v + t * vt + head * vh, nullptr, kFoldNone, 8 * l, D, x[1]);
+    uint4 xk[HPB], xv[HPB];
+#pragma unroll
+    for (int i = 0; i < HPB; ++i) {  // asked for before the table's answer is waited for
+      xk[i] = xv[i] = uint4{0u, 0u, 0u, 0u};
+      if (in && head0 + i < c.kv_heads) {
+        xk[i] = *(const uint4*)(k + t * kt + (head0 + i) * kh + 8 * l);
+        xv[i] = *(const uint4*)(v + t * vt + (head0 + i) * vh + 8 * l);
+      }
     }
-    const int64_t at = in ? kv4_record_at(c, rows.seq, pos, head) : -1;
-    if (at >= 0) {  // the lanes of a row alike
-      uint8_t* rec = c.pages + at;
-      const int p = pos & (P - 1);
+    const int64_t at = in ? kv4_record_at(c, rows.seq, pos, 0) : -1;
+    if (l == 0) page_at[row] = at;
+    const int p = pos & (P - 1);
+    const int j = 8 * l / GS, ing = 8 * l % GS;
+    const int q = ing / (GS / 4), u = ing % (GS / 4) / 8;
+#pragma unroll
+    for (int i = 0; i < HPB; ++i) {
+      if (at < 0 || head0 + i >= c.kv_heads) break;  // the lanes of a row alike
+      uint8_t* rec = c.pages + at + (int64_t)(head0 + i) * c.record;
       uint32_t kp, vp;
-      const uint32_t kw = quantise_group<GS / 8>(x[0], c.zero_point, kp);
-      vwords[row][l] = quantise_group<GS / 8>(x[1], c.zero_point, vp);
+      const uint32_t kw = quantise_group<BF16, GS / 8, ZP>(xk[i], kp);
+      vwords[i][row][l] = quantise_group<BF16, GS / 8, ZP>(xv[i], vp);
       // keys: the lane's 8 channels are one word
-      const int j = 8 * l / GS, ing = 8 * l % GS;
-      const int q = ing / (GS / 4), u = ing % (GS / 4) / 8;
       *(uint32_t*)(rec + p * (D / 2) + q * (D / 8) + j * (GS / 8) + u * 4) = kw;
       if (ing == 0) {
         uint32_t* par = (uint32_t*)(rec + P * D);
@@ -121,24 +189,28 @@ __global__ __launch_bounds__(256) void k_kv4_append(Kv4Cache c, const uint16_t* 
   }
   __syncthreads();
   // values: a thread assembles words of the record, two tokens of four channels 16 apart each
+  // (the two lie in one page)
 #pragma unroll
   for (int w = threadIdx.x; w < R * D / 8; w += 256) {
     const int r0 = value_word_row<D>(w), h = w % D / 64, r = w % 64 / 4;
-    const int t = rows.t0 + r0, pos = rows.pos0 + r0;
-    const int64_t at = pos >= 0 || pos + 1 >= 0 ? kv4_record_at(c, rows.seq, max(pos, 0), head) : -1;
-    if (at < 0) continue;
-    const bool ok0 = t >= rows.first && t < rows.end && pos >= 0;
-    const bool ok1 = t + 1 >= rows.first && t + 1 < rows.end && pos + 1 >= 0;
-    uint32_t word = 0;
+    const int64_t at0 = page_at[r0], at1 = page_at[r0 + 1];
+    if (at0 < 0 && at1 < 0) continue;
+    const int64_t at = (at0 < 0 ? at1 : at0) + P * (D / 2) +
+                       (((rows.pos0 + r0) & (P - 1)) >> 3) * (D * 4) + (w % D) * 4;
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+    for (int i = 0; i < HPB; ++i) {
+      if (head0 + i >= c.kv_heads) break;
+      uint32_t word = 0;
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
-        word |= ((vwords[r0 + e][2 * (4 * h + n) + (r >> 3)] >> (4 * (r & 7))) & 15u) << (16 * e + 4 * n);
-    uint8_t* dst = c.pages + at + P * (D / 2) + ((pos & (P - 1)) >> 3) * (D * 4) + (w % D) * 4;
-    if (ok0 && ok1) *(uint32_t*)dst = word;
-    else if (ok0) *(uint16_t*)dst = (uint16_t)word;
-    else if (ok1) *(uint16_t*)(dst + 2) = (uint16_t)(word >> 16);
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+          word |= ((vwords[i][r0 + e][2 * (4 * h + n) + (r >> 3)] >> (4 * (r & 7))) & 15u) << (16 * e + 4 * n);
+      uint8_t* dst = c.pages + at + (int64_t)(head0 + i) * c.record;
+      if (at0 >= 0 && at1 >= 0) *(uint32_t*)dst = word;
+      else if (at0 >= 0) *(uint16_t*)dst = (uint16_t)word;
+      else *(uint16_t*)(dst + 2) = (uint16_t)(word >> 16);
+    }
   }
 }
 
@@ -147,8 +219,8 @@ __global__ __launch_bounds__(256) void k_kv4_read(Kv4Cache c, uint16_t* __restri
                                                   uint16_t* __restrict__ v, int n_tokens) {
   constexpr int LPR = D / 8, G = D / GS, R = Rows<D>::R;
   __shared__ uint32_t words[R * D / 8];
-  const int head = blockIdx.y;
-  const Rows<D> rows = rows_of<D>(c, blockIdx.x, n_tokens);
+  const int group = blockIdx.x / c.kv_heads, head = blockIdx.x - group * c.kv_heads;
+  const Rows<D> rows = rows_of<D>(c, group, n_tokens);
   if (rows.t0 >= rows.end || rows.t0 + R <= rows.first) return;  // the whole block
   const int P = 1 << c.log2p;
   if (rows.seq >= 0) {
@@ -210,19 +282,32 @@ hipError_t launch_kv4_append(const Kv4Cache& c, const void* k, int64_t kt, int64
                              const void* v, int64_t vt, int64_t vh, int64_t n_tokens, bool bf16,
                              hipStream_t stream) {
   if (n_tokens <= 0) return hipSuccess;
-  const dim3 grid((unsigned)(n_tokens / (2048 / c.dim) + 2 * c.n_seqs + 1), (unsigned)c.kv_heads);
-#define AWQ_APPEND(B, D, GS)                                                           \
-  hipLaunchKernelGGL((k_kv4_append<B, D, GS>), grid, dim3(256), 0, stream, c,           \
+  const int64_t groups = n_tokens / (2048 / c.dim) + 2 * c.n_seqs + 1;
+  const bool four = groups * c.kv_heads >= 8192;  // four blocks a compute unit with four heads each
+  const int64_t blocks = groups * (four ? (c.kv_heads + 3) / 4 : c.kv_heads);
+  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+#define AWQ_APPEND_Z(B, D, GS, H, Z)                                                              \
+  hipLaunchKernelGGL((k_kv4_append<B, D, GS, H, Z>), dim3((unsigned)blocks), dim3(256), 0, stream, c, \
                      (const uint16_t*)k, kt, kh, (const uint16_t*)v, vt, vh, (int)n_tokens)
+#define AWQ_APPEND_H(B, D, GS, H)                         \
+  if (c.zero_point) AWQ_APPEND_Z(B, D, GS, H, true);      \
+  else AWQ_APPEND_Z(B, D, GS, H, false)
+#define AWQ_APPEND(B, D, GS)           \
+  if (four) { AWQ_APPEND_H(B, D, GS, 4); } \
+  else { AWQ_APPEND_H(B, D, GS, 1); }
   if (bf16) { AWQ_KV4_DG(AWQ_APPEND, true) } else { AWQ_KV4_DG(AWQ_APPEND, false) }
 #undef AWQ_APPEND
+#undef AWQ_APPEND_H
+#undef AWQ_APPEND_Z
   return hipGetLastError();
 }
 
 hipError_t launch_kv4_read(const Kv4Cache& c, int64_t n_tokens, bool bf16, void* k, void* v,
                            hipStream_t stream) {
   if (n_tokens <= 0) return hipSuccess;
-  const dim3 grid((unsigned)(n_tokens / (2048 / c.dim) + 2 * c.n_seqs + 1), (unsigned)c.kv_heads);
+  const int64_t blocks = (n_tokens / (2048 / c.dim) + 2 * c.n_seqs + 1) * c.kv_heads;
+  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)blocks);
 #define AWQ_READ(B, D, GS)                                                     \
   hipLaunchKernelGGL((k_kv4_read<B, D, GS>), grid, dim3(256), 0, stream, c, (uint16_t*)k, \
                      (uint16_t*)v, (int)n_tokens)
