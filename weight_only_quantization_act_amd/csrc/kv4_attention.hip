@@ -52,10 +52,7 @@ typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 constexpr float kSlack = 4.0f;
 constexpr float kNegInf = -__builtin_inff();
 constexpr int kWaves = 4;
-#ifndef KV4_NS
-#define KV4_NS 3
-#endif
-constexpr int kStages = KV4_NS;  // tiles a wave has in flight
+constexpr int kStages = 3;  // tiles a wave has in flight
 
 __device__ __forceinline__ float max_q(float v) {  // over the four lanes of a column
   v = fmaxf(v, __shfl_xor(v, 16));
@@ -483,8 +480,28 @@ __device__ __forceinline__ float lse_of(float M, float l) {
 struct Partials {
   float* o;
   float* ml;
-  int splits;
+  int splits, tiles;
 };
+
+// Which work a block does.  Blocks start in the order of their number: later column tiles see more
+// keys, so they go first, of all heads and sequences before any earlier tile (a prompt of 4096
+// tokens: 302 us with a head's tiles together, when long blocks start late, 211 so); and
+// consecutive blocks, which go to different dies, are different key heads: with eight of them
+// each die's L2 holds one.
+struct Place {
+  int head, split, seq, tile;  // tile -1: none
+};
+__device__ __forceinline__ Place place_of(const Kv4Cache& c, const Partials& part) {
+  unsigned n = blockIdx.x + gridDim.x * blockIdx.y;
+  Place p;
+  p.head = n % c.kv_heads;
+  n /= c.kv_heads;
+  p.split = n % part.splits;
+  n /= part.splits;
+  p.seq = n % c.n_seqs;
+  p.tile = part.tiles - 1 - (int)(n / c.n_seqs);
+  return p;
+}
 
 // waves a SIMD that the registers are kept to
 constexpr int waves_per_simd(int dim, int group) {
@@ -499,10 +516,9 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(wave
   constexpr int NC = 1, kCols = 16;  // columns a block
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int b = blockIdx.z, kvh = blockIdx.y % c.kv_heads;
-  const int split = blockIdx.y / c.kv_heads;
-  // later column tiles see more keys: they go first
-  const int tile = gridDim.x - 1 - blockIdx.x;
+  const Place at = place_of(c, part);
+  if (at.tile < 0) return;  // the whole block
+  const int b = at.seq, kvh = at.head, split = at.split, tile = at.tile;
   const int group = a.heads / c.kv_heads;
   const int row0 = c.starts[b];
   const int rows = min(c.starts[b + 1] - row0, a.max_q);
@@ -689,10 +705,36 @@ struct Raw {
   uint32_t k[X::KW], kz[X::G];
   u32x4 v, vz[GH][2];
   uint32_t par[PW];
-  // which of them exist (applied when they are decoded, so that nothing waits for a load here)
-  bool k_ok, par_ok;
-  int v_there;
+  uint64_t dead;  // bit l: key l of the step lies on no page
+  int v_there;    // of the 8 keys of v, those that exist
 };
+
+// Codes minus zeros, exact, without a shift per pair: a nibble in the low four bits of a half
+// under the pattern of 1024 is 1024 + c, one in the next four under that of 64 is 64 + c, and
+// the zero has the same offset added.
+struct CodeConsts2 {
+  uint32_t mask[2], offset[2];
+};
+__device__ __forceinline__ CodeConsts2 code_consts2() {
+  CodeConsts2 c;
+  asm volatile("s_mov_b32 %0, %1" : "=s"(c.mask[0]) : "i"(0x000F000Fu));
+  asm volatile("s_mov_b32 %0, %1" : "=s"(c.mask[1]) : "i"(0x00F000F0u));
+  asm volatile("v_mov_b32 %0, %1" : "=v"(c.offset[0]) : "i"(0x64006400u));
+  asm volatile("v_mov_b32 %0, %1" : "=v"(c.offset[1]) : "i"(0x54005400u));
+  return c;
+}
+__device__ __forceinline__ uint32_t pk_add16(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, a) + __builtin_bit_cast(half2v, b));
+}
+__device__ __forceinline__ uint32_t pk_sub16(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, a) - __builtin_bit_cast(half2v, b));
+}
+// pair n of a word minus zeros z0 (1024 + z), z1 (64 + z)
+template <int N>
+__device__ __forceinline__ uint32_t centred_pair(uint32_t w, uint32_t z0, uint32_t z1,
+                                                 const CodeConsts2& cc) {
+  return pk_sub16(((N >= 2 ? w >> 8 : w) & cc.mask[N & 1]) | cc.offset[N & 1], N & 1 ? z1 : z0);
+}
 
 template <int D, int GS>
 __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2)))
@@ -706,9 +748,9 @@ void k_kv4_attention_wide(Kv4Cache c, Kv4Query a, Partials part) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lr = lane & 15, q = lane >> 4;
-  const int b = blockIdx.z, kvh = blockIdx.y % c.kv_heads;
-  const int split = blockIdx.y / c.kv_heads;
-  const int tile = gridDim.x - 1 - blockIdx.x;  // later column tiles see more keys: they go first
+  const Place at = place_of(c, part);
+  if (at.tile < 0) return;  // the whole block
+  const int b = at.seq, kvh = at.head, split = at.split, tile = at.tile;
   const int group = a.heads / c.kv_heads;
   const int row0 = c.starts[b];
   const int rows = min(c.starts[b + 1] - row0, a.max_q);
@@ -746,113 +788,114 @@ void k_kv4_attention_wide(Kv4Cache c, Kv4Query a, Partials part) {
     t_lo = lo;
     t_hi = hi;
   }
-  const auto* table = (const __attribute__((address_space(4))) int32_t*)(uintptr_t)(
-      c.table + (int64_t)b * c.max_blocks);
   const int last_blk = max(0, (len - 1) >> c.log2p);
-  const int n_pages = (int)c.n_pages;
-  // the table entries of a step's four times 16 keys, read one step ahead
-  int pages[4];
-  auto look_up = [&](int t) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) pages[i] = table[min((64 * t + 16 * i) >> c.log2p, last_blk)];
-  };
-  const CodeConsts cc = code_consts();
   const int tt = wave >> 1, sub = wave & 1;  // the wave's decode passes: 32 keys, K result / V piece
 
+  // A lane's keys of a step (K codes, V codes, parameters) and where they lie in a record: key
+  // 64 t + x is at (64 t mod P) + (x mod P) of its page.
+  const int key_k = 32 * tt + 8 * (lr >> 2) + 4 * sub + (lr & 3), key_v = 32 * tt + 8 * q;
+  const int off_k = (key_k & (P - 1)) * (D / 2) + q * (D / 8), off_kz = P * D + 4 * (key_k & (P - 1));
+  const int off_v = P * (D / 2) + (key_v & (P - 1)) * (D / 2) + 256 * sub + 16 * lr;
+  const int off_vz = P * D + 4 * (P * (X::G + 64 * sub / GS) + (key_v & (P - 1)));
+  const int off_p = P * D + 4 * (lane & (P - 1));
+  const int32_t* table = c.table + (int64_t)b * c.max_blocks;
+  const uint8_t* head_at = c.pages + (int64_t)kvh * c.record;
+  const uint32_t page_bytes = (uint32_t)c.kv_heads * (uint32_t)c.record;  // below 2^32
+  // their table entries, read one step ahead
+  uint32_t page_k, page_v, page_p;
+  auto look_up = [&](int t) {
+    page_k = table[min((64 * t + key_k) >> c.log2p, last_blk)];
+    page_v = table[min((64 * t + key_v) >> c.log2p, last_blk)];
+    page_p = table[min((64 * t + lane) >> c.log2p, last_blk)];
+  };
+  const CodeConsts2 cc = code_consts2();
+
   // the codes of step t into registers
-  // (bit i of what it returns: the 16 keys i of the step lie on no page)
-  auto fetch = [&](R& r, int t) -> int {
-    const uint8_t* rec[4];
-    int bad[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      bad[i] = (unsigned)pages[i] >= (unsigned)n_pages;
-      rec[i] = c.pages + ((int64_t)(bad[i] ? 0 : pages[i]) * c.kv_heads + kvh) * (int64_t)c.record;
-    }
+  auto fetch = [&](R& r, int t) {
+    const int base = (64 * t) & (P - 1);
+    auto record = [&](uint32_t page, bool& bad) {
+      bad = page >= (uint32_t)c.n_pages;
+      return head_at + (uint64_t)(bad ? 0u : page) * page_bytes;
+    };
+    bool bad_k, bad_v, bad_p;
+    const uint8_t* rk = record(page_k, bad_k);
+    const uint8_t* rv = record(page_v, bad_v);
+    const uint8_t* rp = record(page_p, bad_p);
     look_up(t + 1);
-    const int key32 = 64 * t + 32 * tt;
-    {
-      const int half = lr >> 3, in = 8 * (lr >> 2) + 4 * sub + (lr & 3);  // key of the tile of 32
-      const uint8_t* p = half ? (tt ? rec[3] : rec[1]) : (tt ? rec[2] : rec[0]);
-      const int off = (key32 + in) & (P - 1);
-      const uint8_t* kp = p + off * (D / 2) + q * (D / 8);
-      if constexpr (X::KW == 2) {
-        const uint2 w = *(const uint2*)kp;
-        r.k[0] = w.x;
-        r.k[1] = w.y;
-      } else {
-        const u32x4 w = *(const u32x4*)kp;
+    const uint8_t* kp = rk + (off_k + base * (D / 2));
+    if constexpr (X::KW == 2) {
+      const uint2 w = *(const uint2*)kp;
+      r.k[0] = w.x;
+      r.k[1] = w.y;
+    } else {
+      const u32x4 w = *(const u32x4*)kp;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) r.k[e] = w[e];
-      }
-      r.k_ok = key32 + in < len && !(half ? (tt ? bad[3] : bad[1]) : (tt ? bad[2] : bad[0]));
-#pragma unroll
-      for (int g = 0; g < X::G; ++g) r.kz[g] = *(const uint32_t*)(p + P * D + 4 * (P * g + off));
+      for (int e = 0; e < 4; ++e) r.k[e] = w[e];
     }
+    const uint8_t* kz = rk + (off_kz + 4 * base);
+#pragma unroll
+    for (int g = 0; g < X::G; ++g) r.kz[g] = *(const uint32_t*)(kz + 4 * P * g);
     if (sub < X::H) {
-      const int half = q >> 1;
-      const uint8_t* p = half ? (tt ? rec[3] : rec[1]) : (tt ? rec[2] : rec[0]);
-      const int off = (key32 + 8 * q) & (P - 1);
-      r.v = *(const u32x4*)(p + P * (D / 2) + off * (D / 2) + 256 * sub + 16 * lr);
-      r.v_there = (half ? (tt ? bad[3] : bad[1]) : (tt ? bad[2] : bad[0])) ? 0 : len - key32 - 8 * q;
+      r.v = *(const u32x4*)(rv + (off_v + base * (D / 2)));
+      r.v_there = bad_v ? 0 : len - 64 * t - key_v;
+      const uint8_t* vz = rv + (off_vz + 4 * base);
 #pragma unroll
-      for (int g = 0; g < R::GH; ++g) {
-        // the groups of channels 64 sub .. 64 sub + 63
-        const int gg = (64 * sub + 32 * g) / GS;
+      for (int g = 0; g < R::GH; ++g)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          r.vz[g][i] = *(const u32x4*)(p + P * D + 4 * (P * (X::G + gg) + off) + 16 * i);
-      }
+        for (int i = 0; i < 2; ++i) r.vz[g][i] = *(const u32x4*)(vz + 4 * P * g + 16 * i);
     }
+    const uint8_t* pp = rp + (off_p + 4 * base);
 #pragma unroll
     for (int k = 0; k < R::PW; ++k) {
       const int pg = wave + kWaves * k;  // side and group
-      if (pg < 2 * X::G) {
-        const int i = lane >> 4;
-        const uint8_t* p = i & 2 ? (i & 1 ? rec[3] : rec[2]) : (i & 1 ? rec[1] : rec[0]);
-        const int dead = i & 2 ? (i & 1 ? bad[3] : bad[2]) : (i & 1 ? bad[1] : bad[0]);
-        r.par[k] = *(const uint32_t*)(p + P * D + 4 * (P * pg + ((64 * t + lane) & (P - 1))));
-        r.par_ok = 64 * t + lane < len && !dead;
-      }
+      if (pg < 2 * X::G) r.par[k] = *(const uint32_t*)(pp + 4 * P * pg);
     }
-    return bad[0] | bad[1] << 1 | bad[2] << 2 | bad[3] << 3;
+    r.dead = __ballot(bad_p);
   };
-  // 16 + c minus 16 + z, exact in fp16
-  auto sub2 = [&](uint32_t code, uint32_t zero) -> uint32_t {
-    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, code) - __builtin_bit_cast(half2v, zero));
-  };
-  auto plus16 = [&](uint32_t zz) -> uint32_t {
-    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, zz) + __builtin_bit_cast(half2v, kOffset));
-  };
-  // parameters of keys that do not exist may hold anything: they become zero
-  auto decode = [&](const R& r, uint8_t* buf) {
+  // Keys that do not exist may hold anything.  Their scores are replaced later, whatever they
+  // are; their value zeros and steps become zero here.
+  auto decode = [&](R& r, int t, uint8_t* buf) -> uint64_t {
+    if (r.dead || 64 * t + 64 > len) {
+      if (sub < X::H) {
+#pragma unroll
+        for (int g = 0; g < R::GH; ++g)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) r.vz[g][e >> 2][e & 3] = e < r.v_there ? r.vz[g][e >> 2][e & 3] : 0u;
+      }
+      const bool ok = 64 * t + lane < len && !(r.dead >> lane & 1);
+#pragma unroll
+      for (int k = 0; k < R::PW; ++k) r.par[k] = ok ? r.par[k] : 0u;
+    }
 #pragma unroll
     for (int w = 0; w < X::KW; ++w) {
-      const uint32_t par = r.k_ok ? r.kz[w / X::WPG] : 0u;
-      const uint32_t z = plus16(__builtin_amdgcn_perm(par, par, 0x03020302u));
-      const u32x4 o = {sub2(code_pair<0>(r.k[w], cc), z), sub2(code_pair<1>(r.k[w], cc), z),
-                       sub2(code_pair<2>(r.k[w], cc), z), sub2(code_pair<3>(r.k[w], cc), z)};
+      const uint32_t par = r.kz[w / X::WPG], zz = __builtin_amdgcn_perm(par, par, 0x03020302u);
+      const uint32_t z0 = pk_add16(zz, cc.offset[0]), z1 = pk_add16(zz, cc.offset[1]);
+      const u32x4 o = {centred_pair<0>(r.k[w], z0, z1, cc), centred_pair<1>(r.k[w], z0, z1, cc),
+                       centred_pair<2>(r.k[w], z0, z1, cc), centred_pair<3>(r.k[w], z0, z1, cc)};
       *(u32x4*)(buf + ((tt * 2 + sub) * X::KW + w) * 1024 + 16 * lane) = o;
     }
     if (sub < X::H) {
-      uint32_t z[R::GH][4];
+      uint32_t z0[R::GH][4], z1[R::GH][4];
 #pragma unroll
       for (int g = 0; g < R::GH; ++g)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t pa = 2 * i < r.v_there ? r.vz[g][i >> 1][2 * (i & 1)] : 0u;
-          const uint32_t pb = 2 * i + 1 < r.v_there ? r.vz[g][i >> 1][2 * (i & 1) + 1] : 0u;
-          z[g][i] = plus16(__builtin_amdgcn_perm(pb, pa, 0x07060302u));
+          const uint32_t zz = __builtin_amdgcn_perm(r.vz[g][i >> 1][2 * (i & 1) + 1],
+                                                    r.vz[g][i >> 1][2 * (i & 1)], 0x07060302u);
+          z0[g][i] = pk_add16(zz, cc.offset[0]);
+          z1[g][i] = pk_add16(zz, cc.offset[1]);
         }
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
+        const int g = R::GH == 2 ? n >> 1 : 0;
         u32x4 o;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t w = r.v[i];
-          const uint32_t cp = n == 0 ? code_pair<0>(w, cc) : n == 1 ? code_pair<1>(w, cc)
-                              : n == 2 ? code_pair<2>(w, cc) : code_pair<3>(w, cc);
-          o[i] = sub2(cp, z[R::GH == 2 ? n >> 1 : 0][i]);
+          o[i] = n == 0   ? centred_pair<0>(w, z0[g][i], z1[g][i], cc)
+                 : n == 1 ? centred_pair<1>(w, z0[g][i], z1[g][i], cc)
+                 : n == 2 ? centred_pair<2>(w, z0[g][i], z1[g][i], cc)
+                          : centred_pair<3>(w, z0[g][i], z1[g][i], cc);
         }
         *(u32x4*)(buf + W::K_BYTES + (tt * X::N + 4 * sub + n) * 1024 + 16 * lane) = o;
       }
@@ -860,12 +903,13 @@ void k_kv4_attention_wide(Kv4Cache c, Kv4Query a, Partials part) {
 #pragma unroll
     for (int k = 0; k < R::PW; ++k) {
       const int pg = wave + kWaves * k;
-      if (pg < 2 * X::G) *(uint32_t*)(buf + W::K_BYTES + W::V_BYTES + 256 * pg + 4 * lane) = r.par_ok ? r.par[k] : 0u;
+      if (pg < 2 * X::G) *(uint32_t*)(buf + W::K_BYTES + W::V_BYTES + 256 * pg + 4 * lane) = r.par[k];
     }
+    return r.dead;
   };
 
   WeightScale ws;
-  auto compute = [&](const uint8_t* buf, int t, int dead) {
+  auto compute = [&](const uint8_t* buf, int t, uint64_t dead) {
     const int key0 = 64 * t;
     if (key0 > last || key0 + 63 < first - lo_off || last < 0) return;  // nothing for this wave
     const bool whole = !dead && key0 + 64 <= len && key0 + 63 <= first && key0 >= last - lo_off;
@@ -920,7 +964,7 @@ void k_kv4_attention_wide(Kv4Cache c, Kv4Query a, Partials part) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const int at = e < 8 ? e : e + 24;  // key at + 8 q of the step
-          const bool ok = at <= hi && at >= lo && !((dead >> (2 * (e >> 3) + (q >> 1))) & 1);
+          const bool ok = at <= hi && at >= lo && !(dead >> (32 * (e >> 3) + 8 * q) & 1);
           s[n][e] = ok ? s[n][e] : kNegInf;
           seen[n] |= ok ? 1u << e : 0u;
         }
@@ -1031,19 +1075,19 @@ void k_kv4_attention_wide(Kv4Cache c, Kv4Query a, Partials part) {
   if (t_lo < t_hi) {
     R r;
     look_up(t_lo);
-    int dead0 = fetch(r, t_lo), dead1 = 0;
-    decode(r, buf0);
+    fetch(r, t_lo);
+    uint64_t dead = decode(r, t_lo, buf0);
     __syncthreads();
     for (int t = t_lo; t < t_hi; t += 2) {
-      if (t + 1 < t_hi) dead1 = fetch(r, t + 1);
-      compute(buf0, t, dead0);
+      if (t + 1 < t_hi) fetch(r, t + 1);
+      compute(buf0, t, dead);
       if (t + 1 >= t_hi) break;
-      decode(r, buf1);
+      dead = decode(r, t + 1, buf1);
       __syncthreads();
-      if (t + 2 < t_hi) dead0 = fetch(r, t + 2);
-      compute(buf1, t + 1, dead1);
+      if (t + 2 < t_hi) fetch(r, t + 2);
+      compute(buf1, t + 1, dead);
       if (t + 2 >= t_hi) break;
-      decode(r, buf0);
+      dead = decode(r, t + 2, buf0);
       __syncthreads();
     }
   }
@@ -1154,7 +1198,10 @@ hipError_t launch_join(const Kv4Cache& c, const Kv4Query& q, const Partials& par
 template <int D, int GS>
 hipError_t launch_dg(const Kv4Cache& c, const Kv4Query& q, const Kv4Plan& p, const Partials& part,
                      hipStream_t stream) {
-  const dim3 grid((unsigned)p.tiles, (unsigned)(c.kv_heads * p.splits), (unsigned)c.n_seqs);
+  const int64_t blocks = (int64_t)p.tiles * p.splits * c.kv_heads * c.n_seqs;
+  constexpr int64_t kRow = 1 << 20;  // a dimension of a grid holds less than 2^32 threads
+  if (blocks > 0x7fffffff - kRow) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)(blocks < kRow ? blocks : kRow), (unsigned)((blocks + kRow - 1) / kRow));
   if (p.wide)
     hipLaunchKernelGGL((k_kv4_attention_wide<D, GS>), grid, dim3(64 * kWaves), 0, stream, c, q, part);
   else if (p.waves == 8)
@@ -1174,11 +1221,8 @@ Kv4Plan kv4_plan(int64_t n_seqs, int heads, int kv_heads, int dim, int group, in
   const int64_t per = p.wide ? 16 * wide_tiles(dim, group) * kWaves : 16;
   p.tiles = (int)((cols + per - 1) / per);
   const int64_t blocks = n_seqs * kv_heads * p.tiles;
-  // four blocks a compute unit, at least 256 keys a split
-#ifndef KV4_T
-#define KV4_T 1024
-#endif
-  int64_t s = (KV4_T + blocks - 1) / blocks;
+  // four blocks a compute unit, two of the wide form's, at least 256 keys a split
+  int64_t s = ((p.wide ? 512 : 1024) + blocks - 1) / blocks;
   const int64_t most = (max_len + 255) / 256;
   if (s > most) s = most;
   if (kv_heads * s > 65535) s = 65535 / kv_heads;
@@ -1203,6 +1247,7 @@ hipError_t launch_kv4_attention(const Kv4Cache& c, const Kv4Query& q, const Kv4P
   if (rows <= 0 || c.n_seqs <= 0) return hipSuccess;
   Partials part;
   part.splits = p.splits;
+  part.tiles = p.tiles;
   part.o = (float*)workspace;
   part.ml = part.o + rows * p.splits * c.dim;
   hipError_t e;

@@ -137,19 +137,15 @@ __device__ __forceinline__ Rows<D> rows_of(const Kv4Cache& c, int blk, int n_tok
 template <int D>
 __device__ __forceinline__ int value_word_row(int w) { return (w / D) * 8 + 2 * (w & 3); }
 
-// HPB heads a block: finding the sequence, the rows and the page takes a few dependent loads,
-// which one head's work does not hide (prompts of 8191 tokens, 8 heads: HEADS_1 us with one head a
-// block, HEADS_4 with four).
-template <bool BF16, int D, int GS, int HPB, bool ZP>
+template <bool BF16, int D, int GS, bool ZP>
 __global__ __launch_bounds__(256) void k_kv4_append(Kv4Cache c, const uint16_t* __restrict__ k,
                                                     int64_t kt, int64_t kh,
                                                     const uint16_t* __restrict__ v, int64_t vt,
                                                     int64_t vh, int n_tokens) {
   constexpr int LPR = D / 8, G = D / GS, R = Rows<D>::R;
-  __shared__ uint32_t vwords[HPB][R][LPR + 1];
-  __shared__ int64_t page_at[R];  // each row's page, as its offset for head 0, or -1
-  const int per = (c.kv_heads + HPB - 1) / HPB;
-  const int group = blockIdx.x / per, head0 = (blockIdx.x - group * per) * HPB;
+  __shared__ uint32_t vwords[R][LPR + 1];
+  __shared__ int64_t page_at[R];  // each row's record, or -1
+  const int group = blockIdx.x / c.kv_heads, head = blockIdx.x - group * c.kv_heads;
   const Rows<D> rows = rows_of<D>(c, group, n_tokens);
   if (rows.seq < 0 || rows.t0 >= rows.end || rows.t0 + R <= rows.first) return;  // the whole block
   const int row = threadIdx.x / LPR, l = threadIdx.x % LPR;
@@ -157,27 +153,21 @@ __global__ __launch_bounds__(256) void k_kv4_append(Kv4Cache c, const uint16_t* 
   {
     const int t = rows.t0 + row, pos = rows.pos0 + row;
     const bool in = t >= rows.first && t < rows.end;
-    uint4 xk[HPB], xv[HPB];
-#pragma unroll
-    for (int i = 0; i < HPB; ++i) {  // asked for before the table's answer is waited for
-      xk[i] = xv[i] = uint4{0u, 0u, 0u, 0u};
-      if (in && head0 + i < c.kv_heads) {
-        xk[i] = *(const uint4*)(k + t * kt + (head0 + i) * kh + 8 * l);
-        xv[i] = *(const uint4*)(v + t * vt + (head0 + i) * vh + 8 * l);
-      }
+    uint4 xk = {0u, 0u, 0u, 0u}, xv = xk;
+    if (in) {  // asked for before the table's answer is waited for
+      xk = *(const uint4*)(k + t * kt + head * kh + 8 * l);
+      xv = *(const uint4*)(v + t * vt + head * vh + 8 * l);
     }
-    const int64_t at = in ? kv4_record_at(c, rows.seq, pos, 0) : -1;
+    const int64_t at = in ? kv4_record_at(c, rows.seq, pos, head) : -1;
     if (l == 0) page_at[row] = at;
-    const int p = pos & (P - 1);
-    const int j = 8 * l / GS, ing = 8 * l % GS;
-    const int q = ing / (GS / 4), u = ing % (GS / 4) / 8;
-#pragma unroll
-    for (int i = 0; i < HPB; ++i) {
-      if (at < 0 || head0 + i >= c.kv_heads) break;  // the lanes of a row alike
-      uint8_t* rec = c.pages + at + (int64_t)(head0 + i) * c.record;
+    if (at >= 0) {  // the lanes of a row alike
+      const int p = pos & (P - 1);
+      const int j = 8 * l / GS, ing = 8 * l % GS;
+      const int q = ing / (GS / 4), u = ing % (GS / 4) / 8;
+      uint8_t* rec = c.pages + at;
       uint32_t kp, vp;
-      const uint32_t kw = quantise_group<BF16, GS / 8, ZP>(xk[i], kp);
-      vwords[i][row][l] = quantise_group<BF16, GS / 8, ZP>(xv[i], vp);
+      const uint32_t kw = quantise_group<BF16, GS / 8, ZP>(xk, kp);
+      vwords[row][l] = quantise_group<BF16, GS / 8, ZP>(xv, vp);
       // keys: the lane's 8 channels are one word
       *(uint32_t*)(rec + p * (D / 2) + q * (D / 8) + j * (GS / 8) + u * 4) = kw;
       if (ing == 0) {
@@ -195,22 +185,17 @@ __global__ __launch_bounds__(256) void k_kv4_append(Kv4Cache c, const uint16_t* 
     const int r0 = value_word_row<D>(w), h = w % D / 64, r = w % 64 / 4;
     const int64_t at0 = page_at[r0], at1 = page_at[r0 + 1];
     if (at0 < 0 && at1 < 0) continue;
-    const int64_t at = (at0 < 0 ? at1 : at0) + P * (D / 2) +
-                       (((rows.pos0 + r0) & (P - 1)) >> 3) * (D * 4) + (w % D) * 4;
+    uint32_t word = 0;
 #pragma unroll
-    for (int i = 0; i < HPB; ++i) {
-      if (head0 + i >= c.kv_heads) break;
-      uint32_t word = 0;
+    for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-          word |= ((vwords[i][r0 + e][2 * (4 * h + n) + (r >> 3)] >> (4 * (r & 7))) & 15u) << (16 * e + 4 * n);
-      uint8_t* dst = c.pages + at + (int64_t)(head0 + i) * c.record;
-      if (at0 >= 0 && at1 >= 0) *(uint32_t*)dst = word;
-      else if (at0 >= 0) *(uint16_t*)dst = (uint16_t)word;
-      else *(uint16_t*)(dst + 2) = (uint16_t)(word >> 16);
-    }
+      for (int n = 0; n < 4; ++n)
+        word |= ((vwords[r0 + e][2 * (4 * h + n) + (r >> 3)] >> (4 * (r & 7))) & 15u) << (16 * e + 4 * n);
+    uint8_t* dst = c.pages + (at0 < 0 ? at1 : at0) + P * (D / 2) +
+                   (((rows.pos0 + r0) & (P - 1)) >> 3) * (D * 4) + (w % D) * 4;
+    if (at0 >= 0 && at1 >= 0) *(uint32_t*)dst = word;
+    else if (at0 >= 0) *(uint16_t*)dst = (uint16_t)word;
+    else *(uint16_t*)(dst + 2) = (uint16_t)(word >> 16);
   }
 }
 
@@ -282,22 +267,16 @@ hipError_t launch_kv4_append(const Kv4Cache& c, const void* k, int64_t kt, int64
                              const void* v, int64_t vt, int64_t vh, int64_t n_tokens, bool bf16,
                              hipStream_t stream) {
   if (n_tokens <= 0) return hipSuccess;
-  const int64_t groups = n_tokens / (2048 / c.dim) + 2 * c.n_seqs + 1;
-  const bool four = groups * c.kv_heads >= 8192;  // four blocks a compute unit with four heads each
-  const int64_t blocks = groups * (four ? (c.kv_heads + 3) / 4 : c.kv_heads);
+  const int64_t blocks = (n_tokens / (2048 / c.dim) + 2 * c.n_seqs + 1) * c.kv_heads;
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-#define AWQ_APPEND_Z(B, D, GS, H, Z)                                                              \
-  hipLaunchKernelGGL((k_kv4_append<B, D, GS, H, Z>), dim3((unsigned)blocks), dim3(256), 0, stream, c, \
+#define AWQ_APPEND_Z(B, D, GS, Z)                                                              \
+  hipLaunchKernelGGL((k_kv4_append<B, D, GS, Z>), dim3((unsigned)blocks), dim3(256), 0, stream, c, \
                      (const uint16_t*)k, kt, kh, (const uint16_t*)v, vt, vh, (int)n_tokens)
-#define AWQ_APPEND_H(B, D, GS, H)                         \
-  if (c.zero_point) AWQ_APPEND_Z(B, D, GS, H, true);      \
-  else AWQ_APPEND_Z(B, D, GS, H, false)
-#define AWQ_APPEND(B, D, GS)           \
-  if (four) { AWQ_APPEND_H(B, D, GS, 4); } \
-  else { AWQ_APPEND_H(B, D, GS, 1); }
+#define AWQ_APPEND(B, D, GS)                              \
+  if (c.zero_point) { AWQ_APPEND_Z(B, D, GS, true); }     \
+  else { AWQ_APPEND_Z(B, D, GS, false); }
   if (bf16) { AWQ_KV4_DG(AWQ_APPEND, true) } else { AWQ_KV4_DG(AWQ_APPEND, false) }
 #undef AWQ_APPEND
-#undef AWQ_APPEND_H
 #undef AWQ_APPEND_Z
   return hipGetLastError();
 }
