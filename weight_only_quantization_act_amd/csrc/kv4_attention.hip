@@ -1124,74 +1124,75 @@ void k_kv4_attention_wide(Kv4Cache c, Kv4Query a, Partials part) {
   }
 }
 
-// Joins the splits of one (token, head): RW waves a row, wave w adds splits w, w + RW, ... in
-// order, the waves in order.
-template <int D, int RW>
+// Joins the splits of a (token, head): D / 4 threads a row and part, part w adds splits w,
+// w + PARTS, ... in order, then the parts are added in order.
+template <int D, int PARTS>
 __global__ __launch_bounds__(256) void k_kv4_join(Kv4Cache c, Kv4Query a, Partials part,
                                                   int64_t n_rows) {
-  constexpr int PER = D / 64;  // channels a lane
-  typedef float fvec __attribute__((ext_vector_type(PER)));
-  __shared__ float so[4][D], sl[4];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t r = (int64_t)blockIdx.x * (4 / RW) + wave / RW;
-  const int w = wave % RW, S = part.splits;
-  bool there = r < n_rows;
-  if (there) {  // a row past a sequence's bound has no partials
-    const int64_t t = r / a.heads;
-    const int b = kv4_sequence(c, t);
-    there = b >= 0 && t - c.starts[b] < a.max_q;
-  }
+  constexpr int T = D / 4, ROWS = 256 / (T * PARTS);
+  __shared__ f32x4 so[PARTS > 1 ? PARTS : 1][T];
+  __shared__ float sm[PARTS], sl[PARTS];
+  const int x = threadIdx.x % T, w = threadIdx.x / T % PARTS, S = part.splits;
+  const int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / (T * PARTS);
+  if (ROWS > 1 && r >= n_rows) return;
+  // read before it is known whether the row has partials (what is read is workspace either way)
+  const float2* ml = (const float2*)part.ml + r * S;
+  const float* po = part.o + r * S * D + 4 * x;
   float M = kNegInf, l = 0.0f;
-  fvec o;
+#pragma unroll 4
+  for (int s = w; s < S; s += PARTS) M = fmaxf(M, ml[s].x);
+  f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = w; s < S; s += PARTS) {
+    const float2 y = ml[s];
+    const f32x4 v = *(const f32x4*)(po + (int64_t)s * D);
+    const float k = y.x == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(y.x - M);
+    l = fmaf(y.y, k, l);
 #pragma unroll
-  for (int e = 0; e < PER; ++e) o[e] = 0.0f;
-  if (there) {
-    const float* ml = part.ml + r * S * 2;
-    for (int s = lane; s < S; s += 64) M = fmaxf(M, ml[2 * s]);
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off));
-    const float* po = part.o + r * S * D + lane * PER;
-#pragma unroll 8
-    for (int s = w; s < S; s += RW) {
-      const float2 x = *(const float2*)(ml + 2 * s);
-      const fvec v = *(const fvec*)(po + (int64_t)s * D);
-      const float k = x.x == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(x.x - M);
-      l = fmaf(x.y, k, l);
-#pragma unroll
-      for (int e = 0; e < PER; ++e) o[e] = fmaf(v[e], k, o[e]);
-    }
+    for (int e = 0; e < 4; ++e) o[e] = fmaf(v[e], k, o[e]);
   }
-  if constexpr (RW > 1) {
-    if (w > 0) {
-      *(fvec*)&so[wave][lane * PER] = o;
-      if (lane == 0) sl[wave] = l;
+  if constexpr (PARTS > 1) {
+    so[w][x] = o;
+    if (x == 0) {
+      sm[w] = M;
+      sl[w] = l;
     }
     __syncthreads();
     if (w > 0) return;
+    float all = M;
 #pragma unroll
-    for (int i = 1; i < RW; ++i) {
-      l += sl[wave + i];
-      const fvec v = *(const fvec*)&so[wave + i][lane * PER];
+    for (int i = 1; i < PARTS; ++i) all = fmaxf(all, sm[i]);
+    l = 0.0f;
+    o = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int e = 0; e < PER; ++e) o[e] += v[e];
+    for (int i = 0; i < PARTS; ++i) {
+      const float k = sm[i] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(sm[i] - all);
+      l = fmaf(sl[i], k, l);
+      const f32x4 v = so[i][x];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = fmaf(v[e], k, o[e]);
     }
+    M = all;
   }
-  if (!there) return;
+  // a row past a sequence's bound has no partials
+  const int64_t t = r / a.heads;
+  const int b = kv4_sequence(c, t);
+  if (b < 0 || t - c.starts[b] >= a.max_q) return;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  uint16_t* out = (uint16_t*)a.out + r * D + lane * PER;
-#pragma unroll
-  for (int e = 0; e < PER; ++e) out[e] = a.bf16 ? to16<true>(o[e] * inv) : to16<false>(o[e] * inv);
-  if (lane == 0 && a.lse) a.lse[r] = lse_of(M, l);
+  const float v[4] = {o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
+  store4(a.out, r * D + 4 * x, a.bf16, v);
+  if (x == 0 && a.lse) a.lse[r] = lse_of(M, l);
 }
 
 template <int D>
 hipError_t launch_join(const Kv4Cache& c, const Kv4Query& q, const Partials& part, int64_t rows,
                        hipStream_t stream) {
+  constexpr int kParts = 1024 / D, kRows = 1024 / D;
   if (part.splits >= 16)
-    hipLaunchKernelGGL((k_kv4_join<D, 4>), dim3((unsigned)rows), dim3(256), 0, stream, c, q, part, rows);
+    hipLaunchKernelGGL((k_kv4_join<D, kParts>), dim3((unsigned)rows), dim3(256), 0, stream, c, q, part, rows);
   else
-    hipLaunchKernelGGL((k_kv4_join<D, 1>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, c, q,
-                       part, rows);
+    hipLaunchKernelGGL((k_kv4_join<D, 1>), dim3((unsigned)((rows + kRows - 1) / kRows)), dim3(256), 0,
+                       stream, c, q, part, rows);
   return hipGetLastError();
 }
 
