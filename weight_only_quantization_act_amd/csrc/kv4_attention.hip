@@ -35,6 +35,8 @@
 // columns (prompts): each wave keeps NC column tiles and walks all keys itself.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "int8_quant.h"
 #include "kv4_cache.h"
 #include "mfma_dma.h"
@@ -231,23 +233,38 @@ struct Column {
   __device__ float M() const { return m == kNegInf ? kNegInf : -nM; }
 };
 
-// One row of q as operands: scaled by a power of two so that its largest magnitude lies in
+// The lane's part of one row of q, in word order (zeros without a row).
+template <int D, int GS>
+struct QueryRow {
+  uint4 w[Geo<D, GS>::KW];
+};
+template <int D, int GS>
+__device__ __forceinline__ QueryRow<D, GS> read_query(const uint16_t* row, int q) {
+  using X = Geo<D, GS>;
+  QueryRow<D, GS> r;
+#pragma unroll
+  for (int w = 0; w < X::KW; ++w) {
+    r.w[w] = uint4{0u, 0u, 0u, 0u};
+    if (row) r.w[w] = *(const uint4*)(row + (w / X::WPG) * GS + q * (GS / 4) + (w % X::WPG) * 8);
+  }
+  return r;
+}
+
+// A row of q as operands: scaled by a power of two so that its largest magnitude lies in
 // [2^8, 2^9), then rounded to fp16 (exact but for what lies 2^-24 and more below the largest).
 template <int D, int GS>
-__device__ __forceinline__ void load_query(Column<D, GS>& c, const uint16_t* row, bool bf16,
-                                           int q, float scale) {
+__device__ __forceinline__ void set_query(Column<D, GS>& c, const QueryRow<D, GS>& row, bool bf16,
+                                          float scale) {
   using X = Geo<D, GS>;
   float v[X::KW][8];
   float top = 0.0f;
 #pragma unroll
   for (int w = 0; w < X::KW; ++w) {
-    const int c0 = (w / X::WPG) * GS + q * (GS / 4) + (w % X::WPG) * 8;
-    if (row) {
-      if (bf16) load_row8<true, true>(row, nullptr, kFoldNone, c0, D, v[w]);
-      else load_row8<false, true>(row, nullptr, kFoldNone, c0, D, v[w]);
-    } else {
+    const uint32_t r[4] = {row.w[w].x, row.w[w].y, row.w[w].z, row.w[w].w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[w][i] = 0.0f;
+    for (int i = 0; i < 4; ++i) {
+      v[w][2 * i] = bf16 ? from16<true>(r[i] & 0xffffu) : from16<false>(r[i] & 0xffffu);
+      v[w][2 * i + 1] = bf16 ? from16<true>(r[i] >> 16) : from16<false>(r[i] >> 16);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[w][i]));
@@ -302,11 +319,11 @@ struct WeightScale {
   uint32_t limit = 0;
 };
 
-// One tile of 32 keys for NC column tiles.  !whole (the same in every lane): some (key, column)
+// One tile of 32 keys.  !whole (the same in every lane): some (key, column)
 // pairs do not exist; key0 is the tile's first key, lo_off = window - 1 (or a huge number) so that column pos sees
 // keys [pos - lo_off, pos]; dead: bit x set if the keys of half x lie on no page.
-template <int D, int GS, int NC>
-__device__ __forceinline__ void do_tile(TileRegs<D, GS>& r, Column<D, GS> (&col)[NC], bool whole,
+template <int D, int GS>
+__device__ __forceinline__ void do_tile(TileRegs<D, GS>& r, Column<D, GS>& c, bool whole,
                                         int key0, int n_keys, int lo_off, int dead, WeightScale& ws,
                                         const CodeConsts& cc, int lane) {
   using X = Geo<D, GS>;
@@ -337,110 +354,104 @@ __device__ __forceinline__ void do_tile(TileRegs<D, GS>& r, Column<D, GS> (&col)
     }
   const uint32_t top = tp[0];
 
+  float s[8];
 #pragma unroll
-  for (int t = 0; t < NC; ++t) {
-    Column<D, GS>& c = col[t];
-    float s[8];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-#pragma unroll
-      for (int g = 0; g < X::G; ++g) {
-        f32x4 a = c.c16[g];
-#pragma unroll
-        for (int u = 0; u < X::WPG; ++u)
-          a = __builtin_amdgcn_mfma_f32_16x16x32_f16(word_operand(r.k[j][g * X::WPG + u], cc),
-                                                     c.q[g * X::WPG + u], a, 0, 0, 0);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t w = r.kp[g][j][e];
-          const float x = fmaf(-hi16(w), c.qsum[g], a[e]);
-          s[4 * j + e] = fmaf(lo16(w), x, g == 0 ? 0.0f : s[4 * j + e]);
-        }
-      }
-    }
-    uint32_t seen = 0xff;  // bit e: key 8 q + e exists for the column
-    if (!whole) {
-      seen = 0;
-      int last = min(there - 1, c.pos - kq), fst = c.pos - lo_off - kq;
-      asm volatile("" : "+v"(last), "+v"(fst));
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const bool ok = e <= last && e >= fst;
-        s[e] = ok ? s[e] : kNegInf;
-        seen |= ok ? 1u << e : 0u;
-      }
-    }
-    float mx = s[0];
-#pragma unroll
-    for (int e = 1; e < 8; ++e) mx = fmaxf(mx, s[e]);
-    mx *= c.sigma;
-    // seldom: a score above the column's maximum, or a value step above what the weights' scale
-    // was made for
-    if (__any(mx > c.m + kSlack || top >= ws.limit)) {
-      if (t == 0) {
-        uint32_t all = top;
-        all = max(all, (uint32_t)__shfl_xor((int)all, 16));
-        all = max(all, (uint32_t)__shfl_xor((int)all, 32));
-        // zero and subnormal steps count as the smallest normal one, others as finite
-        const uint32_t ex = min(max(all, 0x0400u), 0x7bffu) >> 10;
-        ws.limit = max(ws.limit, (ex + 1) << 10);
-        ws.f = fminf(ws.f, 14.0f - kSlack + 15.0f - (float)ex);
-      }
-      const float m = fmaxf(c.m, max_q(mx));
-      const float nM = m == kNegInf ? 0.0f : ws.f - m;
-      const float a = c.m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(nM - c.nM);
-      c.m = m;
-      c.nM = nM;
-      c.l *= a;
-#pragma unroll
-      for (int g = 0; g < X::G; ++g)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) c.z[g][e] *= a;
-#pragma unroll
-      for (int n = 0; n < X::N; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) c.o[n][e] *= a;
-    }
-    float p[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      p[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c.sigma, c.nM));
-      c.l += p[e];
-    }
+  for (int j = 0; j < 2; ++j) {
 #pragma unroll
     for (int g = 0; g < X::G; ++g) {
-      u32x4 w, zo;
+      f32x4 a = c.c16[g];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t pa = r.vp[g][i >> 1][2 * (i & 1)], pb = r.vp[g][i >> 1][2 * (i & 1) + 1];
-        w[i] = pair16(fmaf(p[2 * i], lo16(pa), 0.0f), fmaf(p[2 * i + 1], lo16(pb), 0.0f));
-        // zeros + 16, exact in fp16
-        zo[i] = __builtin_bit_cast(
-            uint32_t, __builtin_bit_cast(half2v, __builtin_amdgcn_perm(pb, pa, 0x07060302u)) +
-                          __builtin_bit_cast(half2v, kOffset));
+      for (int u = 0; u < X::WPG; ++u)
+        a = __builtin_amdgcn_mfma_f32_16x16x32_f16(word_operand(r.k[j][g * X::WPG + u], cc),
+                                                   c.q[g * X::WPG + u], a, 0, 0, 0);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t w = r.kp[g][j][e];
+        const float x = fmaf(-hi16(w), c.qsum[g], a[e]);
+        s[4 * j + e] = fmaf(lo16(w), x, g == 0 ? 0.0f : s[4 * j + e]);
       }
-      if (!whole) {  // a masked key's step may be NaN
+    }
+  }
+  uint32_t seen = 0xff;  // bit e: key 8 q + e exists for the column
+  if (!whole) {
+    seen = 0;
+    int last = min(there - 1, c.pos - kq), fst = c.pos - lo_off - kq;
+    asm volatile("" : "+v"(last), "+v"(fst));
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] &= (seen >> (2 * i) & 1 ? 0xffffu : 0u) | (seen >> (2 * i + 1) & 1 ? 0xffff0000u : 0u);
-      }
-      // the zeros' sum by the same instruction as the codes' (an operand whose 16 rows are
-      // equal), so that what the two sums share cancels as it was rounded
-      c.z[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8v, zo),
-                                                      __builtin_bit_cast(half8v, w), c.z[g], 0, 0, 0);
+    for (int e = 0; e < 8; ++e) {
+      const bool ok = e <= last && e >= fst;
+      s[e] = ok ? s[e] : kNegInf;
+      seen |= ok ? 1u << e : 0u;
+    }
+  }
+  float mx = s[0];
 #pragma unroll
-      for (int n = g * (GS / 16); n < (g + 1) * (GS / 16); ++n) {
-        const u32x4 vw = r.v[n >> 2];
-        u32x4 a;
+  for (int e = 1; e < 8; ++e) mx = fmaxf(mx, s[e]);
+  mx *= c.sigma;
+  // seldom: a score above the column's maximum, or a value step above what the weights' scale
+  // was made for
+  if (__any(mx > c.m + kSlack || top >= ws.limit)) {
+    uint32_t all = top;
+    all = max(all, (uint32_t)__shfl_xor((int)all, 16));
+    all = max(all, (uint32_t)__shfl_xor((int)all, 32));
+    // zero and subnormal steps count as the smallest normal one, others as finite
+    const uint32_t ex = min(max(all, 0x0400u), 0x7bffu) >> 10;
+    ws.limit = max(ws.limit, (ex + 1) << 10);
+    ws.f = fminf(ws.f, 14.0f - kSlack + 15.0f - (float)ex);
+    const float m = fmaxf(c.m, max_q(mx));
+    const float nM = m == kNegInf ? 0.0f : ws.f - m;
+    const float a = c.m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(nM - c.nM);
+    c.m = m;
+    c.nM = nM;
+    c.l *= a;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          a[i] = (n & 3) == 0   ? code_pair<0>(vw[i], cc)
-                 : (n & 3) == 1 ? code_pair<1>(vw[i], cc)
-                 : (n & 3) == 2 ? code_pair<2>(vw[i], cc)
-                                : code_pair<3>(vw[i], cc);
-        c.o[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8v, a),
-                                                       __builtin_bit_cast(half8v, w), c.o[n], 0, 0, 0);
-      }
+    for (int g = 0; g < X::G; ++g)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c.z[g][e] *= a;
+#pragma unroll
+    for (int n = 0; n < X::N; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c.o[n][e] *= a;
+  }
+  float p[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    p[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c.sigma, c.nM));
+    c.l += p[e];
+  }
+#pragma unroll
+  for (int g = 0; g < X::G; ++g) {
+    u32x4 w, zo;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t pa = r.vp[g][i >> 1][2 * (i & 1)], pb = r.vp[g][i >> 1][2 * (i & 1) + 1];
+      w[i] = pair16(fmaf(p[2 * i], lo16(pa), 0.0f), fmaf(p[2 * i + 1], lo16(pb), 0.0f));
+      // zeros + 16, exact in fp16
+      zo[i] = __builtin_bit_cast(
+          uint32_t, __builtin_bit_cast(half2v, __builtin_amdgcn_perm(pb, pa, 0x07060302u)) +
+                        __builtin_bit_cast(half2v, kOffset));
+    }
+    if (!whole) {  // a masked key's step may be NaN
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] &= (seen >> (2 * i) & 1 ? 0xffffu : 0u) | (seen >> (2 * i + 1) & 1 ? 0xffff0000u : 0u);
+    }
+    // the zeros' sum by the same instruction as the codes' (an operand whose 16 rows are
+    // equal), so that what the two sums share cancels as it was rounded
+    c.z[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8v, zo),
+                                                    __builtin_bit_cast(half8v, w), c.z[g], 0, 0, 0);
+#pragma unroll
+    for (int n = g * (GS / 16); n < (g + 1) * (GS / 16); ++n) {
+      const u32x4 vw = r.v[n >> 2];
+      u32x4 a;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        a[i] = (n & 3) == 0   ? code_pair<0>(vw[i], cc)
+               : (n & 3) == 1 ? code_pair<1>(vw[i], cc)
+               : (n & 3) == 2 ? code_pair<2>(vw[i], cc)
+                              : code_pair<3>(vw[i], cc);
+      c.o[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8v, a),
+                                                     __builtin_bit_cast(half8v, w), c.o[n], 0, 0, 0);
     }
   }
 }
@@ -496,10 +507,10 @@ __device__ __forceinline__ Place place_of(const Kv4Cache& c, const Partials& par
   Place p;
   p.head = n % c.kv_heads;
   n /= c.kv_heads;
-  p.split = n % part.splits;
-  n /= part.splits;
   p.seq = n % c.n_seqs;
-  p.tile = part.tiles - 1 - (int)(n / c.n_seqs);
+  n /= c.n_seqs;
+  p.split = n % part.splits;
+  p.tile = part.tiles - 1 - (int)(n / part.splits);
   return p;
 }
 
@@ -513,7 +524,7 @@ template <int D, int GS, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(waves_per_simd(D, GS)))) void k_kv4_attention(Kv4Cache c, Kv4Query a,
                                                                Partials part) {
   using X = Geo<D, GS>;
-  constexpr int NC = 1, kCols = 16;  // columns a block
+  constexpr int kCols = 16;  // columns a block
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Place at = place_of(c, part);
@@ -530,44 +541,43 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(wave
   const int cap = (int)min((int64_t)c.max_blocks << c.log2p, (int64_t)a.max_len);
   const int len = min(len0, cap);
 
-  Column<D, GS> col[NC];
-  const int col0 = tile * kCols;
-#pragma unroll
-  for (int t = 0; t < NC; ++t) {
-    const int x = col0 + 16 * t + (lane & 15);
-    const int i = x / group, h = x - i * group;
-    const bool has = x < n_cols;
-    const uint16_t* row =
-        has ? (const uint16_t*)a.q + (int64_t)(row0 + i) * a.qt + (int64_t)(kvh * group + h) * a.qh
-            : nullptr;
-    load_query<D, GS>(col[t], row, a.bf16, lane >> 4, a.scale);
-    col[t].pos = has ? len0 - (c.starts[b + 1] - row0) + i : -1;
-  }
   // keys that some column sees
+  const int col0 = tile * kCols;
   const int lo_off = a.window > 0 ? a.window - 1 : 0x3fffffff;
   const int first_i = col0 / group;
-  const int last_i = min(col0 + 16 * NC - 1, n_cols - 1) / group;
+  const int last_i = min(col0 + 15, n_cols - 1) / group;
   const int pos0 = len0 - (c.starts[b + 1] - row0);
   const int end = min(len, pos0 + last_i + 1);  // may be <= 0
   const int begin = max(0, pos0 + first_i - lo_off);
   int t_lo = begin >> 5, t_hi = max(0, end + 31) >> 5;
-  {
-    // this split's share of the tiles
-    const int n = max(0, t_hi - t_lo), s = part.splits;
-    const int lo = t_lo + (int)((int64_t)n * split / s), hi = t_lo + (int)((int64_t)n * (split + 1) / s);
-    t_lo = lo;
-    t_hi = hi;
+  if (part.splits > 1) {
+    // This split's tiles.  All sequences are cut to the same length, that of the longest allowed
+    // over the splits: equal blocks fill the compute units better than equal numbers of them.
+    const int64_t keys = a.window > 0 ? min((int64_t)a.max_len, (int64_t)a.window + 47) : a.max_len;
+    const int n = max(0, t_hi - t_lo), most = c.n_seqs > 1 ? (int)((keys + 31) >> 5) : 0;
+    const int share = (max(n, most) + part.splits - 1) / part.splits;
+    t_lo = min(t_lo + (int)min((int64_t)share * split, (int64_t)n), t_hi);
+    t_hi = min(t_lo + share, t_hi);
+    if (t_lo >= t_hi) {
+      if (threadIdx.x < kCols && col0 + (int)threadIdx.x < n_cols) {
+        const int x = col0 + threadIdx.x, i = x / group;
+        const int64_t r = (int64_t)(row0 + i) * a.heads + kvh * group + (x - i * group);
+        *(float2*)(part.ml + (r * part.splits + split) * 2) = float2{kNegInf, 0.0f};
+      }
+      return;  // the whole block
+    }
   }
+  const int x = col0 + (lane & 15), xi = x / group;
+  const bool has = x < n_cols;
+  const QueryRow<D, GS> query = read_query<D, GS>(
+      has ? (const uint16_t*)a.q + (int64_t)(row0 + xi) * a.qt + (int64_t)(kvh * group + x - xi * group) * a.qh
+          : nullptr,
+      lane >> 4);
   // (the table is not written here: scalar loads)
   const auto* table = (const __attribute__((address_space(4))) int32_t*)(uintptr_t)(
       c.table + (int64_t)b * c.max_blocks);
   const int last_blk = max(0, (len - 1) >> c.log2p);
   const int n_pages = (int)c.n_pages;
-  auto page_of = [&](int key, int& bad) -> const uint8_t* {
-    const int pg = table[min(key >> c.log2p, last_blk)];
-    bad = (unsigned)pg >= (unsigned)n_pages;
-    return c.pages + ((int64_t)(bad ? 0 : pg) * c.kv_heads + kvh) * (int64_t)c.record;
-  };
   WeightScale ws;
   const CodeConsts cc = code_consts();
   using R = Ring<D, GS>;
@@ -583,17 +593,30 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(wave
   // tiles t0, t0 + step, ...: tile i of the wave in stage i mod NS
   const int n_tiles = t_hi > t0 ? (t_hi - t0 + step - 1) / step : 0;
   int dead_of[NS];
+  // the table entries of the next tile to start, read one tile ahead
+  int page_a, page_b;
+  auto look_up = [&](int i) {
+    const int key = 32 * (t0 + i * step);
+    page_a = table[min(key >> c.log2p, last_blk)];
+    page_b = table[min((key + 16) >> c.log2p, last_blk)];
+  };
   auto start = [&](int i, int s) {
     const int key = 32 * (t0 + i * step);
-    int bad_a, bad_b;
-    const uint8_t* ra = page_of(key, bad_a);
-    const uint8_t* rb = page_of(key + 16, bad_b);
+    const int bad_a = (unsigned)page_a >= (unsigned)n_pages, bad_b = (unsigned)page_b >= (unsigned)n_pages;
+    const uint8_t* ra = c.pages + ((int64_t)(bad_a ? 0 : page_a) * c.kv_heads + kvh) * (int64_t)c.record;
+    const uint8_t* rb = c.pages + ((int64_t)(bad_b ? 0 : page_b) * c.kv_heads + kvh) * (int64_t)c.record;
+    look_up(i + 1);
     dead_of[s] = bad_a | (bad_b << 1);
     dma_tile<D, GS>(ring_at + s * R::BYTES, ra, rb, key & (P - 1), P, lo);
   };
+  if (n_tiles > 0) look_up(0);
 #pragma unroll
   for (int s = 0; s < NS; ++s)
     if (s < n_tiles) start(s, s);
+  // the query's arithmetic while the first tiles come in
+  Column<D, GS> col;
+  set_query<D, GS>(col, query, a.bf16, a.scale);
+  col.pos = has ? pos0 + xi : -1;
   for (int i0 = 0; i0 < n_tiles; i0 += NS) {
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
@@ -611,13 +634,12 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(wave
         // every key of the tile exists and every column sees all of it
         const bool whole = !dead && key0 + 32 <= len && key0 + 31 <= pos0 + first_i &&
                            key0 >= pos0 + last_i - lo_off;
-        do_tile<D, GS, NC>(r, col, whole, key0, len, lo_off, dead, ws, cc, lane);
+        do_tile<D, GS>(r, col, whole, key0, len, lo_off, dead, ws, cc, lane);
       }
     }
   }
 
-#pragma unroll
-  for (int t = 0; t < NC; ++t) finish<D, GS>(col[t]);
+  finish<D, GS>(col);
 
   {
     // the waves' results joined in wave order: each scaled to the block's largest M
@@ -625,50 +647,46 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(wave
     float (*sm)[16] = (float (*)[16])(so + WAVES);
     float (*sl)[16] = sm + WAVES;
     __syncthreads();  // the rings are done with
+    const int cx = lane & 15;
 #pragma unroll
-    for (int t = 0; t < NC; ++t) {
-      const int x = lane & 15;
-      if (t > 0) __syncthreads();
+    for (int n = 0; n < X::N; ++n) *(f32x4*)&so[wave][cx][16 * n + 4 * (lane >> 4)] = col.o[n];
+    if ((lane >> 4) == 0) {
+      sm[wave][cx] = col.M();
+      sl[wave][cx] = col.l;
+    }
+    __syncthreads();
+    // thread -> column, 4 channels at a time
+    for (int w = threadIdx.x; w < 16 * (D / 4); w += 64 * WAVES) {
+      const int cx = w / (D / 4), ch = (w % (D / 4)) * 4;
+      const int xx = col0 + cx;
+      if (xx >= n_cols) continue;
+      float M = sm[0][cx];
 #pragma unroll
-      for (int n = 0; n < X::N; ++n) *(f32x4*)&so[wave][x][16 * n + 4 * (lane >> 4)] = col[t].o[n];
-      if ((lane >> 4) == 0) {
-        sm[wave][x] = col[t].M();
-        sl[wave][x] = col[t].l;
+      for (int i = 1; i < WAVES; ++i) M = fmaxf(M, sm[i][cx]);
+      float l = 0.0f;
+      f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < WAVES; ++i) {
+        if (sm[i][cx] == kNegInf) continue;
+        const float k = __builtin_amdgcn_exp2f(sm[i][cx] - M);
+        l = fmaf(sl[i][cx], k, l);
+        const f32x4 v = *(const f32x4*)&so[i][cx][ch];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = fmaf(v[e], k, o[e]);
       }
-      __syncthreads();
-      // thread -> column, 4 channels at a time
-      for (int w = threadIdx.x; w < 16 * (D / 4); w += 64 * WAVES) {
-        const int cx = w / (D / 4), ch = (w % (D / 4)) * 4;
-        const int xx = col0 + 16 * t + cx;
-        if (xx >= n_cols) continue;
-        float M = sm[0][cx];
-#pragma unroll
-        for (int i = 1; i < WAVES; ++i) M = fmaxf(M, sm[i][cx]);
-        float l = 0.0f;
-        f32x4 o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < WAVES; ++i) {
-          if (sm[i][cx] == kNegInf) continue;
-          const float k = __builtin_amdgcn_exp2f(sm[i][cx] - M);
-          l = fmaf(sl[i][cx], k, l);
-          const f32x4 v = *(const f32x4*)&so[i][cx][ch];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[e] = fmaf(v[e], k, o[e]);
+      const int i = xx / group, h = xx - i * group;
+      const int64_t r = (int64_t)(row0 + i) * a.heads + kvh * group + h;
+      if (part.splits > 1) {
+        *(f32x4*)(part.o + (r * part.splits + split) * D + ch) = o;
+        if (ch == 0) {
+          part.ml[(r * part.splits + split) * 2] = M;
+          part.ml[(r * part.splits + split) * 2 + 1] = l;
         }
-        const int i = xx / group, h = xx - i * group;
-        const int64_t r = (int64_t)(row0 + i) * a.heads + kvh * group + h;
-        if (part.splits > 1) {
-          *(f32x4*)(part.o + (r * part.splits + split) * D + ch) = o;
-          if (ch == 0) {
-            part.ml[(r * part.splits + split) * 2] = M;
-            part.ml[(r * part.splits + split) * 2 + 1] = l;
-          }
-        } else {
-          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-          const float v[4] = {o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
-          store4(a.out, r * D + ch, a.bf16, v);
-          if (ch == 0 && a.lse) a.lse[r] = lse_of(M, l);
-        }
+      } else {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const float v[4] = {o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
+        store4(a.out, r * D + ch, a.bf16, v);
+        if (ch == 0 && a.lse) a.lse[r] = lse_of(M, l);
       }
     }
   }
@@ -773,7 +791,7 @@ void k_kv4_attention_wide(Kv4Cache c, Kv4Query a, Partials part) {
     const uint16_t* row =
         has ? (const uint16_t*)a.q + (int64_t)(row0 + i) * a.qt + (int64_t)(kvh * group + h) * a.qh
             : nullptr;
-    load_query<D, GS>(col[t], row, a.bf16, q, a.scale);
+    set_query<D, GS>(col[t], read_query<D, GS>(row, q), a.bf16, a.scale);
     col[t].pos = has ? pos0 + i : -1;
   }
   // positions of the block's and of the wave's rows
@@ -1152,10 +1170,11 @@ __global__ __launch_bounds__(256) void k_kv4_join(Kv4Cache c, Kv4Query a, Partia
   for (int s = w; s < S; s += PARTS) {
     const float2 y = ml[s];
     const f32x4 v = *(const f32x4*)(po + (int64_t)s * D);
-    const float k = y.x == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(y.x - M);
+    const bool any = y.x != kNegInf;  // else o may not have been written
+    const float k = any ? __builtin_amdgcn_exp2f(y.x - M) : 0.0f;
     l = fmaf(y.y, k, l);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = fmaf(v[e], k, o[e]);
+    for (int e = 0; e < 4; ++e) o[e] = fmaf(any ? v[e] : 0.0f, k, o[e]);
   }
   if constexpr (PARTS > 1) {
     so[w][x] = o;
@@ -1221,22 +1240,23 @@ hipError_t launch_dg(const Kv4Cache& c, const Kv4Query& q, const Kv4Plan& p, con
 }  // namespace
 
 Kv4Plan kv4_plan(int64_t n_seqs, int heads, int kv_heads, int dim, int group, int64_t max_q,
-                 int64_t max_len) {
+                 int64_t max_len, int64_t window) {
   Kv4Plan p;
   const int64_t cols = max_q * (heads / kv_heads);
   p.wide = cols > 16;
   const int64_t per = p.wide ? 16 * wide_tiles(dim, group) * kWaves : 16;
   p.tiles = (int)((cols + per - 1) / per);
   const int64_t blocks = n_seqs * kv_heads * p.tiles;
-  // four blocks a compute unit, two of the wide form's, at least 256 keys a split
-  int64_t s = ((p.wide ? 512 : 1024) + blocks - 1) / blocks;
-  const int64_t most = (max_len + 255) / 256;
+  const int64_t keys = window > 0 ? std::min(max_len, window + max_q) : max_len;
+  // two blocks a compute unit, at least 256 keys a split
+  int64_t s = (512 + blocks - 1) / blocks;
+  const int64_t most = (keys + 255) / 256;
   if (s > most) s = most;
   if (kv_heads * s > 65535) s = 65535 / kv_heads;
   p.splits = (int)(s < 1 ? 1 : s);
   p.waves = kWaves;
   // short sequences in few blocks: eight waves a block and no second launch
-  if (!p.wide && blocks <= 256 && max_len <= 2048) {
+  if (!p.wide && blocks <= 256 && keys <= 2048) {
     p.waves = 8;
     p.splits = 1;
   }

@@ -253,9 +253,9 @@ size_t awq_kv4_attention_workspace_bytes(int64_t n_tokens, int64_t n_seqs, int64
                                          int64_t max_len) {
   if (!kv4_valid(cfg) || attention_shape(n_tokens, n_seqs, heads, cfg, max_q, max_len)) return 0;
   if (n_tokens == 0 || n_seqs == 0 || max_q == 0) return 0;
-  const awq::Kv4Plan p =
-      awq::kv4_plan(n_seqs, (int)heads, cfg->kv_heads, cfg->head_dim,
-                                        cfg->group_size, max_q, max_len);
+  // without a window: with one there are no more splits
+  const awq::Kv4Plan p = awq::kv4_plan(n_seqs, (int)heads, cfg->kv_heads, cfg->head_dim,
+                                       cfg->group_size, max_q, max_len, 0);
   return round_up(awq::kv4_workspace(p, n_tokens, (int)heads, cfg->head_dim), kAlign);
 }
 
@@ -278,11 +278,9 @@ int awq_kv4_attention(const void* q, int64_t q_token_stride, int64_t q_head_stri
   if ((st = kv4_rows(q, q_token_stride, q_head_stride))) return st;
   if (!aligned(out, 16) || !aligned(lse_out, 4)) return AWQ_E_ALIGN;
   if (n_tokens == 0 || n_seqs == 0 || max_q == 0) return AWQ_OK;
-  const awq::Kv4Plan p =
-      awq::kv4_plan(n_seqs, (int)heads, cfg->kv_heads, cfg->head_dim,
-                                        cfg->group_size, max_q, max_len);
-  const size_t need =
-      round_up(awq::kv4_workspace(p, n_tokens, (int)heads, cfg->head_dim), kAlign);
+  const awq::Kv4Plan p = awq::kv4_plan(n_seqs, (int)heads, cfg->kv_heads, cfg->head_dim,
+                                       cfg->group_size, max_q, max_len, window);
+  const size_t need = awq_kv4_attention_workspace_bytes(n_tokens, n_seqs, heads, cfg, max_q, max_len);
   if (need && (!workspace || workspace_bytes < need)) return AWQ_E_WORKSPACE;
   if (need && !aligned(workspace, kAlign)) return AWQ_E_ALIGN;
   if ((st = device_ptrs({q, cache, block_table, seq_lens, q_start, out, lse_out,

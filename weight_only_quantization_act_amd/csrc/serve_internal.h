@@ -77,7 +77,7 @@ struct Kv4Plan {
   int waves;   // waves a block
 };
 Kv4Plan kv4_plan(int64_t n_seqs, int heads, int kv_heads, int dim, int group, int64_t max_q,
-                 int64_t max_len);
+                 int64_t max_len, int64_t window);
 size_t kv4_workspace(const Kv4Plan& p, int64_t n_tokens, int heads, int dim);
 hipError_t launch_kv4_attention(const Kv4Cache& c, const Kv4Query& q, const Kv4Plan& p,
                                 void* workspace, hipStream_t stream);
