@@ -486,19 +486,22 @@ __device__ __forceinline__ float lse_of(float M, float l) {
   return l == 0.0f ? kNegInf : (M + __builtin_amdgcn_logf(l)) * 0.69314718055994530942f;
 }
 
-// Workspace of a split call: o fp32 [rows][splits][D], then (M, l) [rows][splits] with rows =
-// (token, head).
+// Workspace of a call whose keys are divided, fp32: o [slot][D], then (M, l) [slot].
+//   wide: slot = (token, head) x splits.
+//   decode: slot = (key head, place) x 16 columns; then int32 [sequence][key head] x 2: the first
+//   place of a sequence's parts and their number.
 struct Partials {
   float* o;
   float* ml;
+  int32_t* parts;
   int splits, tiles;
 };
 
-// Which work a block does.  Blocks start in the order of their number: later column tiles see more
-// keys, so they go first, of all heads and sequences before any earlier tile (a prompt of 4096
-// tokens: 302 us with a head's tiles together, when long blocks start late, 211 so); and
-// consecutive blocks, which go to different dies, are different key heads: with eight of them
-// each die's L2 holds one.
+// Which work a block of the wide form does.  Blocks start in the order of their number: later
+// column tiles see more keys, so they go first, of all heads and sequences before any earlier tile
+// (a prompt of 4096 tokens: 302 us with a head's tiles together, when long blocks start late, 211
+// so); and consecutive blocks, which go to different dies, are different key heads: with eight
+// of them each die's L2 holds one.
 struct Place {
   int head, split, seq, tile;  // tile -1: none
 };
@@ -514,60 +517,180 @@ __device__ __forceinline__ Place place_of(const Kv4Cache& c, const Partials& par
   return p;
 }
 
+// A sequence of a call with few columns: its rows, its keys and the tiles that some row sees.
+struct Extent {
+  int row0, rows, len, pos0;  // first row, rows, keys that are there, position of the first row
+  int t_lo, t_hi;             // tiles of 32 keys
+  // what it counts in the division of the work: a sequence without keys still has rows to write
+  __device__ unsigned weight() const { return rows > 0 ? (unsigned)max(1, t_hi - t_lo) : 0u; }
+};
+__device__ __forceinline__ Extent extent_of(const Kv4Cache& c, const Kv4Query& a, int b) {
+  // (not written here: scalar loads where b is the same in all lanes)
+  const auto* starts = (const __attribute__((address_space(4))) int32_t*)(uintptr_t)c.starts;
+  const auto* lens = (const __attribute__((address_space(4))) int32_t*)(uintptr_t)c.lens;
+  Extent e;
+  e.row0 = starts[b];
+  const int count = starts[b + 1] - e.row0, len0 = lens[b];
+  e.rows = min(count, a.max_q);
+  // bounded by the table and by the caller's bound
+  e.len = min(len0, (int)min((int64_t)c.max_blocks << c.log2p, (int64_t)a.max_len));
+  e.pos0 = len0 - count;
+  const int lo_off = a.window > 0 ? a.window - 1 : 0x3fffffff;
+  e.t_lo = max(0, e.pos0 - lo_off) >> 5;
+  e.t_hi = max(e.t_lo, max(0, min(e.len, e.pos0 + e.rows) + 31) >> 5);
+  return e;
+}
+
+__device__ __forceinline__ unsigned lane_value(unsigned v, int lane) {
+  return (unsigned)__builtin_amdgcn_readlane((int)v, lane);
+}
+
+// sum over lanes 0 .. lane: within rows of 16 lanes, then their totals
+__device__ __forceinline__ unsigned wave_scan(unsigned v) {
+#define AWQ_SCAN(CTRL, ROWS) \
+  v += (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false)
+  AWQ_SCAN(0x111, 0xf);  // row_shr 1, 2, 4, 8
+  AWQ_SCAN(0x112, 0xf);
+  AWQ_SCAN(0x114, 0xf);
+  AWQ_SCAN(0x118, 0xf);
+  AWQ_SCAN(0x142, 0xa);  // lane 15 of a row to the next, rows 1 and 3
+  AWQ_SCAN(0x143, 0xc);  // lane 31 to rows 2 and 3
+#undef AWQ_SCAN
+  return v;
+}
+
+// The division of the tiles of all sequences (of one key head) over `blocks` blocks: block j takes
+// positions [j share, (j + 1) share) of the sequences' weights laid end to end (32 bits hold
+// them: see kv4_plan).  Every wave works it out, 64 sequences at a time.
+struct Share {
+  unsigned total, share, at;  // at: the block's first position
+  int seq;                    // the sequence there, -1: none
+  unsigned offset;            // position within it
+  Extent mine;                // of sequence base + lane
+  int base;
+};
+__device__ __forceinline__ Share share_of(const Kv4Cache& c, const Kv4Query& a, int j, int blocks,
+                                          int lane) {
+  Share s;
+  auto read = [&](int base) -> unsigned {
+    s.base = base;
+    s.mine = extent_of(c, a, min(base + lane, c.n_seqs - 1));
+    return base + lane < c.n_seqs ? s.mine.weight() : 0u;
+  };
+  s.total = 0;
+  unsigned v = 0, sum = 0;
+  for (int base = 0; base < c.n_seqs; base += 64) {
+    v = read(base);
+    sum = wave_scan(v);
+    s.total += lane_value(sum, 63);
+  }
+  s.share = max((s.total + blocks - 1) / blocks, 8u);
+  s.at = s.share * j;
+  s.seq = -1;
+  s.offset = 0;
+  if (s.at >= s.total) return s;
+  unsigned before = 0;
+  for (int base = 0; base < c.n_seqs; base += 64) {
+    if (c.n_seqs > 64) {
+      v = read(base);
+      sum = wave_scan(v);
+    }
+    const unsigned all = lane_value(sum, 63);
+    if (s.at < before + all) {
+      const int who = __builtin_ctzll(__ballot(sum > s.at - before));
+      s.seq = base + who;
+      s.offset = s.at - before - (lane_value(sum, who) - lane_value(v, who));
+      break;
+    }
+    before += all;
+  }
+  return s;
+}
+__device__ __forceinline__ Extent share_extent(const Share& s, const Kv4Cache& c, const Kv4Query& a, int b) {
+  if (b - s.base >= 64) return extent_of(c, a, b);
+  const int l = b - s.base;
+  Extent e;
+  e.row0 = (int)lane_value((unsigned)s.mine.row0, l);
+  e.rows = (int)lane_value((unsigned)s.mine.rows, l);
+  e.len = (int)lane_value((unsigned)s.mine.len, l);
+  e.pos0 = (int)lane_value((unsigned)s.mine.pos0, l);
+  e.t_lo = (int)lane_value((unsigned)s.mine.t_lo, l);
+  e.t_hi = (int)lane_value((unsigned)s.mine.t_hi, l);
+  return e;
+}
+
 // waves a SIMD that the registers are kept to
 constexpr int waves_per_simd(int dim, int group) {
   return dim / group > 2 ? 2 : dim == 64 && group == 64 ? 4 : 3;
 }
 
 // Up to 16 columns (decode): the waves of a block share the columns and take the tiles in turn.
-template <int D, int GS, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(waves_per_simd(D, GS)))) void k_kv4_attention(Kv4Cache c, Kv4Query a,
-                                                               Partials part) {
+// DIVIDED: the tiles of all sequences are dealt out evenly, so that a block may do parts of
+// several sequences; a sequence that lies in one block is written from there, the parts of the
+// others are joined by a second launch.  Otherwise a block does one sequence.
+template <int D, int GS, int WAVES, bool DIVIDED>
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DIVIDED ? 2 : waves_per_simd(D, GS))))
+void k_kv4_attention(Kv4Cache c, Kv4Query a, Partials part) {
   using X = Geo<D, GS>;
-  constexpr int kCols = 16;  // columns a block
+  using R = Ring<D, GS>;
+  constexpr int NS = kStages, step = WAVES;
+  constexpr int kRing = NS * R::BYTES * WAVES;
+  constexpr int kJoin = WAVES * 16 * (D + 6) * (int)sizeof(float);
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing > kJoin ? kRing : kJoin];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Place at = place_of(c, part);
-  if (at.tile < 0) return;  // the whole block
-  const int b = at.seq, kvh = at.head, split = at.split, tile = at.tile;
+  const unsigned number = blockIdx.x + gridDim.x * blockIdx.y;
+  const int kvh = number % c.kv_heads, index = number / c.kv_heads;  // index: of the head's blocks
   const int group = a.heads / c.kv_heads;
-  const int row0 = c.starts[b];
-  const int rows = min(c.starts[b + 1] - row0, a.max_q);
-  const int len0 = c.lens[b];
-  const int n_cols = rows * group;
-  if (tile * kCols >= n_cols) return;  // the whole block
-  const int P = 1 << c.log2p;
-  // keys that are there: bounded by the table and by the caller's bound
-  const int cap = (int)min((int64_t)c.max_blocks << c.log2p, (int64_t)a.max_len);
-  const int len = min(len0, cap);
-
-  // keys that some column sees
-  const int col0 = tile * kCols;
   const int lo_off = a.window > 0 ? a.window - 1 : 0x3fffffff;
-  const int first_i = col0 / group;
-  const int last_i = min(col0 + 15, n_cols - 1) / group;
-  const int pos0 = len0 - (c.starts[b + 1] - row0);
-  const int end = min(len, pos0 + last_i + 1);  // may be <= 0
-  const int begin = max(0, pos0 + first_i - lo_off);
-  int t_lo = begin >> 5, t_hi = max(0, end + 31) >> 5;
-  if (part.splits > 1) {
-    // This split's tiles.  All sequences are cut to the same length, that of the longest allowed
-    // over the splits: equal blocks fill the compute units better than equal numbers of them.
-    const int64_t keys = a.window > 0 ? min((int64_t)a.max_len, (int64_t)a.window + 47) : a.max_len;
-    const int n = max(0, t_hi - t_lo), most = c.n_seqs > 1 ? (int)((keys + 31) >> 5) : 0;
-    const int share = (max(n, most) + part.splits - 1) / part.splits;
-    t_lo = min(t_lo + (int)min((int64_t)share * split, (int64_t)n), t_hi);
-    t_hi = min(t_lo + share, t_hi);
-    if (t_lo >= t_hi) {
-      if (threadIdx.x < kCols && col0 + (int)threadIdx.x < n_cols) {
-        const int x = col0 + threadIdx.x, i = x / group;
-        const int64_t r = (int64_t)(row0 + i) * a.heads + kvh * group + (x - i * group);
-        *(float2*)(part.ml + (r * part.splits + split) * 2) = float2{kNegInf, 0.0f};
-      }
-      return;  // the whole block
-    }
+  const int P = 1 << c.log2p, n_pages = (int)c.n_pages;
+  uint8_t* ring = lds + wave * (NS * R::BYTES);
+  const unsigned ring_at = lds_address(ring);
+  const LaneOffsets<D, GS> lo = lane_offsets<D, GS>(lane, P);
+  const CodeConsts cc = code_consts();
+
+  Share s;
+  unsigned left;  // what the block still has to do
+  if constexpr (DIVIDED) {
+    s = share_of(c, a, index, part.splits, lane);
+    if (s.seq < 0) return;  // the whole block
+    left = min(s.share, s.total - s.at);
+  } else {
+    if (index >= c.n_seqs) return;
+    s.seq = index;
+    s.offset = 0;
+    left = 1;
   }
-  const int x = col0 + (lane & 15), xi = x / group;
+  for (; left > 0; ++s.seq) {
+  const int b = s.seq;
+  const Extent ex = DIVIDED ? share_extent(s, c, a, b) : extent_of(c, a, b);
+  const unsigned weight = ex.weight();
+  if (weight == 0) {
+    if (DIVIDED) continue;
+    return;
+  }
+  const int len = ex.len, pos0 = ex.pos0, row0 = ex.row0, n_cols = ex.rows * group;
+  const int last_i = ex.rows - 1;
+  int t_lo = ex.t_lo, t_hi = ex.t_hi;
+  bool whole_seq = true;
+  if constexpr (DIVIDED) {
+    const unsigned take = min(left, weight - s.offset);
+    whole_seq = take == weight;
+    t_lo += s.offset;
+    t_hi = min(t_hi, t_lo + (int)take);
+    if (s.offset == 0 && threadIdx.x == 0) {
+      int2 w;
+      w.x = index + b;
+      w.y = (int)((s.at + weight - 1) / s.share) - index + 1;
+      *(int2*)(part.parts + 2 * ((int64_t)b * c.kv_heads + kvh)) = w;
+    }
+    left -= take;
+    s.at += take;
+    s.offset = 0;
+  } else {
+    left = 0;
+  }
+  const int x = lane & 15, xi = x / group;
   const bool has = x < n_cols;
   const QueryRow<D, GS> query = read_query<D, GS>(
       has ? (const uint16_t*)a.q + (int64_t)(row0 + xi) * a.qt + (int64_t)(kvh * group + x - xi * group) * a.qh
@@ -577,18 +700,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(wave
   const auto* table = (const __attribute__((address_space(4))) int32_t*)(uintptr_t)(
       c.table + (int64_t)b * c.max_blocks);
   const int last_blk = max(0, (len - 1) >> c.log2p);
-  const int n_pages = (int)c.n_pages;
   WeightScale ws;
-  const CodeConsts cc = code_consts();
-  using R = Ring<D, GS>;
-  constexpr int NS = kStages;
-  constexpr int kRing = NS * R::BYTES * WAVES;
-  constexpr int kJoin = WAVES * 16 * (D + 6) * (int)sizeof(float);
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing > kJoin ? kRing : kJoin];
-  uint8_t* ring = lds + wave * (NS * R::BYTES);
-  const unsigned ring_at = lds_address(ring);
-  const LaneOffsets<D, GS> lo = lane_offsets<D, GS>(lane, P);
-  const int step = WAVES;
   const int t0 = t_lo + wave;
   // tiles t0, t0 + step, ...: tile i of the wave in stage i mod NS
   const int n_tiles = t_hi > t0 ? (t_hi - t0 + step - 1) / step : 0;
@@ -632,7 +744,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(wave
         if (i + NS < n_tiles) start(i + NS, s);
         const int key0 = 32 * (t0 + i * step);
         // every key of the tile exists and every column sees all of it
-        const bool whole = !dead && key0 + 32 <= len && key0 + 31 <= pos0 + first_i &&
+        const bool whole = !dead && key0 + 32 <= len && key0 + 31 <= pos0 &&
                            key0 >= pos0 + last_i - lo_off;
         do_tile<D, GS>(r, col, whole, key0, len, lo_off, dead, ws, cc, lane);
       }
@@ -658,8 +770,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(wave
     // thread -> column, 4 channels at a time
     for (int w = threadIdx.x; w < 16 * (D / 4); w += 64 * WAVES) {
       const int cx = w / (D / 4), ch = (w % (D / 4)) * 4;
-      const int xx = col0 + cx;
-      if (xx >= n_cols) continue;
+      if (cx >= n_cols) continue;
       float M = sm[0][cx];
 #pragma unroll
       for (int i = 1; i < WAVES; ++i) M = fmaxf(M, sm[i][cx]);
@@ -674,14 +785,12 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(wave
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] = fmaf(v[e], k, o[e]);
       }
-      const int i = xx / group, h = xx - i * group;
+      const int i = cx / group, h = cx - i * group;
       const int64_t r = (int64_t)(row0 + i) * a.heads + kvh * group + h;
-      if (part.splits > 1) {
-        *(f32x4*)(part.o + (r * part.splits + split) * D + ch) = o;
-        if (ch == 0) {
-          part.ml[(r * part.splits + split) * 2] = M;
-          part.ml[(r * part.splits + split) * 2 + 1] = l;
-        }
+      if (DIVIDED && !whole_seq) {
+        const int64_t slot = ((int64_t)kvh * (part.splits + c.n_seqs) + index + b) * 16 + cx;
+        *(f32x4*)(part.o + slot * D + ch) = o;
+        if (ch == 0) *(float2*)(part.ml + slot * 2) = float2{M, l};
       } else {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const float v[4] = {o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
@@ -689,6 +798,8 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(wave
         if (ch == 0 && a.lse) a.lse[r] = lse_of(M, l);
       }
     }
+  }
+  if (DIVIDED && left > 0) __syncthreads();  // the next sequence's tiles go where this one's sums lie
   }
 }
 
@@ -1150,31 +1261,43 @@ void k_kv4_attention_wide(Kv4Cache c, Kv4Query a, Partials part) {
 
 // Joins the splits of a (token, head): D / 4 threads a row and part, part w adds splits w,
 // w + PARTS, ... in order, then the parts are added in order.
-template <int D, int PARTS>
+template <int D, int PARTS, bool DIVIDED>
 __global__ __launch_bounds__(256) void k_kv4_join(Kv4Cache c, Kv4Query a, Partials part,
                                                   int64_t n_rows) {
   constexpr int T = D / 4, ROWS = 256 / (T * PARTS);
   __shared__ f32x4 so[PARTS > 1 ? PARTS : 1][T];
   __shared__ float sm[PARTS], sl[PARTS];
-  const int x = threadIdx.x % T, w = threadIdx.x / T % PARTS, S = part.splits;
+  const int x = threadIdx.x % T, w = threadIdx.x / T % PARTS;
   const int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / (T * PARTS);
   if (ROWS > 1 && r >= n_rows) return;
-  // read before it is known whether the row has partials (what is read is workspace either way)
-  const float2* ml = (const float2*)part.ml + r * S;
-  const float* po = part.o + r * S * D + 4 * x;
+  const int64_t t = r / a.heads;
+  int64_t first = r * part.splits, step = 1;  // slots
+  int S = part.splits;
+  if constexpr (DIVIDED) {
+    const int b = kv4_sequence(c, t);
+    if (b < 0 || t - c.starts[b] >= a.max_q) return;  // (one row a block, or no barrier)
+    const int group = a.heads / c.kv_heads, h = (int)(r - t * a.heads), kvh = h / group;
+    const int2 p = *(const int2*)(part.parts + 2 * ((int64_t)b * c.kv_heads + kvh));
+    if (p.y == 1) return;
+    S = p.y;
+    step = 16;
+    first = ((int64_t)kvh * (part.splits + c.n_seqs) + p.x) * 16 + (t - c.starts[b]) * group + h - kvh * group;
+  }
+  // wide: read before it is known whether the row has partials (what is read is workspace either way)
+  const float2* ml = (const float2*)part.ml + first;
+  const float* po = part.o + first * D + 4 * x;
   float M = kNegInf, l = 0.0f;
 #pragma unroll 4
-  for (int s = w; s < S; s += PARTS) M = fmaxf(M, ml[s].x);
+  for (int s = w; s < S; s += PARTS) M = fmaxf(M, ml[s * step].x);
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
   for (int s = w; s < S; s += PARTS) {
-    const float2 y = ml[s];
-    const f32x4 v = *(const f32x4*)(po + (int64_t)s * D);
-    const bool any = y.x != kNegInf;  // else o may not have been written
-    const float k = any ? __builtin_amdgcn_exp2f(y.x - M) : 0.0f;
+    const float2 y = ml[s * step];
+    const f32x4 v = *(const f32x4*)(po + s * step * D);
+    const float k = y.x == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(y.x - M);
     l = fmaf(y.y, k, l);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = fmaf(any ? v[e] : 0.0f, k, o[e]);
+    for (int e = 0; e < 4; ++e) o[e] = fmaf(v[e], k, o[e]);
   }
   if constexpr (PARTS > 1) {
     so[w][x] = o;
@@ -1199,42 +1322,49 @@ __global__ __launch_bounds__(256) void k_kv4_join(Kv4Cache c, Kv4Query a, Partia
     }
     M = all;
   }
-  // a row past a sequence's bound has no partials
-  const int64_t t = r / a.heads;
-  const int b = kv4_sequence(c, t);
-  if (b < 0 || t - c.starts[b] >= a.max_q) return;
+  if constexpr (!DIVIDED) {  // a row past a sequence's bound has no partials
+    const int b = kv4_sequence(c, t);
+    if (b < 0 || t - c.starts[b] >= a.max_q) return;
+  }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const float v[4] = {o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
   store4(a.out, r * D + 4 * x, a.bf16, v);
   if (x == 0 && a.lse) a.lse[r] = lse_of(M, l);
 }
 
-template <int D>
+template <int D, bool DIVIDED>
 hipError_t launch_join(const Kv4Cache& c, const Kv4Query& q, const Partials& part, int64_t rows,
                        hipStream_t stream) {
   constexpr int kParts = 1024 / D, kRows = 1024 / D;
-  if (part.splits >= 16)
-    hipLaunchKernelGGL((k_kv4_join<D, kParts>), dim3((unsigned)rows), dim3(256), 0, stream, c, q, part, rows);
+  // many parts a row
+  if (part.splits / (DIVIDED ? c.n_seqs : 1) >= 16)
+    hipLaunchKernelGGL((k_kv4_join<D, kParts, DIVIDED>), dim3((unsigned)rows), dim3(256), 0, stream, c, q,
+                       part, rows);
   else
-    hipLaunchKernelGGL((k_kv4_join<D, 1>), dim3((unsigned)((rows + kRows - 1) / kRows)), dim3(256), 0,
-                       stream, c, q, part, rows);
+    hipLaunchKernelGGL((k_kv4_join<D, 1, DIVIDED>), dim3((unsigned)((rows + kRows - 1) / kRows)), dim3(256),
+                       0, stream, c, q, part, rows);
   return hipGetLastError();
 }
 
 template <int D, int GS>
 hipError_t launch_dg(const Kv4Cache& c, const Kv4Query& q, const Kv4Plan& p, const Partials& part,
-                     hipStream_t stream) {
-  const int64_t blocks = (int64_t)p.tiles * p.splits * c.kv_heads * c.n_seqs;
+                     int64_t rows, hipStream_t stream) {
+  const int64_t blocks =
+      (int64_t)c.kv_heads * (p.wide ? (int64_t)p.tiles * p.splits * c.n_seqs : p.splits > 1 ? p.splits : c.n_seqs);
   constexpr int64_t kRow = 1 << 20;  // a dimension of a grid holds less than 2^32 threads
   if (blocks > 0x7fffffff - kRow) return hipErrorInvalidValue;
   const dim3 grid((unsigned)(blocks < kRow ? blocks : kRow), (unsigned)((blocks + kRow - 1) / kRow));
   if (p.wide)
     hipLaunchKernelGGL((k_kv4_attention_wide<D, GS>), grid, dim3(64 * kWaves), 0, stream, c, q, part);
+  else if (p.splits > 1)
+    hipLaunchKernelGGL((k_kv4_attention<D, GS, kWaves, true>), grid, dim3(64 * kWaves), 0, stream, c, q, part);
   else if (p.waves == 8)
-    hipLaunchKernelGGL((k_kv4_attention<D, GS, 8>), grid, dim3(512), 0, stream, c, q, part);
+    hipLaunchKernelGGL((k_kv4_attention<D, GS, 8, false>), grid, dim3(512), 0, stream, c, q, part);
   else
-    hipLaunchKernelGGL((k_kv4_attention<D, GS, kWaves>), grid, dim3(64 * kWaves), 0, stream, c, q, part);
-  return hipGetLastError();
+    hipLaunchKernelGGL((k_kv4_attention<D, GS, kWaves, false>), grid, dim3(64 * kWaves), 0, stream, c, q, part);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.splits <= 1) return e;
+  return p.wide ? launch_join<D, false>(c, q, part, rows, stream) : launch_join<D, true>(c, q, part, rows, stream);
 }
 
 }  // namespace
@@ -1243,52 +1373,64 @@ Kv4Plan kv4_plan(int64_t n_seqs, int heads, int kv_heads, int dim, int group, in
                  int64_t max_len, int64_t window) {
   Kv4Plan p;
   const int64_t cols = max_q * (heads / kv_heads);
-  p.wide = cols > 16;
-  const int64_t per = p.wide ? 16 * wide_tiles(dim, group) * kWaves : 16;
-  p.tiles = (int)((cols + per - 1) / per);
-  const int64_t blocks = n_seqs * kv_heads * p.tiles;
   const int64_t keys = window > 0 ? std::min(max_len, window + max_q) : max_len;
-  // two blocks a compute unit, at least 256 keys a split
-  int64_t s = (512 + blocks - 1) / blocks;
-  const int64_t most = (keys + 255) / 256;
-  if (s > most) s = most;
-  if (kv_heads * s > 65535) s = 65535 / kv_heads;
-  p.splits = (int)(s < 1 ? 1 : s);
+  p.wide = cols > 16;
   p.waves = kWaves;
-  // short sequences in few blocks: eight waves a block and no second launch
-  if (!p.wide && blocks <= 256 && keys <= 2048) {
-    p.waves = 8;
-    p.splits = 1;
+  if (p.wide) {
+    const int64_t per = 16 * wide_tiles(dim, group) * kWaves;
+    p.tiles = (int)((cols + per - 1) / per);
+    const int64_t blocks = n_seqs * kv_heads * p.tiles;
+    // two blocks a compute unit, at least 256 keys a split
+    const int64_t s = std::min((512 + blocks - 1) / blocks, (keys + 255) / 256);
+    p.splits = (int)std::max<int64_t>(s, 1);
+    return p;
   }
+  p.tiles = 1;
+  p.splits = 1;
+  const int64_t blocks = n_seqs * kv_heads;
+  // short sequences in few blocks: eight waves a block and no second launch
+  if (blocks <= 256 && keys <= 2048) p.waves = 8;
+  // else the work is divided over two blocks a compute unit, unless there are many sequences or
+  // short ones
+  else if (blocks < 4096 && (blocks < 512 || keys > 1024) && n_seqs * (keys / 32 + 2) < ((int64_t)1 << 30))
+    p.splits = std::max(512 / kv_heads, 1);
   return p;
 }
 
-size_t kv4_workspace(const Kv4Plan& p, int64_t n_tokens, int heads, int dim) {
+namespace {
+
+// slots of partial sums
+int64_t kv4_slots(const Kv4Plan& p, int64_t n_tokens, int64_t n_seqs, int heads, int kv_heads) {
+  return p.wide ? n_tokens * heads * p.splits : (int64_t)kv_heads * (p.splits + n_seqs) * 16;
+}
+
+}  // namespace
+
+size_t kv4_workspace(const Kv4Plan& p, int64_t n_tokens, int64_t n_seqs, int heads, int kv_heads, int dim) {
   if (p.splits <= 1) return 0;
-  return (size_t)n_tokens * heads * p.splits * (dim + 2) * sizeof(float);
+  return (size_t)kv4_slots(p, n_tokens, n_seqs, heads, kv_heads) * (dim + 2) * sizeof(float) +
+         (p.wide ? 0 : (size_t)n_seqs * kv_heads * 2 * sizeof(int32_t));
 }
 
 hipError_t launch_kv4_attention(const Kv4Cache& c, const Kv4Query& q, const Kv4Plan& p,
                                 void* workspace, hipStream_t stream) {
   const int64_t rows = q.n_tokens * q.heads;
   if (rows <= 0 || c.n_seqs <= 0) return hipSuccess;
+  const int64_t slots = kv4_slots(p, q.n_tokens, c.n_seqs, q.heads, c.kv_heads);
   Partials part;
   part.splits = p.splits;
   part.tiles = p.tiles;
   part.o = (float*)workspace;
-  part.ml = part.o + rows * p.splits * c.dim;
-  hipError_t e;
+  part.ml = part.o + slots * c.dim;
+  part.parts = (int32_t*)(part.ml + slots * 2);
   switch (c.dim * 1000 + c.group) {
-    case 64032: e = launch_dg<64, 32>(c, q, p, part, stream); break;
-    case 64064: e = launch_dg<64, 64>(c, q, p, part, stream); break;
-    case 128032: e = launch_dg<128, 32>(c, q, p, part, stream); break;
-    case 128064: e = launch_dg<128, 64>(c, q, p, part, stream); break;
-    case 128128: e = launch_dg<128, 128>(c, q, p, part, stream); break;
+    case 64032: return launch_dg<64, 32>(c, q, p, part, rows, stream);
+    case 64064: return launch_dg<64, 64>(c, q, p, part, rows, stream);
+    case 128032: return launch_dg<128, 32>(c, q, p, part, rows, stream);
+    case 128064: return launch_dg<128, 64>(c, q, p, part, rows, stream);
+    case 128128: return launch_dg<128, 128>(c, q, p, part, rows, stream);
     default: return hipErrorInvalidValue;
   }
-  if (e != hipSuccess || p.splits <= 1) return e;
-  return c.dim == 64 ? launch_join<64>(c, q, part, rows, stream)
-                     : launch_join<128>(c, q, part, rows, stream);
 }
 
 }  // namespace awq

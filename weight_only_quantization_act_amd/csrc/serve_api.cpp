@@ -256,7 +256,7 @@ size_t awq_kv4_attention_workspace_bytes(int64_t n_tokens, int64_t n_seqs, int64
   // without a window: with one there are no more splits
   const awq::Kv4Plan p = awq::kv4_plan(n_seqs, (int)heads, cfg->kv_heads, cfg->head_dim,
                                        cfg->group_size, max_q, max_len, 0);
-  return round_up(awq::kv4_workspace(p, n_tokens, (int)heads, cfg->head_dim), kAlign);
+  return round_up(awq::kv4_workspace(p, n_tokens, n_seqs, (int)heads, cfg->kv_heads, cfg->head_dim), kAlign);
 }
 
 int awq_kv4_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,

@@ -68,17 +68,19 @@ struct Kv4Query {
   void* out;
   float* lse;
 };
-// How one attention call is laid out (by sizes only): columns (query rows x heads of a key
-// head) a block, and the splits of the keys.
+// How one attention call is laid out (by sizes only).  Columns are query rows x heads of a key
+// head.
 struct Kv4Plan {
-  int wide;    // 0: one 16-column tile a block, its waves share the keys; 1: a tile set a wave
-  int tiles;   // blocks of columns a (sequence, key head)
-  int splits;  // parts of the keys, joined by a second launch if more than one
+  int wide;    // 0: up to 16 columns, a block's waves share the keys; 1: column tiles a wave
+  int tiles;   // wide: blocks of columns a (sequence, key head)
+  int splits;  // wide: parts of the keys; else blocks of a key head over which all keys are dealt
+               // out.  1: none, otherwise a second launch joins the parts
   int waves;   // waves a block
 };
 Kv4Plan kv4_plan(int64_t n_seqs, int heads, int kv_heads, int dim, int group, int64_t max_q,
                  int64_t max_len, int64_t window);
-size_t kv4_workspace(const Kv4Plan& p, int64_t n_tokens, int heads, int dim);
+size_t kv4_workspace(const Kv4Plan& p, int64_t n_tokens, int64_t n_seqs, int heads, int kv_heads,
+                     int dim);
 hipError_t launch_kv4_attention(const Kv4Cache& c, const Kv4Query& q, const Kv4Plan& p,
                                 void* workspace, hipStream_t stream);
 
