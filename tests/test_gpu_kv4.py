@@ -257,6 +257,42 @@ def test_rows(D, g, dtype):
             _check(c, q, None, window, where=(P, Hk, grp, window))
 
 
+@pytest.mark.parametrize("D,g", LAYOUTS)
+def test_sequences_dealt_out(D, g):
+    """More sequences than lanes, of very different lengths: a block does parts of several, some
+    without rows, without keys or before their first token."""
+    rng = np.random.default_rng(D + g)
+    lens = [int(x) for x in np.exp(rng.uniform(0, np.log(300), 150))]
+    news = [int(x) for x in rng.integers(0, 4, 150)]
+    lens[3], lens[5], lens[64], lens[100], lens[149] = 0, -2, 2500, 1, 1300
+    news[3], news[5], news[7], news[64], news[149] = 1, 3, 0, 3, 1
+    for n in (150, 65, 4):
+        c = Case(D, 2, 16 if n == 65 else 64, g, 1, lens[:n], news[:n], "fp16", seed=n)
+        c.fill()
+        q = torch.randn(int(c.starts[-1]), 10, D, device="cuda").half()
+        for window in (0, 700, 3):
+            say(f"kv4 dealt out D={D} g={g} n={n} window={window}")
+            a, la = _check(c, q, None, window, max_len=5000, where=(n, window))
+            b, lb = awq.awq_kv4_attention(q, c.cache, c.dtable, c.dlens, c.dstarts, c.cfg, max_q=max(c.news),
+                                          max_len=5000, window=window)
+            assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+@pytest.mark.parametrize("D,g", LAYOUTS)
+def test_many_short_sequences(D, g):
+    """A block a sequence, no second launch."""
+    rng = np.random.default_rng(D + g)
+    lens = [int(x) for x in rng.integers(-1, 90, 600)]
+    news = [int(x) for x in rng.integers(0, 3, 600)]
+    c = Case(D, 1, 32, g, 0, lens, news, "bf16", seed=g)
+    c.fill()
+    q = torch.randn(int(c.starts[-1]), 8, D, device="cuda").bfloat16()
+    assert awq.awq_kv4_attention_workspace_bytes(len(q), 600, 8, c.cfg, 2, 1000) == 0
+    for window in (0, 33):
+        say(f"kv4 short D={D} g={g} window={window}")
+        _check(c, q, None, window, max_q=2, max_len=1000, where=window)
+
+
 @pytest.mark.parametrize("news", [1, 3, 40])
 def test_long_context_splits(news):
     """Few sequences and many keys: the keys are split over blocks and joined."""

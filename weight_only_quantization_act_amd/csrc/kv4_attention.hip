@@ -30,9 +30,15 @@
 // down to 2^-29 of the largest.  A rise of the maximum or of that step multiplies what was
 // summed so far by exp2 of the difference.
 //
-// Few columns (decode): the four waves of a block take the tiles in turn and add their results
-// through LDS; long sequences are split over blocks and joined by a second launch.  Many
-// columns (prompts): each wave keeps NC column tiles and walks all keys itself.
+// Two forms.  Up to 16 columns (decode): a block's waves share the columns and take the tiles in
+// turn, each with a ring of tiles in LDS that DMAs fill ahead; bound by the reading of the codes
+// and by the vector instructions that make operands of them (two a pair of codes, about 350 a
+// tile).  64 sequences of 2000 to 8192 tokens, 64 heads on 8 key heads of 128, groups of 64:
+// 91 us, 4.1 TB/s of codes and parameters; one of 131072 tokens, groups of 128: 40 us, 3.6 TB/s.
+// More columns (prompts): column tiles a wave, and the codes are decoded once a block; bound by
+// the vector instructions of the softmax and by the products, which share the issue.  A prompt of
+// 4096 tokens, 32 heads on 8: 188 us, 0.73 PFLOP/s.  One form for both would decode the codes once a
+// column tile (the prompt: 524 us), or leave three of four waves without work at a single token.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -624,10 +630,12 @@ constexpr int waves_per_simd(int dim, int group) {
   return dim / group > 2 ? 2 : dim == 64 && group == 64 ? 4 : 3;
 }
 
-// Up to 16 columns (decode): the waves of a block share the columns and take the tiles in turn.
+// Up to 16 columns (decode): the waves of a block share the columns and take the tiles in turn,
+// a ring of kStages tiles each (64 sequences: 169 us with two stages, 96 with three, 97 with four).
 // DIVIDED: the tiles of all sequences are dealt out evenly, so that a block may do parts of
 // several sequences; a sequence that lies in one block is written from there, the parts of the
-// others are joined by a second launch.  Otherwise a block does one sequence.
+// others are joined by a second launch (64 sequences of 2000 to 8192 tokens: 96 us with a block a
+// sequence and head, 101 with equal pieces of 2048 keys, 91 so).  Otherwise a block does one sequence.
 template <int D, int GS, int WAVES, bool DIVIDED>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DIVIDED ? 2 : waves_per_simd(D, GS))))
 void k_kv4_attention(Kv4Cache c, Kv4Query a, Partials part) {
@@ -1388,10 +1396,13 @@ Kv4Plan kv4_plan(int64_t n_seqs, int heads, int kv_heads, int dim, int group, in
   p.tiles = 1;
   p.splits = 1;
   const int64_t blocks = n_seqs * kv_heads;
-  // short sequences in few blocks: eight waves a block and no second launch
+  // short sequences in few blocks: eight waves a block and no second launch (one sequence of 777
+  // tokens, 8 key heads: MSHORT_8 us, divided MSHORT_D)
   if (blocks <= 256 && keys <= 2048) p.waves = 8;
-  // else the work is divided over two blocks a compute unit, unless there are many sequences or
-  // short ones
+  // else the work is divided over two blocks a compute unit (one sequence of 131072 tokens: 39 us
+  // with 512 blocks, 42 with 1024, 65 with 4096), unless there are many sequences or short ones,
+  // for which a second launch costs more than their different lengths (64 sequences of MS_L tokens:
+  // MS_A us a block a sequence, MS_B divided; of 250 to 1000: MT_A and MT_B)
   else if (blocks < 4096 && (blocks < 512 || keys > 1024) && n_seqs * (keys / 32 + 2) < ((int64_t)1 << 30))
     p.splits = std::max(512 / kv_heads, 1);
   return p;
