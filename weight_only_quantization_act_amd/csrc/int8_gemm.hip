@@ -240,7 +240,9 @@ __global__ __launch_bounds__(256) void k_int8_finish(Int8Args a, int splits,
 // from memory to the operand registers of v_mfma_i32_16x16x64_i8 directly (lane l: 16 bytes of
 // row l mod 16 at 16 (l div 16); four instructions cover 256 contiguous bytes of a row), the
 // next piece's ahead of the products of this one; the tokens' operands come from L2.  The
-// waves' int32 sums are added through LDS.  Result element e of lane l is output
+// waves' int32 sums are added through LDS.  Measured: one token, 4096 x 4096 with the quantisation
+// 6 us (2.8 TB/s; a launch alone is 2), 16 tokens, 11008 x 4096 without it 15 us (3.0 TB/s): short
+// of the memory's rate because 512 threads a block start, load twice or four times and end.  Result element e of lane l is output
 // 4 (l div 16) + e, token l mod 16.
 //
 // FUSED (one token): the block first quantises the token into LDS, with the first weights
@@ -425,15 +427,36 @@ struct Plan {
   int form, splits;
 };
 
+// Which form: what each measured, in us at 4096 x 4096, 11008 x 4096, 5120 x 13824 (out x in):
+//   up to 16 tokens  weight streaming 7.3, 14.8, 27.6; 32-token tiles 9.0, 14.6, 20.6 (so weights of
+//                    2^26 bytes and more take those)
+//   32 tokens        32-token tiles 9.7, 15.6, 21.1; 64-token tiles 11.0, 16.7, 21.7
+//   128              64: 15.4, 22.0, 24.0; 128: 16.3, 22.9, 26.8
+//   200              64: 20.3, 27.0, 33.8; 128: 19.7, 28.9, 37.8
+//   512              64: 24.9, 44.5, 67.2; 128: 28.0, 41.1, 53.9
+//   1024             64: 31.2, 79.2, 109; 128: 36.9, 72.0, 94.9; 256: 53.3, 63.8, 131
+//   4096             128: 88.7, 233, 298; 256: 72.7, 196, 322
+// 64-token tiles stay ahead while they are one round of two blocks a compute unit and the sums are
+// short.  256 x 256 tiles do 1.3 times the work of 128 x 128 ones a unit of time, but one a compute
+// unit: a round of them costs 1.53 rounds of the small ones, a round begun nearly as much as a whole.
 Plan plan_of(int64_t T, int64_t M, int64_t K) {
-  Plan p{kTile256, 1};
-  p.form = T <= 16 && M * K < (int64_t)1 << 27 ? kFew : T <= 32 ? kTile32 : T <= 128 ? kTile64 : kTile128;
-  if (T > 128 && ((T + 255) / 256) * ((M + 255) / 256) >= 256) p.form = kTile256;
+  Plan p{kTile128, 1};
+  auto tiles_of = [&](int64_t bt, int64_t bm) { return ((T + bt - 1) / bt) * ((M + bm - 1) / bm); };
+  if (T <= 16 && M * K < (int64_t)1 << 26) p.form = kFew;
+  else if (T <= 32) p.form = kTile32;
+  else if (T <= 128 || (K <= 6144 && tiles_of(64, 128) <= 512)) p.form = kTile64;
+  else {
+    const int64_t small = tiles_of(128, 128), large = tiles_of(256, 256);
+    const double rs = small / 512.0, cs = (double)((small + 511) / 512);
+    const double rl = large / 256.0, cl = (double)((large + 255) / 256);
+    if (1.53 * (0.25 * rl + 0.75 * cl) < 0.5 * (rs + cs)) p.form = kTile256;
+  }
   if (p.form < kTile32 || p.form == kTile256) return p;
-  const int bt = p.form == kTile32 ? 32 : p.form == kTile64 ? 64 : 128;
-  const int64_t tiles = ((T + bt - 1) / bt) * ((M + 127) / 128);
-  int64_t s = 512 / tiles;          // two blocks a compute unit
-  const int64_t most = K / 1024;        // at least eight steps a split
+  const int64_t tiles = tiles_of(p.form == kTile32 ? 32 : p.form == kTile64 ? 64 : 128, 128);
+  // K split over two blocks a compute unit, at least eight steps a split (5120 x 13824, unsplit and
+  // split: 64 tokens 41.5 and 23.4 us, 200 tokens 72.5 and 35.1, 512 tokens 75.3 and 55.3)
+  int64_t s = 512 / tiles;
+  const int64_t most = K / 1024;
   if (s > most) s = most;
   if (s > 8) s = 8;
   p.splits = (int)(s < 1 ? 1 : s);

@@ -325,9 +325,9 @@ struct WeightScale {
   uint32_t limit = 0;
 };
 
-// One tile of 32 keys.  !whole (the same in every lane): some (key, column)
-// pairs do not exist; key0 is the tile's first key, lo_off = window - 1 (or a huge number) so that column pos sees
-// keys [pos - lo_off, pos]; dead: bit x set if the keys of half x lie on no page.
+// One tile of 32 keys.  !whole (the same in every lane): some (key, column) pairs do not exist;
+// key0 is the tile's first key, lo_off = window - 1 (or a huge number) so that column pos sees keys
+// [pos - lo_off, pos]; dead: bit x set if the keys of half x lie on no page.
 template <int D, int GS>
 __device__ __forceinline__ void do_tile(TileRegs<D, GS>& r, Column<D, GS>& c, bool whole,
                                         int key0, int n_keys, int lo_off, int dead, WeightScale& ws,
@@ -462,7 +462,8 @@ __device__ __forceinline__ void do_tile(TileRegs<D, GS>& r, Column<D, GS>& c, bo
   }
 }
 
-// Results of a column tile: sums over the column's lanes, the zeros subtracted.  o is then sum_t w_t (c - z), l the weights' sum, both over exp2(M()).
+// Results of a column tile: sums over the column's lanes, the zeros subtracted.  o is then
+// sum_t w_t (c - z), l the weights' sum, both over exp2(M()).
 template <int D, int GS>
 __device__ __forceinline__ void finish(Column<D, GS>& c) {
   using X = Geo<D, GS>;
@@ -516,10 +517,10 @@ __device__ __forceinline__ Place place_of(const Kv4Cache& c, const Partials& par
   Place p;
   p.head = n % c.kv_heads;
   n /= c.kv_heads;
-  p.seq = n % c.n_seqs;
-  n /= c.n_seqs;
   p.split = n % part.splits;
-  p.tile = part.tiles - 1 - (int)(n / part.splits);
+  n /= part.splits;
+  p.seq = n % c.n_seqs;
+  p.tile = part.tiles - 1 - (int)(n / c.n_seqs);
   return p;
 }
 
@@ -625,7 +626,9 @@ __device__ __forceinline__ Extent share_extent(const Share& s, const Kv4Cache& c
   return e;
 }
 
-// waves a SIMD that the registers are kept to
+// Waves a SIMD that the registers of the undivided form are kept to (divided, two blocks a compute
+// unit are two waves a SIMD, and fewer registers would spill: one sequence of 131072 tokens, 44 us
+// with three, 40 with two).
 constexpr int waves_per_simd(int dim, int group) {
   return dim / group > 2 ? 2 : dim == 64 && group == 64 ? 4 : 3;
 }
@@ -637,7 +640,8 @@ constexpr int waves_per_simd(int dim, int group) {
 // others are joined by a second launch (64 sequences of 2000 to 8192 tokens: 96 us with a block a
 // sequence and head, 101 with equal pieces of 2048 keys, 91 so).  Otherwise a block does one sequence.
 template <int D, int GS, int WAVES, bool DIVIDED>
-__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DIVIDED ? 2 : waves_per_simd(D, GS))))
+__global__ __launch_bounds__(64 * WAVES)
+__attribute__((amdgpu_waves_per_eu(DIVIDED ? 2 : waves_per_simd(D, GS))))
 void k_kv4_attention(Kv4Cache c, Kv4Query a, Partials part) {
   using X = Geo<D, GS>;
   using R = Ring<D, GS>;
@@ -670,144 +674,145 @@ void k_kv4_attention(Kv4Cache c, Kv4Query a, Partials part) {
     left = 1;
   }
   for (; left > 0; ++s.seq) {
-  const int b = s.seq;
-  const Extent ex = DIVIDED ? share_extent(s, c, a, b) : extent_of(c, a, b);
-  const unsigned weight = ex.weight();
-  if (weight == 0) {
-    if (DIVIDED) continue;
-    return;
-  }
-  const int len = ex.len, pos0 = ex.pos0, row0 = ex.row0, n_cols = ex.rows * group;
-  const int last_i = ex.rows - 1;
-  int t_lo = ex.t_lo, t_hi = ex.t_hi;
-  bool whole_seq = true;
-  if constexpr (DIVIDED) {
-    const unsigned take = min(left, weight - s.offset);
-    whole_seq = take == weight;
-    t_lo += s.offset;
-    t_hi = min(t_hi, t_lo + (int)take);
-    if (s.offset == 0 && threadIdx.x == 0) {
-      int2 w;
-      w.x = index + b;
-      w.y = (int)((s.at + weight - 1) / s.share) - index + 1;
-      *(int2*)(part.parts + 2 * ((int64_t)b * c.kv_heads + kvh)) = w;
+    const int b = s.seq;
+    const Extent ex = DIVIDED ? share_extent(s, c, a, b) : extent_of(c, a, b);
+    const unsigned weight = ex.weight();
+    if (weight == 0) {
+      if (DIVIDED) continue;
+      return;
     }
-    left -= take;
-    s.at += take;
-    s.offset = 0;
-  } else {
-    left = 0;
-  }
-  const int x = lane & 15, xi = x / group;
-  const bool has = x < n_cols;
-  const QueryRow<D, GS> query = read_query<D, GS>(
-      has ? (const uint16_t*)a.q + (int64_t)(row0 + xi) * a.qt + (int64_t)(kvh * group + x - xi * group) * a.qh
-          : nullptr,
-      lane >> 4);
-  // (the table is not written here: scalar loads)
-  const auto* table = (const __attribute__((address_space(4))) int32_t*)(uintptr_t)(
-      c.table + (int64_t)b * c.max_blocks);
-  const int last_blk = max(0, (len - 1) >> c.log2p);
-  WeightScale ws;
-  const int t0 = t_lo + wave;
-  // tiles t0, t0 + step, ...: tile i of the wave in stage i mod NS
-  const int n_tiles = t_hi > t0 ? (t_hi - t0 + step - 1) / step : 0;
-  int dead_of[NS];
-  // the table entries of the next tile to start, read one tile ahead
-  int page_a, page_b;
-  auto look_up = [&](int i) {
-    const int key = 32 * (t0 + i * step);
-    page_a = table[min(key >> c.log2p, last_blk)];
-    page_b = table[min((key + 16) >> c.log2p, last_blk)];
-  };
-  auto start = [&](int i, int s) {
-    const int key = 32 * (t0 + i * step);
-    const int bad_a = (unsigned)page_a >= (unsigned)n_pages, bad_b = (unsigned)page_b >= (unsigned)n_pages;
-    const uint8_t* ra = c.pages + ((int64_t)(bad_a ? 0 : page_a) * c.kv_heads + kvh) * (int64_t)c.record;
-    const uint8_t* rb = c.pages + ((int64_t)(bad_b ? 0 : page_b) * c.kv_heads + kvh) * (int64_t)c.record;
-    look_up(i + 1);
-    dead_of[s] = bad_a | (bad_b << 1);
-    dma_tile<D, GS>(ring_at + s * R::BYTES, ra, rb, key & (P - 1), P, lo);
-  };
-  if (n_tiles > 0) look_up(0);
+    const int len = ex.len, pos0 = ex.pos0, row0 = ex.row0, n_cols = ex.rows * group;
+    const int last_i = ex.rows - 1;
+    int t_lo = ex.t_lo, t_hi = ex.t_hi;
+    bool whole_seq = true;
+    if constexpr (DIVIDED) {
+      const unsigned take = min(left, weight - s.offset);
+      whole_seq = take == weight;
+      t_lo += s.offset;
+      t_hi = min(t_hi, t_lo + (int)take);
+      if (s.offset == 0 && threadIdx.x == 0) {
+        int2 w;
+        w.x = index + b;
+        w.y = (int)((s.at + weight - 1) / s.share) - index + 1;
+        *(int2*)(part.parts + 2 * ((int64_t)b * c.kv_heads + kvh)) = w;
+      }
+      left -= take;
+      s.at += take;
+      s.offset = 0;
+    } else {
+      left = 0;
+    }
+    const int x = lane & 15, xi = x / group;
+    const bool has = x < n_cols;
+    const QueryRow<D, GS> query = read_query<D, GS>(
+        has ? (const uint16_t*)a.q + (int64_t)(row0 + xi) * a.qt + (int64_t)(kvh * group + x - xi * group) * a.qh
+            : nullptr,
+        lane >> 4);
+    // (the table is not written here: scalar loads)
+    const auto* table = (const __attribute__((address_space(4))) int32_t*)(uintptr_t)(
+        c.table + (int64_t)b * c.max_blocks);
+    const int last_blk = max(0, (len - 1) >> c.log2p);
+    WeightScale ws;
+    const int t0 = t_lo + wave;
+    // tiles t0, t0 + step, ...: tile i of the wave in stage i mod NS
+    const int n_tiles = t_hi > t0 ? (t_hi - t0 + step - 1) / step : 0;
+    int dead_of[NS];
+    // the table entries of the next tile to start, read one tile ahead
+    int page_a, page_b;
+    auto look_up = [&](int i) {
+      const int key = 32 * (t0 + i * step);
+      page_a = table[min(key >> c.log2p, last_blk)];
+      page_b = table[min((key + 16) >> c.log2p, last_blk)];
+    };
+    auto start = [&](int i, int s) {
+      const int key = 32 * (t0 + i * step);
+      const int bad_a = (unsigned)page_a >= (unsigned)n_pages, bad_b = (unsigned)page_b >= (unsigned)n_pages;
+      const uint8_t* ra = c.pages + ((int64_t)(bad_a ? 0 : page_a) * c.kv_heads + kvh) * (int64_t)c.record;
+      const uint8_t* rb = c.pages + ((int64_t)(bad_b ? 0 : page_b) * c.kv_heads + kvh) * (int64_t)c.record;
+      look_up(i + 1);
+      dead_of[s] = bad_a | (bad_b << 1);
+      dma_tile<D, GS>(ring_at + s * R::BYTES, ra, rb, key & (P - 1), P, lo);
+    };
+    if (n_tiles > 0) look_up(0);
 #pragma unroll
-  for (int s = 0; s < NS; ++s)
-    if (s < n_tiles) start(s, s);
-  // the query's arithmetic while the first tiles come in
-  Column<D, GS> col;
-  set_query<D, GS>(col, query, a.bf16, a.scale);
-  col.pos = has ? pos0 + xi : -1;
-  for (int i0 = 0; i0 < n_tiles; i0 += NS) {
+    for (int s = 0; s < NS; ++s)
+      if (s < n_tiles) start(s, s);
+    // the query's arithmetic while the first tiles come in
+    Column<D, GS> col;
+    set_query<D, GS>(col, query, a.bf16, a.scale);
+    col.pos = has ? pos0 + xi : -1;
+    for (int i0 = 0; i0 < n_tiles; i0 += NS) {
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      const int i = i0 + s;
-      if (i < n_tiles) {
-        // this stage's DMAs have landed: NS - 1 later tiles may be in flight
-        if (i + NS <= n_tiles) wait_dma<(NS - 1) * R::DMAS>();
-        else wait_dma<0>();
-        TileRegs<D, GS> r;
-        read_tile<D, GS>(r, ring + s * R::BYTES, lane);
-        wait_lds();  // the stage is in registers: refill it
-        const int dead = dead_of[s];
-        if (i + NS < n_tiles) start(i + NS, s);
-        const int key0 = 32 * (t0 + i * step);
-        // every key of the tile exists and every column sees all of it
-        const bool whole = !dead && key0 + 32 <= len && key0 + 31 <= pos0 &&
-                           key0 >= pos0 + last_i - lo_off;
-        do_tile<D, GS>(r, col, whole, key0, len, lo_off, dead, ws, cc, lane);
+      for (int s = 0; s < NS; ++s) {
+        const int i = i0 + s;
+        if (i < n_tiles) {
+          // this stage's DMAs have landed: NS - 1 later tiles may be in flight
+          if (i + NS <= n_tiles) wait_dma<(NS - 1) * R::DMAS>();
+          else wait_dma<0>();
+          TileRegs<D, GS> r;
+          read_tile<D, GS>(r, ring + s * R::BYTES, lane);
+          wait_lds();  // the stage is in registers: refill it
+          const int dead = dead_of[s];
+          if (i + NS < n_tiles) start(i + NS, s);
+          const int key0 = 32 * (t0 + i * step);
+          // every key of the tile exists and every column sees all of it
+          const bool whole = !dead && key0 + 32 <= len && key0 + 31 <= pos0 &&
+                             key0 >= pos0 + last_i - lo_off;
+          do_tile<D, GS>(r, col, whole, key0, len, lo_off, dead, ws, cc, lane);
+        }
       }
     }
-  }
 
-  finish<D, GS>(col);
+    finish<D, GS>(col);
 
-  {
-    // the waves' results joined in wave order: each scaled to the block's largest M
-    float (*so)[16][D + 4] = (float (*)[16][D + 4])lds;
-    float (*sm)[16] = (float (*)[16])(so + WAVES);
-    float (*sl)[16] = sm + WAVES;
-    __syncthreads();  // the rings are done with
-    const int cx = lane & 15;
+    {
+      // the waves' results joined in wave order: each scaled to the block's largest M
+      float (*so)[16][D + 4] = (float (*)[16][D + 4])lds;
+      float (*sm)[16] = (float (*)[16])(so + WAVES);
+      float (*sl)[16] = sm + WAVES;
+      __syncthreads();  // the rings are done with
+      const int cx = lane & 15;
 #pragma unroll
-    for (int n = 0; n < X::N; ++n) *(f32x4*)&so[wave][cx][16 * n + 4 * (lane >> 4)] = col.o[n];
-    if ((lane >> 4) == 0) {
-      sm[wave][cx] = col.M();
-      sl[wave][cx] = col.l;
-    }
-    __syncthreads();
-    // thread -> column, 4 channels at a time
-    for (int w = threadIdx.x; w < 16 * (D / 4); w += 64 * WAVES) {
-      const int cx = w / (D / 4), ch = (w % (D / 4)) * 4;
-      if (cx >= n_cols) continue;
-      float M = sm[0][cx];
-#pragma unroll
-      for (int i = 1; i < WAVES; ++i) M = fmaxf(M, sm[i][cx]);
-      float l = 0.0f;
-      f32x4 o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < WAVES; ++i) {
-        if (sm[i][cx] == kNegInf) continue;
-        const float k = __builtin_amdgcn_exp2f(sm[i][cx] - M);
-        l = fmaf(sl[i][cx], k, l);
-        const f32x4 v = *(const f32x4*)&so[i][cx][ch];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = fmaf(v[e], k, o[e]);
+      for (int n = 0; n < X::N; ++n) *(f32x4*)&so[wave][cx][16 * n + 4 * (lane >> 4)] = col.o[n];
+      if ((lane >> 4) == 0) {
+        sm[wave][cx] = col.M();
+        sl[wave][cx] = col.l;
       }
-      const int i = cx / group, h = cx - i * group;
-      const int64_t r = (int64_t)(row0 + i) * a.heads + kvh * group + h;
-      if (DIVIDED && !whole_seq) {
-        const int64_t slot = ((int64_t)kvh * (part.splits + c.n_seqs) + index + b) * 16 + cx;
-        *(f32x4*)(part.o + slot * D + ch) = o;
-        if (ch == 0) *(float2*)(part.ml + slot * 2) = float2{M, l};
-      } else {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const float v[4] = {o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
-        store4(a.out, r * D + ch, a.bf16, v);
-        if (ch == 0 && a.lse) a.lse[r] = lse_of(M, l);
+      __syncthreads();
+      // thread -> column, 4 channels at a time
+      for (int w = threadIdx.x; w < 16 * (D / 4); w += 64 * WAVES) {
+        const int cx = w / (D / 4), ch = (w % (D / 4)) * 4;
+        if (cx >= n_cols) continue;
+        float M = sm[0][cx];
+#pragma unroll
+        for (int i = 1; i < WAVES; ++i) M = fmaxf(M, sm[i][cx]);
+        float l = 0.0f;
+        f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) {
+          if (sm[i][cx] == kNegInf) continue;
+          const float k = __builtin_amdgcn_exp2f(sm[i][cx] - M);
+          l = fmaf(sl[i][cx], k, l);
+          const f32x4 v = *(const f32x4*)&so[i][cx][ch];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = fmaf(v[e], k, o[e]);
+        }
+        const int i = cx / group, h = cx - i * group;
+        const int64_t r = (int64_t)(row0 + i) * a.heads + kvh * group + h;
+        if (DIVIDED && !whole_seq) {
+          const int64_t slot = ((int64_t)kvh * (part.splits + c.n_seqs) + index + b) * 16 + cx;
+          *(f32x4*)(part.o + slot * D + ch) = o;
+          if (ch == 0) *(float2*)(part.ml + slot * 2) = float2{M, l};
+        } else {
+          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+          const float v[4] = {o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
+          store4(a.out, r * D + ch, a.bf16, v);
+          if (ch == 0 && a.lse) a.lse[r] = lse_of(M, l);
+        }
       }
     }
-  }
-  if (DIVIDED && left > 0) __syncthreads();  // the next sequence's tiles go where this one's sums lie
+    // the next sequence's tiles go where this one's sums lie
+    if (DIVIDED && left > 0) __syncthreads();
   }
 }
 
@@ -824,7 +829,7 @@ constexpr int wide_tiles(int dim, int group) { return dim / group > 2 ? 1 : 2; }
 template <int D, int GS>
 struct Wide {
   using X = Geo<D, GS>;
-    static constexpr int NC = wide_tiles(D, GS);           // column tiles a wave
+  static constexpr int NC = wide_tiles(D, GS);       // column tiles a wave
   static constexpr int COLS = 16 * NC * kWaves;      // columns a block
   static constexpr int K_BYTES = 2 * 2 * X::KW * 1024;  // [32 keys][result j][word][lane] pieces
   static constexpr int V_BYTES = 2 * X::N * 1024;       // [32 keys][value result][lane] pieces
@@ -1396,15 +1401,20 @@ Kv4Plan kv4_plan(int64_t n_seqs, int heads, int kv_heads, int dim, int group, in
   p.tiles = 1;
   p.splits = 1;
   const int64_t blocks = n_seqs * kv_heads;
-  // short sequences in few blocks: eight waves a block and no second launch (one sequence of 777
-  // tokens, 8 key heads: MSHORT_8 us, divided MSHORT_D)
-  if (blocks <= 256 && keys <= 2048) p.waves = 8;
-  // else the work is divided over two blocks a compute unit (one sequence of 131072 tokens: 39 us
-  // with 512 blocks, 42 with 1024, 65 with 4096), unless there are many sequences or short ones,
-  // for which a second launch costs more than their different lengths (64 sequences of MS_L tokens:
-  // MS_A us a block a sequence, MS_B divided; of 250 to 1000: MT_A and MT_B)
-  else if (blocks < 4096 && (blocks < 512 || keys > 1024) && n_seqs * (keys / 32 + 2) < ((int64_t)1 << 30))
+  // Dividing the keys over two blocks a compute unit (one sequence of 131072 tokens: 39 us with 512
+  // blocks, 42 with 1024, 65 with 4096) costs a second launch and a start for each part of a
+  // sequence; it pays once sequences are long for their number.  8 key heads of 128, lengths from
+  // a quarter of the largest to the largest, undivided and divided: one sequence of 1024 tokens
+  // 11.9 and 11.7 us, of 4096 27.2 and 12.5; 8 sequences up to 2048 16.9 and 19.0, up to 3072
+  // 22.0 and 19.9; 32 up to 4096 31.2 and 33.1, up to 6144 40.7 and 40.0; 64 up to 4096 46.4 and
+  // 46.9, up to 8192 87.8 and 84.7; 256 up to 8192 291 and 288.
+  if (keys > std::min<int64_t>(1024 + 20 * blocks, 5120) && blocks <= 2048 &&
+      n_seqs * (keys / 32 + 2) < ((int64_t)1 << 30))
     p.splits = std::max(512 / kv_heads, 1);
+  // Undivided: eight waves a block where the blocks are no more than the compute units (32
+  // sequences up to 2048 tokens: 22.1 us with four, 20.2 with eight), else four (64: 28.7 and 34.5).
+  else if (blocks <= 256)
+    p.waves = 8;
   return p;
 }
 
