@@ -72,8 +72,9 @@ int awq_int8_matmul(const int8_t* xq, int64_t ldx, const float* xstep, int64_t n
                     void* workspace, size_t workspace_bytes, void* stream);
 
 /* The linear layer on floating activations: awq_int8_quantize of x (AWQ_FOLD_DIVIDE by s if
- * s is given) and awq_int8_matmul, with the same result bit for bit.  A few tokens run in one
- * launch that quantises the tokens on the fly; otherwise the codes go to the workspace.
+ * s is given) and awq_int8_matmul, with the same result bit for bit.  One token of up to
+ * 16384 columns runs in one launch that quantises it on the fly; otherwise the codes go to the
+ * workspace.
  *   x fp16 or bf16 [n_tokens][ldx >= in_features], y, bias in the same type; other arguments
  *   as above. */
 size_t awq_int8_linear_workspace_bytes(int64_t n_tokens, int64_t out_features,
@@ -148,9 +149,10 @@ int awq_kv4_read(const void* cache, int64_t n_pages, const int32_t* block_table,
  *   t <= position of r (and t > position - window if window > 0), with key/value head
  *   h / (heads / kv_heads); lse[r][h] = log sum_t exp(scale q . k_t).
  * A row without keys gives out 0 and lse -infinity.  Scores, softmax statistics and sums are
- * fp32; q enters the products exactly in fp16 (each row scaled by a power of two), the
- * probabilities times the value's step rounded to fp16 with 2^-11 relative error.  The order
- * of every sum is fixed: results repeat bit for bit for the same bounds.
+ * fp32; q enters the products in fp16, each row scaled by a power of two (exact but for parts
+ * 2^-24 and more below the row's largest), the probabilities times the value's step rounded to
+ * fp16 with 2^-11 relative error; keys and values enter as the integers code - zero, with zeros
+ * 0 .. 15.  The order of every sum is fixed: results repeat bit for bit for the same bounds.
  *   q        as above, n_tokens rows, heads a multiple of kv_heads
  *   max_q    bound on the rows of one sequence, max_len bound on seq_lens (both host values:
  *            they size the launch; rows and keys beyond them are not computed)

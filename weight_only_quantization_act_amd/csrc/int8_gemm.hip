@@ -4,7 +4,7 @@
 // int32, so neither the order of the sum nor a split of it changes a result.
 //
 // Tiles (many tokens): both operands are K-contiguous bytes.  A block computes BT tokens x BM
-// outputs from tiles of 128 bytes of K, which move global -> LDS by DMA into a ring of two
+// outputs from tiles of 128 bytes of K, which move global -> LDS by DMA into a ring of NS
 // stages (rows of 128 bytes, the 16-byte chunk index XOR-swizzled with the row, so that the
 // fragment reads of 32 rows are free of bank conflicts), and feeds
 // v_mfma_i32_32x32x32_i8: lane l supplies 16 bytes of row l mod 32 at chunk 2 k + l div 32 for
@@ -43,6 +43,10 @@ struct Tile {
   __device__ static int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 };
 
+// Bound by the matrix cores: 256 x 256 tiles on sixteen waves of 128 x 32, one block a compute
+// unit, do 8192 tokens through 28672 x 8192 in 1.70 ms, 2.27 Pop/s (128 x 128 tiles, two blocks a
+// compute unit, 2.19 ms).  Small tiles keep more blocks for fewer tokens; see plan_of.
+//
 // splits > 1: block z sums its share of K and stores the int32 tile to part [splits][T][M].
 template <class S, bool BF16>
 __global__ __launch_bounds__(S::THREADS) void k_int8_tiles(Int8Args a, int tiles_t, int tiles_m,
@@ -240,10 +244,10 @@ __global__ __launch_bounds__(256) void k_int8_finish(Int8Args a, int splits,
 // from memory to the operand registers of v_mfma_i32_16x16x64_i8 directly (lane l: 16 bytes of
 // row l mod 16 at 16 (l div 16); four instructions cover 256 contiguous bytes of a row), the
 // next piece's ahead of the products of this one; the tokens' operands come from L2.  The
-// waves' int32 sums are added through LDS.  Measured: one token, 4096 x 4096 with the quantisation
-// 6 us (2.8 TB/s; a launch alone is 2), 16 tokens, 11008 x 4096 without it 15 us (3.0 TB/s): short
-// of the memory's rate because 512 threads a block start, load twice or four times and end.  Result element e of lane l is output
-// 4 (l div 16) + e, token l mod 16.
+// waves' int32 sums are added through LDS.  Result element e of lane l is output 4 (l div 16) + e,
+// token l mod 16.  Measured: 16 tokens, 11008 x 4096 15 us (3.0 TB/s), one token, 4096 x 4096 with
+// the quantisation 7 to 9 us: short of the memory's rate because a wave has two pieces to load
+// between its start and its end.
 //
 // FUSED (one token): the block first quantises the token into LDS, with the first weights
 // already on their way; every block repeats that (a few thousand values from L2) in place of a

@@ -38,7 +38,7 @@
 // More columns (prompts): column tiles a wave, and the codes are decoded once a block; bound by
 // the vector instructions of the softmax and by the products, which share the issue.  A prompt of
 // 4096 tokens, 32 heads on 8: 188 us, 0.73 PFLOP/s.  One form for both would decode the codes once a
-// column tile (the prompt: 524 us), or leave three of four waves without work at a single token.
+// column tile (the prompt: 523 us), or leave three of four waves without work at a single token.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -33,7 +33,7 @@ __device__ __forceinline__ float quotient(float a, float b, float y) {
 // values: the quantiser of quantizer.h (4 bits, no channel scales) with the same results.  Values
 // of 16 bits tie often (a wave of them nearly always somewhere), so the quotients are all
 // corrected, without its test for half-integers and division behind a branch (write of 27000
-// tokens, 8 heads: 39 us with the test, 35 without).
+// tokens, 8 heads: 39 us with the test, 35 without and with ZP a template argument).
 template <bool BF16, int LANES, bool ZP>
 __device__ __forceinline__ uint32_t quantise_group(const uint4 raw, uint32_t& par) {
   const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w};
