@@ -122,8 +122,8 @@ def _rows(t: torch.Tensor, name: str, dtype: Optional[torch.dtype] = None) -> in
 
 def _vec(t: torch.Tensor, dtype: torch.dtype, name: str, n: int) -> int:
     """Check a contiguous device vector of n elements; returns its address."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.dim() == 1
-            and t.shape[0] == n and t.is_contiguous()):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == (n,) and t.is_cuda
+            and t.is_contiguous()):
         _dev(t, dtype, name, (n,))
     return t.data_ptr()
 
@@ -168,9 +168,9 @@ def awq_int8_linear_workspace_bytes(n_tokens: int, out_features: int, in_feature
     return int(lib().awq_int8_linear_workspace_bytes(n_tokens, out_features, in_features))
 
 
-def _out_rows(T, M, dtype, out, device):
+def _out_rows(T, M, dtype, out, like):
     if out is None:
-        return torch.empty((T, M), dtype=dtype, device=device), M
+        return like.new_empty((T, M), dtype=dtype), M
     ldy = _rows(out, "out", dtype)
     if tuple(out.shape) != (T, M):
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {(T, M)}")
@@ -203,7 +203,7 @@ def awq_int8_matmul(xq: torch.Tensor, xstep: torch.Tensor, wq: torch.Tensor, wst
     dt = _dtype(dtype, "dtype")
     px, pw = _vec(xstep, _FP32, "xstep", T), _vec(wstep, _FP32, "wstep", M)
     pb = None if bias is None else _vec(bias, dtype, "bias", M)
-    y, ldy = _out_rows(T, M, dtype, out, xq.device)
+    y, ldy = _out_rows(T, M, dtype, out, xq)
     if T == 0 or M == 0:
         return y
     py = y.data_ptr()
@@ -232,7 +232,7 @@ def awq_int8_linear(x: torch.Tensor, wq: torch.Tensor, wstep: torch.Tensor,
     pw = _vec(wstep, _FP32, "wstep", M)
     ps = None if s is None else _vec(s, _FP32, "s", K)
     pb = None if bias is None else _vec(bias, dtype, "bias", M)
-    y, ldy = _out_rows(T, M, dtype, out, x.device)
+    y, ldy = _out_rows(T, M, dtype, out, x)
     if T == 0 or M == 0:
         return y
     py = y.data_ptr()
@@ -262,21 +262,33 @@ def _kv4_args(cache, table, lens, starts, cfg):
     """Check the cache and its index tensors; returns the number of sequences."""
     d, p, hk, g = cfg.head_dim, cfg.page_size, cfg.kv_heads, cfg.group_size
     rec = p * (d + 8 * (d // g)) if g > 0 else 0  # the C side refuses what is no configuration
-    if not (isinstance(cache, torch.Tensor) and cache.is_cuda and cache.dtype == _U8
-            and cache.dim() == 3 and cache.shape[1] == hk and cache.shape[2] == rec
-            and cache.is_contiguous()):
-        if awq_kv4_record_bytes(cfg) == 0:
-            raise ValueError("invalid awq_kv4_config")
-        _dev(cache, _U8, "cache")
-        raise ValueError(f"cache has shape {tuple(cache.shape)}, expected [n_pages, {hk}, {rec}]")
-    if not (isinstance(table, torch.Tensor) and table.is_cuda and table.dtype == _INT32
-            and table.dim() == 2 and table.is_contiguous()):
-        _dev(table, _INT32, "block_table")
+    try:
+        cs, ts = cache.shape, table.shape
+        n = ts[0]
+        if (cache.dtype is _U8 and cs[1] == hk and cs[2] == rec and len(cs) == 3 and cache.is_cuda
+                and cache.is_contiguous() and table.dtype is _INT32 and len(ts) == 2 and table.is_cuda
+                and table.is_contiguous() and lens.dtype is _INT32 and lens.shape == (n,) and lens.is_cuda
+                and lens.is_contiguous() and starts.dtype is _INT32 and starts.shape == (n + 1,)
+                and starts.is_cuda and starts.is_contiguous()):
+            return n
+    except (AttributeError, IndexError, TypeError):
+        pass
+    _kv4_complain(cache, table, lens, starts, cfg, rec)
+
+
+def _kv4_complain(cache, table, lens, starts, cfg, rec):
+    """Say which of the arguments that _kv4_args refused is wrong."""
+    if awq_kv4_record_bytes(cfg) == 0:
+        raise ValueError("invalid awq_kv4_config")
+    _dev(cache, _U8, "cache")
+    if cache.dim() != 3 or tuple(cache.shape[1:]) != (cfg.kv_heads, rec):
+        raise ValueError(f"cache has shape {tuple(cache.shape)}, expected [n_pages, {cfg.kv_heads}, {rec}]")
+    _dev(table, _INT32, "block_table")
+    if table.dim() != 2:
         raise ValueError("block_table must be [n_seqs, max_blocks]")
-    n = table.shape[0]
-    _vec(lens, _INT32, "seq_lens", n)
-    _vec(starts, _INT32, "q_start", n + 1)
-    return n
+    _dev(lens, _INT32, "seq_lens", (table.shape[0],))
+    _dev(starts, _INT32, "q_start", (table.shape[0] + 1,))
+    raise ValueError("invalid cache arguments")
 
 
 def _heads(t, name, heads, dim, dtype=None):
@@ -285,7 +297,7 @@ def _heads(t, name, heads, dim, dtype=None):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device (HIP) tensor")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     shape = t.shape
     if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
@@ -328,8 +340,8 @@ def awq_kv4_read(cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch
     n = _kv4_args(cache, block_table, seq_lens, q_start, cfg)
     dt = _dtype(dtype, "dtype")
     shape = (n_tokens, cfg.kv_heads, cfg.head_dim)
-    k = torch.empty(shape, dtype=dtype, device=cache.device)
-    v = torch.empty(shape, dtype=dtype, device=cache.device)
+    k = cache.new_empty(shape, dtype=dtype)
+    v = torch.empty_like(k)
     if n_tokens == 0:
         return k, v
     if n == 0:
@@ -369,15 +381,15 @@ def awq_kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.T
     qt, qh = _heads(q, "q", None, d)
     T, H, _ = q.shape
     if out is None:
-        out = torch.empty((T, H, d), dtype=dtype, device=q.device)
+        out = q.new_empty((T, H, d))
     else:
         _dev(out, dtype, "out", (T, H, d))
-    lse = torch.empty((T, H), dtype=_FP32, device=q.device)
+    lse = q.new_empty((T, H), dtype=_FP32)
     if T == 0 or n == 0:
         return out, lse
-    ws, pws, nws = _workspace(
-        workspace, _attention_workspace(T, n, H, d, cfg.kv_heads, cfg.page_size, cfg.group_size, max_q,
-                                        max_len) if workspace is None else 0, q.device)
+    need = 0 if workspace is not None else _attention_workspace(
+        T, n, H, d, cfg.kv_heads, cfg.page_size, cfg.group_size, max_q, max_len)
+    ws, pws, nws = _workspace(workspace, need, q.device)
     st = lib().awq_kv4_attention(q.data_ptr(), qt, qh, T, H, dt, cache.data_ptr(), cache.shape[0],
                                  block_table.data_ptr(), n, block_table.shape[1],
                                  seq_lens.data_ptr(), q_start.data_ptr(), cfg, max_q, max_len,
