@@ -111,7 +111,7 @@ int awq_int8_linear(const void* x, int64_t ldx, const float* s, int64_t n_tokens
  *   q_start      int32 [n_seqs + 1], ascending from 0: rows q_start[b] .. q_start[b + 1] - 1 of
  *                k, v and q are the last tokens of sequence b (positions seq_lens[b] - count
  *                .. seq_lens[b] - 1).  Rows at negative positions do not exist: they are not
- *                written, read as zeros and attend to nothing
+ *                written, read as zeros and attend to nothing.  Nor do rows past n_tokens
  *   k, v, q      fp16 or bf16 [token][head][head_dim], unit stride in head_dim, token and head
  *                strides in elements (multiples of 8, 16-byte aligned base)
  * All sizes are device data except the bounds named below; a call may be captured and replayed

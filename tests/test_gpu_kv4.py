@@ -401,6 +401,24 @@ def test_bounds_strides_and_lost_pages():
         _within(c.lay, got[r:r + 1], lse[r:r + 1], ref, r)
 
 
+def test_fewer_rows_than_the_starts_say():
+    """q_start may point past the rows that q has: those rows do not exist."""
+    for lens, news, T in (((40, 90), (5, 7), 9), ((40, 90, 3), (50, 40, 1), 70), ((3000, 2500), (2, 3), 4)):
+        c = Case(128, 2, 32, 64, 1, lens, news, seed=T)
+        c.fill()
+        n = sum(news)
+        q = torch.randn(n, 4, 128, device="cuda").half()
+        a, la = awq.awq_kv4_attention(q, c.cache, c.dtable, c.dlens, c.dstarts, c.cfg, max_q=max(news),
+                                      max_len=max(lens))
+        out = torch.full((n, 4, 128), 7.0, device="cuda").half()
+        b, lb = awq.awq_kv4_attention(q[:T], c.cache, c.dtable, c.dlens, c.dstarts, c.cfg, max_q=max(news),
+                                      max_len=max(lens), out=out[:T])
+        assert (out[T:] == 7).all()
+        # the same keys in the same order, but for where a division of the work cuts them
+        assert torch.allclose(b.float(), a[:T].float(), rtol=2.0 ** -10, atol=2.0 ** -9)
+        assert torch.allclose(lb, la[:T], rtol=0, atol=2.0 ** -17)
+
+
 def test_offsets_beyond_32_bits():
     """Pages whose bytes lie past 4 GiB of the cache."""
     cfg = awq.awq_kv4_config(128, 8, 256, 128, 1)

@@ -538,7 +538,7 @@ __device__ __forceinline__ Extent extent_of(const Kv4Cache& c, const Kv4Query& a
   Extent e;
   e.row0 = starts[b];
   const int count = starts[b + 1] - e.row0, len0 = lens[b];
-  e.rows = min(count, a.max_q);
+  e.rows = min(min(count, a.max_q), (int)a.n_tokens - e.row0);
   // bounded by the table and by the caller's bound
   e.len = min(len0, (int)min((int64_t)c.max_blocks << c.log2p, (int64_t)a.max_len));
   e.pos0 = len0 - count;
@@ -895,7 +895,7 @@ void k_kv4_attention_wide(Kv4Cache c, Kv4Query a, Partials part) {
   const int b = at.seq, kvh = at.head, split = at.split, tile = at.tile;
   const int group = a.heads / c.kv_heads;
   const int row0 = c.starts[b];
-  const int rows = min(c.starts[b + 1] - row0, a.max_q);
+  const int rows = min(min(c.starts[b + 1] - row0, a.max_q), (int)a.n_tokens - row0);
   const int len0 = c.lens[b];
   const int n_cols = rows * group;
   if (tile * W::COLS >= n_cols) return;  // the whole block
