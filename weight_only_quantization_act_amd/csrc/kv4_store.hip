@@ -20,10 +20,13 @@ namespace awq {
 
 namespace {
 
-// a / b, correctly rounded, from y = RN(1 / b): the residual a - b q of a quotient q within an ulp
-// is exact in one fused multiply-add, and q plus residual times y rounds to RN(a / b)
-// (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990)
-// while nothing underflows.
+// a / b from y = RN(1 / b), while nothing underflows: the residual a - b q of the product q = a y is
+// exact in one fused multiply-add (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990), so that the last one rounds a / b to within 2^-23 of an ulp.  That
+// is RN(a / b) unless a / b lies that near the middle of two floats.  For b = 15 or 7 none does
+// (1 / 30 of an ulp at least).  Of the other quotients only rint is used, so only those near
+// k + 1/2, k < 16, count: for a 16-bit a they come that near the middle beside k + 1/2 only with a =
+// S (k + 1/2), S of few bits, and b one ulp beside S, and then only for b of all mantissa bits.
 __device__ __forceinline__ float quotient(float a, float b, float y) {
   const float q = a * y;
   return fmaf(fmaf(-q, b, a), y, q);
@@ -61,7 +64,7 @@ __device__ __forceinline__ uint32_t quantise_group(const uint4 raw, uint32_t& pa
   const float range = hi - lo, top = ZP ? 15.0f : 7.0f;
   float st = quotient(range, top, ZP ? 1.0f / 15.0f : 1.0f / 7.0f);
   // what the corrected quotients do not cover: steps whose residuals may underflow, and those of
-  // all mantissa bits, whose reciprocal one step of Newton's need not round correctly
+  // all mantissa bits (whose reciprocal one step of Newton's need not round correctly either)
   const uint32_t bits = __builtin_bit_cast(uint32_t, st);
   const bool rare = st < 0x1p-90f || (bits & 0x7fffffu) == 0x7fffffu;
   float q[8], z;
