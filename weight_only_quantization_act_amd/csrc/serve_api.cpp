@@ -74,7 +74,8 @@ int awq_int8_quantize(const void* A, int64_t rows, int64_t cols, int64_t lda, in
 
 size_t awq_int8_matmul_workspace_bytes(int64_t T, int64_t M, int64_t K) {
   if (T <= 0 || M <= 0 || K <= 0 || T > kMaxRows || M > kMaxRows || K > awq::kInt8MaxK) return 0;
-  return round_up(awq::int8_matmul_workspace(T, M, K), kAlign);
+  // planned, as the launch is, from the columns that are read: rows of whole 16-byte chunks
+  return round_up(awq::int8_matmul_workspace(T, M, round16(K)), kAlign);
 }
 
 int awq_int8_matmul(const int8_t* xq, int64_t ldx, const float* xstep, int64_t n_tokens,
