@@ -1,11 +1,15 @@
 """How the serving operators lay a call out, on the host: the workspace that a query names covers
 what the call it is made for uses.  Nothing is launched (fake pointers, never dereferenced)."""
+import ctypes
 import random
 
 import pytest
 
 import weight_only_quantization_act_amd as awq
 from weight_only_quantization_act_amd import _serve
+
+
+DEVICE = 6  # a pointer that must be device memory is not
 
 
 @pytest.fixture(scope="module")
@@ -29,3 +33,41 @@ def test_int8_workspace_counts_whole_chunks(L):
         assert L.awq_int8_linear_workspace_bytes(T, M, K) == L.awq_int8_linear_workspace_bytes(T, M, whole), \
             (T, M, K)
     assert divided > 500
+
+
+def _attend(L, cfg, n, heads, max_q, max_len, window, ws, nbytes):
+    P = ctypes.c_void_p(0x10000)
+    return L.awq_kv4_attention(P, cfg.head_dim * heads, cfg.head_dim, n * max_q, heads, 0, P, 10, P, n, 4, P,
+                               P, ctypes.byref(cfg), max_q, max_len, 0.1, window, P, P, ws, nbytes, None)
+
+
+def test_attention_workspace_covers_every_window(L):
+    """A call is given what the query names, which does not know the window.  A window is a smaller
+    bound on the keys, so a larger bound may never need less; and no window makes the call ask for
+    more than it was given: with these pointers it gets as far as finding that they are no device
+    memory."""
+    rng = random.Random(2)
+    P = ctypes.c_void_p(0x10000)
+    sizes = [(64, 8, 8, 1, 1 << 30, 8192), (32, 8, 4, 1, 1 << 30, 8192), (64, 8, 8, 1, 1 << 29, 8192),
+             (2048, 1, 4, 1, 1 << 24, 8192), (40, 8, 4, 1, 1 << 30, 6000), (4, 2, 1, 40, 1 << 30, 3)]
+    for _ in range(3000):
+        hk = rng.choice([1, 2, 8, 40])
+        sizes.append((round(2 ** rng.uniform(0, 12)), hk, rng.choice([1, 3, 8]),
+                      rng.choice([1, 1, 2, 5, round(2 ** rng.uniform(0, 10))]),
+                      round(2 ** rng.uniform(0, 30)), round(2 ** rng.uniform(0, 31))))
+    needed = 0
+    for n, hk, grp, max_q, max_len, window in sizes:
+        cfg = awq.awq_kv4_config(128, hk, 64, 128, 1)
+        H = hk * grp
+
+        def query(length):
+            return L.awq_kv4_attention_workspace_bytes(n * max_q, n, H, ctypes.byref(cfg), max_q, length)
+        need = query(max_len)
+        needed += need > 0
+        where = (n, hk, grp, max_q, max_len, window)
+        for smaller in (window + max_q, window, max_len // 2, 5000, 6000, 100000):
+            assert query(min(smaller, max_len)) <= need, (where, smaller)
+        for w in (0, window, 1, 8192):
+            got = _attend(L, cfg, n, H, max_q, max_len, w, P if need else None, need)
+            assert got == DEVICE, (where, w, need, got)
+    assert needed > 500

@@ -1384,6 +1384,9 @@ hipError_t launch_dg(const Kv4Cache& c, const Kv4Query& q, const Kv4Plan& p, con
 
 }  // namespace
 
+// Keys beyond which few columns are divided whatever the number of sequences.
+constexpr int64_t kUndivided = 5120;
+
 Kv4Plan kv4_plan(int64_t n_seqs, int heads, int kv_heads, int dim, int group, int64_t max_q,
                  int64_t max_len, int64_t window) {
   Kv4Plan p;
@@ -1412,7 +1415,7 @@ Kv4Plan kv4_plan(int64_t n_seqs, int heads, int kv_heads, int dim, int group, in
   // 11.9 and 11.7 us, of 4096 27.2 and 12.5; 8 sequences up to 2048 16.9 and 19.0, up to 3072
   // 22.0 and 19.9; 32 up to 4096 31.2 and 33.1, up to 6144 40.7 and 40.0; 64 up to 4096 46.4 and
   // 46.9, up to 8192 87.8 and 84.7; 256 up to 8192 291 and 288.
-  if (keys > std::min<int64_t>(1024 + 20 * blocks, 5120) && blocks <= 2048 &&
+  if (keys > std::min(1024 + 20 * blocks, kUndivided) && blocks <= 2048 &&
       n_seqs * (keys / 32 + 2) < ((int64_t)1 << 30))
     p.splits = std::max(512 / kv_heads, 1);
   // Undivided: eight waves a block where the blocks are no more than the compute units (32
@@ -1435,6 +1438,19 @@ size_t kv4_workspace(const Kv4Plan& p, int64_t n_tokens, int64_t n_seqs, int hea
   if (p.splits <= 1) return 0;
   return (size_t)kv4_slots(p, n_tokens, n_seqs, heads, kv_heads) * (dim + 2) * sizeof(float) +
          (p.wide ? 0 : (size_t)n_seqs * kv_heads * 2 * sizeof(int32_t));
+}
+
+size_t kv4_workspace_any_window(int64_t n_tokens, int64_t n_seqs, int heads, int kv_heads, int dim,
+                                int group, int64_t max_q, int64_t max_len) {
+  auto of = [&](int64_t keys) {
+    return kv4_workspace(kv4_plan(n_seqs, heads, kv_heads, dim, group, max_q, keys, 0), n_tokens, n_seqs,
+                         heads, kv_heads, dim);
+  };
+  // A window is a smaller bound on the keys.  The parts of the wide form grow with that bound.  Few
+  // columns have one number of parts or none, and none also where the tiles are too many to count, so
+  // that a window may divide what the whole length does not: the fewest keys that are divided in any
+  // case (or all) decide that.
+  return std::max(of(max_len), of(std::min(max_len, kUndivided + 1)));
 }
 
 hipError_t launch_kv4_attention(const Kv4Cache& c, const Kv4Query& q, const Kv4Plan& p,

@@ -254,10 +254,9 @@ size_t awq_kv4_attention_workspace_bytes(int64_t n_tokens, int64_t n_seqs, int64
                                          int64_t max_len) {
   if (!kv4_valid(cfg) || attention_shape(n_tokens, n_seqs, heads, cfg, max_q, max_len)) return 0;
   if (n_tokens == 0 || n_seqs == 0 || max_q == 0) return 0;
-  // without a window: with one there are no more splits
-  const awq::Kv4Plan p = awq::kv4_plan(n_seqs, (int)heads, cfg->kv_heads, cfg->head_dim,
-                                       cfg->group_size, max_q, max_len, 0);
-  return round_up(awq::kv4_workspace(p, n_tokens, n_seqs, (int)heads, cfg->kv_heads, cfg->head_dim), kAlign);
+  return round_up(awq::kv4_workspace_any_window(n_tokens, n_seqs, (int)heads, cfg->kv_heads, cfg->head_dim,
+                                                cfg->group_size, max_q, max_len),
+                  kAlign);
 }
 
 int awq_kv4_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
@@ -281,7 +280,9 @@ int awq_kv4_attention(const void* q, int64_t q_token_stride, int64_t q_head_stri
   if (n_tokens == 0 || n_seqs == 0 || max_q == 0) return AWQ_OK;
   const awq::Kv4Plan p = awq::kv4_plan(n_seqs, (int)heads, cfg->kv_heads, cfg->head_dim,
                                        cfg->group_size, max_q, max_len, window);
-  const size_t need = awq_kv4_attention_workspace_bytes(n_tokens, n_seqs, heads, cfg, max_q, max_len);
+  // of this very plan, so that no launch can write past what it was given
+  const size_t need =
+      round_up(awq::kv4_workspace(p, n_tokens, n_seqs, (int)heads, cfg->kv_heads, cfg->head_dim), kAlign);
   if (need && (!workspace || workspace_bytes < need)) return AWQ_E_WORKSPACE;
   if (need && !aligned(workspace, kAlign)) return AWQ_E_ALIGN;
   if ((st = device_ptrs({q, cache, block_table, seq_lens, q_start, out, lse_out,

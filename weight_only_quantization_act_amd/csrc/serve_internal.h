@@ -81,6 +81,9 @@ Kv4Plan kv4_plan(int64_t n_seqs, int heads, int kv_heads, int dim, int group, in
                  int64_t max_len, int64_t window);
 size_t kv4_workspace(const Kv4Plan& p, int64_t n_tokens, int64_t n_seqs, int heads, int kv_heads,
                      int dim);
+// What covers the plan of every window.
+size_t kv4_workspace_any_window(int64_t n_tokens, int64_t n_seqs, int heads, int kv_heads, int dim,
+                                int group, int64_t max_q, int64_t max_len);
 hipError_t launch_kv4_attention(const Kv4Cache& c, const Kv4Query& q, const Kv4Plan& p,
                                 void* workspace, hipStream_t stream);
 
