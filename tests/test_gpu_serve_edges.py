@@ -43,7 +43,7 @@ def test_window_with_a_loose_bound(n, Hk, grp):
     c = Case(64, Hk, 16, 64, 1, lens, [1] * n, seed=n)
     c.fill()
     q = torch.randn(n, Hk * grp, 64, device="cuda").half()
-    for window, max_len in ((8192, 1 << 30), (1 << 20, 1 << 30), (8192, 1 << 24),
+    for window, max_len in ((8192, 1 << 30), (1 << 20, 1 << 30), ((1 << 63) - 1, 1 << 30), (8192, 1 << 24),
                             (50, 1 << 30)):
         say(f"kv4 window={window} max_len={max_len} n={n}")
         need = awq.awq_kv4_attention_workspace_bytes(n, n, Hk * grp, c.cfg, 1, max_len)

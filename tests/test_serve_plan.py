@@ -9,7 +9,8 @@ import weight_only_quantization_act_amd as awq
 from weight_only_quantization_act_amd import _serve
 
 
-DEVICE = 6  # a pointer that must be device memory is not
+# a workspace smaller than required, a pointer that must be device memory and is not
+WORKSPACE, DEVICE = 5, 6
 
 
 @pytest.fixture(scope="module")
@@ -49,7 +50,8 @@ def test_attention_workspace_covers_every_window(L):
     rng = random.Random(2)
     P = ctypes.c_void_p(0x10000)
     sizes = [(64, 8, 8, 1, 1 << 30, 8192), (32, 8, 4, 1, 1 << 30, 8192), (64, 8, 8, 1, 1 << 29, 8192),
-             (2048, 1, 4, 1, 1 << 24, 8192), (40, 8, 4, 1, 1 << 30, 6000), (4, 2, 1, 40, 1 << 30, 3)]
+             (2048, 1, 4, 1, 1 << 24, 8192), (1, 8, 4, 1, 1 << 30, (1 << 63) - 1),
+             (3, 8, 4, 500, 1 << 30, (1 << 63) - 1), (40, 8, 4, 1, 1 << 30, 6000), (4, 2, 1, 40, 1 << 30, 3)]
     for _ in range(3000):
         hk = rng.choice([1, 2, 8, 40])
         sizes.append((round(2 ** rng.uniform(0, 12)), hk, rng.choice([1, 3, 8]),
@@ -71,3 +73,16 @@ def test_attention_workspace_covers_every_window(L):
             got = _attend(L, cfg, n, H, max_q, max_len, w, P if need else None, need)
             assert got == DEVICE, (where, w, need, got)
     assert needed > 500
+
+
+def test_window_beyond_every_key_is_none(L):
+    """Windows up to the type's largest are laid out as no window is (window + max_q stays in 64
+    bits): such a call asks for the same workspace."""
+    cfg = awq.awq_kv4_config(128, 8, 64, 128, 1)
+    for n, max_q, max_len in ((1, 1, 1 << 30), (3, 500, 1 << 20), (8, 1, 8192)):
+        need = L.awq_kv4_attention_workspace_bytes(n * max_q, n, 32, ctypes.byref(cfg), max_q, max_len)
+        assert need > 0
+        P = ctypes.c_void_p(0x10000)
+        for window in (0, max_len, 1 << 31, (1 << 63) - max_q, (1 << 63) - 1):
+            assert _attend(L, cfg, n, 32, max_q, max_len, window, P, need) == DEVICE, window
+            assert _attend(L, cfg, n, 32, max_q, max_len, window, P, need - 256) == WORKSPACE, window

@@ -1391,7 +1391,7 @@ Kv4Plan kv4_plan(int64_t n_seqs, int heads, int kv_heads, int dim, int group, in
                  int64_t max_len, int64_t window) {
   Kv4Plan p;
   const int64_t cols = max_q * (heads / kv_heads);
-  const int64_t keys = window > 0 ? std::min(max_len, window + max_q) : max_len;
+  const int64_t keys = window > 0 && window < max_len ? std::min(max_len, window + max_q) : max_len;
   p.wide = cols > 16;
   p.waves = kWaves;
   if (p.wide) {
