@@ -52,3 +52,63 @@ def test_window_with_a_loose_bound(n, Hk, grp):
                                          max_len=max_len, window=window, workspace=buf[:need])
         assert (buf[need:] == 0x5A).all()
         _compare(c, q, out, lse, None, min(window, 1 << 20), where=(n, window, max_len))
+
+
+# How a call is laid out: sequences, key heads, rows a sequence, bound on the lengths.
+FORMS = {"eight waves": (5, 2, 1, 0), "four waves": (300, 1, 2, 0), "divided": (5, 2, 1, 9000),
+         "divided, many parts": (2, 1, 3, 100000), "prompt": (3, 2, 30, 0), "prompt, split": (1, 1, 30, 0)}
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_nan_reaches_the_rows_that_see_it(form, dtype):
+    """NaN is never taken for a key that is not there: a query row with a NaN, a key that holds
+    one and is alone in its tile, keys that all hold one.  Rows without keys stay rows without keys."""
+    say(f"kv4 nan {form} {dtype}")
+    n, Hk, news, bound = FORMS[form]
+    rng = np.random.default_rng(n)
+    lens = [int(x) for x in rng.integers(news, 400, n)]
+    lens[0] = 0 if news == 1 else lens[0]            # a row without keys
+    lens[-1] = 33 if news < 30 else 1025
+    c = Case(128, Hk, 16, 64, 1, lens, [news] * n, dtype, seed=n)
+    bound = bound or max(lens)
+
+    def run(spoil_keys, spoil_q):
+        k, v = c.kv(sum(lens))
+        starts = torch.tensor(np.concatenate(([0], np.cumsum(lens))), dtype=torch.int32, device="cuda")
+        spoil_keys(k, starts)
+        awq.awq_kv4_append(k, v, c.cache, c.dtable, c.dlens, starts, c.cfg)
+        q = torch.randn(n * news, 3 * Hk, 128, device="cuda").to(c.dt)
+        spoil_q(q)
+        out, lse = awq.awq_kv4_attention(q, c.cache, c.dtable, c.dlens, c.dstarts, c.cfg, max_q=news,
+                                         max_len=bound)
+        o, ls = out.isnan(), lse.isnan()
+        assert torch.equal(o.all(-1), o.any(-1)) and torch.equal(o.all(-1), ls)
+        if lens[0] == 0:
+            assert not out[0].any() and torch.isneginf(lse[0]).all()
+        return ls.cpu().numpy()
+
+    keys = np.repeat(np.array(lens) > 0, news)[:, None]
+
+    def nothing(*_):
+        pass
+    assert not run(nothing, nothing).any()
+    bad = np.zeros((n * news, 3 * Hk), bool)          # every third row, one head
+    bad[::3, 1] = True
+
+    def spoil_q(q):
+        q[::3, 1, 77] = float("nan")
+    assert np.array_equal(run(nothing, spoil_q), bad & keys)
+    # the last token of the last sequence, first key head: seen by the last row only
+    bad[:] = False
+    bad[-1, :3] = True
+
+    def last_key(k, starts):
+        k[-1, 0, 3] = float("nan")
+    assert np.array_equal(run(last_key, nothing), bad)
+    bad[:] = False
+    bad[:, :3] = True
+
+    def all_keys(k, starts):
+        k[:, 0, 100] = float("nan")
+    assert np.array_equal(run(all_keys, nothing), bad & keys)

@@ -792,8 +792,8 @@ void k_kv4_attention(Kv4Cache c, Kv4Query a, Partials part) {
         f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < WAVES; ++i) {
-          if (sm[i][cx] == kNegInf) continue;
-          const float k = __builtin_amdgcn_exp2f(sm[i][cx] - M);
+          // a wave without a maximum has seen no key (sums 0) or only NaN (sums NaN, which stay)
+          const float k = sm[i][cx] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(sm[i][cx] - M);
           l = fmaf(sl[i][cx], k, l);
           const f32x4 v = *(const f32x4*)&so[i][cx][ch];
 #pragma unroll
