@@ -112,3 +112,24 @@ def test_nan_reaches_the_rows_that_see_it(form, dtype):
     def all_keys(k, starts):
         k[:, 0, 100] = float("nan")
     assert np.array_equal(run(all_keys, nothing), bad & keys)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("news", [1, 40])
+def test_queries_at_the_ends_of_their_type(dtype, news):
+    """Query rows from the type's subnormals to its largest values, with a scale that brings the
+    scores back to about one: each row is scaled exactly, so the model's bound holds as ever."""
+    c = Case(64, 2, 32, 64, 1, (300, 77), (news, news), dtype, seed=news)
+    c.fill()
+    info = torch.finfo(c.dt)
+    lo, hi = (-22, 15) if dtype == "fp16" else (-131, 127)
+    q0 = torch.randn(2 * news, 4, 64, device="cuda")
+    q0 /= q0.abs().amax(-1, keepdim=True)               # largest magnitude 1
+    for exp in sorted({lo, lo + 3, -126 if lo < -126 else lo, -110, -100, -93, -92, 0, 92, 108, 115, 116, 117,
+                       hi - 1, hi}):
+        if not lo <= exp <= hi:
+            continue
+        say(f"kv4 queries of 2^{exp} {dtype} rows={news}")
+        q = (q0.double() * 2.0 ** exp).clamp(float(info.min), float(info.max)).to(c.dt)
+        assert q.isfinite().all() and (q != 0).any()
+        _check(c, q, 2.0 ** min(-3 - exp, 127), 0, where=(exp, dtype, news))

@@ -96,7 +96,7 @@ __device__ __forceinline__ half8v word_operand(uint32_t w, const CodeConsts& cc)
   return __builtin_bit_cast(half8v, v);
 }
 
-// exponent e with 2^e <= v < 2^(e+1), for a positive normal v
+// exponent e with 2^e <= v < 2^(e+1), for a positive normal v; -127 for a subnormal
 __device__ __forceinline__ int exponent_of(float v) {
   return (int)(__builtin_bit_cast(uint32_t, v) >> 23 & 255u) - 127;
 }
@@ -276,10 +276,11 @@ __device__ __forceinline__ void set_query(Column<D, GS>& c, const QueryRow<D, GS
     for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[w][i]));
   }
   top = max_q(top);
-  // a row of zeros or one with infinities is left as it is
-  int e = top >= 0x1p-126f && top < __builtin_inff() ? 8 - exponent_of(top) : 0;
-  e = min(max(e, -100), 100);
-  c.sigma = ldexpf(scale * 1.44269504088896340736f, -e);
+  // -119 .. 135 (a subnormal counts as 2^-127); a row of zeros or one with infinities is left as it is
+  const int e = top > 0.0f && top < __builtin_inff() ? 8 - exponent_of(top) : 0;
+  // scale log2(e) 2^-e, in the order in which nothing on the way leaves fp32's range
+  constexpr float kLog2e = 1.44269504088896340736f;
+  c.sigma = e < 0 ? ldexpf(scale, -e) * kLog2e : ldexpf(scale * (0.5f * kLog2e), 1 - e);
 #pragma unroll
   for (int g = 0; g < X::G; ++g) c.qsum[g] = 0.0f;
 #pragma unroll
