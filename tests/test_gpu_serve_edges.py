@@ -133,3 +133,21 @@ def test_queries_at_the_ends_of_their_type(dtype, news):
         q = (q0.double() * 2.0 ** exp).clamp(float(info.min), float(info.max)).to(c.dt)
         assert q.isfinite().all() and (q != 0).any()
         _check(c, q, 2.0 ** min(-3 - exp, 127), 0, where=(exp, dtype, news))
+
+
+@pytest.mark.parametrize("news", [1, 40])
+def test_scales_at_the_ends(news):
+    """Scales down to fp32's least subnormal: the scores vanish and masked keys still count nothing.
+    Up to its largest: rows whose scores are 0 are averages still."""
+    c = Case(128, 2, 32, 64, 1, (300, 77, 0), (news, news, 1), "bf16", seed=news)
+    c.fill()
+    q = torch.randn(2 * news + 1, 4, 128, device="cuda").bfloat16()
+    for scale in (2.0 ** -149, 2.0 ** -140, 2.0 ** -126, 2.0 ** -118, 2.0 ** -100):
+        say(f"kv4 scale {scale} rows={news}")
+        for x in (q, q * 2.0 ** 100, q * 2.0 ** -100):
+            _check(c, x, scale, 0, where=(scale, news))
+            _check(c, x, scale, 50, where=(scale, news, "window"))
+    for scale in (1e30, 2.9e38, float(np.finfo(np.float32).max)):
+        say(f"kv4 scale {scale} rows={news}")
+        _check(c, q * 0, scale, 0, where=(scale, news))
+        _check(c, q * 0, scale, 50, where=(scale, news, "window"))

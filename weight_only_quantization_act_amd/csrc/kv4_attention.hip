@@ -281,6 +281,10 @@ __device__ __forceinline__ void set_query(Column<D, GS>& c, const QueryRow<D, GS
   // scale log2(e) 2^-e, in the order in which nothing on the way leaves fp32's range
   constexpr float kLog2e = 1.44269504088896340736f;
   c.sigma = e < 0 ? ldexpf(scale, -e) * kLog2e : ldexpf(scale * (0.5f * kLog2e), 1 - e);
+  // a factor of 0 or infinity would make NaN of masked scores, -infinity, or of scores of 0.  Raw scores
+  // stay below 2^38, so that under the least normal factor each weight is 1; where the largest is short
+  // of scale log2(e) 2^-e, scores other than 0 decide alone or leave fp32's range
+  c.sigma = fminf(fmaxf(c.sigma, 0x1p-126f), 0x1.fffffep127f);
 #pragma unroll
   for (int g = 0; g < X::G; ++g) c.qsum[g] = 0.0f;
 #pragma unroll
