@@ -151,3 +151,28 @@ def test_scales_at_the_ends(news):
         say(f"kv4 scale {scale} rows={news}")
         _check(c, q * 0, scale, 0, where=(scale, news))
         _check(c, q * 0, scale, 50, where=(scale, news, "window"))
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_infinite_queries(form):
+    """A query row with an infinity is NaN whatever the signs of the codes it meets: keys of one sign
+    make all its scores +infinity or all -infinity."""
+    say(f"kv4 infinite queries {form}")
+    n, Hk, news, bound = FORMS[form]
+    lens = [int(x) for x in np.random.default_rng(n).integers(news, 400, n)]
+    lens[0] = 0 if news == 1 else lens[0]
+    for zp in (0, 1):
+        c = Case(64, Hk, 16, 32, zp, lens, [news] * n, "bf16", seed=n)
+        k, v = c.kv(sum(lens))
+        k = -k.abs() - 1
+        starts = torch.tensor(np.concatenate(([0], np.cumsum(lens))), dtype=torch.int32, device="cuda")
+        awq.awq_kv4_append(k, v, c.cache, c.dtable, c.dlens, starts, c.cfg)
+        q = torch.randn(n * news, 3 * Hk, 64, device="cuda").bfloat16()
+        q[::2, 0, 5], q[1::2, 1, 63] = float("inf"), float("-inf")
+        out, lse = awq.awq_kv4_attention(q, c.cache, c.dtable, c.dlens, c.dstarts, c.cfg, max_q=news,
+                                         max_len=bound or max(lens))
+        keys = torch.from_numpy(np.repeat(np.array(lens) > 0, news))[:, None].cuda()
+        want = ~torch.isfinite(q).all(-1) & keys
+        assert torch.equal(out.isnan().all(-1), want) and torch.equal(out.isnan().any(-1), want)
+        assert torch.equal(lse.isnan(), want)
+        assert torch.equal(torch.isneginf(lse), (~keys).expand_as(lse)) and not out[~keys[:, 0]].any()

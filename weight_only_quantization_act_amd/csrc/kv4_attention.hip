@@ -276,7 +276,10 @@ __device__ __forceinline__ void set_query(Column<D, GS>& c, const QueryRow<D, GS
     for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[w][i]));
   }
   top = max_q(top);
-  // -119 .. 135 (a subnormal counts as 2^-127); a row of zeros or one with infinities is left as it is
+  // an infinity makes the row NaN here already: a sum of products that happened to be -infinity for every
+  // key would pass for a row without keys
+  const float poison = top < __builtin_inff() ? 0.0f : __builtin_nanf("");
+  // -119 .. 135 (a subnormal counts as 2^-127); a row of zeros is left as it is
   const int e = top > 0.0f && top < __builtin_inff() ? 8 - exponent_of(top) : 0;
   // scale log2(e) 2^-e, in the order in which nothing on the way leaves fp32's range
   constexpr float kLog2e = 1.44269504088896340736f;
@@ -292,7 +295,8 @@ __device__ __forceinline__ void set_query(Column<D, GS>& c, const QueryRow<D, GS
     half8v h;
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
-      const _Float16 lo = (_Float16)ldexpf(v[w][n], e), hi = (_Float16)ldexpf(v[w][n + 4], e);
+      const _Float16 lo = (_Float16)(ldexpf(v[w][n], e) + poison),
+                     hi = (_Float16)(ldexpf(v[w][n + 4], e) + poison);
       h[2 * n] = lo;
       h[2 * n + 1] = hi;
       c.qsum[w / X::WPG] += (float)lo + (float)hi;
