@@ -151,8 +151,10 @@ int awq_kv4_read(const void* cache, int64_t n_pages, const int32_t* block_table,
  * A row without keys gives out 0 and lse -infinity.  Scores, softmax statistics and sums are
  * fp32; q enters the products in fp16, each row scaled by a power of two (exact but for parts
  * 2^-24 and more below the row's largest), the probabilities times the value's step rounded to
- * fp16 with 2^-11 relative error; keys and values enter as the integers code - zero, with zeros
- * 0 .. 15.  The order of every sum is fixed: results repeat bit for bit for the same bounds.
+ * fp16 with 2^-11 relative error (or 2^-36 of the largest finite value step that the row sees);
+ * keys and values enter as the integers code - zero, with zeros 0 .. 15.  A NaN or infinity in a row
+ * of q or a NaN in a key that it sees makes the row NaN, one in a value the channels of its group;
+ * keys that a row does not see cost it no precision either.  The order of every sum is fixed: results repeat bit for bit for the same bounds.
  *   q        as above, n_tokens rows, heads a multiple of kv_heads
  *   max_q    bound on the rows of one sequence, max_len bound on seq_lens (both host values:
  *            they size the launch; rows and keys beyond them are not computed)

@@ -6,7 +6,8 @@ import torch
 
 import weight_only_quantization_act_amd as awq
 from tests.gpu_util import requires_gpu, say
-from tests.test_gpu_kv4 import Case, _check, _compare
+from tests.kv4_ref import attention
+from tests.test_gpu_kv4 import Case, _check, _compare, _within
 
 pytestmark = [pytest.mark.gpu, requires_gpu]
 
@@ -176,3 +177,55 @@ def test_infinite_queries(form):
         assert torch.equal(out.isnan().all(-1), want) and torch.equal(out.isnan().any(-1), want)
         assert torch.equal(lse.isnan(), want)
         assert torch.equal(torch.isneginf(lse), (~keys).expand_as(lse)) and not out[~keys[:, 0]].any()
+
+
+@pytest.mark.parametrize("D,g", [(128, 64), (128, 128), (64, 32), (64, 64)])
+@pytest.mark.parametrize("spoil", ["nan", "huge"])
+def test_values_that_do_not_count_cost_no_precision(D, g, spoil):
+    """Small values beside a token whose value is NaN or huge: rows that the mask keeps from it meet
+    the bound of their own values, and so do, beside a NaN, the channels of other groups."""
+    rng = np.random.default_rng(D + g)
+    for lens, news, window, at in (((300,), 1, 20, (-21,)),            # just before the window, in its tile
+                                   ((300, 90), 3, 40, (-45, -44)),     # several rows, divided below
+                                   ((200, 150), 40, 0, (-1,)),         # prompt: later than all rows but one
+                                   ((500,), 90, 64, (-155, -30))):     # before some windows, inside others
+        say(f"kv4 values beside {spoil} D={D} g={g} news={news} window={window}")
+        n = len(lens)
+        c = Case(D, 1, 16, g, 1, lens, [news] * n, "bf16", seed=news)
+        k, v = c.kv(sum(lens))
+        v = v * 2.0 ** -13
+        ends = np.cumsum(lens)
+        rows = [int(e + a) for e in ends for a in at]
+        fill = float("nan") if spoil == "nan" else 6.0e5              # a step of about 40000
+        v[rows, 0, 1] = fill
+        starts = torch.tensor(np.concatenate(([0], ends)), dtype=torch.int32, device="cuda")
+        awq.awq_kv4_append(k, v, c.cache, c.dtable, c.dlens, starts, c.cfg)
+        q = torch.from_numpy(rng.standard_normal((n * news, 3, D))).to(c.dt).cuda()
+        pos = np.concatenate([np.arange(x - news, x) for x in lens])
+        own = np.repeat(ends - np.array(lens), news)                   # first row of the sequence in k, v
+        hit = np.zeros(n * news, bool)
+        for r in rows:
+            p = r - own
+            hit |= (p >= 0) & (p <= pos) & (pos - p < (window or 1 << 30))
+        assert (~hit).any()
+        ref = attention(c.lay, q.double().cpu().numpy(), c.cache.cpu().numpy(), c.table, c.lens, c.starts,
+                        D ** -0.5, window)
+        if spoil == "nan":
+            # channels of the other groups in all rows: their sums never touch the NaN
+            vc = v.clone()
+            vc[rows, 0, :g] = v[0, 0, :g]
+            clean = Case(D, 1, 16, g, 1, lens, [news] * n, "bf16", seed=news)
+            awq.awq_kv4_append(k, vc, clean.cache, clean.dtable, clean.dlens, starts, clean.cfg)
+            ref2 = attention(c.lay, q.double().cpu().numpy(), clean.cache.cpu().numpy(), clean.table,
+                             c.lens, c.starts, D ** -0.5, window)
+        for bound in (max(lens), 9000):
+            out, lse = awq.awq_kv4_attention(q, c.cache, c.dtable, c.dlens, c.dstarts, c.cfg, max_q=news,
+                                             max_len=bound, window=window)
+            keep = torch.from_numpy(~hit).cuda()
+            _within(c.lay, out[keep], lse[keep], [x[~hit] for x in ref], (news, window, bound))
+            if spoil == "nan":
+                assert out[~keep][..., :g].isnan().all()
+                if g < D:
+                    want, wl, absv, cz, dmax, keys, smax = ref2
+                    _within(c.lay, out[..., g:], lse, (want[..., g:], wl, absv[..., g:], cz[..., g:], dmax, keys,
+                                                       smax), (news, window, bound, "other groups"))

@@ -26,9 +26,10 @@
 // 2^kSlack, so that after the first tiles hardly any tile has to rescale what was summed
 // (without it a column of random scores does so in one of t tiles after t, the wave's 16 or 32
 // columns in nearly all of the first few dozen).  The weights are scaled by 2^f, f so chosen
-// from the largest value step seen that w 2^f stays below 2^15: fp16 holds them with full precision
-// down to 2^-29 of the largest.  A rise of the maximum or of that step multiplies what was
-// summed so far by exp2 of the difference.
+// from the largest finite value step that the column has seen that w 2^f stays below 2^15: fp16
+// holds them with full precision down to 2^-29 of the largest (a step of a masked key, NaN or
+// infinite, does not count, or it would cost the others their precision).  A rise of the maximum or
+// of that step multiplies what was summed so far by exp2 of the difference.
 //
 // Two forms.  Up to 16 columns (decode): a block's waves share the columns and take the tiles in
 // turn, each with a ring of tiles in LDS that DMAs fill ahead; bound by the reading of the codes
@@ -232,6 +233,7 @@ struct Column {
   float sigma;         // from the raw score to log2 units
   int pos;             // the row's position; -1: no row
   float m;             // reference of the scores, log2 units: their maximum to within kSlack
+  uint32_t limit;      // fp16 pattern that the value steps seen lie below; 0 before the first tile
   float nM;            // f - m: weights are exp2(s + nM); 0 before the first key
   float l;             // this lane's sum of exp2(s + nM)
   f32x4 z[X::G];       // sum of weight x (zero + 16): every row the same
@@ -311,6 +313,7 @@ __device__ __forceinline__ void set_query(Column<D, GS>& c, const QueryRow<D, GS
     c.z[g] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
   c.m = kNegInf;
+  c.limit = 0;
   c.nM = 0.0f;
   c.l = 0.0f;
 #pragma unroll
@@ -327,19 +330,36 @@ __device__ __forceinline__ uint32_t pair16(float x, float y) {
 __device__ __forceinline__ float lo16(uint32_t w) { return h2f((uint16_t)w); }
 __device__ __forceinline__ float hi16(uint32_t w) { return h2f((uint16_t)(w >> 16)); }
 
-// The power of two of the weights of a wave: w = exp2(s - m + f) step stays below 2^15 for steps
-// below the fp16 pattern `limit`.
-struct WeightScale {
-  float f = 64.0f;
-  uint32_t limit = 0;
-};
+// The power of two f of a column's weights: w = exp2(s - m + f) step stays below 2^15 for steps below
+// the fp16 pattern `limit`, a whole exponent, 1 << 10 and more.
+__device__ __forceinline__ float weight_exponent(uint32_t limit) {
+  return 14.0f - kSlack + 15.0f + 1.0f - (float)(limit >> 10);
+}
+// `limit` raised above the pattern of a step (zero and subnormal steps count as the smallest normal
+// one).
+__device__ __forceinline__ uint32_t limit_above(uint32_t step, uint32_t limit) {
+  return max(limit, ((max(step, 0x0400u) >> 10) + 1) << 10);
+}
+// The step of a parameter word if it counts: its key is seen and it is finite.
+__device__ __forceinline__ uint32_t counted_step(uint32_t par, bool seen) {
+  const uint32_t s = par & 0xffffu;
+  return seen && s < 0x7c00u ? s : 0u;
+}
+// The halves of a pair of keys that are seen (bits e and e + 1).
+__device__ __forceinline__ uint32_t seen_halves(uint32_t seen, int e) {
+  return (seen >> e & 1 ? 0xffffu : 0u) | (seen >> (e + 1) & 1 ? 0xffff0000u : 0u);
+}
+// The steps of a pair of parameter words.
+__device__ __forceinline__ uint32_t step_pair(uint32_t a, uint32_t b) {
+  return __builtin_amdgcn_perm(b, a, 0x05040100u);
+}
 
 // One tile of 32 keys.  !whole (the same in every lane): some (key, column) pairs do not exist;
 // key0 is the tile's first key, lo_off = window - 1 (or a huge number) so that column pos sees keys
 // [pos - lo_off, pos]; dead: bit x set if the keys of half x lie on no page.
 template <int D, int GS>
 __device__ __forceinline__ void do_tile(TileRegs<D, GS>& r, Column<D, GS>& c, bool whole,
-                                        int key0, int n_keys, int lo_off, int dead, WeightScale& ws,
+                                        int key0, int n_keys, int lo_off, int dead,
                                         const CodeConsts& cc, int lane) {
   using X = Geo<D, GS>;
   const int q = lane >> 4;
@@ -405,16 +425,32 @@ __device__ __forceinline__ void do_tile(TileRegs<D, GS>& r, Column<D, GS>& c, bo
   mx *= c.sigma;
   // seldom: a score above the column's maximum, or a value step above what the weights' scale
   // was made for
-  if (__any(mx > c.m + kSlack || top >= ws.limit)) {
+  if (__any(mx > c.m + kSlack || top >= c.limit)) {
     uint32_t all = top;
+    if (!whole) {  // of keys that the column sees
+      tp = u16x2{0, 0};
+#pragma unroll
+      for (int g = 0; g < X::G; ++g)
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const u32x4 w = r.vp[g][e >> 2];
+          tp = __builtin_elementwise_max(
+              tp, __builtin_bit_cast(u16x2, step_pair(w[e & 3], w[(e & 3) + 1]) & seen_halves(seen, e)));
+        }
+      all = max(tp[0], tp[1]);
+    }
+    if (__any(all >= 0x7c00u)) {  // NaN or infinite: the largest of the others
+      all = 0;
+#pragma unroll
+      for (int g = 0; g < X::G; ++g)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) all = max(all, counted_step(r.vp[g][e >> 2][e & 3], seen >> e & 1));
+    }
     all = max(all, (uint32_t)__shfl_xor((int)all, 16));
     all = max(all, (uint32_t)__shfl_xor((int)all, 32));
-    // zero and subnormal steps count as the smallest normal one, others as finite
-    const uint32_t ex = min(max(all, 0x0400u), 0x7bffu) >> 10;
-    ws.limit = max(ws.limit, (ex + 1) << 10);
-    ws.f = fminf(ws.f, 14.0f - kSlack + 15.0f - (float)ex);
+    c.limit = limit_above(all, c.limit);
     const float m = fmaxf(c.m, max_q(mx));
-    const float nM = m == kNegInf ? 0.0f : ws.f - m;
+    const float nM = m == kNegInf ? 0.0f : weight_exponent(c.limit) - m;
     const float a = c.m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(nM - c.nM);
     c.m = m;
     c.nM = nM;
@@ -723,7 +759,6 @@ void k_kv4_attention(Kv4Cache c, Kv4Query a, Partials part) {
     const auto* table = (const __attribute__((address_space(4))) int32_t*)(uintptr_t)(
         c.table + (int64_t)b * c.max_blocks);
     const int last_blk = max(0, (len - 1) >> c.log2p);
-    WeightScale ws;
     const int t0 = t_lo + wave;
     // tiles t0, t0 + step, ...: tile i of the wave in stage i mod NS
     const int n_tiles = t_hi > t0 ? (t_hi - t0 + step - 1) / step : 0;
@@ -769,7 +804,7 @@ void k_kv4_attention(Kv4Cache c, Kv4Query a, Partials part) {
           // every key of the tile exists and every column sees all of it
           const bool whole = !dead && key0 + 32 <= len && key0 + 31 <= pos0 &&
                              key0 >= pos0 + last_i - lo_off;
-          do_tile<D, GS>(r, col, whole, key0, len, lo_off, dead, ws, cc, lane);
+          do_tile<D, GS>(r, col, whole, key0, len, lo_off, dead, cc, lane);
         }
       }
     }
@@ -1061,7 +1096,7 @@ void k_kv4_attention_wide(Kv4Cache c, Kv4Query a, Partials part) {
     return r.dead;
   };
 
-  WeightScale ws;
+  uint32_t low = 0;  // the least of the columns' limits
   auto compute = [&](const uint8_t* buf, int t, uint64_t dead) {
     const int key0 = 64 * t;
     if (key0 > last || key0 + 63 < first - lo_off || last < 0) return;  // nothing for this wave
@@ -1111,7 +1146,9 @@ void k_kv4_attention_wide(Kv4Cache c, Kv4Query a, Partials part) {
           }
     }
     __builtin_amdgcn_s_setprio(0);
-    uint32_t seen[NC];
+    uint32_t seen[NC];  // bit e: the key of score e exists for the column
+#pragma unroll
+    for (int n = 0; n < NC; ++n) seen[n] = 0xffff;
     if (!whole) {
 #pragma unroll
       for (int n = 0; n < NC; ++n) {
@@ -1144,7 +1181,7 @@ void k_kv4_attention_wide(Kv4Cache c, Kv4Query a, Partials part) {
         }
     const uint32_t top = tp[0];
     float mx[NC];
-    bool up = top >= ws.limit;
+    bool up = top >= low;
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
       mx[n] = s[n][0];
@@ -1154,17 +1191,49 @@ void k_kv4_attention_wide(Kv4Cache c, Kv4Query a, Partials part) {
       up |= mx[n] > col[n].m + kSlack;
     }
     if (__any(up)) {
-      uint32_t all = top;
-      all = max(all, (uint32_t)__shfl_xor((int)all, 16));
-      all = max(all, (uint32_t)__shfl_xor((int)all, 32));
-      const uint32_t ex = min(max(all, 0x0400u), 0x7bffu) >> 10;
-      ws.limit = max(ws.limit, (ex + 1) << 10);
-      ws.f = fminf(ws.f, 14.0f - kSlack + 15.0f - (float)ex);
+      // the steps that count for each column: finite ones of keys that it sees.  Read from LDS once more,
+      // so that the loop over all tiles keeps its registers (prompt of 4096 tokens: 194 us from vp, 187 so)
+      uint32_t most[NC];
+#pragma unroll
+      for (int n = 0; n < NC; ++n) most[n] = top;
+      if (!whole) {
+        u16x2 t[NC];
+#pragma unroll
+        for (int n = 0; n < NC; ++n) t[n] = u16x2{0, 0};
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 8; e += 2)
+#pragma unroll
+            for (int g = 0; g < X::G; ++g) {
+              const uint2 v = *(const uint2*)(par + 256 * (X::G + g) + 128 * h + 4 * e);
+#pragma unroll
+              for (int n = 0; n < NC; ++n)
+                t[n] = __builtin_elementwise_max(
+                    t[n], __builtin_bit_cast(u16x2, step_pair(v.x, v.y) & seen_halves(seen[n] >> (8 * h), e)));
+            }
+#pragma unroll
+        for (int n = 0; n < NC; ++n) most[n] = max(t[n][0], t[n][1]);
+      }
+      low = 0xffffu;
 #pragma unroll
       for (int n = 0; n < NC; ++n) {
         Column<D, GS>& cl = col[n];
+        uint32_t all = most[n];
+        if (__any(all >= 0x7c00u)) {  // NaN or infinite: the largest of the others
+          all = 0;
+#pragma unroll 1
+          for (int x = 0; x < 16 * X::G; ++x) {
+            const uint32_t v = *(const uint32_t*)(par + 256 * (X::G + (x >> 4)) + 128 * (x >> 3 & 1) + 4 * (x & 7));
+            all = max(all, counted_step(v, seen[n] >> (x & 15) & 1));
+          }
+        }
+        all = max(all, (uint32_t)__shfl_xor((int)all, 16));
+        all = max(all, (uint32_t)__shfl_xor((int)all, 32));
+        cl.limit = limit_above(all, cl.limit);
+        low = min(low, cl.limit);
         const float m = fmaxf(cl.m, max_q(mx[n]));
-        const float nM = m == kNegInf ? 0.0f : ws.f - m;
+        const float nM = m == kNegInf ? 0.0f : weight_exponent(cl.limit) - m;
         const float x = cl.m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(nM - cl.nM);
         cl.m = m;
         cl.nM = nM;
