@@ -229,3 +229,20 @@ def test_values_that_do_not_count_cost_no_precision(D, g, spoil):
                     want, wl, absv, cz, dmax, keys, smax = ref2
                     _within(c.lay, out[..., g:], lse, (want[..., g:], wl, absv[..., g:], cz[..., g:], dmax, keys,
                                                        smax), (news, window, bound, "other groups"))
+
+
+def test_more_rows_than_a_grid_dimension():
+    """2^24 rows and more, a block of 256 threads each: the codes of every part by itself."""
+    say("int8 rows 2^24 + 3")
+    R, K = (1 << 24) + 3, 16
+    A = torch.empty((R, K), dtype=torch.float16, device="cuda").normal_()
+    q, st = awq.awq_int8_quantize(A)
+    for a in range(0, R, 1 << 22):
+        qa, sa = awq.awq_int8_quantize(A[a:a + (1 << 22)])
+        assert torch.equal(q[a:a + (1 << 22)], qa) and torch.equal(st[a:a + (1 << 22)], sa), a
+    want = A[-3:].float().abs().amax(1) / torch.full((3,), 127.0, device="cuda")
+    assert torch.equal(st[-3:], want)
+    wq, ws = awq.awq_int8_quantize(torch.randn(3, K, device="cuda").half())
+    y = awq.awq_int8_linear(A, wq, ws)
+    assert torch.equal(y[-1000:], awq.awq_int8_linear(A[-1000:], wq, ws))
+    assert torch.equal(y[:1000], awq.awq_int8_linear(A[:1000], wq, ws))
