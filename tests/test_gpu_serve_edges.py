@@ -246,3 +246,32 @@ def test_more_rows_than_a_grid_dimension():
     y = awq.awq_int8_linear(A, wq, ws)
     assert torch.equal(y[-1000:], awq.awq_int8_linear(A[-1000:], wq, ws))
     assert torch.equal(y[:1000], awq.awq_int8_linear(A[:1000], wq, ws))
+
+
+def test_more_blocks_than_a_grid_dimension_write_the_cache():
+    """65535 sequences on 160 key heads, more than 2^24 blocks of 256 threads: the few that have a new
+    token write and read back what they would by themselves."""
+    say("kv4 store, 65535 sequences x 160 heads")
+    n, Hk = 65535, 160
+    cfg = awq.awq_kv4_config(64, Hk, 16, 64, 1)
+    seqs = [0, 1, 777, 40000, 52429, 65533, 65534]
+    news = np.zeros(n, np.int64)
+    news[seqs] = 2
+    lens = np.where(news > 0, 9, 0)
+    table = np.full((n, 1), -1, np.int32)
+    table[seqs, 0] = np.arange(len(seqs))
+    T = int(news.sum())
+    k, v = torch.randn(2, T + 3, Hk, 64, device="cuda").half()
+
+    def run(pick):
+        def ints(x):
+            return torch.from_numpy(np.ascontiguousarray(x)).to(torch.int32).cuda()
+        cache = awq.awq_kv4_cache(len(seqs), cfg)
+        args = (cache, ints(table[pick]), ints(lens[pick]),
+                ints(np.concatenate(([0], np.cumsum(news[pick])))), cfg)
+        awq.awq_kv4_append(k, v, *args)
+        return (cache, *awq.awq_kv4_read(*args, T + 3))
+    all_of, few = run(np.arange(n)), run(np.array(seqs))
+    for a, b in zip(all_of, few):
+        assert torch.equal(a, b)
+    assert few[1][:T].any(-1).all() and not few[1][T:].any()
