@@ -275,3 +275,26 @@ def test_more_blocks_than_a_grid_dimension_write_the_cache():
     for a, b in zip(all_of, few):
         assert torch.equal(a, b)
     assert few[1][:T].any(-1).all() and not few[1][T:].any()
+
+
+def test_more_rows_than_a_grid_dimension_are_joined():
+    """2^24 rows and more of which the sequence has four, its keys divided over many parts: the join, a
+    block a row, reaches them all and writes no other."""
+    say("kv4 join, 2^24 + 5 rows")
+    T, news = (1 << 24) + 5, 4
+    c = Case(64, 1, 64, 64, 1, (9000,), (news,), seed=1)
+    c.fill()
+    out = torch.full((T, 1, 64), 7.0, dtype=torch.float16, device="cuda")
+    q = torch.randn(1, 1, 64, device="cuda").half().expand(T, 1, 64)
+    # an empty sequence holds the rows before the last four
+    table = torch.cat([c.dtable * 0 - 1, c.dtable])
+    lens = torch.tensor([0, 9000], dtype=torch.int32, device="cuda")
+    starts = torch.tensor([0, T - news, T], dtype=torch.int32, device="cuda")
+    got, lse = awq.awq_kv4_attention(q, c.cache, table, lens, starts, c.cfg, max_q=news, max_len=9000, out=out)
+    want, wl = awq.awq_kv4_attention(q[:news], c.cache, c.dtable, c.dlens, c.dstarts, c.cfg, max_q=news,
+                                     max_len=9000)
+    assert got is out
+    assert torch.allclose(got[-news:].float(), want.float(), rtol=2.0 ** -10, atol=2.0 ** -9)
+    assert torch.allclose(lse[-news:], wl, rtol=0, atol=2.0 ** -17)
+    assert not got[:news].any() and torch.isneginf(lse[:news]).all()
+    assert (got[news:-news] == 7).all()

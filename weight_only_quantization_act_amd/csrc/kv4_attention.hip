@@ -44,6 +44,7 @@
 
 #include <algorithm>
 
+#include "grid.h"
 #include "int8_quant.h"
 #include "kv4_cache.h"
 #include "mfma_dma.h"
@@ -559,7 +560,7 @@ struct Place {
   int head, split, seq, tile;  // tile -1: none
 };
 __device__ __forceinline__ Place place_of(const Kv4Cache& c, const Partials& part) {
-  unsigned n = blockIdx.x + gridDim.x * blockIdx.y;
+  unsigned n = block_number();
   Place p;
   p.head = n % c.kv_heads;
   n /= c.kv_heads;
@@ -698,7 +699,7 @@ void k_kv4_attention(Kv4Cache c, Kv4Query a, Partials part) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing > kJoin ? kRing : kJoin];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const unsigned number = blockIdx.x + gridDim.x * blockIdx.y;
+  const unsigned number = block_number();
   const int kvh = number % c.kv_heads, index = number / c.kv_heads;  // index: of the head's blocks
   const int group = a.heads / c.kv_heads;
   const int lo_off = a.window > 0 ? a.window - 1 : 0x3fffffff;
@@ -1361,8 +1362,8 @@ __global__ __launch_bounds__(256) void k_kv4_join(Kv4Cache c, Kv4Query a, Partia
   __shared__ f32x4 so[PARTS > 1 ? PARTS : 1][T];
   __shared__ float sm[PARTS], sl[PARTS];
   const int x = threadIdx.x % T, w = threadIdx.x / T % PARTS;
-  const int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / (T * PARTS);
-  if (ROWS > 1 && r >= n_rows) return;
+  const int64_t r = (int64_t)block_number() * ROWS + threadIdx.x / (T * PARTS);
+  if (r >= n_rows) return;  // (one row a block, or no barrier)
   const int64_t t = r / a.heads;
   int64_t first = r * part.splits, step = 1;  // slots
   int S = part.splits;
@@ -1431,11 +1432,10 @@ hipError_t launch_join(const Kv4Cache& c, const Kv4Query& q, const Partials& par
   constexpr int kParts = 1024 / D, kRows = 1024 / D;
   // many parts a row
   if (part.splits / (DIVIDED ? c.n_seqs : 1) >= 16)
-    hipLaunchKernelGGL((k_kv4_join<D, kParts, DIVIDED>), dim3((unsigned)rows), dim3(256), 0, stream, c, q,
+    hipLaunchKernelGGL((k_kv4_join<D, kParts, DIVIDED>), grid_of(rows), dim3(256), 0, stream, c, q,
                        part, rows);
   else
-    hipLaunchKernelGGL((k_kv4_join<D, 1, DIVIDED>), dim3((unsigned)((rows + kRows - 1) / kRows)), dim3(256),
-                       0, stream, c, q, part, rows);
+    hipLaunchKernelGGL((k_kv4_join<D, 1, DIVIDED>), grid_of((rows + kRows - 1) / kRows), dim3(256), 0, stream, c, q, part, rows);
   return hipGetLastError();
 }
 
@@ -1444,9 +1444,8 @@ hipError_t launch_dg(const Kv4Cache& c, const Kv4Query& q, const Kv4Plan& p, con
                      int64_t rows, hipStream_t stream) {
   const int64_t blocks =
       (int64_t)c.kv_heads * (p.wide ? (int64_t)p.tiles * p.splits * c.n_seqs : p.splits > 1 ? p.splits : c.n_seqs);
-  constexpr int64_t kRow = 1 << 20;  // a dimension of a grid holds less than 2^32 threads
-  if (blocks > 0x7fffffff - kRow) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)(blocks < kRow ? blocks : kRow), (unsigned)((blocks + kRow - 1) / kRow));
+  if (blocks > 0x7fffffff - (1 << 20)) return hipErrorInvalidValue;
+  const dim3 grid = grid_of(blocks);
   if (p.wide)
     hipLaunchKernelGGL((k_kv4_attention_wide<D, GS>), grid, dim3(64 * kWaves), 0, stream, c, q, part);
   else if (p.splits > 1)
