@@ -298,3 +298,22 @@ def test_more_rows_than_a_grid_dimension_are_joined():
     assert torch.allclose(lse[-news:], wl, rtol=0, atol=2.0 ** -17)
     assert not got[:news].any() and torch.isneginf(lse[:news]).all()
     assert (got[news:-news] == 7).all()
+
+
+def test_more_outputs_than_a_grid_dimension():
+    """One token through 2^28 outputs and more, a block of 512 threads for every 32: each part as it is
+    by itself."""
+    say("int8 linear, 2^28 + 40 outputs")
+    M, K = (1 << 28) + 40, 16
+    g = torch.Generator(device="cuda").manual_seed(1)
+    wq = torch.randint(-127, 128, (M, K), generator=g, device="cuda", dtype=torch.int8)
+    ws = torch.rand(M, generator=g, device="cuda")
+    x = torch.randn(1, K, generator=g, device="cuda").half()
+    y = torch.full((1, M), float("nan"), device="cuda").half()
+    awq.awq_int8_linear(x, wq, ws, out=y)
+    for a in range(0, M, 1 << 26):
+        part = slice(a, min(a + (1 << 26), M))
+        assert torch.equal(y[:, part], awq.awq_int8_linear(x, wq[part], ws[part])), a
+    xq, xs = awq.awq_int8_quantize(x)
+    want = (xq.double() @ wq[-5:].double().t()).float() * xs[:, None] * ws[-5:]
+    assert torch.equal(y[:, -5:], want.half())

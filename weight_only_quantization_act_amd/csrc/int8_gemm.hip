@@ -16,6 +16,7 @@
 
 #include <type_traits>
 
+#include "grid.h"
 #include "int8_quant.h"
 #include "mfma_dma.h"
 #include "serve_internal.h"
@@ -62,7 +63,8 @@ __global__ __launch_bounds__(S::THREADS) void k_int8_tiles(Int8Args a, int tiles
   // tiles in bands of 8 token tiles, whose panels its compute units share in that XCD's L2.
   constexpr int kBand = 8;
   const int total = tiles_t * tiles_m;
-  const int b = blockIdx.x, xcd = b & 7, local = b >> 3;
+  const int b = (int)block_number(), xcd = b & 7, local = b >> 3;
+  if (b >= total) return;  // the whole block
   const int q8 = total >> 3, r8 = total & 7;
   const int logical = xcd < r8 ? xcd * (q8 + 1) + local : r8 * (q8 + 1) + (xcd - r8) * q8 + local;
   const int band = logical / (kBand * tiles_m);
@@ -86,7 +88,7 @@ __global__ __launch_bounds__(S::THREADS) void k_int8_tiles(Int8Args a, int tiles
   const unsigned row_x = wave * S::DMA_X * 8 + dr, row_w = wave * S::DMA_W * 8 + dr;
   const unsigned ldsb = lds_address(sm);
   // 128-byte steps of this split: kt0 .. kt1 - 1, walked in whole turns of the ring
-  const int steps = (a.K + S::BK - 1) / S::BK, z = blockIdx.y;
+  const int steps = (a.K + S::BK - 1) / S::BK, z = blockIdx.z;
   const int kt0 = (int)((int64_t)steps * z / splits);
   const int n_steps = (int)((int64_t)steps * (z + 1) / splits) - kt0;
   const int nk = (n_steps + NS - 1) / NS * NS;
@@ -270,7 +272,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_int8_few(FewArgs f) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, q = lane >> 4;
-  const int m0 = blockIdx.x * 16 * RT;
+  const int64_t first = (int64_t)block_number() * 16 * RT;
+  if (first >= a.M) return;  // the whole block
+  const int m0 = (int)first;
   const int nch = (a.K + 255) >> 8;
 
   // rows past the last repeat it and are dropped; pieces past K read the row's start and count 0
@@ -396,8 +400,11 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_int8_few(FewArgs f) {
 template <class S, bool BF16>
 hipError_t launch_tiles(const Int8Args& a, int splits, int* part, hipStream_t stream) {
   const int tt = (a.T + S::BT - 1) / S::BT, tm = (a.M + S::BM - 1) / S::BM;
-  if ((long long)tt * tm > 0x7fffffffLL) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((k_int8_tiles<S, BF16>), dim3((unsigned)(tt * tm), (unsigned)splits),
+  const int64_t tiles = (int64_t)tt * tm;
+  if (tiles > 0x7fffffff - (1 << 20)) return hipErrorInvalidValue;
+  dim3 grid = grid_of(tiles);
+  grid.z = (unsigned)splits;
+  hipLaunchKernelGGL((k_int8_tiles<S, BF16>), grid,
                      dim3(S::THREADS), 0, stream, a, tt, tm, splits, part);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits <= 1) return e;
@@ -416,7 +423,7 @@ constexpr int kTwoRows = 32 * 512;
 
 template <int RT, bool FUSED, bool VEC>
 hipError_t launch_few(const FewArgs& f, hipStream_t stream) {
-  const dim3 grid((unsigned)((f.g.M + 16 * RT - 1) / (16 * RT))), block(64 * kFewWaves);
+  const dim3 grid = grid_of((f.g.M + 16 * RT - 1) / (16 * RT)), block(64 * kFewWaves);
   const size_t lds = FUSED ? (size_t)f.g.K : 0;
   if (f.g.bf16)
     hipLaunchKernelGGL((k_int8_few<RT, FUSED, true, VEC>), grid, block, lds, stream, f);
