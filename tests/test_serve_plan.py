@@ -1,11 +1,14 @@
 """How the serving operators lay a call out, on the host: the workspace that a query names covers
 what the call it is made for uses.  Nothing is launched (fake pointers, never dereferenced)."""
 import ctypes
+import os
 import random
+import subprocess
 
 import pytest
 
 import weight_only_quantization_act_amd as awq
+from tests.int8_forms import SHAPES
 from weight_only_quantization_act_amd import _serve
 
 
@@ -86,3 +89,33 @@ def test_window_beyond_every_key_is_none(L):
         for window in (0, max_len, 1 << 31, (1 << 63) - max_q, (1 << 63) - 1):
             assert _attend(L, cfg, n, 32, max_q, max_len, window, P, need) == DEVICE, window
             assert _attend(L, cfg, n, 32, max_q, max_len, window, P, need - 256) == WORKSPACE, window
+
+
+def test_int8_forms_are_covered(tmp_path):
+    """The sizes that the GPU tests run land on the forms that they are meant for, so that a changed rule
+    cannot leave a form untested."""
+    src = tmp_path / "plan.cpp"
+    src.write_text("""#include <stdio.h>
+#include "int8_plan.h"
+int main() {
+  long long T, M, K;
+  const char* name[] = {"few", "32", "64", "128", "256"};
+  while (scanf("%lld %lld %lld", &T, &M, &K) == 3) {
+    const awq::Int8Plan p = awq::int8_plan(T, M, K);
+    printf("%s %d %d\\n", name[p.form], p.splits, awq::few_rows(M));
+  }
+}
+""")
+    exe = tmp_path / "plan"
+    csrc = os.path.join(os.path.dirname(awq.LIB_PATH), "csrc")
+    subprocess.run(["g++", "-std=c++17", "-I", csrc, str(src), "-o", str(exe)], check=True)
+    sizes = "\n".join("%d %d %d" % s[2:] for s in SHAPES)
+    out = subprocess.run([str(exe)], input=sizes, capture_output=True, text=True, check=True).stdout.split("\n")
+    got = [line.split() for line in out if line]
+    for shape, (form, splits, rows) in zip(SHAPES, got):
+        assert (form, int(splits)) == shape[:2], (shape, form, splits)
+    assert len(got) == len(SHAPES)
+    assert {s[0] for s in SHAPES} == {"few", "32", "64", "128", "256"}
+    assert {int(rows) for (form, _, rows) in got if form == "few"} == {1, 2}
+    for form in ("32", "64", "128"):
+        assert {s[1] > 1 for s in SHAPES if s[0] == form} == {True, False}, form

@@ -17,6 +17,7 @@
 #include <type_traits>
 
 #include "grid.h"
+#include "int8_plan.h"
 #include "int8_quant.h"
 #include "mfma_dma.h"
 #include "serve_internal.h"
@@ -46,7 +47,7 @@ struct Tile {
 
 // Bound by the matrix cores: 256 x 256 tiles on sixteen waves of 128 x 32, one block a compute
 // unit, do 8192 tokens through 28672 x 8192 in 1.70 ms, 2.27 Pop/s (128 x 128 tiles, two blocks a
-// compute unit, 2.19 ms).  Small tiles keep more blocks for fewer tokens; see plan_of.
+// compute unit, 2.19 ms).  Small tiles keep more blocks for fewer tokens (int8_plan.h).
 //
 // splits > 1: block z sums its share of K and stores the int32 tile to part [splits][T][M].
 template <class S, bool BF16>
@@ -418,9 +419,6 @@ hipError_t launch_tiles(const Int8Args& a, int splits, int* part, hipStream_t st
   return hipGetLastError();
 }
 
-// 32 outputs a block where that still leaves two blocks a compute unit
-constexpr int kTwoRows = 32 * 512;
-
 template <int RT, bool FUSED, bool VEC>
 hipError_t launch_few(const FewArgs& f, hipStream_t stream) {
   const dim3 grid = grid_of((f.g.M + 16 * RT - 1) / (16 * RT)), block(64 * kFewWaves);
@@ -432,50 +430,8 @@ hipError_t launch_few(const FewArgs& f, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// How one product runs, by its sizes.
-enum { kFew, kTile32, kTile64, kTile128, kTile256 };
-struct Plan {
-  int form, splits;
-};
-
-// Which form: what each measured, in us at 4096 x 4096, 11008 x 4096, 5120 x 13824 (out x in):
-//   up to 16 tokens  weight streaming 7.3, 14.8, 27.6; 32-token tiles 9.0, 14.6, 20.6 (so weights of
-//                    2^26 bytes and more take those)
-//   32 tokens        32-token tiles 9.7, 15.6, 21.1; 64-token tiles 11.0, 16.7, 21.7
-//   128              64: 15.4, 22.0, 24.0; 128: 16.3, 22.9, 26.8
-//   200              64: 20.3, 27.0, 33.8; 128: 19.7, 28.9, 37.8
-//   512              64: 24.9, 44.5, 67.2; 128: 28.0, 41.1, 53.9
-//   1024             64: 31.2, 79.2, 109; 128: 36.9, 72.0, 94.9; 256: 53.3, 63.8, 131
-//   4096             128: 88.7, 233, 298; 256: 72.7, 196, 322
-// 64-token tiles stay ahead while they are one round of two blocks a compute unit and the sums are
-// short.  256 x 256 tiles do 1.3 times the work of 128 x 128 ones a unit of time, but one a compute
-// unit: a round of them costs 1.53 rounds of the small ones, a round begun nearly as much as a whole.
-Plan plan_of(int64_t T, int64_t M, int64_t K) {
-  Plan p{kTile128, 1};
-  auto tiles_of = [&](int64_t bt, int64_t bm) { return ((T + bt - 1) / bt) * ((M + bm - 1) / bm); };
-  if (T <= 16 && M * K < (int64_t)1 << 26) p.form = kFew;
-  else if (T <= 32) p.form = kTile32;
-  else if (T <= 128 || (K <= 6144 && tiles_of(64, 128) <= 512)) p.form = kTile64;
-  else {
-    const int64_t small = tiles_of(128, 128), large = tiles_of(256, 256);
-    const double rs = small / 512.0, cs = (double)((small + 511) / 512);
-    const double rl = large / 256.0, cl = (double)((large + 255) / 256);
-    if (1.53 * (0.25 * rl + 0.75 * cl) < 0.5 * (rs + cs)) p.form = kTile256;
-  }
-  if (p.form < kTile32 || p.form == kTile256) return p;
-  const int64_t tiles = tiles_of(p.form == kTile32 ? 32 : p.form == kTile64 ? 64 : 128, 128);
-  // K split over two blocks a compute unit, at least eight steps a split (5120 x 13824, unsplit and
-  // split: 64 tokens 41.5 and 23.4 us, 200 tokens 72.5 and 35.1, 512 tokens 75.3 and 55.3)
-  int64_t s = 512 / tiles;
-  const int64_t most = K / 1024;
-  if (s > most) s = most;
-  if (s > 8) s = 8;
-  p.splits = (int)(s < 1 ? 1 : s);
-  return p;
-}
-
 template <bool BF16>
-hipError_t launch_plan(const Int8Args& a, const Plan& p, int* part, hipStream_t stream) {
+hipError_t launch_plan(const Int8Args& a, const Int8Plan& p, int* part, hipStream_t stream) {
   switch (p.form) {
     case kTile32: return launch_tiles<Tile<32, 128, 1, 4, 4>, BF16>(a, p.splits, part, stream);
     case kTile64: return launch_tiles<Tile<64, 128, 2, 2, 3>, BF16>(a, p.splits, part, stream);
@@ -487,16 +443,16 @@ hipError_t launch_plan(const Int8Args& a, const Plan& p, int* part, hipStream_t 
 }  // namespace
 
 size_t int8_matmul_workspace(int64_t T, int64_t M, int64_t K) {
-  const Plan p = plan_of(T, M, K);
+  const Int8Plan p = int8_plan(T, M, K);
   return p.splits > 1 ? (size_t)p.splits * T * M * sizeof(int) : 0;
 }
 
 hipError_t launch_int8_matmul(const Int8Args& a, void* workspace, hipStream_t stream) {
   if (a.T <= 0 || a.M <= 0) return hipSuccess;
-  const Plan p = plan_of(a.T, a.M, a.K);
+  const Int8Plan p = int8_plan(a.T, a.M, a.K);
   if (p.form < kTile32) {
     const FewArgs f{a, nullptr, nullptr, 0};
-    return a.M >= kTwoRows ? launch_few<2, false, false>(f, stream) : launch_few<1, false, false>(f, stream);
+    return few_rows(a.M) == 2 ? launch_few<2, false, false>(f, stream) : launch_few<1, false, false>(f, stream);
   }
   return a.bf16 ? launch_plan<true>(a, p, (int*)workspace, stream)
                 : launch_plan<false>(a, p, (int*)workspace, stream);
@@ -509,7 +465,7 @@ hipError_t launch_int8_linear_fused(const Int8Args& a, const void* x, const floa
   if (a.T <= 0 || a.M <= 0) return hipSuccess;
   const FewArgs f{a, x, s, cols};
   const bool vec = row_vector_loads(x, 0, s);
-  const bool two = a.M >= kTwoRows;
+  const bool two = few_rows(a.M) == 2;
   if (vec) return two ? launch_few<2, true, true>(f, stream) : launch_few<1, true, true>(f, stream);
   return two ? launch_few<2, true, false>(f, stream) : launch_few<1, true, false>(f, stream);
 }
