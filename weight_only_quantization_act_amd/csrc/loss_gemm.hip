@@ -41,6 +41,7 @@
 
 #include "awq_act.h"
 #include "awq_internal.h"
+#include "mfma_dma.h"
 
 // Stage geometry, overridable for sweeps; the defaults (64 channels per stage, 2 stages,
 // 2 x 4 waves) are the fastest measured on MI355X.
@@ -83,52 +84,8 @@ constexpr int kBandG = 8;  // tile-row pairs per raster band (G form; same-devic
 
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
-typedef __attribute__((address_space(3))) void lds_void;
-
-typedef int int32x4 __attribute__((ext_vector_type(4)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
-
-// Raw buffer resource (gfx9 layout): 48-bit base, stride 0, byte range, 32-bit data
-// format.  Accesses at offsets >= num_bytes return zero.
-__device__ __forceinline__ int32x4 make_rsrc(const void* base, unsigned num_bytes) {
-  const unsigned long long b = (unsigned long long)base;
-  int32x4 r;
-  r[0] = __builtin_amdgcn_readfirstlane((int)(unsigned)(b & 0xffffffffu));
-  r[1] = __builtin_amdgcn_readfirstlane((int)(unsigned)((b >> 32) & 0xffffu));
-  r[2] = __builtin_amdgcn_readfirstlane((int)num_bytes);
-  r[3] = 0x00020000;
-  return r;
-}
-
-__device__ __forceinline__ unsigned lds_addr(const void* p) {
-  return __builtin_amdgcn_readfirstlane(
-      (int)(unsigned)(size_t)(const __attribute__((address_space(3))) void*)p);
-}
-
-// One wave-level 16-byte-per-lane DMA from global memory into LDS: lane l's 16 bytes at
-// buffer offset voff + soff land at LDS byte lds + 16 l.  Issued as inline assembly so
-// that the compiler's automatic waits do not drain the DMA queue before unrelated LDS
-// reads; every wait for these transfers is the explicit s_waitcnt at the barriers.
-// The instruction writes no VGPR (its data goes to LDS), so no register of the asm is
-// overwritten after the statement.
-__device__ __forceinline__ void dma16(const int32x4& rsrc, unsigned lds, unsigned voff,
-                                      unsigned soff) {
-  asm volatile(
-      "s_mov_b32 m0, %0\n\t"
-      "s_nop 0\n\t"
-      "buffer_load_dwordx4 %1, %2, %3 offen lds"
-      :
-      : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
-      : "memory", "m0");
-}
-
-// s_waitcnt immediate for gfx9: vmcnt(vm) with expcnt/lgkmcnt: lgkmcnt(0), expcnt(7).
-template <int VM>
-struct WaitVmLgkm {
-  static_assert(VM >= 0 && VM < 64, "vmcnt range");
-  static constexpr int value = (VM & 0xF) | ((VM >> 4) << 14) | (7 << 4);
-};
 
 // Tile geometry: a K slice of BK channels per stage, NS stages, WM x WN waves.
 template <int BK_, int NS_, int WM_, int WN_>
@@ -274,7 +231,7 @@ __global__ __launch_bounds__(S::THREADS) void k_loss_gemm(
   const int dma_lchunk_even = (lane % S::CPR) ^ S::swz(dma_row_in);
   const int dma_lchunk_odd = (lane % S::CPR) ^ S::swz(dma_row_in + (S::ROWS_PER_DMA == 8 ? 8 : 0));
   int32x4 rsrc_a;  // set per tile row (part) below
-  const int32x4 rsrc_b = make_rsrc(B, (unsigned)rows_b * (unsigned)LD * 2u);
+  const int32x4 rsrc_b = buffer_rsrc(B, (unsigned)rows_b * (unsigned)LD * 2u);
   static_assert(S::DMA_A % 2 == 0 && S::DMA_B % 2 == 0, "block parity follows j");
   const unsigned row_a = (unsigned)(wave * S::DMA_A * S::ROWS_PER_DMA + dma_row_in);
   const unsigned row_b = (unsigned)(wave * S::DMA_B * S::ROWS_PER_DMA + dma_row_in);
@@ -294,8 +251,8 @@ __global__ __launch_bounds__(S::THREADS) void k_loss_gemm(
   };
 
   // LDS byte addresses of the stage buffers (uniform, computed once).
-  const unsigned lds_stage[4] = {lds_addr(sm0), lds_addr(sm1), lds_addr(sm2), lds_addr(sm3)};
-  const unsigned lds_spare = REV ? lds_addr(smx) : 0u;
+  const unsigned lds_stage[4] = {lds_address(sm0), lds_address(sm1), lds_address(sm2), lds_address(sm3)};
+  const unsigned lds_spare = REV ? lds_address(smx) : 0u;
 
   // k-tiles rounded up to a multiple of NS: the padding tiles lie past the reduction
   // length, read as zeros and add nothing, and the NS-unrolled loop below then has a
@@ -332,7 +289,7 @@ __global__ __launch_bounds__(S::THREADS) void k_loss_gemm(
     if (!epi) {
 #pragma unroll
       for (int j = 0; j < S::DMA_A; ++j)
-        dma16(rsrc_a, la + j * 1024u, (j & 1) ? va1 : va0, kbytes + j * dma_row_stride);
+        lds_dma16(rsrc_a, la + j * 1024u, (j & 1) ? va1 : va0, kbytes + j * dma_row_stride);
     } else {
       // dW rows (wave - WAVES/2) 32 + ... of channels kt0 + 2 into the A-region rows 128 + ...
       const int ke = (kt0 + 2) * S::BK;
@@ -341,11 +298,11 @@ __global__ __launch_bounds__(S::THREADS) void k_loss_gemm(
       const unsigned ve0 = e0 ? vo_b0 - sh : kOutOfRange, ve1 = e1 ? vo_b1 - sh : kOutOfRange;
 #pragma unroll
       for (int j = 0; j < S::DMA_A; ++j)
-        dma16(rsrc_b, la + j * 1024u, (j & 1) ? ve1 : ve0, (unsigned)ke * 2u + j * dma_row_stride);
+        lds_dma16(rsrc_b, la + j * 1024u, (j & 1) ? ve1 : ve0, (unsigned)ke * 2u + j * dma_row_stride);
     }
 #pragma unroll
     for (int j = 0; j < S::DMA_B; ++j)
-      dma16(rsrc_b, lb + j * 1024u, (j & 1) ? vb1 : vb0, kbytes + j * dma_row_stride);
+      lds_dma16(rsrc_b, lb + j * 1024u, (j & 1) ? vb1 : vb0, kbytes + j * dma_row_stride);
     if constexpr (REV && ST == 0) {
       if (nkt >= 4 && i == nkt - 2) {  // channels kt0 + 3 of every row into the spare buffer
         const int ks3 = (kt0 + 3) * S::BK;
@@ -354,7 +311,7 @@ __global__ __launch_bounds__(S::THREADS) void k_loss_gemm(
         const unsigned ls = lds_spare + (unsigned)(wave * S::DMA_B) * 1024u;
 #pragma unroll
         for (int j = 0; j < S::DMA_B; ++j)
-          dma16(rsrc_b, ls + j * 1024u, (j & 1) ? vs1 : vs0, (unsigned)ks3 * 2u + j * dma_row_stride);
+          lds_dma16(rsrc_b, ls + j * 1024u, (j & 1) ? vs1 : vs0, (unsigned)ks3 * 2u + j * dma_row_stride);
       }
     }
   };
@@ -429,7 +386,7 @@ __global__ __launch_bounds__(S::THREADS) void k_loss_gemm(
     sb();
     mma(f0);
     // stage kt+1 has landed (own DMAs) and this wave's reads of stage kt are done
-    __builtin_amdgcn_s_waitcnt(WaitVmLgkm<(S::NS - 2) * S::PER_STAGE>::value);
+    __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<(S::NS - 2) * S::PER_STAGE>::value);
     __builtin_amdgcn_s_barrier();
     // the refill DMAs, too, go out at raised priority (same-device A/B, three rounds: loss
     // product 1.339 against 1.370 ms)
@@ -450,7 +407,7 @@ __global__ __launch_bounds__(S::THREADS) void k_loss_gemm(
   auto step_idle = [&](auto st, int kt) {
     constexpr int ST = decltype(st)::value;
     using NEXT = std::integral_constant<int, (ST + 1) % S::NS>;
-    __builtin_amdgcn_s_waitcnt(WaitVmLgkm<(S::NS - 2) * S::PER_STAGE>::value);
+    __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<(S::NS - 2) * S::PER_STAGE>::value);
     __builtin_amdgcn_s_barrier();
     if constexpr (LOSS_PRIO) __builtin_amdgcn_s_setprio(1);
     dma_stage(st, kt + S::NS);
@@ -479,7 +436,7 @@ __global__ __launch_bounds__(S::THREADS) void k_loss_gemm(
                         : GRAM ? X + (size_t)tmc * BM * K
                                : dW + (size_t)kk_alpha * M * K + (size_t)tmc * BM * K;
     const int rows_a = BUILD ? min(BM, K - tmc * BM) : GRAM ? min(BM, N - tmc * BM) : min(BM, M - tmc * BM);
-    rsrc_a = make_rsrc(A, (unsigned)rows_a * (unsigned)LD * 2u);
+    rsrc_a = buffer_rsrc(A, (unsigned)rows_a * (unsigned)LD * 2u);
     if constexpr (GRAM) {
       kt0 = min(tmc * (BM / S::BK), nk);
       nkt = nk - kt0;
@@ -499,7 +456,7 @@ __global__ __launch_bounds__(S::THREADS) void k_loss_gemm(
   if constexpr (S::NS > 1) dma_stage(I1{}, 1);
   if constexpr (S::NS > 2) dma_stage(I2{}, 2);
   if constexpr (S::NS > 3) dma_stage(I3{}, 3);
-  __builtin_amdgcn_s_waitcnt(WaitVmLgkm<(S::NS - 1) * S::PER_STAGE>::value);
+  __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<(S::NS - 1) * S::PER_STAGE>::value);
   __builtin_amdgcn_s_barrier();
 
   // Fragments ping-pong between two register sets; KSTEPS is even, so a stage always
@@ -532,7 +489,7 @@ __global__ __launch_bounds__(S::THREADS) void k_loss_gemm(
       step_idle(I1{}, nkt - 1);
     }
   }
-  __builtin_amdgcn_s_waitcnt(WaitVmLgkm<0>::value);  // no LDS write may outlive the block
+  __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<0>::value);  // no LDS write may outlive the block
 
   // ---- epilogue: sum of squares of the 256 x 256 output tile (GRAM: sum of
   //      dW (C + dW gdiag) at the output positions; BUILD: the tile itself); element e
@@ -626,12 +583,12 @@ __global__ __launch_bounds__(S::THREADS) void k_loss_gemm(
         const int rpair = wave * kRowsPerWave + 2 * i;  // first row of this DMA (uniform)
         const unsigned lds = (rpair < 128 ? lds_stage[0] + (unsigned)rpair * 512u
                                           : lds_stage[1] + (unsigned)(rpair - 128) * 512u);
-        dma16(rsrc_b, lds, voff, 0u);
+        lds_dma16(rsrc_b, lds, voff, 0u);
       }
     }
     float* gds = gds_a;
     if (tid < BM) gds[tid] = gd_pre;
-    __builtin_amdgcn_s_waitcnt(WaitVmLgkm<0>::value);
+    __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<0>::value);
     __syncthreads();
 #pragma unroll
     for (int mi = 0; mi < S::MI; ++mi) {

@@ -29,8 +29,8 @@ __device__ __forceinline__ unsigned lds_address(const void* p) {
 
 // One wave-level 16-byte-per-lane DMA: lane l's 16 bytes at buffer offset voff + soff land at
 // LDS byte lds + 16 l.  Inline assembly keeps the compiler's automatic waits from draining
-// the DMA queue before unrelated LDS reads; every wait for these transfers is explicit.  No
-// VGPR is written.
+// the DMA queue before unrelated LDS reads; every wait for these transfers is explicit.  Its data
+// goes to LDS: no VGPR of the asm is overwritten after the statement.
 __device__ __forceinline__ void lds_dma16(const int32x4& rsrc, unsigned lds, unsigned voff,
                                           unsigned soff) {
   asm volatile(
