@@ -4,6 +4,7 @@ documented status codes before anything touches the GPU (fake pointers, never de
 import ctypes
 import os
 import re
+import subprocess
 
 import pytest
 
@@ -163,3 +164,12 @@ def test_kv4_attention_refusals(L):
     for bad in ((-1, 2, 8, 1, 10), (2, 2, 7, 1, 10), (2, 65536, 8, 1, 10), (2, 2, 8, -1, 10)):
         T, n, H, mq, ml = bad
         assert L.awq_kv4_attention_workspace_bytes(T, n, H, _cfg(), mq, ml) == 0
+
+
+def test_c_symbols_are_the_library_s_own(L):
+    """Every symbol of C linkage that the library exports carries its prefix (another could stand in the
+    way of a program's own)."""
+    out = subprocess.run(["nm", "-D", "--defined-only", awq.LIB_PATH], capture_output=True, text=True, check=True)
+    names = [line.split()[-1] for line in out.stdout.splitlines() if line]
+    own = [n for n in names if not n.startswith(("_Z", "__hip", "_init", "_fini", "_edata", "_end", "__bss"))]
+    assert len(own) > 30 and all(n.startswith("awq_") for n in own), [n for n in own if not n.startswith("awq_")]

@@ -484,6 +484,8 @@ int awq_fake_quant_delta(const void* W, const float* s, int64_t out_features,
       cfg->group_size, cfg->zero_point, (uint16_t*)dW_out, (hipStream_t)stream));
 }
 
+}  // extern "C"
+
 namespace {
 int pack_impl(const void* W, const float* s, const float* clip, int64_t out_features,
               int64_t in_features, const awq_qconfig* cfg, uint8_t* codes_out,
@@ -518,6 +520,8 @@ int pack_impl(const void* W, const float* s, const float* clip, int64_t out_feat
                                            (hipStream_t)stream));
 }
 }  // namespace
+
+extern "C" {
 
 int awq_quantize_pack(const void* W, const float* s, int64_t out_features, int64_t in_features,
                       const awq_qconfig* cfg, uint8_t* codes_out, void* scales_out,

@@ -49,6 +49,56 @@ int int8_shape(int64_t T, int64_t M, int64_t K, int64_t ldw, int64_t ldy) {
   return AWQ_OK;
 }
 
+bool kv4_valid(const awq_kv4_config* c) {
+  if (!c) return false;
+  if (c->head_dim != 64 && c->head_dim != 128) return false;
+  if (c->kv_heads < 1 || c->kv_heads > 65535) return false;
+  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return false;
+  if (c->group_size != 32 && c->group_size != 64 && c->group_size != 128) return false;
+  if (c->group_size > c->head_dim) return false;
+  return c->zero_point == 0 || c->zero_point == 1;
+}
+
+// Sizes common to the cache's calls; fills the launch description.
+int kv4_cache(const void* cache, int64_t n_pages, const int32_t* table, int64_t n_seqs,
+              int64_t max_blocks, const int32_t* lens, const int32_t* starts, int64_t n_tokens,
+              const awq_kv4_config* cfg, awq::Kv4Cache* out) {
+  if (!cache || !table || !lens || !starts || !cfg) return AWQ_E_NULL;
+  if (!kv4_valid(cfg)) return AWQ_E_CONFIG;
+  // n_seqs is a grid dimension; positions are 32-bit
+  if (n_pages < 1 || n_pages > 0x7fffffff || n_seqs < 0 || n_seqs > 65535 || max_blocks < 1 ||
+      max_blocks > 0x7fffffff / cfg->page_size || n_tokens < 0 || n_tokens > kMaxRows)
+    return AWQ_E_SHAPE;
+  if (!aligned(cache, 16) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(starts, 4))
+    return AWQ_E_ALIGN;
+  int log2p = 0;
+  while ((1 << log2p) < cfg->page_size) ++log2p;
+  *out = awq::Kv4Cache{(uint8_t*)cache, n_pages, table, lens, starts, (int)n_seqs, (int)max_blocks,
+                       cfg->kv_heads, cfg->head_dim, cfg->group_size, log2p, cfg->zero_point,
+                       awq::kv4_record(cfg->head_dim, cfg->group_size, cfg->page_size)};
+  return AWQ_OK;
+}
+
+// Rows of heads: 16-byte pieces from any (token, head); spans stay far from 64-bit overflow.
+int kv4_rows(const void* p, int64_t token_stride, int64_t head_stride) {
+  if (token_stride < 0 || head_stride < 0 || token_stride % 8 || head_stride % 8 ||
+      token_stride > ((int64_t)1 << 31) || head_stride > ((int64_t)1 << 31))
+    return AWQ_E_SHAPE;
+  return aligned(p, 16) ? AWQ_OK : AWQ_E_ALIGN;
+}
+
+int attention_shape(int64_t n_tokens, int64_t n_seqs, int64_t heads, const awq_kv4_config* cfg,
+                    int64_t max_q, int64_t max_len) {
+  if (n_tokens < 0 || n_tokens > kMaxRows || n_seqs < 0 || n_seqs > 65535 || max_q < 0 ||
+      max_len < 0 || max_len > ((int64_t)1 << 30) || max_q > ((int64_t)1 << 30))
+    return AWQ_E_SHAPE;
+  if (heads < 1 || heads > 65535 || heads % cfg->kv_heads) return AWQ_E_SHAPE;
+  // columns of a key head and (token, head) rows are counted in 32 bits
+  if (max_q * (heads / cfg->kv_heads) > ((int64_t)1 << 30)) return AWQ_E_SHAPE;
+  if (n_tokens > (((int64_t)1 << 31) - 1024) / heads) return AWQ_E_SHAPE;
+  return AWQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -145,48 +195,6 @@ int awq_int8_linear(const void* x, int64_t ldx, const float* s, int64_t n_tokens
   return hip_status(awq::launch_int8_matmul(a, ws, (hipStream_t)stream));
 }
 
-namespace {
-
-bool kv4_valid(const awq_kv4_config* c) {
-  if (!c) return false;
-  if (c->head_dim != 64 && c->head_dim != 128) return false;
-  if (c->kv_heads < 1 || c->kv_heads > 65535) return false;
-  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return false;
-  if (c->group_size != 32 && c->group_size != 64 && c->group_size != 128) return false;
-  if (c->group_size > c->head_dim) return false;
-  return c->zero_point == 0 || c->zero_point == 1;
-}
-
-// Sizes common to the cache's calls; fills the launch description.
-int kv4_cache(const void* cache, int64_t n_pages, const int32_t* table, int64_t n_seqs,
-              int64_t max_blocks, const int32_t* lens, const int32_t* starts, int64_t n_tokens,
-              const awq_kv4_config* cfg, awq::Kv4Cache* out) {
-  if (!cache || !table || !lens || !starts || !cfg) return AWQ_E_NULL;
-  if (!kv4_valid(cfg)) return AWQ_E_CONFIG;
-  // n_seqs is a grid dimension; positions are 32-bit
-  if (n_pages < 1 || n_pages > 0x7fffffff || n_seqs < 0 || n_seqs > 65535 || max_blocks < 1 ||
-      max_blocks > 0x7fffffff / cfg->page_size || n_tokens < 0 || n_tokens > kMaxRows)
-    return AWQ_E_SHAPE;
-  if (!aligned(cache, 16) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(starts, 4))
-    return AWQ_E_ALIGN;
-  int log2p = 0;
-  while ((1 << log2p) < cfg->page_size) ++log2p;
-  *out = awq::Kv4Cache{(uint8_t*)cache, n_pages, table, lens, starts, (int)n_seqs, (int)max_blocks,
-                       cfg->kv_heads, cfg->head_dim, cfg->group_size, log2p, cfg->zero_point,
-                       awq::kv4_record(cfg->head_dim, cfg->group_size, cfg->page_size)};
-  return AWQ_OK;
-}
-
-// Rows of heads: 16-byte pieces from any (token, head); spans stay far from 64-bit overflow.
-int kv4_rows(const void* p, int64_t token_stride, int64_t head_stride) {
-  if (token_stride < 0 || head_stride < 0 || token_stride % 8 || head_stride % 8 ||
-      token_stride > ((int64_t)1 << 31) || head_stride > ((int64_t)1 << 31))
-    return AWQ_E_SHAPE;
-  return aligned(p, 16) ? AWQ_OK : AWQ_E_ALIGN;
-}
-
-}  // namespace
-
 size_t awq_kv4_record_bytes(const awq_kv4_config* cfg) {
   return kv4_valid(cfg) ? awq::kv4_record(cfg->head_dim, cfg->group_size, cfg->page_size) : 0;
 }
@@ -232,22 +240,6 @@ int awq_kv4_read(const void* cache, int64_t n_pages, const int32_t* block_table,
   return hip_status(awq::launch_kv4_read(c, n_tokens, dtype == AWQ_BF16, k_out, v_out,
                                          (hipStream_t)stream));
 }
-
-namespace {
-
-int attention_shape(int64_t n_tokens, int64_t n_seqs, int64_t heads, const awq_kv4_config* cfg,
-                    int64_t max_q, int64_t max_len) {
-  if (n_tokens < 0 || n_tokens > kMaxRows || n_seqs < 0 || n_seqs > 65535 || max_q < 0 ||
-      max_len < 0 || max_len > ((int64_t)1 << 30) || max_q > ((int64_t)1 << 30))
-    return AWQ_E_SHAPE;
-  if (heads < 1 || heads > 65535 || heads % cfg->kv_heads) return AWQ_E_SHAPE;
-  // columns of a key head and (token, head) rows are counted in 32 bits
-  if (max_q * (heads / cfg->kv_heads) > ((int64_t)1 << 30)) return AWQ_E_SHAPE;
-  if (n_tokens > (((int64_t)1 << 31) - 1024) / heads) return AWQ_E_SHAPE;
-  return AWQ_OK;
-}
-
-}  // namespace
 
 size_t awq_kv4_attention_workspace_bytes(int64_t n_tokens, int64_t n_seqs, int64_t heads,
                                          const awq_kv4_config* cfg, int64_t max_q,
