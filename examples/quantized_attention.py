@@ -1,10 +1,10 @@
 """One attention block of a transformer on quantised operators, as a serving loop would run it.
 
   query/key/value projection: 8-bit weights and 8-bit activations per token, under the scales of
-                              the activation-aware search;
+                              the activation-aware search on calibration tokens;
   key/value cache:            4 bits, paged;
   attention:                  over the cache, prompts and single tokens through the same calls;
-  output projection:          4-bit weights, 16-bit activations.
+  output projection:          4-bit weights packed under its own search's scales, 16-bit activations.
 
 Random weights and inputs: the point is the order of the calls.  A batch of prompts of different
 lengths is taken in, then decoded a token at a time, the decoding step once as plain calls and
@@ -35,14 +35,17 @@ class Block:
         calib = torch.randn(512, hidden, generator=g, device=device).half()
         calib[:, ::97] *= 8  # a few channels stand out, as in real activations
 
-        # scales a^0.5 from the calibration activations, folded into the 8-bit weights
-        self.s = awq.awq_act_stats(calib).clamp_min(1e-4).sqrt()
-        self.wq, self.wstep = awq.awq_int8_quantize(w_qkv, self.s, fold="multiply")
-        # the 4-bit layer: group steps and zeros as the packer makes them, no scales
+        # the activation-aware search of both layers on the calibration tokens: the projection's scales
+        # go into its 8-bit weights, the output layer is packed with its own to 4 bits
+        self.w_qkv, self.w_out, self.calib = w_qkv, w_out, calib
         self.cfg4 = awq.qconfig(w_bit=4, group_size=128, zero_point=1)
-        ones = torch.ones(heads * head_dim, device=device)
-        self.codes, self.scales, self.zeros = awq.awq_quantize_pack(w_out, ones, self.cfg4)
-        self.w_qkv, self.w_out = w_qkv, w_out  # for a comparison only
+        self.alphas = [i / 20 for i in range(20)]
+        search = awq.awq_search_scales(w_qkv, calib, awq.awq_act_stats(calib), self.alphas, self.cfg4)
+        self.s = search["s"]
+        self.wq, self.wstep = awq.awq_int8_quantize(w_qkv, self.s, fold="multiply")
+        layer = awq.quantize_layer(w_out, self.attend_plain(calib).half(), self.alphas, self.cfg4)
+        self.s_out = layer["s"]
+        self.codes, self.scales, self.zeros = layer["codes"], layer["scales"], layer["zeros"]
 
         self.kv = awq.awq_kv4_config(head_dim, kv_heads, page_size=64, group_size=64, zero_point=1)
         pages = -(-max_len // 64)
@@ -60,18 +63,22 @@ class Block:
         awq.awq_kv4_append(k, v, self.cache, self.table, lens, starts, self.kv)
         o, _ = awq.awq_kv4_attention(q, self.cache, self.table, lens, starts, self.kv, max_q=max_q,
                                      max_len=max_len or self.max_len)
-        return awq.awq_w4a16_matmul(o.view(T, H * D), self.codes, self.scales, self.zeros, self.cfg4)
+        return awq.awq_w4a16_matmul(o.view(T, H * D), self.codes, self.scales, self.zeros, self.cfg4,
+                                    s=self.s_out)
 
-    def plain(self, x):
-        """The same block on 16-bit weights and keys, one whole sequence, in fp32."""
+    def attend_plain(self, x):
+        """Projection and attention on 16-bit weights and keys, one whole sequence, in fp32."""
         T, H, Hk, D = x.shape[0], self.heads, self.kv_heads, self.dim
         qkv = (x.float() @ self.w_qkv.float().t()).view(T, H + 2 * Hk, D)
         q, k, v = qkv.split([H, Hk, Hk], dim=1)
         k, v = (t.repeat_interleave(H // Hk, dim=1).transpose(0, 1).contiguous() for t in (k, v))
         s = torch.matmul(q.transpose(0, 1).contiguous(), k.transpose(1, 2).contiguous()) * D ** -0.5
         s = s.masked_fill(torch.ones(T, T, dtype=torch.bool, device=x.device).triu(1), float("-inf"))
-        o = torch.matmul(s.softmax(-1), v).transpose(0, 1).reshape(T, H * D)
-        return o @ self.w_out.float().t()
+        return torch.matmul(s.softmax(-1), v).transpose(0, 1).reshape(T, H * D)
+
+    def plain(self, x):
+        """The whole block so."""
+        return self.attend_plain(x) @ self.w_out.float().t()
 
 
 def run(tokens=16, hidden=4096, heads=32, kv_heads=8, prompts=(200, 1, 77), max_len=1024):

@@ -15,6 +15,7 @@ import os
 import pytest
 import torch
 
+import weight_only_quantization_act_amd as awq
 from tests.gpu_util import requires_gpu, say
 
 pytestmark = [pytest.mark.gpu, requires_gpu]
@@ -38,3 +39,19 @@ def test_block_decodes_and_replays():
         assert o.shape == w.shape == (p + tokens, 512)
         assert float((o.float() - w).norm() / w.norm()) < 0.32
     assert torch.equal(replayed, last)
+
+
+def test_layers_carry_the_scales_of_the_search():
+    """What the example says of its two layers: the projection's codes stand for its weights times the
+    scales that the search found on the calibration tokens, the output layer is packed with its own."""
+    say("attention block: scales")
+    b = _example().Block(hidden=512, heads=8, kv_heads=2, max_seqs=1, max_len=64)
+    found = awq.awq_search_scales(b.w_qkv, b.calib, awq.awq_act_stats(b.calib), b.alphas, b.cfg4)
+    assert torch.equal(b.s, found["s"]) and int(found["best"]) > 0
+    wq, wstep = awq.awq_int8_quantize(b.w_qkv, found["s"], fold="multiply")
+    assert torch.equal(b.wq, wq) and torch.equal(b.wstep, wstep)
+    o = b.attend_plain(b.calib).half()
+    found = awq.awq_search_scales(b.w_out, o, awq.awq_act_stats(o), b.alphas, b.cfg4)
+    assert torch.equal(b.s_out, found["s"])
+    codes, scales, zeros = awq.awq_quantize_pack(b.w_out, found["s"], b.cfg4)
+    assert torch.equal(b.codes, codes) and torch.equal(b.scales, scales) and torch.equal(b.zeros, zeros)
