@@ -317,3 +317,36 @@ def test_more_outputs_than_a_grid_dimension():
     xq, xs = awq.awq_int8_quantize(x)
     want = (xq.double() @ wq[-5:].double().t()).float() * xs[:, None] * ws[-5:]
     assert torch.equal(y[:, -5:], want.half())
+
+
+@pytest.mark.parametrize("news", [1, 50])
+def test_cache_operators_on_another_stream(news):
+    """Work follows the given stream: what is made on a side stream is read after it, and a workspace and
+    outputs that the call allocates belong to that stream."""
+    say(f"kv4 side stream rows={news}")
+    lens = (2000, 300, 77)
+    c = Case(128, 2, 16, 64, 1, lens, [news] * 3, seed=news)
+    c.fill()
+    ref = Case(128, 2, 16, 64, 1, lens, [news] * 3, seed=news)
+    ref.cache.copy_(c.cache)
+    T = 3 * news
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    big = torch.randn(4096, 4096, device="cuda")
+    for rep in range(4):
+        with torch.cuda.stream(side):
+            for _ in range(4):
+                big = torch.mm(big, big).clamp_(-1, 1)       # keeps the stream busy
+            x = torch.randn(3, T, 8, 128, device="cuda").half() + big[0, 0].half() * 0
+        awq.awq_kv4_append(x[0, :, :2], x[1, :, :2], c.cache, c.dtable, c.dlens, c.dstarts, c.cfg, stream=side)
+        k, v = awq.awq_kv4_read(c.cache, c.dtable, c.dlens, c.dstarts, c.cfg, T, stream=side)
+        out, lse = awq.awq_kv4_attention(x[2], c.cache, c.dtable, c.dlens, c.dstarts, c.cfg, max_q=news,
+                                         max_len=2000, stream=side)
+        side.synchronize()
+        awq.awq_kv4_append(x[0, :, :2], x[1, :, :2], ref.cache, c.dtable, c.dlens, c.dstarts, c.cfg)
+        k2, v2 = awq.awq_kv4_read(ref.cache, c.dtable, c.dlens, c.dstarts, c.cfg, T)
+        o2, l2 = awq.awq_kv4_attention(x[2], ref.cache, c.dtable, c.dlens, c.dstarts, c.cfg, max_q=news,
+                                       max_len=2000)
+        torch.cuda.synchronize()
+        assert torch.equal(c.cache, ref.cache) and torch.equal(k, k2) and torch.equal(v, v2), rep
+        assert torch.equal(out, o2) and torch.equal(lse, l2), rep

@@ -373,6 +373,8 @@ def awq_kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.T
     [T, heads, head_dim] in q's type and lse fp32 [T, heads].  max_q and max_len are host
     bounds on the rows of a sequence and on seq_lens; scale defaults to 1 / sqrt(head_dim);
     window > 0 keeps the last `window` keys of each row.  Rows without keys give 0 and -inf.
+    Rows of no sequence (past q_start[-1]) and rows beyond max_q are not written: without an
+    `out` of the caller's they hold anything.
     A workspace (see awq_kv4_attention_workspace_bytes) is allocated unless one is passed."""
     n = _kv4_args(cache, block_table, seq_lens, q_start, cfg)
     dtype = q.dtype
