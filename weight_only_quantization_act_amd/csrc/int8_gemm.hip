@@ -273,8 +273,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_int8_few(FewArgs f) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, q = lane >> 4;
-  const int64_t first = (int64_t)block_number() * 16 * RT;
-  if (first >= a.M) return;  // the whole block
+  const unsigned first = block_number() * 16u * RT;  // below 2^32 past M, too
+  if (first >= (unsigned)a.M) return;                // the whole block
   const int m0 = (int)first;
   const int nch = (a.K + 255) >> 8;
 

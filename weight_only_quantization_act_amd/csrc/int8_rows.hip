@@ -24,11 +24,12 @@ constexpr int kRowThreads = 256;
 // NCH: 8-column chunks a thread keeps in registers (0: reads the row twice).
 template <bool BF16, bool VEC, int NCH>
 __global__ __launch_bounds__(kRowThreads) void k_int8_rows(
-    const uint16_t* __restrict__ A, int64_t rows, int K, int64_t lda, const float* __restrict__ s, int fold,
+    const uint16_t* __restrict__ A, unsigned rows, int K, int64_t lda, const float* __restrict__ s, int fold,
     int8_t* __restrict__ codes, int64_t ldc, float* __restrict__ steps) {
   __shared__ uint32_t red[kRowThreads / 64];
-  const int64_t row = block_number();
-  if (row >= rows) return;  // the whole block
+  const unsigned number = block_number();
+  if (number >= rows) return;  // the whole block
+  const int64_t row = number;
   const int tid = threadIdx.x;
   const uint16_t* a = A + row * lda;
   const int nch = ((K + 15) / 16) * 2;  // 8-column chunks, whole 16-byte groups of codes
@@ -80,7 +81,7 @@ hipError_t launch_int8_rows(const void* A, int64_t rows, int cols, int64_t lda, 
   const int f = s ? fold : kFoldNone;
 #define AWQ_ROWS(B, V, N)                                                                     \
   hipLaunchKernelGGL((k_int8_rows<B, V, N>), grid_of(rows), dim3(kRowThreads), 0, stream, \
-                     (const uint16_t*)A, rows, cols, lda, s, f, codes, ld_codes, steps)
+                     (const uint16_t*)A, (unsigned)rows, cols, lda, s, f, codes, ld_codes, steps)
 #define AWQ_ROWS_N(B, V)            \
   switch (keep) {                   \
     case 2: AWQ_ROWS(B, V, 2); break; \

@@ -106,7 +106,7 @@ __device__ __forceinline__ uint32_t quantise_group(const uint4 raw, uint32_t& pa
 // Sequence s owns the R-row groups from starts[s] / R + 2 s on: that leaves it enough of them
 // wherever its first position lies, without a sum over the sequences before it.  The groups
 // after the last sequence's hold the rows that belong to none.
-__host__ __device__ constexpr int64_t row_groups(int64_t n_tokens, int dim, int n_seqs) {
+__host__ __device__ constexpr int row_groups(int n_tokens, int dim, int n_seqs) {
   return n_tokens / (2048 / dim) + 2 * n_seqs + 1;
 }
 template <int D>
@@ -283,7 +283,7 @@ hipError_t launch_kv4_append(const Kv4Cache& c, const void* k, int64_t kt, int64
                              const void* v, int64_t vt, int64_t vh, int64_t n_tokens, bool bf16,
                              hipStream_t stream) {
   if (n_tokens <= 0) return hipSuccess;
-  const int64_t blocks = row_groups(n_tokens, c.dim, c.n_seqs) * c.kv_heads;
+  const int64_t blocks = (int64_t)row_groups((int)n_tokens, c.dim, c.n_seqs) * c.kv_heads;
   if (blocks > 0x7fffffff - (1 << 20)) return hipErrorInvalidValue;
 #define AWQ_APPEND_Z(B, D, GS, Z)                                                              \
   hipLaunchKernelGGL((k_kv4_append<B, D, GS, Z>), grid_of(blocks), dim3(256), 0, stream, c, \
@@ -300,7 +300,7 @@ hipError_t launch_kv4_append(const Kv4Cache& c, const void* k, int64_t kt, int64
 hipError_t launch_kv4_read(const Kv4Cache& c, int64_t n_tokens, bool bf16, void* k, void* v,
                            hipStream_t stream) {
   if (n_tokens <= 0) return hipSuccess;
-  const int64_t blocks = row_groups(n_tokens, c.dim, c.n_seqs) * c.kv_heads;
+  const int64_t blocks = (int64_t)row_groups((int)n_tokens, c.dim, c.n_seqs) * c.kv_heads;
   if (blocks > 0x7fffffff - (1 << 20)) return hipErrorInvalidValue;
   const dim3 grid = grid_of(blocks);
 #define AWQ_READ(B, D, GS)                                                     \
