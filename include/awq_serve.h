@@ -52,8 +52,8 @@ int awq_int8_quantize(const void* A, int64_t rows, int64_t cols, int64_t lda, in
  *   y[t][m] = float(sum_i xq[t][i] wq[m][i]) * xstep[t] * wstep[m] + bias[m]
  * The sum is exact (int32), then each operation, left to right, rounds once in fp32 and the
  * result once to the output type.
- *   xq     int8 [n_tokens][ldx], wq int8 [out][ldw], 16-byte aligned, strides multiples of 16
- *          and at least in_features rounded up to 16.  Columns from in_features up to that are
+ *   xq     int8 [n_tokens][ldx], wq int8 [out][ldw], 16-byte aligned, strides multiples of 16,
+ *          at least in_features rounded up to 16 and below 2^22.  Columns from in_features up to that are
  *          read: they must be zero in xq or in wq (awq_int8_quantize writes zeros)
  *   xstep  fp32 [n_tokens], wstep fp32 [out], 4-byte aligned
  *   bias   [out] in the output's type, or NULL
@@ -113,7 +113,8 @@ int awq_int8_linear(const void* x, int64_t ldx, const float* s, int64_t n_tokens
  *                .. seq_lens[b] - 1).  Rows at negative positions do not exist: they are not
  *                written, read as zeros and attend to nothing.  Nor do rows past n_tokens
  *   k, v, q      fp16 or bf16 [token][head][head_dim], unit stride in head_dim, token and head
- *                strides in elements (multiples of 8, 16-byte aligned base)
+ *                strides in elements (multiples of 8, 0 .. 2^31, 16-byte aligned base)
+ * n_seqs <= 65535, n_pages < 2^31, max_blocks x page_size < 2^31.
  * All sizes are device data except the bounds named below; a call may be captured and replayed
  * while lengths and tables change within those bounds.
  * ---------------------------------------------------------------------------------- */
@@ -152,12 +153,15 @@ int awq_kv4_read(const void* cache, int64_t n_pages, const int32_t* block_table,
  * fp32; q enters the products in fp16, each row scaled by a power of two (exact but for parts
  * 2^-24 and more below the row's largest), the probabilities times the value's step rounded to
  * fp16 with 2^-11 relative error (or 2^-36 of the largest finite value step that the row sees);
- * keys and values enter as the integers code - zero, with zeros 0 .. 15.  A NaN or infinity in a row
- * of q or a NaN in a key that it sees makes the row NaN, one in a value the channels of its group;
- * keys that a row does not see cost it no precision either.  The order of every sum is fixed: results repeat bit for bit for the same bounds.
+ * keys and values enter as the integers code - zero, with zeros 0 .. 15; where max_q x heads /
+ * kv_heads is at most 16, as 16 + code and 16 + zero, whose fp32 sums round at sum p step (code +
+ * zero + 32) and are subtracted at the end.  A NaN or infinity in a row of q or a NaN in a key
+ * that it sees makes the row NaN, one in a value the channels of its group; keys that a row does
+ * not see cost it no precision either.  The order of every sum is fixed: results repeat bit for
+ * bit for the same bounds.
  *   q        as above, n_tokens rows, heads a multiple of kv_heads
- *   max_q    bound on the rows of one sequence, max_len bound on seq_lens (both host values:
- *            they size the launch; rows and keys beyond them are not computed)
+ *   max_q    bound on the rows of one sequence, max_len bound on seq_lens (both host values, up to
+ *            2^30: they size the launch; rows and keys beyond them are not computed)
  *   scale    finite, > 0; window 0 or more
  *   out      [n_tokens][heads][head_dim] contiguous, q's type, 16-byte aligned; rows past
  *            q_start[n_seqs] are not written

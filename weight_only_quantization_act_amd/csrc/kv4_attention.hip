@@ -11,7 +11,8 @@
 //
 // Codes as operands: a nibble in the top four mantissa bits of a fp16 pattern whose other bits
 // are those of 16.0 is the number 16 + c, exactly: a shift and a v_and_or per pair of codes.
-// The 16 goes into the zeros' sums.  (Lower bits would save shifts and cost accuracy: 64 + c or
+// The 16 goes into the zeros' sums: fp32 rounds at sum w (c + z + 32), which a key of a large step
+// raises even where its code is its zero.  (Lower bits would save shifts and cost accuracy: 64 + c or
 // 1024 + c cancel more of the fp32 sums, and the subnormals c 2^-24 lose their leading zeros in
 // the matrix cores, which align the terms of a sum by their exponent fields: 2^-17 of the sum,
 // measured.)  The cache's word order (awq_serve.h) is the operand order of these instructions.
@@ -29,16 +30,19 @@
 // from the largest finite value step that the column has seen that w 2^f stays below 2^15: fp16
 // holds them with full precision down to 2^-29 of the largest (a step of a masked key, NaN or
 // infinite, does not count, or it would cost the others their precision).  A rise of the maximum or
-// of that step multiplies what was summed so far by exp2 of the difference.
+// of that step multiplies what was summed so far by exp2 of the difference.  The weights' 11 bits are a
+// choice: the error against 64 bits is 0.00026 of an fp16 output's norm where fp32 weights leave the
+// output's own rounding, 0.00021 (bf16: 0.0017 both); a second fp16 part of each weight would double
+// the second product's instructions.
 //
 // Two forms.  Up to 16 columns (decode): a block's waves share the columns and take the tiles in
 // turn, each with a ring of tiles in LDS that DMAs fill ahead; bound by the reading of the codes
 // and by the vector instructions that make operands of them (two a pair of codes, about 350 a
 // tile).  64 sequences of 2000 to 8192 tokens, 64 heads on 8 key heads of 128, groups of 64:
-// 91 us, 4.1 TB/s of codes and parameters; one of 131072 tokens, groups of 128: 40 us, 3.6 TB/s.
-// More columns (prompts): column tiles a wave, and the codes are decoded once a block; bound by
-// the vector instructions of the softmax and by the products, which share the issue.  A prompt of
-// 4096 tokens, 32 heads on 8: 188 us, 0.73 PFLOP/s.  One form for both would decode the codes once a
+// 91 us, 4.1 TB/s of codes and parameters; one of 131072 tokens, groups of 128: 38 us, 3.7 TB/s.
+// More columns (prompts): column tiles a wave, and the codes are decoded once a block; registers and
+// LDS leave two waves a SIMD, which fill neither the vector unit (55% of the cycles: softmax, decoding)
+// nor the matrix cores (28%).  A prompt of 4096 tokens, 32 heads on 8: 187 us, 0.73 PFLOP/s.  One form for both would decode the codes once a
 // column tile (the prompt: 523 us), or leave three of four waves without work at a single token.
 #include <hip/hip_runtime.h>
 
