@@ -114,7 +114,8 @@ int awq_int8_linear(const void* x, int64_t ldx, const float* s, int64_t n_tokens
  *                written, read as zeros and attend to nothing.  Nor do rows past n_tokens
  *   k, v, q      fp16 or bf16 [token][head][head_dim], unit stride in head_dim, token and head
  *                strides in elements (multiples of 8, 0 .. 2^31, 16-byte aligned base)
- * n_seqs <= 65535, n_pages < 2^31, max_blocks x page_size < 2^31.
+ * n_seqs <= 65535, n_pages < 2^31, max_blocks x page_size < 2^31.  A call that would take 2^31
+ * blocks or so (n_tokens x kv_heads x head_dim 2^42, n_seqs x kv_heads 2^30) is AWQ_E_SHAPE.
  * All sizes are device data except the bounds named below; a call may be captured and replayed
  * while lengths and tables change within those bounds.
  * ---------------------------------------------------------------------------------- */

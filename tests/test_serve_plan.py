@@ -119,3 +119,25 @@ int main() {
     assert {int(rows) for (form, _, rows) in got if form == "few"} == {1, 2}
     for form in ("32", "64", "128"):
         assert {s[1] > 1 for s in SHAPES if s[0] == form} == {True, False}, form
+
+
+def test_calls_of_too_many_blocks_are_refused_for_their_size(L):
+    """Sizes within their own bounds that together make more blocks than a launch numbers: a status that
+    says so, before anything is launched."""
+    P = ctypes.c_void_p(0x10000)
+    SHAPE = 2
+
+    def append(hk, n, T):
+        cfg = awq.awq_kv4_config(128, hk, 64, 128, 1)
+        return L.awq_kv4_append(P, 128 * hk, 128, P, 128 * hk, 128, T, 0, P, 10, P, n, 4, P, P, ctypes.byref(cfg), None)
+
+    def read(hk, n, T):
+        cfg = awq.awq_kv4_config(128, hk, 64, 128, 1)
+        return L.awq_kv4_read(P, 10, P, n, 4, P, P, T, ctypes.byref(cfg), 0, P, P, None)
+    for call in (append, read):
+        assert call(65535, 65535, 1) == SHAPE and call(65535, 1, 1 << 20) == SHAPE
+        assert call(8000, 65535, 1) == DEVICE and call(8, 65535, 1 << 30) == DEVICE
+    cfg = awq.awq_kv4_config(128, 65535, 64, 128, 1)
+    assert _attend(L, cfg, 65535, 65535, 1, 8, 0, P, 1 << 60) == SHAPE
+    cfg = awq.awq_kv4_config(128, 8000, 64, 128, 1)
+    assert _attend(L, cfg, 30000, 8000, 1, 8, 0, P, 1 << 60) == DEVICE

@@ -402,7 +402,7 @@ template <class S, bool BF16>
 hipError_t launch_tiles(const Int8Args& a, int splits, int* part, hipStream_t stream) {
   const int tt = (a.T + S::BT - 1) / S::BT, tm = (a.M + S::BM - 1) / S::BM;
   const int64_t tiles = (int64_t)tt * tm;
-  if (tiles > 0x7fffffff - (1 << 20)) return hipErrorInvalidValue;
+  if (tiles > kMaxBlocks) return hipErrorInvalidValue;
   dim3 grid = grid_of(tiles);
   grid.z = (unsigned)splits;
   hipLaunchKernelGGL((k_int8_tiles<S, BF16>), grid,

@@ -1446,9 +1446,8 @@ hipError_t launch_join(const Kv4Cache& c, const Kv4Query& q, const Partials& par
 template <int D, int GS>
 hipError_t launch_dg(const Kv4Cache& c, const Kv4Query& q, const Kv4Plan& p, const Partials& part,
                      int64_t rows, hipStream_t stream) {
-  const int64_t blocks =
-      (int64_t)c.kv_heads * (p.wide ? (int64_t)p.tiles * p.splits * c.n_seqs : p.splits > 1 ? p.splits : c.n_seqs);
-  if (blocks > 0x7fffffff - (1 << 20)) return hipErrorInvalidValue;
+  const int64_t blocks = kv4_blocks(p, c.n_seqs, c.kv_heads);
+  if (blocks > kMaxBlocks) return hipErrorInvalidValue;
   const dim3 grid = grid_of(blocks);
   if (p.wide)
     hipLaunchKernelGGL((k_kv4_attention_wide<D, GS>), grid, dim3(64 * kWaves), 0, stream, c, q, part);

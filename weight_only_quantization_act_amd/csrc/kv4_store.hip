@@ -106,9 +106,6 @@ __device__ __forceinline__ uint32_t quantise_group(const uint4 raw, uint32_t& pa
 // Sequence s owns the R-row groups from starts[s] / R + 2 s on: that leaves it enough of them
 // wherever its first position lies, without a sum over the sequences before it.  The groups
 // after the last sequence's hold the rows that belong to none.
-__host__ __device__ constexpr int row_groups(int n_tokens, int dim, int n_seqs) {
-  return n_tokens / (2048 / dim) + 2 * n_seqs + 1;
-}
 template <int D>
 struct Rows {
   static constexpr int R = 2048 / D;
@@ -159,7 +156,7 @@ __global__ __launch_bounds__(256) void k_kv4_append(Kv4Cache c, const uint16_t* 
   __shared__ int64_t page_at[R];  // each row's record, or -1
   const int number = (int)block_number();
   const int group = number / c.kv_heads, head = number - group * c.kv_heads;
-  if (group >= row_groups(n_tokens, D, c.n_seqs)) return;  // the whole block
+  if (group > n_tokens / Rows<D>::R + 2 * c.n_seqs) return;  // the whole block
   const Rows<D> rows = rows_of<D>(c, group, n_tokens);
   if (rows.seq < 0 || rows.t0 >= rows.end || rows.t0 + R <= rows.first) return;  // the whole block
   const int row = threadIdx.x / LPR, l = threadIdx.x % LPR;
@@ -220,7 +217,7 @@ __global__ __launch_bounds__(256) void k_kv4_read(Kv4Cache c, uint16_t* __restri
   __shared__ uint32_t words[R * D / 8];
   const int number = (int)block_number();
   const int group = number / c.kv_heads, head = number - group * c.kv_heads;
-  if (group >= row_groups(n_tokens, D, c.n_seqs)) return;  // the whole block
+  if (group > n_tokens / Rows<D>::R + 2 * c.n_seqs) return;  // the whole block
   const Rows<D> rows = rows_of<D>(c, group, n_tokens);
   if (rows.t0 >= rows.end || rows.t0 + R <= rows.first) return;  // the whole block
   const int P = 1 << c.log2p;
@@ -283,8 +280,8 @@ hipError_t launch_kv4_append(const Kv4Cache& c, const void* k, int64_t kt, int64
                              const void* v, int64_t vt, int64_t vh, int64_t n_tokens, bool bf16,
                              hipStream_t stream) {
   if (n_tokens <= 0) return hipSuccess;
-  const int64_t blocks = (int64_t)row_groups((int)n_tokens, c.dim, c.n_seqs) * c.kv_heads;
-  if (blocks > 0x7fffffff - (1 << 20)) return hipErrorInvalidValue;
+  const int64_t blocks = kv4_store_blocks(n_tokens, c.dim, c.n_seqs, c.kv_heads);
+  if (blocks > kMaxBlocks) return hipErrorInvalidValue;
 #define AWQ_APPEND_Z(B, D, GS, Z)                                                              \
   hipLaunchKernelGGL((k_kv4_append<B, D, GS, Z>), grid_of(blocks), dim3(256), 0, stream, c, \
                      (const uint16_t*)k, kt, kh, (const uint16_t*)v, vt, vh, (int)n_tokens)
@@ -300,8 +297,8 @@ hipError_t launch_kv4_append(const Kv4Cache& c, const void* k, int64_t kt, int64
 hipError_t launch_kv4_read(const Kv4Cache& c, int64_t n_tokens, bool bf16, void* k, void* v,
                            hipStream_t stream) {
   if (n_tokens <= 0) return hipSuccess;
-  const int64_t blocks = (int64_t)row_groups((int)n_tokens, c.dim, c.n_seqs) * c.kv_heads;
-  if (blocks > 0x7fffffff - (1 << 20)) return hipErrorInvalidValue;
+  const int64_t blocks = kv4_store_blocks(n_tokens, c.dim, c.n_seqs, c.kv_heads);
+  if (blocks > kMaxBlocks) return hipErrorInvalidValue;
   const dim3 grid = grid_of(blocks);
 #define AWQ_READ(B, D, GS)                                                     \
   hipLaunchKernelGGL((k_kv4_read<B, D, GS>), grid, dim3(256), 0, stream, c, (uint16_t*)k, \

@@ -214,7 +214,8 @@ int awq_kv4_append(const void* k, int64_t k_token_stride, int64_t k_head_stride,
       (st = kv4_rows(v, v_token_stride, v_head_stride)))
     return st;
   if (n_tokens == 0 || n_seqs == 0) return AWQ_OK;
-  if (n_tokens > ((int64_t)1 << 38) / ((int64_t)cfg->kv_heads * cfg->head_dim)) return AWQ_E_SHAPE;
+  if (awq::kv4_store_blocks(n_tokens, cfg->head_dim, (int)n_seqs, cfg->kv_heads) > awq::kMaxBlocks)
+    return AWQ_E_SHAPE;
   if ((st = device_ptrs({k, v, cache, block_table, seq_lens, q_start}))) return st;
   clear_pending_error();
   return hip_status(awq::launch_kv4_append(c, k, k_token_stride, k_head_stride, v, v_token_stride,
@@ -234,7 +235,8 @@ int awq_kv4_read(const void* cache, int64_t n_pages, const int32_t* block_table,
   if (!dtype_valid(dtype)) return AWQ_E_CONFIG;
   if (!aligned(k_out, 16) || !aligned(v_out, 16)) return AWQ_E_ALIGN;
   if (n_tokens == 0) return AWQ_OK;
-  if (n_tokens > ((int64_t)1 << 38) / ((int64_t)cfg->kv_heads * cfg->head_dim)) return AWQ_E_SHAPE;
+  if (awq::kv4_store_blocks(n_tokens, cfg->head_dim, (int)n_seqs, cfg->kv_heads) > awq::kMaxBlocks)
+    return AWQ_E_SHAPE;
   if ((st = device_ptrs({cache, block_table, seq_lens, q_start, k_out, v_out}))) return st;
   clear_pending_error();
   return hip_status(awq::launch_kv4_read(c, n_tokens, dtype == AWQ_BF16, k_out, v_out,
@@ -272,6 +274,7 @@ int awq_kv4_attention(const void* q, int64_t q_token_stride, int64_t q_head_stri
   if (n_tokens == 0 || n_seqs == 0 || max_q == 0) return AWQ_OK;
   const awq::Kv4Plan p = awq::kv4_plan(n_seqs, (int)heads, cfg->kv_heads, cfg->head_dim,
                                        cfg->group_size, max_q, max_len, window);
+  if (awq::kv4_blocks(p, (int)n_seqs, cfg->kv_heads) > awq::kMaxBlocks) return AWQ_E_SHAPE;
   // of this very plan, so that no launch can write past what it was given
   const size_t need =
       round_up(awq::kv4_workspace(p, n_tokens, n_seqs, (int)heads, cfg->kv_heads, cfg->head_dim), kAlign);

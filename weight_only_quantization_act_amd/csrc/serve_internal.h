@@ -8,6 +8,9 @@
 
 namespace awq {
 
+// Blocks of one launch at most: numbered in 32 bits, with a row of the grid to spare (grid.h).
+constexpr int64_t kMaxBlocks = 0x7fffffff - (1 << 20);
+
 // ---- rows of 8-bit integers ------------------------------------------------------------
 constexpr int kFoldNone = -1, kFoldDivide = 0, kFoldMultiply = 1;
 hipError_t launch_int8_rows(const void* A, int64_t rows, int cols, int64_t lda, bool bf16,
@@ -52,6 +55,10 @@ struct Kv4Cache {
 inline unsigned kv4_record(int dim, int group, int page) {
   return (unsigned)page * dim + 8u * page * (dim / group);
 }
+// Blocks of a write or read-back: groups of 2048 / dim rows (see kv4_store.hip) for each key head.
+constexpr int64_t kv4_store_blocks(int64_t n_tokens, int dim, int n_seqs, int kv_heads) {
+  return (n_tokens / (2048 / dim) + 2 * n_seqs + 1) * kv_heads;
+}
 hipError_t launch_kv4_append(const Kv4Cache& c, const void* k, int64_t kt, int64_t kh,
                              const void* v, int64_t vt, int64_t vh, int64_t n_tokens, bool bf16,
                              hipStream_t stream);
@@ -79,6 +86,9 @@ struct Kv4Plan {
 };
 Kv4Plan kv4_plan(int64_t n_seqs, int heads, int kv_heads, int dim, int group, int64_t max_q,
                  int64_t max_len, int64_t window);
+inline int64_t kv4_blocks(const Kv4Plan& p, int n_seqs, int kv_heads) {
+  return (int64_t)kv_heads * (p.wide ? (int64_t)p.tiles * p.splits * n_seqs : p.splits > 1 ? p.splits : n_seqs);
+}
 size_t kv4_workspace(const Kv4Plan& p, int64_t n_tokens, int64_t n_seqs, int heads, int kv_heads,
                      int dim);
 // What covers the plan of every window.
