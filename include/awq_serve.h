@@ -93,8 +93,7 @@ int awq_int8_linear(const void* x, int64_t ldx, const float* s, int64_t n_tokens
  *   A group whose range is not finite (it holds a NaN or an infinity, or the range overflows) is
  *   stored with step NaN, codes and zero 0.
  *   A finite step beyond fp16's 65504 (bf16 ranges of a million) is stored as infinity: such values
- *   read as infinite or NaN, and a key of such a step makes the rows that see it NaN or, where all
- *   it gives is -infinity, weighs nothing in them.
+ *   read as infinite or NaN, and a key of such a step makes the rows that see it NaN.
  *
  *   cache        uint8 [n_pages][kv_heads][record], 16-byte aligned; record =
  *                awq_kv4_record_bytes(cfg).  With D = head_dim, P = page_size, g = group_size,

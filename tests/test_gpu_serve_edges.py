@@ -350,3 +350,29 @@ def test_cache_operators_on_another_stream(news):
         torch.cuda.synchronize()
         assert torch.equal(c.cache, ref.cache) and torch.equal(k, k2) and torch.equal(v, v2), rep
         assert torch.equal(out, o2) and torch.equal(lse, l2), rep
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_keys_of_infinite_step(form):
+    """Keys so large (bf16) that their step is infinite in fp16 are NaN to the rows that see them, whatever
+    the sign of what they give, and nothing to the others."""
+    say(f"kv4 keys of infinite step {form}")
+    n, Hk, news, bound = FORMS[form]
+    lens = [int(x) for x in np.random.default_rng(n).integers(news + 1, 400, n)]
+    for sign in (1, -1):
+        c = Case(64, Hk, 16, 32, 1, lens, [news] * n, "bf16", seed=n)
+        k, v = c.kv(sum(lens))
+        ends = np.cumsum(lens)
+        at = [int(e) - 1 - b % 3 * (news // 2) for b, e in enumerate(ends)]   # one key a sequence, head 0
+        k[at, 0, 32:] = sign * 4.0e6
+        starts = torch.tensor(np.concatenate(([0], ends)), dtype=torch.int32, device="cuda")
+        awq.awq_kv4_append(k, v, c.cache, c.dtable, c.dlens, starts, c.cfg)
+        q = torch.rand(n * news, 3 * Hk, 64, device="cuda").bfloat16() + 0.1
+        out, lse = awq.awq_kv4_attention(q, c.cache, c.dtable, c.dlens, c.dstarts, c.cfg, max_q=news,
+                                         max_len=bound or max(lens))
+        row = np.concatenate([np.arange(e - news, e) for e in ends])          # the rows' own tokens
+        want = np.zeros((n * news, 3 * Hk), bool)
+        want[:, :3] = (row >= np.repeat(at, news))[:, None]
+        assert np.array_equal(lse.isnan().cpu().numpy(), want), (sign, form)
+        assert np.array_equal(out.isnan().all(-1).cpu().numpy(), want)
+        assert np.array_equal(out.isnan().any(-1).cpu().numpy(), want)

@@ -412,14 +412,19 @@ __device__ __forceinline__ void do_tile(TileRegs<D, GS>& r, Column<D, GS>& c, bo
       }
     }
   }
+  float mn = s[0];  // the least score of a key that is seen
+#pragma unroll
+  for (int e = 1; e < 8; ++e) mn = fminf(mn, s[e]);
   uint32_t seen = 0xff;  // bit e: key 8 q + e exists for the column
   if (!whole) {
     seen = 0;
     int last = min(there - 1, c.pos - kq), fst = c.pos - lo_off - kq;
     asm volatile("" : "+v"(last), "+v"(fst));
+    mn = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const bool ok = e <= last && e >= fst;
+      mn = ok ? fminf(mn, s[e]) : mn;
       s[e] = ok ? s[e] : kNegInf;
       seen |= ok ? 1u << e : 0u;
     }
@@ -427,6 +432,8 @@ __device__ __forceinline__ void do_tile(TileRegs<D, GS>& r, Column<D, GS>& c, bo
   float mx = s[0];
 #pragma unroll
   for (int e = 1; e < 8; ++e) mx = fmaxf(mx, s[e]);
+  // a key of infinite step is NaN, also where what it gives is -infinity, as if it were not there
+  if (mn == kNegInf) c.l = __builtin_nanf("");
   mx *= c.sigma;
   // seldom: a score above the column's maximum, or a value step above what the weights' scale
   // was made for
@@ -1059,6 +1066,10 @@ void k_kv4_attention_wide(Kv4Cache c, Kv4Query a, Partials part) {
 #pragma unroll
       for (int k = 0; k < R::PW; ++k) r.par[k] = ok ? r.par[k] : 0u;
     }
+    // an infinite step of a key as NaN: its scores could be -infinity, as if it were not there
+#pragma unroll
+    for (int k = 0; k < R::PW; ++k)
+      if (wave + kWaves * k < X::G && (r.par[k] & 0xffffu) == 0x7c00u) r.par[k] |= 0x7e00u;
 #pragma unroll
     for (int w = 0; w < X::KW; ++w) {
       const uint32_t par = r.kz[w / X::WPG], zz = __builtin_amdgcn_perm(par, par, 0x03020302u);
