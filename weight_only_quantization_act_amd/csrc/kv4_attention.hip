@@ -31,8 +31,8 @@
 // holds them with full precision down to 2^-29 of the largest (a step of a masked key, NaN or
 // infinite, does not count, or it would cost the others their precision).  A rise of the maximum or
 // of that step multiplies what was summed so far by exp2 of the difference.  The weights' 11 bits are a
-// choice: the error against 64 bits is 0.00026 of an fp16 output's norm where fp32 weights leave the
-// output's own rounding, 0.00021 (bf16: 0.0017 both); a second fp16 part of each weight would double
+// choice: the error against 64 bits is 0.00022 to 0.00027 of an fp16 output's norm where fp32 weights
+// leave the output's own rounding, 0.00020 (bf16: 0.0017 both); a second fp16 part of each weight would double
 // the second product's instructions.
 //
 // Two forms.  Up to 16 columns (decode): a block's waves share the columns and take the tiles in
@@ -42,7 +42,7 @@
 // 91 us, 4.1 TB/s of codes and parameters; one of 131072 tokens, groups of 128: 38 us, 3.7 TB/s.
 // More columns (prompts): column tiles a wave, and the codes are decoded once a block; registers and
 // LDS leave two waves a SIMD, which fill neither the vector unit (55% of the cycles: softmax, decoding)
-// nor the matrix cores (28%).  A prompt of 4096 tokens, 32 heads on 8: 187 us, 0.73 PFLOP/s.  One form for both would decode the codes once a
+// nor the matrix cores (28%).  A prompt of 4096 tokens, 32 heads on 8: 188 us, 0.73 PFLOP/s.  One form for both would decode the codes once a
 // column tile (the prompt: 523 us), or leave three of four waves without work at a single token.
 #include <hip/hip_runtime.h>
 
