@@ -42,8 +42,8 @@
 // 91 us, 4.1 TB/s of codes and parameters; one of 131072 tokens, groups of 128: 38 us, 3.7 TB/s.
 // More columns (prompts): column tiles a wave, and the codes are decoded once a block; registers and
 // LDS leave two waves a SIMD, which fill neither the vector unit (55% of the cycles: softmax, decoding)
-// nor the matrix cores (28%).  A prompt of 4096 tokens, 32 heads on 8: 188 us, 0.73 PFLOP/s.  One form for both would decode the codes once a
-// column tile (the prompt: 523 us), or leave three of four waves without work at a single token.
+// nor the matrix cores (28%).  A prompt of 4096 tokens, 32 heads on 8: 188 us, 0.73 PFLOP/s.  One
+// form for both would decode the codes once a column tile (the prompt: 523 us), or leave three of four waves without work at a single token.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -1450,7 +1450,8 @@ hipError_t launch_join(const Kv4Cache& c, const Kv4Query& q, const Partials& par
     hipLaunchKernelGGL((k_kv4_join<D, kParts, DIVIDED>), grid_of(rows), dim3(256), 0, stream, c, q,
                        part, rows);
   else
-    hipLaunchKernelGGL((k_kv4_join<D, 1, DIVIDED>), grid_of((rows + kRows - 1) / kRows), dim3(256), 0, stream, c, q, part, rows);
+    hipLaunchKernelGGL((k_kv4_join<D, 1, DIVIDED>), grid_of((rows + kRows - 1) / kRows), dim3(256), 0,
+                       stream, c, q, part, rows);
   return hipGetLastError();
 }
 
