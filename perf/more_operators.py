@@ -179,7 +179,7 @@ def _quantise(v):
     q, byte = _elements(v)
     a = q.abs()
     code = torch.where(a < 2, a * 2, torch.where(a < 4, a + 2, a / 2 + 4)).to(torch.uint8)
-    code = (code + 8 * torch.signbit(q)).flatten(1)
+    code = (code + 8 * torch.signbit(q).to(torch.uint8)).flatten(1)
     codes = code[:, 0::2] | (code[:, 1::2] << 4)
     rows, nb = byte.shape
     byte = torch.nn.functional.pad(byte, (0, -nb % 4, 0, -rows % 4)).to(torch.uint8)
