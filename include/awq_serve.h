@@ -3,7 +3,11 @@
  *   - rows quantised to 8-bit integers (activations per token, weights per output channel),
  *     the product of two such matrices, and the linear layer that does both;
  *   - a paged key/value cache held in 4 bits by the same group quantiser as the weights, its
- *     write and read-back, and the attention that reads it.
+ *     write and read-back, and the attention that reads it;
+ *   - rows of microscaled 4-bit floating point (MXFP4), the product of two such matrices and the
+ *     linear layer that does both;
+ *   - the root-mean-square norm between two layers, with the residual's addition, which leaves its
+ *     output in 16 bits or as the rows that either product takes.
  *
  * Conventions are those of awq_act.h: device pointers owned by the caller, caller-provided
  * workspaces, work enqueued on `stream` without synchronising, status codes, every check on
@@ -19,8 +23,9 @@
 extern "C" {
 #endif
 
-/* Element type of activations, outputs, biases, queries, keys and values. */
-enum { AWQ_FP16 = 0, AWQ_BF16 = 1 };
+/* Element type of activations, outputs, biases, queries, keys and values; AWQ_FP32 is one of the
+ * norm's weight only. */
+enum { AWQ_FP16 = 0, AWQ_BF16 = 1, AWQ_FP32 = 2 };
 
 /* ------------------------------------------------------------------------------------
  * Rows of 8-bit integers
@@ -46,6 +51,13 @@ enum { AWQ_FOLD_DIVIDE = 0, AWQ_FOLD_MULTIPLY = 1 };
 int awq_int8_quantize(const void* A, int64_t rows, int64_t cols, int64_t lda, int32_t dtype,
                       const float* s, int32_t fold, int8_t* codes_out, int64_t ld_codes,
                       float* steps_out, void* stream);
+
+/* The values that the codes of awq_int8_quantize stand for: out[r][i] = codes[r][i] * steps[r], one
+ * fp32 rounding and one to dtype.
+ *   codes  int8 [rows][ld_codes], 16-byte aligned, ld_codes a multiple of 16 and at least cols rounded
+ *          up to 16;  steps fp32 [rows];  out fp16 or bf16 [rows][ldo >= cols] */
+int awq_int8_dequantize(const int8_t* codes, int64_t ld_codes, const float* steps, int64_t rows,
+                        int64_t cols, int32_t dtype, void* out, int64_t ldo, void* stream);
 
 /* ------------------------------------------------------------------------------------
  * Product in 8-bit integers
@@ -181,6 +193,106 @@ int awq_kv4_attention(const void* q, int64_t q_token_stride, int64_t q_head_stri
                       const awq_kv4_config* cfg, int64_t max_q, int64_t max_len, float scale,
                       int64_t window, void* out, float* lse_out, void* workspace,
                       size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Rows of microscaled 4-bit floating point (MXFP4, the OCP microscaling format with elements e2m1
+ * and scales e8m0)
+ *   v[r][i] = A[r][i], A[r][i] / s[i] (AWQ_FOLD_DIVIDE: activations under the scales of a
+ *             search [AWQ-notes §4.3]) or A[r][i] * s[i] (AWQ_FOLD_MULTIPLY: weights), in fp32,
+ *             one rounding, divisions correctly rounded
+ *   A block is 32 consecutive columns of a row (columns past the last are zeros) with one scale
+ *   2^(b - 127): b = max(0, floor(log2 max|v|) - 2 + 127), 0 for a block of zeros.  An element is the
+ *   value nearest to v / scale among +-{0, 0.5, 1, 1.5, 2, 3, 4, 6}, the one with an even code on ties,
+ *   6 for all above it.  A block that holds a NaN or an infinity (also one that the fold makes) gets
+ *   b = 255, which stands for NaN, and codes 0, so that whatever it is multiplied with is NaN.
+ *   A           fp16 or bf16 [rows][cols], row stride lda >= cols elements; 2-byte aligned
+ *               (16-byte loads are used where the base and lda allow them)
+ *   s           fp32 [cols] or NULL
+ *   codes       uint8 [rows][ld_codes], 16-byte aligned, ld_codes a multiple of 16, at least
+ *               16 ceil(cols / 32) and below 2^22: column 2 j in the low half of byte j, a code is the
+ *               sign (bit 3) and the index of the magnitude above.  Bytes up to 16 ceil(cols / 32) are
+ *               written, later ones not
+ *   scales      uint8 [ceil(cols / 128)][ld_scales][4], 16-byte aligned, ld_scales a multiple of 4, at
+ *               least rows: byte c of (q, r) is b of block 4 q + c of row r (0 past the last block);
+ *               rows past the last are not written
+ * rows < 2^29 - 512 (and ld_scales), cols <= 2^22.
+ * ---------------------------------------------------------------------------------- */
+int awq_mxfp4_quantize(const void* A, int64_t rows, int64_t cols, int64_t lda, int32_t dtype,
+                       const float* s, int32_t fold, uint8_t* codes_out, int64_t ld_codes,
+                       uint8_t* scales_out, int64_t ld_scales, void* stream);
+
+/* The values that they stand for, element times scale in fp32 (infinite beyond its range), rounded
+ * once to dtype; blocks of scale 255 are NaN.  out [rows][ldo >= cols], 2-byte aligned. */
+int awq_mxfp4_dequantize(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales,
+                         int64_t ld_scales, int64_t rows, int64_t cols, int32_t dtype, void* out,
+                         int64_t ldo, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Product in MXFP4
+ *   y[t][m] = sum_i x[t][i] w[m][i] + bias[m]
+ * on the values that codes and scales stand for.  The matrix cores add 64 or 128 products at a time
+ * to an fp32 sum (products of two elements are exact; each such step rounds within 2^-22 of its largest
+ * term or result); the parts of a divided K are added in a fixed order, the bias in fp32, and the
+ * result is rounded once to the output type.  Results repeat bit for bit.  A scale of 255 in a
+ * row makes the row's results NaN.
+ *   xc, xs  tokens' codes and scales, wc, ws the weights', as awq_mxfp4_quantize lays them out.
+ *           Columns from in_features up to a whole block are read: they must be zero in one of the two
+ *   bias    [out] in the output's type, or NULL
+ *   y       fp16 or bf16 [n_tokens][ldy], ldy >= out
+ *   workspace  device, 256-byte aligned, awq_mxfp4_matmul_workspace_bytes(...) bytes (0: may
+ *           be NULL); contents unspecified before and after
+ * n_tokens, out_features < 2^29 - 512, in_features <= 2^22, n_tokens * ldx, out * ldw and
+ * n_tokens * ldy below 2^47; 0 tokens or outputs enqueue nothing, in_features = 0 gives y = bias or 0.
+ * ---------------------------------------------------------------------------------- */
+size_t awq_mxfp4_matmul_workspace_bytes(int64_t n_tokens, int64_t out_features,
+                                        int64_t in_features);
+int awq_mxfp4_matmul(const uint8_t* xc, int64_t ldx, const uint8_t* xs, int64_t ldxs, int64_t n_tokens,
+                     const uint8_t* wc, int64_t ldw, const uint8_t* ws, int64_t ldws,
+                     int64_t out_features, int64_t in_features, const void* bias, int32_t dtype, void* y,
+                     int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The linear layer on floating activations: awq_mxfp4_quantize of x (AWQ_FOLD_DIVIDE by s if
+ * s is given) and awq_mxfp4_matmul, with the same result bit for bit.  Where tokens are few one launch
+ * quantises them on the fly; otherwise codes and scales go to the workspace.
+ *   x fp16 or bf16 [n_tokens][ldx >= in_features], y, bias in the same type; other arguments
+ *   as above. */
+size_t awq_mxfp4_linear_workspace_bytes(int64_t n_tokens, int64_t out_features,
+                                        int64_t in_features);
+int awq_mxfp4_linear(const void* x, int64_t ldx, const float* s, int64_t n_tokens, const uint8_t* wc,
+                     int64_t ldw, const uint8_t* ws, int64_t ldws, int64_t out_features,
+                     int64_t in_features, const void* bias, int32_t dtype, void* y, int64_t ldy,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Root-mean-square norm with the residual's addition
+ *   h[r][i] = x[r][i] + residual[r][i], rounded to dtype (x itself without a residual)
+ *   v[r][i] = h[r][i] weight[i] / sqrt(mean_i h[r][i]^2 + eps), rounded to fp32 (the sum and the
+ *             products are formed in fp64)
+ * and from v, by entry point: y = v rounded to dtype; the row's 8-bit codes and step as
+ * awq_int8_quantize makes them of fp32 values v; its MXFP4 codes and scales as awq_mxfp4_quantize does.
+ * The scales of a search are folded into the weight (weight / s) [AWQ-notes §4.3].  A row of h
+ * that holds a NaN or an infinity comes out as NaN whole (8 bits: step NaN and codes 0; MXFP4: scales
+ * 255 and codes 0); so does, in 8 bits, every row if the weight holds one.  Sums are taken in a
+ * fixed order: results repeat bit for bit.
+ *   x, residual  fp16 or bf16 [rows][cols] of one type, row strides ldx, ldr >= cols; residual NULL: none
+ *   weight       [cols] in dtype or fp32 (weight_dtype AWQ_FP32), or NULL: ones
+ *   eps          finite, at least 2^-126
+ *   h_out        [rows][ldh >= cols], written where a residual is given (else not looked at); may be
+ *                x or residual itself (same address and stride), or overlap neither
+ *   y, codes_out, ...  as in the calls above, no input's memory
+ * rows >= 0, cols 1 .. 2^31 - 512 (MXFP4: 2^22).
+ * ---------------------------------------------------------------------------------- */
+int awq_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr, int64_t rows,
+                int64_t cols, int32_t dtype, const void* weight, int32_t weight_dtype, double eps,
+                void* h_out, int64_t ldh, void* y, int64_t ldy, void* stream);
+int awq_rmsnorm_int8(const void* x, int64_t ldx, const void* residual, int64_t ldr, int64_t rows,
+                     int64_t cols, int32_t dtype, const void* weight, int32_t weight_dtype, double eps,
+                     void* h_out, int64_t ldh, int8_t* codes_out, int64_t ld_codes, float* steps_out,
+                     void* stream);
+int awq_rmsnorm_mxfp4(const void* x, int64_t ldx, const void* residual, int64_t ldr, int64_t rows,
+                      int64_t cols, int32_t dtype, const void* weight, int32_t weight_dtype, double eps,
+                      void* h_out, int64_t ldh, uint8_t* codes_out, int64_t ld_codes,
+                      uint8_t* scales_out, int64_t ld_scales, void* stream);
 
 #ifdef __cplusplus
 }

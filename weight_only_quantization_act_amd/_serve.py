@@ -16,7 +16,7 @@ import torch
 from ._lib import _buf, _check, _dev, _i32, _i64, _sz, _vp
 from ._lib import lib as _base_lib
 
-AWQ_FP16, AWQ_BF16 = 0, 1
+AWQ_FP16, AWQ_BF16, AWQ_FP32 = 0, 1, 2
 AWQ_FOLD_DIVIDE, AWQ_FOLD_MULTIPLY = 0, 1
 
 class awq_kv4_config(ctypes.Structure):
@@ -51,6 +51,22 @@ _SIGNATURES = {
     "awq_kv4_attention": (ctypes.c_int, [_vp, _i64, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _i64,
                                          _i64, _vp, _vp, _kvp, _i64, _i64, ctypes.c_float, _i64, _vp,
                                          _vp, _vp, _sz, _vp]),
+    "awq_int8_dequantize": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i64, _i32, _vp, _i64, _vp]),
+    "awq_mxfp4_quantize": (ctypes.c_int, [_vp, _i64, _i64, _i64, _i32, _vp, _i32, _vp, _i64, _vp, _i64,
+                                          _vp]),
+    "awq_mxfp4_dequantize": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i64, _i64, _i32, _vp, _i64, _vp]),
+    "awq_mxfp4_matmul_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "awq_mxfp4_matmul": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _i64,
+                                        _vp, _i32, _vp, _i64, _vp, _sz, _vp]),
+    "awq_mxfp4_linear_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "awq_mxfp4_linear": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _vp,
+                                        _i32, _vp, _i64, _vp, _sz, _vp]),
+    "awq_rmsnorm": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i64, _i64, _i32, _vp, _i32, ctypes.c_double,
+                                   _vp, _i64, _vp, _i64, _vp]),
+    "awq_rmsnorm_int8": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i64, _i64, _i32, _vp, _i32,
+                                        ctypes.c_double, _vp, _i64, _vp, _i64, _vp, _vp]),
+    "awq_rmsnorm_mxfp4": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i64, _i64, _i32, _vp, _i32,
+                                         ctypes.c_double, _vp, _i64, _vp, _i64, _vp, _i64, _vp]),
 }
 
 _BOUND: Optional[ctypes.CDLL] = None

@@ -42,6 +42,17 @@ __device__ __forceinline__ void lds_dma16(const int32x4& rsrc, unsigned lds, uns
       : "memory", "m0");
 }
 
+// The same with 4 bytes a lane, at buffer offset voff: to LDS byte lds + 4 l.
+__device__ __forceinline__ void lds_dma4(const int32x4& rsrc, unsigned lds, unsigned voff) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dword %1, %2, 0 offen lds"
+      :
+      : "s"(lds), "v"(voff), "s"(rsrc)
+      : "memory", "m0");
+}
+
 // s_waitcnt immediate: vmcnt(VM), lgkmcnt(0).
 template <int VM>
 struct WaitVmLgkm0 {

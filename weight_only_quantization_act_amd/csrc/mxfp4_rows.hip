@@ -1,0 +1,189 @@
+// Rows of MXFP4 from 16-bit rows (A, A / s or A * s) and back; read-back of 8-bit rows.
+//
+// Pages: "AWQ" scholia-log notes §2.3 (a group's range sets its step, values round to the grid), §4.3
+// (S^-1 folded into the activations).  The format is the OCP microscaling one: see mx_format.h.
+//
+// Bound by memory: 2 bytes of every value in, 17/32 out.  A block takes 16 rows of 512 columns, each
+// wave four rows one after another with its 512 columns, so that loads are 1 KiB in one
+// piece, the fold's scales are loaded once for four rows, and the scale words of 16 rows fill 64
+// contiguous bytes.
+#include <hip/hip_runtime.h>
+
+#include "grid.h"
+#include "int8_quant.h"
+#include "mx_format.h"
+#include "mx_internal.h"
+#include "serve_internal.h"
+
+namespace awq {
+
+namespace {
+
+constexpr int kRowsTile = 16;  // rows a block
+constexpr int kTileWords = 4;  // scale words (128 columns) of a row a block
+
+template <bool BF16, bool VEC>
+__global__ __launch_bounds__(256) void k_mxfp4_rows(const uint16_t* __restrict__ A, unsigned rows,
+                                                    int K, int64_t lda, const float* __restrict__ s,
+                                                    int fold, uint8_t* __restrict__ codes,
+                                                    int64_t ldc, uint32_t* __restrict__ scales,
+                                                    int64_t lds, unsigned tiles_k) {
+  const unsigned b = block_number();
+  const unsigned tr = b / tiles_k, tk = b - tr * tiles_k;
+  if (tr * kRowsTile >= rows) return;  // the whole block
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c0 = (int)(tk * (kTileWords * 128)) + 8 * lane;
+  const int q = c0 >> 7;
+  if (q >= (K + 127) >> 7) return;  // sixteen lanes together; no barrier follows
+  const bool stored = c0 < (K + 31) / 32 * 32;
+#pragma unroll
+  for (int i = 0; i < kRowsTile / 4; ++i) {
+    const unsigned row = tr * kRowsTile + 4 * i + wave;
+    if (row >= rows) return;  // the whole wave
+    float v[8];
+    load_row8<BF16, VEC>(A + (int64_t)row * lda, s, fold, c0, K, v);
+    uint32_t byte;
+    const uint32_t c = mx_codes8(v, byte);
+    if (stored) *(uint32_t*)(codes + (int64_t)row * ldc + (c0 >> 1)) = c;
+    const uint32_t w = mx_scale_word(byte);
+    if ((lane & 15) == 0) scales[(int64_t)q * lds + row] = w;
+  }
+}
+
+// 8 columns of a row from 4 bytes of codes or 8 of integers a thread.
+template <bool BF16>
+__device__ __forceinline__ void store_row8(uint16_t* out, int c0, int K, bool vec, const float (&v)[8]) {
+  uint16_t o[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o[j] = to16<BF16>(v[j]);
+  if (vec && c0 + 8 <= K) {
+    uint4 p;
+    p.x = o[0] | ((uint32_t)o[1] << 16);
+    p.y = o[2] | ((uint32_t)o[3] << 16);
+    p.z = o[4] | ((uint32_t)o[5] << 16);
+    p.w = o[6] | ((uint32_t)o[7] << 16);
+    *(uint4*)(out + c0) = p;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c0 + j < K) out[c0 + j] = o[j];
+  }
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(256) void k_mxfp4_values(const uint8_t* __restrict__ codes, int64_t ldc,
+                                                      const uint32_t* __restrict__ scales, int64_t lds,
+                                                      unsigned rows, int K, uint16_t* __restrict__ out,
+                                                      int64_t ldo, bool vec, unsigned tiles_k) {
+  const unsigned b = block_number();
+  const unsigned tr = b / tiles_k, tk = b - tr * tiles_k;
+  if (tr * kRowsTile >= rows) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c0 = (int)(tk * (kTileWords * 128)) + 8 * lane;
+  if (c0 >= K) return;
+#pragma unroll
+  for (int i = 0; i < kRowsTile / 4; ++i) {
+    const unsigned row = tr * kRowsTile + 4 * i + wave;
+    if (row >= rows) return;
+    const uint32_t c = *(const uint32_t*)(codes + (int64_t)row * ldc + (c0 >> 1));
+    const uint32_t word = scales[(int64_t)(c0 >> 7) * lds + row];
+    const uint32_t byte = (word >> (8 * ((c0 >> 5) & 3))) & 255u;
+    const float sc = byte == 255 ? __builtin_nanf("") : mx_scale(byte);
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    const f2 e[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, sc, 0),
+                     __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, sc, 1),
+                     __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, sc, 2),
+                     __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, sc, 3)};
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = e[j >> 1][j & 1];
+    store_row8<BF16>(out + (int64_t)row * ldo, c0, K, vec, v);
+  }
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(256) void k_int8_values(const int8_t* __restrict__ codes, int64_t ldc,
+                                                     const float* __restrict__ steps, unsigned rows,
+                                                     int K, uint16_t* __restrict__ out, int64_t ldo,
+                                                     bool vec, unsigned tiles_k) {
+  const unsigned b = block_number();
+  const unsigned tr = b / tiles_k, tk = b - tr * tiles_k;
+  if (tr * kRowsTile >= rows) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c0 = (int)(tk * (kTileWords * 128)) + 8 * lane;
+  if (c0 >= K) return;
+#pragma unroll
+  for (int i = 0; i < kRowsTile / 4; ++i) {
+    const unsigned row = tr * kRowsTile + 4 * i + wave;
+    if (row >= rows) return;
+    const uint2 c = *(const uint2*)(codes + (int64_t)row * ldc + c0);
+    const float st = steps[row];
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = (float)(int8_t)(c.x >> (8 * j)) * st;
+      v[j + 4] = (float)(int8_t)(c.y >> (8 * j)) * st;
+    }
+    store_row8<BF16>(out + (int64_t)row * ldo, c0, K, vec, v);
+  }
+}
+
+int64_t tiles(int64_t rows, int64_t cols) {
+  return (rows + kRowsTile - 1) / kRowsTile * ((cols + kTileWords * 128 - 1) / (kTileWords * 128));
+}
+unsigned col_tiles(int cols) { return (unsigned)((cols + kTileWords * 128 - 1) / (kTileWords * 128)); }
+
+}  // namespace
+
+int64_t mxfp4_rows_blocks(int64_t rows, int64_t cols) { return tiles(rows, cols); }
+int64_t values_blocks(int64_t rows, int64_t cols) { return tiles(rows, cols); }
+
+hipError_t launch_mxfp4_rows(const void* A, int64_t rows, int cols, int64_t lda, bool bf16,
+                             const float* s, int fold, uint8_t* codes, int64_t ld_codes,
+                             uint32_t* scales, int64_t ld_scales, hipStream_t stream) {
+  if (rows <= 0 || cols <= 0) return hipSuccess;
+  const bool vec = row_vector_loads(A, lda, s);
+  const int f = s ? fold : kFoldNone;
+#define AWQ_MXROWS(B, V)                                                                          \
+  hipLaunchKernelGGL((k_mxfp4_rows<B, V>), grid_of(tiles(rows, cols)), dim3(256), 0, stream,      \
+                     (const uint16_t*)A, (unsigned)rows, cols, lda, s, f, codes, ld_codes, scales, \
+                     ld_scales, col_tiles(cols))
+  if (bf16) {
+    if (vec) AWQ_MXROWS(true, true); else AWQ_MXROWS(true, false);
+  } else {
+    if (vec) AWQ_MXROWS(false, true); else AWQ_MXROWS(false, false);
+  }
+#undef AWQ_MXROWS
+  return hipGetLastError();
+}
+
+hipError_t launch_mxfp4_values(const uint8_t* codes, int64_t ld_codes, const uint32_t* scales,
+                               int64_t ld_scales, int64_t rows, int cols, bool bf16, void* out,
+                               int64_t ldo, hipStream_t stream) {
+  if (rows <= 0 || cols <= 0) return hipSuccess;
+  const bool vec = row_vector_loads(out, ldo, nullptr);
+  const dim3 grid = grid_of(tiles(rows, cols));
+  if (bf16)
+    hipLaunchKernelGGL((k_mxfp4_values<true>), grid, dim3(256), 0, stream, codes, ld_codes, scales,
+                       ld_scales, (unsigned)rows, cols, (uint16_t*)out, ldo, vec, col_tiles(cols));
+  else
+    hipLaunchKernelGGL((k_mxfp4_values<false>), grid, dim3(256), 0, stream, codes, ld_codes, scales,
+                       ld_scales, (unsigned)rows, cols, (uint16_t*)out, ldo, vec, col_tiles(cols));
+  return hipGetLastError();
+}
+
+hipError_t launch_int8_values(const int8_t* codes, int64_t ld_codes, const float* steps, int64_t rows,
+                              int cols, bool bf16, void* out, int64_t ldo, hipStream_t stream) {
+  if (rows <= 0 || cols <= 0) return hipSuccess;
+  const bool vec = row_vector_loads(out, ldo, nullptr);
+  const dim3 grid = grid_of(tiles(rows, cols));
+  if (bf16)
+    hipLaunchKernelGGL((k_int8_values<true>), grid, dim3(256), 0, stream, codes, ld_codes, steps,
+                       (unsigned)rows, cols, (uint16_t*)out, ldo, vec, col_tiles(cols));
+  else
+    hipLaunchKernelGGL((k_int8_values<false>), grid, dim3(256), 0, stream, codes, ld_codes, steps,
+                       (unsigned)rows, cols, (uint16_t*)out, ldo, vec, col_tiles(cols));
+  return hipGetLastError();
+}
+
+}  // namespace awq
