@@ -232,30 +232,28 @@ int awq_mxfp4_dequantize(const uint8_t* codes, int64_t ld_codes, const uint8_t* 
  *   y[t][m] = sum_i x[t][i] w[m][i] + bias[m]
  * on the values that codes and scales stand for.  The matrix cores add 64 or 128 products at a time
  * to an fp32 sum (products of two elements are exact; each such step rounds within 2^-22 of its largest
- * term or result); the parts of a divided K are added in a fixed order, the bias in fp32, and the
- * result is rounded once to the output type.  Results repeat bit for bit.  A scale of 255 in a
+ * term or result); the sums of waves that share the columns are added in a fixed order, the bias in
+ * fp32, and the result is rounded once to the output type.  Results repeat bit for bit.  A scale of 255 in a
  * row makes the row's results NaN.
  *   xc, xs  tokens' codes and scales, wc, ws the weights', as awq_mxfp4_quantize lays them out.
  *           Columns from in_features up to a whole block are read: they must be zero in one of the two
  *   bias    [out] in the output's type, or NULL
  *   y       fp16 or bf16 [n_tokens][ldy], ldy >= out
- *   workspace  device, 256-byte aligned, awq_mxfp4_matmul_workspace_bytes(...) bytes (0: may
- *           be NULL); contents unspecified before and after
  * n_tokens, out_features < 2^29 - 512, in_features <= 2^22, n_tokens * ldx, out * ldw and
  * n_tokens * ldy below 2^47; 0 tokens or outputs enqueue nothing, in_features = 0 gives y = bias or 0.
  * ---------------------------------------------------------------------------------- */
-size_t awq_mxfp4_matmul_workspace_bytes(int64_t n_tokens, int64_t out_features,
-                                        int64_t in_features);
 int awq_mxfp4_matmul(const uint8_t* xc, int64_t ldx, const uint8_t* xs, int64_t ldxs, int64_t n_tokens,
                      const uint8_t* wc, int64_t ldw, const uint8_t* ws, int64_t ldws,
                      int64_t out_features, int64_t in_features, const void* bias, int32_t dtype, void* y,
-                     int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
+                     int64_t ldy, void* stream);
 
 /* The linear layer on floating activations: awq_mxfp4_quantize of x (AWQ_FOLD_DIVIDE by s if
  * s is given) and awq_mxfp4_matmul, with the same result bit for bit.  Where tokens are few one launch
  * quantises them on the fly; otherwise codes and scales go to the workspace.
  *   x fp16 or bf16 [n_tokens][ldx >= in_features], y, bias in the same type; other arguments
- *   as above. */
+ *   as above
+ *   workspace  device, 256-byte aligned, awq_mxfp4_linear_workspace_bytes(...) bytes (0: may
+ *           be NULL); contents unspecified before and after */
 size_t awq_mxfp4_linear_workspace_bytes(int64_t n_tokens, int64_t out_features,
                                         int64_t in_features);
 int awq_mxfp4_linear(const void* x, int64_t ldx, const float* s, int64_t n_tokens, const uint8_t* wc,

@@ -4,9 +4,9 @@ Bars, derived from the kernels' arithmetic:
   - codes and scales follow from single fp32 operations and comparisons, so they are equal bit for bit;
     so are the values read back (a power of two times an element, one rounding);
   - the product adds 64 columns at a time to an fp32 sum, each step within 2^-22 of its largest term or
-    result, both at most S = sum |x w|: (K / 64 + 1) 2^-22 S; up to 8 parts of a divided K or
-    waves are joined, 8 * 2^-24 S more, and the bias adds 2^-24 (S + |bias|); the output's rounding is
-    half a step of the type;
+    result, both at most S = sum |x w|: (K / 64 + 1) 2^-22 S; the sums of up to 8 waves are joined,
+    8 * 2^-24 S more, and the bias adds 2^-24 (S + |bias|); the output's rounding is half a step of the
+    type;
   - where every term is a multiple of 1/4 and S 4 < 2^24 all sums are exact in fp32, whatever their
     order: equal bit for bit.
 """
@@ -17,6 +17,7 @@ import torch
 import weight_only_quantization_act_amd as awq
 from tests import mx_ref
 from tests.gpu_util import requires_gpu, say
+from tests.mx_forms import SHAPES
 
 pytestmark = [pytest.mark.gpu, requires_gpu]
 
@@ -197,20 +198,11 @@ def _check_product(y, xc, xs, wc, ws, K, bias, where):
     assert not bad.any(), (where, int(bad.sum()), np.argwhere(bad)[:3], got[bad][:3], want[bad][:3])
 
 
-SHAPES = [  # tokens, outputs, K: one of each, tile edges, odd counts, partial blocks, words and steps
-    (1, 1, 1), (1, 4096, 4096), (2, 257, 500), (3, 33, 64), (5, 1000, 1056), (15, 640, 100), (16, 512, 8192),
-    (9, 16401, 1300), (17, 129, 272), (31, 100, 2048), (32, 300, 16384), (33, 300, 5120), (63, 64, 512),
-    (64, 777, 1024), (65, 5120, 208), (100, 1000, 13824), (127, 128, 160), (128, 256, 256), (129, 255, 400),
-    (255, 300, 4096), (256, 512, 512), (257, 513, 1024), (333, 1111, 656), (700, 500, 9000), (1000, 1500, 272),
-    (2100, 700, 160), (4, 28672, 256), (3900, 4000, 96), (3850, 4090, 544), (4090, 4001, 1040),
-]
-
-
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "-".join(map(str, s)))
 def test_product(shape, dtype):
-    T, M, K = shape
-    say(f"mxfp4 product T={T} M={M} K={K} {dtype}")
+    form, T, M, K = shape
+    say(f"mxfp4 product, form {form}, T={T} M={M} K={K} {dtype}")
     g = torch.Generator(device="cuda").manual_seed(T * 31 + M + K)
     (xc, xs), (wc, ws) = _random_rows(T, K, g), _random_rows(M, K, g)
     xs, ws = xs - 4, ws - 4                                     # (fp16's range; 255 stays a power of two)
@@ -222,8 +214,8 @@ def test_product(shape, dtype):
 @pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "-".join(map(str, s)))
 def test_product_bit_for_bit(shape):
     """Scales of 1 and sums that are exact in fp32: every bit is the formula's."""
-    T, M, K = shape
-    say(f"mxfp4 product, exact, T={T} M={M} K={K}")
+    form, T, M, K = shape
+    say(f"mxfp4 product, exact, form {form}, T={T} M={M} K={K}")
     g = torch.Generator(device="cuda").manual_seed(T + M + K)
     xc, xs = _random_rows(T, K, g)
     wc, ws = _random_rows(M, K, g)

@@ -2,6 +2,8 @@
 get the documented status codes before anything touches the GPU (fake pointers, never dereferenced), and the plain
 forms of the tests agree with the format's definition."""
 import ctypes
+import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -9,6 +11,7 @@ import torch
 
 import weight_only_quantization_act_amd as awq
 from tests import mx_ref
+from tests.mx_forms import SHAPES
 from weight_only_quantization_act_amd import _serve
 
 OK, NULL, SHAPE, CONFIG, WORKSPACE, DEVICE, ALIGN = 0, 1, 2, 3, 5, 6, 9
@@ -72,8 +75,8 @@ def test_int8_dequantize_refusals(L):
 
 
 def _mm(L, xc=P, ldx=64, xs=P, ldxs=4, T=4, wc=P, ldw=64, ws=P, ldws=8, M=8, K=128, bias=None, dtype=0, y=P,
-        ldy=8, wsp=P, n=1 << 40):
-    return L.awq_mxfp4_matmul(xc, ldx, xs, ldxs, T, wc, ldw, ws, ldws, M, K, bias, dtype, y, ldy, wsp, n, None)
+        ldy=8):
+    return L.awq_mxfp4_matmul(xc, ldx, xs, ldxs, T, wc, ldw, ws, ldws, M, K, bias, dtype, y, ldy, None)
 
 
 def _lin(L, x=P, ldx=128, s=None, T=4, wc=P, ldw=64, ws=P, ldws=8, M=8, K=128, bias=None, dtype=0, y=P, ldy=8,
@@ -102,20 +105,13 @@ def test_product_refusals(L):
     assert _lin(L, ldx=127) == SHAPE and _lin(L, x=P1) == ALIGN and _lin(L, s=P2) == ALIGN
 
 
-def test_product_workspaces(L):
-    need = L.awq_mxfp4_matmul_workspace_bytes(64, 512, 16384)
-    assert need > 0                                    # K is divided
-    big = dict(T=64, M=512, K=16384, ldw=8192, ldws=512, ldy=512)
-    mm = dict(big, ldx=8192, ldxs=64)
-    assert _mm(L, **mm, wsp=None, n=0) == WORKSPACE and _mm(L, **mm, n=need - 1) == WORKSPACE
-    assert _mm(L, **mm, wsp=ctypes.c_void_p(0x10080), n=need) == ALIGN and _mm(L, **mm, n=need) == DEVICE
-    lin = dict(big, ldx=16384)
-    more = L.awq_mxfp4_linear_workspace_bytes(64, 512, 16384)
-    assert more >= need + 64 * 8192 + 64 * 512
-    assert _lin(L, **lin, wsp=None, n=0) == WORKSPACE and _lin(L, **lin, n=more - 1) == WORKSPACE
-    assert _lin(L, **lin, n=more) == DEVICE
+def test_linear_workspaces(L):
+    lin = dict(T=64, M=512, K=16384, ldw=8192, ldws=512, ldy=512, ldx=16384)
+    need = L.awq_mxfp4_linear_workspace_bytes(64, 512, 16384)
+    assert need >= 64 * 8192 + 64 * 512
+    assert _lin(L, **lin, wsp=None, n=0) == WORKSPACE and _lin(L, **lin, n=need - 1) == WORKSPACE
+    assert _lin(L, **lin, wsp=ctypes.c_void_p(0x10080), n=need) == ALIGN and _lin(L, **lin, n=need) == DEVICE
     for bad in ((-1, 8, 128), (0, 8, 128), (4, 0, 128), (4, 8, 0), (4, 8, (1 << 22) + 1), (ROWS + 1, 8, 128)):
-        assert L.awq_mxfp4_matmul_workspace_bytes(*bad) == 0
         assert L.awq_mxfp4_linear_workspace_bytes(*bad) == 0
 
 
@@ -182,3 +178,25 @@ def test_plain_rows_are_the_format():
     assert list(scales[0, 0]) == [127, 0, 255, 0]
     assert list(got[32:34]) == [2.0 ** -126, 2.0 ** -128] and np.isnan(got[64:]).all()
     assert codes.shape == (1, 48) and scales.shape == (1, 4, 4) and not codes[0, 32:].any()
+
+
+def test_forms_are_covered(tmp_path):
+    """The sizes that the GPU tests run land on the forms that they are meant for, so that a changed rule
+    cannot leave a form untested."""
+    src = tmp_path / "plan.cpp"
+    src.write_text("""#include <stdio.h>
+#include "mxfp4_plan.h"
+int main() {
+  long long T, M, K;
+  const char* name[] = {"few", "64k", "64", "64x128", "128", "256"};
+  while (scanf("%lld %lld %lld", &T, &M, &K) == 3)
+    printf("%s\\n", name[awq::mxfp4_form(T, M, (K + 31) / 32 * 16)]);
+}
+""")
+    exe = tmp_path / "plan"
+    csrc = os.path.join(os.path.dirname(awq.LIB_PATH), "csrc")
+    subprocess.run(["g++", "-std=c++17", "-I", csrc, str(src), "-o", str(exe)], check=True)
+    sizes = "\n".join("%d %d %d" % s[1:] for s in SHAPES)
+    out = subprocess.run([str(exe)], input=sizes, capture_output=True, text=True, check=True).stdout.split()
+    assert out == [s[0] for s in SHAPES], [(s, f) for s, f in zip(SHAPES, out) if s[0] != f]
+    assert set(out) == {"few", "64k", "64", "64x128", "128", "256"}

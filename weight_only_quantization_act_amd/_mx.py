@@ -178,11 +178,6 @@ def awq_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: int,
 
 # ---------------------------------------------------------------------------------- product
 @functools.lru_cache(maxsize=4096)
-def awq_mxfp4_matmul_workspace_bytes(n_tokens: int, out_features: int, in_features: int) -> int:
-    return int(lib().awq_mxfp4_matmul_workspace_bytes(n_tokens, out_features, in_features))
-
-
-@functools.lru_cache(maxsize=4096)
 def awq_mxfp4_linear_workspace_bytes(n_tokens: int, out_features: int, in_features: int) -> int:
     return int(lib().awq_mxfp4_linear_workspace_bytes(n_tokens, out_features, in_features))
 
@@ -190,7 +185,7 @@ def awq_mxfp4_linear_workspace_bytes(n_tokens: int, out_features: int, in_featur
 @_entry
 def awq_mxfp4_matmul(xc: torch.Tensor, xs: torch.Tensor, wc: torch.Tensor, ws: torch.Tensor,
                      dtype: torch.dtype = torch.float16, bias: Optional[torch.Tensor] = None,
-                     out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+                     out: Optional[torch.Tensor] = None):
     """y [T, M] = x w^T (+ bias) in `dtype` for MXFP4 codes and scales of tokens (xc, xs) and weights
     (wc, ws), as awq_mxfp4_quantize and awq_rmsnorm_mxfp4 make them."""
     dev = _device()
@@ -206,11 +201,10 @@ def awq_mxfp4_matmul(xc: torch.Tensor, xs: torch.Tensor, wc: torch.Tensor, ws: t
     if T == 0 or M == 0:
         return y
     py = y.data_ptr()
-    ws_, pws, nws = _workspace(workspace, awq_mxfp4_matmul_workspace_bytes(T, M, 2 * nb), xc.device)
     # an empty tensor has no address; the call does not read it, any device pointer serves
     st = lib().awq_mxfp4_matmul(xc.data_ptr() or py, ldx, xs.data_ptr() or py, ldxs, T,
                                 wc.data_ptr() or py, ldw, ws.data_ptr() or py, ldws, M, 2 * nb, pb, dt,
-                                py, ldy, pws, nws, _raw_stream(dev))
+                                py, ldy, _raw_stream(dev))
     if st:
         _check(st, "awq_mxfp4_matmul")
     return y

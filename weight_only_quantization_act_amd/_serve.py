@@ -55,9 +55,8 @@ _SIGNATURES = {
     "awq_mxfp4_quantize": (ctypes.c_int, [_vp, _i64, _i64, _i64, _i32, _vp, _i32, _vp, _i64, _vp, _i64,
                                           _vp]),
     "awq_mxfp4_dequantize": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i64, _i64, _i32, _vp, _i64, _vp]),
-    "awq_mxfp4_matmul_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "awq_mxfp4_matmul": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _i64,
-                                        _vp, _i32, _vp, _i64, _vp, _sz, _vp]),
+                                        _vp, _i32, _vp, _i64, _vp]),
     "awq_mxfp4_linear_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "awq_mxfp4_linear": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _vp,
                                         _i32, _vp, _i64, _vp, _sz, _vp]),

@@ -130,39 +130,31 @@ int awq_mxfp4_dequantize(const uint8_t* codes, int64_t ld_codes, const uint8_t* 
                                              (hipStream_t)stream));
 }
 
-size_t awq_mxfp4_matmul_workspace_bytes(int64_t T, int64_t M, int64_t K) {
-  if (!matmul_sizes(T, M, K)) return 0;
-  return round_up(awq::mxfp4_matmul_workspace(T, M, awq::mx_code_bytes(K)), kAlign);
-}
-
 int awq_mxfp4_matmul(const uint8_t* xc, int64_t ldx, const uint8_t* xs, int64_t ldxs, int64_t n_tokens,
                      const uint8_t* wc, int64_t ldw, const uint8_t* ws, int64_t ldws,
                      int64_t out_features, int64_t in_features, const void* bias, int32_t dtype, void* y,
-                     int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
+                     int64_t ldy, void* stream) {
   const int64_t T = n_tokens, M = out_features, K = in_features;
   if (!xc || !xs || !wc || !ws || !y) return AWQ_E_NULL;
   if (!dtype_valid(dtype)) return AWQ_E_CONFIG;
   int st = matmul_shape(T, M, K, ldw, ldws, ldy);
   if (st) return st;
   if (!codes_shape(T, K, ldx, ldxs)) return AWQ_E_SHAPE;
-  const size_t need = awq_mxfp4_matmul_workspace_bytes(T, M, K);
-  if (need && (!workspace || workspace_bytes < need)) return AWQ_E_WORKSPACE;
   if (!aligned(xc, 16) || !aligned(wc, 16) || !aligned(xs, 16) || !aligned(ws, 16) ||
-      !aligned(bias, 2) || !aligned(y, 2) || (need && !aligned(workspace, kAlign)))
+      !aligned(bias, 2) || !aligned(y, 2))
     return AWQ_E_ALIGN;
   if (T == 0 || M == 0) return AWQ_OK;
-  if ((st = device_ptrs({xc, xs, wc, ws, bias, y, need ? workspace : nullptr}))) return st;
+  if ((st = device_ptrs({xc, xs, wc, ws, bias, y}))) return st;
   clear_pending_error();
   const awq::MxArgs a{xc, ldx, (const uint32_t*)xs, ldxs, wc, ldw, (const uint32_t*)ws, ldws, bias, y, ldy,
                       (int)T, (int)M, (int)awq::mx_code_bytes(K), dtype == AWQ_BF16};
-  return hip_status(awq::launch_mxfp4_matmul(a, workspace, (hipStream_t)stream));
+  return hip_status(awq::launch_mxfp4_matmul(a, (hipStream_t)stream));
 }
 
 size_t awq_mxfp4_linear_workspace_bytes(int64_t T, int64_t M, int64_t K) {
   if (!matmul_sizes(T, M, K) || awq::mxfp4_linear_fused(T, M, K)) return 0;
   return round_up((size_t)T * (size_t)awq::mx_code_bytes(K), kAlign) +
-         round_up((size_t)awq::mx_words(K) * (size_t)((T + 3) / 4 * 4) * 4, kAlign) +
-         awq_mxfp4_matmul_workspace_bytes(T, M, K);
+         round_up((size_t)awq::mx_words(K) * (size_t)((T + 3) / 4 * 4) * 4, kAlign);
 }
 
 int awq_mxfp4_linear(const void* x, int64_t ldx, const float* s, int64_t n_tokens, const uint8_t* wc,
@@ -191,13 +183,12 @@ int awq_mxfp4_linear(const void* x, int64_t ldx, const float* s, int64_t n_token
     return hip_status(awq::launch_mxfp4_linear_fused(a, x, ldx, s, (int)K, (hipStream_t)stream));
   uint8_t* p = (uint8_t*)workspace;
   const size_t n_codes = round_up((size_t)T * (size_t)KB, kAlign);
-  const size_t n_scales = round_up((size_t)awq::mx_words(K) * (size_t)lds * 4, kAlign);
   a.x = p;
   a.xs = (const uint32_t*)(p + n_codes);
   hipError_t e = awq::launch_mxfp4_rows(x, T, (int)K, ldx, bf16, s, awq::kFoldDivide, p, KB,
                                         (uint32_t*)(p + n_codes), lds, (hipStream_t)stream);
   if (e != hipSuccess) return hip_status(e);
-  return hip_status(awq::launch_mxfp4_matmul(a, p + n_codes + n_scales, (hipStream_t)stream));
+  return hip_status(awq::launch_mxfp4_matmul(a, (hipStream_t)stream));
 }
 
 int awq_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr, int64_t rows,

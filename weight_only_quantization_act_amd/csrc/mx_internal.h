@@ -42,8 +42,7 @@ struct MxArgs {
   int T, M, KB;  // KB: bytes of codes a row that are read, a multiple of 16
   bool bf16;
 };
-size_t mxfp4_matmul_workspace(int64_t T, int64_t M, int64_t KB);
-hipError_t launch_mxfp4_matmul(const MxArgs& a, void* workspace, hipStream_t stream);
+hipError_t launch_mxfp4_matmul(const MxArgs& a, hipStream_t stream);
 // The linear layer of few tokens in one launch: a.x and a.xs unused, x 16-bit with `cols` columns
 // and row stride ldx.  Taken where mxfp4_linear_fused says so.
 bool mxfp4_linear_fused(int64_t T, int64_t M, int64_t cols);

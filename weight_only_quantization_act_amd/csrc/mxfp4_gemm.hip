@@ -6,16 +6,16 @@
 // they are.  An instruction adds 64 or 128 products of 4-bit elements (exact, multiples of 1/4 times a
 // power of two) and the running fp32 sum with one rounding.
 //
-// Tiles (many tokens): as for 8-bit integers, a block computes BT tokens x BM outputs from stages of 128 bytes of
-// K (256 columns) that move global -> LDS by DMA into a ring of NS (rows of 128 bytes, the 16-byte
-// chunk index XOR-swizzled with the row).  v_mfma_scale_f32_32x32x64_f8f6f4 takes, in lane l, one block of row l
-// mod 32 of both operands and its scale byte.  Which columns an instruction multiplies is free as
-// long as both operands agree: step k of a stage takes block 4 (l div 32) + k, so that a lane's
-// four scales of a stage are one 32-bit word of the scales' layout, byte k of it chosen by the
-// instruction.  The words of a tile's rows are contiguous ([column word][row]) and come
-// by DMA as well.  Element e of the result is row 8 (e div 4) + 4 (l div 32) + e mod 4 of the first operand
-// (token), column l mod 32 of the second (output).  Rows past the matrices and chunks past K arrive as
-// zeros, or as scales of rows that are dropped.
+// Tiles: a block computes BT tokens x BM outputs from stages of 128 bytes of K (256 columns) that
+// move global -> LDS by DMA into a ring of NS (rows of 128 bytes, the 16-byte chunk index XOR-swizzled
+// with the row).  v_mfma_scale_f32_32x32x64_f8f6f4 takes, in lane l, one block of row l mod 32 of both
+// operands and its scale byte.  Which columns an instruction multiplies is free as long as both
+// operands agree: step k of a stage takes block 4 (l div 32) + k, so that a lane's four scales of a
+// stage are one 32-bit word of the scales' layout, byte k of it chosen by the instruction.  The
+// words of a tile's rows are contiguous ([column word][row]) and come by DMA as well.  Element e of the
+// result is row 8 (e div 4) + 4 (l div 32) + e mod 4 of the first operand (output), column l mod 32 of
+// the second (token).  Rows past the matrices and chunks past K arrive as zeros, or as scales of rows
+// that are dropped.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -35,18 +35,22 @@ namespace {
 typedef int int32x8 __attribute__((ext_vector_type(8)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kFp4 = 4;  // the instruction's code for the format e2m1
+constexpr int64_t kCacheBytes = 256 << 20;  // the last-level cache
 
 __device__ __forceinline__ int32x8 operand(const int32x4& a) {  // 32 elements; the rest is not read
   return int32x8{a[0], a[1], a[2], a[3], 0, 0, 0, 0};
 }
 
-template <int BT_, int BM_, int WT_, int WM_, int NS_>
+template <int BT_, int BM_, int WT_, int WM_, int KG_, int NS_>
 struct MxTile {
-  static constexpr int BT = BT_, BM = BM_, WT = WT_, WM = WM_, NS = NS_;
-  static constexpr int BK = 128;  // bytes of K a stage
-  static constexpr int WAVES = WT * WM, THREADS = 64 * WAVES;
+  static constexpr int BT = BT_, BM = BM_, WT = WT_, WM = WM_;
+  static constexpr int KG = KG_, NS = NS_;  // groups of waves, which take the steps in turn, stages of each
+  static constexpr int BK = 128;            // bytes of K a stage
+  static constexpr int KS = 4;              // instructions along K a stage
+  static constexpr int WAVES = WT * WM, THREADS = 64 * WAVES * KG;
   static constexpr int TI = BT / WT / 32, MI = BM / WM / 32;
   static constexpr int X_BYTES = BT * BK, CODES = (BT + BM) * BK;
   static constexpr int XS_BYTES = 2 * 4 * BT, BYTES = CODES + 2 * 4 * (BT + BM);
@@ -55,20 +59,29 @@ struct MxTile {
   static constexpr int S_X = 2 * BT / 64, S_ALL = 2 * (BT + BM) / 64;
   static constexpr int DMA_S = (S_ALL + WAVES - 1) / WAVES;
   static constexpr int PER = DMA_X + DMA_W + DMA_S;
-  static_assert(DMA_X >= 1 && DMA_W >= 1 && S_X >= 1, "each wave loads a part of both operands");
+  static_assert(X_BYTES % (1024 * WAVES) == 0 && BM * BK % (1024 * WAVES) == 0 && S_X >= 1,
+                "each wave loads a part of both operands");
   static_assert(TI >= 1 && MI >= 1, "each wave has a 32 x 32 tile at least");
+  // Physical chunk of a row's chunk c: c ^ swz(row).  Eight consecutive rows' chunks c fall on eight
+  // different 16-byte groups of banks.
   __device__ static int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+  // After the last step LDS holds the sums of the groups but the first, then the tile's results in rows
+  // 16 bytes apart more than their length (bank conflicts), then the biases.
+  static constexpr int OUT = BM * 2 + 16;
+  static constexpr int RESULTS = (KG - 1) * BT * BM * 4;
+  static constexpr int BIAS = RESULTS + BT * OUT;
+  static constexpr int LDS = KG * NS * BYTES > BIAS + 4 * BM ? KG * NS * BYTES : BIAS + 4 * BM;
 };
 
-// splits > 1: block z sums its share of K and stores the fp32 tile to part [splits][T][M].
 template <class S, bool BF16>
-__global__ __launch_bounds__(S::THREADS) void k_mxfp4_tiles(MxArgs a, int tiles_t, int tiles_m,
-                                                            int splits, float* __restrict__ part) {
+__global__ __launch_bounds__(S::THREADS) void k_mxfp4_tiles(MxArgs a, int tiles_t, int tiles_m) {
   constexpr int NS = S::NS;
-  __shared__ __attribute__((aligned(1024))) uint8_t sm[NS * S::BYTES];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
   const int tid = threadIdx.x;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int all = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int group = all / S::WAVES, wave = all % S::WAVES;
   const int lane = tid & 63;
+  uint8_t* const sm = lds + group * NS * S::BYTES;
   const int wt = wave / S::WM, wm = wave % S::WM;
 
   // Blocks go to the 8 XCDs in turn; renumbered so that each XCD walks a contiguous range of
@@ -91,59 +104,66 @@ __global__ __launch_bounds__(S::THREADS) void k_mxfp4_tiles(MxArgs a, int tiles_
   const int32x4 rx = buffer_rsrc(a.x + (int64_t)t0 * a.ldx, (unsigned)(rows_x - 1) * ldx + a.KB);
   const int32x4 rw = buffer_rsrc(a.w + (int64_t)m0 * a.ldw, (unsigned)(rows_w - 1) * ldw + a.KB);
 
+  // steps of 128 bytes, which the groups take in turn, each the same number
+  const int steps = (a.KB + S::BK - 1) / S::BK;
+  const int n_steps = (steps + S::KG - 1) / S::KG;
+  const int words = (a.KB + 63) >> 6;  // scale words a row
+
   // A wave-DMA fills 8 rows of 128 bytes: lane l its row l / 8, physical chunk l % 8, which
   // holds logical chunk (l % 8) ^ swz(row).  swz depends on row mod 16, so on the parity of
-  // the 8-row block as well as on the lane.
+  // the 8-row block as well as on the lane.  Rows past the last lie out of range.
   constexpr unsigned kOut = 0x80000000u;
   const int dr = lane >> 3;
   const int ce = (lane & 7) ^ S::swz(dr), co = (lane & 7) ^ S::swz(dr + 8);
-  const unsigned row_x = wave * S::DMA_X * 8 + dr, row_w = wave * S::DMA_W * 8 + dr;
   const unsigned ldsb = lds_address(sm);
-  // 128-byte steps of this split: kt0 .. kt1 - 1, walked in whole turns of the ring
-  const int steps = (a.KB + S::BK - 1) / S::BK, z = blockIdx.z;
-  const int kt0 = (int)((int64_t)steps * z / splits);
-  const int n_steps = (int)((int64_t)steps * (z + 1) / splits) - kt0;
-  const int nk = (n_steps + NS - 1) / NS * NS;
-  const int words = (a.KB + 63) >> 6;  // scale words a row
+  unsigned vx[S::DMA_X], vw[S::DMA_W];
+#pragma unroll
+  for (int j = 0; j < S::DMA_X; ++j) {
+    const int p = wave * S::DMA_X + j, r = 8 * p + dr;
+    vx[j] = r < rows_x ? (unsigned)r * ldx + (p & 1 ? co : ce) * 16 : kOut;
+  }
+#pragma unroll
+  for (int j = 0; j < S::DMA_W; ++j) {
+    const int p = wave * S::DMA_W + j, r = 8 * p + dr;
+    vw[j] = r < rows_w ? (unsigned)r * ldw + (p & 1 ? co : ce) * 16 : kOut;
+  }
+  // Scales: the step's two words of the tile's rows, [2][BT], then [2][BM].  The address walks with
+  // the steps; a lane's offset in the rows of words stays.
+  const uint32_t* sp[S::DMA_S];
+  unsigned vs[S::DMA_S];
+  bool sq[S::DMA_S];  // the lane's word is the second one
+#pragma unroll
+  for (int j = 0; j < S::DMA_S; ++j) {
+    const int d = (wave * S::DMA_S + j) % S::S_ALL;
+    const bool is_x = d < S::S_X;
+    const int64_t ld = is_x ? a.ldxs : a.ldws;
+    const int i = (is_x ? d : d - S::S_X) * 64 + lane, n = is_x ? S::BT : S::BM;
+    const int q = i / n, r = i % n;
+    sp[j] = (is_x ? a.xs + t0 : a.ws + m0) + 2 * (int64_t)group * ld;
+    vs[j] = r < (is_x ? rows_x : rows_w) ? ((unsigned)q * (unsigned)ld + r) * 4u : kOut;
+    sq[j] = q == 1;
+  }
 
-  auto dma = [&](int st, int kt) {
-    const int k0 = (kt0 + kt) * S::BK;
-    const bool in = kt < n_steps;
-    const bool oke = in && k0 + ce * 16 < a.KB, oko = in && k0 + co * 16 < a.KB;
-#pragma unroll
-    for (int j = 0; j < S::DMA_X; ++j) {
-      const bool odd = (wave * S::DMA_X + j) & 1;
-      const unsigned r = row_x + 8 * j;
-      const unsigned v = (odd ? oko : oke) && r < (unsigned)rows_x
-                             ? r * ldx + (odd ? co : ce) * 16 : kOut;
-      lds_dma16(rx, ldsb + st * S::BYTES + (wave * S::DMA_X + j) * 1024u, v, k0);
-    }
-#pragma unroll
-    for (int j = 0; j < S::DMA_W; ++j) {
-      const bool odd = (wave * S::DMA_W + j) & 1;
-      const unsigned r = row_w + 8 * j;
-      const unsigned v = (odd ? oko : oke) && r < (unsigned)rows_w
-                             ? r * ldw + (odd ? co : ce) * 16 : kOut;
-      lds_dma16(rw, ldsb + st * S::BYTES + S::X_BYTES + (wave * S::DMA_W + j) * 1024u, v, k0);
-    }
-    // scale words 2 kt and 2 kt + 1 of the tile's rows: [2][BT], then [2][BM]
-    const int q0 = 2 * (kt0 + kt);
-    const int nq = in ? min(2, words - q0) : 0;
-#pragma unroll
-    for (int j = 0; j < S::DMA_S; ++j) {
-      const int d = (wave * S::DMA_S + j) % S::S_ALL;
-      const bool is_x = d < S::S_X;
-      const int64_t ld = is_x ? a.ldxs : a.ldws;
-      const uint32_t* base = (is_x ? a.xs + t0 : a.ws + m0) + (nq > 0 ? (int64_t)q0 * ld : 0);
-      const int rows = is_x ? rows_x : rows_w;
-      const int32x4 rs = buffer_rsrc(base, nq > 0 ? ((unsigned)(nq - 1) * (unsigned)ld + rows) * 4u : 0u);
-      const int i = (is_x ? d : d - S::S_X) * 64 + lane, n = is_x ? S::BT : S::BM;
-      const int q = i / n, r = i % n;
-      const unsigned v = q < nq && r < rows ? ((unsigned)q * (unsigned)ld + r) * 4u : kOut;
-      lds_dma4(rs, ldsb + st * S::BYTES + S::CODES + d * 256u, v);
+  // Piece j of a wave's part of its group's step kt (called with kt = 0, 1, 2, ...).
+  auto dma_piece = [&](int st, int kt, int j) {
+    const int at = kt * S::KG + group, k0 = at * S::BK;
+    const bool in = at < steps;
+    if (j < S::DMA_X + S::DMA_W) {
+      const bool is_x = j < S::DMA_X;
+      const int i = is_x ? j : j - S::DMA_X;
+      const int p = wave * (is_x ? S::DMA_X : S::DMA_W) + i;
+      const bool ok = in && k0 + (p & 1 ? co : ce) * 16 < a.KB;
+      lds_dma16(is_x ? rx : rw, ldsb + st * S::BYTES + (is_x ? 0 : S::X_BYTES) + p * 1024u,
+                ok ? (is_x ? vx[i] : vw[i]) : kOut, k0);
+    } else {
+      const int i = j - S::DMA_X - S::DMA_W;
+      const int d = (wave * S::DMA_S + i) % S::S_ALL;
+      const int nq = in ? words - 2 * at : 0;
+      lds_dma4(buffer_rsrc(sp[i], kOut), ldsb + st * S::BYTES + S::CODES + d * 256u,
+               nq > (sq[i] ? 1 : 0) ? vs[i] : kOut);
+      sp[i] += 2 * S::KG * (d < S::S_X ? a.ldxs : a.ldws);
     }
   };
-
   const int fr = lane & 31, fh = lane >> 5, fs = S::swz(fr);
   const int x_off = (wt * S::TI * 32 + fr) * S::BK;
   const int w_off = S::X_BYTES + (wm * S::MI * 32 + fr) * S::BK;
@@ -175,113 +195,192 @@ __global__ __launch_bounds__(S::THREADS) void k_mxfp4_tiles(MxArgs a, int tiles_
     for (int j = 0; j < S::MI; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-  auto mma = [&](auto ks, const Frag& f, const Scales& s) {
+  // outputs are the rows of the result, tokens its columns
+  auto mma1 = [&](auto ks, int i, int j, const Frag& f, const Scales& s) {
     constexpr int B = decltype(ks)::value;
+    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+        operand(f.w[j]), operand(f.x[i]), acc[i][j], kFp4, kFp4, B, s.w[j], B, s.x[i]);
+  };
+  auto mma = [&](auto ks, const Frag& f, const Scales& s) {
 #pragma unroll
     for (int i = 0; i < S::TI; ++i)
 #pragma unroll
-      for (int j = 0; j < S::MI; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-            operand(f.x[i]), operand(f.w[j]), acc[i][j], kFp4, kFp4, B, s.x[i], B, s.w[j]);
+      for (int j = 0; j < S::MI; ++j) mma1(ks, i, j, f, s);
   };
   using std::integral_constant;
 
   // NS stages in flight; a stage is refilled after the barrier that follows its last fragment
   // read, and the DMAs past the end of K read zeros into a slot nobody uses, so the number in
   // flight, hence the vmcnt to wait for, is constant.
-  Frag f0, f1;
-  Scales sc, sn;
-  auto step = [&](int st, int kt) {
-    const uint8_t* cur = sm + st * S::BYTES;
-    const uint8_t* next = sm + (st + 1) % NS * S::BYTES;
-    load(cur, 1, f1);
-    mma(integral_constant<int, 0>{}, f0, sc);
-    load(cur, 2, f0);
-    mma(integral_constant<int, 1>{}, f1, sc);
-    load(cur, 3, f1);
-    mma(integral_constant<int, 2>{}, f0, sc);
-    __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<(NS - 2) * S::PER>::value);  // stage kt + 1 has landed
-    __builtin_amdgcn_s_barrier();
-    dma(st, kt + NS);
-    load_scales(next, sn);
-    load(next, 0, f0);
-    mma(integral_constant<int, 3>{}, f1, sc);
-    sc = sn;
-  };
-  if (nk > 0) {
+  auto begin = [&] {
 #pragma unroll
-    for (int st = 0; st < NS; ++st) dma(st, st);
+    for (int st = 0; st < NS; ++st)
+#pragma unroll
+      for (int j = 0; j < S::PER; ++j) dma_piece(st, st, j);
     __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<(NS - 1) * S::PER>::value);
     __builtin_amdgcn_s_barrier();
+  };
+  auto landed = [&] {  // the step after this one's
+    __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<(NS - 2) * S::PER>::value);
+    __builtin_amdgcn_s_barrier();
+  };
+  if (n_steps == 0) {
+  } else if constexpr (S::TI * S::MI == 1) {
+    // One tile a wave: a step has too few products to hide its own reads, so a whole stage's operands
+    // are read during the products of the one before (50 tokens of 11008 x 4096 7.8 -> 7.2 us).
+    Frag f[2][4];
+    Scales s[2];
+    auto read = [&](int st, Frag (&to)[4], Scales& ts) {
+      load_scales(sm + st * S::BYTES, ts);
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) load(sm + st * S::BYTES, ks, to[ks]);
+    };
+    begin();
+    read(0, f[0], s[0]);
+    constexpr int U = NS % 2 ? 2 * NS : NS;
+    for (int kt = 0; kt < n_steps; kt += U) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (kt + u >= n_steps) break;
+        landed();
+        read((u + 1) % NS, f[~u & 1], s[~u & 1]);
+#pragma unroll
+        for (int j = 0; j < S::PER; ++j) dma_piece(u % NS, kt + u + NS, j);
+        mma(integral_constant<int, 0>{}, f[u & 1][0], s[u & 1]);
+        mma(integral_constant<int, 1>{}, f[u & 1][1], s[u & 1]);
+        mma(integral_constant<int, 2>{}, f[u & 1][2], s[u & 1]);
+        mma(integral_constant<int, 3>{}, f[u & 1][3], s[u & 1]);
+      }
+    }
+  } else {
+    Frag f0, f1;
+    Scales sc, sn;
+    begin();
     load_scales(sm, sc);
     load(sm, 0, f0);
-    for (int kt = 0; kt < nk; kt += NS) {
+    for (int kt = 0; kt < n_steps; kt += NS) {
 #pragma unroll
-      for (int st = 0; st < NS; ++st) step(st, kt + st);
-    }
-    __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<0>::value);  // no LDS write may outlive the block
-  }
-
-  if (splits > 1) {
-    float* dst = part + (int64_t)z * a.T * a.M;
+      for (int st = 0; st < NS; ++st) {
+        if (kt + st >= n_steps) break;
+        const uint8_t* cur = sm + st * S::BYTES;
+        const uint8_t* next = sm + (st + 1) % NS * S::BYTES;
+        load(cur, 1, f1);
+        mma(integral_constant<int, 0>{}, f0, sc);
+        load(cur, 2, f0);
+        mma(integral_constant<int, 1>{}, f1, sc);
+        load(cur, 3, f1);
+        mma(integral_constant<int, 2>{}, f0, sc);
+        landed();
+        load_scales(next, sn);
+        load(next, 0, f0);
+        // the refill's instructions between the products, which keep the matrix cores busy meanwhile
+        constexpr int N = S::TI * S::MI;
 #pragma unroll
-    for (int j = 0; j < S::MI; ++j)
+        for (int n = 0; n < N; ++n) {
+          mma1(integral_constant<int, 3>{}, n / S::MI, n % S::MI, f1, sc);
+          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < S::TI; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int m = m0 + (wm * S::MI + j) * 32 + (lane & 31);
-          const int t = t0 + (wt * S::TI + i) * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-          if (t < a.T && m < a.M) dst[(int64_t)t * a.M + m] = acc[i][j][e];
+          for (int p = n * S::PER / N; p < (n + 1) * S::PER / N; ++p) dma_piece(st, kt + st + NS, p);
+          __builtin_amdgcn_sched_barrier(0);
         }
-    return;
-  }
-  const uint16_t* bias = (const uint16_t*)a.bias;
-  uint16_t* y = (uint16_t*)a.y;
-#pragma unroll
-  for (int j = 0; j < S::MI; ++j) {
-    const int m = m0 + (wm * S::MI + j) * 32 + (lane & 31);
-    const bool mok = m < a.M;
-    const float bs = mok && bias ? from16<BF16>(bias[m]) : 0.0f;
-#pragma unroll
-    for (int i = 0; i < S::TI; ++i) {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int t = t0 + (wt * S::TI + i) * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-        if (t < a.T && mok) {
-          float v = acc[i][j][e];
-          if (bias) v = v + bs;
-          y[(int64_t)t * a.ldy + m] = to16<BF16>(v);
-        }
+        sc = sn;
       }
     }
   }
-}
+  __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<0>::value);  // no LDS write may come after this
+  __syncthreads();
 
-// The sum of the splits' tiles in their order.  Four outputs a thread where M allows it.
-template <bool BF16, int V>
-__global__ __launch_bounds__(256) void k_mxfp4_finish(MxArgs a, int splits,
-                                                      const float* __restrict__ part) {
-  typedef float fvec __attribute__((ext_vector_type(V)));
-  const int64_t n = (int64_t)a.T * a.M;
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;
-  if (i >= n) return;
-  const int t = (int)(i / a.M), m = (int)(i - (int64_t)t * a.M);
-  fvec s = *(const fvec*)(part + i);
-  for (int z = 1; z < splits; ++z) s += *(const fvec*)(part + z * n + i);
-  const uint16_t* bias = (const uint16_t*)a.bias;
-  uint16_t* y = (uint16_t*)a.y + (int64_t)t * a.ldy + m;
+  if constexpr (S::KG > 1) {  // the groups' sums, added in their order
+    floatx4* const sums = (floatx4*)lds;
+    auto slot = [&](int g, int i, int j, int e) {
+      return (((g - 1) * S::WAVES + wave) * S::TI * S::MI * 4 + (i * S::MI + j) * 4 + e) * 64 + lane;
+    };
+    if (group > 0) {
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    float v = s[e];
-    if (bias) v = v + from16<BF16>(bias[m + e]);
-    y[e] = to16<BF16>(v);
+      for (int i = 0; i < S::TI; ++i)
+#pragma unroll
+        for (int j = 0; j < S::MI; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            sums[slot(group, i, j, e)] = floatx4{acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]};
+    }
+    __syncthreads();
+    if (group == 0) {
+#pragma unroll
+      for (int g = 1; g < S::KG; ++g)
+#pragma unroll
+        for (int i = 0; i < S::TI; ++i)
+#pragma unroll
+          for (int j = 0; j < S::MI; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const floatx4 v = sums[slot(g, i, j, e)];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) acc[i][j][4 * e + k] += v[k];
+            }
+    }
   }
+
+  // Results through LDS, so that stores fill whole lines: a lane has four consecutive outputs of a
+  // token at a time; the rows of the tile are then read 16 bytes a lane (8192 tokens of 28672 x 8192
+  // 945 -> 889 us).
+  uint8_t* const results = lds + S::RESULTS;
+  const uint16_t* bias = (const uint16_t*)a.bias;
+  float* const lbias = (float*)(lds + S::BIAS);
+  if (bias) {
+    for (int m = tid; m < S::BM; m += S::THREADS) lbias[m] = m < rows_w ? from16<BF16>(bias[m0 + m]) : 0.0f;
+    __syncthreads();
+  }
+  if (group == 0) {
+#pragma unroll
+    for (int i = 0; i < S::TI; ++i)
+#pragma unroll
+      for (int j = 0; j < S::MI; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int t = (wt * S::TI + i) * 32 + fr;
+          const int m = (wm * S::MI + j) * 32 + 8 * g + 4 * fh;
+          floatx4 o = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+          if (bias) {
+            const floatx4 bb = *(const floatx4*)(lbias + m);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] = o[k] + bb[k];
+          }
+          uint2 p;
+          p.x = to16<BF16>(o[0]) | ((uint32_t)to16<BF16>(o[1]) << 16);
+          p.y = to16<BF16>(o[2]) | ((uint32_t)to16<BF16>(o[3]) << 16);
+          *(uint2*)(results + t * S::OUT + 2 * m) = p;
+        }
+  }
+  __syncthreads();
+  uint16_t* y = (uint16_t*)a.y + (int64_t)t0 * a.ldy + m0;
+  const bool vec = a.ldy % 8 == 0 && ((uintptr_t)a.y & 15) == 0;
+  auto store = [&](auto stream) {
+    constexpr int kPer = S::BM / 8;
+    for (int c = tid; c < S::BT * kPer; c += S::THREADS) {
+      const int t = c / kPer, m = 8 * (c % kPer);
+      if (t >= rows_x || m >= rows_w) continue;
+      const u32x4 v = *(const u32x4*)(results + t * S::OUT + 2 * m);
+      uint16_t* o = y + (int64_t)t * a.ldy + m;
+      if (vec && m + 8 <= rows_w) {
+        if constexpr (decltype(stream)::value) __builtin_nontemporal_store(v, (u32x4*)o);
+        else *(u32x4*)o = v;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (m + e < rows_w) o[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+      }
+    }
+  };
+  // Results that no cache will hold are kept from pushing the panels out of it: output of 470 MB 882
+  // -> 843 us, of 90 MB 97 -> 99 us.
+  if ((int64_t)a.T * a.M * 2 > kCacheBytes) store(std::true_type{});
+  else store(std::false_type{});
 }
 
 // ---- few tokens --------------------------------------------------------------------------
 //
-// Up to 16 tokens the product is bound by reading the weights once.  A block takes 16 RT outputs
+// Up to 16 tokens the product is bound by reading the weights once.  A block takes 16 outputs
 // and all tokens; its eight waves take 256-byte pieces of K (512 columns) in turn.  The weights go
 // from memory to the operand registers of v_mfma_scale_f32_16x16x128_f8f6f4 directly: lane l has
 // row l mod 16 and the 64 bytes from 64 (l div 16) of a piece, whose four blocks' scales are one word;
@@ -302,57 +401,46 @@ struct MxFewArgs {
   bool vec;
 };
 
-template <int RT, bool FUSED, bool BF16>
+template <bool FUSED, bool BF16>
 __global__ __launch_bounds__(64 * kFewWaves) void k_mxfp4_few(MxFewArgs f) {
   const MxArgs& a = f.g;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // FUSED: codes [T][pieces 256], words [T][4 pieces]
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, q = lane >> 4;
-  const unsigned first = block_number() * 16u * RT;  // below 2^32 past M, too
-  if (first >= (unsigned)a.M) return;                // the whole block
+  const unsigned first = block_number() * 16u;  // below 2^32 past M, too
+  if (first >= (unsigned)a.M) return;           // the whole block
   const int m0 = (int)first;
   const int nch = (a.KB + 255) >> 8;
   const int words = (a.KB + 63) >> 6;
 
   // rows past the last repeat it and are dropped; blocks past K read the row's start and count 0
   struct Piece {
-    int32x4 w[RT][4];
-    int s[RT];
+    int32x4 v[4];
+    int s;
   };
-  const uint8_t* wrow[RT];
-  const uint32_t* srow[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const int row = min(m0 + 16 * r + lr, a.M - 1);
-    wrow[r] = a.w + (int64_t)row * a.ldw;
-    srow[r] = a.ws + row;
-  }
+  const int row = min(m0 + lr, a.M - 1);
+  const uint8_t* const wrow = a.w + (int64_t)row * a.ldw;
+  const uint32_t* const srow = a.ws + row;
   auto load_w = [&](Piece& o, int ch) {
-    const int k = ch * 256 + 64 * q;
-    const int word = 4 * ch + q;
+    const int k = ch * 256 + 64 * q, word = 4 * ch + q;
+    o.s = (int)srow[(int64_t)(word < words ? word : 0) * a.ldws];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) o.s[r] = (int)srow[r][(int64_t)(word < words ? word : 0) * a.ldws];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const bool in = k + 16 * u < a.KB;
-#pragma unroll
-      for (int r = 0; r < RT; ++r) o.w[r][u] = *(const int32x4*)(wrow[r] + (in ? k + 16 * u : 0));
-    }
+    for (int u = 0; u < 4; ++u) o.v[u] = *(const int32x4*)(wrow + (k + 16 * u < a.KB ? k + 16 * u : 0));
   };
   Piece p0, p1;
   if (wave < nch) load_w(p0, wave);
 
-  uint32_t* lwords = (uint32_t*)(lds + (size_t)a.T * nch * 256);
+  uint32_t* const lwords = (uint32_t*)(lds + (size_t)a.T * nch * 256);
   if constexpr (FUSED) {
     const int n8 = nch * 64;  // 8-column chunks of whole pieces
     for (int i = tid; i < a.T * n8; i += 64 * kFewWaves) {
       const int t = i / n8, ch = i - t * n8;  // sixteen lanes have one token and one word
       float v[8];
-      const uint16_t* row = f.x16 + t * f.ldx16;
+      const uint16_t* x = f.x16 + t * f.ldx16;
       const int fold = f.s ? kFoldDivide : kFoldNone;
-      if (f.vec) load_row8<BF16, true>(row, f.s, fold, 8 * ch, f.cols, v);
-      else load_row8<BF16, false>(row, f.s, fold, 8 * ch, f.cols, v);
+      if (f.vec) load_row8<BF16, true>(x, f.s, fold, 8 * ch, f.cols, v);
+      else load_row8<BF16, false>(x, f.s, fold, 8 * ch, f.cols, v);
       uint32_t byte;
       const uint32_t c = mx_codes8(v, byte);
       *(uint32_t*)(lds + (size_t)t * nch * 256 + 4 * ch) = c;
@@ -364,47 +452,35 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mxfp4_few(MxFewArgs f) {
 
   // columns past the last token repeat it and are dropped
   const int tok = min(lr, a.T - 1);
-  floatx4 acc[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) acc[r] = floatx4{0.f, 0.f, 0.f, 0.f};
-  struct XPiece {
-    int32x4 x[4];
-    int s;
-  };
-  auto load_x = [&](XPiece& o, int ch) {
-    const int k = ch * 256 + 64 * q;
-    const int word = 4 * ch + q;
+  floatx4 acc = {0.f, 0.f, 0.f, 0.f};
+  auto load_x = [&](Piece& o, int ch) {
+    const int k = ch * 256 + 64 * q, word = 4 * ch + q;
     if constexpr (FUSED) {
       o.s = (int)lwords[tok * nch * 4 + word];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) o.x[u] = *(const int32x4*)(lds + (size_t)tok * nch * 256 + k + 16 * u);
+      for (int u = 0; u < 4; ++u) o.v[u] = *(const int32x4*)(lds + (size_t)tok * nch * 256 + k + 16 * u);
     } else {
       o.s = (int)a.xs[(int64_t)(word < words ? word : 0) * a.ldxs + tok];
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        o.x[u] = *(const int32x4*)(a.x + (int64_t)tok * a.ldx + (k + 16 * u < a.KB ? k + 16 * u : 0));
+        o.v[u] = *(const int32x4*)(a.x + (int64_t)tok * a.ldx + (k + 16 * u < a.KB ? k + 16 * u : 0));
     }
   };
-  auto piece = [&](Piece& w, XPiece& x, int ch) {
+  auto piece = [&](Piece& w, Piece& x, int ch) {
     if (ch == nch - 1) {  // blocks past K count nothing (their scales may be any row's)
       const int k = ch * 256 + 64 * q;
 #pragma unroll
       for (int u = 0; u < 4; ++u)
         if (k + 16 * u >= a.KB) {
-#pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            w.w[r][u] = int32x4{0, 0, 0, 0};
-            w.s[r] = w.s[r] & ~(255 << (8 * u));
-          }
+          w.v[u] = int32x4{0, 0, 0, 0};
+          w.s = w.s & ~(255 << (8 * u));
           x.s = x.s & ~(255 << (8 * u));
         }
     }
     auto step = [&](auto uu) {
       constexpr int u = decltype(uu)::value;
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-        acc[r] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-            operand(w.w[r][u]), operand(x.x[u]), acc[r], kFp4, kFp4, u, w.s[r], u, x.s);
+      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w.v[u]), operand(x.v[u]), acc, kFp4,
+                                                             kFp4, u, w.s, u, x.s);
     };
     step(std::integral_constant<int, 0>{});
     step(std::integral_constant<int, 1>{});
@@ -414,7 +490,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mxfp4_few(MxFewArgs f) {
   // a piece's tokens are asked for before the next piece's weights: loads return in order, so
   // waiting for the tokens does not wait for those weights
   for (int ch = wave; ch < nch; ch += 2 * kFewWaves) {
-    XPiece x;
+    Piece x;
     load_x(x, ch);
     if (ch + kFewWaves < nch) load_w(p1, ch + kFewWaves);
     __builtin_amdgcn_sched_barrier(0);
@@ -426,113 +502,95 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mxfp4_few(MxFewArgs f) {
     piece(p1, x, ch + kFewWaves);
   }
 
-  // the waves' sums, then one (tile, lane) a thread
-  __shared__ floatx4 sum[kFewWaves][RT][64];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) sum[wave][r][lane] = acc[r];
+  // the waves' sums, then one lane's four outputs a thread
+  __shared__ floatx4 sum[kFewWaves][64];
+  sum[wave][lane] = acc;
   __syncthreads();
+  if (wave > 0) return;
+  floatx4 v = acc;
+#pragma unroll
+  for (int w = 1; w < kFewWaves; ++w) {
+    const floatx4 o = sum[w][lane];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += o[e];
+  }
+  const int t = lr, m = m0 + 4 * q;
+  if (t >= a.T) return;
   const uint16_t* bias = (const uint16_t*)a.bias;
-  for (int i = tid; i < RT * 64; i += 64 * kFewWaves) {
-    const int tile = i >> 6, l = i & 63;
-    floatx4 v = sum[0][tile][l];
+  uint16_t o[4];
 #pragma unroll
-    for (int w = 1; w < kFewWaves; ++w) {
-      const floatx4 o = sum[w][tile][l];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] += o[e];
+  for (int e = 0; e < 4; ++e) {
+    if (m + e < a.M) {
+      float y = v[e];
+      if (bias) y = y + from16<BF16>(bias[m + e]);
+      o[e] = to16<BF16>(y);
     }
-    const int t = l & 15, m = m0 + 16 * tile + 4 * (l >> 4);
-    if (t >= a.T) continue;
-    uint16_t o[4];
+  }
+  uint16_t* y = (uint16_t*)a.y + (int64_t)t * a.ldy + m;
+  if (m + 4 <= a.M && a.ldy % 4 == 0 && ((uintptr_t)a.y & 7) == 0) {
+    uint2 p;
+    p.x = o[0] | ((uint32_t)o[1] << 16);
+    p.y = o[2] | ((uint32_t)o[3] << 16);
+    *(uint2*)y = p;
+  } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (m + e < a.M) {
-        float y = v[e];
-        if (bias) y = y + from16<BF16>(bias[m + e]);
-        o[e] = to16<BF16>(y);
-      }
-    }
-    uint16_t* y = (uint16_t*)a.y + (int64_t)t * a.ldy + m;
-    if (m + 4 <= a.M && a.ldy % 4 == 0 && ((uintptr_t)a.y & 7) == 0) {
-      uint2 p;
-      p.x = o[0] | ((uint32_t)o[1] << 16);
-      p.y = o[2] | ((uint32_t)o[3] << 16);
-      *(uint2*)y = p;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (m + e < a.M) y[e] = o[e];
-    }
+    for (int e = 0; e < 4; ++e)
+      if (m + e < a.M) y[e] = o[e];
   }
 }
 
 template <class S, bool BF16>
-hipError_t launch_tiles(const MxArgs& a, int splits, float* part, hipStream_t stream) {
+hipError_t launch_tiles(const MxArgs& a, hipStream_t stream) {
   const int tt = (a.T + S::BT - 1) / S::BT, tm = (a.M + S::BM - 1) / S::BM;
   const int64_t tiles = (int64_t)tt * tm;
   if (tiles > kMaxBlocks) return hipErrorInvalidValue;
-  dim3 grid = grid_of(tiles);
-  grid.z = (unsigned)splits;
-  hipLaunchKernelGGL((k_mxfp4_tiles<S, BF16>), grid, dim3(S::THREADS), 0, stream, a, tt, tm, splits,
-                     part);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || splits <= 1) return e;
-  const int64_t n = (int64_t)a.T * a.M;
-  if (a.M % 4 == 0)
-    hipLaunchKernelGGL((k_mxfp4_finish<BF16, 4>), dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0,
-                       stream, a, splits, part);
-  else
-    hipLaunchKernelGGL((k_mxfp4_finish<BF16, 1>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0,
-                       stream, a, splits, part);
+  hipLaunchKernelGGL((k_mxfp4_tiles<S, BF16>), grid_of(tiles), dim3(S::THREADS), 0, stream, a, tt, tm);
   return hipGetLastError();
 }
 
-template <int RT, bool FUSED>
+template <bool FUSED>
 hipError_t launch_few(const MxFewArgs& f, hipStream_t stream) {
-  const dim3 grid = grid_of((f.g.M + 16 * RT - 1) / (16 * RT)), block(64 * kFewWaves);
+  const dim3 grid = grid_of((f.g.M + 15) / 16), block(64 * kFewWaves);
   const size_t lds = FUSED ? (size_t)f.g.T * ((f.g.KB + 255) / 256) * (256 + 16) : 0;
   if (f.g.bf16)
-    hipLaunchKernelGGL((k_mxfp4_few<RT, FUSED, true>), grid, block, lds, stream, f);
+    hipLaunchKernelGGL((k_mxfp4_few<FUSED, true>), grid, block, lds, stream, f);
   else
-    hipLaunchKernelGGL((k_mxfp4_few<RT, FUSED, false>), grid, block, lds, stream, f);
+    hipLaunchKernelGGL((k_mxfp4_few<FUSED, false>), grid, block, lds, stream, f);
   return hipGetLastError();
 }
 
 template <bool BF16>
-hipError_t launch_plan(const MxArgs& a, const MxPlan& p, float* part, hipStream_t stream) {
-  switch (p.form) {
-    case kMxTile32: return launch_tiles<MxTile<32, 128, 1, 4, 3>, BF16>(a, p.splits, part, stream);
-    case kMxTile64: return launch_tiles<MxTile<64, 128, 2, 2, 3>, BF16>(a, p.splits, part, stream);
-    case kMxTile128: return launch_tiles<MxTile<128, 128, 2, 2, 2>, BF16>(a, p.splits, part, stream);
-    default: return launch_tiles<MxTile<256, 256, 2, 4, 2>, BF16>(a, 1, nullptr, stream);
+hipError_t launch_form(const MxArgs& a, int form, hipStream_t stream) {
+  switch (form) {
+    case kMxTile64K: return launch_tiles<MxTile<64, 64, 2, 2, 2, 3>, BF16>(a, stream);
+    case kMxTile64: return launch_tiles<MxTile<64, 64, 2, 2, 1, 3>, BF16>(a, stream);
+    case kMxTile64x128: return launch_tiles<MxTile<64, 128, 2, 4, 1, 3>, BF16>(a, stream);
+    case kMxTile128: return launch_tiles<MxTile<128, 128, 4, 2, 1, 2>, BF16>(a, stream);
+    default: return launch_tiles<MxTile<256, 256, 4, 2, 1, 2>, BF16>(a, stream);
   }
 }
 
 }  // namespace
 
-size_t mxfp4_matmul_workspace(int64_t T, int64_t M, int64_t KB) {
-  const MxPlan p = mxfp4_plan(T, M, KB);
-  return p.splits > 1 ? (size_t)p.splits * T * M * sizeof(float) : 0;
-}
-
-hipError_t launch_mxfp4_matmul(const MxArgs& a, void* workspace, hipStream_t stream) {
+hipError_t launch_mxfp4_matmul(const MxArgs& a, hipStream_t stream) {
   if (a.T <= 0 || a.M <= 0) return hipSuccess;
-  const MxPlan p = mxfp4_plan(a.T, a.M, a.KB);
-  if (p.form == kMxFew) {
+  const int form = mxfp4_form(a.T, a.M, a.KB);
+  if (form == kMxFew) {
     const MxFewArgs f{a, nullptr, nullptr, 0, 0, false};
-    return mxfp4_few_rows(a.M) == 2 ? launch_few<2, false>(f, stream) : launch_few<1, false>(f, stream);
+    return launch_few<false>(f, stream);
   }
-  return a.bf16 ? launch_plan<true>(a, p, (float*)workspace, stream)
-                : launch_plan<false>(a, p, (float*)workspace, stream);
+  return a.bf16 ? launch_form<true>(a, form, stream) : launch_form<false>(a, form, stream);
 }
 
-bool mxfp4_linear_fused(int64_t T, int64_t M, int64_t cols) { return T == 1 && cols <= 65536; }
+bool mxfp4_linear_fused(int64_t T, int64_t M, int64_t cols) {
+  return T == 1 && cols <= 65536 && mxfp4_form(T, M, (cols + 31) / 32 * 16) == kMxFew;
+}
 
 hipError_t launch_mxfp4_linear_fused(const MxArgs& a, const void* x, int64_t ldx, const float* s,
                                      int cols, hipStream_t stream) {
   if (a.T <= 0 || a.M <= 0) return hipSuccess;
   const MxFewArgs f{a, (const uint16_t*)x, s, ldx, cols, row_vector_loads(x, a.T > 1 ? ldx : 0, s)};
-  return mxfp4_few_rows(a.M) == 2 ? launch_few<2, true>(f, stream) : launch_few<1, true>(f, stream);
+  return launch_few<true>(f, stream);
 }
 
 }  // namespace awq
