@@ -59,7 +59,8 @@ def _check(x, w, eps, r, outs=("same", "int8", "mxfp4"), where=""):
 
 SHAPES = [  # rows, columns: one value, partial blocks, each count of registers a thread and beyond
     (1, 1), (3, 7), (2, 33), (5, 127), (1, 128), (4, 1000), (1, 4096), (33, 5120), (2, 4097), (3, 8192), (2, 8200),
-    (1, 16384), (2, 16391), (1, 70001), (300, 512), (1000, 64), (17, 2047),
+    (1, 16384), (2, 16391), (1, 70001), (300, 512), (1000, 64), (17, 2047), (1027, 511), (1025, 129), (1026, 1000),
+    (1030, 2001), (1031, 4090), (1025, 5003), (1029, 8191), (1025, 8200),
 ]
 
 

@@ -12,32 +12,48 @@ from typing import Optional
 import torch
 
 from ._lib import _check
-from ._serve import (AWQ_FOLD_DIVIDE, AWQ_FOLD_MULTIPLY, AWQ_FP32, _FP32, _I8, _U8, _dtype, _round16,
-                     _workspace, lib)
+from ._serve import (AWQ_FOLD_DIVIDE, AWQ_FOLD_MULTIPLY, AWQ_FP32, _FP32, _I8, _U8, _dtype,
+                     _round16, _workspace, lib)
 
-_empty = torch.empty
+# Short calls are at the host's pace, so the usual case (contiguous tensors of the current device) is
+# told by a few cheap tests in place, and only what they do not cover goes through the full checks.
+_empty = torch.empty_strided
 _device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_C = None
 
 
-def _entry(fn):
-    """Run the wrapper with `stream` (when given) as torch's current stream and with the device of its
+def _lib():
+    global _C
+    _C = lib()
+    return _C
+
+
+def _elsewhere(fn, stream, first, *args, **kwargs):
+    """Run an entry point with `stream` (when given) as torch's current stream, or with the device of its
     first argument as the current one, so that what it allocates belongs to the stream that the kernels
     are enqueued on."""
-    @functools.wraps(fn)
-    def wrapper(first, *args, stream=None, **kwargs):
-        if stream is not None:
-            with torch.cuda.stream(stream):
-                return fn(first, *args, **kwargs)
-        if isinstance(first, torch.Tensor) and first.is_cuda and first.get_device() != _device():
-            with torch.cuda.device(first.device):
-                return fn(first, *args, **kwargs)
+    if not isinstance(first, torch.Tensor):
+        raise TypeError("the first argument must be a torch.Tensor")
+    if not first.is_cuda:
+        raise ValueError("tensors must be device (HIP) tensors")
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fn(first, *args, **kwargs)
+    with torch.cuda.device(first.device):
         return fn(first, *args, **kwargs)
-    return wrapper
+
+
+def _away(t, dev: int) -> bool:
+    """Whether t is anything but a tensor on device dev."""
+    return getattr(t, "get_device", int)() != dev or not t.is_cuda
 
 
 def _matrix(t: torch.Tensor, name: str, dtype: Optional[torch.dtype], dev: int) -> int:
     """Check a 2-D tensor on the call's device with unit stride along its rows; returns the row stride."""
+    if (isinstance(t, torch.Tensor) and t.get_device() == dev and t.is_contiguous() and t.dim() == 2
+            and (dtype is None or t.dtype is dtype)):
+        return t.shape[1]
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -60,6 +76,9 @@ def _matrix(t: torch.Tensor, name: str, dtype: Optional[torch.dtype], dev: int) 
 
 def _vector(t: torch.Tensor, dtype: torch.dtype, name: str, n: int, dev: int) -> int:
     """Check a contiguous vector of n elements on the call's device; returns its address."""
+    if (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.shape == (n,)
+            and t.is_contiguous()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda or t.get_device() != dev:
@@ -76,24 +95,25 @@ def _blocks(cols: int) -> int:
 
 
 def _codes(codes: torch.Tensor, scales: torch.Tensor, names, dev: int):
-    """Check MXFP4 codes [R, 16 a block] and scales [blocks / 4, at least R, 4]; returns the rows'
-    strides of both (bytes, words)."""
+    """Check MXFP4 codes [R, 16 a block] and scales [blocks / 4, at least R, 4]; returns rows, bytes a
+    row and the rows' strides of both (bytes, words)."""
     ld = _matrix(codes, names[0], _U8, dev)
-    if not (isinstance(scales, torch.Tensor) and scales.dtype is _U8 and scales.is_cuda
-            and scales.get_device() == dev and scales.is_contiguous() and scales.dim() == 3):
+    if not (isinstance(scales, torch.Tensor) and scales.dtype is _U8 and scales.get_device() == dev
+            and scales.is_contiguous() and scales.dim() == 3):
         raise TypeError(f"{names[1]} must be contiguous uint8 [column words, rows, 4] on device {dev}")
     rows, nb = codes.shape
     words, lds, four = scales.shape
     if nb % 16 or words != (nb // 16 + 3) // 4 or four != 4 or lds < rows or lds % 4:
         raise ValueError(f"{names[0]} {tuple(codes.shape)} and {names[1]} {tuple(scales.shape)} do not belong "
                          "together: expected [R, 16 B] and [ceil(B / 4), R rounded up to 4, 4]")
-    return (ld if rows > 1 else max(nb, 16)), lds
+    return rows, nb, ld, lds
 
 
-def _new_codes(rows: int, cols: int, like: torch.Tensor):
-    nb = _blocks(cols)
-    return (_empty((rows, 16 * nb), dtype=_U8, device=like.device),
-            _empty(((nb + 3) // 4, (rows + 3) // 4 * 4, 4), dtype=_U8, device=like.device))
+def _new_codes(rows: int, cols: int, device):
+    nb = (cols + 31) // 32 * 16
+    lds = (rows + 3) // 4 * 4
+    return (_empty((rows, nb), (nb, 1), dtype=_U8, device=device),
+            _empty(((cols + 127) // 128, lds, 4), (4 * lds, 4, 1), dtype=_U8, device=device))
 
 
 def _fold(fold: str) -> int:
@@ -105,7 +125,7 @@ def _fold(fold: str) -> int:
 def _out(out: Optional[torch.Tensor], rows: int, cols: int, dtype: torch.dtype, like: torch.Tensor,
          dev: int, name: str = "out"):
     if out is None:
-        return _empty((rows, cols), dtype=dtype, device=like.device), cols
+        return _empty((rows, cols), (cols, 1), dtype=dtype, device=like.device), cols
     ld = _matrix(out, name, dtype, dev)
     if tuple(out.shape) != (rows, cols):
         raise ValueError(f"{name} has shape {tuple(out.shape)}, expected {(rows, cols)}")
@@ -113,12 +133,14 @@ def _out(out: Optional[torch.Tensor], rows: int, cols: int, dtype: torch.dtype, 
 
 
 # -------------------------------------------------------------------------- rows and values
-@_entry
 def awq_int8_dequantize(codes: torch.Tensor, steps: torch.Tensor, cols: int,
-                        dtype: torch.dtype = torch.float16, out: Optional[torch.Tensor] = None):
+                        dtype: torch.dtype = torch.float16, out: Optional[torch.Tensor] = None, *,
+                        stream=None):
     """The values [R, cols] in dtype (fp16 or bf16) that 8-bit rows stand for: codes int8 [R, cols rounded
     up to 16] (as awq_int8_quantize and awq_rmsnorm_int8 make them) times steps fp32 [R]."""
     dev = _device()
+    if stream is not None or _away(codes, dev):
+        return _elsewhere(awq_int8_dequantize, stream, codes, steps, cols, dtype, out)
     ld = _matrix(codes, "codes", _I8, dev)
     R, nc = codes.shape
     if cols < 0 or nc != _round16(cols):
@@ -128,48 +150,51 @@ def awq_int8_dequantize(codes: torch.Tensor, steps: torch.Tensor, cols: int,
     y, ldo = _out(out, R, cols, dtype, codes, dev)
     if R == 0 or cols == 0:
         return y
-    st = lib().awq_int8_dequantize(codes.data_ptr(), ld, ps, R, cols, dt, y.data_ptr(), ldo,
+    st = (_C or _lib()).awq_int8_dequantize(codes.data_ptr(), ld, ps, R, cols, dt, y.data_ptr(), ldo,
                                    _raw_stream(dev))
     if st:
         _check(st, "awq_int8_dequantize")
     return y
 
 
-@_entry
-def awq_mxfp4_quantize(A: torch.Tensor, s: Optional[torch.Tensor] = None, fold: str = "divide"):
+def awq_mxfp4_quantize(A: torch.Tensor, s: Optional[torch.Tensor] = None, fold: str = "divide", *,
+                       stream=None):
     """Rows of A (fp16 or bf16 [R, K]) in MXFP4: codes uint8 [R, 16 ceil(K / 32)], two columns a byte, and
     scales uint8 [ceil(K / 128), R rounded up to 4, 4] (see awq_serve.h for both).  With s (fp32 [K])
     the values are A / s (fold="divide", activations) or A * s (fold="multiply", weights)."""
     dev = _device()
+    if stream is not None or _away(A, dev):
+        return _elsewhere(awq_mxfp4_quantize, stream, A, s, fold)
     lda = _matrix(A, "A", None, dev)
     dt = _dtype(A.dtype, "A")
     f = _fold(fold)
     R, K = A.shape
     ps = None if s is None else _vector(s, _FP32, "s", K, dev)
-    codes, scales = _new_codes(R, K, A)
+    codes, scales = _new_codes(R, K, A.device)
     if R == 0 or K == 0:
         return codes, scales
-    st = lib().awq_mxfp4_quantize(A.data_ptr(), R, K, lda, dt, ps, f, codes.data_ptr(), codes.shape[1],
-                                  scales.data_ptr(), scales.shape[1], _raw_stream(dev))
+    st = (_C or _lib()).awq_mxfp4_quantize(A.data_ptr(), R, K, lda, dt, ps, f, codes.data_ptr(), (K + 31) // 32 * 16,
+                                  scales.data_ptr(), (R + 3) // 4 * 4, _raw_stream(dev))
     if st:
         _check(st, "awq_mxfp4_quantize")
     return codes, scales
 
 
-@_entry
 def awq_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: int,
-                         dtype: torch.dtype = torch.float16, out: Optional[torch.Tensor] = None):
+                         dtype: torch.dtype = torch.float16, out: Optional[torch.Tensor] = None, *,
+                         stream=None):
     """The values [R, cols] in dtype (fp16 or bf16) that MXFP4 codes and scales stand for."""
     dev = _device()
-    ld, lds = _codes(codes, scales, ("codes", "scales"), dev)
-    R, nb = codes.shape
+    if stream is not None or _away(codes, dev):
+        return _elsewhere(awq_mxfp4_dequantize, stream, codes, scales, cols, dtype, out)
+    R, nb, ld, lds = _codes(codes, scales, ("codes", "scales"), dev)
     if cols < 0 or nb != 16 * _blocks(cols):
         raise ValueError(f"codes has {nb} bytes a row, expected {16 * _blocks(cols)}")
     dt = _dtype(dtype, "dtype")
     y, ldo = _out(out, R, cols, dtype, codes, dev)
     if R == 0 or cols == 0:
         return y
-    st = lib().awq_mxfp4_dequantize(codes.data_ptr(), ld, scales.data_ptr(), lds, R, cols, dt,
+    st = (_C or _lib()).awq_mxfp4_dequantize(codes.data_ptr(), ld, scales.data_ptr(), lds, R, cols, dt,
                                     y.data_ptr(), ldo, _raw_stream(dev))
     if st:
         _check(st, "awq_mxfp4_dequantize")
@@ -182,19 +207,18 @@ def awq_mxfp4_linear_workspace_bytes(n_tokens: int, out_features: int, in_featur
     return int(lib().awq_mxfp4_linear_workspace_bytes(n_tokens, out_features, in_features))
 
 
-@_entry
 def awq_mxfp4_matmul(xc: torch.Tensor, xs: torch.Tensor, wc: torch.Tensor, ws: torch.Tensor,
                      dtype: torch.dtype = torch.float16, bias: Optional[torch.Tensor] = None,
-                     out: Optional[torch.Tensor] = None):
+                     out: Optional[torch.Tensor] = None, *, stream=None):
     """y [T, M] = x w^T (+ bias) in `dtype` for MXFP4 codes and scales of tokens (xc, xs) and weights
     (wc, ws), as awq_mxfp4_quantize and awq_rmsnorm_mxfp4 make them."""
     dev = _device()
-    ldx, ldxs = _codes(xc, xs, ("xc", "xs"), dev)
-    ldw, ldws = _codes(wc, ws, ("wc", "ws"), dev)
-    T, nb = xc.shape
-    M = wc.shape[0]
-    if wc.shape[1] != nb:
-        raise ValueError(f"xc and wc differ in columns ({nb} and {wc.shape[1]} bytes)")
+    if stream is not None or _away(xc, dev):
+        return _elsewhere(awq_mxfp4_matmul, stream, xc, xs, wc, ws, dtype, bias, out)
+    T, nb, ldx, ldxs = _codes(xc, xs, ("xc", "xs"), dev)
+    M, nw, ldw, ldws = _codes(wc, ws, ("wc", "ws"), dev)
+    if nw != nb:
+        raise ValueError(f"xc and wc differ in columns ({nb} and {nw} bytes)")
     dt = _dtype(dtype, "dtype")
     pb = None if bias is None else _vector(bias, dtype, "bias", M, dev)
     y, ldy = _out(out, T, M, dtype, xc, dev)
@@ -202,7 +226,7 @@ def awq_mxfp4_matmul(xc: torch.Tensor, xs: torch.Tensor, wc: torch.Tensor, ws: t
         return y
     py = y.data_ptr()
     # an empty tensor has no address; the call does not read it, any device pointer serves
-    st = lib().awq_mxfp4_matmul(xc.data_ptr() or py, ldx, xs.data_ptr() or py, ldxs, T,
+    st = (_C or _lib()).awq_mxfp4_matmul(xc.data_ptr() or py, ldx, xs.data_ptr() or py, ldxs, T,
                                 wc.data_ptr() or py, ldw, ws.data_ptr() or py, ldws, M, 2 * nb, pb, dt,
                                 py, ldy, _raw_stream(dev))
     if st:
@@ -210,22 +234,23 @@ def awq_mxfp4_matmul(xc: torch.Tensor, xs: torch.Tensor, wc: torch.Tensor, ws: t
     return y
 
 
-@_entry
 def awq_mxfp4_linear(x: torch.Tensor, wc: torch.Tensor, ws: torch.Tensor,
                      s: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
-                     out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+                     out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, *,
+                     stream=None):
     """y [T, M] in x's type: each token of x (fp16 or bf16 [T, K]) divided by s (fp32 [K], if given),
     quantised to MXFP4 and multiplied with the weight's codes and scales wc, ws (as
     awq_mxfp4_quantize(W, s, "multiply") makes them)."""
     dev = _device()
+    if stream is not None or _away(x, dev):
+        return _elsewhere(awq_mxfp4_linear, stream, x, wc, ws, s, bias, out, workspace)
     ldx = _matrix(x, "x", None, dev)
     dtype = x.dtype
     dt = _dtype(dtype, "x")
-    ldw, ldws = _codes(wc, ws, ("wc", "ws"), dev)
+    M, nb, ldw, ldws = _codes(wc, ws, ("wc", "ws"), dev)
     T, K = x.shape
-    M = wc.shape[0]
-    if wc.shape[1] != 16 * _blocks(K):
-        raise ValueError(f"wc has {wc.shape[1]} bytes a row, expected {16 * _blocks(K)}")
+    if nb != 16 * _blocks(K):
+        raise ValueError(f"wc has {nb} bytes a row, expected {16 * _blocks(K)}")
     ps = None if s is None else _vector(s, _FP32, "s", K, dev)
     pb = None if bias is None else _vector(bias, dtype, "bias", M, dev)
     y, ldy = _out(out, T, M, dtype, x, dev)
@@ -233,7 +258,7 @@ def awq_mxfp4_linear(x: torch.Tensor, wc: torch.Tensor, ws: torch.Tensor,
         return y
     py = y.data_ptr()
     ws_, pws, nws = _workspace(workspace, awq_mxfp4_linear_workspace_bytes(T, M, K), x.device)
-    st = lib().awq_mxfp4_linear(x.data_ptr() or py, ldx, (ps or py) if s is not None else None, T,
+    st = (_C or _lib()).awq_mxfp4_linear(x.data_ptr() or py, ldx, (ps or py) if s is not None else None, T,
                                 wc.data_ptr() or py, ldw, ws.data_ptr() or py, ldws, M, K, pb, dt, py,
                                 ldy, pws, nws, _raw_stream(dev))
     if st:
@@ -247,7 +272,7 @@ def _norm_args(x, weight, eps, residual, h_out, dev):
     ldx = _matrix(x, "x", None, dev)
     dtype = x.dtype
     dt = _dtype(dtype, "x")
-    R, K = x.shape
+    R, K = shape = x.shape
     if K == 0:
         raise ValueError("x must have columns")
     pw, wt = None, dt
@@ -261,61 +286,65 @@ def _norm_args(x, weight, eps, residual, h_out, dev):
             raise ValueError("h_out is written only where a residual is given")
         return (x.data_ptr(), ldx, None, 0, R, K, dt, pw, wt, eps, None, 0), x
     ldr = _matrix(residual, "residual", dtype, dev)
-    if residual.shape != x.shape:
+    if residual.shape != shape:
         raise ValueError(f"residual has shape {tuple(residual.shape)}, expected {(R, K)}")
     h, ldh = _out(h_out, R, K, dtype, x, dev, "h_out")
     return (x.data_ptr(), ldx, residual.data_ptr(), ldr, R, K, dt, pw, wt, eps, h.data_ptr(), ldh), h
 
 
-@_entry
 def awq_rmsnorm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-6, *,
                 residual: Optional[torch.Tensor] = None, h_out: Optional[torch.Tensor] = None,
-                out: Optional[torch.Tensor] = None):
+                out: Optional[torch.Tensor] = None, stream=None):
     """Root-mean-square norm of the rows of x (fp16 or bf16 [R, K]): returns (y, h) with h = x + residual in
     x's type (x itself without a residual) and y = h weight / sqrt(mean h^2 + eps) in x's type.
     weight [K] is fp32 or of x's type (None: ones); the scales of a search are folded into it (weight
     / s).  h goes to h_out if given, which may be the residual or x itself; out receives y."""
     dev = _device()
+    if stream is not None or _away(x, dev):
+        return _elsewhere(awq_rmsnorm, stream, x, weight, eps, residual=residual, h_out=h_out, out=out)
     args, h = _norm_args(x, weight, eps, residual, h_out, dev)
-    R, K = x.shape
-    y, ldy = _out(out, R, K, x.dtype, x, dev)
-    if R:
-        st = lib().awq_rmsnorm(*args, y.data_ptr(), ldy, _raw_stream(dev))
+    y, ldy = _out(out, args[4], args[5], x.dtype, x, dev)
+    if args[4]:
+        st = (_C or _lib()).awq_rmsnorm(*args, y.data_ptr(), ldy, _raw_stream(dev))
         if st:
             _check(st, "awq_rmsnorm")
     return y, h
 
 
-@_entry
 def awq_rmsnorm_int8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-6, *,
-                     residual: Optional[torch.Tensor] = None, h_out: Optional[torch.Tensor] = None):
+                     residual: Optional[torch.Tensor] = None, h_out: Optional[torch.Tensor] = None,
+                     stream=None):
     """The same norm as rows of 8-bit integers: returns (codes, steps, h), codes int8 [R, K rounded up to
     16] and steps fp32 [R] as awq_int8_matmul takes them."""
     dev = _device()
+    if stream is not None or _away(x, dev):
+        return _elsewhere(awq_rmsnorm_int8, stream, x, weight, eps, residual=residual, h_out=h_out)
     args, h = _norm_args(x, weight, eps, residual, h_out, dev)
-    R, K = x.shape
-    codes = _empty((R, _round16(K)), dtype=_I8, device=x.device)
-    steps = _empty(R, dtype=_FP32, device=x.device)
+    R, nc = args[4], _round16(args[5])
+    device = x.device
+    codes = _empty((R, nc), (nc, 1), dtype=_I8, device=device)
+    steps = _empty((R,), (1,), dtype=_FP32, device=device)
     if R:
-        st = lib().awq_rmsnorm_int8(*args, codes.data_ptr(), codes.shape[1], steps.data_ptr(),
-                                    _raw_stream(dev))
+        st = (_C or _lib()).awq_rmsnorm_int8(*args, codes.data_ptr(), nc, steps.data_ptr(), _raw_stream(dev))
         if st:
             _check(st, "awq_rmsnorm_int8")
     return codes, steps, h
 
 
-@_entry
 def awq_rmsnorm_mxfp4(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-6, *,
-                      residual: Optional[torch.Tensor] = None, h_out: Optional[torch.Tensor] = None):
+                      residual: Optional[torch.Tensor] = None, h_out: Optional[torch.Tensor] = None,
+                      stream=None):
     """The same norm as rows of MXFP4: returns (codes, scales, h), codes and scales as awq_mxfp4_quantize
     gives them and awq_mxfp4_matmul takes them."""
     dev = _device()
+    if stream is not None or _away(x, dev):
+        return _elsewhere(awq_rmsnorm_mxfp4, stream, x, weight, eps, residual=residual, h_out=h_out)
     args, h = _norm_args(x, weight, eps, residual, h_out, dev)
-    R, K = x.shape
-    codes, scales = _new_codes(R, K, x)
+    R, K = args[4], args[5]
+    codes, scales = _new_codes(R, K, x.device)
     if R:
-        st = lib().awq_rmsnorm_mxfp4(*args, codes.data_ptr(), codes.shape[1], scales.data_ptr(),
-                                     scales.shape[1], _raw_stream(dev))
+        st = (_C or _lib()).awq_rmsnorm_mxfp4(*args, codes.data_ptr(), (K + 31) // 32 * 16, scales.data_ptr(),
+                                              (R + 3) // 4 * 4, _raw_stream(dev))
         if st:
             _check(st, "awq_rmsnorm_mxfp4")
     return codes, scales, h

@@ -12,13 +12,74 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "int8_quant.h"
 #include "quantizer.h"
 
 #pragma clang fp contract(off)
 
 namespace awq {
 
-constexpr int kMxBlock = 32;
+// Columns [c0, c0 + 8) of a 16-bit row as they lie in memory, zeros from K on; their values; such
+// values stored; 8 of a vector of fp32, `fill` from K on.  Rows begin at any even address: a global
+// load or store of 16 bytes takes every alignment on this target.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
+typedef f32x4 f32x4_at4 __attribute__((aligned(4)));
+
+__device__ __forceinline__ u32x4 raw8(const uint16_t* a, int c0, int K) {
+  if (c0 + 8 <= K) return *(const u32x4_at2*)(a + c0);
+  uint32_t h[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) h[j] = a[min(c0 + j, K - 1)];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) h[j] = c0 + j < K ? h[j] : 0u;
+  return u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
+}
+
+template <bool BF16>
+__device__ __forceinline__ void values8(const u32x4& r, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t w = r[j];
+    v[2 * j] = from16<BF16>(w & 0xffffu);
+    v[2 * j + 1] = from16<BF16>(w >> 16);
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
+  u32x4 r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r[j] = to16<BF16>(v[2 * j]) | ((uint32_t)to16<BF16>(v[2 * j + 1]) << 16);
+  return r;
+}
+
+__device__ __forceinline__ void store8(uint16_t* a, int c0, int K, const u32x4& r) {
+  if (c0 + 8 <= K) {
+    *(u32x4_at2*)(a + c0) = r;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c0 + j < K) a[c0 + j] = (uint16_t)(r[j >> 1] >> (16 * (j & 1)));
+  }
+}
+
+__device__ __forceinline__ void floats8(const float* a, int c0, int K, float fill, float (&v)[8]) {
+  if (c0 + 8 <= K) {
+    const f32x4 lo = *(const f32x4_at4*)(a + c0), hi = *(const f32x4_at4*)(a + c0 + 4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = lo[j];
+      v[j + 4] = hi[j];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = a[min(c0 + j, K - 1)];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c0 + j < K ? v[j] : fill;
+  }
+}
 
 __device__ __forceinline__ uint32_t quad_max_u32(uint32_t x) {
   x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, kDppQuadXor1, 0xf, 0xf, false));
@@ -39,10 +100,11 @@ __device__ __forceinline__ float mx_scale(uint32_t b) {
 
 // The lane's 8 codes, column 0 in the low nibble, and its block's scale byte.
 __device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8], uint32_t& byte) {
-  uint32_t top = 0;
+  // (maxima that keep a NaN; one instruction for three values)
+  float m = __builtin_elementwise_maximum(fabsf(v[0]), fabsf(v[1]));
 #pragma unroll
-  for (int j = 0; j < 8; ++j) top = max(top, __builtin_bit_cast(uint32_t, v[j]) & 0x7fffffffu);
-  byte = mx_scale_byte(quad_max_u32(top));
+  for (int j = 2; j < 8; ++j) m = __builtin_elementwise_maximum(m, fabsf(v[j]));
+  byte = mx_scale_byte(quad_max_u32(__builtin_bit_cast(uint32_t, m) & 0x7fffffffu));
   const float sc = mx_scale(byte);
   uint32_t c = 0;
   c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0], v[1], sc, 0);

@@ -35,7 +35,6 @@ namespace {
 typedef int int32x8 __attribute__((ext_vector_type(8)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kFp4 = 4;  // the instruction's code for the format e2m1
 constexpr int64_t kCacheBytes = 256 << 20;  // the last-level cache
@@ -398,7 +397,6 @@ struct MxFewArgs {
   const float* s;
   int64_t ldx16;
   int cols;
-  bool vec;
 };
 
 template <bool FUSED, bool BF16>
@@ -438,9 +436,13 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mxfp4_few(MxFewArgs f) {
       const int t = i / n8, ch = i - t * n8;  // sixteen lanes have one token and one word
       float v[8];
       const uint16_t* x = f.x16 + t * f.ldx16;
-      const int fold = f.s ? kFoldDivide : kFoldNone;
-      if (f.vec) load_row8<BF16, true>(x, f.s, fold, 8 * ch, f.cols, v);
-      else load_row8<BF16, false>(x, f.s, fold, 8 * ch, f.cols, v);
+      values8<BF16>(raw8(x, 8 * ch, f.cols), v);
+      if (f.s) {
+        float sv[8];
+        floats8(f.s, 8 * ch, f.cols, 1.0f, sv);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = v[j] / sv[j];
+      }
       uint32_t byte;
       const uint32_t c = mx_codes8(v, byte);
       *(uint32_t*)(lds + (size_t)t * nch * 256 + 4 * ch) = c;
@@ -576,7 +578,7 @@ hipError_t launch_mxfp4_matmul(const MxArgs& a, hipStream_t stream) {
   if (a.T <= 0 || a.M <= 0) return hipSuccess;
   const int form = mxfp4_form(a.T, a.M, a.KB);
   if (form == kMxFew) {
-    const MxFewArgs f{a, nullptr, nullptr, 0, 0, false};
+    const MxFewArgs f{a, nullptr, nullptr, 0, 0};
     return launch_few<false>(f, stream);
   }
   return a.bf16 ? launch_form<true>(a, form, stream) : launch_form<false>(a, form, stream);
@@ -589,7 +591,7 @@ bool mxfp4_linear_fused(int64_t T, int64_t M, int64_t cols) {
 hipError_t launch_mxfp4_linear_fused(const MxArgs& a, const void* x, int64_t ldx, const float* s,
                                      int cols, hipStream_t stream) {
   if (a.T <= 0 || a.M <= 0) return hipSuccess;
-  const MxFewArgs f{a, (const uint16_t*)x, s, ldx, cols, row_vector_loads(x, a.T > 1 ? ldx : 0, s)};
+  const MxFewArgs f{a, (const uint16_t*)x, s, ldx, cols};
   return launch_few<true>(f, stream);
 }
 

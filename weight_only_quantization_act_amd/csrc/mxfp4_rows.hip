@@ -10,7 +10,6 @@
 #include <hip/hip_runtime.h>
 
 #include "grid.h"
-#include "int8_quant.h"
 #include "mx_format.h"
 #include "mx_internal.h"
 #include "serve_internal.h"
@@ -22,12 +21,14 @@ namespace {
 constexpr int kRowsTile = 16;  // rows a block
 constexpr int kTileWords = 4;  // scale words (128 columns) of a row a block
 
-template <bool BF16, bool VEC>
+// FOLD: kFoldNone, kFoldDivide or kFoldMultiply.
+template <bool BF16, int FOLD>
 __global__ __launch_bounds__(256) void k_mxfp4_rows(const uint16_t* __restrict__ A, unsigned rows,
                                                     int K, int64_t lda, const float* __restrict__ s,
-                                                    int fold, uint8_t* __restrict__ codes,
-                                                    int64_t ldc, uint32_t* __restrict__ scales,
-                                                    int64_t lds, unsigned tiles_k) {
+                                                    uint8_t* __restrict__ codes, int64_t ldc,
+                                                    uint32_t* __restrict__ scales, int64_t lds,
+                                                    unsigned tiles_k) {
+  constexpr int R = kRowsTile / 4;  // rows a wave
   const unsigned b = block_number();
   const unsigned tr = b / tiles_k, tk = b - tr * tiles_k;
   if (tr * kRowsTile >= rows) return;  // the whole block
@@ -36,12 +37,24 @@ __global__ __launch_bounds__(256) void k_mxfp4_rows(const uint16_t* __restrict__
   const int q = c0 >> 7;
   if (q >= (K + 127) >> 7) return;  // sixteen lanes together; no barrier follows
   const bool stored = c0 < (K + 31) / 32 * 32;
+  const unsigned row0 = tr * kRowsTile + R * wave;
+  // all rows' loads before the first is used; rows past the last repeat it
+  u32x4 raw[R];
 #pragma unroll
-  for (int i = 0; i < kRowsTile / 4; ++i) {
-    const unsigned row = tr * kRowsTile + 4 * i + wave;
+  for (int i = 0; i < R; ++i) raw[i] = raw8(A + (int64_t)min(row0 + i, rows - 1) * lda, c0, K);
+  float sv[8];
+  if constexpr (FOLD != kFoldNone) floats8(s, c0, K, 1.0f, sv);
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const unsigned row = row0 + i;
     if (row >= rows) return;  // the whole wave
     float v[8];
-    load_row8<BF16, VEC>(A + (int64_t)row * lda, s, fold, c0, K, v);
+    values8<BF16>(raw[i], v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (FOLD == kFoldMultiply) v[j] = v[j] * sv[j];
+      if constexpr (FOLD == kFoldDivide) v[j] = v[j] / sv[j];
+    }
     uint32_t byte;
     const uint32_t c = mx_codes8(v, byte);
     if (stored) *(uint32_t*)(codes + (int64_t)row * ldc + (c0 >> 1)) = c;
@@ -50,31 +63,11 @@ __global__ __launch_bounds__(256) void k_mxfp4_rows(const uint16_t* __restrict__
   }
 }
 
-// 8 columns of a row from 4 bytes of codes or 8 of integers a thread.
-template <bool BF16>
-__device__ __forceinline__ void store_row8(uint16_t* out, int c0, int K, bool vec, const float (&v)[8]) {
-  uint16_t o[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) o[j] = to16<BF16>(v[j]);
-  if (vec && c0 + 8 <= K) {
-    uint4 p;
-    p.x = o[0] | ((uint32_t)o[1] << 16);
-    p.y = o[2] | ((uint32_t)o[3] << 16);
-    p.z = o[4] | ((uint32_t)o[5] << 16);
-    p.w = o[6] | ((uint32_t)o[7] << 16);
-    *(uint4*)(out + c0) = p;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c0 + j < K) out[c0 + j] = o[j];
-  }
-}
-
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_mxfp4_values(const uint8_t* __restrict__ codes, int64_t ldc,
                                                       const uint32_t* __restrict__ scales, int64_t lds,
                                                       unsigned rows, int K, uint16_t* __restrict__ out,
-                                                      int64_t ldo, bool vec, unsigned tiles_k) {
+                                                      int64_t ldo, unsigned tiles_k) {
   const unsigned b = block_number();
   const unsigned tr = b / tiles_k, tk = b - tr * tiles_k;
   if (tr * kRowsTile >= rows) return;
@@ -97,7 +90,7 @@ __global__ __launch_bounds__(256) void k_mxfp4_values(const uint8_t* __restrict_
     float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = e[j >> 1][j & 1];
-    store_row8<BF16>(out + (int64_t)row * ldo, c0, K, vec, v);
+    store8(out + (int64_t)row * ldo, c0, K, pack8<BF16>(v));
   }
 }
 
@@ -105,7 +98,7 @@ template <bool BF16>
 __global__ __launch_bounds__(256) void k_int8_values(const int8_t* __restrict__ codes, int64_t ldc,
                                                      const float* __restrict__ steps, unsigned rows,
                                                      int K, uint16_t* __restrict__ out, int64_t ldo,
-                                                     bool vec, unsigned tiles_k) {
+                                                     unsigned tiles_k) {
   const unsigned b = block_number();
   const unsigned tr = b / tiles_k, tk = b - tr * tiles_k;
   if (tr * kRowsTile >= rows) return;
@@ -124,7 +117,7 @@ __global__ __launch_bounds__(256) void k_int8_values(const int8_t* __restrict__ 
       v[j] = (float)(int8_t)(c.x >> (8 * j)) * st;
       v[j + 4] = (float)(int8_t)(c.y >> (8 * j)) * st;
     }
-    store_row8<BF16>(out + (int64_t)row * ldo, c0, K, vec, v);
+    store8(out + (int64_t)row * ldo, c0, K, pack8<BF16>(v));
   }
 }
 
@@ -142,17 +135,21 @@ hipError_t launch_mxfp4_rows(const void* A, int64_t rows, int cols, int64_t lda,
                              const float* s, int fold, uint8_t* codes, int64_t ld_codes,
                              uint32_t* scales, int64_t ld_scales, hipStream_t stream) {
   if (rows <= 0 || cols <= 0) return hipSuccess;
-  const bool vec = row_vector_loads(A, lda, s);
   const int f = s ? fold : kFoldNone;
-#define AWQ_MXROWS(B, V)                                                                          \
-  hipLaunchKernelGGL((k_mxfp4_rows<B, V>), grid_of(tiles(rows, cols)), dim3(256), 0, stream,      \
-                     (const uint16_t*)A, (unsigned)rows, cols, lda, s, f, codes, ld_codes, scales, \
+#define AWQ_MXROWS(B, F)                                                                     \
+  hipLaunchKernelGGL((k_mxfp4_rows<B, F>), grid_of(tiles(rows, cols)), dim3(256), 0, stream, \
+                     (const uint16_t*)A, (unsigned)rows, cols, lda, s, codes, ld_codes, scales, \
                      ld_scales, col_tiles(cols))
+#define AWQ_MXROWS_F(B)                                    \
+  if (f == kFoldNone) AWQ_MXROWS(B, kFoldNone);            \
+  else if (f == kFoldDivide) AWQ_MXROWS(B, kFoldDivide);   \
+  else AWQ_MXROWS(B, kFoldMultiply)
   if (bf16) {
-    if (vec) AWQ_MXROWS(true, true); else AWQ_MXROWS(true, false);
+    AWQ_MXROWS_F(true);
   } else {
-    if (vec) AWQ_MXROWS(false, true); else AWQ_MXROWS(false, false);
+    AWQ_MXROWS_F(false);
   }
+#undef AWQ_MXROWS_F
 #undef AWQ_MXROWS
   return hipGetLastError();
 }
@@ -161,28 +158,26 @@ hipError_t launch_mxfp4_values(const uint8_t* codes, int64_t ld_codes, const uin
                                int64_t ld_scales, int64_t rows, int cols, bool bf16, void* out,
                                int64_t ldo, hipStream_t stream) {
   if (rows <= 0 || cols <= 0) return hipSuccess;
-  const bool vec = row_vector_loads(out, ldo, nullptr);
   const dim3 grid = grid_of(tiles(rows, cols));
   if (bf16)
     hipLaunchKernelGGL((k_mxfp4_values<true>), grid, dim3(256), 0, stream, codes, ld_codes, scales,
-                       ld_scales, (unsigned)rows, cols, (uint16_t*)out, ldo, vec, col_tiles(cols));
+                       ld_scales, (unsigned)rows, cols, (uint16_t*)out, ldo, col_tiles(cols));
   else
     hipLaunchKernelGGL((k_mxfp4_values<false>), grid, dim3(256), 0, stream, codes, ld_codes, scales,
-                       ld_scales, (unsigned)rows, cols, (uint16_t*)out, ldo, vec, col_tiles(cols));
+                       ld_scales, (unsigned)rows, cols, (uint16_t*)out, ldo, col_tiles(cols));
   return hipGetLastError();
 }
 
 hipError_t launch_int8_values(const int8_t* codes, int64_t ld_codes, const float* steps, int64_t rows,
                               int cols, bool bf16, void* out, int64_t ldo, hipStream_t stream) {
   if (rows <= 0 || cols <= 0) return hipSuccess;
-  const bool vec = row_vector_loads(out, ldo, nullptr);
   const dim3 grid = grid_of(tiles(rows, cols));
   if (bf16)
     hipLaunchKernelGGL((k_int8_values<true>), grid, dim3(256), 0, stream, codes, ld_codes, steps,
-                       (unsigned)rows, cols, (uint16_t*)out, ldo, vec, col_tiles(cols));
+                       (unsigned)rows, cols, (uint16_t*)out, ldo, col_tiles(cols));
   else
     hipLaunchKernelGGL((k_int8_values<false>), grid, dim3(256), 0, stream, codes, ld_codes, steps,
-                       (unsigned)rows, cols, (uint16_t*)out, ldo, vec, col_tiles(cols));
+                       (unsigned)rows, cols, (uint16_t*)out, ldo, col_tiles(cols));
   return hipGetLastError();
 }
 

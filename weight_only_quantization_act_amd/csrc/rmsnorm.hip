@@ -23,64 +23,36 @@ namespace awq {
 
 namespace {
 
-// 8 columns of a 16-bit row as they lie in memory (0 past the last), and their values.
-__device__ __forceinline__ uint4 raw8(const uint16_t* a, int c0, int K, bool vec) {
-  if (vec && c0 + 8 <= K) return *(const uint4*)(a + c0);
-  uint32_t w[4];
+// The weights of 8 columns as they lie in memory: W32 fp32, else 16-bit (0 past the last column, 1 where
+// there is no weight).
+template <bool BF16, bool W32>
+struct Weights {
+  u32x4 r[W32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* w, int c0, int K) {
+    if constexpr (W32) {
+      float v[8];
+      floats8((const float*)w, c0, K, 0.0f, v);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t lo = c0 + 2 * j < K ? a[c0 + 2 * j] : 0u, hi = c0 + 2 * j + 1 < K ? a[c0 + 2 * j + 1] : 0u;
-    w[j] = lo | (hi << 16);
+      for (int j = 0; j < 8; ++j) r[j >> 2][j & 3] = __builtin_bit_cast(uint32_t, v[j]);
+    } else if (w) {
+      r[0] = raw8((const uint16_t*)w, c0, K);
+    } else {
+      const uint32_t one = to16<BF16>(1.0f) * 0x10001u;
+      r[0] = u32x4{one, one, one, one};
+    }
   }
-  return uint4{w[0], w[1], w[2], w[3]};
-}
-
-template <bool BF16>
-__device__ __forceinline__ void values8(const uint4& r, float (&v)[8]) {
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    if constexpr (W32) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    v[2 * j] = from16<BF16>(w[j] & 0xffffu);
-    v[2 * j + 1] = from16<BF16>(w[j] >> 16);
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t u = r[j >> 2][j & 3];
+        v[j] = __builtin_bit_cast(float, u);
+      }
+    } else {
+      values8<BF16>(r[0], v);
+    }
   }
-}
-
-template <bool BF16>
-__device__ __forceinline__ void store8(uint16_t* a, int c0, int K, bool vec, const float (&v)[8]) {
-  uint16_t o[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) o[j] = to16<BF16>(v[j]);
-  if (vec && c0 + 8 <= K) {
-    uint4 p;
-    p.x = o[0] | ((uint32_t)o[1] << 16);
-    p.y = o[2] | ((uint32_t)o[3] << 16);
-    p.z = o[4] | ((uint32_t)o[5] << 16);
-    p.w = o[6] | ((uint32_t)o[7] << 16);
-    *(uint4*)(a + c0) = p;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c0 + j < K) a[c0 + j] = o[j];
-  }
-}
-
-template <bool BF16>
-__device__ __forceinline__ void weight8(const NormArgs& a, int c0, bool vec, float (&w)[8]) {
-  if (!a.w) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = 1.0f;
-  } else if (!a.w32) {
-    values8<BF16>(raw8((const uint16_t*)a.w, c0, a.cols, vec), w);
-  } else if (vec && c0 + 8 <= a.cols) {
-    const float4 s0 = *(const float4*)((const float*)a.w + c0), s1 = *(const float4*)((const float*)a.w + c0 + 4);
-    const float sv[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = sv[j];
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = c0 + j < a.cols ? ((const float*)a.w)[c0 + j] : 0.0f;
-  }
-}
+};
 
 // 1 / sqrt(x): the hardware's estimate e0 (relative error d, 2^-26 or so) and one step of third order,
 // y = e0 (1 + d + 3/2 d^2 ...) with 2 d = 1 - x e0^2; NaN for an infinite x.
@@ -90,15 +62,22 @@ __device__ __forceinline__ double inverse_root(double x) {
   return fma(y * e, fma(e, 0.375, 0.5), y);
 }
 
-// WPR waves a row; NCH 8-column chunks a thread in registers (0: the row is read twice).
-template <bool BF16, int OUT, int WPR, int NCH>
-__global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void k_rmsnorm(NormArgs a, unsigned vec_mask) {
-  __shared__ double red[2][WPR == 1 ? 1 : WPR];
+// WPR waves a row (1: four rows a block); NCH 8-column chunks a thread in registers, as they lie in
+// memory (0: the row is read twice).  Times below and the launch's choice: device time with inputs that
+// change from call to call.
+template <bool BF16, bool W32, int OUT, int WPR, int NCH>
+__global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void k_rmsnorm(NormArgs a) {
+  __shared__ double red[2][WPR];
   constexpr int kThreads = 64 * WPR;
   const int tid = WPR == 1 ? threadIdx.x & 63 : threadIdx.x;
-  const int64_t row = WPR == 1 ? (int64_t)block_number() * 4 + (threadIdx.x >> 6) : (int64_t)block_number();
-  if (row >= a.rows) return;  // the whole wave, or block
-  const bool vx = vec_mask & 1, vr = vec_mask & 2, vh = vec_mask & 4, vw = vec_mask & 8, vy = vec_mask & 16;
+  // Blocks go to the 8 XCDs in turn; renumbered so that neighbouring rows, whose scale words share
+  // lines, are written through one XCD's L2.
+  const unsigned n = (unsigned)(WPR == 1 ? (a.rows + 3) >> 2 : a.rows), b = block_number();
+  if (b >= n) return;  // the whole block
+  const unsigned xcd = b & 7, q8 = n >> 3, r8 = n & 7;
+  const unsigned at = xcd * q8 + min(xcd, r8) + (b >> 3);
+  const int64_t row = WPR == 1 ? (int64_t)at * 4 + (threadIdx.x >> 6) : (int64_t)at;
+  if (row >= a.rows) return;  // the whole wave
   const int K = a.cols;
   // 8-column chunks: whole 16-byte groups of codes, whole words of scales
   const int nch = OUT == kNormMxfp4 ? (K + 127) / 128 * 16 : OUT == kNormInt8 ? (K + 15) / 16 * 2 : (K + 7) / 8;
@@ -108,54 +87,60 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void k_rmsnorm(NormArgs 
 
   double sum = 0.0, top = 0.0;
   // the sum of x and r, stored
-  auto take = [&](int ch, const uint4& xv, const uint4& rv, float (&h)[8]) {
+  auto take = [&](int ch, const u32x4& xv, const u32x4& rv) {
+    if (!r) return xv;
+    float h[8], t[8];
     values8<BF16>(xv, h);
-    if (r) {
-      float t[8];
-      values8<BF16>(rv, t);
+    values8<BF16>(rv, t);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) h[j] = from16<BF16>(to16<BF16>(h[j] + t[j]));
-      store8<BF16>(hrow, 8 * ch, K, vh, h);
-    }
+    for (int j = 0; j < 8; ++j) h[j] = h[j] + t[j];
+    const u32x4 p = pack8<BF16>(h);
+    store8(hrow, 8 * ch, K, p);
+    return p;
   };
-  auto add = [&](int ch, const float (&h)[8]) {
+  auto add = [&](const u32x4& p, const Weights<BF16, W32>& wv) {
+    float h[8];
+    values8<BF16>(p, h);
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum = fma((double)h[j], (double)h[j], sum);
     if constexpr (OUT == kNormInt8) {
       float w[8];
-      weight8<BF16>(a, 8 * ch, vw, w);
+      wv.values(w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const double p = (double)h[j] * (double)w[j];
-        top = fmax(top, fabs(p));
-        sum = fma(p, 0.0, sum);  // an infinite or NaN weight makes the row NaN
+        const double v = (double)h[j] * (double)w[j];
+        top = fmax(top, fabs(v));
+        sum = fma(v, 0.0, sum);  // an infinite or NaN weight makes the row NaN
       }
     }
   };
-  float h[NCH > 0 ? NCH : 1][8];
+  u32x4 h[NCH > 0 ? NCH : 1];
+  Weights<BF16, W32> w[NCH > 0 ? NCH : 1];
   if constexpr (NCH > 0) {
     // all loads before the first store (h may be x or r themselves)
-    uint4 xv[NCH], rv[NCH];
+    u32x4 rv[NCH];
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       const int ch = tid + c * kThreads;
       if (ch < nch) {
-        xv[c] = raw8(x, 8 * ch, K, vx);
-        rv[c] = r ? raw8(r, 8 * ch, K, vr) : uint4{0, 0, 0, 0};
+        h[c] = raw8(x, 8 * ch, K);
+        if (r) rv[c] = raw8(r, 8 * ch, K);
+        if constexpr (OUT == kNormInt8) w[c].load(a.w, 8 * ch, K);
       }
     }
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       const int ch = tid + c * kThreads;
       if (ch < nch) {
-        take(ch, xv[c], rv[c], h[c]);
-        add(ch, h[c]);
+        h[c] = take(ch, h[c], rv[c]);
+        add(h[c], w[c]);
       }
     }
   } else {
     for (int ch = tid; ch < nch; ch += kThreads) {
-      take(ch, raw8(x, 8 * ch, K, vx), r ? raw8(r, 8 * ch, K, vr) : uint4{0, 0, 0, 0}, h[0]);
-      add(ch, h[0]);
+      const u32x4 xv = raw8(x, 8 * ch, K);
+      if constexpr (OUT == kNormInt8) w[0].load(a.w, 8 * ch, K);
+      add(take(ch, xv, r ? raw8(r, 8 * ch, K) : xv), w[0]);
     }
   }
 
@@ -180,20 +165,30 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void k_rmsnorm(NormArgs 
     }
   }
   const double inv = inverse_root(fma(sum, a.inv_cols, a.eps));
+  // what is kept of the row stays as it lies in memory: without this its conversions are kept instead
+  if constexpr (NCH > 0) {
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      asm volatile("" : "+v"(h[c]));
+      if constexpr (OUT == kNormInt8) asm volatile("" : "+v"(w[c].r[0]));
+      if constexpr (OUT == kNormInt8 && W32) asm volatile("" : "+v"(w[c].r[1]));
+    }
+  }
 
   RowStep st;
   if constexpr (OUT == kNormInt8) {
-    // top and inv are at least 0 or inv is NaN
+    // top is at least 0 and inv positive, or inv is NaN
     st = row_step(__builtin_bit_cast(uint32_t, (float)(top * inv)) & 0x7fffffffu);
     if (tid == 0) ((float*)a.scales)[row] = st.step;
   }
-  auto write = [&](int ch, const float (&hc)[8]) {
-    float w[8], v[8];
-    weight8<BF16>(a, 8 * ch, vw, w);
+  auto write = [&](int ch, const u32x4& p, const Weights<BF16, W32>& wp) {
+    float hc[8], wv[8], v[8];
+    values8<BF16>(p, hc);
+    wp.values(wv);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = (float)((double)hc[j] * (double)w[j] * inv);
+    for (int j = 0; j < 8; ++j) v[j] = (float)((double)hc[j] * (double)wv[j] * inv);
     if constexpr (OUT == kNormSame) {
-      store8<BF16>((uint16_t*)a.y + row * a.ldy, 8 * ch, K, vy, v);
+      store8((uint16_t*)a.y + row * a.ldy, 8 * ch, K, pack8<BF16>(v));
     } else if constexpr (OUT == kNormInt8) {
       *(uint2*)((int8_t*)a.y + row * a.ldy + 8 * ch) = row_codes8(v, st);
     } else {
@@ -212,26 +207,41 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void k_rmsnorm(NormArgs 
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       const int ch = tid + c * kThreads;
-      if (ch < nch) write(ch, h[c]);
+      if (ch < nch) {
+        // (kept in registers from the start they cost more waves than their wait does time: 16384 rows of
+        // 8192 189 us, loaded here 174)
+        if constexpr (OUT != kNormInt8) w[c].load(a.w, 8 * ch, K);
+        write(ch, h[c], w[c]);
+      }
     }
   } else {
     for (int ch = tid; ch < nch; ch += kThreads) {
-      values8<BF16>(raw8(r ? hrow : x, 8 * ch, K, r ? vh : vx), h[0]);
-      write(ch, h[0]);
+      w[0].load(a.w, 8 * ch, K);
+      write(ch, raw8(r ? hrow : x, 8 * ch, K), w[0]);
     }
   }
 }
 
-template <bool BF16, int OUT>
-hipError_t launch_out(const NormArgs& a, unsigned vec, hipStream_t stream) {
+template <bool BF16, bool W32, int OUT>
+hipError_t launch_out(const NormArgs& a, hipStream_t stream) {
   const int nch = (a.cols + 127) / 128 * 16;
-  const dim3 grid = grid_of(a.rows);
-#define AWQ_NORM(W, N)                                                                              \
-  hipLaunchKernelGGL((k_rmsnorm<BF16, OUT, W, N>), grid, dim3(64 * W), 0, stream, a, vec)
-  if (nch <= 2 * 256) AWQ_NORM(4, 2);
-  else if (nch <= 4 * 256) AWQ_NORM(4, 4);
-  else if (nch <= 8 * 256) AWQ_NORM(4, 8);
-  else AWQ_NORM(4, 0);
+#define AWQ_NORM(W, N)                                                                           \
+  hipLaunchKernelGGL((k_rmsnorm<BF16, W32, OUT, W, N>), grid_of(W == 1 ? (a.rows + 3) / 4 : a.rows), \
+                     dim3(W == 1 ? 256 : 64 * W), 0, stream, a)
+  // Waves a row, in us: few rows wait for their loads (1 of 8192 to MXFP4: two waves 9.8, four 5.6, eight
+  // 4.1; 256 of 5120 6.8, 5.3, 4.4), many want theirs close to full waves without a barrier among many
+  // (16384 of 256: one wave 8.7, two 11.2, four 15.7; of 1024 24.0, 23.8, 26.3; 4096 of 4096 to 8 bits 57,
+  // 30, 25.6, eight 27.6; 500 of 16000 four 16.6, eight 14.4).
+  if (a.rows > 1024 && nch <= 64) AWQ_NORM(1, 1);
+  else if (a.rows > 1024 && nch <= 128) AWQ_NORM(2, 1);
+  else if (a.rows > 1024 && nch <= 256) AWQ_NORM(4, 1);
+  else if (a.rows > 1024 && nch <= 2 * 256) AWQ_NORM(4, 2);
+  else if (a.rows > 1024 && nch <= 3 * 256) AWQ_NORM(4, 3);
+  else if (a.rows > 1024 && nch <= 4 * 256) AWQ_NORM(4, 4);
+  else if (nch <= 512) AWQ_NORM(8, 1);
+  else if (nch <= 2 * 512) AWQ_NORM(8, 2);
+  else if (nch <= 4 * 512) AWQ_NORM(8, 4);
+  else AWQ_NORM(8, 0);
 #undef AWQ_NORM
   return hipGetLastError();
 }
@@ -240,15 +250,13 @@ hipError_t launch_out(const NormArgs& a, unsigned vec, hipStream_t stream) {
 
 hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t stream) {
   if (a.rows <= 0) return hipSuccess;
-  auto rows16 = [](const void* p, int64_t ld) { return ((uintptr_t)p % 16) == 0 && ld % 8 == 0; };
-  const unsigned vec = (rows16(a.x, a.ldx) ? 1 : 0) | (rows16(a.r, a.ldr) ? 2 : 0) |
-                       (rows16(a.h, a.ldh) ? 4 : 0) | (((uintptr_t)a.w % 16) == 0 ? 8 : 0) |
-                       (a.out == kNormSame && rows16(a.y, a.ldy) ? 16 : 0);
-#define AWQ_NORM_OUT(B)                                                  \
-  a.out == kNormSame   ? launch_out<B, kNormSame>(a, vec, stream)        \
-  : a.out == kNormInt8 ? launch_out<B, kNormInt8>(a, vec, stream)        \
-                       : launch_out<B, kNormMxfp4>(a, vec, stream)
-  return a.bf16 ? (AWQ_NORM_OUT(true)) : (AWQ_NORM_OUT(false));
+#define AWQ_NORM_OUT(B, W)                                             \
+  a.out == kNormSame   ? launch_out<B, W, kNormSame>(a, stream)        \
+  : a.out == kNormInt8 ? launch_out<B, W, kNormInt8>(a, stream)        \
+                       : launch_out<B, W, kNormMxfp4>(a, stream)
+  const bool w32 = a.w && a.w32;
+  if (a.bf16) return w32 ? (AWQ_NORM_OUT(true, true)) : (AWQ_NORM_OUT(true, false));
+  return w32 ? (AWQ_NORM_OUT(false, true)) : (AWQ_NORM_OUT(false, false));
 #undef AWQ_NORM_OUT
 }
 
