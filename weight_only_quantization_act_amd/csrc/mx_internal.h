@@ -11,6 +11,7 @@ namespace awq {
 // MXFP4 rows: codes [rows][ld bytes], scales [columns / 128][ld_scales][4].
 constexpr int64_t kMxMaxRows = ((int64_t)1 << 29) - 512;  // two rows of scales span less than 2^32 bytes
 constexpr int64_t kMxMaxK = (int64_t)1 << 22;
+constexpr int64_t kCacheBytes = 256 << 20;  // the last-level cache
 inline int64_t mx_code_bytes(int64_t cols) { return (cols + 31) / 32 * 16; }
 inline int64_t mx_words(int64_t cols) { return (cols + 127) / 128; }  // scale words of a row
 
@@ -59,7 +60,7 @@ struct NormArgs {
   uint16_t* h;  // the sum (with r only)
   int64_t ldh;
   const void* w;  // 16-bit or fp32, or NULL: ones
-  bool w32, bf16;
+  bool w32, bf16, stream;  // stream: set by the launch
   double eps, inv_cols;  // inv_cols: 1 / cols
   int64_t rows;
   int cols;

@@ -37,7 +37,6 @@ typedef float floatx16 __attribute__((ext_vector_type(16)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 
 constexpr int kFp4 = 4;  // the instruction's code for the format e2m1
-constexpr int64_t kCacheBytes = 256 << 20;  // the last-level cache
 
 __device__ __forceinline__ int32x8 operand(const int32x4& a) {  // 32 elements; the rest is not read
   return int32x8{a[0], a[1], a[2], a[3], 0, 0, 0, 0};

@@ -3,10 +3,9 @@
 // Pages: "AWQ" scholia-log notes §2.3 (a group's range sets its step, values round to the grid), §4.3
 // (S^-1 folded into the activations).  The format is the OCP microscaling one: see mx_format.h.
 //
-// Bound by memory: 2 bytes of every value in, 17/32 out.  A block takes 16 rows of 512 columns, each
-// wave four rows one after another with its 512 columns, so that loads are 1 KiB in one
-// piece, the fold's scales are loaded once for four rows, and the scale words of 16 rows fill 64
-// contiguous bytes.
+// Bound by memory: 2 bytes of every value in, 17/32 out.  A block takes 8 rows of 512 columns, each
+// wave two rows with its 512 columns, so that loads are 1 KiB in one piece and the fold's scales
+// serve two rows.  28672 rows of 8192 times scales 106-124 us (595 MB, 4.8-5.6 TB/s), back 92-95 us.
 #include <hip/hip_runtime.h>
 
 #include "grid.h"
@@ -18,7 +17,9 @@ namespace awq {
 
 namespace {
 
-constexpr int kRowsTile = 16;  // rows a block
+// Rows a block, in us at 4, 8, 16 and 32: 333 rows of 13824 divided by scales 6.2, 6.1, 6.9, 8.4; 28672 of
+// 8192 times scales 129, 120, 125, 131; read back 110, 99, 95, 110.
+constexpr int kRowsTile = 8, kValuesTile = 16;
 constexpr int kTileWords = 4;  // scale words (128 columns) of a row a block
 
 // FOLD: kFoldNone, kFoldDivide or kFoldMultiply.
@@ -70,13 +71,13 @@ __global__ __launch_bounds__(256) void k_mxfp4_values(const uint8_t* __restrict_
                                                       int64_t ldo, unsigned tiles_k) {
   const unsigned b = block_number();
   const unsigned tr = b / tiles_k, tk = b - tr * tiles_k;
-  if (tr * kRowsTile >= rows) return;
+  if (tr * kValuesTile >= rows) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c0 = (int)(tk * (kTileWords * 128)) + 8 * lane;
   if (c0 >= K) return;
 #pragma unroll
-  for (int i = 0; i < kRowsTile / 4; ++i) {
-    const unsigned row = tr * kRowsTile + 4 * i + wave;
+  for (int i = 0; i < kValuesTile / 4; ++i) {
+    const unsigned row = tr * kValuesTile + 4 * i + wave;
     if (row >= rows) return;
     const uint32_t c = *(const uint32_t*)(codes + (int64_t)row * ldc + (c0 >> 1));
     const uint32_t word = scales[(int64_t)(c0 >> 7) * lds + row];
@@ -101,13 +102,13 @@ __global__ __launch_bounds__(256) void k_int8_values(const int8_t* __restrict__ 
                                                      unsigned tiles_k) {
   const unsigned b = block_number();
   const unsigned tr = b / tiles_k, tk = b - tr * tiles_k;
-  if (tr * kRowsTile >= rows) return;
+  if (tr * kValuesTile >= rows) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c0 = (int)(tk * (kTileWords * 128)) + 8 * lane;
   if (c0 >= K) return;
 #pragma unroll
-  for (int i = 0; i < kRowsTile / 4; ++i) {
-    const unsigned row = tr * kRowsTile + 4 * i + wave;
+  for (int i = 0; i < kValuesTile / 4; ++i) {
+    const unsigned row = tr * kValuesTile + 4 * i + wave;
     if (row >= rows) return;
     const uint2 c = *(const uint2*)(codes + (int64_t)row * ldc + c0);
     const float st = steps[row];
@@ -121,15 +122,15 @@ __global__ __launch_bounds__(256) void k_int8_values(const int8_t* __restrict__ 
   }
 }
 
-int64_t tiles(int64_t rows, int64_t cols) {
-  return (rows + kRowsTile - 1) / kRowsTile * ((cols + kTileWords * 128 - 1) / (kTileWords * 128));
+int64_t tiles(int64_t rows, int64_t cols, int tile) {
+  return (rows + tile - 1) / tile * ((cols + kTileWords * 128 - 1) / (kTileWords * 128));
 }
 unsigned col_tiles(int cols) { return (unsigned)((cols + kTileWords * 128 - 1) / (kTileWords * 128)); }
 
 }  // namespace
 
-int64_t mxfp4_rows_blocks(int64_t rows, int64_t cols) { return tiles(rows, cols); }
-int64_t values_blocks(int64_t rows, int64_t cols) { return tiles(rows, cols); }
+int64_t mxfp4_rows_blocks(int64_t rows, int64_t cols) { return tiles(rows, cols, kRowsTile); }
+int64_t values_blocks(int64_t rows, int64_t cols) { return tiles(rows, cols, kValuesTile); }
 
 hipError_t launch_mxfp4_rows(const void* A, int64_t rows, int cols, int64_t lda, bool bf16,
                              const float* s, int fold, uint8_t* codes, int64_t ld_codes,
@@ -137,7 +138,7 @@ hipError_t launch_mxfp4_rows(const void* A, int64_t rows, int cols, int64_t lda,
   if (rows <= 0 || cols <= 0) return hipSuccess;
   const int f = s ? fold : kFoldNone;
 #define AWQ_MXROWS(B, F)                                                                     \
-  hipLaunchKernelGGL((k_mxfp4_rows<B, F>), grid_of(tiles(rows, cols)), dim3(256), 0, stream, \
+  hipLaunchKernelGGL((k_mxfp4_rows<B, F>), grid_of(mxfp4_rows_blocks(rows, cols)), dim3(256), 0, stream, \
                      (const uint16_t*)A, (unsigned)rows, cols, lda, s, codes, ld_codes, scales, \
                      ld_scales, col_tiles(cols))
 #define AWQ_MXROWS_F(B)                                    \
@@ -158,7 +159,7 @@ hipError_t launch_mxfp4_values(const uint8_t* codes, int64_t ld_codes, const uin
                                int64_t ld_scales, int64_t rows, int cols, bool bf16, void* out,
                                int64_t ldo, hipStream_t stream) {
   if (rows <= 0 || cols <= 0) return hipSuccess;
-  const dim3 grid = grid_of(tiles(rows, cols));
+  const dim3 grid = grid_of(values_blocks(rows, cols));
   if (bf16)
     hipLaunchKernelGGL((k_mxfp4_values<true>), grid, dim3(256), 0, stream, codes, ld_codes, scales,
                        ld_scales, (unsigned)rows, cols, (uint16_t*)out, ldo, col_tiles(cols));
@@ -171,7 +172,7 @@ hipError_t launch_mxfp4_values(const uint8_t* codes, int64_t ld_codes, const uin
 hipError_t launch_int8_values(const int8_t* codes, int64_t ld_codes, const float* steps, int64_t rows,
                               int cols, bool bf16, void* out, int64_t ldo, hipStream_t stream) {
   if (rows <= 0 || cols <= 0) return hipSuccess;
-  const dim3 grid = grid_of(tiles(rows, cols));
+  const dim3 grid = grid_of(values_blocks(rows, cols));
   if (bf16)
     hipLaunchKernelGGL((k_int8_values<true>), grid, dim3(256), 0, stream, codes, ld_codes, steps,
                        (unsigned)rows, cols, (uint16_t*)out, ldo, col_tiles(cols));
