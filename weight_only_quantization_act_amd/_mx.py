@@ -3,6 +3,10 @@
 
 Every tensor of a call has to be on one device, which is made the current one for the call if it
 is not.
+
+Short calls are at the host's pace, so the usual case (tensors of the current device, outputs allocated,
+the current stream) goes through one step of native code, the extension module _calls
+(csrc/python/calls.cpp).  What that does not take (it returns None) is checked and called from here.
 """
 from __future__ import annotations
 
@@ -15,18 +19,30 @@ from ._lib import _check
 from ._serve import (AWQ_FOLD_DIVIDE, AWQ_FOLD_MULTIPLY, AWQ_FP32, _FP32, _I8, _U8, _dtype,
                      _round16, _workspace, lib)
 
-# Short calls are at the host's pace, so the usual case (contiguous tensors of the current device) is
-# told by a few cheap tests in place, and only what they do not cover goes through the full checks.
 _empty = torch.empty_strided
 _device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _C = None
+_N = None
 
 
 def _lib():
     global _C
     _C = lib()
     return _C
+
+
+def _native():
+    """The extension module, after the library that it calls."""
+    global _N
+    lib()
+    try:
+        from . import _calls
+    except ImportError as e:
+        raise RuntimeError("the extension module _calls is missing or does not fit this interpreter: build it "
+                           "with `python -m weight_only_quantization_act_amd.build`") from e
+    _N = _calls
+    return _N
 
 
 def _elsewhere(fn, stream, first, *args, **kwargs):
@@ -51,9 +67,6 @@ def _away(t, dev: int) -> bool:
 
 def _matrix(t: torch.Tensor, name: str, dtype: Optional[torch.dtype], dev: int) -> int:
     """Check a 2-D tensor on the call's device with unit stride along its rows; returns the row stride."""
-    if (isinstance(t, torch.Tensor) and t.get_device() == dev and t.is_contiguous() and t.dim() == 2
-            and (dtype is None or t.dtype is dtype)):
-        return t.shape[1]
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -76,9 +89,6 @@ def _matrix(t: torch.Tensor, name: str, dtype: Optional[torch.dtype], dev: int) 
 
 def _vector(t: torch.Tensor, dtype: torch.dtype, name: str, n: int, dev: int) -> int:
     """Check a contiguous vector of n elements on the call's device; returns its address."""
-    if (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.shape == (n,)
-            and t.is_contiguous()):
-        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda or t.get_device() != dev:
@@ -138,6 +148,10 @@ def awq_int8_dequantize(codes: torch.Tensor, steps: torch.Tensor, cols: int,
                         stream=None):
     """The values [R, cols] in dtype (fp16 or bf16) that 8-bit rows stand for: codes int8 [R, cols rounded
     up to 16] (as awq_int8_quantize and awq_rmsnorm_int8 make them) times steps fp32 [R]."""
+    if out is None and stream is None:
+        y = (_N or _native()).int8_dequantize(codes, steps, cols, dtype)
+        if y is not None:
+            return y
     dev = _device()
     if stream is not None or _away(codes, dev):
         return _elsewhere(awq_int8_dequantize, stream, codes, steps, cols, dtype, out)
@@ -162,12 +176,17 @@ def awq_mxfp4_quantize(A: torch.Tensor, s: Optional[torch.Tensor] = None, fold: 
     """Rows of A (fp16 or bf16 [R, K]) in MXFP4: codes uint8 [R, 16 ceil(K / 32)], two columns a byte, and
     scales uint8 [ceil(K / 128), R rounded up to 4, 4] (see awq_serve.h for both).  With s (fp32 [K])
     the values are A / s (fold="divide", activations) or A * s (fold="multiply", weights)."""
+    multiply = _fold(fold) == AWQ_FOLD_MULTIPLY
+    if stream is None:
+        got = (_N or _native()).mxfp4_quantize(A, s, multiply)
+        if got is not None:
+            return got
     dev = _device()
     if stream is not None or _away(A, dev):
         return _elsewhere(awq_mxfp4_quantize, stream, A, s, fold)
     lda = _matrix(A, "A", None, dev)
     dt = _dtype(A.dtype, "A")
-    f = _fold(fold)
+    f = AWQ_FOLD_MULTIPLY if multiply else AWQ_FOLD_DIVIDE
     R, K = A.shape
     ps = None if s is None else _vector(s, _FP32, "s", K, dev)
     codes, scales = _new_codes(R, K, A.device)
@@ -184,6 +203,10 @@ def awq_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: int,
                          dtype: torch.dtype = torch.float16, out: Optional[torch.Tensor] = None, *,
                          stream=None):
     """The values [R, cols] in dtype (fp16 or bf16) that MXFP4 codes and scales stand for."""
+    if out is None and stream is None:
+        y = (_N or _native()).mxfp4_dequantize(codes, scales, cols, dtype)
+        if y is not None:
+            return y
     dev = _device()
     if stream is not None or _away(codes, dev):
         return _elsewhere(awq_mxfp4_dequantize, stream, codes, scales, cols, dtype, out)
@@ -212,6 +235,10 @@ def awq_mxfp4_matmul(xc: torch.Tensor, xs: torch.Tensor, wc: torch.Tensor, ws: t
                      out: Optional[torch.Tensor] = None, *, stream=None):
     """y [T, M] = x w^T (+ bias) in `dtype` for MXFP4 codes and scales of tokens (xc, xs) and weights
     (wc, ws), as awq_mxfp4_quantize and awq_rmsnorm_mxfp4 make them."""
+    if out is None and stream is None:
+        y = (_N or _native()).mxfp4_matmul(xc, xs, wc, ws, dtype, bias)
+        if y is not None:
+            return y
     dev = _device()
     if stream is not None or _away(xc, dev):
         return _elsewhere(awq_mxfp4_matmul, stream, xc, xs, wc, ws, dtype, bias, out)
@@ -241,6 +268,10 @@ def awq_mxfp4_linear(x: torch.Tensor, wc: torch.Tensor, ws: torch.Tensor,
     """y [T, M] in x's type: each token of x (fp16 or bf16 [T, K]) divided by s (fp32 [K], if given),
     quantised to MXFP4 and multiplied with the weight's codes and scales wc, ws (as
     awq_mxfp4_quantize(W, s, "multiply") makes them)."""
+    if out is None and workspace is None and stream is None:
+        y = (_N or _native()).mxfp4_linear(x, wc, ws, s, bias)
+        if y is not None:
+            return y
     dev = _device()
     if stream is not None or _away(x, dev):
         return _elsewhere(awq_mxfp4_linear, stream, x, wc, ws, s, bias, out, workspace)
@@ -299,6 +330,10 @@ def awq_rmsnorm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: flo
     x's type (x itself without a residual) and y = h weight / sqrt(mean h^2 + eps) in x's type.
     weight [K] is fp32 or of x's type (None: ones); the scales of a search are folded into it (weight
     / s).  h goes to h_out if given, which may be the residual or x itself; out receives y."""
+    if h_out is None and out is None and stream is None:
+        got = (_N or _native()).rmsnorm(x, weight, eps, residual)
+        if got is not None:
+            return got
     dev = _device()
     if stream is not None or _away(x, dev):
         return _elsewhere(awq_rmsnorm, stream, x, weight, eps, residual=residual, h_out=h_out, out=out)
@@ -316,6 +351,10 @@ def awq_rmsnorm_int8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps
                      stream=None):
     """The same norm as rows of 8-bit integers: returns (codes, steps, h), codes int8 [R, K rounded up to
     16] and steps fp32 [R] as awq_int8_matmul takes them."""
+    if h_out is None and stream is None:
+        got = (_N or _native()).rmsnorm_int8(x, weight, eps, residual)
+        if got is not None:
+            return got
     dev = _device()
     if stream is not None or _away(x, dev):
         return _elsewhere(awq_rmsnorm_int8, stream, x, weight, eps, residual=residual, h_out=h_out)
@@ -336,6 +375,10 @@ def awq_rmsnorm_mxfp4(x: torch.Tensor, weight: Optional[torch.Tensor] = None, ep
                       stream=None):
     """The same norm as rows of MXFP4: returns (codes, scales, h), codes and scales as awq_mxfp4_quantize
     gives them and awq_mxfp4_matmul takes them."""
+    if h_out is None and stream is None:
+        got = (_N or _native()).rmsnorm_mxfp4(x, weight, eps, residual)
+        if got is not None:
+            return got
     dev = _device()
     if stream is not None or _away(x, dev):
         return _elsewhere(awq_rmsnorm_mxfp4, stream, x, weight, eps, residual=residual, h_out=h_out)

@@ -3,7 +3,9 @@
     python -m weight_only_quantization_act_amd.build
 
 Compiles every .hip file under csrc/ with hipcc for gfx950 and the host-only C ABI
-(api.cpp), then links one shared library next to this file.  Always recompiles.
+(api.cpp), then links one shared library next to this file, and an extension module of this
+interpreter on top of it (csrc/python/, the short way from a Python call to the C ABI).  Always
+recompiles.
 """
 from __future__ import annotations
 
@@ -12,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -42,6 +45,17 @@ HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__",
               f"-I{ROCM}/include"]
 
 
+# The extension module: its header files are torch's and Python's.
+CALLS = os.path.join(PKG, "_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
+
+
+def _torch_dirs():
+    import torch
+    at = os.path.dirname(torch.__file__)
+    return ([os.path.join(at, "include"), os.path.join(at, "include", "torch", "csrc", "api", "include")],
+            os.path.join(at, "lib"), int(torch.compiled_with_cxx11_abi()))
+
+
 def _run(cmd):
     res = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
     out = "\n".join(l for l in res.stdout.splitlines()
@@ -69,17 +83,26 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
                               "-o", obj])
         elif f.endswith(".cpp"):
             jobs_list.append([clangxx, *HOST_FLAGS, *incs, "-c", src, "-o", obj])
+    dirs, torch_lib, abi = _torch_dirs()
+    calls_obj = os.path.join(BUILD, "calls.cpp.o")
+    calls = [clangxx, *HOST_FLAGS, "-DUSE_ROCM", f"-D_GLIBCXX_USE_CXX11_ABI={abi}", *incs,
+             f"-I{sysconfig.get_path('include')}", *(f"-isystem{d}" for d in dirs), "-c",
+             os.path.join(CSRC, "python", "calls.cpp"), "-o", calls_obj]
+    jobs_list.append(calls)
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
         outs = list(ex.map(_run, jobs_list))
     if verbose:
         for o in outs:
             if o.strip():
                 print(o)
-    objs = [cmd[-1] for cmd in jobs_list]
+    objs = [cmd[-1] for cmd in jobs_list if cmd is not calls]
     tmp = lib_path() + ".tmp"
     _run([hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp,
           f"-L{ROCM}/lib", "-lamdhip64"])
     os.replace(tmp, lib_path())
+    _run([clangxx, "-shared", "-fPIC", calls_obj, "-o", CALLS + ".tmp", f"-L{torch_lib}", "-ltorch_python",
+          "-ltorch_cpu", "-ltorch_hip", "-lc10", "-lc10_hip", f"-L{PKG}", f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN"])
+    os.replace(CALLS + ".tmp", CALLS)
     if verbose:
         print("built", lib_path())
     return lib_path()
