@@ -216,11 +216,11 @@ __global__ __launch_bounds__(S::THREADS) void k_mxfp4_tiles(MxArgs a, int tiles_
 #pragma unroll
       for (int j = 0; j < S::PER; ++j) dma_piece(st, st, j);
     __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<(NS - 1) * S::PER>::value);
-    __builtin_amdgcn_s_barrier();
+    if constexpr (S::WAVES > 1) __builtin_amdgcn_s_barrier();
   };
   auto landed = [&] {  // the step after this one's
     __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<(NS - 2) * S::PER>::value);
-    __builtin_amdgcn_s_barrier();
+    if constexpr (S::WAVES > 1) __builtin_amdgcn_s_barrier();
   };
   if (n_steps == 0) {
   } else if constexpr (S::TI * S::MI == 1) {
@@ -563,6 +563,8 @@ hipError_t launch_few(const MxFewArgs& f, hipStream_t stream) {
 template <bool BF16>
 hipError_t launch_form(const MxArgs& a, int form, hipStream_t stream) {
   switch (form) {
+    case kMxTile32K: return launch_tiles<MxTile<32, 32, 1, 1, 4, 4>, BF16>(a, stream);
+    case kMxTile32x64K: return launch_tiles<MxTile<32, 64, 1, 2, 2, 3>, BF16>(a, stream);
     case kMxTile64K: return launch_tiles<MxTile<64, 64, 2, 2, 2, 3>, BF16>(a, stream);
     case kMxTile64: return launch_tiles<MxTile<64, 64, 2, 2, 1, 3>, BF16>(a, stream);
     case kMxTile64x128: return launch_tiles<MxTile<64, 128, 2, 4, 1, 3>, BF16>(a, stream);

@@ -6,39 +6,44 @@
 
 namespace awq {
 
-// Weights streamed through registers (few tokens); tiles by tokens x outputs, "K" with two groups of
-// waves that share the columns.
-enum { kMxFew, kMxTile64K, kMxTile64, kMxTile64x128, kMxTile128, kMxTile256 };
+// Weights streamed through registers (few tokens); tiles by tokens x outputs, "K" with groups of waves that
+// share the columns.
+enum { kMxFew, kMxTile32K, kMxTile32x64K, kMxTile64K, kMxTile64, kMxTile64x128, kMxTile128, kMxTile256 };
 
 // KB: bytes of codes a row (two columns a byte).
 //
 // Few: one round of blocks of 16 outputs, two blocks a compute unit, while the tokens' operands, which
-// every block reads, stay small beside the weights.  Measured, streaming and tiles of 64, in us:
+// every block reads, stay small beside the weights.  Measured, streaming and the best tiles, in us:
 //   tokens              1            16
-//   4096 x 4096         4.1,  6.8    4.7,  6.9
-//   4096 x 11008        6.2, 10.6    8.1, 10.8
-//   5120 x 13824        11.0, 12.8   15.7, 13.0
-//   11008 x 4096        6.6,  7.0    8.2,  6.9
+//   4096 x 4096         4.1,  5.4    4.4,  5.4
+//   4096 x 11008        6.2,  7.9    8.1,  8.0
+//   5120 x 13824        11.0, 9.3    15.7, 9.3
+//   11008 x 4096        6.6,  6.4    8.2,  6.4
 //   28672 x 8192        28.4, 20.0   32.9, 20.5
 //
 // Tiles: the form with the smallest time a step of 256 columns, fitted to measurements (us a step at r
-// tiles a compute unit; a tile alone waits for its memory, 128 x 128 ones run in rounds of two a
-// compute unit, 256 x 256 ones of one):
-//   tiles of 64 x 64    0.28 up to r = 1, 0.56 at 2, 0.68 at 2.7, 2.4 at 10.8
+// tiles a compute unit; small tiles are bound by what goes through LDS, 128 x 128 ones run in rounds of two
+// a compute unit, 256 x 256 ones of one):
+//   tiles of 64 x 64    0.22-0.28 up to r = 1, 0.56 at 2, 0.68 at 2.7, 2.4 at 10.8
 //            64 x 128   0.37-0.42 up to r = 1, 0.7 at 1.3, 1.15 at 2.7, 2.2 at 5.4
 //            128 x 128  0.56-0.7 up to r = 1, 0.94-1.1 at 1 to 1.3, 1.95 at 2 to 2.7
 //            256 x 256  1.4-1.5 up to r = 1, 1.8-2.0 a round beyond
 // Between neighbours, in us, 64 x 64, 64 x 128, 128 x 128, 256 x 256: 333 tokens of 5120 x 13824 24.2,
 // 22.3, 38, 69; 512 of 11008 x 4096 23.1, 20.9, 20.0, 26.8; 1024 of 11008 x 4096 40.6, 38.2, 33.7, 30.1;
 // 4096 of 11008 x 4096 165, 145, 109, 97.
-// Tiles of 64 that leave one a compute unit have two groups of waves (17 tokens of 5120 x 13824 16.8 ->
-// 13.0 us); where there are more, the second tile does as much (100 tokens of 11008 x 4096 9.6, 12.4).
+// Where tiles leave at most one a compute unit, groups of waves share the columns of one (17 tokens of
+// 5120 x 13824 on 64 x 64: one group 16.8, two 13.0) and the smallest tiles that fit are the fastest: 16
+// tokens of 5120 x 13824 on 32 x 32 in four groups 9.3, 32 x 64 in two 11.7, 64 x 64 in two 12.8; 50 of
+// 4096 x 4096 5.6, 6.4, 6.7; with more than one a unit they are not (50 of 11008 x 4096 12.6, 8.7, 7.1; 100
+// of it 64 x 64 in two groups 12.4, one 9.6).
 inline int mxfp4_form(int64_t T, int64_t M, int64_t KB) {
-  if (T <= 16 && M <= 8192 && M * KB * (T + 16) <= (int64_t)3 << 28) return kMxFew;
+  if (T <= 16 && M <= 8192 && M * KB * (T + 16) <= (int64_t)1 << 29) return kMxFew;
   auto per_unit = [&](int64_t bt, int64_t bm) {
     return (double)(((T + bt - 1) / bt) * ((M + bm - 1) / bm)) / 256.0;
   };
   auto rounds = [](double r) { return (double)(int64_t)(r + 0.999999); };
+  if (per_unit(32, 32) <= 1) return kMxTile32K;
+  if (per_unit(32, 64) <= 1) return kMxTile32x64K;
   const double r1 = per_unit(64, 64), r2 = per_unit(64, 128), r3 = per_unit(128, 128), r4 = per_unit(256, 256);
   const double t1 = r1 <= 1 ? 0.27 : 0.1 + 0.24 * r1;
   const double t2 = r2 <= 1 ? 0.40 : 0.15 + 0.4 * r2;
