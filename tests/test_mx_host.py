@@ -188,7 +188,7 @@ def test_forms_are_covered(tmp_path):
 #include "mxfp4_plan.h"
 int main() {
   long long T, M, K;
-  const char* name[] = {"few", "32k", "32x64k", "64k", "64", "64x128", "128", "256"};
+  const char* name[] = {"few", "32k", "32x64k", "64k", "64", "64x128", "128w", "128", "256"};
   while (scanf("%lld %lld %lld", &T, &M, &K) == 3)
     printf("%s\\n", name[awq::mxfp4_form(T, M, (K + 31) / 32 * 16)]);
 }
@@ -199,4 +199,4 @@ int main() {
     sizes = "\n".join("%d %d %d" % s[1:] for s in SHAPES)
     out = subprocess.run([str(exe)], input=sizes, capture_output=True, text=True, check=True).stdout.split()
     assert out == [s[0] for s in SHAPES], [(s, f) for s, f in zip(SHAPES, out) if s[0] != f]
-    assert set(out) == {"few", "32k", "32x64k", "64k", "64", "64x128", "128", "256"}
+    assert set(out) == {"few", "32k", "32x64k", "64k", "64", "64x128", "128w", "128", "256"}

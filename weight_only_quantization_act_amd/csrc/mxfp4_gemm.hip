@@ -42,12 +42,13 @@ __device__ __forceinline__ int32x8 operand(const int32x4& a) {  // 32 elements; 
   return int32x8{a[0], a[1], a[2], a[3], 0, 0, 0, 0};
 }
 
-template <int BT_, int BM_, int WT_, int WM_, int KG_, int NS_>
+template <int BT_, int BM_, int WT_, int WM_, int KG_, int NS_, bool WHOLE_>
 struct MxTile {
   static constexpr int BT = BT_, BM = BM_, WT = WT_, WM = WM_;
   static constexpr int KG = KG_, NS = NS_;  // groups of waves, which take the steps in turn, stages of each
+  static constexpr bool WHOLE = WHOLE_;     // a stage's operands are read one stage ahead (else an instruction)
   static constexpr int BK = 128;            // bytes of K a stage
-  static constexpr int KS = 4;              // instructions along K a stage
+  static constexpr int KS = 4;
   static constexpr int WAVES = WT * WM, THREADS = 64 * WAVES * KG;
   static constexpr int TI = BT / WT / 32, MI = BM / WM / 32;
   static constexpr int X_BYTES = BT * BK, CODES = (BT + BM) * BK;
@@ -223,9 +224,10 @@ __global__ __launch_bounds__(S::THREADS) void k_mxfp4_tiles(MxArgs a, int tiles_
     if constexpr (S::WAVES > 1) __builtin_amdgcn_s_barrier();
   };
   if (n_steps == 0) {
-  } else if constexpr (S::TI * S::MI == 1) {
-    // One tile a wave: a step has too few products to hide its own reads, so a whole stage's operands
-    // are read during the products of the one before (50 tokens of 11008 x 4096 7.8 -> 7.2 us).
+  } else if constexpr (S::WHOLE) {
+    // One or two tiles a wave: a step has too few products to hide its own reads, so a whole stage's
+    // operands are read during the products of the one before (50 tokens of 11008 x 4096 on 64 x 64
+    // 7.8 -> 7.2 us; 512 of 5120 x 13824 on 128 x 128 in three stages, one block a unit, 43.5 -> 29.2).
     Frag f[2][4];
     Scales s[2];
     auto read = [&](int st, Frag (&to)[4], Scales& ts) {
@@ -563,13 +565,14 @@ hipError_t launch_few(const MxFewArgs& f, hipStream_t stream) {
 template <bool BF16>
 hipError_t launch_form(const MxArgs& a, int form, hipStream_t stream) {
   switch (form) {
-    case kMxTile32K: return launch_tiles<MxTile<32, 32, 1, 1, 4, 4>, BF16>(a, stream);
-    case kMxTile32x64K: return launch_tiles<MxTile<32, 64, 1, 2, 2, 3>, BF16>(a, stream);
-    case kMxTile64K: return launch_tiles<MxTile<64, 64, 2, 2, 2, 3>, BF16>(a, stream);
-    case kMxTile64: return launch_tiles<MxTile<64, 64, 2, 2, 1, 3>, BF16>(a, stream);
-    case kMxTile64x128: return launch_tiles<MxTile<64, 128, 2, 4, 1, 3>, BF16>(a, stream);
-    case kMxTile128: return launch_tiles<MxTile<128, 128, 4, 2, 1, 2>, BF16>(a, stream);
-    default: return launch_tiles<MxTile<256, 256, 4, 2, 1, 2>, BF16>(a, stream);
+    case kMxTile32K: return launch_tiles<MxTile<32, 32, 1, 1, 4, 4, true>, BF16>(a, stream);
+    case kMxTile32x64K: return launch_tiles<MxTile<32, 64, 1, 2, 2, 3, true>, BF16>(a, stream);
+    case kMxTile64K: return launch_tiles<MxTile<64, 64, 2, 2, 2, 3, true>, BF16>(a, stream);
+    case kMxTile64: return launch_tiles<MxTile<64, 64, 2, 2, 1, 3, true>, BF16>(a, stream);
+    case kMxTile64x128: return launch_tiles<MxTile<64, 128, 2, 4, 1, 3, true>, BF16>(a, stream);
+    case kMxTile128W: return launch_tiles<MxTile<128, 128, 4, 2, 1, 3, true>, BF16>(a, stream);
+    case kMxTile128: return launch_tiles<MxTile<128, 128, 4, 2, 1, 2, false>, BF16>(a, stream);
+    default: return launch_tiles<MxTile<256, 256, 4, 2, 1, 2, false>, BF16>(a, stream);
   }
 }
 
