@@ -161,6 +161,22 @@ def test_int8_values(dtype):
         assert _same(wide[:, 3:3 + K].contiguous(), want) and (wide[:, :3] == 3).all() and (wide[:, 3 + K:] == 3).all()
 
 
+def test_int8_values_are_rounded_twice():
+    """Steps whose products lie so close to a border of fp16 that fp32 rounds them onto it."""
+    say("int8 values at borders")
+    rng = np.random.default_rng(0)
+    steps = rng.uniform(0.001, 1, 1 << 22).astype(F32)
+    exact = steps.astype(F64) * 3
+    near = exact.astype(np.float16) != exact.astype(F32).astype(np.float16)
+    steps = steps[near]
+    assert steps.size > 50
+    q = torch.zeros(steps.size, 16, dtype=torch.int8, device="cuda")
+    q[:, 0], q[:, 15] = 3, -3
+    y = awq.awq_int8_dequantize(q, torch.from_numpy(steps).cuda(), 16)
+    want = torch.from_numpy((steps * F32(3)).astype(np.float16))
+    assert _same(y[:, 0].contiguous(), want) and _same(y[:, 15].contiguous(), -want)
+
+
 # ---------------------------------------------------------------------------------- product
 def _ulp(v, dtype):
     bits, emin = (10, -14) if dtype == torch.float16 else (7, -126)

@@ -118,6 +118,10 @@ __global__ __launch_bounds__(256) void k_int8_values(const int8_t* __restrict__ 
       v[j] = (float)(int8_t)(c.x >> (8 * j)) * st;
       v[j + 4] = (float)(int8_t)(c.y >> (8 * j)) * st;
     }
+    // the product is an fp32 number before it is rounded to the type: product and conversion would
+    // otherwise become one instruction that rounds once
+#pragma unroll
+    for (int j = 0; j < 8; ++j) asm volatile("" : "+v"(v[j]));
     store8(out + (int64_t)row * ldo, c0, K, pack8<BF16>(v));
   }
 }
