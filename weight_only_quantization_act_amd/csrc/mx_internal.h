@@ -60,7 +60,7 @@ struct NormArgs {
   uint16_t* h;  // the sum (with r only)
   int64_t ldh;
   const void* w;  // 16-bit or fp32, or NULL: ones
-  bool w32, bf16, stream;  // stream: set by the launch
+  bool w32, bf16;
   double eps, inv_cols;  // inv_cols: 1 / cols
   int64_t rows;
   int cols;

@@ -95,9 +95,7 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void k_rmsnorm(NormArgs 
 #pragma unroll
     for (int j = 0; j < 8; ++j) h[j] = h[j] + t[j];
     const u32x4 p = pack8<BF16>(h);
-    // a sum that no cache will hold is kept from pushing the rest out of it
-    if (a.stream && 8 * ch + 8 <= K) __builtin_nontemporal_store(p, (u32x4_at2*)(hrow + 8 * ch));
-    else store8(hrow, 8 * ch, K, p);
+    store8(hrow, 8 * ch, K, p);  // (stored past the caches, large sums cost the same, 16384 x 8192 2 % more)
     return p;
   };
   auto add = [&](const u32x4& p, const Weights<BF16, W32>& wv) {
@@ -250,10 +248,8 @@ hipError_t launch_out(const NormArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_rmsnorm(const NormArgs& args, hipStream_t stream) {
-  if (args.rows <= 0) return hipSuccess;
-  NormArgs a = args;
-  a.stream = a.r && a.rows * a.cols * 2 > kCacheBytes;
+hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t stream) {
+  if (a.rows <= 0) return hipSuccess;
 #define AWQ_NORM_OUT(B, W)                                             \
   a.out == kNormSame   ? launch_out<B, W, kNormSame>(a, stream)        \
   : a.out == kNormInt8 ? launch_out<B, W, kNormInt8>(a, stream)        \
