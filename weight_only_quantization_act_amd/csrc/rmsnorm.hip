@@ -7,9 +7,12 @@
 // Codes are decided at borders between values, so v is defined as the formula's value rounded to fp32
 // once: squares of 16-bit values are exact in fp64 and summed there, the product h w (11 + 24 bits) is
 // exact there, and v = fp32((h w) r) with r to within two ulp of fp64.  What of this is fp64 costs a few
-// instructions a value at fp32's rate; the call is bound by memory: each value is read once (and the
-// residual, and the sum written) and stays in registers between the sum and the rounding.  Rows too
-// long for that are read a second time, from cache.  The 8-bit row's step needs the largest |v|:
+// instructions a value at fp32's rate.  Each value is read once (and the residual, and the sum written)
+// and stays in registers between the sum and the rounding; rows too long for that are read a second
+// time, from cache.  Large calls are bound by memory (16384 rows of 8192 in bf16 with a residual to MXFP4
+// 168 us, 877 MB at 5.2 TB/s), calls of a few thousand rows by their vector instructions and one
+// pass of latencies (2047 rows of 5000 to MXFP4 11.4 us, 2.3 TB/s), few rows by the latencies alone (33 of
+// 5120 to 8 bits 4.6 us, one of 4096 2.4 us).  The 8-bit row's step needs the largest |v|:
 // rounding is monotone, so it is that of max |h w|, found beside the sum.
 #include <hip/hip_runtime.h>
 
@@ -53,6 +56,18 @@ struct Weights {
     }
   }
 };
+
+// The products of 8 fp16 values with 8 others, exact in fp32: one instruction from the packed halves (the
+// third operand is -0, which keeps the sign of a product of 0).  Conversions are most of the norm's vector
+// instructions: 2047 rows of 5000 to MXFP4 12.7 -> 11.4 us.
+__device__ __forceinline__ void products8(const u32x4& a, const u32x4& b, float (&p)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t x = a[j], y = b[j];
+    asm("v_fma_mix_f32 %0, %1, %2, neg(0) op_sel_hi:[1,1,0]" : "=v"(p[2 * j]) : "v"(x), "v"(y));
+    asm("v_fma_mix_f32 %0, %1, %2, neg(0) op_sel:[1,1,0] op_sel_hi:[1,1,0]" : "=v"(p[2 * j + 1]) : "v"(x), "v"(y));
+  }
+}
 
 // 1 / sqrt(x): the hardware's estimate e0 (relative error d, 2^-26 or so) and one step of third order,
 // y = e0 (1 + d + 3/2 d^2 ...) with 2 d = 1 - x e0^2; NaN for an infinite x.
@@ -105,10 +120,11 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void k_rmsnorm(NormArgs 
     for (int j = 0; j < 8; ++j) sum = fma((double)h[j], (double)h[j], sum);
     if constexpr (OUT == kNormInt8) {
       float w[8];
-      wv.values(w);
+      if constexpr (!BF16 && !W32) products8(p, wv.r[0], w);
+      else wv.values(w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const double v = (double)h[j] * (double)w[j];
+        const double v = !BF16 && !W32 ? (double)w[j] : (double)h[j] * (double)w[j];
         top = fmax(top, fabs(v));
         sum = fma(v, 0.0, sum);  // an infinite or NaN weight makes the row NaN
       }
@@ -182,11 +198,18 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void k_rmsnorm(NormArgs 
     if (tid == 0) ((float*)a.scales)[row] = st.step;
   }
   auto write = [&](int ch, const u32x4& p, const Weights<BF16, W32>& wp) {
-    float hc[8], wv[8], v[8];
-    values8<BF16>(p, hc);
-    wp.values(wv);
+    float v[8];
+    if constexpr (!BF16 && !W32) {
+      products8(p, wp.r[0], v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = (float)((double)hc[j] * (double)wv[j] * inv);
+      for (int j = 0; j < 8; ++j) v[j] = (float)((double)v[j] * inv);
+    } else {
+      float hc[8], wv[8];
+      values8<BF16>(p, hc);
+      wp.values(wv);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = (float)((double)hc[j] * (double)wv[j] * inv);
+    }
     if constexpr (OUT == kNormSame) {
       store8((uint16_t*)a.y + row * a.ldy, 8 * ch, K, pack8<BF16>(v));
     } else if constexpr (OUT == kNormInt8) {
