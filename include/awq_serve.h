@@ -206,7 +206,6 @@ int awq_kv4_attention(const void* q, int64_t q_token_stride, int64_t q_head_stri
  *   6 for all above it.  A block that holds a NaN or an infinity (also one that the fold makes) gets
  *   b = 255, which stands for NaN, and codes 0, so that whatever it is multiplied with is NaN.
  *   A           fp16 or bf16 [rows][cols], row stride lda >= cols elements; 2-byte aligned
- *               (16-byte loads are used where the base and lda allow them)
  *   s           fp32 [cols] or NULL
  *   codes       uint8 [rows][ld_codes], 16-byte aligned, ld_codes a multiple of 16, at least
  *               16 ceil(cols / 32) and below 2^22: column 2 j in the low half of byte j, a code is the
@@ -215,7 +214,7 @@ int awq_kv4_attention(const void* q, int64_t q_token_stride, int64_t q_head_stri
  *   scales      uint8 [ceil(cols / 128)][ld_scales][4], 16-byte aligned, ld_scales a multiple of 4, at
  *               least rows: byte c of (q, r) is b of block 4 q + c of row r (0 past the last block);
  *               rows past the last are not written
- * rows < 2^29 - 512 (and ld_scales), cols <= 2^22.
+ * rows and ld_scales at most 2^29 - 512, cols at most 2^22.
  * ---------------------------------------------------------------------------------- */
 int awq_mxfp4_quantize(const void* A, int64_t rows, int64_t cols, int64_t lda, int32_t dtype,
                        const float* s, int32_t fold, uint8_t* codes_out, int64_t ld_codes,
@@ -239,7 +238,7 @@ int awq_mxfp4_dequantize(const uint8_t* codes, int64_t ld_codes, const uint8_t* 
  *           Columns from in_features up to a whole block are read: they must be zero in one of the two
  *   bias    [out] in the output's type, or NULL
  *   y       fp16 or bf16 [n_tokens][ldy], ldy >= out
- * n_tokens, out_features < 2^29 - 512, in_features <= 2^22, n_tokens * ldx, out * ldw and
+ * n_tokens, out_features at most 2^29 - 512, in_features at most 2^22, n_tokens * ldx, out * ldw and
  * n_tokens * ldy below 2^47; 0 tokens or outputs enqueue nothing, in_features = 0 gives y = bias or 0.
  * ---------------------------------------------------------------------------------- */
 int awq_mxfp4_matmul(const uint8_t* xc, int64_t ldx, const uint8_t* xs, int64_t ldxs, int64_t n_tokens,

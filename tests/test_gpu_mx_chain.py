@@ -172,3 +172,95 @@ def test_two_calls_at_once():
         torch.cuda.synchronize()
         for k in (0, 1):
             assert _same(got[k], want[k]), (rep, k)
+
+
+def test_calls_from_threads():
+    """Threads of one process, a stream each: the short way into the calls frees the interpreter while it
+    enqueues."""
+    import threading
+    say("mxfp4 block from threads")
+    b = Block(520, 1000, 300, torch.float16, seed=4)
+    ins = [[torch.randn(t, 520, device="cuda").half() for _ in range(2)] for t in (1, 9, 64, 130)]
+    want = [b.forward(*i) for i in ins]
+    torch.cuda.synchronize()
+    bad = []
+
+    def run(k):
+        side = torch.cuda.Stream()
+        try:
+            for rep in range(20):
+                with torch.cuda.stream(side):
+                    got = b.forward(*ins[k])
+                side.synchronize()
+                if not _same(got, want[k]):
+                    bad.append((k, rep))
+        except Exception as e:  # noqa: BLE001  (a thread's error is the test's)
+            bad.append((k, repr(e)))
+
+    threads = [threading.Thread(target=run, args=(k,)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+def test_what_a_program_passes():
+    """Parameters, views, tensors of another mode, whole numbers for eps: all the same as plain tensors; rows that
+    overlap are refused."""
+    say("mxfp4 kinds of tensors")
+    x = torch.randn(7, 520, device="cuda").half()
+    w = (1 + 0.1 * torch.randn(520, device="cuda")).half()
+    want = awq.awq_rmsnorm(x, w, 1.0)
+    assert want[1] is x
+    p = torch.nn.Parameter(w)
+    wide = torch.randn(9, 3 * 520, device="cuda").half()
+    wide[1:8, 520:1040] = x
+    view = wide[1:8, 520:1040]
+    for got in (awq.awq_rmsnorm(x, p, 1.0), awq.awq_rmsnorm(x, w, 1), awq.awq_rmsnorm(view, w, 1.0),
+                awq.awq_rmsnorm(view, p, 1)):
+        assert torch.equal(got[0], want[0]) and not got[0].requires_grad
+    with torch.inference_mode():
+        got = awq.awq_rmsnorm(x + 0, w, 1.0)
+    assert torch.equal(got[0], want[0])
+    c, s = awq.awq_mxfp4_quantize(view)
+    c1, s1 = awq.awq_mxfp4_quantize(x)
+    assert torch.equal(c, c1) and torch.equal(s[:, :7], s1[:, :7])
+    one = x[:1].expand(5, 520)
+    for call in (lambda: awq.awq_rmsnorm(one), lambda: awq.awq_mxfp4_quantize(one),
+                 lambda: awq.awq_mxfp4_linear(one, c1, s1), lambda: awq.awq_rmsnorm_int8(x, residual=one)):
+        with pytest.raises(ValueError):
+            call()
+    # a row by itself, however far its neighbours would be
+    assert torch.equal(awq.awq_rmsnorm(wide[3:4, 520:1040], w, 1.0)[0], want[0][2:3])
+    # a prefix of the tokens' codes with the scales of all of them
+    wc, ws = awq.awq_mxfp4_quantize(torch.randn(33, 520, device="cuda").half())
+    y = awq.awq_mxfp4_matmul(c1, s1, wc, ws)
+    assert torch.equal(awq.awq_mxfp4_matmul(c1[:3], s1, wc, ws), y[:3])
+    assert torch.equal(awq.awq_mxfp4_matmul(c1, s1, wc[:5], ws), y[:, :5])
+    # both operands the same tensors
+    z = awq.awq_mxfp4_matmul(c1, s1, c1, s1)
+    assert torch.equal(z, z.t().contiguous()) and bool(torch.isfinite(z).all())
+
+
+def test_capture_of_calls_in_place():
+    """h written over the residual in a captured graph: each replay adds once more."""
+    say("norm in place, captured")
+    x = torch.full((5, 264), 0.5, device="cuda", dtype=torch.bfloat16)
+    r = torch.zeros(5, 264, device="cuda", dtype=torch.bfloat16)
+    awq.awq_rmsnorm_mxfp4(x, residual=r, h_out=r)
+    torch.cuda.synchronize()
+    r.zero_()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c, s, h = awq.awq_rmsnorm_mxfp4(x, residual=r, h_out=r)
+    assert h is r
+    for rep in range(1, 6):
+        g.replay()
+        torch.cuda.synchronize()
+        assert bool((r == 0.5 * rep).all())
+        v = awq.awq_mxfp4_dequantize(c, s, 264)
+        # v = h / sqrt(h^2 + 1e-6) = 1 - 5e-7 / h^2 for h up to 2.5: at most 1 - 8e-8, which fp32 (steps of 6e-8 there) keeps
+        # below 1, so the scale is 2^(-1 - 2) and v over it lies in (6, 8): the element is 6, the value 6 / 8
+        assert bool((v == 0.75).all()), rep
+    del g
