@@ -120,6 +120,26 @@ def test_rows_not_finite(dtype):
     _check_rows(A, s, "multiply")
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("R,K", [(3, 640), (40, 3200), (2050, 4096)])
+def test_divisions_at_borders(R, K, dtype):
+    """Quotients within three fp32 numbers of every border between two elements and of the borders of the scale,
+    where one wrong rounding of v / s is another code; scales at the ends of fp32."""
+    say(f"mxfp4 divisions {R}x{K} {dtype}")
+    rng = np.random.default_rng(R)
+    t = torch.from_numpy(rng.uniform(1, 2, (R, K)) * 2.0 ** rng.integers(-3, 4, (R, K))).to(DT[dtype])
+    border = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 4.0, 8.0])[rng.integers(0, 9, K)]
+    first = t[rng.integers(0, R, K), np.arange(K)].float().numpy()  # the row whose quotient lies at the border
+    s = (first / border).astype(F32)
+    for n in range(3):
+        s = np.where(rng.integers(0, 3, K) == n, np.nextafter(s, F32(rng.choice([0, 1e30]))), s)
+    t[:, ::32], s[::32] = 4.0, 1.0                              # scales of 1 or so
+    _check_rows(t.cuda(), torch.from_numpy(s).cuda(), "divide")
+    if R < 100:
+        for k in (-149, -140, -126, -100, 100, 127):
+            _check_rows(t.cuda(), torch.from_numpy(np.ldexp(s, k).astype(F32)).cuda(), "divide", k)
+
+
 def test_rows_strides():
     """Row strides and bases that rule the 16-byte loads out, strided views, padded codes."""
     base = torch.randn(40, 301, device="cuda").half()

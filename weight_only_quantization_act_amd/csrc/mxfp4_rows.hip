@@ -18,33 +18,57 @@ namespace awq {
 namespace {
 
 // Rows a block, in us at 4, 8, 16 and 32: 333 rows of 13824 divided by scales 6.2, 6.1, 6.9, 8.4; 28672 of
-// 8192 times scales 129, 120, 125, 131; read back 110, 99, 95, 110.
-constexpr int kRowsTile = 8, kValuesTile = 16;
+// 8192 times scales 129, 120, 125, 131; read back 110, 99, 95, 110.  Divided by scales, where a block has
+// their reciprocals to find first, and many rows 16: 28672 of 8192 at 8 and 16 158, 128, 4096 of 4096 11.4,
+// 10.5, but 333 of 13824 5.2 both, 50 of 4096 2.9, 3.5.
+constexpr int kRowsTile = 8, kDivideTile = 16, kValuesTile = 16;
 constexpr int kTileWords = 4;  // scale words (128 columns) of a row a block
 
+// 1 / s in fp64, to within 2^-52 of itself: the hardware's estimate y and a step of third order, 1/s = y (1 + e
+// + e^2 ...) with e = 1 - s y.  (1 / inf is y, a zero; of a zero it is NaN in place of an infinity, which
+// makes no difference to a block.)
+//
+// A 16-bit value v times it, rounded to fp32, is v / s rounded correctly: a border between two fp32
+// numbers is M 2^k with an odd M of 25 bits, s = S 2^l with S below 2^24 and v an integer of 11 bits times a
+// power of two, so v - s M 2^k is a multiple of a unit that s M 2^k holds less than 2^49 times, and not 0; v / s
+// lies 2^-49 or more of itself from every border, the product less than 2^-51 from v / s.  (Where the
+// result is subnormal a tie can be exact and come out either way; it is then an odd number of 11 bits times
+// 2^-150, which is far below the least element's border, 2^-129.)
+__device__ __forceinline__ double reciprocal(float s) {
+  const double d = (double)s, y = __builtin_amdgcn_rcp(d);
+  const double e = fma(-d, y, 1.0);
+  const double r = fma(y, fma(e, e, e), y);
+  return fabsf(s) == __builtin_inff() ? y : r;
+}
+
 // FOLD: kFoldNone, kFoldDivide or kFoldMultiply.
-template <bool BF16, int FOLD>
+template <bool BF16, int FOLD, int TILE>
 __global__ __launch_bounds__(256) void k_mxfp4_rows(const uint16_t* __restrict__ A, unsigned rows,
                                                     int K, int64_t lda, const float* __restrict__ s,
                                                     uint8_t* __restrict__ codes, int64_t ldc,
                                                     uint32_t* __restrict__ scales, int64_t lds,
                                                     unsigned tiles_k) {
-  constexpr int R = kRowsTile / 4;  // rows a wave
+  constexpr int R = TILE / 4;  // rows a wave
   const unsigned b = block_number();
   const unsigned tr = b / tiles_k, tk = b - tr * tiles_k;
-  if (tr * kRowsTile >= rows) return;  // the whole block
+  if (tr * TILE >= rows) return;  // the whole block
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c0 = (int)(tk * (kTileWords * 128)) + 8 * lane;
   const int q = c0 >> 7;
   if (q >= (K + 127) >> 7) return;  // sixteen lanes together; no barrier follows
   const bool stored = c0 < (K + 31) / 32 * 32;
-  const unsigned row0 = tr * kRowsTile + R * wave;
+  const unsigned row0 = tr * TILE + R * wave;
   // all rows' loads before the first is used; rows past the last repeat it
   u32x4 raw[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) raw[i] = raw8(A + (int64_t)min(row0 + i, rows - 1) * lda, c0, K);
   float sv[8];
   if constexpr (FOLD != kFoldNone) floats8(s, c0, K, 1.0f, sv);
+  double inv[8];
+  if constexpr (FOLD == kFoldDivide) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) inv[j] = reciprocal(sv[j]);
+  }
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const unsigned row = row0 + i;
@@ -54,7 +78,7 @@ __global__ __launch_bounds__(256) void k_mxfp4_rows(const uint16_t* __restrict__
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       if constexpr (FOLD == kFoldMultiply) v[j] = v[j] * sv[j];
-      if constexpr (FOLD == kFoldDivide) v[j] = v[j] / sv[j];
+      if constexpr (FOLD == kFoldDivide) v[j] = (float)((double)v[j] * inv[j]);
     }
     uint32_t byte;
     const uint32_t c = mx_codes8(v, byte);
@@ -133,6 +157,7 @@ unsigned col_tiles(int cols) { return (unsigned)((cols + kTileWords * 128 - 1) /
 
 }  // namespace
 
+// (at most: the largest of its forms)
 int64_t mxfp4_rows_blocks(int64_t rows, int64_t cols) { return tiles(rows, cols, kRowsTile); }
 int64_t values_blocks(int64_t rows, int64_t cols) { return tiles(rows, cols, kValuesTile); }
 
@@ -141,14 +166,16 @@ hipError_t launch_mxfp4_rows(const void* A, int64_t rows, int cols, int64_t lda,
                              uint32_t* scales, int64_t ld_scales, hipStream_t stream) {
   if (rows <= 0 || cols <= 0) return hipSuccess;
   const int f = s ? fold : kFoldNone;
-#define AWQ_MXROWS(B, F)                                                                     \
-  hipLaunchKernelGGL((k_mxfp4_rows<B, F>), grid_of(mxfp4_rows_blocks(rows, cols)), dim3(256), 0, stream, \
+  const bool many = tiles(rows, cols, kDivideTile) >= 1024;  // (four blocks a compute unit)
+#define AWQ_MXROWS(B, F, TILE)                                                               \
+  hipLaunchKernelGGL((k_mxfp4_rows<B, F, TILE>), grid_of(tiles(rows, cols, TILE)), dim3(256), 0, stream, \
                      (const uint16_t*)A, (unsigned)rows, cols, lda, s, codes, ld_codes, scales, \
                      ld_scales, col_tiles(cols))
-#define AWQ_MXROWS_F(B)                                    \
-  if (f == kFoldNone) AWQ_MXROWS(B, kFoldNone);            \
-  else if (f == kFoldDivide) AWQ_MXROWS(B, kFoldDivide);   \
-  else AWQ_MXROWS(B, kFoldMultiply)
+#define AWQ_MXROWS_F(B)                                                    \
+  if (f == kFoldNone) AWQ_MXROWS(B, kFoldNone, kRowsTile);                 \
+  else if (f == kFoldMultiply) AWQ_MXROWS(B, kFoldMultiply, kRowsTile);    \
+  else if (many) AWQ_MXROWS(B, kFoldDivide, kDivideTile);                  \
+  else AWQ_MXROWS(B, kFoldDivide, kRowsTile)
   if (bf16) {
     AWQ_MXROWS_F(true);
   } else {
