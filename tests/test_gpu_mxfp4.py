@@ -369,6 +369,29 @@ def test_linear_is_quantise_then_product(dtype, smooth):
         _check_product(y[ok], codes, some, wc, ws, K, bias, (T, M, K))
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("smooth", [False, True])
+@pytest.mark.parametrize("K", [1, 250, 1001, 1024, 4096])
+def test_linear_in_one_launch(K, smooth, dtype):
+    """Few tokens times few columns: quantised inside the product, in groups of tokens, the last one short."""
+    W = torch.randn(70, K, device="cuda").to(DT[dtype])
+    s = torch.exp(torch.randn(K, device="cuda")) if smooth else None
+    wc, ws = awq.awq_mxfp4_quantize(W, s, "multiply")
+    for T in (1, 2, 3, 4, 5, 7, 8, 9, 16):
+        if T * K > 16384:
+            continue
+        say(f"mxfp4 linear in one launch T={T} K={K} {dtype} smooth={smooth}")
+        assert awq.awq_mxfp4_linear_workspace_bytes(T, 70, K) == 0
+        wide = torch.randn(T, K + 5, device="cuda").to(DT[dtype])
+        x = wide[:, 3:3 + K]
+        x[T // 2, K // 2] = float("nan") if T % 2 else 1e4
+        xc, xs = awq.awq_mxfp4_quantize(x, s, "divide")
+        want = awq.awq_mxfp4_matmul(xc, xs, wc, ws, dtype=DT[dtype])
+        assert _same(awq.awq_mxfp4_linear(x, wc, ws, s=s), want)
+        if T % 2:
+            assert want[T // 2].isnan().all() and int(want.isnan().sum()) == 70
+
+
 def test_linear_on_another_stream():
     """Work follows the given stream: inputs made on a side stream are read after it."""
     side = torch.cuda.Stream()

@@ -401,22 +401,23 @@ __global__ __launch_bounds__(S::THREADS) void k_mxfp4_tiles(MxArgs a, int tiles_
 // One token through 4096 x 4096 with its quantisation 4.6 us (9 MB: 1.9 TB/s with start and end of the
 // launch); the product alone 4.1 us, of 16 tokens 4.4 (tiles 5.4).
 //
-// FUSED: the block first quantises the tokens into LDS, with the first weights already on their way;
-// every block repeats that (a few thousand values from L2) in place of a launch before this one.
+// FUSED > 0: the block first quantises the tokens into LDS, a lane 8 columns of so many tokens together, with
+// the first weights already on their way; every block repeats that (a few thousand values from L2) in place of
+// a launch before this one.
 constexpr int kFewWaves = 8;
 
 struct MxFewArgs {
   MxArgs g;
-  const uint16_t* x16;  // FUSED: the tokens, their scales, columns and row stride
+  const uint16_t* x16;  // FUSED > 0: the tokens, their scales, columns and row stride
   const float* s;
   int64_t ldx16;
   int cols;
 };
 
-template <bool FUSED, bool BF16>
+template <int FUSED, bool BF16>
 __global__ __launch_bounds__(64 * kFewWaves) void k_mxfp4_few(MxFewArgs f) {
   const MxArgs& a = f.g;
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // FUSED: codes [T][pieces 256], words [T][4 pieces]
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // FUSED > 0: codes [T][pieces 256], words [T][4 pieces]
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, q = lane >> 4;
@@ -444,24 +445,40 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mxfp4_few(MxFewArgs f) {
   if (wave < nch) load_w(p0, wave);
 
   uint32_t* const lwords = (uint32_t*)(lds + (size_t)a.T * nch * 256);
-  if constexpr (FUSED) {
+  if constexpr (FUSED > 0) {
     const int n8 = nch * 64;  // 8-column chunks of whole pieces
-    for (int i = tid; i < a.T * n8; i += 64 * kFewWaves) {
-      const int t = i / n8, ch = i - t * n8;  // sixteen lanes have one token and one word
-      float v[8];
-      const uint16_t* x = f.x16 + t * f.ldx16;
-      values8<BF16>(raw8(x, 8 * ch, f.cols), v);
-      if (f.s) {
-        float sv[8];
-        floats8(f.s, 8 * ch, f.cols, 1.0f, sv);
+    const int T = FUSED == 1 ? 1 : a.T;
+    for (int i = tid; i < (T + FUSED - 1) / FUSED * n8; i += 64 * kFewWaves) {
+      // sixteen lanes have the same tokens and one word
+      const int t0 = FUSED == 1 ? 0 : i / n8 * FUSED, ch = FUSED == 1 ? i : i % n8;
+      u32x4 raw[FUSED];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = v[j] / sv[j];
+      for (int k = 0; k < FUSED; ++k) raw[k] = raw8(f.x16 + min(t0 + k, T - 1) * f.ldx16, 8 * ch, f.cols);
+      float sv[8];
+      double inv[8];
+      if (f.s) {
+        floats8(f.s, 8 * ch, f.cols, 1.0f, sv);
+        if constexpr (FUSED > 1) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) inv[j] = reciprocal(sv[j]);
+        }
       }
-      uint32_t byte;
-      const uint32_t c = mx_codes8(v, byte);
-      *(uint32_t*)(lds + (size_t)t * nch * 256 + 4 * ch) = c;
-      const uint32_t w = mx_scale_word(byte);
-      if ((ch & 15) == 0) lwords[t * nch * 4 + (ch >> 4)] = w;
+#pragma unroll
+      for (int k = 0; k < FUSED; ++k) {
+        const int t = t0 + k;
+        if (t >= T) break;  // sixteen lanes together
+        float v[8];
+        values8<BF16>(raw[k], v);
+        if (f.s) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = FUSED > 1 ? (float)((double)v[j] * inv[j]) : v[j] / sv[j];
+        }
+        uint32_t byte;
+        const uint32_t c = mx_codes8(v, byte);
+        *(uint32_t*)(lds + (size_t)t * nch * 256 + 4 * ch) = c;
+        const uint32_t w = mx_scale_word(byte);
+        if ((ch & 15) == 0) lwords[t * nch * 4 + (ch >> 4)] = w;
+      }
     }
     __syncthreads();
   }
@@ -471,7 +488,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mxfp4_few(MxFewArgs f) {
   floatx4 acc = {0.f, 0.f, 0.f, 0.f};
   auto load_x = [&](Piece& o, int ch) {
     const int k = ch * 256 + 64 * q, word = 4 * ch + q;
-    if constexpr (FUSED) {
+    if constexpr (FUSED > 0) {
       o.s = (int)lwords[tok * nch * 4 + word];
 #pragma unroll
       for (int u = 0; u < 4; ++u) o.v[u] = *(const int32x4*)(lds + (size_t)tok * nch * 256 + k + 16 * u);
@@ -564,10 +581,10 @@ hipError_t launch_tiles(const MxArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <bool FUSED>
+template <int FUSED>
 hipError_t launch_few(const MxFewArgs& f, hipStream_t stream) {
   const dim3 grid = grid_of((f.g.M + 15) / 16), block(64 * kFewWaves);
-  const size_t lds = FUSED ? (size_t)f.g.T * ((f.g.KB + 255) / 256) * (256 + 16) : 0;
+  const size_t lds = FUSED > 0 ? (size_t)f.g.T * ((f.g.KB + 255) / 256) * (256 + 16) : 0;
   if (f.g.bf16)
     hipLaunchKernelGGL((k_mxfp4_few<FUSED, true>), grid, block, lds, stream, f);
   else
@@ -596,20 +613,24 @@ hipError_t launch_mxfp4_matmul(const MxArgs& a, hipStream_t stream) {
   const int form = mxfp4_form(a.T, a.M, a.KB);
   if (form == kMxFew) {
     const MxFewArgs f{a, nullptr, nullptr, 0, 0};
-    return launch_few<false>(f, stream);
+    return launch_few<0>(f, stream);
   }
   return a.bf16 ? launch_form<true>(a, form, stream) : launch_form<false>(a, form, stream);
 }
 
+// Where tokens times columns are few.  Fused and in two launches, in us, without scales and with: 2 tokens of
+// 4096 x 4096 5.1, 6.7 and 5.7, 6.9; 4 of it 5.6, 6.9 and 6.4, 7.1; 8 of it 7.1, 7.1 and 8.6, 7.3; 4 of 6144 x 4096
+// 7.4, 8.3 and 8.7, 8.5; 2 of 4096 x 11008 10.0, 9.6 and 11.7, 9.9; 16 of 8192 x 1024 4.8, 5.2 and 6.1, 5.5.
 bool mxfp4_linear_fused(int64_t T, int64_t M, int64_t cols) {
-  return T == 1 && cols <= 65536 && mxfp4_form(T, M, (cols + 31) / 32 * 16) == kMxFew;
+  return (T == 1 ? cols <= 65536 : T * cols <= 16384) &&
+         mxfp4_form(T, M, (cols + 31) / 32 * 16) == kMxFew;
 }
 
 hipError_t launch_mxfp4_linear_fused(const MxArgs& a, const void* x, int64_t ldx, const float* s,
                                      int cols, hipStream_t stream) {
   if (a.T <= 0 || a.M <= 0) return hipSuccess;
   const MxFewArgs f{a, (const uint16_t*)x, s, ldx, cols};
-  return launch_few<true>(f, stream);
+  return a.T == 1 ? launch_few<1>(f, stream) : a.T == 2 ? launch_few<2>(f, stream) : launch_few<4>(f, stream);
 }
 
 }  // namespace awq

@@ -24,23 +24,6 @@ namespace {
 constexpr int kRowsTile = 8, kDivideTile = 16, kValuesTile = 16;
 constexpr int kTileWords = 4;  // scale words (128 columns) of a row a block
 
-// 1 / s in fp64, to within 2^-52 of itself: the hardware's estimate y and a step of third order, 1/s = y (1 + e
-// + e^2 ...) with e = 1 - s y.  (1 / inf is y, a zero; of a zero it is NaN in place of an infinity, which
-// makes no difference to a block.)
-//
-// A 16-bit value v times it, rounded to fp32, is v / s rounded correctly: a border between two fp32
-// numbers is M 2^k with an odd M of 25 bits, s = S 2^l with S below 2^24 and v an integer of 11 bits times a
-// power of two, so v - s M 2^k is a multiple of a unit that s M 2^k holds less than 2^49 times, and not 0; v / s
-// lies 2^-49 or more of itself from every border, the product less than 2^-51 from v / s.  (Where the
-// result is subnormal a tie can be exact and come out either way; it is then an odd number of 11 bits times
-// 2^-150, which is far below the least element's border, 2^-129.)
-__device__ __forceinline__ double reciprocal(float s) {
-  const double d = (double)s, y = __builtin_amdgcn_rcp(d);
-  const double e = fma(-d, y, 1.0);
-  const double r = fma(y, fma(e, e, e), y);
-  return fabsf(s) == __builtin_inff() ? y : r;
-}
-
 // FOLD: kFoldNone, kFoldDivide or kFoldMultiply.
 template <bool BF16, int FOLD, int TILE>
 __global__ __launch_bounds__(256) void k_mxfp4_rows(const uint16_t* __restrict__ A, unsigned rows,
