@@ -364,7 +364,6 @@ __global__ __launch_bounds__(S::THREADS) void k_mxfp4_tiles(MxArgs a, int tiles_
   }
   __syncthreads();
   uint16_t* y = (uint16_t*)a.y + (int64_t)t0 * a.ldy + m0;
-  const bool vec = a.ldy % 8 == 0 && ((uintptr_t)a.y & 15) == 0;
   auto store = [&](auto stream) {
     constexpr int kPer = S::BM / 8;
     for (int c = tid; c < S::BT * kPer; c += S::THREADS) {
@@ -372,9 +371,9 @@ __global__ __launch_bounds__(S::THREADS) void k_mxfp4_tiles(MxArgs a, int tiles_
       if (t >= rows_x || m >= rows_w) continue;
       const u32x4 v = *(const u32x4*)(results + t * S::OUT + 2 * m);
       uint16_t* o = y + (int64_t)t * a.ldy + m;
-      if (vec && m + 8 <= rows_w) {
-        if constexpr (decltype(stream)::value) __builtin_nontemporal_store(v, (u32x4*)o);
-        else *(u32x4*)o = v;
+      if (m + 8 <= rows_w) {  // (16 bytes at any even address)
+        if constexpr (decltype(stream)::value) __builtin_nontemporal_store(v, (u32x4_at2*)o);
+        else *(u32x4_at2*)o = v;
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -560,11 +559,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mxfp4_few(MxFewArgs f) {
     }
   }
   uint16_t* y = (uint16_t*)a.y + (int64_t)t * a.ldy + m;
-  if (m + 4 <= a.M && a.ldy % 4 == 0 && ((uintptr_t)a.y & 7) == 0) {
-    uint2 p;
-    p.x = o[0] | ((uint32_t)o[1] << 16);
-    p.y = o[2] | ((uint32_t)o[3] << 16);
-    *(uint2*)y = p;
+  if (m + 4 <= a.M) {
+    typedef uint32_t u32x2_at2 __attribute__((ext_vector_type(2), aligned(2)));
+    *(u32x2_at2*)y = u32x2_at2{o[0] | ((uint32_t)o[1] << 16), o[2] | ((uint32_t)o[3] << 16)};
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
