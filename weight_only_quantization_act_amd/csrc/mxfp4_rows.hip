@@ -5,7 +5,8 @@
 //
 // Bound by memory: 2 bytes of every value in, 17/32 out.  A block takes 8 rows of 512 columns, each
 // wave two rows with its 512 columns, so that loads are 1 KiB in one piece and the fold's scales
-// serve two rows.  28672 rows of 8192 times scales 106-124 us (595 MB, 4.8-5.6 TB/s), back 92-95 us.
+// serve two rows.  28672 rows of 8192 times scales 104-121 us (595 MB, 4.9-5.7 TB/s), divided by them 124-130
+// us (the vector instructions of the reciprocals), back 92-95 us.
 #include <hip/hip_runtime.h>
 
 #include "grid.h"
