@@ -147,3 +147,31 @@ def test_grids_past_32_bits():
         part = steps[a:a + (1 << 26)]
         assert torch.equal(y[a:a + (1 << 26), 0], (3 * part).half())
         assert torch.equal(y[a:a + (1 << 26), 1], (-5 * part).half())
+
+
+def test_longest_rows():
+    """The norm over rows of 2^27 columns and more, MXFP4 rows and products over 2^22, the most they take."""
+    say("longest rows")
+    K = (1 << 27) + 9
+    x = torch.full((2, K), 2.0, device="cuda", dtype=torch.float16)
+    x[1] = -2
+    # the mean is 4 to within fp64's rounding, v fp32's 1
+    y, _ = awq.awq_rmsnorm(x, None, 1e-30)
+    assert bool((y[0] == 1).all()) and bool((y[1] == -1).all())
+    q, st, _ = awq.awq_rmsnorm_int8(x, None, 1e-30)
+    assert bool((q[0, :K] == 127).all()) and bool((q[1, :K] == -127).all()) and bool((q[:, K:] == 0).all())
+    del x, y, q
+    K = 1 << 22
+    g = torch.Generator(device="cuda").manual_seed(0)
+    for T, M in ((1, 10), (3, 200), (70, 300), (300, 300)):
+        x, w = (torch.randint(-40, 41, (n, K), generator=g, device="cuda", dtype=torch.int8) for n in (T, M))
+        x, w = (torch.where(a.abs() <= 1, a, 0).half() for a in (x, w))
+        x[:, ::32], w[:, ::32] = 4, 0                               # scales of 1 and of 1 / 4 or 0
+        xq, wq = awq.awq_mxfp4_quantize(x), awq.awq_mxfp4_quantize(w)
+        assert torch.equal(awq.awq_mxfp4_dequantize(*xq, K), x) and torch.equal(awq.awq_mxfp4_dequantize(*wq, K), w)
+        y = awq.awq_mxfp4_matmul(*xq, *wq)
+        want = torch.mm(x.float(), w.float().t().contiguous())      # sums of a few thousand ones: exact
+        assert float(want.abs().max()) < 2048 and torch.equal(y, want.half())
+        assert torch.equal(awq.awq_mxfp4_linear(x, *wq), y)
+    with pytest.raises(Exception):
+        awq.awq_mxfp4_quantize(torch.zeros(1, K + 1, device="cuda", dtype=torch.float16))
