@@ -253,13 +253,25 @@ __global__ __launch_bounds__(S::THREADS) void k_mxfp4_tiles(MxArgs a, int tiles_
       for (int u = 0; u < U; ++u) {
         if (kt + u >= n_steps) break;
         landed();
-        read((u + 1) % NS, f[~u & 1], s[~u & 1]);
+        const uint8_t* next = sm + (u + 1) % NS * S::BYTES;
+        // Products first, a part of the next stage's reads and of the refill behind each: a refill's instruction
+        // waits for the others' addresses, and a wave that issues them all first leaves the matrix
+        // cores idle meanwhile (333 tokens of 5120 x 13824 25.0 -> 22.9 us on the device alone).
+        auto part = [&](auto ks) {
+          mma(ks, f[u & 1][decltype(ks)::value], s[u & 1]);
+          __builtin_amdgcn_sched_barrier(0);
+          load(next, decltype(ks)::value, f[~u & 1][decltype(ks)::value]);
 #pragma unroll
-        for (int j = 0; j < S::PER; ++j) dma_piece(u % NS, kt + u + NS, j);
-        mma(integral_constant<int, 0>{}, f[u & 1][0], s[u & 1]);
-        mma(integral_constant<int, 1>{}, f[u & 1][1], s[u & 1]);
-        mma(integral_constant<int, 2>{}, f[u & 1][2], s[u & 1]);
-        mma(integral_constant<int, 3>{}, f[u & 1][3], s[u & 1]);
+          for (int j = decltype(ks)::value * S::PER / 4; j < (decltype(ks)::value + 1) * S::PER / 4; ++j)
+            dma_piece(u % NS, kt + u + NS, j);
+          __builtin_amdgcn_sched_barrier(0);
+        };
+        __builtin_amdgcn_sched_barrier(0);
+        load_scales(next, s[~u & 1]);
+        part(integral_constant<int, 0>{});
+        part(integral_constant<int, 1>{});
+        part(integral_constant<int, 2>{});
+        part(integral_constant<int, 3>{});
       }
     }
   } else {

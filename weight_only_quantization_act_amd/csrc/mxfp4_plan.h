@@ -26,13 +26,13 @@ enum { kMxFew, kMxTile32K, kMxTile32x64K, kMxTile64K, kMxTile64, kMxTile64x128, 
 // tiles a compute unit; small tiles are bound by what goes through LDS, 128 x 128 ones run in rounds of two
 // a compute unit, 256 x 256 ones of one):
 //   tiles of 64 x 64    0.22-0.28 up to r = 1, 0.56 at 2, 0.68 at 2.7, 2.4 at 10.8
-//            64 x 128   0.37-0.42 up to r = 1, 0.7 at 1.3, 1.15 at 2.7, 2.2 at 5.4
-//            128 x 128  0.42-0.55 up to r = 1 in three stages (0.56-0.7 in two), 0.94-1.1 at 1 to 1.3,
+//            64 x 128   0.30-0.36 up to r = 1, 0.7 at 1.3, 1.15 at 2.7, 2.2 at 5.4
+//            128 x 128  0.38-0.44 up to r = 1 in three stages (0.56-0.7 in two), 0.94-1.1 at 1 to 1.3,
 //                       1.95 at 2 to 2.7 in two stages
 //            256 x 256  1.4-1.5 up to r = 1, 1.8-2.0 a round beyond
 // Between neighbours, in us, 64 x 64, 64 x 128, 128 x 128, 256 x 256: 333 tokens of 5120 x 13824 24.2,
-// 22.3, 27, 69; 512 of it 34.3, 34.8, 27.9, 70; 512 of 11008 x 4096 23.1, 20.9, 20.0, 26.8; 1024 of 11008 x 4096 40.6, 38.2, 33.7, 30.1;
-// 4096 of 11008 x 4096 165, 145, 109, 97.
+// 22.0, 24.5, 69; 512 of it 35.3, 36.4, 25.7, 70; 512 of 11008 x 4096 24.5, 21.5, 20.4, 26.8; 1024 of
+// 11008 x 4096 43, 40, 33.4, 30.1; 4096 of 11008 x 4096 165, 145, 109, 97.
 // Where tiles leave at most one a compute unit, groups of waves share the columns of one (17 tokens of
 // 5120 x 13824 on 64 x 64: one group 16.8, two 13.0) and the smallest tiles that fit are the fastest: 16
 // tokens of 5120 x 13824 on 32 x 32 in four groups 9.3, 32 x 64 in two 11.7, 64 x 64 in two 12.8; 50 of
@@ -48,8 +48,8 @@ inline int mxfp4_form(int64_t T, int64_t M, int64_t KB) {
   if (per_unit(32, 64) <= 1) return kMxTile32x64K;
   const double r1 = per_unit(64, 64), r2 = per_unit(64, 128), r3 = per_unit(128, 128), r4 = per_unit(256, 256);
   const double t1 = r1 <= 1 ? 0.27 : 0.1 + 0.24 * r1;
-  const double t2 = r2 <= 1 ? 0.40 : 0.15 + 0.4 * r2;
-  const double t3 = r3 <= 1 ? 0.46 : r3 <= 2 ? 0.95 : 1.05 * rounds(r3 / 2);
+  const double t2 = r2 <= 1 ? 0.36 : 0.15 + 0.4 * r2;
+  const double t3 = r3 <= 1 ? 0.42 : r3 <= 2 ? 0.95 : 1.05 * rounds(r3 / 2);
   const double t4 = r4 <= 1 ? 1.45 : 1.95 * rounds(r4);
   if (t1 <= t2 && t1 <= t3 && t1 <= t4) return r1 <= 1 ? kMxTile64K : kMxTile64;
   if (t2 <= t3 && t2 <= t4) return kMxTile64x128;
