@@ -24,8 +24,9 @@
 // operand reads placed between the products by hand 885, the loop over one stage with its slot in a
 // register 851 (128 x 128 tiles 22.2 for 21.3), bands of 4, 6 and 16 tiles 855, 856, 866, stages of 64
 // bytes, instructions of 16 x 16 x 128.  Products with a tile or two a compute unit are bound by each step's
-// chain of barrier, reads and refills (333 tokens of 5120 x 13824 21.6 us, 2.2 PFLOP/s, 0.4 us a step;
-// matrix cores busy 16%): neither fewer LDS reads nor deeper rings shorten it.
+// chain of barrier, products, reads and refills (333 tokens of 5120 x 13824 21.2 us, 2.2 PFLOP/s, 0.35 us a
+// step; matrix cores busy 17%; the refills alone would take 0.24): neither fewer LDS reads, deeper rings
+// nor two stages a barrier shorten it.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
