@@ -402,8 +402,8 @@ __global__ __launch_bounds__(S::THREADS) void k_mxfp4_tiles(MxArgs a, int tiles_
 
 // ---- few tokens --------------------------------------------------------------------------
 //
-// Up to 16 tokens the product is bound by reading the weights once.  A block takes 16 outputs
-// and all tokens; its eight waves take 256-byte pieces of K (512 columns) in turn.  The weights go
+// A few tokens' product is bound by reading the weights once.  A block takes 16 outputs
+// and all tokens, TT tiles of 16; its eight waves take 256-byte pieces of K (512 columns) in turn.  The weights go
 // from memory to the operand registers of v_mfma_scale_f32_16x16x128_f8f6f4 directly: lane l has
 // row l mod 16 and the 64 bytes from 64 (l div 16) of a piece, whose four blocks' scales are one word;
 // instruction u takes block u of each lane.  The next piece's loads are ahead of the products of
@@ -411,7 +411,7 @@ __global__ __launch_bounds__(S::THREADS) void k_mxfp4_tiles(MxArgs a, int tiles_
 // order.  Result element e of lane l is output 4 (l div 16) + e, token l mod 16.
 //
 // One token through 4096 x 4096 with its quantisation 4.6 us (9 MB: 1.9 TB/s with start and end of the
-// launch); the product alone 4.1 us, of 16 tokens 4.4 (tiles 5.4).
+// launch); the product alone 4.1 us, of 16 tokens 4.9, of 17 5.1 (tiles 6.0).
 //
 // FUSED > 0: the block first quantises the tokens into LDS, a lane 8 columns of so many tokens together, with
 // the first weights already on their way; every block repeats that (a few thousand values from L2) in place of
@@ -426,7 +426,7 @@ struct MxFewArgs {
   int cols;
 };
 
-template <int FUSED, bool BF16>
+template <int FUSED, int TT, bool BF16>
 __global__ __launch_bounds__(64 * kFewWaves) void k_mxfp4_few(MxFewArgs f) {
   const MxArgs& a = f.g;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // FUSED > 0: codes [T][pieces 256], words [T][4 pieces]
@@ -496,9 +496,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mxfp4_few(MxFewArgs f) {
   }
 
   // columns past the last token repeat it and are dropped
-  const int tok = min(lr, a.T - 1);
-  floatx4 acc = {0.f, 0.f, 0.f, 0.f};
-  auto load_x = [&](Piece& o, int ch) {
+  floatx4 acc[TT];
+#pragma unroll
+  for (int i = 0; i < TT; ++i) acc[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+  auto load_x1 = [&](Piece& o, int ch, int tok) {
     const int k = ch * 256 + 64 * q, word = 4 * ch + q;
     if constexpr (FUSED > 0) {
       o.s = (int)lwords[tok * nch * 4 + word];
@@ -511,7 +512,11 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mxfp4_few(MxFewArgs f) {
         o.v[u] = *(const int32x4*)(a.x + (int64_t)tok * a.ldx + (k + 16 * u < a.KB ? k + 16 * u : 0));
     }
   };
-  auto piece = [&](Piece& w, Piece& x, int ch) {
+  auto load_x = [&](Piece (&o)[TT], int ch) {
+#pragma unroll
+    for (int i = 0; i < TT; ++i) load_x1(o[i], ch, min(16 * i + lr, a.T - 1));
+  };
+  auto piece = [&](Piece& w, Piece (&x)[TT], int ch) {
     if (ch == nch - 1) {  // blocks past K count nothing (their scales may be any row's)
       const int k = ch * 256 + 64 * q;
 #pragma unroll
@@ -519,13 +524,16 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mxfp4_few(MxFewArgs f) {
         if (k + 16 * u >= a.KB) {
           w.v[u] = int32x4{0, 0, 0, 0};
           w.s = w.s & ~(255 << (8 * u));
-          x.s = x.s & ~(255 << (8 * u));
+#pragma unroll
+          for (int i = 0; i < TT; ++i) x[i].s = x[i].s & ~(255 << (8 * u));
         }
     }
     auto step = [&](auto uu) {
       constexpr int u = decltype(uu)::value;
-      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w.v[u]), operand(x.v[u]), acc, kFp4,
-                                                             kFp4, u, w.s, u, x.s);
+#pragma unroll
+      for (int i = 0; i < TT; ++i)
+        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w.v[u]), operand(x[i].v[u]), acc[i], kFp4,
+                                                                  kFp4, u, w.s, u, x[i].s);
     };
     step(std::integral_constant<int, 0>{});
     step(std::integral_constant<int, 1>{});
@@ -535,7 +543,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mxfp4_few(MxFewArgs f) {
   // a piece's tokens are asked for before the next piece's weights: loads return in order, so
   // waiting for the tokens does not wait for those weights
   for (int ch = wave; ch < nch; ch += 2 * kFewWaves) {
-    Piece x;
+    Piece x[TT];
     load_x(x, ch);
     if (ch + kFewWaves < nch) load_w(p1, ch + kFewWaves);
     __builtin_amdgcn_sched_barrier(0);
@@ -547,19 +555,20 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mxfp4_few(MxFewArgs f) {
     piece(p1, x, ch + kFewWaves);
   }
 
-  // the waves' sums, then one lane's four outputs a thread
-  __shared__ floatx4 sum[kFewWaves][64];
-  sum[wave][lane] = acc;
+  // the waves' sums, then one lane's four outputs a thread, a tile of tokens a wave
+  __shared__ floatx4 sum[TT][kFewWaves][64];
+#pragma unroll
+  for (int i = 0; i < TT; ++i) sum[i][wave][lane] = acc[i];
   __syncthreads();
-  if (wave > 0) return;
-  floatx4 v = acc;
+  if (wave >= TT) return;
+  floatx4 v = sum[wave][0][lane];
 #pragma unroll
   for (int w = 1; w < kFewWaves; ++w) {
-    const floatx4 o = sum[w][lane];
+    const floatx4 o = sum[wave][w][lane];
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] += o[e];
   }
-  const int t = lr, m = m0 + 4 * q;
+  const int t = 16 * wave + lr, m = m0 + 4 * q;
   if (t >= a.T) return;
   const uint16_t* bias = (const uint16_t*)a.bias;
   uint16_t o[4];
@@ -591,14 +600,14 @@ hipError_t launch_tiles(const MxArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int FUSED>
+template <int FUSED, int TT>
 hipError_t launch_few(const MxFewArgs& f, hipStream_t stream) {
   const dim3 grid = grid_of((f.g.M + 15) / 16), block(64 * kFewWaves);
   const size_t lds = FUSED > 0 ? (size_t)f.g.T * ((f.g.KB + 255) / 256) * (256 + 16) : 0;
   if (f.g.bf16)
-    hipLaunchKernelGGL((k_mxfp4_few<FUSED, true>), grid, block, lds, stream, f);
+    hipLaunchKernelGGL((k_mxfp4_few<FUSED, TT, true>), grid, block, lds, stream, f);
   else
-    hipLaunchKernelGGL((k_mxfp4_few<FUSED, false>), grid, block, lds, stream, f);
+    hipLaunchKernelGGL((k_mxfp4_few<FUSED, TT, false>), grid, block, lds, stream, f);
   return hipGetLastError();
 }
 
@@ -623,7 +632,7 @@ hipError_t launch_mxfp4_matmul(const MxArgs& a, hipStream_t stream) {
   const int form = mxfp4_form(a.T, a.M, a.KB);
   if (form == kMxFew) {
     const MxFewArgs f{a, nullptr, nullptr, 0, 0};
-    return launch_few<0>(f, stream);
+    return a.T <= 16 ? launch_few<0, 1>(f, stream) : launch_few<0, 2>(f, stream);
   }
   return a.bf16 ? launch_form<true>(a, form, stream) : launch_form<false>(a, form, stream);
 }
@@ -632,7 +641,7 @@ hipError_t launch_mxfp4_matmul(const MxArgs& a, hipStream_t stream) {
 // 4096 x 4096 5.1, 6.7 and 5.7, 6.9; 4 of it 5.6, 6.9 and 6.4, 7.1; 8 of it 7.1, 7.1 and 8.6, 7.3; 4 of 6144 x 4096
 // 7.4, 8.3 and 8.7, 8.5; 2 of 4096 x 11008 10.0, 9.6 and 11.7, 9.9; 16 of 8192 x 1024 4.8, 5.2 and 6.1, 5.5.
 bool mxfp4_linear_fused(int64_t T, int64_t M, int64_t cols) {
-  return (T == 1 ? cols <= 65536 : T * cols <= 16384) &&
+  return (T == 1 ? cols <= 65536 : T <= 16 && T * cols <= 16384) &&
          mxfp4_form(T, M, (cols + 31) / 32 * 16) == kMxFew;
 }
 
@@ -640,7 +649,9 @@ hipError_t launch_mxfp4_linear_fused(const MxArgs& a, const void* x, int64_t ldx
                                      int cols, hipStream_t stream) {
   if (a.T <= 0 || a.M <= 0) return hipSuccess;
   const MxFewArgs f{a, (const uint16_t*)x, s, ldx, cols};
-  return a.T == 1 ? launch_few<1>(f, stream) : a.T == 2 ? launch_few<2>(f, stream) : launch_few<4>(f, stream);
+  return a.T == 1   ? launch_few<1, 1>(f, stream)
+         : a.T == 2 ? launch_few<2, 1>(f, stream)
+                    : launch_few<4, 1>(f, stream);
 }
 
 }  // namespace awq

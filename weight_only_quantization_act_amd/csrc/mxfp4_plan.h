@@ -13,14 +13,17 @@ enum { kMxFew, kMxTile32K, kMxTile32x64K, kMxTile64K, kMxTile64, kMxTile64x128, 
 
 // KB: bytes of codes a row (two columns a byte).
 //
-// Few: one round of blocks of 16 outputs, two blocks a compute unit, while the tokens' operands, which
-// every block reads, stay small beside the weights.  Measured, streaming and the best tiles, in us:
-//   tokens              1            16
-//   4096 x 4096         4.1,  5.4    4.4,  5.4
-//   4096 x 11008        6.2,  7.9    8.1,  8.0
-//   5120 x 13824        11.0, 9.3    15.7, 9.3
-//   11008 x 4096        6.6,  6.4    8.2,  6.4
-//   28672 x 8192        28.4, 20.0   32.9, 20.5
+// Few: blocks of 16 outputs, one or two a compute unit, while what each reads stays small: its weights (as
+// much as 16 tokens) and all tokens' operands.  Measured, streaming and the best tiles, in us:
+//   tokens              1         8         16        32
+//   4096 x 4096         4.1, 5.4  4.6, 5.9  4.9, 6.0  5.9, 5.9
+//   4096 x 11008        6.5, 7.7  7.3, 7.8  8.2, 7.9  10.8, 7.9
+//   2048 x 8192         5.2, 6.7            6.5, 6.9  8.4, 7.0
+//   6144 x 4096                   5.9, 5.9  6.5, 6.0  8.5, 6.0
+//   8192 x 3584                   5.5, 5.9  6.1, 6.0  7.9, 6.1
+//   8192 x 8192                   9.8, 7.7  11.2, 8.1 15.0, 8.7
+//   11008 x 4096        6.8, 6.3            8.4, 6.4  11.4, 6.4
+// (One token's limit is larger: its linear layer saves a launch where the product streams.)
 //
 // Tiles: the form with the smallest time a step of 256 columns, fitted to measurements (us a step at r
 // tiles a compute unit; small tiles are bound by what goes through LDS, 128 x 128 ones run in rounds of two
@@ -39,7 +42,7 @@ enum { kMxFew, kMxTile32K, kMxTile32x64K, kMxTile64K, kMxTile64, kMxTile64x128, 
 // 4096 x 4096 5.6, 6.4, 6.7; with more than one a unit they are not (50 of 11008 x 4096 12.6, 8.7, 7.1; 100
 // of it 64 x 64 in two groups 12.4, one 9.6).
 inline int mxfp4_form(int64_t T, int64_t M, int64_t KB) {
-  if (T <= 16 && M <= 8192 && M * KB * (T + 16) <= (int64_t)1 << 29) return kMxFew;
+  if (T <= 32 && M <= 8192 && KB * (T + 16) <= (M <= 4096 ? 150000 : T == 1 ? 66000 : 54000)) return kMxFew;
   auto per_unit = [&](int64_t bt, int64_t bm) {
     return (double)(((T + bt - 1) / bt) * ((M + bm - 1) / bm)) / 256.0;
   };
