@@ -17,7 +17,8 @@
 // the second (token).  Rows past the matrices and chunks past K arrive as zeros, or as scales of rows
 // that are dropped.
 //
-// Large products run at the power limit: 8192 tokens of 28672 x 8192 939 us, 4.1 PFLOP/s (matrix cores
+// Large products run at the power limit: 8192 tokens of 28672 x 8192 939-962 us, 4.0-4.1
+// PFLOP/s (matrix cores
 // busy 54% of the cycles at 1.81 GHz; the same instructions alone on the same data 6.2 PFLOP/s; without
 // the refills the loop takes 16% less, without its LDS reads 10%, without waiting for the refills nothing).
 // Not faster, in us on 859 of the kernel alone: four waves of 128 x 128 with a third fewer LDS reads 910,
