@@ -18,8 +18,7 @@ namespace awq {
 
 namespace {
 
-// Rows a block, in us at 4, 8, 16 and 32: 333 rows of 13824 divided by scales 6.2, 6.1, 6.9, 8.4; 28672 of
-// 8192 times scales 129, 120, 125, 131; read back 110, 99, 95, 110.  Divided by scales, where a block has
+// Rows a block, in us at 4, 8, 16 and 32: 28672 of 8192 times scales 129, 120, 125, 131; read back 110, 99, 95, 110.  Divided by scales, where a block has
 // their reciprocals to find first, and many rows 16: 28672 of 8192 at 8 and 16 158, 128, 4096 of 4096 11.4,
 // 10.5, but 333 of 13824 5.2 both, 50 of 4096 2.9, 3.5.
 constexpr int kRowsTile = 8, kDivideTile = 16, kValuesTile = 16;
