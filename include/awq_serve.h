@@ -235,7 +235,8 @@ int awq_mxfp4_dequantize(const uint8_t* codes, int64_t ld_codes, const uint8_t* 
  * fp32, and the result is rounded once to the output type.  Results repeat bit for bit.  A scale of 255 in a
  * row makes the row's results NaN.
  *   xc, xs  tokens' codes and scales, wc, ws the weights', as awq_mxfp4_quantize lays them out.
- *           Columns from in_features up to a whole block are read: they must be zero in one of the two
+ *           Columns from in_features up to a whole block are read: they must be zero in one of the two.
+ *           Scale bytes behind a row's last block are not looked at
  *   bias    [out] in the output's type, or NULL
  *   y       fp16 or bf16 [n_tokens][ldy], ldy >= out
  * n_tokens, out_features at most 2^29 - 512, in_features at most 2^22, n_tokens * ldx, out * ldw and

@@ -234,7 +234,8 @@ def awq_mxfp4_matmul(xc: torch.Tensor, xs: torch.Tensor, wc: torch.Tensor, ws: t
                      dtype: torch.dtype = torch.float16, bias: Optional[torch.Tensor] = None,
                      out: Optional[torch.Tensor] = None, *, stream=None):
     """y [T, M] = x w^T (+ bias) in `dtype` for MXFP4 codes and scales of tokens (xc, xs) and weights
-    (wc, ws), as awq_mxfp4_quantize and awq_rmsnorm_mxfp4 make them."""
+    (wc, ws), as awq_mxfp4_quantize and awq_rmsnorm_mxfp4 make them.  All columns of the codes' blocks count:
+    where the last block is not whole, its columns past the last must be zero in one of the two."""
     if out is None and stream is None:
         y = (_N or _native()).mxfp4_matmul(xc, xs, wc, ws, dtype, bias)
         if y is not None:

@@ -199,6 +199,15 @@ __global__ __launch_bounds__(S::THREADS) void k_mxfp4_tiles(MxArgs a, int tiles_
 #pragma unroll
     for (int i = 0; i < S::MI; ++i) s.w[i] = *(const int*)(base + ws_off + i * 128);
   };
+  // The bytes of the last step's words behind the row's last block may be any, 255 (NaN) among them.
+  const int left = (a.KB >> 4) - 8 * ((n_steps - 1) * S::KG + group) - 4 * fh;  // the lane's blocks of that step
+  const int kept = left >= 4 ? -1 : left > 0 ? (1 << (8 * left)) - 1 : 0;
+  auto clear_behind = [&](Scales& s) {
+#pragma unroll
+    for (int i = 0; i < S::TI; ++i) s.x[i] &= kept;
+#pragma unroll
+    for (int i = 0; i < S::MI; ++i) s.w[i] &= kept;
+  };
   floatx16 acc[S::TI][S::MI];
 #pragma unroll
   for (int i = 0; i < S::TI; ++i)
@@ -250,10 +259,10 @@ __global__ __launch_bounds__(S::THREADS) void k_mxfp4_tiles(MxArgs a, int tiles_
     begin();
     read(0, f[0], s[0]);
     constexpr int U = NS % 2 ? 2 * NS : NS;
-    for (int kt = 0; kt < n_steps; kt += U) {
+    for (int kt = 0; kt < n_steps - 1; kt += U) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (kt + u >= n_steps) break;
+        if (kt + u >= n_steps - 1) break;
         landed();
         const uint8_t* next = sm + (u + 1) % NS * S::BYTES;
         // Products first, a part of the next stage's reads and of the refill behind each: a refill's instruction
@@ -276,24 +285,36 @@ __global__ __launch_bounds__(S::THREADS) void k_mxfp4_tiles(MxArgs a, int tiles_
         part(integral_constant<int, 3>{});
       }
     }
+    auto last = [&](const Frag (&of)[4], Scales& os) {  // its operands are here, nothing is refilled
+      clear_behind(os);
+      mma(integral_constant<int, 0>{}, of[0], os);
+      mma(integral_constant<int, 1>{}, of[1], os);
+      mma(integral_constant<int, 2>{}, of[2], os);
+      mma(integral_constant<int, 3>{}, of[3], os);
+    };
+    if (n_steps & 1) last(f[0], s[0]);  // (U is even)
+    else last(f[1], s[1]);
   } else {
     Frag f0, f1;
     Scales sc, sn;
     begin();
     load_scales(sm, sc);
     load(sm, 0, f0);
-    for (int kt = 0; kt < n_steps; kt += NS) {
+    // a step's products but its last instruction's
+    auto most = [&](const uint8_t* cur) {
+      load(cur, 1, f1);
+      mma(integral_constant<int, 0>{}, f0, sc);
+      load(cur, 2, f0);
+      mma(integral_constant<int, 1>{}, f1, sc);
+      load(cur, 3, f1);
+      mma(integral_constant<int, 2>{}, f0, sc);
+    };
+    for (int kt = 0; kt < n_steps - 1; kt += NS) {
 #pragma unroll
       for (int st = 0; st < NS; ++st) {
-        if (kt + st >= n_steps) break;
-        const uint8_t* cur = sm + st * S::BYTES;
+        if (kt + st >= n_steps - 1) break;
         const uint8_t* next = sm + (st + 1) % NS * S::BYTES;
-        load(cur, 1, f1);
-        mma(integral_constant<int, 0>{}, f0, sc);
-        load(cur, 2, f0);
-        mma(integral_constant<int, 1>{}, f1, sc);
-        load(cur, 3, f1);
-        mma(integral_constant<int, 2>{}, f0, sc);
+        most(sm + st * S::BYTES);
         landed();
         load_scales(next, sn);
         load(next, 0, f0);
@@ -310,6 +331,9 @@ __global__ __launch_bounds__(S::THREADS) void k_mxfp4_tiles(MxArgs a, int tiles_
         sc = sn;
       }
     }
+    clear_behind(sc);  // the last step, without a refill
+    most(sm + (n_steps - 1) % NS * S::BYTES);
+    mma(integral_constant<int, 3>{}, f1, sc);
   }
   __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<0>::value);  // no LDS write may come after this
   __syncthreads();
