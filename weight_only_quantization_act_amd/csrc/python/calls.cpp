@@ -4,7 +4,8 @@
 // Each function takes the usual case only: tensors on the current device with unit stride along their rows,
 // outputs allocated, work on the current stream.  For anything else, a refused argument among it, it
 // returns None before anything is enqueued, and the binding's own checks take the call and say what is
-// wrong.  No exception passes: what torch throws (memory) is handed to Python.
+// wrong.  A launch that failed is raised as AwqError: some of the call's work may be enqueued.  No exception
+// passes: what torch throws (memory) is handed to Python.
 #include <Python.h>
 
 #include <ATen/ATen.h>
@@ -66,6 +67,19 @@ int64_t words(int64_t k) { return (k + 127) / 128; }
 int64_t round4(int64_t r) { return (r + 3) / 4 * 4; }
 
 PyObject* none() { Py_RETURN_NONE; }
+
+// What a call that was not carried out returns: None where its arguments were refused.
+PyObject* failed(int status, const char* where) {
+  if (status != AWQ_E_HIP) return none();
+  PyObject* m = PyImport_ImportModule("weight_only_quantization_act_amd._lib");
+  PyObject* type = m ? PyObject_GetAttrString(m, "AwqError") : nullptr;
+  PyObject* e = type ? PyObject_CallFunction(type, "is", status, where) : nullptr;
+  if (e) PyErr_SetObject(type, e);
+  Py_XDECREF(e);
+  Py_XDECREF(type);
+  Py_XDECREF(m);
+  return nullptr;
+}
 
 // The interpreter is free for other threads while a call is enqueued.
 struct Unlocked {
@@ -168,11 +182,11 @@ PyObject* rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!m.ok) return none();
   void* h = m.sum(p);
   Tensor y = p.empty({m.rows, m.cols}, m.x->scalar_type());
-  if (enqueue([&] {
+  if (const int status = enqueue([&] {
         return awq_rmsnorm(m.x->const_data_ptr(), m.ldx, m.r ? m.r->const_data_ptr() : nullptr, m.ldr, m.rows, m.cols,
                       m.type, m.w, m.wtype, m.eps, h, m.cols, y.mutable_data_ptr(), m.cols, p.stream());
       }))
-    return none();
+    return failed(status, "awq_rmsnorm");
   return pair(THPVariable_Wrap(y), m.h_object(a[0]));
   END_HANDLE_TH_ERRORS
 }
@@ -186,12 +200,12 @@ PyObject* rmsnorm_int8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   void* h = m.sum(p);
   const int64_t ld = round16(m.cols);
   Tensor codes = p.empty({m.rows, ld}, at::kChar), steps = p.empty({m.rows}, at::kFloat);
-  if (enqueue([&] {
+  if (const int status = enqueue([&] {
         return awq_rmsnorm_int8(m.x->const_data_ptr(), m.ldx, m.r ? m.r->const_data_ptr() : nullptr, m.ldr, m.rows,
                            m.cols, m.type, m.w, m.wtype, m.eps, h, m.cols, (int8_t*)codes.mutable_data_ptr(), ld,
                            (float*)steps.mutable_data_ptr(), p.stream());
       }))
-    return none();
+    return failed(status, "awq_rmsnorm_int8");
   return triple(THPVariable_Wrap(codes), THPVariable_Wrap(steps), m.h_object(a[0]));
   END_HANDLE_TH_ERRORS
 }
@@ -205,12 +219,12 @@ PyObject* rmsnorm_mxfp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   void* h = m.sum(p);
   const int64_t ld = code_bytes(m.cols), lds = round4(m.rows);
   Tensor codes = p.empty({m.rows, ld}, at::kByte), scales = p.empty({words(m.cols), lds, 4}, at::kByte);
-  if (enqueue([&] {
+  if (const int status = enqueue([&] {
         return awq_rmsnorm_mxfp4(m.x->const_data_ptr(), m.ldx, m.r ? m.r->const_data_ptr() : nullptr, m.ldr, m.rows,
                             m.cols, m.type, m.w, m.wtype, m.eps, h, m.cols, (uint8_t*)codes.mutable_data_ptr(), ld,
                             (uint8_t*)scales.mutable_data_ptr(), lds, p.stream());
       }))
-    return none();
+    return failed(status, "awq_rmsnorm_mxfp4");
   return triple(THPVariable_Wrap(codes), THPVariable_Wrap(scales), m.h_object(a[0]));
   END_HANDLE_TH_ERRORS
 }
@@ -234,11 +248,11 @@ PyObject* int8_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const void* steps = vector(a[1], p, at::kFloat, rows, &ok);
   if (!ok) return none();
   Tensor y = p.empty({rows, cols}, st);
-  if (enqueue([&] {
+  if (const int status = enqueue([&] {
         return awq_int8_dequantize((const int8_t*)codes->const_data_ptr(), ld, (const float*)steps, rows, cols, type,
                               y.mutable_data_ptr(), cols, p.stream());
       }))
-    return none();
+    return failed(status, "awq_int8_dequantize");
   return THPVariable_Wrap(y);
   END_HANDLE_TH_ERRORS
 }
@@ -256,12 +270,12 @@ PyObject* mxfp4_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const void* s = vector(a[1], p, at::kFloat, cols, &ok);
   if (!ok) return none();
   Tensor codes = p.empty({rows, ld}, at::kByte), scales = p.empty({words(cols), lds, 4}, at::kByte);
-  if (enqueue([&] {
+  if (const int status = enqueue([&] {
         return awq_mxfp4_quantize(A->const_data_ptr(), rows, cols, lda, type_of(A->scalar_type()), (const float*)s,
                              a[2] == Py_True ? AWQ_FOLD_MULTIPLY : AWQ_FOLD_DIVIDE, (uint8_t*)codes.mutable_data_ptr(),
                              ld, (uint8_t*)scales.mutable_data_ptr(), lds, p.stream());
       }))
-    return none();
+    return failed(status, "awq_mxfp4_quantize");
   return pair(THPVariable_Wrap(codes), THPVariable_Wrap(scales));
   END_HANDLE_TH_ERRORS
 }
@@ -278,12 +292,12 @@ PyObject* mxfp4_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int type = type_arg(a[3], &st);
   if (!c.codes || type < 0 || cols <= 0 || c.bytes != code_bytes(cols)) return none();
   Tensor y = p.empty({c.rows, cols}, st);
-  if (enqueue([&] {
+  if (const int status = enqueue([&] {
         return awq_mxfp4_dequantize((const uint8_t*)c.codes->const_data_ptr(), c.ld,
                                (const uint8_t*)c.scales->const_data_ptr(), c.lds, c.rows, cols, type,
                                y.mutable_data_ptr(), cols, p.stream());
       }))
-    return none();
+    return failed(status, "awq_mxfp4_dequantize");
   return THPVariable_Wrap(y);
   END_HANDLE_TH_ERRORS
 }
@@ -302,14 +316,14 @@ PyObject* mxfp4_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const void* bias = vector(a[5], p, st, w.rows, &ok);
   if (!ok) return none();
   Tensor y = p.empty({x.rows, w.rows}, st);
-  if (enqueue([&] {
+  if (const int status = enqueue([&] {
         return awq_mxfp4_matmul((const uint8_t*)x.codes->const_data_ptr(), x.ld,
                            (const uint8_t*)x.scales->const_data_ptr(), x.lds, x.rows,
                            (const uint8_t*)w.codes->const_data_ptr(), w.ld,
                            (const uint8_t*)w.scales->const_data_ptr(), w.lds, w.rows, 2 * x.bytes, bias, type,
                            y.mutable_data_ptr(), w.rows, p.stream());
       }))
-    return none();
+    return failed(status, "awq_mxfp4_matmul");
   return THPVariable_Wrap(y);
   END_HANDLE_TH_ERRORS
 }
@@ -332,13 +346,13 @@ PyObject* mxfp4_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Tensor y = p.empty({T, M}, x->scalar_type()), ws;
   const size_t need = awq_mxfp4_linear_workspace_bytes(T, M, K);
   if (need) ws = p.empty({(int64_t)need}, at::kByte);
-  if (enqueue([&] {
+  if (const int status = enqueue([&] {
         return awq_mxfp4_linear(x->const_data_ptr(), ldx, (const float*)s, T, (const uint8_t*)w.codes->const_data_ptr(),
                            w.ld, (const uint8_t*)w.scales->const_data_ptr(), w.lds, M, K, bias,
                            type_of(x->scalar_type()), y.mutable_data_ptr(), M,
                            need ? ws.mutable_data_ptr() : nullptr, need, p.stream());
       }))
-    return none();
+    return failed(status, "awq_mxfp4_linear");
   return THPVariable_Wrap(y);
   END_HANDLE_TH_ERRORS
 }
