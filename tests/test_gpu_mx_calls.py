@@ -9,8 +9,10 @@ import sys
 
 import pytest
 
+import weight_only_quantization_act_amd as awq
 from tests.conftest import ROOT
 from tests.gpu_util import requires_gpu, say
+from tests.test_mx_calls_host import CALLS
 
 pytestmark = [pytest.mark.gpu, requires_gpu]
 
@@ -75,3 +77,16 @@ def test_failed_launches_are_reported_once(tmp_path):
     res = subprocess.run([sys.executable, str(tmp_path / "child.py"), str(fake)], cwd=ROOT, capture_output=True,
                          text=True, timeout=100, env={**os.environ, "PYTHONPATH": ROOT})
     assert res.returncode == 0 and "done" in res.stdout, res.stderr[-3000:]
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_first_arguments(name):
+    """What is refused without a GPU is refused with one."""
+    say(f"first arguments of {name}")
+    call, (first, args, more) = getattr(awq, name), CALLS[name]
+    for kw in ({}, more):
+        with pytest.raises(ValueError, match="device"):
+            call(first, *args, **kw)
+        for bad in (3.0, 0, None, [1], "x"):
+            with pytest.raises(TypeError, match="torch.Tensor"):
+                call(bad, *args, **kw)

@@ -20,7 +20,7 @@ from ._serve import (AWQ_FOLD_DIVIDE, AWQ_FOLD_MULTIPLY, AWQ_FP32, _FP32, _I8, _
                      _round16, _workspace, lib)
 
 _empty = torch.empty_strided
-_device = torch._C._cuda_getDevice
+_current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _C = None
 _N = None
@@ -45,24 +45,24 @@ def _native():
     return _N
 
 
+def _device(first) -> int:
+    """The current device, for a call with this first argument."""
+    if not isinstance(first, torch.Tensor):
+        raise TypeError("the first argument must be a torch.Tensor")
+    if not first.is_cuda:
+        raise ValueError("the first argument must be a device (HIP) tensor")
+    return _current_device()
+
+
 def _elsewhere(fn, stream, first, *args, **kwargs):
     """Run an entry point with `stream` (when given) as torch's current stream, or with the device of its
     first argument as the current one, so that what it allocates belongs to the stream that the kernels
     are enqueued on."""
-    if not isinstance(first, torch.Tensor):
-        raise TypeError("the first argument must be a torch.Tensor")
-    if not first.is_cuda:
-        raise ValueError("tensors must be device (HIP) tensors")
     if stream is not None:
         with torch.cuda.stream(stream):
             return fn(first, *args, **kwargs)
     with torch.cuda.device(first.device):
         return fn(first, *args, **kwargs)
-
-
-def _away(t, dev: int) -> bool:
-    """Whether t is anything but a tensor on device dev."""
-    return getattr(t, "get_device", int)() != dev or not t.is_cuda
 
 
 def _matrix(t: torch.Tensor, name: str, dtype: Optional[torch.dtype], dev: int) -> int:
@@ -152,8 +152,8 @@ def awq_int8_dequantize(codes: torch.Tensor, steps: torch.Tensor, cols: int,
         y = (_N or _native()).int8_dequantize(codes, steps, cols, dtype)
         if y is not None:
             return y
-    dev = _device()
-    if stream is not None or _away(codes, dev):
+    dev = _device(codes)
+    if stream is not None or codes.get_device() != dev:
         return _elsewhere(awq_int8_dequantize, stream, codes, steps, cols, dtype, out)
     ld = _matrix(codes, "codes", _I8, dev)
     R, nc = codes.shape
@@ -181,8 +181,8 @@ def awq_mxfp4_quantize(A: torch.Tensor, s: Optional[torch.Tensor] = None, fold: 
         got = (_N or _native()).mxfp4_quantize(A, s, multiply)
         if got is not None:
             return got
-    dev = _device()
-    if stream is not None or _away(A, dev):
+    dev = _device(A)
+    if stream is not None or A.get_device() != dev:
         return _elsewhere(awq_mxfp4_quantize, stream, A, s, fold)
     lda = _matrix(A, "A", None, dev)
     dt = _dtype(A.dtype, "A")
@@ -207,8 +207,8 @@ def awq_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: int,
         y = (_N or _native()).mxfp4_dequantize(codes, scales, cols, dtype)
         if y is not None:
             return y
-    dev = _device()
-    if stream is not None or _away(codes, dev):
+    dev = _device(codes)
+    if stream is not None or codes.get_device() != dev:
         return _elsewhere(awq_mxfp4_dequantize, stream, codes, scales, cols, dtype, out)
     R, nb, ld, lds = _codes(codes, scales, ("codes", "scales"), dev)
     if cols < 0 or nb != 16 * _blocks(cols):
@@ -240,8 +240,8 @@ def awq_mxfp4_matmul(xc: torch.Tensor, xs: torch.Tensor, wc: torch.Tensor, ws: t
         y = (_N or _native()).mxfp4_matmul(xc, xs, wc, ws, dtype, bias)
         if y is not None:
             return y
-    dev = _device()
-    if stream is not None or _away(xc, dev):
+    dev = _device(xc)
+    if stream is not None or xc.get_device() != dev:
         return _elsewhere(awq_mxfp4_matmul, stream, xc, xs, wc, ws, dtype, bias, out)
     T, nb, ldx, ldxs = _codes(xc, xs, ("xc", "xs"), dev)
     M, nw, ldw, ldws = _codes(wc, ws, ("wc", "ws"), dev)
@@ -273,8 +273,8 @@ def awq_mxfp4_linear(x: torch.Tensor, wc: torch.Tensor, ws: torch.Tensor,
         y = (_N or _native()).mxfp4_linear(x, wc, ws, s, bias)
         if y is not None:
             return y
-    dev = _device()
-    if stream is not None or _away(x, dev):
+    dev = _device(x)
+    if stream is not None or x.get_device() != dev:
         return _elsewhere(awq_mxfp4_linear, stream, x, wc, ws, s, bias, out, workspace)
     ldx = _matrix(x, "x", None, dev)
     dtype = x.dtype
@@ -335,8 +335,8 @@ def awq_rmsnorm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: flo
         got = (_N or _native()).rmsnorm(x, weight, eps, residual)
         if got is not None:
             return got
-    dev = _device()
-    if stream is not None or _away(x, dev):
+    dev = _device(x)
+    if stream is not None or x.get_device() != dev:
         return _elsewhere(awq_rmsnorm, stream, x, weight, eps, residual=residual, h_out=h_out, out=out)
     args, h = _norm_args(x, weight, eps, residual, h_out, dev)
     y, ldy = _out(out, args[4], args[5], x.dtype, x, dev)
@@ -356,8 +356,8 @@ def awq_rmsnorm_int8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps
         got = (_N or _native()).rmsnorm_int8(x, weight, eps, residual)
         if got is not None:
             return got
-    dev = _device()
-    if stream is not None or _away(x, dev):
+    dev = _device(x)
+    if stream is not None or x.get_device() != dev:
         return _elsewhere(awq_rmsnorm_int8, stream, x, weight, eps, residual=residual, h_out=h_out)
     args, h = _norm_args(x, weight, eps, residual, h_out, dev)
     R, nc = args[4], _round16(args[5])
@@ -380,8 +380,8 @@ def awq_rmsnorm_mxfp4(x: torch.Tensor, weight: Optional[torch.Tensor] = None, ep
         got = (_N or _native()).rmsnorm_mxfp4(x, weight, eps, residual)
         if got is not None:
             return got
-    dev = _device()
-    if stream is not None or _away(x, dev):
+    dev = _device(x)
+    if stream is not None or x.get_device() != dev:
         return _elsewhere(awq_rmsnorm_mxfp4, stream, x, weight, eps, residual=residual, h_out=h_out)
     args, h = _norm_args(x, weight, eps, residual, h_out, dev)
     R, K = args[4], args[5]

@@ -34,6 +34,10 @@ struct Place {
 
 int type_of(at::ScalarType t) { return t == at::kHalf ? AWQ_FP16 : t == at::kBFloat16 ? AWQ_BF16 : -1; }
 
+// Whether an argument is a tensor of a GPU: looked at before the current device, which there is none of on
+// a machine without one.
+bool on_gpu(PyObject* o) { return THPVariable_Check(o) && THPVariable_Unpack(o).is_cuda(); }
+
 // The tensor that a Python object is, or NULL; it has to be on the call's device.
 const Tensor* tensor(PyObject* o, const Place& p) {
   if (!THPVariable_Check(o)) return nullptr;
@@ -176,7 +180,7 @@ PyObject* triple(PyObject* a, PyObject* b, PyObject* c) {
 
 PyObject* rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (n != 4) return none();
+  if (n != 4 || !on_gpu(a[0])) return none();
   const Place p;
   Norm m(a, p);
   if (!m.ok) return none();
@@ -193,7 +197,7 @@ PyObject* rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 PyObject* rmsnorm_int8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (n != 4) return none();
+  if (n != 4 || !on_gpu(a[0])) return none();
   const Place p;
   Norm m(a, p);
   if (!m.ok) return none();
@@ -212,7 +216,7 @@ PyObject* rmsnorm_int8(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 PyObject* rmsnorm_mxfp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (n != 4) return none();
+  if (n != 4 || !on_gpu(a[0])) return none();
   const Place p;
   Norm m(a, p);
   if (!m.ok) return none();
@@ -233,7 +237,7 @@ PyObject* rmsnorm_mxfp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // (codes, steps, cols, dtype)
 PyObject* int8_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (n != 4 || !PyLong_CheckExact(a[2])) return none();
+  if (n != 4 || !on_gpu(a[0]) || !PyLong_CheckExact(a[2])) return none();
   const Place p;
   int64_t ld;
   const Tensor* codes = matrix(a[0], p, &ld);
@@ -260,7 +264,7 @@ PyObject* int8_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // (A, s, multiply)
 PyObject* mxfp4_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (n != 3) return none();
+  if (n != 3 || !on_gpu(a[0])) return none();
   const Place p;
   int64_t lda;
   const Tensor* A = matrix(a[0], p, &lda);
@@ -283,7 +287,7 @@ PyObject* mxfp4_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // (codes, scales, cols, dtype)
 PyObject* mxfp4_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (n != 4 || !PyLong_CheckExact(a[2])) return none();
+  if (n != 4 || !on_gpu(a[0]) || !PyLong_CheckExact(a[2])) return none();
   const Place p;
   const Codes c(a[0], a[1], p);
   const int64_t cols = PyLong_AsLongLong(a[2]);
@@ -306,7 +310,7 @@ PyObject* mxfp4_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // (xc, xs, wc, ws, dtype, bias)
 PyObject* mxfp4_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (n != 6) return none();
+  if (n != 6 || !on_gpu(a[0])) return none();
   const Place p;
   const Codes x(a[0], a[1], p), w(a[2], a[3], p);
   at::ScalarType st;
@@ -331,7 +335,7 @@ PyObject* mxfp4_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // (x, wc, ws, s, bias)
 PyObject* mxfp4_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (n != 5) return none();
+  if (n != 5 || !on_gpu(a[0])) return none();
   const Place p;
   int64_t ldx;
   const Tensor* x = matrix(a[0], p, &ldx);
