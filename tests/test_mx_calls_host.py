@@ -1,4 +1,6 @@
 """The binding of the norm and of MXFP4 on the host: what it refuses and how it says so, without a GPU."""
+import types
+
 import pytest
 import torch
 
@@ -31,3 +33,30 @@ def test_first_arguments(name, longer):
     for bad in (3.0, 0, None, [1], "x"):
         with pytest.raises(TypeError, match="torch.Tensor"):
             call(bad, *args, **kw)
+
+
+class Elsewhere(torch.Tensor):
+    """A host tensor that says it is on a GPU: for checks that come before any use of it."""
+    at = 0
+    is_cuda = True
+    device = property(lambda self: torch.device("cuda", self.at))
+
+    def get_device(self):
+        return self.at
+
+
+def _claimed(value):
+    return value.as_subclass(Elsewhere) if isinstance(value, torch.Tensor) else value
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_stream_of_another_device_is_refused(name, monkeypatch):
+    """It would run on its tensors' device, on that device's current stream."""
+    from weight_only_quantization_act_amd import _mx
+    call, (first, args, more) = getattr(awq, name), CALLS[name]
+    for current in (0, 1):
+        monkeypatch.setattr(_mx, "_current_device", lambda: current)
+        for kw in ({}, more):
+            with pytest.raises(ValueError, match="stream"):
+                call(_claimed(first), *map(_claimed, args), **{k: _claimed(v) for k, v in kw.items()},
+                     stream=types.SimpleNamespace(device=torch.device("cuda", 1)))

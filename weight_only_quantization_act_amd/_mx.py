@@ -59,6 +59,8 @@ def _elsewhere(fn, stream, first, *args, **kwargs):
     first argument as the current one, so that what it allocates belongs to the stream that the kernels
     are enqueued on."""
     if stream is not None:
+        if stream.device != first.device:
+            raise ValueError(f"stream is of {stream.device}, the tensors are on {first.device}")
         with torch.cuda.stream(stream):
             return fn(first, *args, **kwargs)
     with torch.cuda.device(first.device):
