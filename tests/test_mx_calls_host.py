@@ -1,5 +1,8 @@
 """The binding of the norm and of MXFP4 on the host: what it refuses and how it says so, without a GPU."""
+import sys
+import sysconfig
 import types
+import warnings
 
 import pytest
 import torch
@@ -60,3 +63,71 @@ def test_stream_of_another_device_is_refused(name, monkeypatch):
             with pytest.raises(ValueError, match="stream"):
                 call(_claimed(first), *map(_claimed, args), **{k: _claimed(v) for k, v in kw.items()},
                      stream=types.SimpleNamespace(device=torch.device("cuda", 1)))
+
+
+def test_calls_without_the_extension_module(monkeypatch):
+    """The binding needs the library alone: without the module calls go the longer way, said once."""
+    from weight_only_quantization_act_amd import _mx
+    monkeypatch.delattr(awq, "_calls", raising=False)
+    monkeypatch.setitem(sys.modules, awq.__name__ + "._calls", None)
+    monkeypatch.setattr(_mx, "_N", None)
+    with pytest.warns(RuntimeWarning, match="_calls"):
+        with pytest.raises(ValueError, match="device"):
+            awq.awq_rmsnorm(X)
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        for name, (first, args, more) in CALLS.items():
+            with pytest.raises(ValueError, match="device"):
+                getattr(awq, name)(first, *args)
+
+
+@pytest.fixture
+def building(tmp_path, monkeypatch):
+    """The build in an empty folder, its commands written down in place of being run."""
+    from weight_only_quantization_act_amd import build
+    ran = []
+
+    def run(cmd):
+        if build.broken and any(build.broken in c for c in cmd):
+            raise RuntimeError(build.broken)
+        ran.append(cmd)
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write("new")
+        return ""
+    monkeypatch.setattr(build, "broken", "", raising=False)
+    monkeypatch.setattr(build, "PKG", str(tmp_path))
+    monkeypatch.setattr(build, "BUILD", str(tmp_path / "_build"))
+    monkeypatch.setattr(build, "CALLS", str(tmp_path / "_calls.so"))
+    monkeypatch.setattr(build, "_run", run)
+    (tmp_path / "_calls.so").write_text("old")
+    (tmp_path / build.LIB_NAME).write_text("old")
+    return build, ran, tmp_path
+
+
+def test_build(building):
+    build, ran, where = building
+    assert build.build() == str(where / build.LIB_NAME)
+    assert (where / build.LIB_NAME).read_text() == "new" and (where / "_calls.so").read_text() == "new"
+    assert sum("calls.cpp" in c for cmd in ran for c in cmd) >= 1
+
+
+def test_build_without_header_files(building, monkeypatch, tmp_path):
+    """The library is built where Python's header files, which it does not need, are not installed; a module on top
+    of the library before does not stay."""
+    build, ran, where = building
+    get = sysconfig.get_path
+    monkeypatch.setattr(build.sysconfig, "get_path", lambda n, *a, **k: str(tmp_path / "none") if n == "include"
+                        else get(n, *a, **k))
+    build.broken = "calls.cpp"                                  # as the compiler would without them
+    assert build.build() == str(where / build.LIB_NAME)
+    assert (where / build.LIB_NAME).read_text() == "new" and not (where / "_calls.so").exists()
+
+
+@pytest.mark.parametrize("step", ["calls.cpp", "-ltorch_python"])
+def test_build_whose_module_fails(building, step):
+    """An error in the module's own build is one, with the library in place."""
+    build, ran, where = building
+    build.broken = step
+    with pytest.raises(RuntimeError, match=step):
+        build.build()
+    assert (where / build.LIB_NAME).read_text() == "new" and not (where / "_calls.so").exists()

@@ -11,6 +11,7 @@ the current stream) goes through one step of native code, the extension module _
 from __future__ import annotations
 
 import functools
+import warnings
 from typing import Optional
 
 import torch
@@ -32,6 +33,12 @@ def _lib():
     return _C
 
 
+class _NoCalls:
+    """In the extension module's place: it takes no call."""
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 def _native():
     """The extension module, after the library that it calls."""
     global _N
@@ -39,8 +46,10 @@ def _native():
     try:
         from . import _calls
     except ImportError as e:
-        raise RuntimeError("the extension module _calls is missing or does not fit this interpreter: build it "
-                           "with `python -m weight_only_quantization_act_amd.build`") from e
+        warnings.warn(f"the extension module _calls is missing or does not fit ({e}): calls of the norm and of MXFP4 "
+                      "take some microseconds more; build it with "
+                      "`python -m weight_only_quantization_act_amd.build`", RuntimeWarning, stacklevel=3)
+        _calls = _NoCalls()
     _N = _calls
     return _N
 

@@ -4,8 +4,9 @@
 
 Compiles every .hip file under csrc/ with hipcc for gfx950 and the host-only C ABI
 (api.cpp), then links one shared library next to this file, and an extension module of this
-interpreter on top of it (csrc/python/, the short way from a Python call to the C ABI).  Always
-recompiles.
+interpreter on top of it (csrc/python/, the short way from a Python call to the C ABI).  Where the
+header files that the module needs are not installed only the library is built; the binding does without
+the module.  Always recompiles.
 """
 from __future__ import annotations
 
@@ -45,15 +46,26 @@ HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__",
               f"-I{ROCM}/include"]
 
 
-# The extension module: its header files are torch's and Python's.
+# The extension module.
 CALLS = os.path.join(PKG, "_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 
-def _torch_dirs():
+def _calls_commands(clangxx, incs):
+    """The commands that compile and link the extension module, or None where the header files of Python or of
+    torch on HIP are missing."""
     import torch
     at = os.path.dirname(torch.__file__)
-    return ([os.path.join(at, "include"), os.path.join(at, "include", "torch", "csrc", "api", "include")],
-            os.path.join(at, "lib"), int(torch.compiled_with_cxx11_abi()))
+    python = sysconfig.get_path("include")
+    dirs = [os.path.join(at, "include"), os.path.join(at, "include", "torch", "csrc", "api", "include")]
+    if not (torch.version.hip and os.path.exists(os.path.join(python, "Python.h"))
+            and os.path.exists(os.path.join(dirs[0], "ATen", "hip", "EmptyTensor.h"))):
+        return None
+    obj = os.path.join(BUILD, "calls.cpp.o")
+    return ([clangxx, *HOST_FLAGS, "-DUSE_ROCM", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+             *incs, f"-I{python}", *(f"-isystem{d}" for d in dirs), "-c", os.path.join(CSRC, "python", "calls.cpp"),
+             "-o", obj],
+            [clangxx, "-shared", "-fPIC", obj, "-o", CALLS + ".tmp", f"-L{os.path.join(at, 'lib')}", "-ltorch_python",
+             "-ltorch_cpu", "-ltorch_hip", "-lc10", "-lc10_hip", f"-L{PKG}", f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN"])
 
 
 def _run(cmd):
@@ -83,26 +95,26 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
                               "-o", obj])
         elif f.endswith(".cpp"):
             jobs_list.append([clangxx, *HOST_FLAGS, *incs, "-c", src, "-o", obj])
-    dirs, torch_lib, abi = _torch_dirs()
-    calls_obj = os.path.join(BUILD, "calls.cpp.o")
-    calls = [clangxx, *HOST_FLAGS, "-DUSE_ROCM", f"-D_GLIBCXX_USE_CXX11_ABI={abi}", *incs,
-             f"-I{sysconfig.get_path('include')}", *(f"-isystem{d}" for d in dirs), "-c",
-             os.path.join(CSRC, "python", "calls.cpp"), "-o", calls_obj]
-    jobs_list.append(calls)
+    calls = _calls_commands(clangxx, incs)
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        calls_out = ex.submit(_run, calls[0]) if calls else None
         outs = list(ex.map(_run, jobs_list))
+    if os.path.exists(CALLS):
+        os.remove(CALLS)  # it fits the library before
+    tmp = lib_path() + ".tmp"
+    _run([hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *(cmd[-1] for cmd in jobs_list), "-o", tmp,
+          f"-L{ROCM}/lib", "-lamdhip64"])
+    os.replace(tmp, lib_path())
+    if calls:  # with the library in place, whatever happens here
+        outs.append(calls_out.result())
+        _run(calls[1])
+        os.replace(CALLS + ".tmp", CALLS)
+    else:
+        print("header files of Python or of torch on HIP not found: built without the extension module _calls")
     if verbose:
         for o in outs:
             if o.strip():
                 print(o)
-    objs = [cmd[-1] for cmd in jobs_list if cmd is not calls]
-    tmp = lib_path() + ".tmp"
-    _run([hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp,
-          f"-L{ROCM}/lib", "-lamdhip64"])
-    os.replace(tmp, lib_path())
-    _run([clangxx, "-shared", "-fPIC", calls_obj, "-o", CALLS + ".tmp", f"-L{torch_lib}", "-ltorch_python",
-          "-ltorch_cpu", "-ltorch_hip", "-lc10", "-lc10_hip", f"-L{PKG}", f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN"])
-    os.replace(CALLS + ".tmp", CALLS)
     if verbose:
         print("built", lib_path())
     return lib_path()
