@@ -54,3 +54,25 @@ def test_linear_with_scales_behind_the_last_block(T):
     w2 = _behind(ws, K, 255)
     assert torch.equal(awq.awq_mxfp4_linear(x, wc, w2), want)
     assert torch.equal(awq.awq_mxfp4_dequantize(wc, w2, K), awq.awq_mxfp4_dequantize(wc, ws, K))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("M,K", [(300, 17632), (4096, 17601), (5000, 7744), (8192, 7001), (33, 11008)])
+def test_linear_of_one_token_at_its_longest(M, K, dtype):
+    """The most columns that one token is quantised inside the product's launch for: no workspace, the two calls'
+    result bit for bit; one block more takes two launches."""
+    say(f"mxfp4 linear of one token M={M} K={K} {dtype}")
+    assert awq.awq_mxfp4_linear_workspace_bytes(1, M, K) == 0
+    most = 17632 if M <= 4096 else 7744
+    assert awq.awq_mxfp4_linear_workspace_bytes(1, M, most) == 0
+    assert awq.awq_mxfp4_linear_workspace_bytes(1, M, most + 1) > 0
+    wc, ws = awq.awq_mxfp4_quantize((torch.randn(M, K, device="cuda") * 0.02).to(dtype))
+    s = torch.exp(torch.randn(K, device="cuda") * 0.5)
+    x = torch.randn(1, K, device="cuda").to(dtype)
+    bias = torch.randn(M, device="cuda").to(dtype)
+    for scale in (None, s):
+        got = awq.awq_mxfp4_linear(x, wc, ws, s=scale, bias=bias)
+        want = awq.awq_mxfp4_matmul(*awq.awq_mxfp4_quantize(x, scale), wc, ws, dtype=dtype, bias=bias)
+        assert torch.equal(got, want) and got.isfinite().all()
+    x[0, K - 1] = float("nan")
+    assert awq.awq_mxfp4_linear(x, wc, ws, s=s).isnan().all()

@@ -60,7 +60,6 @@ struct MxTile {
   static constexpr int KG = KG_, NS = NS_;  // groups of waves, which take the steps in turn, stages of each
   static constexpr bool WHOLE = WHOLE_;     // a stage's operands are read one stage ahead (else an instruction)
   static constexpr int BK = 128;            // bytes of K a stage
-  static constexpr int KS = 4;
   static constexpr int WAVES = WT * WM, THREADS = 64 * WAVES * KG;
   static constexpr int TI = BT / WT / 32, MI = BM / WM / 32;
   static constexpr int X_BYTES = BT * BK, CODES = (BT + BM) * BK;
@@ -665,9 +664,9 @@ hipError_t launch_mxfp4_matmul(const MxArgs& a, hipStream_t stream) {
 // Where tokens times columns are few.  Fused and in two launches, in us, without scales and with: 2 tokens of
 // 4096 x 4096 5.1, 6.7 and 5.7, 6.9; 4 of it 5.6, 6.9 and 6.4, 7.1; 8 of it 7.1, 7.1 and 8.6, 7.3; 4 of 6144 x 4096
 // 7.4, 8.3 and 8.7, 8.5; 2 of 4096 x 11008 10.0, 9.6 and 11.7, 9.9; 16 of 8192 x 1024 4.8, 5.2 and 6.1, 5.5.
+// (One token: wherever the product streams, at most 17632 columns, 9.3 KiB of LDS.)
 bool mxfp4_linear_fused(int64_t T, int64_t M, int64_t cols) {
-  return (T == 1 ? cols <= 65536 : T <= 16 && T * cols <= 16384) &&
-         mxfp4_form(T, M, (cols + 31) / 32 * 16) == kMxFew;
+  return (T == 1 || (T <= 16 && T * cols <= 16384)) && mxfp4_form(T, M, (cols + 31) / 32 * 16) == kMxFew;
 }
 
 hipError_t launch_mxfp4_linear_fused(const MxArgs& a, const void* x, int64_t ldx, const float* s,
