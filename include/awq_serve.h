@@ -233,7 +233,8 @@ int awq_mxfp4_dequantize(const uint8_t* codes, int64_t ld_codes, const uint8_t* 
  * to an fp32 sum (products of two elements are exact; each such step rounds within 2^-22 of its largest
  * term or result); the sums of waves that share the columns are added in a fixed order, the bias in
  * fp32, and the result is rounded once to the output type.  Results repeat bit for bit.  A scale of 255 in a
- * row makes the row's results NaN.
+ * row makes the row's results NaN.  Terms and sums keep fp32's subnormals; where a sum leaves fp32's range
+ * on the way the result is infinite or NaN (unless its terms cancel within one step).
  *   xc, xs  tokens' codes and scales, wc, ws the weights', as awq_mxfp4_quantize lays them out.
  *           Columns from in_features up to a whole block are read: they must be zero in one of the two.
  *           Scale bytes behind a row's last block are not looked at
@@ -265,13 +266,14 @@ int awq_mxfp4_linear(const void* x, int64_t ldx, const float* s, int64_t n_token
  * Root-mean-square norm with the residual's addition
  *   h[r][i] = x[r][i] + residual[r][i], rounded to dtype (x itself without a residual)
  *   v[r][i] = h[r][i] weight[i] / sqrt(mean_i h[r][i]^2 + eps), rounded to fp32 (the sum and the
- *             products are formed in fp64)
+ *             products are formed in fp64, within (cols / 1024 + 29) 2^-53 of the formula's value)
  * and from v, by entry point: y = v rounded to dtype; the row's 8-bit codes and step as
  * awq_int8_quantize makes them of fp32 values v; its MXFP4 codes and scales as awq_mxfp4_quantize does.
  * The scales of a search are folded into the weight (weight / s) [AWQ-notes §4.3].  A row of h
  * that holds a NaN or an infinity comes out as NaN whole (8 bits: step NaN and codes 0; MXFP4: scales
- * 255 and codes 0); so does, in 8 bits, every row if the weight holds one.  Sums are taken in a
- * fixed order: results repeat bit for bit.
+ * 255 and codes 0); so does, in 8 bits, every row if the weight holds one.  Sums are taken in an
+ * order that the sizes fix: results repeat bit for bit.  (Rows by the thousand are added in another order than a
+ * few; a value within the error above of the middle of two fp32 numbers can be the other one there.)
  *   x, residual  fp16 or bf16 [rows][cols] of one type, row strides ldx, ldr >= cols; residual NULL: none
  *   weight       [cols] in dtype or fp32 (weight_dtype AWQ_FP32), or NULL: ones
  *   eps          finite, at least 2^-126

@@ -4,10 +4,13 @@
 // Pages: "AWQ" scholia-log notes §4.3 (S^-1 folded into the preceding operation: the norm's weight
 // takes it), §2.3 (the quantiser of a row).
 //
-// Codes are decided at borders between values, so v is defined as the formula's value rounded to fp32
-// once: squares of 16-bit values are exact in fp64 and summed there, the product h w (11 + 24 bits) is
-// exact there, and v = fp32((h w) r) with r to within two ulp of fp64.  What of this is fp64 costs a few
-// instructions a value at fp32's rate.  Each value is read once (and the residual, and the sum written)
+// Codes are decided at borders between values, so v is the formula's value rounded to fp32 once, but for
+// what fp64 leaves open: squares of 16-bit values are exact in fp64 and summed there, the product h w (11 +
+// 24 bits) is exact there, and v = fp32((h w) r).  A thread adds its n squares one by one, n at most 32 or K /
+// 512 + 8, so the sum lies within (n + 13) 2^-53 of itself, r, whose error is half of that and of the mean's two
+// roundings, and the product within (n / 2 + 13) 2^-53 <= (K / 1024 + 29) 2^-53: only a value that close to the
+// middle of two fp32 numbers can come out as the other one, and differ between forms.  What of this is fp64
+// costs a few instructions a value at fp32's rate.  Each value is read once (and the residual, and the sum written)
 // and stays in registers between the sum and the rounding; rows too long for that are read a second
 // time, from cache.  Large calls are bound by memory (16384 rows of 8192 in bf16 with a residual to MXFP4
 // 168 us, 877 MB at 5.2 TB/s), calls of a few thousand rows by their vector instructions and one
