@@ -18,17 +18,16 @@
 // the second (token).  Rows past the matrices and chunks past K arrive as zeros, or as scales of rows
 // that are dropped.
 //
-// Large products run at the power limit: 8192 tokens of 28672 x 8192 939-962 us, 4.0-4.1
-// PFLOP/s (matrix cores
-// busy 54% of the cycles at 1.81 GHz; the same instructions alone on the same data 6.2 PFLOP/s; without
+// Large products run at the power limit: 8192 tokens of 28672 x 8192 939-962 us, 4.0-4.1 PFLOP/s (matrix
+// cores busy 54% of the cycles at 1.81 GHz; the same instructions alone on the same data 6.2 PFLOP/s; without
 // the refills the loop takes 16% less, without its LDS reads 10%, without waiting for the refills nothing).
 // Not faster, in us on 859 of the kernel alone: four waves of 128 x 128 with a third fewer LDS reads 910,
 // operand reads placed between the products by hand 885, the loop over one stage with its slot in a
 // register 851 (128 x 128 tiles 22.2 for 21.3), bands of 4, 6 and 16 tiles 855, 856, 866, stages of 64
 // bytes, instructions of 16 x 16 x 128.  Products with a tile or two a compute unit are bound by each step's
-// chain of barrier, products, reads and refills (333 tokens of 5120 x 13824 21.2 us, 2.2 PFLOP/s, 0.35 us a
-// step; matrix cores busy 17%; the refills alone would take 0.24): neither fewer LDS reads, deeper rings
-// nor two stages a barrier shorten it.
+// chain of barrier, products, reads and refills (333 tokens of 5120 x 13824 21.2-22.2 us, 2.1-2.2 PFLOP/s, 0.35
+// us a step; matrix cores busy 17%; the refills alone would take 0.24; weights that no cache holds 27.7): neither
+// fewer LDS reads, deeper rings nor two stages a barrier shorten it.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -435,8 +434,9 @@ __global__ __launch_bounds__(S::THREADS) void k_mxfp4_tiles(MxArgs a, int tiles_
 // this one; the tokens' operands come from L2.  The waves' fp32 sums are added through LDS in their
 // order.  Result element e of lane l is output 4 (l div 16) + e, token l mod 16.
 //
-// One token through 4096 x 4096 with its quantisation 4.6 us (9 MB: 1.9 TB/s with start and end of the
-// launch); the product alone 4.1 us, of 16 tokens 4.9, of 17 5.1 (tiles 6.0).
+// One token through 4096 x 4096 with its quantisation and scales 5.4 us, without scales 5.0 (9 MB: 1.9 TB/s with
+// start and end of the launch), the product alone 4.6, of 16 tokens 5.3, of 17 5.6; 1.2 less where the
+// weights are in the last-level cache.
 //
 // FUSED > 0: the block first quantises the tokens into LDS, a lane 8 columns of so many tokens together, with
 // the first weights already on their way; every block repeats that (a few thousand values from L2) in place of

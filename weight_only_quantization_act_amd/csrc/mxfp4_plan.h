@@ -14,7 +14,8 @@ enum { kMxFew, kMxTile32K, kMxTile32x64K, kMxTile64K, kMxTile64, kMxTile64x128, 
 // KB: bytes of codes a row (two columns a byte).
 //
 // Few: blocks of 16 outputs, one or two a compute unit, while what each reads stays small: its weights (as
-// much as 16 tokens) and all tokens' operands.  Measured, streaming and the best tiles, in us:
+// much as 16 tokens) and all tokens' operands.  Measured, streaming and the best tiles, in us (weights in
+// the last-level cache):
 //   tokens              1         8         16        32
 //   4096 x 4096         4.1, 5.4  4.6, 5.9  4.9, 6.0  5.9, 5.9
 //   4096 x 11008        6.5, 7.7  7.3, 7.8  8.2, 7.9  10.8, 7.9
@@ -23,7 +24,12 @@ enum { kMxFew, kMxTile32K, kMxTile32x64K, kMxTile64K, kMxTile64, kMxTile64x128, 
 //   8192 x 3584                   5.5, 5.9  6.1, 6.0  7.9, 6.1
 //   8192 x 8192                   9.8, 7.7  11.2, 8.1 15.0, 8.7
 //   11008 x 4096        6.8, 6.3            8.4, 6.4  11.4, 6.4
-// (One token's limit is larger: its linear layer saves a launch where the product streams.)
+// One token's limit past 4096 outputs is larger: its linear layer saves a launch where the product streams. The
+// product, streamed and tiles, and the linear layer with scales, in one launch and in two with tiles (other
+// weights each call):
+//   5120 x 4096         5.8, 6.1  6.7, 8.3        8192 x 7744         9.4, 9.7  11.3, 12.4
+//   5120 x 7744         8.6, 8.3  10.6, 11.0      past it: 5120 x 8192 9.4, 8.1  12.0, 10.4
+//   6144 x 7744         8.8, 8.7  10.8, 11.3               8192 x 8192 9.8, 10.2 14.3, 12.6
 //
 // Tiles: the form with the smallest time a step of 256 columns, fitted to measurements (us a step at r
 // tiles a compute unit; small tiles are bound by what goes through LDS, 128 x 128 ones run in rounds of two

@@ -3,10 +3,11 @@
 // Pages: "AWQ" scholia-log notes §2.3 (a group's range sets its step, values round to the grid), §4.3
 // (S^-1 folded into the activations).  The format is the OCP microscaling one: see mx_format.h.
 //
-// Bound by memory: 2 bytes of every value in, 17/32 out.  A block takes 8 rows of 512 columns, each
-// wave two rows with its 512 columns, so that loads are 1 KiB in one piece and the fold's scales
-// serve two rows.  28672 rows of 8192 times scales 104-121 us (595 MB, 4.9-5.7 TB/s), divided by them 124-130
-// us (the vector instructions of the reciprocals), back 92-95 us.
+// Bound by memory: 2 bytes of every value in, 17/32 out.  A block takes 8 rows of 512 columns, each wave two
+// of them, so that loads are 1 KiB in one piece and the fold's scales serve two rows; 16 rows, four a wave,
+// where many rows are divided by scales and in both ways back.  28672 rows of 8192 times scales 101-121 us (595
+// MB, 4.9-5.9 TB/s), divided by them 124-130 us (the vector instructions of the reciprocals), back 92-95 us;
+// 8-bit rows of that size back 121 us (705 MB, 5.8 TB/s).
 #include <hip/hip_runtime.h>
 
 #include "grid.h"
@@ -18,9 +19,9 @@ namespace awq {
 
 namespace {
 
-// Rows a block, in us at 4, 8, 16 and 32: 28672 of 8192 times scales 129, 120, 125, 131; read back 110, 99, 95, 110.  Divided by scales, where a block has
-// their reciprocals to find first, and many rows 16: 28672 of 8192 at 8 and 16 158, 128, 4096 of 4096 11.4,
-// 10.5, but 333 of 13824 5.2 both, 50 of 4096 2.9, 3.5.
+// Rows a block, in us at 4, 8, 16 and 32: 28672 of 8192 times scales 129, 120, 125, 131; read back 110, 99,
+// 95, 110.  Divided by scales, where a block has their reciprocals to find first, and many rows 16: 28672 of
+// 8192 at 8 and 16 158, 128, 4096 of 4096 11.4, 10.5, but 333 of 13824 5.2 both, 50 of 4096 2.9, 3.5.
 constexpr int kRowsTile = 8, kDivideTile = 16, kValuesTile = 16;
 constexpr int kTileWords = 4;  // scale words (128 columns) of a row a block
 

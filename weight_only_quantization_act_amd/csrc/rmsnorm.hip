@@ -16,7 +16,9 @@
 // 168 us, 877 MB at 5.2 TB/s), calls of a few thousand rows by their vector instructions and one
 // pass of latencies (2047 rows of 5000 to MXFP4 11.4 us, 2.3 TB/s), few rows by the latencies alone (33 of
 // 5120 to 8 bits 4.6 us, one of 4096 2.4 us).  The 8-bit row's step needs the largest |v|:
-// rounding is monotone, so it is that of max |h w|, found beside the sum.
+// rounding is monotone, so it is that of max |h w|, found beside the sum; these products and, again, the codes'
+// bound many rows without a residual (16384 of 8192 with an fp32 weight 146 us of the 78 that the bytes
+// take, vector units busy 89%; with a residual 186 of 182).
 #include <hip/hip_runtime.h>
 
 #include "grid.h"
@@ -254,10 +256,10 @@ hipError_t launch_out(const NormArgs& a, hipStream_t stream) {
 #define AWQ_NORM(W, N)                                                                           \
   hipLaunchKernelGGL((k_rmsnorm<BF16, W32, OUT, W, N>), grid_of(W == 1 ? (a.rows + 3) / 4 : a.rows), \
                      dim3(W == 1 ? 256 : 64 * W), 0, stream, a)
-  // Waves a row, in us: few rows wait for their loads (1 of 8192 to MXFP4: two waves 9.8, four 5.6, eight
-  // 4.1; 256 of 5120 6.8, 5.3, 4.4), many want theirs close to full waves without a barrier among many
-  // (16384 of 256: one wave 8.7, two 11.2, four 15.7; of 1024 24.0, 23.8, 26.3; 4096 of 4096 to 8 bits 57,
-  // 30, 25.6, eight 27.6; 500 of 16000 four 16.6, eight 14.4).
+  // Waves a row, in us, with a residual and an fp32 weight: few rows wait for their loads (1 of 8192 to MXFP4:
+  // two waves 8.0, four 5.3, eight 4.0; 256 of 5120 7.0, 5.7, 5.0; 500 of 16000 four 16.7, eight 14.8), many want
+  // theirs close to full waves without a barrier among many (16384 of 256 to MXFP4: one wave 11.8, two 15.1, four
+  // 20.5; of 1024 24.3, 24.4, 28.7; 4096 of 4096 to 8 bits 65, 28.7, 25.1, eight 27.7).
   if (a.rows > 1024 && nch <= 64) AWQ_NORM(1, 1);
   else if (a.rows > 1024 && nch <= 128) AWQ_NORM(2, 1);
   else if (a.rows > 1024 && nch <= 256) AWQ_NORM(4, 1);
