@@ -12,7 +12,8 @@
  * Conventions are those of awq_act.h: device pointers owned by the caller, caller-provided
  * workspaces, work enqueued on `stream` without synchronising, status codes, every check on
  * the host before any launch, calls thread-safe given distinct workspaces.  Launches are
- * kernels only, so a call may be captured into a HIP graph.
+ * kernels only, so a call may be captured into a HIP graph.  Outputs of the norm and
+ * of the MXFP4 operators overlap neither inputs nor each other, but where a call says so.
  */
 #ifndef AWQ_SERVE_H
 #define AWQ_SERVE_H
@@ -279,7 +280,8 @@ int awq_mxfp4_linear(const void* x, int64_t ldx, const float* s, int64_t n_token
  *   eps          finite, at least 2^-126
  *   h_out        [rows][ldh >= cols], written where a residual is given (else not looked at); may be
  *                x or residual itself (same address and stride), or overlap neither
- *   y, codes_out, ...  as in the calls above, no input's memory
+ *   y            of awq_rmsnorm: may be x or residual itself, too, where h_out is not the same
+ *   codes_out, ...  as in the calls above, no input's memory
  * rows >= 0, cols 1 .. 2^31 - 512 (MXFP4: 2^22).
  * ---------------------------------------------------------------------------------- */
 int awq_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr, int64_t rows,

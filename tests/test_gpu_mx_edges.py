@@ -76,3 +76,25 @@ def test_linear_of_one_token_at_its_longest(M, K, dtype):
         assert torch.equal(got, want) and got.isfinite().all()
     x[0, K - 1] = float("nan")
     assert awq.awq_mxfp4_linear(x, wc, ws, s=s).isnan().all()
+
+
+@pytest.mark.parametrize("K", [64, 1000, 5000, 17000])
+@pytest.mark.parametrize("T", [1, 7, 1030])
+def test_norm_over_its_inputs(T, K):
+    """y in the place of x or of the residual, rows in registers and rows read twice, one wave a row and eight."""
+    say(f"norm over its inputs T={T} K={K}")
+    x, r = (torch.randn(T, K, device="cuda").half() for _ in range(2))
+    w = torch.randn(K, device="cuda")
+    alone, (both, h) = awq.awq_rmsnorm(x, w)[0], awq.awq_rmsnorm(x, w, residual=r)
+    a, b, c = x.clone(), x.clone(), r.clone()
+    assert torch.equal(awq.awq_rmsnorm(a, w, out=a)[0], alone)
+    got = awq.awq_rmsnorm(b, w, residual=r, out=b)
+    assert torch.equal(b, both) and torch.equal(got[1], h)
+    got = awq.awq_rmsnorm(x, w, residual=c, out=c)
+    assert torch.equal(c, both) and torch.equal(got[1], h)
+    b, c = x.clone(), r.clone()                                  # both results over both inputs, either way round
+    awq.awq_rmsnorm(b, w, residual=c, out=b, h_out=c)
+    assert torch.equal(b, both) and torch.equal(c, h)
+    b, c = x.clone(), r.clone()
+    awq.awq_rmsnorm(b, w, residual=c, out=c, h_out=b)
+    assert torch.equal(c, both) and torch.equal(b, h)

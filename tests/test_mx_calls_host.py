@@ -131,3 +131,18 @@ def test_build_whose_module_fails(building, step):
     with pytest.raises(RuntimeError, match=step):
         build.build()
     assert (where / build.LIB_NAME).read_text() == "new" and not (where / "_calls.so").exists()
+
+
+def test_outputs_over_operands_are_refused(monkeypatch):
+    """A linear layer's out over its tokens would be read by blocks that others have written to already; the norm's
+    out and h_out are two results."""
+    from weight_only_quantization_act_amd import _mx
+    monkeypatch.setattr(_mx, "_current_device", lambda: 0)
+    c, s = torch.zeros(64, 32, dtype=torch.uint8), torch.zeros(1, 64, 4, dtype=torch.uint8)
+    for rows in (1, 3, 40):
+        x = _claimed(torch.zeros(rows, 64).half())
+        with pytest.raises(ValueError, match="out"):
+            awq.awq_mxfp4_linear(x, _claimed(c), _claimed(s), out=x)
+        h = _claimed(torch.zeros(rows, 64).half())
+        with pytest.raises(ValueError, match="out"):
+            awq.awq_rmsnorm(x, residual=_claimed(torch.zeros(rows, 64).half()), h_out=h, out=h)

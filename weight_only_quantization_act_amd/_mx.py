@@ -279,7 +279,7 @@ def awq_mxfp4_linear(x: torch.Tensor, wc: torch.Tensor, ws: torch.Tensor,
                      stream=None):
     """y [T, M] in x's type: each token of x (fp16 or bf16 [T, K]) divided by s (fp32 [K], if given),
     quantised to MXFP4 and multiplied with the weight's codes and scales wc, ws (as
-    awq_mxfp4_quantize(W, s, "multiply") makes them)."""
+    awq_mxfp4_quantize(W, s, "multiply") makes them).  out must not overlap x."""
     if out is None and workspace is None and stream is None:
         y = (_N or _native()).mxfp4_linear(x, wc, ws, s, bias)
         if y is not None:
@@ -300,6 +300,8 @@ def awq_mxfp4_linear(x: torch.Tensor, wc: torch.Tensor, ws: torch.Tensor,
     if T == 0 or M == 0:
         return y
     py = y.data_ptr()
+    if py == x.data_ptr():
+        raise ValueError("out must not be x: blocks read the tokens when others have stored their results")
     ws_, pws, nws = _workspace(workspace, awq_mxfp4_linear_workspace_bytes(T, M, K), x.device)
     st = (_C or _lib()).awq_mxfp4_linear(x.data_ptr() or py, ldx, (ps or py) if s is not None else None, T,
                                 wc.data_ptr() or py, ldw, ws.data_ptr() or py, ldws, M, K, pb, dt, py,
@@ -341,7 +343,7 @@ def awq_rmsnorm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: flo
     """Root-mean-square norm of the rows of x (fp16 or bf16 [R, K]): returns (y, h) with h = x + residual in
     x's type (x itself without a residual) and y = h weight / sqrt(mean h^2 + eps) in x's type.
     weight [K] is fp32 or of x's type (None: ones); the scales of a search are folded into it (weight
-    / s).  h goes to h_out if given, which may be the residual or x itself; out receives y."""
+    / s).  h goes to h_out if given, y to out; each may be x or the residual itself, but not both the same."""
     if h_out is None and out is None and stream is None:
         got = (_N or _native()).rmsnorm(x, weight, eps, residual)
         if got is not None:
@@ -352,6 +354,8 @@ def awq_rmsnorm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: flo
     args, h = _norm_args(x, weight, eps, residual, h_out, dev)
     y, ldy = _out(out, args[4], args[5], x.dtype, x, dev)
     if args[4]:
+        if residual is not None and y.data_ptr() == h.data_ptr():
+            raise ValueError("out and h_out must not be the same")
         st = (_C or _lib()).awq_rmsnorm(*args, y.data_ptr(), ldy, _raw_stream(dev))
         if st:
             _check(st, "awq_rmsnorm")
